@@ -24,11 +24,16 @@ __all__ = [
     "dg_gemm_plan", "dg_init", "dg_sync_status", "dg_set_wait_timeout_us",
     "dg_debug_skip_first_load", "dg_status_string", "dg_version", "dg_release_stream",
     "dg_reload_env", "dg_convert_f16_amax", "dg_convert_f16_amax_pair", "dg_quantize_e4m3_pair",
+    "DG_ROPE_HALF", "DG_ROPE_INTERLEAVED", "DG_ROPE_UNSCALED", "DG_ROPE_LINEAR", "DG_ROPE_NTK",
+    "DG_ROPE_BY_PARTS", "DgRotary", "DgKvCache", "dg_rope_table", "dg_rope", "dg_kv_append",
+    "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch",
     "EXPORTED_SYMBOLS",
 ]
 
 DG_OK, DG_ERR_INVALID_VALUE, DG_ERR_MISALIGNED, DG_ERR_UNSUPPORTED, DG_ERR_CUDA, DG_ERR_TIMEOUT = range(6)
 DG_BF16, DG_E4M3, DG_FP16 = 0, 1, 2
+DG_ROPE_HALF, DG_ROPE_INTERLEAVED = 0, 1
+DG_ROPE_UNSCALED, DG_ROPE_LINEAR, DG_ROPE_NTK, DG_ROPE_BY_PARTS = range(4)
 
 #: Every function include/dg.h declares.
 EXPORTED_SYMBOLS = (
@@ -39,6 +44,8 @@ EXPORTED_SYMBOLS = (
     "dg_init", "dg_sync_status", "dg_set_wait_timeout_us", "dg_debug_skip_first_load",
     "dg_status_string", "dg_version", "dg_release_stream", "dg_reload_env", "dg_convert_f16_amax",
     "dg_convert_f16_amax_pair", "dg_quantize_e4m3_pair",
+    "dg_rope_table", "dg_rope", "dg_kv_append", "dg_kv_read", "dg_attn_decode",
+    "dg_attn_decode_scratch",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -60,6 +67,28 @@ class DgError(RuntimeError):
 class _Plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in
                 ("path", "block_m", "block_n", "block_k", "stages", "grid", "tiles", "smem_bytes")]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("slow_rotations", ctypes.c_double),
+                ("fast_rotations", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int64),
+                ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
 def lib():
@@ -93,6 +122,16 @@ def lib():
             L.dg_quantize_e4m3_pair.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
             L.dg_gemm_plan.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                        ctypes.POINTER(_Plan)]
+            heads, i32 = ctypes.POINTER(_Heads), ctypes.c_int
+            rotary, cache = ctypes.POINTER(_Rotary), ctypes.POINTER(_KvCache)
+            L.dg_rope_table.argtypes = [vp, i64, i32, ctypes.POINTER(_RopeScaling), vp]
+            L.dg_rope.argtypes = [heads, heads, i64, i32, i32, vp, rotary, i32, i32, vp]
+            L.dg_kv_append.argtypes = [heads, heads, i32, heads, heads, i64, vp, rotary, vp, cache,
+                                       i32, vp]
+            L.dg_kv_read.argtypes = [cache, vp, i64, heads, heads, i32, vp]
+            L.dg_attn_decode.argtypes = [heads, heads, vp, i32, i32, i32, cache, vp, i64, i64, vp, vp,
+                                         i64, ctypes.c_double, i32, vp, i64, vp]
+            L.dg_attn_decode_scratch.argtypes = [i32, i32, i32, i32, i64, i32, ctypes.POINTER(i64)]
             L.dg_init.argtypes = []
             L.dg_sync_status.argtypes = [vp]
             L.dg_set_wait_timeout_us.argtypes = [ctypes.c_uint64]
@@ -110,7 +149,8 @@ def lib():
                          "dg_sync_status", "dg_version", "dg_hgemm_scaled", "dg_fp16_range_scale",
                          "dg_convert_f16", "dg_quantize_e4m3_amax", "dg_release_stream",
                          "dg_convert_f16_amax", "dg_convert_f16_amax_pair",
-                         "dg_quantize_e4m3_pair"):
+                         "dg_quantize_e4m3_pair", "dg_rope_table", "dg_rope", "dg_kv_append",
+                         "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch"):
                 getattr(L, name).restype = st
             _lib = L
     return _lib
@@ -281,6 +321,139 @@ def dg_convert_f16_amax_pair(a, b, out_a, out_b, factor, amax_a, amax_b, stream=
     _check(lib().dg_convert_f16_amax_pair(_ptr(a), a.numel(), _ptr(b), b.numel(), _ptr(factor),
                                           _ptr(out_a), _ptr(out_b), _ptr(amax_a), _ptr(amax_b),
                                           _stream(stream)), "dg_convert_f16_amax_pair")
+
+
+_HALF_TYPES = {torch.bfloat16: DG_BF16, torch.float16: DG_FP16}
+
+
+def _heads(t, what, like=None):
+    """[tokens, heads, head_dim] (any token and head stride) as a dg_heads."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be in CUDA device memory")
+    if t.dim() != 3 or t.dtype not in _HALF_TYPES or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{what} must be BF16 or FP16 [tokens, heads, head_dim] with contiguous heads")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{what} must have the shape and type of its counterpart")
+    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _int32(t, n, what):
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what} must be int32 with {n} elements")
+    return _ptr(t)
+
+
+class DgRotary:
+    """A rotary table (FP32 [positions, rotary_dim / 2, 2], see dg_rope_table)
+    with its layout; keeps the tensor alive."""
+
+    def __init__(self, table, layout=DG_ROPE_HALF):
+        if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError("table must be FP32 [positions, rotary_dim / 2, 2]")
+        self.table = table
+        self.c = _Rotary(_ptr(table), table.shape[0], 2 * table.shape[1], int(layout))
+
+
+class DgKvCache:
+    """A paged E4M3 key/value cache: codes k, v uint8 [pages, kv_heads,
+    page_size, head_dim] and scales FP32 [pages, kv_heads, page_size]; keeps
+    the tensors alive."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dtype != torch.uint8 or v.dtype != torch.uint8 or k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be uint8 [pages, kv_heads, page_size, head_dim]")
+        for s in (k_scale, v_scale):
+            if s.dtype != torch.float32 or s.shape != k.shape[:3]:
+                raise ValueError("scales must be FP32 [pages, kv_heads, page_size]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        pages, self.kv_heads, page_size, self.head_dim = k.shape
+        self.c = _KvCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, self.kv_heads,
+                          page_size, self.head_dim)
+
+
+def dg_rope_table(table, base=10000.0, scaling=DG_ROPE_UNSCALED, factor=1.0,
+                  original_positions=0.0, slow_rotations=1.0, fast_rotations=32.0, magnitude=1.0,
+                  stream=None) -> None:
+    """Fill table (FP32 [positions, rotary_dim / 2, 2]) with cosines and sines."""
+    if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table must be FP32 [positions, rotary_dim / 2, 2]")
+    sc = _RopeScaling(base, int(scaling), factor, original_positions, slow_rotations,
+                      fast_rotations, magnitude)
+    _check(lib().dg_rope_table(_ptr(table), table.shape[0], 2 * table.shape[1], ctypes.byref(sc),
+                               _stream(stream)), "dg_rope_table")
+
+
+def dg_rope(x, out, positions, rotary, inverse=False, stream=None) -> None:
+    """out = x with each head's first rotary_dim elements turned (inverse: back)."""
+    hx, ho = _heads(x, "x"), _heads(out, "out", x)
+    _check(lib().dg_rope(hx, ho, x.shape[0], x.shape[1], x.shape[2],
+                         _int32(positions, x.shape[0], "positions"), rotary.c, int(bool(inverse)),
+                         _HALF_TYPES[x.dtype], _stream(stream)), "dg_rope")
+
+
+def dg_kv_append(k, v, slots, cache, positions=None, rotary=None, q=None, q_out=None,
+                 stream=None) -> None:
+    """Turn (with rotary) and quantise k, v [tokens, kv_heads, head_dim] into the
+    cache's slots; q is turned into q_out in the same launch."""
+    n = k.shape[0]
+    hk, hv = _heads(k, "k"), _heads(v, "v", k)
+    if k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+        raise ValueError("k and v must have the cache's heads and head_dim")
+    hq = ho = None
+    if q is not None:
+        hq, ho = _heads(q, "q"), _heads(q_out, "q_out", q)
+        if q.shape[0] != n or q.shape[2] != k.shape[2] or q.dtype != k.dtype:
+            raise ValueError("q must have the tokens, head_dim and type of k")
+    _check(lib().dg_kv_append(hq, ho, 0 if q is None else q.shape[1], hk, hv, n,
+                              None if positions is None else _int32(positions, n, "positions"),
+                              None if rotary is None else rotary.c, _int32(slots, n, "slots"),
+                              cache.c, _HALF_TYPES[k.dtype], _stream(stream)), "dg_kv_append")
+
+
+def dg_kv_read(cache, slots, k=None, v=None, stream=None) -> None:
+    """k[t], v[t] = the cached key and value of slots[t] (code times scale)."""
+    some = k if k is not None else v
+    if some is None:
+        return
+    if some.shape[1] != cache.kv_heads or some.shape[2] != cache.head_dim:
+        raise ValueError("k and v must have the cache's heads and head_dim")
+    hk = None if k is None else _heads(k, "k")
+    hv = None if v is None else _heads(v, "v", k)
+    _check(lib().dg_kv_read(cache.c, _int32(slots, some.shape[0], "slots"), some.shape[0], hk, hv,
+                            _HALF_TYPES[some.dtype], _stream(stream)), "dg_kv_read")
+
+
+def dg_attn_decode_scratch(batch, q_len, q_heads, cache, prefix_len=0, sm_count=0) -> int:
+    """Bytes of scratch dg_attn_decode needs for these sizes."""
+    n = ctypes.c_int64()
+    _check(lib().dg_attn_decode_scratch(batch, q_len, q_heads, cache.head_dim, prefix_len, sm_count,
+                                        ctypes.byref(n)), "dg_attn_decode_scratch")
+    return n.value
+
+
+def dg_attn_decode(q, out, cache, page_table, kv_lens, scratch, scale=None, lse=None,
+                   prefix_pages=None, prefix_len=0, stream=None) -> None:
+    """Attention of q [batch * q_len, q_heads, head_dim] over the cache: own
+    tokens by page_table [batch, max_pages] and kv_lens [batch], after a prefix
+    that the whole batch shares (prefix_pages, prefix_len)."""
+    hq, ho = _heads(q, "q"), _heads(out, "out", q)
+    tokens, heads, dim = q.shape
+    batch, max_pages = page_table.shape
+    if dim != cache.head_dim or page_table.dtype != torch.int32 or not page_table.is_cuda or \
+            (max_pages > 1 and page_table.stride(1) != 1):
+        raise ValueError("q must have the cache's head_dim, page_table must be int32 with contiguous rows")
+    if tokens % batch if batch else tokens:
+        raise ValueError("q must have the same number of tokens for each request")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != tokens * heads):
+        raise ValueError("lse must be FP32 with one element per token and head")
+    if prefix_len and prefix_pages.numel() < -(-prefix_len // cache.c.page_size):
+        raise ValueError("prefix_pages must name every page of the prefix")
+    _check(lib().dg_attn_decode(
+        hq, ho, _ptr(lse), batch, tokens // batch if batch else 1, heads, cache.c, page_table.data_ptr(),
+        max(page_table.stride(0), max_pages), max_pages, _int32(kv_lens, batch, "kv_lens"),
+        _int32(prefix_pages, prefix_pages.numel(), "prefix_pages") if prefix_len else None,
+        prefix_len, dim ** -0.5 if scale is None else scale, _HALF_TYPES[q.dtype], _ptr(scratch),
+        scratch.numel() * scratch.element_size(), _stream(stream)), "dg_attn_decode")
 
 
 def dg_gemm_plan(M, N, K, in_dtype=DG_E4M3, out_dtype=DG_BF16, sm_count=0) -> dict:

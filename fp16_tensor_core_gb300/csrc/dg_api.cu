@@ -788,6 +788,226 @@ dg_status dg_convert_f16_amax_pair(const float* a, int64_t na, const float* b, i
                                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// A view's pointer and strides.
+dg_status check_heads(const dg_heads* h) {
+    if (h == nullptr || h->data == nullptr || h->token_stride < 0 || h->head_stride < 0)
+        return DG_ERR_INVALID_VALUE;
+    if (!aligned16(h->data) || h->token_stride % 8 != 0 || h->head_stride % 8 != 0)
+        return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+dg_status check_16bit(dg_dtype t) {
+    return t == DG_BF16 || t == DG_FP16 ? DG_OK : DG_ERR_INVALID_VALUE;
+}
+
+dg_status check_head_dim(int d) {
+    return d >= 16 && d <= 256 && d % 16 == 0 ? DG_OK : DG_ERR_INVALID_VALUE;
+}
+
+dg_status check_rotary(const dg_rotary* r, const int32_t* positions, int head_dim) {
+    if (r == nullptr || r->table == nullptr || positions == nullptr || r->positions < 1 ||
+        (r->layout != DG_ROPE_HALF && r->layout != DG_ROPE_INTERLEAVED))
+        return DG_ERR_INVALID_VALUE;
+    if (check_head_dim(r->rotary_dim) != DG_OK || r->rotary_dim > head_dim) return DG_ERR_INVALID_VALUE;
+    if (!aligned16(r->table) || !aligned4(positions)) return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+dg_status check_cache(const dg_kv_cache* c) {
+    if (c == nullptr || c->k == nullptr || c->v == nullptr || c->k_scale == nullptr ||
+        c->v_scale == nullptr || c->pages < 1 || c->kv_heads < 1)
+        return DG_ERR_INVALID_VALUE;
+    if (c->page_size < 1 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0 ||
+        c->pages > INT_MAX / c->page_size)
+        return DG_ERR_INVALID_VALUE;
+    const dg_status rc = check_head_dim(c->head_dim);
+    if (rc != DG_OK) return rc;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
+        return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+// Heads of one call: kernels count the rows of a token in 32 bits.
+constexpr int kMaxHeads = 65536;
+
+}  // namespace
+
+dg_status dg_rope_table(float* table, int64_t positions, int rotary_dim,
+                        const dg_rope_scaling* scaling, dg_stream_t stream) {
+    if (positions < 0 || check_head_dim(rotary_dim) != DG_OK || scaling == nullptr ||
+        (positions > 0 && table == nullptr))
+        return DG_ERR_INVALID_VALUE;
+    const dg_rope_scaling& c = *scaling;
+    if (!(c.base > 0.0) || !(c.magnitude > 0.0)) return DG_ERR_INVALID_VALUE;
+    if (c.scaling != DG_ROPE_UNSCALED && c.scaling != DG_ROPE_LINEAR && c.scaling != DG_ROPE_NTK &&
+        c.scaling != DG_ROPE_BY_PARTS)
+        return DG_ERR_INVALID_VALUE;
+    if (c.scaling != DG_ROPE_UNSCALED && !(c.factor > 0.0)) return DG_ERR_INVALID_VALUE;
+    if (c.scaling == DG_ROPE_BY_PARTS &&
+        (!(c.original_positions > 0.0) || !(c.slow_rotations < c.fast_rotations)))
+        return DG_ERR_INVALID_VALUE;
+    if (!aligned16(table)) return DG_ERR_MISALIGNED;
+    if (positions == 0) return DG_OK;
+    DeviceState* st = nullptr;
+    const dg_status rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    return from_cuda(launch_rope_table(table, positions, rotary_dim, c, st->sm_count,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_rope(const dg_heads* x, const dg_heads* out, int64_t tokens, int heads, int head_dim,
+                  const int32_t* positions, const dg_rotary* rotary, int inverse, dg_dtype dtype,
+                  dg_stream_t stream) {
+    if (tokens < 0 || tokens > INT_MAX || heads < 0 || heads > kMaxHeads) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_head_dim(head_dim);
+    if (rc != DG_OK) return rc;
+    if (tokens == 0 || heads == 0) return DG_OK;
+    rc = check_heads(x);
+    if (rc == DG_OK) rc = check_heads(out);
+    if (rc == DG_OK) rc = check_rotary(rotary, positions, head_dim);
+    if (rc != DG_OK) return rc;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    return from_cuda(launch_rope(*x, *out, tokens, heads, head_dim, positions, *rotary, inverse != 0,
+                                 dtype == DG_FP16, st->sm_count, st->status,
+                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_kv_append(const dg_heads* q, const dg_heads* q_out, int q_heads, const dg_heads* k,
+                       const dg_heads* v, int64_t tokens, const int32_t* positions,
+                       const dg_rotary* rotary, const int32_t* slots, const dg_kv_cache* cache,
+                       dg_dtype dtype, dg_stream_t stream) {
+    if (tokens < 0 || tokens > INT_MAX || q_heads < 0 || q_heads > kMaxHeads) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_cache(cache);
+    if (rc != DG_OK) return rc;
+    if (cache->kv_heads > kMaxHeads || (q_heads > 0) != (q != nullptr) || (q == nullptr) != (q_out == nullptr) ||
+        (rotary == nullptr) != (positions == nullptr))
+        return DG_ERR_INVALID_VALUE;
+    if (tokens == 0) return DG_OK;
+    if (slots == nullptr) return DG_ERR_INVALID_VALUE;
+    rc = check_heads(k);
+    if (rc == DG_OK) rc = check_heads(v);
+    if (rc == DG_OK && q != nullptr) rc = check_heads(q);
+    if (rc == DG_OK && q != nullptr) rc = check_heads(q_out);
+    if (rc == DG_OK && rotary != nullptr) rc = check_rotary(rotary, positions, cache->head_dim);
+    if (rc != DG_OK) return rc;
+    if (!aligned4(slots)) return DG_ERR_MISALIGNED;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    return from_cuda(launch_kv_append(q, q_out, q_heads, *k, *v, tokens, positions, rotary, slots,
+                                      *cache, dtype == DG_FP16, st->sm_count, st->status,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tokens,
+                     const dg_heads* k, const dg_heads* v, dg_dtype dtype, dg_stream_t stream) {
+    if (tokens < 0 || tokens > INT_MAX) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_cache(cache);
+    if (rc != DG_OK) return rc;
+    if (cache->kv_heads > kMaxHeads) return DG_ERR_INVALID_VALUE;
+    if (tokens == 0 || (k == nullptr && v == nullptr)) return DG_OK;
+    if (slots == nullptr) return DG_ERR_INVALID_VALUE;
+    if (k != nullptr) rc = check_heads(k);
+    if (rc == DG_OK && v != nullptr) rc = check_heads(v);
+    if (rc != DG_OK) return rc;
+    if (!aligned4(slots)) return DG_ERR_MISALIGNED;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    return from_cuda(launch_kv_read(*cache, slots, tokens, k, v, dtype == DG_FP16, st->sm_count,
+                                    st->status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+dg_status check_attn_sizes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len) {
+    if (batch < 0 || batch > kAttnMaxBatch || q_len < 1 || q_heads < 1 || q_heads > kMaxHeads ||
+        prefix_len < 0 || prefix_len > INT_MAX - 64)
+        return DG_ERR_INVALID_VALUE;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return DG_ERR_INVALID_VALUE;
+    // rows of the prefix are counted in 32 bits
+    if (static_cast<int64_t>(batch) * q_len > INT_MAX / 2 / q_heads) return DG_ERR_INVALID_VALUE;
+    return DG_OK;
+}
+
+}  // namespace
+
+dg_status dg_attn_decode_scratch(int batch, int q_len, int q_heads, int head_dim,
+                                 int64_t prefix_len, int sm_count, int64_t* bytes) {
+    if (bytes == nullptr) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_attn_sizes(batch, q_len, q_heads, head_dim, prefix_len);
+    if (rc != DG_OK) return rc;
+    if (sm_count <= 0) {
+        DeviceState* st = nullptr;
+        rc = current_device_state(&st);
+        if (rc != DG_OK) return rc;
+        sm_count = st->sm_count;
+    }
+    *bytes = attn_scratch_bytes(batch, q_len, q_heads, head_dim, prefix_len, sm_count);
+    return DG_OK;
+}
+
+dg_status dg_attn_decode(const dg_heads* q, const dg_heads* out, float* lse, int batch, int q_len,
+                         int q_heads, const dg_kv_cache* cache, const int32_t* page_table,
+                         int64_t table_stride, int64_t max_pages, const int32_t* kv_lens,
+                         const int32_t* prefix_pages, int64_t prefix_len, double scale,
+                         dg_dtype dtype, void* scratch, int64_t scratch_bytes, dg_stream_t stream) {
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_cache(cache);
+    if (rc != DG_OK) return rc;
+    rc = check_attn_sizes(batch, q_len, q_heads, cache->head_dim, prefix_len);
+    if (rc != DG_OK) return rc;
+    if (q_heads % cache->kv_heads != 0 || !(scale - scale == 0.0)) return DG_ERR_INVALID_VALUE;
+    if (max_pages < 0 || table_stride < max_pages) return DG_ERR_INVALID_VALUE;
+    // tile counts are summed over the batch in 32 bits
+    if (max_pages > (INT_MAX - 64) / cache->page_size ||
+        (max_pages * cache->page_size + 63) / 32 * std::max(batch, 1) > INT_MAX)
+        return DG_ERR_INVALID_VALUE;
+    if (batch == 0) return DG_OK;
+    if (kv_lens == nullptr || (max_pages > 0 && page_table == nullptr) ||
+        (prefix_len > 0 && prefix_pages == nullptr) || scratch == nullptr)
+        return DG_ERR_INVALID_VALUE;
+    rc = check_heads(q);
+    if (rc == DG_OK) rc = check_heads(out);
+    if (rc != DG_OK) return rc;
+    if (!aligned16(scratch) || !aligned4(lse) || !aligned4(page_table) || !aligned4(kv_lens) ||
+        !aligned4(prefix_pages))
+        return DG_ERR_MISALIGNED;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    if (scratch_bytes < attn_scratch_bytes(batch, q_len, q_heads, cache->head_dim, prefix_len, st->sm_count))
+        return DG_ERR_INVALID_VALUE;
+    AttnLaunch L{};
+    L.q = q;
+    L.out = out;
+    L.lse = lse;
+    L.batch = batch;
+    L.q_len = q_len;
+    L.q_heads = q_heads;
+    L.cache = cache;
+    L.page_table = page_table;
+    L.table_stride = table_stride;
+    L.max_len = max_pages * cache->page_size;
+    L.kv_lens = kv_lens;
+    L.prefix_pages = prefix_pages;
+    L.prefix_len = prefix_len;
+    L.scale = scale;
+    L.fp16 = dtype == DG_FP16;
+    L.scratch = scratch;
+    L.sm_count = st->sm_count;
+    L.status = st->status;
+    return from_cuda(launch_attn_decode(L, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 dg_status dg_gemm_plan(int64_t M, int64_t N, int64_t K, dg_dtype in, dg_dtype out,
                        int sm_count, dg_plan* plan) {
     if (plan == nullptr) return DG_ERR_INVALID_VALUE;

@@ -176,6 +176,50 @@ cudaError_t launch_gemm_skinny(const TcLaunch& L, float* partials, uint32_t* cou
                                cudaStream_t s);
 void plan_skinny(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count, dg_plan* p);
 
+// Rotary positions and the E4M3 key/value cache (arguments already checked).
+// The smallest scale of a cached row: a row of zeros (or of values that no
+// 16-bit output could tell from zero) has a positive scale too, so that its
+// logarithm and reciprocal are finite.
+constexpr float kKvMinScale = 0x1p-60f;
+cudaError_t launch_rope_table(float* table, int64_t positions, int rotary_dim,
+                              const dg_rope_scaling& sc, int sm_count, cudaStream_t s);
+cudaError_t launch_rope(const dg_heads& x, const dg_heads& out, int64_t tokens, int heads,
+                        int head_dim, const int32_t* positions, const dg_rotary& rot, bool inverse,
+                        bool fp16, int sm_count, uint32_t* status, cudaStream_t s);
+cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_heads,
+                             const dg_heads& k, const dg_heads& v, int64_t tokens,
+                             const int32_t* positions, const dg_rotary* rot, const int32_t* slots,
+                             const dg_kv_cache& cache, bool fp16, int sm_count, uint32_t* status,
+                             cudaStream_t s);
+cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64_t tokens,
+                           const dg_heads* k, const dg_heads* v, bool fp16, int sm_count,
+                           uint32_t* status, cudaStream_t s);
+
+// Attention over the cache.
+constexpr int kAttnMaxBatch = 4096;
+struct AttnLaunch {
+    const dg_heads* q;
+    const dg_heads* out;
+    float* lse;
+    int batch, q_len, q_heads;
+    const dg_kv_cache* cache;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int64_t max_len;             // tokens a row of the page table can name
+    const int32_t* kv_lens;
+    const int32_t* prefix_pages;
+    int64_t prefix_len;
+    double scale;
+    bool fp16;
+    void* scratch;
+    int sm_count;
+    uint32_t* status;
+};
+cudaError_t launch_attn_decode(const AttnLaunch& L, cudaStream_t s);
+int64_t attn_slot_floats(int sm_count, int head_dim);
+int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
+                           int sm_count);
+
 // Tile table for the tensor-core path (fills block_n, stages, smem, grid).
 void plan_tc(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count,
              dg_plan* p);

@@ -1,6 +1,7 @@
 /*
- * dg.h -- C ABI of libdg: per-tensor-scaled E4M3 GEMM, FP16 GEMM and the
- * E4M3 quantiser on one NVIDIA GB300 (sm_103a).
+ * dg.h -- C ABI of libdg: per-tensor-scaled E4M3 GEMM, FP16 GEMM, the E4M3
+ * quantiser, rotary positions and attention over an E4M3 key/value cache on
+ * one NVIDIA GB300 (sm_103a).
  *
  * Page shorthands used in the citations:
  *   [FP8-guide] "DeepGEMM实战：FP8矩阵乘法与JIT编译优化指南"
@@ -13,7 +14,8 @@
  * ---------------------------------------
  * Memory.    Every data pointer is DEVICE memory on the current CUDA device,
  *            owned by the caller.  The library allocates nothing per call and
- *            takes no workspace argument.  The first call on a device (or
+ *            takes no workspace argument (but for dg_attn_decode, whose
+ *            scratch grows with the call).  The first call on a device (or
  *            dg_init) allocates a 16-byte device status word and a split-K
  *            workspace (two 128 x 128 FP32 partial tiles per SM and 8192
  *            counters, 20 MB on 152 SMs) that live until exit.  Split-K
@@ -325,6 +327,168 @@ dg_status dg_convert_f16_amax(const float* x, int64_t n, const float* factor,
 dg_status dg_convert_f16_amax_pair(const float* a, int64_t na, const float* b, int64_t nb,
                                    const float* factor, uint16_t* out_a, uint16_t* out_b,
                                    float* amax_a, float* amax_b, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Behind the QKV projection: rotary positions, an E4M3 key/value cache and
+ * attention over it ([DG-FP16] §2.1 and §4.1: the decode QKV projection is
+ * the workload; the pages stop at its output, and what follows has no
+ * counterpart there).
+ * ------------------------------------------------------------------------ */
+
+/* tokens x heads x head_dim elements: element (t, h, d) at
+ * data[t * token_stride + h * head_stride + d], strides in elements.  data
+ * must be 16-byte aligned and both strides multiples of 8 elements
+ * (DG_ERR_MISALIGNED), strides not negative.  A packed QKV row of
+ * (q_heads + 2 kv_heads) * head_dim elements is three such views with that
+ * token stride.  As an output, rows must not overlap one another. */
+typedef struct {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} dg_heads;
+
+/* Which elements of a head form the rotated pairs. */
+typedef enum {
+    DG_ROPE_HALF = 0,        /* (i, i + rotary_dim / 2)                        */
+    DG_ROPE_INTERLEAVED = 1  /* (2 i, 2 i + 1)                                 */
+} dg_rope_layout;
+
+/* How frequencies are changed for contexts longer than the trained one. */
+typedef enum {
+    DG_ROPE_UNSCALED = 0,
+    DG_ROPE_LINEAR = 1,   /* every frequency / factor                          */
+    DG_ROPE_NTK = 2,      /* base * factor^(r / (r - 2))                       */
+    DG_ROPE_BY_PARTS = 3  /* / factor for slow pairs, kept for fast ones       */
+} dg_rope_scaling_kind;
+
+typedef struct {
+    double base;               /* f_i = base^(-2 i / rotary_dim), i < rotary_dim / 2 */
+    dg_rope_scaling_kind scaling;
+    double factor;             /* > 0 (unused when unscaled)                        */
+    double original_positions; /* BY_PARTS: the trained context L                   */
+    double slow_rotations;     /* BY_PARTS: a pair turning L f / 2 pi <= slow times */
+    double fast_rotations;     /*   over L is divided by factor, one turning >= fast
+                                    times is kept, linear in between; slow < fast   */
+    double magnitude;          /* cosines and sines are multiplied by this          */
+} dg_rope_scaling;
+
+/* Cosines and sines of positions 0 .. positions - 1, formed in FP64 and
+ * rounded once: table[p][i] = magnitude * { cos(p f_i), sin(p f_i) }.
+ *   table   FP32[positions][rotary_dim / 2][2], device, 16-byte aligned.
+ *   rotary_dim  a positive multiple of 16, at most 256. */
+dg_status dg_rope_table(float* table, int64_t positions, int rotary_dim,
+                        const dg_rope_scaling* scaling, dg_stream_t stream);
+
+/* A rotary table with the layout it is applied in. */
+typedef struct {
+    const float* table;   /* as dg_rope_table writes it                       */
+    int64_t positions;
+    int rotary_dim;       /* the first rotary_dim elements of a head turn     */
+    dg_rope_layout layout;
+} dg_rotary;
+
+/* Rotary positions: for each pair (a, b) of the first rotary_dim elements of
+ * each head of token t, with (c, s) the table's entry of position
+ * positions[t],
+ *   (a, b) -> (a c - b s, b c + a s)
+ * in FP32, rounded once; the other elements are copied.  inverse != 0 takes
+ * -s: the transposed map, which carries a gradient back.
+ *   x, out     BF16 or FP16 (dtype); out may be x itself (same pointer and
+ *              strides) or must not overlap it.
+ *   head_dim   a multiple of 16, rotary_dim .. 256.
+ *   positions  int32[tokens], device.  A position outside the table leaves
+ *              its token's output unwritten and dg_sync_status reports
+ *              DG_ERR_INVALID_VALUE. */
+dg_status dg_rope(const dg_heads* x, const dg_heads* out, int64_t tokens, int heads, int head_dim,
+                  const int32_t* positions, const dg_rotary* rotary, int inverse, dg_dtype dtype,
+                  dg_stream_t stream);
+
+/* A paged E4M3 key/value cache.  Token slot s lies in page s / page_size at
+ * place s % page_size; keys and values are
+ *   k, v              E4M3 codes [pages][kv_heads][page_size][head_dim]
+ *   k_scale, v_scale  FP32       [pages][kv_heads][page_size]
+ * all in device memory, codes 16-byte aligned, scales 4-byte aligned; value =
+ * code * scale, one scale per head of a token ([FP8-guide] §3.2's rule with
+ * that as the tensor): scale = max(fl32(amax / 448), 2^-60), code =
+ * E4M3(fl32(x / scale)) (§4.3).  The floor stands in for dg_amax's scale 1
+ * of an all-zero tensor.  A row that holds a NaN or an infinity has scale
+ * NaN and codes 0, so codes are always finite.
+ *   head_dim   a multiple of 16 up to 256 (dg_attn_decode: 64, 128 or 256)
+ *   page_size  a power of two, 1 .. 65536
+ *   pages * page_size < 2^31. */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int kv_heads;
+    int page_size;
+    int head_dim;
+} dg_kv_cache;
+
+/* Writes tokens into the cache; with a rotary table the keys are turned
+ * first (in FP32, quantised without a 16-bit rounding in between), and
+ * queries given beside them are turned into q_out, all in one launch.
+ *   q, q_out   BF16 or FP16 (dtype), q_heads heads; both NULL with q_heads 0
+ *              when there are none.  q_out may be q itself.
+ *   k, v       the same type, cache->kv_heads heads.
+ *   positions, rotary  as dg_rope; both NULL for no rotation.
+ *   slots      int32[tokens], device: where token t goes; negative: its key
+ *              and value are dropped (q_out is still written).  A slot past
+ *              the cache or a position outside the table leaves everything
+ *              of its token unwritten and dg_sync_status reports
+ *              DG_ERR_INVALID_VALUE.  No slot may be named twice. */
+dg_status dg_kv_append(const dg_heads* q, const dg_heads* q_out, int q_heads, const dg_heads* k,
+                       const dg_heads* v, int64_t tokens, const int32_t* positions,
+                       const dg_rotary* rotary, const int32_t* slots, const dg_kv_cache* cache,
+                       dg_dtype dtype, dg_stream_t stream);
+
+/* Reads tokens back: k[t] and v[t] = code * scale of slot slots[t], rounded
+ * once to dtype (BF16 or FP16); zeros for a negative slot.  k or v may be
+ * NULL.  A slot past the cache leaves its token unwritten and dg_sync_status
+ * reports DG_ERR_INVALID_VALUE. */
+dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tokens,
+                     const dg_heads* k, const dg_heads* v, dg_dtype dtype, dg_stream_t stream);
+
+/* Attention of q_len new tokens per request over the cache.  Token
+ * b * q_len + i of q is query i of request b.  It sees the whole shared
+ * prefix (prefix_len tokens on prefix_pages, in order; the same for every
+ * request, and computed for all of them at once) and tokens
+ * 0 .. kv_lens[b] - q_len + i of the request's own kv_lens[b] tokens (whose
+ * last q_len are the new ones, already in the cache):
+ *   out = sum_t softmax_t(scale * q . k_t) v_t
+ * per query head; q_heads / kv_heads consecutive query heads share a key
+ * head.  A query that sees nothing gets zeros and lse -infinity.
+ *   q, out      BF16 or FP16 (dtype), batch * q_len tokens, q_heads heads.
+ *   lse         FP32[batch * q_len][q_heads], natural log of the sum of
+ *               exponentials, or NULL.
+ *   batch       0 .. 4096; q_len >= 1; q_heads a multiple of kv_heads.
+ *   page_table  int32, device: row b, at b * table_stride, names the pages of
+ *               request b's tokens in order; max_pages entries a row.
+ *   kv_lens     int32[batch], device, 0 .. max_pages * page_size each.  A
+ *               length outside that counts as 0, a page outside the cache as
+ *               a page of zeros (no access leaves the cache), and
+ *               dg_sync_status reports DG_ERR_INVALID_VALUE.
+ *   prefix_pages  int32[ceil(prefix_len / page_size)], device; NULL with
+ *               prefix_len 0.
+ *   scale       finite, typically 1 / sqrt(head_dim).
+ *   scratch     device, 16-byte aligned, at least dg_attn_decode_scratch()
+ *               bytes; need not be initialised, and holds nothing between
+ *               calls.  Calls that may overlap in time need one each.
+ * Weights enter the second product as FP16 relative to the row's largest
+ * weight times value scale; everything else is FP32.  Results do not depend
+ * on timing. */
+dg_status dg_attn_decode(const dg_heads* q, const dg_heads* out, float* lse, int batch, int q_len,
+                         int q_heads, const dg_kv_cache* cache, const int32_t* page_table,
+                         int64_t table_stride, int64_t max_pages, const int32_t* kv_lens,
+                         const int32_t* prefix_pages, int64_t prefix_len, double scale,
+                         dg_dtype dtype, void* scratch, int64_t scratch_bytes, dg_stream_t stream);
+
+/* Bytes of scratch dg_attn_decode needs for these sizes, in *bytes.
+ * sm_count <= 0 queries the current device. */
+dg_status dg_attn_decode_scratch(int batch, int q_len, int q_heads, int head_dim,
+                                 int64_t prefix_len, int sm_count, int64_t* bytes);
 
 /* Tile / path selection for a GEMM shape, host only (launches nothing).
  * [FP8-guide] §2.2, §3.1, §3.3 (per-shape tile choice, smaller tiles where
