@@ -196,7 +196,7 @@ cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64
                            uint32_t* status, cudaStream_t s);
 
 // Attention over the cache.
-constexpr int kAttnMaxBatch = 4096;
+constexpr int kAttnMaxBatch = 2048;
 struct AttnLaunch {
     const dg_heads* q;
     const dg_heads* out;

@@ -16,10 +16,12 @@
 // A cached element is read once and takes 4 flop per row, so for the few
 // rows that share a key head the kernel is bound by HBM: it streams codes
 // through shared memory with asynchronous copies and takes both products on
-// warp-level MMAs (16 rows; tcgen05's 128 would be idle).
+// warp-level MMAs with the cached operand on their 16-row side and 8 query
+// rows on the other (tcgen05's 128 rows would be idle).
 //
-// Split: all (request, key head, 16-row tile) units are laid end to end in
-// 32-token tiles, and every warp of the grid takes an equal run of them, so
+// Split: all (request, key head, row tile) units are laid end to end in
+// 32-token tiles, with room for the cost of taking up a unit before each,
+// and every warp of the grid takes an equal run of them, so
 // ragged lengths balance and one long cache spreads over all SMs.  A warp
 // writes the units that lie inside its run; the pieces of a unit that
 // crosses warps are joined in shared memory, and those of a unit that
@@ -35,8 +37,8 @@
 namespace dg {
 namespace {
 
-constexpr int kTile = 32;      // tokens per warp step
-constexpr int kRows = 16;      // query rows per unit (the MMA's M side)
+constexpr int kTile = 32;        // tokens per warp step
+constexpr int kMaxUnitRows = 16; // query rows of a unit
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct AttnArgs {
@@ -64,7 +66,8 @@ struct AttnArgs {
     int q_heads;
     bool causal;
     float scale_log2;          // softmax scale * log2(e)
-    float* slots;              // two states of 16 rows per block
+    float* slots;              // two states of kRows rows per block
+    int4* crossings;           // per block: the unit that goes on past it
     const float* prefix;       // states of the prefix, per (token, head), or null
     float* states;             // where this call leaves states instead of outputs, or null
     uint32_t* status;
@@ -93,6 +96,18 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The transpose of an 8 x 8 matrix of 16-bit values held two to a lane (row
+// lane / 4, columns 2 (lane % 4), + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -108,94 +123,135 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t half2_of(uint32_t codes, int hi) {
-    return e4m3x2_to_f16x2(static_cast<uint16_t>(hi ? codes >> 16 : codes));
+// Four E4M3 codes (low byte first) -> two FP16 pairs, exactly.
+__device__ __forceinline__ void codes_to_halves(uint32_t codes, uint32_t* lo, uint32_t* hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(*lo), "=r"(*hi) : "r"(codes));
 }
 
-// Shapes per head width.  kDims: dims of one lane quarter in a run (a lane
-// with lane % 4 == c owns dims c * kDims .. of each kSpan-wide part of the
-// head, in both products).
-template <int D>
+// Shapes per head width D and number of 8-row tiles NT.  A lane with
+// lane % 4 == c holds dims c * kDims .. of each kSpan-wide part of the head
+// in the first product, one with lane / 4 == g dims g * kSpan / 8 .. in the
+// second.
+template <int D, int NT>
 struct Shape {
-    static constexpr int kWarps = D == 256 ? 4 : 8;
-    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kRows = 8 * NT;             // query rows per unit
+    static constexpr int kWarps = D == 256 ? 4 : D == 128 && NT == 2 ? 8 : 16;
+    static constexpr int kStages = D == 64 || kWarps <= 8 ? 2 : 1;
     static constexpr int kParts = D == 256 ? 2 : 1;
-    static constexpr int kSpan = D / kParts;        // 64 or 128
-    static constexpr int kDims = kSpan / 4;         // 16 or 32
-    static constexpr int kStageBytes = kTile * D * 2 + kTile * 8;
-    static constexpr int kState = D + 4;            // m, l, 2 unused, acc[D]
+    static constexpr int kSpan = D / kParts;         // 64 or 128
+    static constexpr int kDims = kSpan / 4;          // 16 or 32
+    static constexpr int kTileBytes = kTile * D;     // keys or values of a tile
+    static constexpr int kState = D + 4;             // m, l, 2 unused, acc[D]
     static constexpr int kStashBytes = kRows * kState * 4;
-    // tail pieces are stashed over the warp's (drained) stages
-    static constexpr int kRingBytes = kStages * kStageBytes;
+    // per warp: stages of keys, of values, of scales; log2 and reciprocal of
+    // the value scales in use
+    static constexpr int kScaleAt = 2 * kStages * kTileBytes;
+    static constexpr int kLogAt = kScaleAt + kStages * 2 * kTile * 4;
+    static constexpr int kRingBytes = kLogAt + 2 * kTile * 4;
+    // a run's last piece is stashed over the warp's (drained) stages
     static_assert(kRingBytes >= kStashBytes, "a tail piece fits the ring");
-    static constexpr int kSmem = kWarps * (kRingBytes + kStashBytes) + 256;
+    static constexpr int kSmem = kWarps * (kRingBytes + kStashBytes);
 };
 
-// Byte offset of 16-byte chunk `chunk` of token t in a tile: the chunks of a
-// 128-byte line are permuted by the token so that neither product's reads
-// meet in a bank (key reads: 2 tokens x 4 chunks a quarter warp; value
-// reads: 4 even tokens x 2 chunks).
+// Row r (0 .. 31) of a tile's MMA operands is token 4 (r % 8) + r / 8, so
+// that a lane's four tokens are neighbours (their scales are one 16-byte
+// read).  Byte offset of 16-byte chunk `chunk` of token t in a tile: the
+// chunks of a 128-byte line are permuted by the token so that neither
+// product's reads meet in a bank (a quarter warp reads 4 chunks of tokens t
+// and t + 4 of the keys, and 2 chunks of tokens t, t + 8, t + 16, t + 24 of
+// the values).
 template <int D>
 __device__ __forceinline__ uint32_t chunk_at(int t, int chunk) {
     if constexpr (D == 64)
-        return (t >> 1) * 128 + ((((t & 1) * 4 + chunk) ^ (((t >> 1) & 3) << 1)) * 16);
+        return (t >> 1) * 128 +
+               ((((t & 1) * 4 + chunk) ^ ((((t >> 3) & 3) << 1) ^ (t & 4))) * 16);
     else
-        return t * D + (chunk >> 3) * 128 + (((chunk & 7) ^ (t & 7)) * 16);
+        return t * D + (chunk >> 3) * 128 + (((chunk & 7) ^ ((t >> 2) & 7)) * 16);
 }
 
-// A place in the flat order of tiles.
+// A place in the flat order of tiles.  Units are laid out with kUnitCost
+// tiles' worth of room before their first tile: about what a warp spends on
+// taking up a unit and leaving it.
+constexpr int kUnitCost = 1;
 struct Cursor {
     int b;       // request
     int unit;    // key head * row_tiles + row tile
     int tile;
     int ntile;   // tiles of the request's units
     int len;     // its tokens
+    int stop;    // the run's end in this unit: its last tile + 1
 };
 
-// A warp's state of one unit: rows g and g + 8 of the lane.
+__device__ __forceinline__ float4 scaled(float4 x, float w) {
+    return make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
+}
+__device__ __forceinline__ float4 plus_scaled(float4 x, float w, float4 y) {
+    return make_float4(fmaf(w, y.x, x.x), fmaf(w, y.y, x.y), fmaf(w, y.z, x.z), fmaf(w, y.w, x.w));
+}
+
+// Where a row's result goes and what it is joined with: factors for its
+// partial sums, so that out = x * wx (+ prefix state * wp).
+struct RowEnd {
+    float* state;          // raw state wanted: there
+    const float* prefix;   // state to join with, or null
+    uint16_t* out;
+    float wx, wp;
+};
+
 template <int D>
-struct State {
-    float m[2], l[2];
-    float acc[D / 8][4];
-};
-
-// Final output (or state) of 4 dims of one row from its joined state.
-template <int D, bool kFp16>
-__device__ __forceinline__ void emit4(const AttnArgs& a, int64_t token, int head, int d, float m,
-                                      float l, float4 x) {
+__device__ __forceinline__ RowEnd row_end(const AttnArgs& a, int64_t token, int head, float m, float l,
+                                          bool leader) {
+    RowEnd e;
+    const int64_t row = token * a.q_heads + head;
+    e.state = nullptr;
+    e.prefix = nullptr;
     if (a.states != nullptr) {
-        float* s = a.states + (token * a.q_heads + head) * (D + 4);
-        *reinterpret_cast<float4*>(s + 4 + d) = x;
-        if (d == 0) {
-            s[0] = m;
-            s[1] = l;
-        }
-        return;
+        e.state = a.states + row * (D + 4);
+        if (leader) *reinterpret_cast<float2*>(e.state) = make_float2(m, l);
+        return e;
     }
+    e.out = a.out + token * a.o_ts + head * a.o_hs;
+    e.wx = 1.0f;
+    e.wp = 0.0f;
     if (a.prefix != nullptr) {
-        const float* s = a.prefix + (token * a.q_heads + head) * (D + 4);
-        const float pm = s[0], pl = s[1];
-        const float4 p = *reinterpret_cast<const float4*>(s + 4 + d);
-        const float top = fmaxf(m, pm);
+        e.prefix = a.prefix + row * (D + 4);
+        const float2 p = *reinterpret_cast<const float2*>(e.prefix);
+        const float top = fmaxf(m, p.x);
         const float base = top == -INFINITY ? 0.0f : top;
-        const float wm = ex2(m - base), wp = ex2(pm - base);
+        e.wx = ex2(m - base);
+        e.wp = ex2(p.x - base);
         m = top;
-        l = wm * l + wp * pl;
-        x.x = wm * x.x + wp * p.x;
-        x.y = wm * x.y + wp * p.y;
-        x.z = wm * x.z + wp * p.z;
-        x.w = wm * x.w + wp * p.w;
+        l = e.wx * l + e.wp * p.y;
     }
     const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
+    e.wx *= inv;
+    e.wp *= inv;
+    if (leader && a.lse != nullptr)
+        a.lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    return e;
+}
+
+// Dims d .. d + 3 of a row.
+template <int D, bool kFp16>
+__device__ __forceinline__ void emit4(const RowEnd& e, int d, float4 x) {
+    if (e.state != nullptr) {
+        *reinterpret_cast<float4*>(e.state + 4 + d) = x;
+        return;
+    }
+    x = scaled(x, e.wx);
+    if (e.prefix != nullptr)
+        x = plus_scaled(x, e.wp, *reinterpret_cast<const float4*>(e.prefix + 4 + d));
     uint2 o;
     if constexpr (kFp16) {
-        o = make_uint2(f32x2_to_f16x2(x.x * inv, x.y * inv), f32x2_to_f16x2(x.z * inv, x.w * inv));
+        o = make_uint2(f32x2_to_f16x2(x.x, x.y), f32x2_to_f16x2(x.z, x.w));
     } else {
-        o = make_uint2(f32x2_to_bf16x2(x.x * inv, x.y * inv), f32x2_to_bf16x2(x.z * inv, x.w * inv));
+        o = make_uint2(f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w));
     }
-    *reinterpret_cast<uint2*>(a.out + token * a.o_ts + head * a.o_hs + d) = o;
-    if (d == 0 && a.lse != nullptr)
-        a.lse[token * a.q_heads + head] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    *reinterpret_cast<uint2*>(e.out + d) = o;
 }
 
 // Row r (0 .. rows-1) of request b's key head h: its token and query head.
@@ -217,14 +273,19 @@ __device__ __forceinline__ int request_len(const AttnArgs& a, int b) {
     return n;
 }
 
-// cum[b] = tiles of one unit of requests 0 .. b-1, over the whole block.
+// cum[b] = room of one unit of each of requests 0 .. b-1 (its tiles and the
+// unit's cost; nothing for an empty request), and the requests' lengths;
+// over the whole block.
 template <int kThreads>
-__device__ __forceinline__ void scan_tiles(const AttnArgs& a, uint32_t* cum, uint32_t* warp_sum) {
+__device__ __forceinline__ void scan_tiles(const AttnArgs& a, uint32_t* cum, int* lens, uint32_t* warp_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t carry = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        uint32_t n = b < a.batch ? (request_len(a, b) + kTile - 1) / kTile : 0;
+        const int len = b < a.batch ? request_len(a, b) : 0;
+        if (b < a.batch) lens[b] = len;
+        uint32_t n = (len + kTile - 1) / kTile;
+        if (n > 0) n += kUnitCost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, n, o);
@@ -246,9 +307,10 @@ __device__ __forceinline__ void scan_tiles(const AttnArgs& a, uint32_t* cum, uin
     __syncthreads();
 }
 
-// Tiles a warp takes: an equal share of all.
-__device__ __forceinline__ int64_t tiles_per_warp(int64_t total, int64_t warps) {
-    return max(static_cast<int64_t>(1), (total + warps - 1) / warps);
+// Room a warp takes: an equal share of all, at least one tile beside a
+// unit's cost.
+__device__ __forceinline__ int64_t room_per_warp(int64_t total, int64_t warps) {
+    return max(static_cast<int64_t>(kUnitCost + 1), (total + warps - 1) / warps);
 }
 
 // The request whose tiles hold flat position f (which is below the total).
@@ -262,24 +324,26 @@ __device__ __forceinline__ int find_request(const uint32_t* cum, int batch, int6
     return lo;
 }
 
-template <int D, bool kFp16>
-__global__ void __launch_bounds__(Shape<D>::kWarps * 32, 1)
+template <int D, int NT, bool kFp16>
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1)
 attn_split_kernel(const AttnArgs a) {
-    using S = Shape<D>;
-    constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kStages = S::kStages;
+    using S = Shape<D, NT>;
+    constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kStages = S::kStages, kRows = S::kRows;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t warp_sum[kWarps];
     __shared__ int piece_b[2 * kWarps], piece_unit[2 * kWarps];   // request (-1: no piece), unit
     uint32_t* cum = reinterpret_cast<uint32_t*>(smem + S::kSmem);
+    int* lens = reinterpret_cast<int*>(cum + a.batch + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     pdl_wait();
-    scan_tiles<kThreads>(a, cum, warp_sum);
+    scan_tiles<kThreads>(a, cum, lens, warp_sum);
+    pdl_launch_dependents();
 
     const int units = a.kv_heads * a.row_tiles;
     const int64_t total = static_cast<int64_t>(cum[a.batch]) * units;
-    const int64_t run = tiles_per_warp(total, static_cast<int64_t>(gridDim.x) * kWarps);
-    const int64_t block0 = static_cast<int64_t>(blockIdx.x) * kWarps * run;
+    const int64_t run = room_per_warp(total, static_cast<int64_t>(gridDim.x) * kWarps);
+    const int64_t block0 = min(total, static_cast<int64_t>(blockIdx.x) * kWarps * run);
     const int64_t block1 = min(total, block0 + kWarps * run);
     const int64_t f0 = min(total, block0 + warp * run), f1 = min(total, f0 + run);
 
@@ -287,124 +351,159 @@ attn_split_kernel(const AttnArgs a) {
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
         if (cum[b + 1] != cum[b]) continue;
         for (int i = threadIdx.x; i < a.q_len * a.q_heads * (D / 4); i += kThreads) {
-            const int row = i / (D / 4);
-            emit4<D, kFp16>(a, static_cast<int64_t>(b) * a.q_len + row / a.q_heads, row % a.q_heads,
-                            4 * (i % (D / 4)), -INFINITY, 0.0f, make_float4(0, 0, 0, 0));
+            const int row = i / (D / 4), d = 4 * (i % (D / 4));
+            const RowEnd e = row_end<D>(a, static_cast<int64_t>(b) * a.q_len + row / a.q_heads,
+                                        row % a.q_heads, -INFINITY, 0.0f, d == 0);
+            emit4<D, kFp16>(e, d, make_float4(0, 0, 0, 0));
         }
     }
 
-    const uint32_t ring = smem_addr(smem) + warp * S::kRingBytes;
+    uint8_t* mine = smem + warp * S::kRingBytes;
+    const uint32_t ring = smem_addr(mine);
+    float* logs = reinterpret_cast<float*>(mine + S::kLogAt);
     float* head_stash =
         reinterpret_cast<float*>(smem + kWarps * S::kRingBytes + warp * S::kStashBytes);
-    float* tail_stash = reinterpret_cast<float*>(smem + warp * S::kRingBytes);
+    float* tail_stash = reinterpret_cast<float*>(mine);
     if (lane == 0) piece_b[2 * warp] = piece_b[2 * warp + 1] = -1;
 
     if (f0 < f1) {
-        // ---- producer side: the next tile to load, and its tokens' pages
-        auto start = [&](int64_t f) {
+        // ---- the run's tiles: from the one at f0 up to the one at f1
+        auto at_room = [&](int64_t f) {
             Cursor u;
             u.b = find_request(cum, a.batch, units, f);
-            u.ntile = static_cast<int>(cum[u.b + 1] - cum[u.b]);
-            u.len = request_len(a, u.b);
+            const int room = static_cast<int>(cum[u.b + 1] - cum[u.b]);
+            u.ntile = room - kUnitCost;
             const int64_t in = f - static_cast<int64_t>(cum[u.b]) * units;
-            u.unit = static_cast<int>(in / u.ntile);
-            u.tile = static_cast<int>(in - static_cast<int64_t>(u.unit) * u.ntile);
+            u.unit = in < 0x7FFFFFFF ? static_cast<int>(in) / room : static_cast<int>(in / room);
+            u.tile = max(0, static_cast<int>(in - static_cast<int64_t>(u.unit) * room) - kUnitCost);
+            u.len = lens[u.b];
             return u;
         };
+        const Cursor end = f1 < total ? at_room(f1) : Cursor{a.batch, 0, 0, 0, 0, 0};
+        // Sets u.stop; whether u (at its unit's first tile of the run) is in the run.
+        auto settle = [&](Cursor& u) {
+            u.stop = u.b == end.b && u.unit == end.unit ? end.tile : u.ntile;
+            return u.b < a.batch && u.tile < u.stop;
+        };
+        // The next tile; whether it is in the run.
         auto advance = [&](Cursor& u) {
-            if (++u.tile < u.ntile) return;
+            if (++u.tile < u.stop) return true;
+            if (u.stop < u.ntile) return false;
             u.tile = 0;
-            if (++u.unit < units) return;
-            u.unit = 0;
-            do ++u.b; while (cum[u.b + 1] == cum[u.b]);   // f < total: there is one
-            u.ntile = static_cast<int>(cum[u.b + 1] - cum[u.b]);
-            u.len = request_len(a, u.b);
-        };
-        auto page_of = [&](const Cursor& u) {   // this lane's token of the tile: its page or -1
-            const int t = u.tile * kTile + lane;
-            if (t >= u.len) return -1;
-            const int p = a.page_table[u.b * a.table_stride + (t >> a.page_shift)];
-            if (p >= 0 && p < a.pages) return p;
-            atomicOr(a.status, kStatusBadArgument);
-            return -1;
-        };
-        const int in_page = (1 << a.page_shift) - 1;
-        auto issue = [&](const Cursor& u, int page, int stage) {
-            const uint32_t base = ring + stage * S::kStageBytes;
-            const int h = u.unit / a.row_tiles;
-            const int t0 = u.tile * kTile;
-            constexpr int kPerRow = D / 16, kPerStep = 32 / kPerRow;
-            const int chunk = lane % kPerRow;
-#pragma unroll
-            for (int i = 0; i < kTile / kPerStep; ++i) {
-                const int t = i * kPerStep + lane / kPerRow;
-                const int p = __shfl_sync(0xFFFFFFFFu, page, t);
-                const int64_t row = ((static_cast<int64_t>(max(p, 0)) * a.kv_heads + h) << a.page_shift) +
-                                    ((t0 + t) & in_page);
-                const uint32_t dst = base + chunk_at<D>(t, chunk);
-                const int64_t off = row * D + chunk * 16;
-                cp_async16(dst, a.k + off, p < 0 ? 0 : 16);
-                cp_async16(dst + kTile * D, a.v + off, p < 0 ? 0 : 16);
+            if (++u.unit == units) {
+                u.unit = 0;
+                do ++u.b; while (u.b < a.batch && cum[u.b + 1] == cum[u.b]);
+                if (u.b == a.batch) return false;
+                u.ntile = static_cast<int>(cum[u.b + 1] - cum[u.b]) - kUnitCost;
+                u.len = lens[u.b];
             }
-            const int64_t row = ((static_cast<int64_t>(max(page, 0)) * a.kv_heads + h) << a.page_shift) +
-                                ((t0 + lane) & in_page);
-            const uint32_t sc = base + 2 * kTile * D + lane * 4;
-            cp_async4(sc, a.k_scale + row, page < 0 ? 0 : 4);
-            cp_async4(sc + kTile * 4, a.v_scale + row, page < 0 ? 0 : 4);
+            return settle(u);
+        };
+        Cursor at = at_room(f0);
+        bool running = settle(at);
+        Cursor in = at;
+
+        // ---- loads: this lane's token of the tile to load next
+        const int in_page = (1 << a.page_shift) - 1;
+        constexpr int kPerRow = D / 16, kPerStep = 32 / kPerRow;   // 16-byte copies of a row; rows a step
+        const int chunk = lane % kPerRow, row_in = lane / kPerRow;
+        int64_t token_row = -1;   // its row in the cache, or -1
+        auto find_row = [&]() {
+            const int t = in.tile * kTile + lane;
+            token_row = -1;
+            if (t >= in.len) return;
+            const int p = a.page_table[in.b * a.table_stride + (t >> a.page_shift)];
+            if (p >= 0 && p < a.pages) {
+                const int h = in.unit / a.row_tiles;
+                token_row = ((static_cast<int64_t>(p) * a.kv_heads + h) << a.page_shift) + (t & in_page);
+            } else {
+                atomicOr(a.status, kStatusBadArgument);
+            }
+        };
+        auto load_codes = [&](const uint8_t* codes, uint32_t base) {
+            if (a.page_shift >= 5 && in.tile * kTile + kTile <= in.len) {
+                // a whole tile inside one page: one address for all of it
+                const int64_t first = __shfl_sync(0xFFFFFFFFu, token_row, 0);
+                const uint8_t* p = codes + (max(first, static_cast<int64_t>(0)) + row_in) * D + chunk * 16;
+                const uint32_t n = first < 0 ? 0 : 16;
+#pragma unroll
+                for (int i = 0; i < kTile / kPerStep; ++i)
+                    cp_async16(base + chunk_at<D>(i * kPerStep + row_in, chunk), p + i * kPerStep * D, n);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTile / kPerStep; ++i) {
+                    const int t = i * kPerStep + row_in;
+                    const int64_t r = __shfl_sync(0xFFFFFFFFu, token_row, t);
+                    cp_async16(base + chunk_at<D>(t, chunk),
+                               codes + max(r, static_cast<int64_t>(0)) * D + chunk * 16, r < 0 ? 0 : 16);
+                }
+            }
+        };
+        auto load_keys = [&](int stage) {   // and both scales
+            load_codes(a.k, ring + stage * S::kTileBytes);
+            const uint32_t sc = ring + S::kScaleAt + stage * (2 * kTile * 4) + lane * 4;
+            const int64_t r = max(token_row, static_cast<int64_t>(0));
+            cp_async4(sc, a.k_scale + r, token_row < 0 ? 0 : 4);
+            cp_async4(sc + kTile * 4, a.v_scale + r, token_row < 0 ? 0 : 4);
+        };
+        auto load_values = [&](int stage) {
+            load_codes(a.v, ring + (kStages + stage) * S::kTileBytes);
         };
 
-        Cursor in = start(f0), at = in;
-        int64_t fin = f0;
-        int page = page_of(in);
+        bool more = running;   // `in` is a tile of this run
+        if (more) find_row();
 #pragma unroll 1
         for (int s = 0; s < kStages; ++s) {
-            if (fin < f1) {
-                issue(in, page, s);
-                if (++fin < f1) {
-                    advance(in);
-                    page = page_of(in);
-                }
+            if (more) load_keys(s);
+            cp_commit();
+            if (more) {
+                load_values(s);
+                more = advance(in);
+                if (more) find_row();
             }
             cp_commit();
         }
 
-        uint32_t qa[D / 16][4];   // this unit's queries, as the first product's A operand
-        float qscale[2] = {0.0f, 0.0f};
-        int seen[2] = {0, 0}, seen_min = 0;
-        State<D> st;
-        int stage = 0, first_tile = 0;
+        // This unit's queries as the first product's B operand (row 8 n + g
+        // of the unit), and per row 8 n + 2c + i of this lane's scores:
+        uint32_t qb[NT][D / 16][2];
+        float qscale[NT][2];      // factor from MMA sums to base-2 scores
+        int seen[NT][2];          // tokens the row sees
+        float m[NT][2], l[NT][2]; // running maximum; this lane's part of l
+        float acc[D / 16][NT][4]; // [.][n][i]: dim pair's first, [.][n][2 + i]: second
+        int seen_min = 0, stage = 0, first_tile = 0, h = 0, r0 = 0;
+        bool fresh = true;
 
-        for (int64_t f = f0; f < f1; ++f) {
-            const int h = at.unit / a.row_tiles, r0 = (at.unit - h * a.row_tiles) * kRows;
-            if (f == f0 || at.tile == 0) {
+        while (running) {
+            if (fresh) {
                 // ---- a new unit: its queries, normalised by a power of two
+                fresh = false;
+                h = at.unit / a.row_tiles;
+                r0 = (at.unit - h * a.row_tiles) * kRows;
                 first_tile = at.tile;
-                const int len = at.len;
-                seen_min = 0x7FFFFFFF;
+                seen_min = at.len;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = r0 + g + 8 * j;
+                for (int n = 0; n < NT; ++n) {
+                    const int r = r0 + 8 * n + g;
                     const bool valid = r < a.rows;
                     int64_t token = 0;
                     int head = 0;
                     if (valid) row_place(a, at.b, h, r, &token, &head);
                     const uint16_t* src = a.q + token * a.q_ts + head * a.q_hs;
                     uint4 w[D / 32];
-                    uint32_t top = 0;
 #pragma unroll
                     for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
-                        for (int i = 0; i < S::kDims / 8; ++i) {
-                            const int k = p * (S::kDims / 8) + i;
-                            w[k] = valid ? *reinterpret_cast<const uint4*>(src + p * S::kSpan + c * S::kDims + 8 * i)
-                                         : make_uint4(0, 0, 0, 0);
-                        }
-                    float mul = 1.0f;
-                    qscale[j] = a.scale_log2;
+                        for (int i = 0; i < S::kDims / 8; ++i)
+                            w[p * (S::kDims / 8) + i] =
+                                valid ? *reinterpret_cast<const uint4*>(src + p * S::kSpan + c * S::kDims + 8 * i)
+                                      : make_uint4(0, 0, 0, 0);
+                    float mul = 1.0f, factor = a.scale_log2;
                     if constexpr (!kFp16) {
                         // BF16 queries: FP16 has more mantissa but less
                         // range, so a row is scaled by a power of two that
                         // brings its largest value to [1, 2).
+                        uint32_t top = 0;
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k) {
                             const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
@@ -416,7 +515,7 @@ attn_split_kernel(const AttnArgs a) {
                         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                         const int e = min(max(static_cast<int>(top >> 7), 1), 253);   // biased exponent
                         mul = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                        qscale[j] *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+                        factor *= __uint_as_float(static_cast<uint32_t>(e) << 23);
                     }
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
@@ -427,182 +526,204 @@ attn_split_kernel(const AttnArgs a) {
                             if constexpr (!kFp16)
                                 v = f32x2_to_f16x2(__uint_as_float(v << 16) * mul,
                                                    __uint_as_float(v & 0xFFFF0000u) * mul);
-                            // dims 8k + 2i, +1: MMA step 2k + i/2, k columns 2c.. (i even) or 2c + 8..
-                            qa[2 * k + (i >> 1)][2 * (i & 1) + j] = v;
+                            // dims 8k + 2i, +1 of the lane's run: MMA step 2k + i/2
+                            qb[n][2 * k + (i >> 1)][i & 1] = v;
                         }
                     }
-                    const int i = r / a.group;
-                    seen[j] = !valid || !a.causal ? len : max(0, len - a.q_len + 1 + i);
-                    if (valid) seen_min = min(seen_min, seen[j]);
-                    st.m[j] = -INFINITY;
-                    st.l[j] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int rr = r0 + 8 * n + 2 * c + i;
+                        qscale[n][i] = __shfl_sync(0xFFFFFFFFu, factor, 4 * (2 * c + i));
+                        seen[n][i] = rr >= a.rows || !a.causal
+                                         ? at.len
+                                         : max(0, at.len - a.q_len + 1 + rr / a.group);
+                        seen_min = min(seen_min, seen[n][i]);
+                        m[n][i] = -INFINITY;
+                        l[n][i] = 0.0f;
+                    }
                 }
                 seen_min = __reduce_min_sync(0xFFFFFFFFu, seen_min);
-                seen_min = min(seen_min, len);
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j)
+                for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) st.acc[j][i] = 0.0f;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[j][n][i] = 0.0f;
             }
 
-            cp_wait<kStages - 1>();
+            // ---- scores: s[t][n][..] of tokens 4g + 2t (first two) and 4g + 2t + 1
+            cp_wait<2 * kStages - 1>();
             __syncwarp();
-            const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + kTile * D;
-            const float* sk = reinterpret_cast<const float*>(smem + (kb - smem_addr(smem)) + 2 * kTile * D);
-            const float* sv = sk + kTile;
-
-            // ---- scores
-            float s[4][4];
+            const uint32_t kb = ring + stage * S::kTileBytes, vb = ring + (kStages + stage) * S::kTileBytes;
+            const float* sc = reinterpret_cast<const float*>(mine + S::kScaleAt + stage * (2 * kTile * 4));
+            {   // this lane's token: log2 and reciprocal of the value's scale
+                const float sv = sc[kTile + lane];
+                const float safe = sv < 0x1p-100f ? 0x1p-100f : sv;
+                logs[lane] = __log2f(safe);
+                logs[kTile + lane] = rcp(safe);
+            }
+            const float4 sk4 = *reinterpret_cast<const float4*>(sc + 4 * g);
+            float s[2][NT][4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
-            if constexpr (D == 64) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint4 x = lds128(kb + chunk_at<D>(8 * n + g, c));
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma16816(s[n], qa[i][0], qa[i][1], qa[i][2], qa[i][3], half2_of(w[i], 0),
-                                 half2_of(w[i], 1));
-                }
-            } else {
+                    for (int i = 0; i < 4; ++i) s[t][n][i] = 0.0f;
 #pragma unroll
                 for (int p = 0; p < D / 64; ++p) {
+                    const int ch = D == 64 ? c : 8 * (p >> 1) + 2 * c + (p & 1);
+                    const uint4 x = lds128(kb + chunk_at<D>(4 * g + 2 * t, ch));
+                    const uint4 y = lds128(kb + chunk_at<D>(4 * g + 2 * t + 1, ch));
+                    const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint4 x = lds128(kb + chunk_at<D>(8 * n + g, 8 * (p >> 1) + 2 * c + (p & 1)));
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_halves(wx[i], &a0, &a2);
+                        codes_to_halves(wy[i], &a1, &a3);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma16816(s[n], qa[4 * p + i][0], qa[4 * p + i][1], qa[4 * p + i][2],
-                                     qa[4 * p + i][3], half2_of(w[i], 0), half2_of(w[i], 1));
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(s[t][n], a0, a1, a2, a3, qb[n][4 * p + i][0], qb[n][4 * p + i][1]);
                     }
                 }
             }
+            __syncwarp();   // the keys are read, the logs written
+            if (more) load_keys(stage);
+            cp_commit();
 
-            // ---- softmax: lane holds tokens 8n + 2c, +1 of rows g (s[n][0..1]) and g + 8
-            const int t0 = at.tile * kTile;
-            const bool masked = t0 + kTile > seen_min;
-            // this lane's token: log2 and reciprocal of the value's scale
-            const float own_sv = sv[lane];
-            const float safe_sv = own_sv < 0x1p-100f ? 0x1p-100f : own_sv;
-            const float own_log = __log2f(safe_sv), own_rcp = __frcp_rn(safe_sv);
-            float rsv[4][2];
-            float top[2] = {-INFINITY, -INFINITY};
+            // ---- softmax
+            const float4 lg4 = *reinterpret_cast<const float4*>(logs + 4 * g);
+            const float4 rs4 = *reinterpret_cast<const float4*>(logs + kTile + 4 * g);
+            const float kk[4] = {sk4.x, sk4.y, sk4.z, sk4.w}, lg[4] = {lg4.x, lg4.y, lg4.z, lg4.w};
+            const float rsv[4] = {rs4.x, rs4.y, rs4.z, rs4.w};
+            const int t0 = at.tile * kTile + 4 * g;   // this lane's tokens: t0 .. t0 + 3
+            const bool masked = at.tile * kTile + kTile > seen_min;
+            float top[NT][2];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float2 k2 = *reinterpret_cast<const float2*>(sk + 8 * n + 2 * c);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int tok = 8 * n + 2 * c + i;
-                    const float lg = __shfl_sync(0xFFFFFFFFu, own_log, tok);
-                    rsv[n][i] = __shfl_sync(0xFFFFFFFFu, own_rcp, tok);
-                    const float kk = i == 0 ? k2.x : k2.y;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float y = fmaf(s[n][2 * j + i] * kk, qscale[j], lg);
-                        if (masked && t0 + tok >= seen[j]) y = -INFINITY;
-                        s[n][2 * j + i] = y;
-                        top[j] = fmaxf(top[j], y);
+                    for (int q = 0; q < 4; ++q) {
+                        float& y = s[q >> 1][n][2 * (q & 1) + i];
+                        y = fmaf(y * kk[q], qscale[n][i], lg[q]);
                     }
+                    if (masked) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (t0 + q >= seen[n][i]) s[q >> 1][n][2 * (q & 1) + i] = -INFINITY;
+                    }
+                    top[n][i] = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
                 }
-            }
-            float base[2];
             bool grew = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 1));
-                top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], 2));
-                grew |= top[j] > st.m[j];
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[n][i] = fmaxf(top[n][i], __shfl_xor_sync(0xFFFFFFFFu, top[n][i], 4));
+                    top[n][i] = fmaxf(top[n][i], __shfl_xor_sync(0xFFFFFFFFu, top[n][i], 8));
+                    top[n][i] = fmaxf(top[n][i], __shfl_xor_sync(0xFFFFFFFFu, top[n][i], 16));
+                    grew |= top[n][i] > m[n][i];
+                }
             if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float m = fmaxf(st.m[j], top[j]);
-                    const float f = m == -INFINITY ? 1.0f : ex2(st.m[j] - m);
-                    st.m[j] = m;
-                    st.l[j] *= f;
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < D / 8; ++k) {
-                        st.acc[k][2 * j] *= f;
-                        st.acc[k][2 * j + 1] *= f;
+                    for (int i = 0; i < 2; ++i) {
+                        const float to = fmaxf(m[n][i], top[n][i]);
+                        const float by = to == -INFINITY ? 1.0f : ex2(m[n][i] - to);
+                        m[n][i] = to;
+                        l[n][i] *= by;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            acc[j][n][i] *= by;
+                            acc[j][n][2 + i] *= by;
+                        }
                     }
-                }
             }
+            // weights, turned from (token, row) to the second product's B
+            // operand (row, token pair)
+            uint32_t wt[2][NT][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) base[j] = st.m[j] == -INFINITY ? 0.0f : st.m[j];
-            uint32_t pw[4][2];
+            for (int n = 0; n < NT; ++n) {
+                float w[4][2];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+                for (int i = 0; i < 2; ++i) {
+                    const float base = m[n][i] == -INFINITY ? 0.0f : m[n][i];
+                    float part = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float w0 = ex2(s[n][2 * j] - base[j]), w1 = ex2(s[n][2 * j + 1] - base[j]);
-                    // a token that a row does not see adds nothing, whatever its scale holds
-                    const int tok = t0 + 8 * n + 2 * c;
-                    if (!masked || tok < seen[j]) st.l[j] += w0 * rsv[n][0];
-                    if (!masked || tok + 1 < seen[j]) st.l[j] += w1 * rsv[n][1];
-                    pw[n][j] = f32x2_to_f16x2(w0, w1);
+                    for (int q = 0; q < 4; ++q) w[q][i] = ex2(s[q >> 1][n][2 * (q & 1) + i] - base);
+                    if (masked) {   // a token that a row does not see adds nothing, whatever its scale holds
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (t0 + q < seen[n][i]) part = fmaf(w[q][i], rsv[q], part);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) part = fmaf(w[q][i], rsv[q], part);
+                    }
+                    l[n][i] += part;
                 }
-
-            // ---- values: tokens 2c, 2c+1, 2c+8, 2c+9 of each 16; dims of chunk g
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int t = 16 * kk + 2 * c;
-                const uint32_t a0 = pw[2 * kk][0], a1 = pw[2 * kk][1], a2 = pw[2 * kk + 1][0],
-                               a3 = pw[2 * kk + 1][1];
-                auto words = [&](int j0, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
-                    const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
-                    const uint32_t lp = __byte_perm(x2, x3, 0x5140), hp = __byte_perm(x2, x3, 0x7362);
-                    mma16816(st.acc[j0], a0, a1, a2, a3, half2_of(lo, 0), half2_of(lp, 0));
-                    mma16816(st.acc[j0 + 1], a0, a1, a2, a3, half2_of(lo, 1), half2_of(lp, 1));
-                    mma16816(st.acc[j0 + 2], a0, a1, a2, a3, half2_of(hi, 0), half2_of(hp, 0));
-                    mma16816(st.acc[j0 + 3], a0, a1, a2, a3, half2_of(hi, 1), half2_of(hp, 1));
+                for (int q = 0; q < 4; ++q)
+                    wt[q >> 1][n][q & 1] = transpose8x8(f32x2_to_f16x2(w[q][0], w[q][1]));
+            }
+
+            // ---- values: k columns 2c, 2c + 1 of MMA t are tokens 8c + 2t, 8c + 4 + 2t,
+            // columns 2c + 8, + 9 the tokens after them; dims of chunk g
+            cp_wait<2 * kStages - 1>();
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tok = 8 * c + 2 * t;
+                auto words = [&](int j, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+                    uint32_t p[4], q[4];   // dims of bytes 0..3: token pairs 0, 1 and 2, 3
+                    codes_to_halves(__byte_perm(x0, x1, 0x5140), &p[0], &p[1]);
+                    codes_to_halves(__byte_perm(x0, x1, 0x7362), &p[2], &p[3]);
+                    codes_to_halves(__byte_perm(x2, x3, 0x5140), &q[0], &q[1]);
+                    codes_to_halves(__byte_perm(x2, x3, 0x7362), &q[2], &q[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(acc[j][n], p[0], p[1], q[0], q[1], wt[t][n][0], wt[t][n][1]);
+                        mma16816(acc[j + 1][n], p[2], p[3], q[2], q[3], wt[t][n][0], wt[t][n][1]);
+                    }
                 };
                 if constexpr (D == 64) {
                     const int ch = g >> 1, part = (g & 1) * 8;
-                    const uint2 x0 = lds64(vb + chunk_at<D>(t, ch) + part);
-                    const uint2 x1 = lds64(vb + chunk_at<D>(t + 1, ch) + part);
-                    const uint2 x2 = lds64(vb + chunk_at<D>(t + 8, ch) + part);
-                    const uint2 x3 = lds64(vb + chunk_at<D>(t + 9, ch) + part);
+                    const uint2 x0 = lds64(vb + chunk_at<D>(tok, ch) + part);
+                    const uint2 x1 = lds64(vb + chunk_at<D>(tok + 4, ch) + part);
+                    const uint2 x2 = lds64(vb + chunk_at<D>(tok + 1, ch) + part);
+                    const uint2 x3 = lds64(vb + chunk_at<D>(tok + 5, ch) + part);
                     words(0, x0.x, x1.x, x2.x, x3.x);
-                    words(4, x0.y, x1.y, x2.y, x3.y);
+                    words(2, x0.y, x1.y, x2.y, x3.y);
                 } else {
 #pragma unroll
                     for (int p = 0; p < S::kParts; ++p) {
-                        const uint4 x0 = lds128(vb + chunk_at<D>(t, 8 * p + g));
-                        const uint4 x1 = lds128(vb + chunk_at<D>(t + 1, 8 * p + g));
-                        const uint4 x2 = lds128(vb + chunk_at<D>(t + 8, 8 * p + g));
-                        const uint4 x3 = lds128(vb + chunk_at<D>(t + 9, 8 * p + g));
-                        words(16 * p, x0.x, x1.x, x2.x, x3.x);
-                        words(16 * p + 4, x0.y, x1.y, x2.y, x3.y);
-                        words(16 * p + 8, x0.z, x1.z, x2.z, x3.z);
-                        words(16 * p + 12, x0.w, x1.w, x2.w, x3.w);
+                        const uint4 x0 = lds128(vb + chunk_at<D>(tok, 8 * p + g));
+                        const uint4 x1 = lds128(vb + chunk_at<D>(tok + 4, 8 * p + g));
+                        const uint4 x2 = lds128(vb + chunk_at<D>(tok + 1, 8 * p + g));
+                        const uint4 x3 = lds128(vb + chunk_at<D>(tok + 5, 8 * p + g));
+                        words(8 * p, x0.x, x1.x, x2.x, x3.x);
+                        words(8 * p + 2, x0.y, x1.y, x2.y, x3.y);
+                        words(8 * p + 4, x0.z, x1.z, x2.z, x3.z);
+                        words(8 * p + 6, x0.w, x1.w, x2.w, x3.w);
                     }
                 }
             }
-
-            // ---- refill the stage
             __syncwarp();
-            if (fin < f1) {
-                issue(in, page, stage);
-                if (++fin < f1) {
-                    advance(in);
-                    page = page_of(in);
-                }
+            if (more) {
+                load_values(stage);
+                more = advance(in);
+                if (more) find_row();
             }
             cp_commit();
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
             // ---- the unit's (or the run's) end
             const bool unit_end = at.tile + 1 == at.ntile;
-            if (unit_end || f + 1 == f1) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    st.l[j] += __shfl_xor_sync(0xFFFFFFFFu, st.l[j], 1);
-                    st.l[j] += __shfl_xor_sync(0xFFFFFFFFu, st.l[j], 2);
-                }
+            const int was_b = at.b, was_unit = at.unit;
+            running = advance(at);
+            if (unit_end || !running) {
+                fresh = true;
                 const bool whole = unit_end && first_tile == 0;
                 // first piece of the run when its unit began before it, else the last one
                 const bool is_head = !whole && first_tile != 0;
@@ -612,128 +733,133 @@ attn_split_kernel(const AttnArgs a) {
                     __syncwarp();
                 }
                 if (!whole && lane == 0) {
-                    piece_b[2 * warp + (is_head ? 0 : 1)] = at.b;
-                    piece_unit[2 * warp + (is_head ? 0 : 1)] = at.unit;
+                    piece_b[2 * warp + (is_head ? 0 : 1)] = was_b;
+                    piece_unit[2 * warp + (is_head ? 0 : 1)] = was_unit;
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int rr = g + 8 * j;
-                    const bool valid = r0 + rr < a.rows;
-                    int64_t token = 0;
-                    int head = 0;
-                    if (valid) row_place(a, at.b, h, r0 + rr, &token, &head);
-                    float* row = stash + rr * S::kState;
-                    if (!whole && c == 0) {
-                        row[0] = st.m[j];
-                        row[1] = st.l[j];
-                    }
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int p = 0; p < S::kParts; ++p) {
+                    for (int i = 0; i < 2; ++i) {
+                        l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 4);
+                        l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
+                        l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
+                        const int rr = 8 * n + 2 * c + i;
+                        if (r0 + rr >= a.rows) continue;
+                        RowEnd e;
+                        if (whole) {
+                            int64_t token;
+                            int head;
+                            row_place(a, was_b, h, r0 + rr, &token, &head);
+                            e = row_end<D>(a, token, head, m[n][i], l[n][i], g == 0);
+                        } else {
+                            e.state = stash + rr * S::kState;
+                            if (g == 0) {
+                                e.state[0] = m[n][i];
+                                e.state[1] = l[n][i];
+                            }
+                        }
+                        // dims of chunk g, two per MMA tile
 #pragma unroll
-                        for (int k = 0; k < S::kDims / 4; ++k) {
-                            // column 2c of n-tile i is dim c * kDims + i, column 2c + 1 dim + kDims / 2
-                            const int half = k / (S::kDims / 8), i = (k % (S::kDims / 8)) * 4;
-                            const int e = 2 * j + half, n = p * (S::kDims / 2) + i;
-                            const float4 x = make_float4(st.acc[n][e], st.acc[n + 1][e],
-                                                         st.acc[n + 2][e], st.acc[n + 3][e]);
-                            const int d = p * S::kSpan + c * S::kDims + 4 * k;
-                            if (!whole)
-                                *reinterpret_cast<float4*>(row + 4 + d) = x;
-                            else if (valid)
-                                emit4<D, kFp16>(a, token, head, d, st.m[j], st.l[j], x);
+                        for (int k = 0; k < D / 32; ++k) {
+                            const float4 x = make_float4(acc[2 * k][n][i], acc[2 * k][n][2 + i],
+                                                         acc[2 * k + 1][n][i], acc[2 * k + 1][n][2 + i]);
+                            const int part = k / (S::kSpan / 32), in_part = k % (S::kSpan / 32);
+                            emit4<D, kFp16>(e, part * S::kSpan + g * (S::kSpan / 8) + 4 * in_part, x);
                         }
                     }
-                }
             }
-            if (f + 1 < f1) advance(at);
         }
         cp_wait<0>();
     }
     __syncthreads();
 
-    // ---- join the pieces of each unit, in warp (token) order
-    for (int i = 0; i < 2 * kWarps;) {
-        const int b = piece_b[i];
-        if (b < 0) {
-            ++i;
-            continue;
-        }
-        const int unit = piece_unit[i];
-        int end = i + 1;
-        while (end < 2 * kWarps && (piece_b[end] < 0 || (piece_b[end] == b && piece_unit[end] == unit))) ++end;
-        const int64_t ntile = cum[b + 1] - cum[b];
-        const int64_t u0 = static_cast<int64_t>(cum[b]) * units + unit * ntile, u1 = u0 + ntile;
-        const bool inside = u0 >= block0 && u1 <= block1;
-        float* slot = a.slots + (2 * static_cast<int64_t>(blockIdx.x) + (u0 < block0 ? 0 : 1)) *
-                                    (kRows * S::kState);
+    // ---- join the pieces of each unit, in warp (token) order.  Lane p of
+    // every warp looks at piece p; a unit's pieces are neighbours among those
+    // that exist, and its rows are dealt out over the warps.
+    static_assert(2 * kWarps <= 32, "a lane per piece");
+    bool crossed = false;
+    const int my_b = lane < 2 * kWarps ? piece_b[lane] : -1;
+    const int my_unit = my_b >= 0 ? piece_unit[lane] : 0;
+    const uint32_t exist = __ballot_sync(0xFFFFFFFFu, my_b >= 0);
+    const uint32_t below = exist & ((1u << lane) - 1u);
+    const int prev = below != 0 ? 31 - __clz(below) : lane;
+    const int prev_b = __shfl_sync(0xFFFFFFFFu, my_b, prev), prev_unit = __shfl_sync(0xFFFFFFFFu, my_unit, prev);
+    uint32_t starts = __ballot_sync(0xFFFFFFFFu, my_b >= 0 && (below == 0 || prev_b != my_b || prev_unit != my_unit));
+    const uint8_t* my_piece = (lane & 1) ? smem + (lane >> 1) * S::kRingBytes
+                                         : smem + kWarps * S::kRingBytes + (lane >> 1) * S::kStashBytes;
+    int turn = 0;   // (unit, row) pairs so far
+    while (starts != 0) {
+        const int first = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const uint32_t upto = starts != 0 ? (starts & -starts) - 1u : 0xFFFFFFFFu;
+        const uint32_t chain = exist & upto & ~((1u << first) - 1u);
+        const int b = __shfl_sync(0xFFFFFFFFu, my_b, first), unit = __shfl_sync(0xFFFFFFFFu, my_unit, first);
+        const int64_t room = cum[b + 1] - cum[b];
+        const int64_t u0 = static_cast<int64_t>(cum[b]) * units + unit * room, u1 = u0 + room;
+        const bool begins = block0 <= u0 + kUnitCost, ends = u1 <= block1;
+        float* slot = a.slots + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * (kRows * S::kState);
         const int h = unit / a.row_tiles, r0 = (unit - h * a.row_tiles) * kRows;
         const int rows = min(kRows, a.rows - r0);
-        for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
-            const int r = e / (D / 4), d = 4 * (e % (D / 4));
-            float m = -INFINITY;
-            for (int p = i; p < end; ++p) {
-                if (piece_b[p] < 0) continue;
-                const uint8_t* base = (p & 1) ? smem + (p >> 1) * S::kRingBytes
-                                              : smem + kWarps * S::kRingBytes + (p >> 1) * S::kStashBytes;
-                m = fmaxf(m, reinterpret_cast<const float*>(base)[r * S::kState]);
-            }
-            const float safe = m == -INFINITY ? 0.0f : m;
-            float l = 0.0f;
-            float4 x = make_float4(0, 0, 0, 0);
-            for (int p = i; p < end; ++p) {
-                if (piece_b[p] < 0) continue;
-                const uint8_t* base = (p & 1) ? smem + (p >> 1) * S::kRingBytes
-                                              : smem + kWarps * S::kRingBytes + (p >> 1) * S::kStashBytes;
-                const float* row = reinterpret_cast<const float*>(base) + r * S::kState;
-                const float w = ex2(row[0] - safe);
-                const float4 y = *reinterpret_cast<const float4*>(row + 4 + d);
-                l += w * row[1];
-                x.x += w * y.x;
-                x.y += w * y.y;
-                x.z += w * y.z;
-                x.w += w * y.w;
-            }
-            if (inside) {
+        const bool mine_too = (chain >> lane & 1u) != 0;
+        for (int r = ((warp - turn) % kWarps + kWarps) % kWarps; r < rows; r += kWarps) {
+            const float2 ml = mine_too ? reinterpret_cast<const float2*>(my_piece)[r * (S::kState / 2)]
+                                       : make_float2(-INFINITY, 0.0f);
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float w = mine_too ? ex2(ml.x - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+            float l = mine_too ? w * ml.y : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            RowEnd e;
+            if (begins && ends) {
                 int64_t token;
                 int head;
                 row_place(a, b, h, r0 + r, &token, &head);
-                emit4<D, kFp16>(a, token, head, d, m, l, x);
+                e = row_end<D>(a, token, head, m, l, lane == 0);
             } else {
-                float* row = slot + r * S::kState;
-                *reinterpret_cast<float4*>(row + 4 + d) = x;
-                if (d == 0) {
-                    row[0] = m;
-                    row[1] = l;
+                e.state = slot + r * S::kState;
+                if (lane == 0) *reinterpret_cast<float2*>(e.state) = make_float2(m, l);
+            }
+#pragma unroll
+            for (int d0 = 0; d0 < D; d0 += 128) {
+                const int d = d0 + 4 * lane;
+                float4 x = make_float4(0, 0, 0, 0);
+                for (uint32_t left = chain; left != 0; left &= left - 1) {
+                    const int p = __ffs(left) - 1;
+                    const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
+                    const uint8_t* base = (p & 1) ? smem + (p >> 1) * S::kRingBytes
+                                                  : smem + kWarps * S::kRingBytes + (p >> 1) * S::kStashBytes;
+                    if (D >= 128 || d < D) {
+                        const float4 y = reinterpret_cast<const float4*>(base)[(r * S::kState + 4 + d) / 4];
+                        x = plus_scaled(x, wp, y);
+                    }
                 }
+                if (D >= 128 || d < D) emit4<D, kFp16>(e, d, x);
             }
         }
-        i = end;
+        turn += rows;
+        // what the joining kernel needs to know of this block's end
+        if (begins && !ends && threadIdx.x == 0) {
+            const int last = static_cast<int>((u1 - 1) / (kWarps * run));
+            a.crossings[blockIdx.x] = make_int4(b, unit, last, 0);
+            crossed = true;
+        }
     }
+    if (threadIdx.x == 0 && !crossed) a.crossings[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
 // Joins the units that cross blocks: block x of the grid takes the unit that
-// begins in block x's run of the split kernel and goes on past its end, warp
-// y one of its rows.
-template <int D, bool kFp16>
+// begins in block x of the split kernel and goes on past it, warp y one of
+// its rows.
+template <int D, int NT, bool kFp16>
 __global__ void __launch_bounds__(128)
-attn_join_kernel(const AttnArgs a, int split_blocks) {
-    constexpr int kState = Shape<D>::kState, kWarps = Shape<D>::kWarps;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint32_t warp_sum[4];
-    uint32_t* cum = reinterpret_cast<uint32_t*>(smem);
+attn_join_kernel(const AttnArgs a) {
+    constexpr int kState = Shape<D, NT>::kState, kRows = Shape<D, NT>::kRows;
     pdl_wait();
-    scan_tiles<128>(a, cum, warp_sum);
-    const int units = a.kv_heads * a.row_tiles;
-    const int64_t total = static_cast<int64_t>(cum[a.batch]) * units;
-    const int64_t per_block = kWarps * tiles_per_warp(total, static_cast<int64_t>(split_blocks) * kWarps);
-    const int64_t f0 = blockIdx.x * per_block, f1 = f0 + per_block;
-    if (f1 >= total) return;
-    const int b = find_request(cum, a.batch, units, f1);
-    const int64_t ntile = cum[b + 1] - cum[b], before = static_cast<int64_t>(cum[b]) * units;
-    const int unit = static_cast<int>((f1 - before) / ntile);
-    const int64_t u0 = before + unit * ntile, u1 = u0 + ntile;
-    if (u0 == f1 || u0 < f0) return;   // ends there, or began in an earlier block
-    const int last = static_cast<int>((u1 - 1) / per_block);
+    const int4 crossing = a.crossings[blockIdx.x];
+    if (crossing.x < 0) return;
+    const int b = crossing.x, unit = crossing.y, first = blockIdx.x, last = crossing.z;
     const int h = unit / a.row_tiles, r0 = (unit - h * a.row_tiles) * kRows;
     const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (r0 + r >= a.rows) return;
@@ -742,44 +868,79 @@ attn_join_kernel(const AttnArgs a, int split_blocks) {
     row_place(a, b, h, r0 + r, &token, &head);
     // slot 2x + 1 of the first block, then slot 2y of each later one
     auto state = [&](int blk) {
-        return a.slots + ((2 * static_cast<int64_t>(blk) + (blk == static_cast<int>(blockIdx.x) ? 1 : 0)) * kRows + r) * kState;
+        return a.slots + ((2 * static_cast<int64_t>(blk) + (blk == first ? 1 : 0)) * kRows + r) * kState;
     };
-    float m = -INFINITY;
-    for (int i = blockIdx.x + lane; i <= last; i += 32) m = fmaxf(m, state(i)[0]);
+    // Eight states at a time, their loads in flight together.
+    float4 x[D > 128 ? 2 : 1];
+    float m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float safe = m == -INFINITY ? 0.0f : m;
-    for (int d = 4 * lane; d < D; d += 128) {
-        float l = 0.0f;
-        float4 x = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int i = blockIdx.x; i <= last; ++i) {
-            const float* row = state(i);
-            const float w = ex2(row[0] - safe);
-            const float4 y = *reinterpret_cast<const float4*>(row + 4 + d);
-            l += w * row[1];
-            x.x += w * y.x;
-            x.y += w * y.y;
-            x.z += w * y.z;
-            x.w += w * y.w;
+    for (int k = 0; k < (D > 128 ? 2 : 1); ++k) x[k] = make_float4(0, 0, 0, 0);
+    const bool live = 4 * lane < D;
+    for (int i0 = first; i0 <= last; i0 += 8) {
+        float2 ml[8];
+        float4 y[8][D > 128 ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            if (i0 + i > last) continue;
+            const float* row = state(i0 + i);
+            ml[i] = *reinterpret_cast<const float2*>(row);
+            if (live) {
+#pragma unroll
+                for (int k = 0; k < (D > 128 ? 2 : 1); ++k)
+                    y[i][k] = *reinterpret_cast<const float4*>(row + 4 + 4 * lane + 128 * k);
+            }
         }
-        emit4<D, kFp16>(a, token, head, d, m, l, x);
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float w0 = ex2(m - base);
+        m = top;
+        l *= w0;
+#pragma unroll
+        for (int k = 0; k < (D > 128 ? 2 : 1); ++k) x[k] = scaled(x[k], w0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i > last) continue;
+            const float w = ex2(ml[i].x - base);
+            l = fmaf(w, ml[i].y, l);
+#pragma unroll
+            for (int k = 0; k < (D > 128 ? 2 : 1); ++k) x[k] = plus_scaled(x[k], w, y[i][k]);
+        }
+    }
+    const RowEnd e = row_end<D>(a, token, head, m, l, lane == 0);
+    if (live) {
+#pragma unroll
+        for (int k = 0; k < (D > 128 ? 2 : 1); ++k) emit4<D, kFp16>(e, 4 * lane + 128 * k, x[k]);
     }
 }
 
+template <int D, int NT, bool kFp16>
+cudaError_t run_split_nt(AttnArgs a, int blocks, cudaStream_t s) {
+    using S = Shape<D, NT>;
+    a.row_tiles = (a.rows + S::kRows - 1) / S::kRows;
+    const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
+    const size_t smem = S::kSmem + cum;
+    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, NT, kFp16>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(attn_split_kernel<D, NT, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(blocks, (std::min(S::kRows, a.rows) + 3) / 4);
+    return launch_kernel(attn_join_kernel<D, NT, kFp16>, grid, dim3(128), 0, s, a);
+}
+
+// 8-row units while a key head's rows fit one (a 16-row one would idle half
+// of its MMAs and registers), else 16-row ones; 256-wide heads leave no
+// registers for a second row tile.
 template <int D, bool kFp16>
 cudaError_t run_split(const AttnArgs& a, int blocks, cudaStream_t s) {
-    using S = Shape<D>;
-    const size_t cum = sizeof(uint32_t) * (a.batch + 1);
-    const size_t smem = S::kSmem + cum;
-    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, kFp16>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         S::kSmem + static_cast<int>(sizeof(uint32_t)) * (kAttnMaxBatch + 1));
-    if (e != cudaSuccess) return e;
-    e = launch_kernel(attn_split_kernel<D, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(std::max(1, blocks - 1), (std::min(kRows, a.rows) + 3) / 4);
-    return launch_kernel(attn_join_kernel<D, kFp16>, grid, dim3(128), cum, s, a, blocks);
+    if constexpr (D < 256) {
+        if (a.rows > 8) return run_split_nt<D, 2, kFp16>(a, blocks, s);
+    }
+    return run_split_nt<D, 1, kFp16>(a, blocks, s);
 }
 
 template <int D, bool kFp16>
@@ -802,7 +963,8 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.q_heads = L.q_heads;
     a.group = L.q_heads / a.kv_heads;
     a.scale_log2 = static_cast<float>(L.scale * 1.4426950408889634074);
-    a.slots = reinterpret_cast<float*>(L.scratch);
+    a.crossings = static_cast<int4*>(L.scratch);
+    a.slots = reinterpret_cast<float*>(a.crossings + L.sm_count);
     a.status = L.status;
     float* states = a.slots + attn_slot_floats(L.sm_count, D);
     if (L.prefix_len > 0) {
@@ -813,7 +975,6 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
         p.batch = 1;
         p.q_len = L.batch * L.q_len;
         p.rows = p.q_len * p.group;
-        p.row_tiles = (p.rows + kRows - 1) / kRows;
         p.states = states;
         const cudaError_t e = run_split<D, kFp16>(p, L.sm_count, s);
         if (e != cudaSuccess) return e;
@@ -826,7 +987,6 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.batch = L.batch;
     a.q_len = L.q_len;
     a.rows = L.q_len * a.group;
-    a.row_tiles = (a.rows + kRows - 1) / kRows;
     a.causal = true;
     return run_split<D, kFp16>(a, L.sm_count, s);
 }
@@ -834,12 +994,12 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
 }  // namespace
 
 int64_t attn_slot_floats(int sm_count, int head_dim) {
-    return static_cast<int64_t>(2) * sm_count * kRows * (head_dim + 4);
+    return static_cast<int64_t>(2) * sm_count * kMaxUnitRows * (head_dim + 4);
 }
 
 int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
                            int sm_count) {
-    int64_t n = attn_slot_floats(sm_count, head_dim);
+    int64_t n = attn_slot_floats(sm_count, head_dim) + static_cast<int64_t>(sm_count) * 4;
     if (prefix_len > 0) n += static_cast<int64_t>(batch) * q_len * q_heads * (head_dim + 4);
     return n * static_cast<int64_t>(sizeof(float));
 }

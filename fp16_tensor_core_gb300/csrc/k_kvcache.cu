@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
@@ -23,6 +24,12 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_once8(const void* p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
     return v;
 }
 
@@ -98,10 +105,12 @@ struct RopeArgs {
     int head_steps;        // heads are taken in this many interleaved sets (one per thread)
     int threads_per_token; // items * head_steps
     int tokens_per_block;
-    const int32_t* positions;
+    const int32_t* positions;   // null: nothing is rotated
     const float4* table;   // rows of rotary_dim floats: (cos, sin) per pair
     int64_t table_positions;
     float sign;            // -1 for the transposed rotation
+    const int32_t* slots;  // beside a cache write: a token whose slot is past
+    int64_t nslots;        // the cache is left alone; else null
     uint32_t* status;
 };
 
@@ -110,19 +119,14 @@ struct RopeArgs {
 // its cosines and sines stay in registers across the heads, and both halves
 // of a pair are in its hands, so each element is read and written once.
 template <bool kFp16, bool kHalf, int kHeads>
-__global__ void __launch_bounds__(256)
-rope_kernel(const RopeArgs a) {
+__device__ __forceinline__ void rope_block(const RopeArgs& a, int64_t block) {
     const int local = static_cast<int>(threadIdx.x) / a.threads_per_token;
     const int rest = static_cast<int>(threadIdx.x) - local * a.threads_per_token;
     const int item = rest % a.items, h0 = rest / a.items;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block + local;
-    pdl_wait();
+    const int64_t t = block * a.tokens_per_block + local;
     if (local >= a.tokens_per_block || t >= a.tokens) return;
-    const int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.table_positions) {
-        if (rest == 0) atomicOr(a.status, kStatusBadArgument);
-        return;
-    }
+    const int64_t pos = a.positions != nullptr ? a.positions[t] : 0;
+    const int slot = a.slots != nullptr ? a.slots[t] : -1;
     const int pair_items = kHalf ? a.rot8 / 2 : a.rot8;
     const bool turn = item < pair_items;
     // first (and for the half layout second) 8 dims of the item
@@ -139,6 +143,11 @@ rope_kernel(const RopeArgs a) {
             if (kHalf && turn) v1[k] = ld_once(x + h * a.x_hs + d1);
         }
     }
+    if (a.positions != nullptr && (pos < 0 || pos >= a.table_positions)) {
+        if (rest == 0) atomicOr(a.status, kStatusBadArgument);
+        return;
+    }
+    if (a.slots != nullptr && slot >= a.nslots) return;   // the cache's blocks report it
     constexpr int kPairs = kHalf ? 8 : 4;
     float c[kPairs], s[kPairs];
     if (turn) {
@@ -183,124 +192,139 @@ rope_kernel(const RopeArgs a) {
     }
 }
 
+template <bool kFp16, bool kHalf, int kHeads>
+__global__ void __launch_bounds__(256)
+rope_kernel(const RopeArgs a) {
+    pdl_wait();
+    rope_block<kFp16, kHalf, kHeads>(a, blockIdx.x);
+}
+
 // ------------------------------------------------------------ cache writes
 
 struct AppendArgs {
-    const uint16_t* q;
-    uint16_t* q_out;
     const uint16_t* k;
     const uint16_t* v;
-    int64_t q_ts, q_hs, o_ts, o_hs, k_ts, k_hs, v_ts, v_hs;
-    int q_heads;
+    int64_t k_ts, k_hs, v_ts, v_hs;
+    int64_t tokens;
     int dim;
     int rot;               // rotated dims (0: none)
-    int interleaved;
     const int32_t* positions;
     const float* table;
     int64_t table_positions;
     const int32_t* slots;
     dg_kv_cache cache;
     int page_shift;
-    int row_step;          // rows of a token between a lane group's rows
+    int row_blocks;        // blocks that share out a token's rows
+    int tokens_at_once;    // tokens whose rows one pass of a block holds
     uint32_t* status;
 };
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// One row (one head of one token) per group of kLanes lanes, 8 dims a lane;
-// a group takes kRows rows of its token.  A rotated lane also reads the 8
-// dims that its own are paired with (the other lane's line, from L1).
-template <bool kFp16, int kLanes, int kRows>
-__global__ void __launch_bounds__(128)
-kv_append_kernel(const AppendArgs a) {
-    constexpr int kGroups = 128 / kLanes;
-    const int l = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const int64_t t = blockIdx.x;
-    const int d = 8 * l;
-    const bool live = d < a.dim;
-    const bool turn = d < a.rot;
-    const int half = a.rot / 2;
-    const bool upper = !a.interleaved && d >= half;
-    const int dp = !turn || a.interleaved ? d : upper ? d - half : d + half;
-    const int kv_heads = a.cache.kv_heads;
-    const int rows = a.q_heads + 2 * kv_heads;
-    const int row0 = static_cast<int>(blockIdx.y) * (kGroups * kRows) + group;
-    pdl_wait();
-    const int slot = a.slots[t];
-    const int64_t nslots = a.cache.pages << a.page_shift;
-    const int64_t pos = a.rot > 0 ? a.positions[t] : 0;
-    const bool bad = slot >= nslots || (a.rot > 0 && (pos < 0 || pos >= a.table_positions));
-    if (bad) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusBadArgument);
-        return;
-    }
+__device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(q[2 * i], q[2 * i + 1]);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
 
-    uint4 own[kRows], pair[kRows];
+// E4M3(fl32(x / scale)) of 8 elements, scale finite and at least 2^-60, |x|
+// at most about 448 scale.  An IEEE division per element would cost more
+// than the memory time of the whole row, so the quotient is enclosed: with
+// r the rounded reciprocal, x * r (1 - 2^-21) and x * r (1 + 2^-21) lie on
+// either side of fl32(x / scale) (each step rounds by at most 2^-24 of the
+// value; quotients below 2^-100 have code 0 throughout).  Rounding to E4M3
+// is monotone, so where both ends have one code that is the quotient's; the
+// divisions are done for the few elements near the middle of two codes.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
+    const float r = __frcp_rn(scale);
+    const float below = r * (1.0f - 0x1p-21f), above = r * (1.0f + 0x1p-21f);
+    float q[8];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-        const int r = row0 + j * kGroups;
+    for (int i = 0; i < 8; ++i) q[i] = x[i] * below;
+    const uint2 lo = codes8(q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = x[i] * above;
+    const uint2 hi = codes8(q);
+    if (lo.x == hi.x && lo.y == hi.y) return lo;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], scale);
+    return codes8(q);
+}
+
+// A group of kLanes lanes owns one row (a key or value head) and walks over
+// kTokens tokens, 8 dims a lane: row and dims are fixed, so a token costs
+// little more than its loads.  A rotated lane also reads the 8 dims that its
+// own are paired with (the other lane's line, from L1).
+template <bool kFp16, bool kHalf, int kLanes, int kTokens>
+__device__ __forceinline__ void append_block(const AppendArgs& a, int64_t block) {
+    constexpr int kGroups = 256 / kLanes;
+    const int l = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int kv_heads = a.cache.kv_heads, rows = 2 * kv_heads;
+    const int64_t token_block = block / a.row_blocks;
+    const int row_block = static_cast<int>(block - token_block * a.row_blocks);
+    const int r = row_block * kGroups + (a.tokens_at_once > 1 ? group % rows : group);
+    const int local = a.tokens_at_once > 1 ? group / rows : 0;
+    const int64_t t0 = token_block * (a.tokens_at_once * kTokens) + local;
+    const int d = 8 * l;
+    const bool is_k = r < kv_heads;
+    const bool live = d < a.dim && r < rows && local < a.tokens_at_once;
+    const bool turn = live && is_k && d < a.rot;
+    const int half = a.rot / 2;
+    const bool upper = kHalf && d >= half;
+    const int h = is_k ? r : r - kv_heads;
+    const uint16_t* src = is_k ? a.k + h * a.k_hs + d : a.v + h * a.v_hs + d;
+    const int64_t ts = is_k ? a.k_ts : a.v_ts;
+    const int to_pair = !kHalf ? 0 : upper ? -half : half;
+    const int64_t nslots = a.cache.pages << a.page_shift;
+
+    uint4 own[kTokens], pair[kTokens];
+    int slot[kTokens];
+    int64_t pos[kTokens];
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+        const int64_t t = t0 + j * a.tokens_at_once;
         own[j] = pair[j] = make_uint4(0, 0, 0, 0);
-        if (r < rows && live) {
-            const uint16_t* src =
-                r < a.q_heads ? a.q + t * a.q_ts + r * a.q_hs
-                : r < a.q_heads + kv_heads ? a.k + t * a.k_ts + (r - a.q_heads) * a.k_hs
-                                           : a.v + t * a.v_ts + (r - a.q_heads - kv_heads) * a.v_hs;
-            own[j] = *reinterpret_cast<const uint4*>(src + d);
-            if (turn && !a.interleaved && r < a.q_heads + kv_heads)
-                pair[j] = *reinterpret_cast<const uint4*>(src + dp);
+        slot[j] = -1;
+        pos[j] = 0;
+        if (t < a.tokens) {
+            slot[j] = a.slots[t];
+            if (a.rot > 0) pos[j] = a.positions[t];
+            if (live) own[j] = *reinterpret_cast<const uint4*>(src + t * ts);
+            if (kHalf && turn) pair[j] = *reinterpret_cast<const uint4*>(src + t * ts + to_pair);
         }
     }
-    __syncwarp();   // q may be rotated in place: a row is read before any of it is written
-    // cosines and (signed) sines of this lane's dims
-    float c[8], s[8];
-    if (turn) {
-        const float* row = a.table + pos * a.rot;
-        if (a.interleaved) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(row + d + 4 * i));
-                c[4 * i] = c[4 * i + 1] = f.x;
-                s[4 * i] = -f.y;
-                s[4 * i + 1] = f.y;
-                c[4 * i + 2] = c[4 * i + 3] = f.z;
-                s[4 * i + 2] = -f.w;
-                s[4 * i + 3] = f.w;
-            }
-        } else {
-            const int i0 = upper ? d - half : d;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(row + 2 * i0 + 4 * i));
-                c[2 * i] = f.x;
-                s[2 * i] = upper ? f.y : -f.y;
-                c[2 * i + 1] = f.z;
-                s[2 * i + 1] = upper ? f.w : -f.w;
-            }
-        }
-    }
-    const int page = slot >> a.page_shift, at = slot & ((1 << a.page_shift) - 1);
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-        const int r = row0 + j * kGroups;
-        const bool is_q = r < a.q_heads, is_k = !is_q && r < a.q_heads + kv_heads;
+    for (int j = 0; j < kTokens; ++j) {
+        const bool bad = slot[j] >= nslots || pos[j] < 0 || (a.rot > 0 && pos[j] >= a.table_positions);
+        if (bad && threadIdx.x % kLanes == 0) atomicOr(a.status, kStatusBadArgument);
+        if (bad) slot[j] = -1;
         float x[8];
         unpack8<kFp16>(own[j], x);
-        if (turn && (is_q || is_k)) {
+        if (turn && slot[j] >= 0) {
             float y[8], p[8];
-            if (a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
-            } else {
+            const float* row = a.table + pos[j] * a.rot;
+            if constexpr (kHalf) {
                 unpack8<kFp16>(pair[j], p);
+                const int i0 = upper ? d - half : d;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + 2 * i0 + 4 * i));
+                    y[2 * i] = x[2 * i] * f.x + p[2 * i] * (upper ? f.y : -f.y);
+                    y[2 * i + 1] = x[2 * i + 1] * f.z + p[2 * i + 1] * (upper ? f.w : -f.w);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + d + 4 * i));
+                    y[4 * i] = x[4 * i] * f.x - x[4 * i + 1] * f.y;
+                    y[4 * i + 1] = x[4 * i + 1] * f.x + x[4 * i] * f.y;
+                    y[4 * i + 2] = x[4 * i + 2] * f.z - x[4 * i + 3] * f.w;
+                    y[4 * i + 3] = x[4 * i + 3] * f.z + x[4 * i + 2] * f.w;
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i] * c[i] + p[i] * s[i];
-#pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = y[i];
-        }
-        if (is_q) {
-            if (live)
-                *reinterpret_cast<uint4*>(a.q_out + t * a.o_ts + r * a.o_hs + d) = pack8<kFp16>(x);
         }
         // The rotated key goes to its scale and code in FP32, not through a
         // 16-bit rounding.
@@ -310,24 +334,27 @@ kv_append_kernel(const AppendArgs a) {
 #pragma unroll
         for (int w = kLanes / 2; w > 0; w >>= 1)
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-        if (is_q || r >= rows || slot < 0) continue;
-        const int h = is_k ? r - a.q_heads : r - a.q_heads - kv_heads;
-        const int64_t row = ((static_cast<int64_t>(page) * kv_heads + h) << a.page_shift) + at;
+        if (!live || slot[j] < 0) continue;
+        const int64_t page = slot[j] >> a.page_shift;
+        const int64_t row = ((page * kv_heads + h) << a.page_shift) + (slot[j] & ((1 << a.page_shift) - 1));
         const bool finite = top < 0x7F800000u;
         const float scale = finite ? fmaxf(__fdiv_rn(__uint_as_float(top), 448.0f), kKvMinScale)
                                    : __int_as_float(0x7FC00000);
-        if (live) {
-            uint32_t code[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                code[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
-            const uint2 packed = finite ? make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16)
-                                        : make_uint2(0, 0);
-            uint8_t* codes = is_k ? a.cache.k : a.cache.v;
-            *reinterpret_cast<uint2*>(codes + row * a.dim + d) = packed;
-        }
+        const uint2 packed = finite ? quantise8(x, scale) : make_uint2(0, 0);
+        *reinterpret_cast<uint2*>((is_k ? a.cache.k : a.cache.v) + row * a.dim + d) = packed;
         if (l == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
     }
+}
+
+// The first q_blocks blocks turn the queries, the others write the cache.
+template <bool kFp16, bool kHalf, int kLanes, int kTokens>
+__global__ void __launch_bounds__(256)
+kv_append_kernel(const AppendArgs a, const RopeArgs q, int64_t q_blocks) {
+    pdl_wait();
+    if (blockIdx.x < q_blocks)
+        rope_block<kFp16, kHalf, kTokens>(q, blockIdx.x);
+    else
+        append_block<kFp16, kHalf, kLanes, kTokens>(a, blockIdx.x - q_blocks);
 }
 
 // ------------------------------------------------------------- cache reads
@@ -340,70 +367,71 @@ struct ReadArgs {
     uint16_t* k;
     uint16_t* v;
     int64_t k_ts, k_hs, v_ts, v_hs;
-    int chunks;            // head_dim / 16
-    int per_token;         // chunks * kv_heads * tensors
-    int tokens_per_block;
+    int chunks;            // head_dim / 8
+    int items;             // chunks * kv_heads * tensors
+    int item_blocks;       // blocks that share out a token's items
+    int tokens_at_once;    // tokens whose items one pass of a block holds
     uint32_t* status;
 };
 
-// 16 codes of one row a thread and step: code x scale in FP32 (exact: 4 + 24
-// bits need no more than one rounding), rounded once to the output type.
-template <bool kFp16>
+// A thread owns 8 dims of one row (a warp's stores are whole lines) and walks
+// over kTokens tokens: code x scale in FP32, rounded once to the output type.
+template <bool kFp16, int kTokens>
 __global__ void __launch_bounds__(256)
 kv_read_kernel(const ReadArgs a) {
-    pdl_wait();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
-    const int n = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_block), a.tokens - t0)) *
-                  a.per_token;
-    const int64_t nslots = a.cache.pages << a.page_shift;
+    const int64_t token_block = blockIdx.x / a.item_blocks;
+    const int item_block = static_cast<int>(blockIdx.x - token_block * a.item_blocks);
+    const int local = a.tokens_at_once > 1 ? threadIdx.x / a.items : 0;
+    const int item = item_block * 256 + static_cast<int>(threadIdx.x) - local * a.items;
+    if (item >= a.items || local >= a.tokens_at_once) return;
+    const int row = item / a.chunks, chunk = item - row * a.chunks;
     const int kv_heads = a.cache.kv_heads;
-    constexpr int kU = 4;
-    for (int i0 = threadIdx.x; i0 < n; i0 += 256 * kU) {
-        uint4 code[kU];
-        float scale[kU];
-        uint16_t* dst[kU];
+    const bool is_v = a.k == nullptr || row >= kv_heads;
+    const int h = row >= kv_heads ? row - kv_heads : row;
+    const uint8_t* codes = (is_v ? a.cache.v : a.cache.k) + 8 * chunk;
+    const float* scales = is_v ? a.cache.v_scale : a.cache.k_scale;
+    uint16_t* dst = (is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs) + 8 * chunk;
+    const int64_t ts = is_v ? a.v_ts : a.k_ts;
+    const int64_t nslots = a.cache.pages << a.page_shift;
+    const int64_t t0 = token_block * (a.tokens_at_once * kTokens) + local;
+    pdl_wait();
+    int slot[kTokens];
+    uint2 code[kTokens];
+    float scale[kTokens];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = i0 + 256 * u;
-            dst[u] = nullptr;
-            if (i >= n) continue;
-            const int lt = i / a.per_token, in_token = i - lt * a.per_token;
-            const int row = in_token / a.chunks, chunk = in_token - row * a.chunks;
-            const bool is_v = a.k == nullptr || row >= kv_heads;
-            const int h = row >= kv_heads ? row - kv_heads : row;
-            const int64_t t = t0 + lt;
-            const int slot = a.slots[t];
-            dst[u] = (is_v ? a.v + t * a.v_ts + h * a.v_hs : a.k + t * a.k_ts + h * a.k_hs) + 16 * chunk;
-            if (slot >= nslots) {
-                atomicOr(a.status, kStatusBadArgument);
-                dst[u] = nullptr;
-            } else if (slot < 0) {
-                code[u] = make_uint4(0, 0, 0, 0);
-                scale[u] = 0.0f;
-            } else {
-                const int64_t page = slot >> a.page_shift;
-                const int64_t r = ((page * kv_heads + h) << a.page_shift) +
-                                  (slot & ((1 << a.page_shift) - 1));
-                code[u] = ld_once((is_v ? a.cache.v : a.cache.k) + (r * a.chunks + chunk) * 16);
-                scale[u] = __ldg((is_v ? a.cache.v_scale : a.cache.k_scale) + r);
-            }
+    for (int j = 0; j < kTokens; ++j) {
+        const int64_t t = t0 + j * a.tokens_at_once;
+        slot[j] = t < a.tokens ? a.slots[t] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+        code[j] = make_uint2(0, 0);
+        scale[j] = 0.0f;
+        if (slot[j] >= 0 && slot[j] < nslots) {
+            const int64_t page = slot[j] >> a.page_shift;
+            const int64_t r = ((page * kv_heads + h) << a.page_shift) + (slot[j] & ((1 << a.page_shift) - 1));
+            code[j] = ld_once8(codes + r * (8 * a.chunks));
+            scale[j] = __ldg(scales + r);
         }
+    }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (dst[u] == nullptr) continue;
-            const uint32_t w[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 lo = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i])));
-                const float2 hi = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
-                o[2 * i] = pack2<kFp16>(lo.x * scale[u], lo.y * scale[u]);
-                o[2 * i + 1] = pack2<kFp16>(hi.x * scale[u], hi.y * scale[u]);
-            }
-            uint4* p = reinterpret_cast<uint4*>(dst[u]);
-            p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int j = 0; j < kTokens; ++j) {
+        const int64_t t = t0 + j * a.tokens_at_once;
+        if (t >= a.tokens) continue;
+        if (slot[j] >= nslots) {
+            if (chunk == 0) atomicOr(a.status, kStatusBadArgument);
+            continue;
         }
+        const uint32_t w[2] = {code[j].x, code[j].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 lo = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i])));
+            const float2 hi = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
+            o[2 * i] = pack2<kFp16>(lo.x * scale[j], lo.y * scale[j]);
+            o[2 * i + 1] = pack2<kFp16>(hi.x * scale[j], hi.y * scale[j]);
+        }
+        *reinterpret_cast<uint4*>(dst + t * ts) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -414,20 +442,12 @@ cudaError_t rope_dispatch(const RopeArgs& a, int heads_per_thread, dim3 grid, cu
                : launch_kernel(rope_kernel<kFp16, kHalf, 1>, grid, dim3(256), 0, s, a);
 }
 
-template <bool kFp16>
-cudaError_t append_dispatch(const AppendArgs& a, int64_t tokens, int rows, bool few, cudaStream_t s) {
-    const int lanes = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32;
-    const int per_block = 128 / lanes * (few ? 1 : 4);
-    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((rows + per_block - 1) / per_block));
-    const dim3 block(128);
-    if (few) {
-        if (lanes == 8) return launch_kernel(kv_append_kernel<kFp16, 8, 1>, grid, block, 0, s, a);
-        if (lanes == 16) return launch_kernel(kv_append_kernel<kFp16, 16, 1>, grid, block, 0, s, a);
-        return launch_kernel(kv_append_kernel<kFp16, 32, 1>, grid, block, 0, s, a);
-    }
-    if (lanes == 8) return launch_kernel(kv_append_kernel<kFp16, 8, 4>, grid, block, 0, s, a);
-    if (lanes == 16) return launch_kernel(kv_append_kernel<kFp16, 16, 4>, grid, block, 0, s, a);
-    return launch_kernel(kv_append_kernel<kFp16, 32, 4>, grid, block, 0, s, a);
+template <bool kFp16, bool kHalf, int kTokens>
+cudaError_t append_dispatch(const AppendArgs& a, const RopeArgs& q, int64_t q_blocks, dim3 grid,
+                            cudaStream_t s) {
+    if (a.dim <= 64) return launch_kernel(kv_append_kernel<kFp16, kHalf, 8, kTokens>, grid, dim3(256), 0, s, a, q, q_blocks);
+    if (a.dim <= 128) return launch_kernel(kv_append_kernel<kFp16, kHalf, 16, kTokens>, grid, dim3(256), 0, s, a, q, q_blocks);
+    return launch_kernel(kv_append_kernel<kFp16, kHalf, 32, kTokens>, grid, dim3(256), 0, s, a, q, q_blocks);
 }
 
 int shift_of(int page_size) {
@@ -447,10 +467,12 @@ cudaError_t launch_rope_table(float* table, int64_t positions, int rotary_dim,
                          reinterpret_cast<float2*>(table), positions, half, sc);
 }
 
-cudaError_t launch_rope(const dg_heads& x, const dg_heads& out, int64_t tokens, int heads,
-                        int head_dim, const int32_t* positions, const dg_rotary& rot, bool inverse,
-                        bool fp16, int sm_count, uint32_t* status, cudaStream_t s) {
-    RopeArgs a;
+namespace {
+
+// The arguments of a rotation but for the split over blocks.
+RopeArgs rope_args(const dg_heads& x, const dg_heads& out, int64_t tokens, int heads, int head_dim,
+                   const int32_t* positions, const dg_rotary* rot, bool inverse, uint32_t* status) {
+    RopeArgs a{};
     a.x = static_cast<const uint16_t*>(x.data);
     a.out = static_cast<uint16_t*>(out.data);
     a.x_ts = x.token_stride;
@@ -458,31 +480,47 @@ cudaError_t launch_rope(const dg_heads& x, const dg_heads& out, int64_t tokens, 
     a.o_ts = out.token_stride;
     a.o_hs = out.head_stride;
     a.tokens = tokens;
-    a.rot8 = rot.rotary_dim / 8;
     a.heads = heads;
-    const bool half = rot.layout == DG_ROPE_HALF;
+    if (rot != nullptr) {
+        a.rot8 = rot->rotary_dim / 8;
+        a.positions = positions;
+        a.table = reinterpret_cast<const float4*>(rot->table);
+        a.table_positions = rot->positions;
+    }
+    const bool half = rot == nullptr || rot->layout == DG_ROPE_HALF;
     a.items = half ? head_dim / 8 - a.rot8 / 2 : head_dim / 8;
-    // Four heads a thread once that still leaves every SM two blocks.
-    int per_thread = 4;
-    if (tokens * heads * a.items < static_cast<int64_t>(4) * 2 * sm_count * 256) per_thread = 1;
-    a.head_steps = (heads + per_thread - 1) / per_thread;
-    // A token has to fit one block: more heads a token than that are taken by further launches.
-    const int most = 256 / a.items;
-    const int64_t chunk_heads = static_cast<int64_t>(most) * per_thread;
-    a.positions = positions;
-    a.table = reinterpret_cast<const float4*>(rot.table);
-    a.table_positions = rot.positions;
     a.sign = inverse ? -1.0f : 1.0f;
     a.status = status;
-    for (int h = 0; h < heads; h += static_cast<int>(chunk_heads)) {
+    return a;
+}
+
+// Splits a rotation over blocks with `per_thread` heads a thread; false if a
+// token does not fit one block.  Returns the number of blocks.
+int64_t rope_split(RopeArgs* a, int per_thread) {
+    a->head_steps = (a->heads + per_thread - 1) / per_thread;
+    a->threads_per_token = a->items * a->head_steps;
+    if (a->threads_per_token > 256) return 0;
+    a->tokens_per_block = 256 / a->threads_per_token;
+    return (a->tokens + a->tokens_per_block - 1) / a->tokens_per_block;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const dg_heads& x, const dg_heads& out, int64_t tokens, int heads,
+                        int head_dim, const int32_t* positions, const dg_rotary& rot, bool inverse,
+                        bool fp16, int sm_count, uint32_t* status, cudaStream_t s) {
+    const RopeArgs a = rope_args(x, out, tokens, heads, head_dim, positions, &rot, inverse, status);
+    const bool half = rot.layout == DG_ROPE_HALF;
+    // Four heads a thread once that still leaves every SM two blocks.
+    const int per_thread = tokens * heads * a.items < static_cast<int64_t>(4) * 2 * sm_count * 256 ? 1 : 4;
+    // A token has to fit one block: more heads a token than that are taken by further launches.
+    const int most = 256 / a.items * per_thread;
+    for (int h = 0; h < heads; h += most) {
         RopeArgs b = a;
         b.x += h * a.x_hs;
         b.out += h * a.o_hs;
-        b.heads = static_cast<int>(std::min<int64_t>(chunk_heads, heads - h));
-        b.head_steps = (b.heads + per_thread - 1) / per_thread;
-        b.threads_per_token = b.items * b.head_steps;
-        b.tokens_per_block = 256 / b.threads_per_token;
-        const dim3 grid(static_cast<unsigned>((tokens + b.tokens_per_block - 1) / b.tokens_per_block));
+        b.heads = std::min(most, heads - h);
+        const dim3 grid(static_cast<unsigned>(rope_split(&b, per_thread)));
         cudaError_t e;
         if (fp16)
             e = half ? rope_dispatch<true, true>(b, per_thread, grid, s)
@@ -501,25 +539,16 @@ cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_hea
                              const dg_kv_cache& cache, bool fp16, int sm_count, uint32_t* status,
                              cudaStream_t s) {
     AppendArgs a{};
-    if (q != nullptr) {
-        a.q = static_cast<const uint16_t*>(q->data);
-        a.q_ts = q->token_stride;
-        a.q_hs = q->head_stride;
-        a.q_out = static_cast<uint16_t*>(q_out->data);
-        a.o_ts = q_out->token_stride;
-        a.o_hs = q_out->head_stride;
-        a.q_heads = q_heads;
-    }
     a.k = static_cast<const uint16_t*>(k.data);
     a.k_ts = k.token_stride;
     a.k_hs = k.head_stride;
     a.v = static_cast<const uint16_t*>(v.data);
     a.v_ts = v.token_stride;
     a.v_hs = v.head_stride;
+    a.tokens = tokens;
     a.dim = cache.head_dim;
     if (rot != nullptr) {
         a.rot = rot->rotary_dim;
-        a.interleaved = rot->layout == DG_ROPE_INTERLEAVED;
         a.table = rot->table;
         a.table_positions = rot->positions;
         a.positions = positions;
@@ -528,12 +557,60 @@ cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_hea
     a.cache = cache;
     a.page_shift = shift_of(cache.page_size);
     a.status = status;
-    const int rows = a.q_heads + 2 * cache.kv_heads;
-    // One row a lane group while the call has too few rows to fill the SMs
-    // (16 groups of 4 warps' worth each), four otherwise.
-    const bool few = tokens * rows < static_cast<int64_t>(sm_count) * 512;
-    return fp16 ? append_dispatch<true>(a, tokens, rows, few, s)
-                : append_dispatch<false>(a, tokens, rows, few, s);
+    const bool half = rot == nullptr || rot->layout == DG_ROPE_HALF;
+    const int lanes = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32;
+    const int groups = 256 / lanes, rows = 2 * cache.kv_heads;
+    a.row_blocks = (rows + groups - 1) / groups;
+    a.tokens_at_once = a.row_blocks == 1 ? groups / rows : 1;
+    // Four tokens a lane group (and four query heads a thread) once that
+    // still leaves every SM two blocks of cache rows.
+    const int64_t passes = (tokens + a.tokens_at_once - 1) / a.tokens_at_once;
+    const bool few = passes * a.row_blocks < static_cast<int64_t>(4) * 2 * sm_count;
+    const int per_block = a.tokens_at_once * (few ? 1 : 4);
+    const int64_t kv_blocks = (tokens + per_block - 1) / per_block * a.row_blocks;
+    RopeArgs qa{};
+    int64_t q_blocks = 0;
+    if (q != nullptr) {
+        qa = rope_args(*q, *q_out, tokens, q_heads, cache.head_dim, positions, rot, false, status);
+        qa.slots = slots;
+        qa.nslots = cache.pages * cache.page_size;
+        q_blocks = rope_split(&qa, few ? 1 : 4);
+        if (q_blocks == 0) {
+            // More heads than one block takes: a launch of their own.
+            const int most = 256 / qa.items * (few ? 1 : 4);
+            for (int h = most; h < q_heads; h += most) {
+                RopeArgs b = qa;
+                b.x += h * qa.x_hs;
+                b.out += h * qa.o_hs;
+                b.heads = std::min(most, q_heads - h);
+                const dim3 grid(static_cast<unsigned>(rope_split(&b, few ? 1 : 4)));
+                cudaError_t e;
+                if (fp16)
+                    e = half ? rope_dispatch<true, true>(b, few ? 1 : 4, grid, s)
+                             : rope_dispatch<true, false>(b, few ? 1 : 4, grid, s);
+                else
+                    e = half ? rope_dispatch<false, true>(b, few ? 1 : 4, grid, s)
+                             : rope_dispatch<false, false>(b, few ? 1 : 4, grid, s);
+                if (e != cudaSuccess) return e;
+            }
+            qa.heads = most;
+            q_blocks = rope_split(&qa, few ? 1 : 4);
+        }
+    }
+    if (q_blocks + kv_blocks > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks));
+    if (fp16) {
+        if (half)
+            return few ? append_dispatch<true, true, 1>(a, qa, q_blocks, grid, s)
+                       : append_dispatch<true, true, 4>(a, qa, q_blocks, grid, s);
+        return few ? append_dispatch<true, false, 1>(a, qa, q_blocks, grid, s)
+                   : append_dispatch<true, false, 4>(a, qa, q_blocks, grid, s);
+    }
+    if (half)
+        return few ? append_dispatch<false, true, 1>(a, qa, q_blocks, grid, s)
+                   : append_dispatch<false, true, 4>(a, qa, q_blocks, grid, s);
+    return few ? append_dispatch<false, false, 1>(a, qa, q_blocks, grid, s)
+               : append_dispatch<false, false, 4>(a, qa, q_blocks, grid, s);
 }
 
 cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64_t tokens,
@@ -554,16 +631,23 @@ cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64
         a.v_ts = v->token_stride;
         a.v_hs = v->head_stride;
     }
-    a.chunks = cache.head_dim / 16;
-    a.per_token = a.chunks * cache.kv_heads * ((k != nullptr) + (v != nullptr));
-    // About 1024 items (4 a thread) a block, fewer while that leaves SMs idle.
-    int per_block = std::max(1, 1024 / a.per_token);
-    while (per_block > 1 && tokens / per_block < 4 * sm_count) per_block /= 2;
-    a.tokens_per_block = per_block;
+    a.chunks = cache.head_dim / 8;
+    a.items = a.chunks * cache.kv_heads * ((k != nullptr) + (v != nullptr));
+    a.item_blocks = (a.items + 255) / 256;
+    a.tokens_at_once = a.item_blocks == 1 ? 256 / a.items : 1;
     a.status = status;
-    const dim3 grid(static_cast<unsigned>((tokens + per_block - 1) / per_block));
-    return fp16 ? launch_kernel(kv_read_kernel<true>, grid, dim3(256), 0, s, a)
-                : launch_kernel(kv_read_kernel<false>, grid, dim3(256), 0, s, a);
+    // Eight tokens a thread once that still leaves every SM four blocks.
+    const int64_t passes = (tokens + a.tokens_at_once - 1) / a.tokens_at_once;
+    const bool few = passes * a.item_blocks < static_cast<int64_t>(8) * 4 * sm_count;
+    const int per_block = a.tokens_at_once * (few ? 1 : 8);
+    const int64_t blocks = (tokens + per_block - 1) / per_block * a.item_blocks;
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (fp16)
+        return few ? launch_kernel(kv_read_kernel<true, 1>, grid, dim3(256), 0, s, a)
+                   : launch_kernel(kv_read_kernel<true, 8>, grid, dim3(256), 0, s, a);
+    return few ? launch_kernel(kv_read_kernel<false, 1>, grid, dim3(256), 0, s, a)
+               : launch_kernel(kv_read_kernel<false, 8>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace dg

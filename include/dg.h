@@ -463,7 +463,7 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  *   q, out      BF16 or FP16 (dtype), batch * q_len tokens, q_heads heads.
  *   lse         FP32[batch * q_len][q_heads], natural log of the sum of
  *               exponentials, or NULL.
- *   batch       0 .. 4096; q_len >= 1; q_heads a multiple of kv_heads.
+ *   batch       0 .. 2048; q_len >= 1; q_heads a multiple of kv_heads.
  *   page_table  int32, device: row b, at b * table_stride, names the pages of
  *               request b's tokens in order; max_pages entries a row.
  *   kv_lens     int32[batch], device, 0 .. max_pages * page_size each.  A

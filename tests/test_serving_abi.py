@@ -100,7 +100,7 @@ def test_kv_read(L, kw, expect):
 
 
 @pytest.mark.parametrize("kw,expect", CACHE_ERRORS + [
-    (dict(batch=-1), BAD), (dict(batch=4097), BAD), (dict(q_len=0), BAD), (dict(q_heads=0), BAD),
+    (dict(batch=-1), BAD), (dict(batch=2049), BAD), (dict(q_len=0), BAD), (dict(q_heads=0), BAD),
     (dict(q_heads=7), BAD), (dict(cache=cache(dim=96)), BAD), (dict(max_pages=-1), BAD),
     (dict(stride=3), BAD), (dict(max_pages=1 << 28, stride=1 << 28), BAD), (dict(lens=None), BAD),
     (dict(lens=FAKE + 1), OFF), (dict(table=None), BAD), (dict(table=FAKE + 2), OFF),
