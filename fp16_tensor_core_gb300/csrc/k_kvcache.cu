@@ -219,7 +219,12 @@ struct AppendArgs {
     uint32_t* status;
 };
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// max(|a|, |b|, |c|), NaN if any is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 __device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
     uint32_t c[4];
@@ -231,13 +236,15 @@ __device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
 // E4M3(fl32(x / scale)) of 8 elements, scale finite and at least 2^-60, |x|
 // at most about 448 scale.  An IEEE division per element would cost more
 // than the memory time of the whole row, so the quotient is enclosed: with
-// r the rounded reciprocal, x * r (1 - 2^-21) and x * r (1 + 2^-21) lie on
-// either side of fl32(x / scale) (each step rounds by at most 2^-24 of the
-// value; quotients below 2^-100 have code 0 throughout).  Rounding to E4M3
+// r the approximate reciprocal (off by at most 2^-23 of it), x * r (1 -
+// 2^-21) and x * r (1 + 2^-21) lie on either side of fl32(x / scale): the
+// two products and the quotient itself round by at most 2^-24 each
+// (quotients below 2^-100 have code 0 throughout).  Rounding to E4M3
 // is monotone, so where both ends have one code that is the quotient's; the
 // divisions are done for the few elements near the middle of two codes.
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
-    const float r = __frcp_rn(scale);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
     const float below = r * (1.0f - 0x1p-21f), above = r * (1.0f + 0x1p-21f);
     float q[8];
 #pragma unroll
@@ -257,15 +264,15 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
 // little more than its loads.  A rotated lane also reads the 8 dims that its
 // own are paired with (the other lane's line, from L1).
 template <bool kFp16, bool kHalf, int kLanes, int kTokens>
-__device__ __forceinline__ void append_block(const AppendArgs& a, int64_t block) {
+__device__ __forceinline__ void append_block(const AppendArgs& a, int block) {
     constexpr int kGroups = 256 / kLanes;
     const int l = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
     const int kv_heads = a.cache.kv_heads, rows = 2 * kv_heads;
-    const int64_t token_block = block / a.row_blocks;
-    const int row_block = static_cast<int>(block - token_block * a.row_blocks);
+    const int token_block = block / a.row_blocks;
+    const int row_block = block - token_block * a.row_blocks;
     const int r = row_block * kGroups + (a.tokens_at_once > 1 ? group % rows : group);
     const int local = a.tokens_at_once > 1 ? group / rows : 0;
-    const int64_t t0 = token_block * (a.tokens_at_once * kTokens) + local;
+    const int64_t t0 = static_cast<int64_t>(token_block) * (a.tokens_at_once * kTokens) + local;
     const int d = 8 * l;
     const bool is_k = r < kv_heads;
     const bool live = d < a.dim && r < rows && local < a.tokens_at_once;
@@ -328,33 +335,38 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t block)
         }
         // The rotated key goes to its scale and code in FP32, not through a
         // 16-bit rounding.
-        uint32_t top = 0;
+        float top = max3_abs(x[0], x[1], x[2]);
+        top = max3_abs(top, x[3], x[4]);
+        top = max3_abs(top, x[5], x[6]);
+        top = max3_abs(top, x[7], x[7]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, abs_bits(x[i]));
-#pragma unroll
-        for (int w = kLanes / 2; w > 0; w >>= 1)
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
+        for (int w = kLanes / 2; w > 0; w >>= 1) {
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, top, w);
+            top = max3_abs(top, other, other);
+        }
         if (!live || slot[j] < 0) continue;
         const int64_t page = slot[j] >> a.page_shift;
         const int64_t row = ((page * kv_heads + h) << a.page_shift) + (slot[j] & ((1 << a.page_shift) - 1));
-        const bool finite = top < 0x7F800000u;
-        const float scale = finite ? fmaxf(__fdiv_rn(__uint_as_float(top), 448.0f), kKvMinScale)
-                                   : __int_as_float(0x7FC00000);
+        const bool finite = top <= 3.4028235e38f;   // false for NaN
+        const float scale = finite ? fmaxf(__fdiv_rn(top, 448.0f), kKvMinScale) : __int_as_float(0x7FC00000);
         const uint2 packed = finite ? quantise8(x, scale) : make_uint2(0, 0);
         *reinterpret_cast<uint2*>((is_k ? a.cache.k : a.cache.v) + row * a.dim + d) = packed;
         if (l == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
     }
 }
 
-// The first q_blocks blocks turn the queries, the others write the cache.
+// Every kv_every-th block writes the cache (bound by its instructions), the
+// others turn the queries (bound by HBM): dealt out among one another they
+// share the SMs.
 template <bool kFp16, bool kHalf, int kLanes, int kTokens>
 __global__ void __launch_bounds__(256)
-kv_append_kernel(const AppendArgs a, const RopeArgs q, int64_t q_blocks) {
+kv_append_kernel(const AppendArgs a, const RopeArgs q, int kv_blocks, int kv_every) {
     pdl_wait();
-    if (blockIdx.x < q_blocks)
-        rope_block<kFp16, kHalf, kTokens>(q, blockIdx.x);
+    const int round = static_cast<int>(blockIdx.x) / kv_every;
+    if (round < kv_blocks && static_cast<int>(blockIdx.x) - round * kv_every == kv_every - 1)
+        append_block<kFp16, kHalf, kLanes, kTokens>(a, round);
     else
-        append_block<kFp16, kHalf, kLanes, kTokens>(a, blockIdx.x - q_blocks);
+        rope_block<kFp16, kHalf, kTokens>(q, static_cast<int>(blockIdx.x) - min(round, kv_blocks));
 }
 
 // ------------------------------------------------------------- cache reads
@@ -375,12 +387,13 @@ struct ReadArgs {
 };
 
 // A thread owns 8 dims of one row (a warp's stores are whole lines) and walks
-// over kTokens tokens: code x scale in FP32, rounded once to the output type.
+// over the tokens, kTokens at a time, the next ones' slots already on their
+// way: code x scale in FP32, rounded once to the output type.
 template <bool kFp16, int kTokens>
 __global__ void __launch_bounds__(256)
 kv_read_kernel(const ReadArgs a) {
-    const int64_t token_block = blockIdx.x / a.item_blocks;
-    const int item_block = static_cast<int>(blockIdx.x - token_block * a.item_blocks);
+    const int lane_block = static_cast<int>(blockIdx.x) / a.item_blocks, steps = gridDim.x / a.item_blocks;
+    const int item_block = static_cast<int>(blockIdx.x) - lane_block * a.item_blocks;
     const int local = a.tokens_at_once > 1 ? threadIdx.x / a.items : 0;
     const int item = item_block * 256 + static_cast<int>(threadIdx.x) - local * a.items;
     if (item >= a.items || local >= a.tokens_at_once) return;
@@ -393,45 +406,55 @@ kv_read_kernel(const ReadArgs a) {
     uint16_t* dst = (is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs) + 8 * chunk;
     const int64_t ts = is_v ? a.v_ts : a.k_ts;
     const int64_t nslots = a.cache.pages << a.page_shift;
-    const int64_t t0 = token_block * (a.tokens_at_once * kTokens) + local;
+    const int in_page = (1 << a.page_shift) - 1;
+    const int64_t step = static_cast<int64_t>(steps) * (a.tokens_at_once * kTokens);
+    int64_t t = static_cast<int64_t>(lane_block) * (a.tokens_at_once * kTokens) + local;
     pdl_wait();
     int slot[kTokens];
-    uint2 code[kTokens];
-    float scale[kTokens];
+    auto fetch = [&](int64_t from) {
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-        const int64_t t = t0 + j * a.tokens_at_once;
-        slot[j] = t < a.tokens ? a.slots[t] : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-        code[j] = make_uint2(0, 0);
-        scale[j] = 0.0f;
-        if (slot[j] >= 0 && slot[j] < nslots) {
-            const int64_t page = slot[j] >> a.page_shift;
-            const int64_t r = ((page * kv_heads + h) << a.page_shift) + (slot[j] & ((1 << a.page_shift) - 1));
-            code[j] = ld_once8(codes + r * (8 * a.chunks));
-            scale[j] = __ldg(scales + r);
+        for (int j = 0; j < kTokens; ++j) {
+            const int64_t u = from + j * a.tokens_at_once;
+            slot[j] = u < a.tokens ? a.slots[u] : -1;
         }
-    }
+    };
+    fetch(t);
+    for (; t < a.tokens; t += step) {
+        uint2 code[kTokens];
+        float scale[kTokens];
+        bool past[kTokens];
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-        const int64_t t = t0 + j * a.tokens_at_once;
-        if (t >= a.tokens) continue;
-        if (slot[j] >= nslots) {
-            if (chunk == 0) atomicOr(a.status, kStatusBadArgument);
-            continue;
+        for (int j = 0; j < kTokens; ++j) {
+            code[j] = make_uint2(0, 0);
+            scale[j] = 0.0f;
+            past[j] = slot[j] >= nslots;
+            if (slot[j] >= 0 && !past[j]) {
+                const int64_t r = ((static_cast<int64_t>(slot[j] >> a.page_shift) * kv_heads + h) << a.page_shift) +
+                                  (slot[j] & in_page);
+                code[j] = ld_once8(codes + r * (8 * a.chunks));
+                scale[j] = __ldg(scales + r);
+            }
         }
-        const uint32_t w[2] = {code[j].x, code[j].y};
-        uint32_t o[4];
+        fetch(t + step);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 lo = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i])));
-            const float2 hi = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
-            o[2 * i] = pack2<kFp16>(lo.x * scale[j], lo.y * scale[j]);
-            o[2 * i + 1] = pack2<kFp16>(hi.x * scale[j], hi.y * scale[j]);
+        for (int j = 0; j < kTokens; ++j) {
+            const int64_t u = t + j * a.tokens_at_once;
+            if (u >= a.tokens) continue;
+            if (past[j]) {
+                if (chunk == 0) atomicOr(a.status, kStatusBadArgument);
+                continue;
+            }
+            const uint32_t w[2] = {code[j].x, code[j].y};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 lo = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i])));
+                const float2 hi = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
+                o[2 * i] = pack2<kFp16>(lo.x * scale[j], lo.y * scale[j]);
+                o[2 * i + 1] = pack2<kFp16>(hi.x * scale[j], hi.y * scale[j]);
+            }
+            *reinterpret_cast<uint4*>(dst + u * ts) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4*>(dst + t * ts) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -443,11 +466,13 @@ cudaError_t rope_dispatch(const RopeArgs& a, int heads_per_thread, dim3 grid, cu
 }
 
 template <bool kFp16, bool kHalf, int kTokens>
-cudaError_t append_dispatch(const AppendArgs& a, const RopeArgs& q, int64_t q_blocks, dim3 grid,
+cudaError_t append_dispatch(const AppendArgs& a, const RopeArgs& q, int64_t q_blocks, int64_t kv_blocks,
                             cudaStream_t s) {
-    if (a.dim <= 64) return launch_kernel(kv_append_kernel<kFp16, kHalf, 8, kTokens>, grid, dim3(256), 0, s, a, q, q_blocks);
-    if (a.dim <= 128) return launch_kernel(kv_append_kernel<kFp16, kHalf, 16, kTokens>, grid, dim3(256), 0, s, a, q, q_blocks);
-    return launch_kernel(kv_append_kernel<kFp16, kHalf, 32, kTokens>, grid, dim3(256), 0, s, a, q, q_blocks);
+    const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks)), block(256);
+    const int kv = static_cast<int>(kv_blocks), every = static_cast<int>((q_blocks + kv_blocks) / kv_blocks);
+    if (a.dim <= 64) return launch_kernel(kv_append_kernel<kFp16, kHalf, 8, kTokens>, grid, block, 0, s, a, q, kv, every);
+    if (a.dim <= 128) return launch_kernel(kv_append_kernel<kFp16, kHalf, 16, kTokens>, grid, block, 0, s, a, q, kv, every);
+    return launch_kernel(kv_append_kernel<kFp16, kHalf, 32, kTokens>, grid, block, 0, s, a, q, kv, every);
 }
 
 int shift_of(int page_size) {
@@ -598,19 +623,18 @@ cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_hea
         }
     }
     if (q_blocks + kv_blocks > INT_MAX) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks));
     if (fp16) {
         if (half)
-            return few ? append_dispatch<true, true, 1>(a, qa, q_blocks, grid, s)
-                       : append_dispatch<true, true, 4>(a, qa, q_blocks, grid, s);
-        return few ? append_dispatch<true, false, 1>(a, qa, q_blocks, grid, s)
-                   : append_dispatch<true, false, 4>(a, qa, q_blocks, grid, s);
+            return few ? append_dispatch<true, true, 1>(a, qa, q_blocks, kv_blocks, s)
+                       : append_dispatch<true, true, 4>(a, qa, q_blocks, kv_blocks, s);
+        return few ? append_dispatch<true, false, 1>(a, qa, q_blocks, kv_blocks, s)
+                   : append_dispatch<true, false, 4>(a, qa, q_blocks, kv_blocks, s);
     }
     if (half)
-        return few ? append_dispatch<false, true, 1>(a, qa, q_blocks, grid, s)
-                   : append_dispatch<false, true, 4>(a, qa, q_blocks, grid, s);
-    return few ? append_dispatch<false, false, 1>(a, qa, q_blocks, grid, s)
-               : append_dispatch<false, false, 4>(a, qa, q_blocks, grid, s);
+        return few ? append_dispatch<false, true, 1>(a, qa, q_blocks, kv_blocks, s)
+                   : append_dispatch<false, true, 4>(a, qa, q_blocks, kv_blocks, s);
+    return few ? append_dispatch<false, false, 1>(a, qa, q_blocks, kv_blocks, s)
+               : append_dispatch<false, false, 4>(a, qa, q_blocks, kv_blocks, s);
 }
 
 cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64_t tokens,
@@ -636,18 +660,20 @@ cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64
     a.item_blocks = (a.items + 255) / 256;
     a.tokens_at_once = a.item_blocks == 1 ? 256 / a.items : 1;
     a.status = status;
-    // Eight tokens a thread once that still leaves every SM four blocks.
+    // Four tokens a thread and step once that still leaves every SM its
+    // resident blocks (4), which then stay and walk over the tokens.
     const int64_t passes = (tokens + a.tokens_at_once - 1) / a.tokens_at_once;
-    const bool few = passes * a.item_blocks < static_cast<int64_t>(8) * 4 * sm_count;
-    const int per_block = a.tokens_at_once * (few ? 1 : 8);
-    const int64_t blocks = (tokens + per_block - 1) / per_block * a.item_blocks;
-    if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const int64_t resident = static_cast<int64_t>(4) * sm_count;
+    const bool few = passes * a.item_blocks < 4 * resident;
+    const int64_t want = (passes + (few ? 1 : 4) - 1) / (few ? 1 : 4);
+    const int64_t walk = few ? want : std::max<int64_t>(1, std::min(want, resident / a.item_blocks));
+    if (walk * a.item_blocks > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(walk * a.item_blocks));
     if (fp16)
         return few ? launch_kernel(kv_read_kernel<true, 1>, grid, dim3(256), 0, s, a)
-                   : launch_kernel(kv_read_kernel<true, 8>, grid, dim3(256), 0, s, a);
+                   : launch_kernel(kv_read_kernel<true, 4>, grid, dim3(256), 0, s, a);
     return few ? launch_kernel(kv_read_kernel<false, 1>, grid, dim3(256), 0, s, a)
-               : launch_kernel(kv_read_kernel<false, 8>, grid, dim3(256), 0, s, a);
+               : launch_kernel(kv_read_kernel<false, 4>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace dg
