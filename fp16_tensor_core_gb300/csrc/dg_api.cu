@@ -930,7 +930,7 @@ namespace {
 
 dg_status check_attn_sizes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len) {
     if (batch < 0 || batch > kAttnMaxBatch || q_len < 1 || q_heads < 1 || q_heads > kMaxHeads ||
-        prefix_len < 0 || prefix_len > INT_MAX - 64)
+        prefix_len < 0 || prefix_len > INT_MAX - 256)
         return DG_ERR_INVALID_VALUE;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return DG_ERR_INVALID_VALUE;
     // rows of the prefix are counted in 32 bits

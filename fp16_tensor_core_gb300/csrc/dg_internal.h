@@ -216,6 +216,11 @@ struct AttnLaunch {
     uint32_t* status;
 };
 cudaError_t launch_attn_decode(const AttnLaunch& L, cudaStream_t s);
+// The prefix's states on tcgen05, into `states`; `slots` holds the shares'.
+cudaError_t launch_attn_prefix(const AttnLaunch& L, float* slots, float* states, cudaStream_t s);
+bool attn_prefix_on_tensor_cores(int64_t rows, int head_dim);
+int64_t attn_prefix_slot_floats(int sm_count, int head_dim);
+int64_t attn_state_floats(int batch, int q_len, int q_heads, int head_dim);
 int64_t attn_slot_floats(int sm_count, int head_dim);
 int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
                            int sm_count);

@@ -31,6 +31,7 @@
 
 #include <algorithm>
 
+#include "attn_common.cuh"
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
 
@@ -96,11 +97,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // The transpose of an 8 x 8 matrix of 16-bit values held two to a lane (row
 // lane / 4, columns 2 (lane % 4), + 1).
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -108,12 +104,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -121,15 +111,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four E4M3 codes (low byte first) -> two FP16 pairs, exactly.
-__device__ __forceinline__ void codes_to_halves(uint32_t codes, uint32_t* lo, uint32_t* hi) {
-    asm("{\n\t.reg .b16 l, h;\n\t"
-        "mov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(*lo), "=r"(*hi) : "r"(codes));
 }
 
 // Shapes per head width D and number of 8-row tiles NT.  A lane with
@@ -185,13 +166,6 @@ struct Cursor {
     int len;     // its tokens
     int stop;    // the run's end in this unit: its last tile + 1
 };
-
-__device__ __forceinline__ float4 scaled(float4 x, float w) {
-    return make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
-}
-__device__ __forceinline__ float4 plus_scaled(float4 x, float w, float4 y) {
-    return make_float4(fmaf(w, y.x, x.x), fmaf(w, y.y, x.y), fmaf(w, y.z, x.z), fmaf(w, y.w, x.w));
-}
 
 // Where a row's result goes and what it is joined with: factors for its
 // partial sums, so that out = x * wx (+ prefix state * wp).
@@ -476,7 +450,7 @@ attn_split_kernel(const AttnArgs a) {
 
         while (running) {
             if (fresh) {
-                // ---- a new unit: its queries, normalised by a power of two
+                // ---- a new unit: its queries
                 fresh = false;
                 h = at.unit / a.row_tiles;
                 r0 = (at.unit - h * a.row_tiles) * kRows;
@@ -500,35 +474,23 @@ attn_split_kernel(const AttnArgs a) {
                                       : make_uint4(0, 0, 0, 0);
                     float mul = 1.0f, factor = a.scale_log2;
                     if constexpr (!kFp16) {
-                        // BF16 queries: FP16 has more mantissa but less
-                        // range, so a row is scaled by a power of two that
-                        // brings its largest value to [1, 2).
                         uint32_t top = 0;
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
-                        }
+                        for (int k = 0; k < D / 32; ++k) top = max(top, top_abs_bf16(w[k]));
                         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                        const int e = min(max(static_cast<int>(top >> 7), 1), 253);   // biased exponent
-                        mul = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                        factor *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+                        const PowerOfTwo p = power_below(top);
+                        mul = p.inverse;
+                        factor *= p.value;
                     }
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
-                        const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t v = x[i];
-                            if constexpr (!kFp16)
-                                v = f32x2_to_f16x2(__uint_as_float(v << 16) * mul,
-                                                   __uint_as_float(v & 0xFFFF0000u) * mul);
-                            // dims 8k + 2i, +1 of the lane's run: MMA step 2k + i/2
-                            qb[n][2 * k + (i >> 1)][i & 1] = v;
-                        }
+                        if constexpr (!kFp16) w[k] = bf16_to_half8(w[k], mul);
+                        // dims 8k + 2i, +1 of the lane's run: MMA step 2k + i/2
+                        qb[n][2 * k][0] = w[k].x;
+                        qb[n][2 * k][1] = w[k].y;
+                        qb[n][2 * k + 1][0] = w[k].z;
+                        qb[n][2 * k + 1][1] = w[k].w;
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -866,53 +828,25 @@ attn_join_kernel(const AttnArgs a) {
     int64_t token;
     int head;
     row_place(a, b, h, r0 + r, &token, &head);
-    // slot 2x + 1 of the first block, then slot 2y of each later one
-    auto state = [&](int blk) {
-        return a.slots + ((2 * static_cast<int64_t>(blk) + (blk == first ? 1 : 0)) * kRows + r) * kState;
-    };
-    // Eight states at a time, their loads in flight together.
-    float4 x[D > 128 ? 2 : 1];
-    float m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < (D > 128 ? 2 : 1); ++k) x[k] = make_float4(0, 0, 0, 0);
+    // slot 1 of the first block, then slot 0 of each later one
+    constexpr int64_t kBlock = 2 * kRows * kState;
+    const float* tail = a.slots + first * kBlock + (kRows + r) * kState;
+    constexpr int kParts = D > 128 ? 2 : 1;
+    float4 x[kParts], y[kParts];
+    float m, l;
+    join_states<D>(tail + (kBlock - kRows * kState), kBlock, last - first, lane, &m, &l, y);
+    // the first piece, joined last: a sum of two
+    const float2 ml = *reinterpret_cast<const float2*>(tail);
+    const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
+    const float w0 = ex2(ml.x - base), w1 = ex2(m - base);
     const bool live = 4 * lane < D;
-    for (int i0 = first; i0 <= last; i0 += 8) {
-        float2 ml[8];
-        float4 y[8][D > 128 ? 2 : 1];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.0f);
-            if (i0 + i > last) continue;
-            const float* row = state(i0 + i);
-            ml[i] = *reinterpret_cast<const float2*>(row);
-            if (live) {
-#pragma unroll
-                for (int k = 0; k < (D > 128 ? 2 : 1); ++k)
-                    y[i][k] = *reinterpret_cast<const float4*>(row + 4 + 4 * lane + 128 * k);
-            }
-        }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float w0 = ex2(m - base);
-        m = top;
-        l *= w0;
-#pragma unroll
-        for (int k = 0; k < (D > 128 ? 2 : 1); ++k) x[k] = scaled(x[k], w0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i0 + i > last) continue;
-            const float w = ex2(ml[i].x - base);
-            l = fmaf(w, ml[i].y, l);
-#pragma unroll
-            for (int k = 0; k < (D > 128 ? 2 : 1); ++k) x[k] = plus_scaled(x[k], w, y[i][k]);
-        }
-    }
-    const RowEnd e = row_end<D>(a, token, head, m, l, lane == 0);
+    const RowEnd e = row_end<D>(a, token, head, top, w0 * ml.y + w1 * l, lane == 0);
     if (live) {
 #pragma unroll
-        for (int k = 0; k < (D > 128 ? 2 : 1); ++k) emit4<D, kFp16>(e, 4 * lane + 128 * k, x[k]);
+        for (int k = 0; k < kParts; ++k) {
+            x[k] = *reinterpret_cast<const float4*>(tail + 4 + 4 * lane + 128 * k);
+            emit4<D, kFp16>(e, 4 * lane + 128 * k, plus_scaled(scaled(x[k], w0), w1, y[k]));
+        }
     }
 }
 
@@ -967,7 +901,13 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.slots = reinterpret_cast<float*>(a.crossings + L.sm_count);
     a.status = L.status;
     float* states = a.slots + attn_slot_floats(L.sm_count, D);
-    if (L.prefix_len > 0) {
+    const int64_t prefix_rows = static_cast<int64_t>(L.batch) * L.q_len * a.group;
+    if (L.prefix_len > 0 && attn_prefix_on_tensor_cores(prefix_rows, D)) {
+        float* prefix_slots = states + attn_state_floats(L.batch, L.q_len, L.q_heads, D);
+        const cudaError_t e = launch_attn_prefix(L, prefix_slots, states, s);
+        if (e != cudaSuccess) return e;
+        a.prefix = states;
+    } else if (L.prefix_len > 0) {
         // The prefix as one request that every query row of the batch asks.
         AttnArgs p = a;
         p.page_table = L.prefix_pages;
@@ -997,10 +937,19 @@ int64_t attn_slot_floats(int sm_count, int head_dim) {
     return static_cast<int64_t>(2) * sm_count * kMaxUnitRows * (head_dim + 4);
 }
 
+int64_t attn_state_floats(int batch, int q_len, int q_heads, int head_dim) {
+    return static_cast<int64_t>(batch) * q_len * q_heads * (head_dim + 4);
+}
+
+// Rows of a key head from which the prefix goes to the tcgen05 kernel (which
+// holds heads of 64 and 128).
+bool attn_prefix_on_tensor_cores(int64_t rows, int head_dim) { return head_dim < 256 && rows > 32; }
+
 int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
                            int sm_count) {
     int64_t n = attn_slot_floats(sm_count, head_dim) + static_cast<int64_t>(sm_count) * 4;
-    if (prefix_len > 0) n += static_cast<int64_t>(batch) * q_len * q_heads * (head_dim + 4);
+    if (prefix_len > 0)
+        n += attn_state_floats(batch, q_len, q_heads, head_dim) + attn_prefix_slot_floats(sm_count, head_dim);
     return n * static_cast<int64_t>(sizeof(float));
 }
 
