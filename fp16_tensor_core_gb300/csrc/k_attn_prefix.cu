@@ -8,13 +8,16 @@
 //   W = exp(scale sk S + ln sv - m), to FP16, back into tensor memory
 //   O += W Vc    (W from tensor memory, Vc from shared memory)
 // A CTA holds one 128-row tile of one key head and walks over its share of
-// the prefix.  Roles: four warps take the codes from the cache and write them
-// as FP16 (exact) into swizzled shared memory, keys and values in two stages
-// each; one thread issues the MMAs; four warps turn scores into weights.  S
-// has two buffers (a tile's weights take the place of its scores), so the
-// next tile's scores are formed while this one's weights are.
+// the prefix.  Roles: four warps each take the codes of the keys and of the
+// values from the cache and write them as FP16 (exact) into swizzled shared
+// memory, in two stages; one thread issues the MMAs; two groups of four warps turn scores into
+// weights.  Tiles of even and odd number are two streams with a group, a
+// stage, S and O of their own (a tile's weights take the place of its
+// scores), joined at the end: while one stream's weights are formed the
+// tensor cores work for the other.  One stream alone left them idle: its
+// softmax is a chain of latencies (4300 cycles a tile against 1024 of MMA).
 //
-// A warp of the softmax reads its 32 rows in the MMA fragment shape (a thread
+// A warp of the softmax reads its rows in the MMA fragment shape (a thread
 // holds 2 of 8 columns of 4 rows) instead of a row per thread: the per-token
 // factors it needs are then a quarter, and packed pairs of columns feed the
 // two-wide FP32 instructions.  The reference m of a row follows its maximum
@@ -36,56 +39,26 @@ namespace {
 
 constexpr int kTileTokens = 128;
 constexpr int kTileRows = 128;
-constexpr int kThreads = 384;   // warpgroups: softmax, converters, MMA (one thread of it)
+constexpr int kThreads = 640;   // warpgroups: softmax of even and of odd tiles, keys, values, MMA
 constexpr float kGrowth = 8.0f; // log2 of how far weights may pass 1
 
-__device__ __forceinline__ void tmem_load_frag16(uint32_t taddr, uint32_t (&r)[64]) {
+__device__ __forceinline__ void tmem_load_frag4(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, "
-        "%33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, "
-        "%49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, "
-        "[%64];"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
-          "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
-          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
-          "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
-          "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_load_frag8(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_store_frag4(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-        "[%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_store_frag8(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
-        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
         :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
           "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-          "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-          "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-          "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+          "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -123,6 +96,14 @@ __device__ __forceinline__ uint64_t sdesc_mn_major_sw128(uint32_t smem_byte_addr
     uint64_t d = sdesc_k_major_sw128(smem_byte_addr);
     d &= ~(static_cast<uint64_t>(0x3FFF) << 16);
     return d | static_cast<uint64_t>(column_bytes >> 4) << 16;
+}
+
+// wait_bounded for waits that are on the critical path and often short: the
+// clock (a read of about a microsecond) is first looked at after 64 tries.
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_bounded(bar, parity, ctl);
 }
 
 // Two FP32 lanes at once.
@@ -180,36 +161,123 @@ struct PrefixShape {
     static constexpr int kColumnBytes = kTileTokens * 128;       // 16 KB
     static constexpr int kOperandBytes = kHalves * kColumnBytes; // Q, or one stage of K or V
     static constexpr int kState = D + 4;
-    static constexpr int kOCol = 256;                            // tensor memory: S0, S1, O
+    static constexpr int kOCol = 256;                            // tensor memory: S0, S1, O0, O1
+    static_assert(kOCol + 2 * D <= 512, "tensor memory");
     static constexpr int kKAt = kOperandBytes;
     static constexpr int kVAt = kKAt + 2 * kOperandBytes;
     static constexpr int kFactorsAt = kVAt + 2 * kOperandBytes;  // [2][3][128] per-token factors
-    static constexpr int kRowsAt = kFactorsAt + 2 * 3 * 128 * 4; // [2][128] cache rows
-    static constexpr int kQScaleAt = kRowsAt + 2 * 128 * 8;
+    static constexpr int kRowsAt = kFactorsAt + 2 * 3 * 128 * 4; // [2][2][128] cache rows
+    static constexpr int kQScaleAt = kRowsAt + 2 * 2 * 128 * 8;
     static constexpr int kBarsAt = kQScaleAt + 128 * 4;
     static constexpr int kSmem = kBarsAt + 256 + 1024;           // and alignment
 };
 
-// 16 codes of a token's row as two 16-byte chunks of FP16 in the swizzled
-// operand; lanes of the upper half store their second chunk first, which
-// keeps a quarter warp's stores in different banks.
-template <int D>
-__device__ __forceinline__ void store_chunk16(uint8_t* operand, int token, int chunk, uint4 codes) {
-    uint32_t h[8];
-    codes_to_halves(codes.x, &h[0], &h[1]);
-    codes_to_halves(codes.y, &h[2], &h[3]);
-    codes_to_halves(codes.z, &h[4], &h[5]);
-    codes_to_halves(codes.w, &h[6], &h[7]);
-    const int c0 = 2 * chunk;
-    uint8_t* row = operand + (c0 >> 3) * PrefixShape<D>::kColumnBytes + token * 128;
-    const uint32_t a0 = smem_addr(row + (((c0 & 7) ^ (token & 7)) * 16));
-    const uint32_t a1 = smem_addr(row + ((((c0 & 7) + 1) ^ (token & 7)) * 16));
-    if (D == 128 && chunk >= 4) {
-        st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-        st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-    } else {
-        st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-        st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+// The keys' (or values') four warps: codes from the cache to swizzled FP16.
+template <int D, bool kValues>
+__device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem, uint64_t* bars,
+                                             const WaitCtl& ctl, int tile0, int tiles, int head) {
+    using S = PrefixShape<D>;
+    constexpr uint32_t kBarrier = kValues ? 4 : 2;
+    uint64_t* full = kValues ? bars + 3 : bars + 1;
+    uint64_t* free = kValues ? bars + 9 : bars + 7;   // values: O done; keys: scores and factors read
+    float* factors = reinterpret_cast<float*>(smem + S::kFactorsAt);
+    int64_t* cache_rows = reinterpret_cast<int64_t*>(smem + S::kRowsAt) + (kValues ? 2 * 128 : 0);
+    uint8_t* operand = smem + (kValues ? S::kVAt : S::kKAt);
+    const int i = static_cast<int>(threadIdx.x) & 127;
+    // 16 bytes a thread and pass: 32 tokens x 64 dims.  Four chunks of two
+    // tokens a quarter warp keep its stores (chunks 2c, then 2c + 1, of FP16)
+    // in different banks.
+    constexpr int kHalves = S::kHalves, kPasses = 4 * kHalves;   // pass s: tokens 32 (s / kHalves) ..
+    const int token0 = i >> 2, swz = token0 & 7;
+    const uint32_t dst0 = smem_addr(operand) + token0 * 128 + ((2 * (i & 3)) ^ swz) * 16;
+    const uint32_t dst1 = smem_addr(operand) + token0 * 128 + ((2 * (i & 3) + 1) ^ swz) * 16;
+    const int in_page = (1 << a.page_shift) - 1;
+    const uint8_t* codes = (kValues ? a.v : a.k) + (i & 3) * 16;
+    // Page of token i of tile j (kNoToken past the end); its cache row is
+    // formed later, so that nothing waits for the load.
+    constexpr int kNoToken = -0x7FFFFFFF;
+    auto find_page = [&](int j) {
+        const int t = (tile0 + j) * kTileTokens + i;
+        return j < tiles && t < a.len ? a.page_list[t >> a.page_shift] : kNoToken;
+    };
+    auto row_of = [&](int p, int j) -> int64_t {   // -1: none
+        if (p < 0 || p >= a.pages) {
+            if (p != kNoToken) atomicOr(a.status, kStatusBadArgument);
+            return -1;
+        }
+        const int t = (tile0 + j) * kTileTokens + i;
+        return ((static_cast<int64_t>(p) * a.kv_heads + head) << a.page_shift) + (t & in_page);
+    };
+    // The next tile's codes wait in registers: through shared memory they
+    // would take its bandwidth, which is what the CTA runs short of.
+    uint4 x[kPasses];
+    auto fetch = [&](int j) {
+        const int64_t* rows = cache_rows + (j & 1) * 128;
+#pragma unroll
+        for (int s = 0; s < kPasses; ++s) {
+            const int64_t r = rows[token0 + 32 * (s / kHalves)];
+            x[s] = make_uint4(0, 0, 0, 0);
+            if (r >= 0) x[s] = __ldg(reinterpret_cast<const uint4*>(codes + r * D + 64 * (s % kHalves)));
+        }
+    };
+    auto load_scales = [&](int64_t r, float* sk, float* sv) {
+        *sk = 0.0f;
+        *sv = -1.0f;   // no token
+        if (!kValues && r >= 0) {
+            *sk = __ldg(a.k_scale + r);
+            *sv = __ldg(a.v_scale + r);
+        }
+    };
+    float sk, sv;
+    int64_t row1;   // this thread's token of the next tile
+    {
+        const int p0 = find_page(0), p1 = find_page(1);
+        const int64_t row0 = row_of(p0, 0);
+        row1 = row_of(p1, 1);
+        cache_rows[i] = row0;
+        cache_rows[128 + i] = row1;
+        load_scales(row0, &sk, &sv);
+    }
+    named_bar_sync(kBarrier, 128);
+    fetch(0);
+    named_bar_sync(kBarrier, 128);   // before rows are replaced
+    bool ok = true;
+    for (int j = 0; j < tiles && ok; ++j) {
+        const int b = j & 1;
+        const int page2 = find_page(j + 2);   // on its way meanwhile
+        if (j >= 2) ok = __all_sync(0xFFFFFFFFu, wait_soon(&free[b], ((j - 2) >> 1) & 1, ctl));
+        if (ok) {
+#pragma unroll
+            for (int s = 0; s < kPasses; ++s) {
+                const uint32_t at = b * S::kOperandBytes + (s % kHalves) * S::kColumnBytes + (s / kHalves) * (32 * 128);
+                uint32_t h[8];
+                codes_to_halves(x[s].x, &h[0], &h[1]);
+                codes_to_halves(x[s].y, &h[2], &h[3]);
+                codes_to_halves(x[s].z, &h[4], &h[5]);
+                codes_to_halves(x[s].w, &h[6], &h[7]);
+                st_shared_v4(dst0 + at, h[0], h[1], h[2], h[3]);
+                st_shared_v4(dst1 + at, h[4], h[5], h[6], h[7]);
+            }
+            if constexpr (!kValues) {
+                float* f = factors + b * 3 * 128;
+                const float safe = sv < 0x1p-100f ? 0x1p-100f : sv;
+                f[i] = sk;
+                f[128 + i] = sv == -1.0f ? -INFINITY : __log2f(safe);
+                f[256 + i] = sv == -1.0f ? 0.0f : rcp(safe);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&full[b]);
+            if (j + 1 < tiles) {
+                fetch(j + 1);
+                load_scales(row1, &sk, &sv);
+            }
+        }
+        // rows of tile j (whose loads were issued an iteration ago) make room
+        // for those of tile j + 2; after a wait that ran out the four warps
+        // leave together
+        row1 = row_of(page2, j + 2);
+        cache_rows[b * 128 + i] = row1;
+        ok = named_bar_and(kBarrier, 128, ok);
     }
 }
 
@@ -221,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* sq = smem;
     float* factors = reinterpret_cast<float*>(smem + S::kFactorsAt);
-    int64_t* cache_rows = reinterpret_cast<int64_t*>(smem + S::kRowsAt);
     float* qscale = reinterpret_cast<float*>(smem + S::kQScaleAt);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBarsAt);
     uint64_t* q_full = bars;          // 128 arrivals
@@ -248,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc<512>(tmem_slot);
         tmem_relinquish();
     }
@@ -267,13 +334,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     const int tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / a.splits) - tile0;
     pdl_wait();
 
-    // Registers: 168 a thread at launch; the softmax warps hold 128 scores
-    // each and take 72 more of the MMA warpgroup's (240 + 168 + 96 = 3 * 168).
-    if (warp < 4) {
+    // Registers: 96 a thread at launch; the softmax warps take what the
+    // others leave (144 + 144 + 72 + 72 + 40 <= 5 * 96).
+    if (warp < 8) {
         // -------------------------------------------------- queries, softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        const int b = warp >> 2;   // stream
         const int g = lane >> 2, c = lane & 3;
-        {   // thread i takes row i of the tile, scaled by a power of two (BF16)
+        if (b == 0) {   // thread i takes row i of the tile, scaled by a power of two (BF16)
             const int i = threadIdx.x, r = rt * kTileRows + i;
             uint4 w[D / 8];
             float factor = a.scale_log2;
@@ -305,8 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             qscale[i] = factor;
             fence_proxy_async_smem();
             mbar_arrive(q_full);
-            named_bar_sync(1, 128);
         }
+        named_bar_sync(1, 256);   // before the factors are read
+        const int quarter = warp & 3;
         // row 16 h + 8 i + g of the warp's 32: index 2 h + i
         float m[4], qs[4];
         f32x2 l[4];
@@ -314,254 +383,239 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
         for (int x = 0; x < 4; ++x) {
             m[x] = -INFINITY;
             l[x] = 0ull;
-            qs[x] = qscale[32 * warp + 16 * (x >> 1) + 8 * (x & 1) + g];
+            qs[x] = qscale[32 * quarter + 16 * (x >> 1) + 8 * (x & 1) + g];
         }
-        const uint32_t quad = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const uint32_t quad = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        const uint32_t o_col = S::kOCol + D * b;
         bool ok = true;
-        for (int j = 0; j < tiles; ++j) {
-            const int b = j & 1;
+        for (int j = b; j < tiles; j += 2) {
             const uint32_t parity = (j >> 1) & 1;
             // the keys' barrier also hands over the per-token factors
-            ok = wait_bounded(&k_full[b], parity, ctl) && wait_bounded(&s_full[b], parity, ctl);
+            ok = *ctl.abort_flag == 0 && wait_soon(&k_full[b], parity, ctl) && wait_soon(&s_full[b], parity, ctl);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after_sync();
-            uint32_t s[2][64];
-            tmem_load_frag16(quad + 128 * b, s[0]);
-            tmem_load_frag16(quad + (16u << 16) + 128 * b, s[1]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 64; ++k) asm volatile("" : "+r"(s[h][k]));
             const float* f = factors + b * 3 * 128 + 2 * c;
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-                const f32x2 sk = *reinterpret_cast<const f32x2*>(f + 8 * n);
-                const f32x2 lg = *reinterpret_cast<const f32x2*>(f + 128 + 8 * n);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t* p = &s[x >> 1][4 * n + 2 * (x & 1)];
-                    const f32x2 y = fma2(mul2(pack(__uint_as_float(p[0]), __uint_as_float(p[1])), sk),
-                                         pack(qs[x], qs[x]), lg);
-                    const float2 v = unpack(y);
-                    top[x] = fmaxf(top[x], fmaxf(v.x, v.y));
-                    p[0] = __float_as_uint(v.x);
-                    p[1] = __float_as_uint(v.y);
-                }
-            }
-            bool grew = false;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
-                grew |= top[x] > m[x] + kGrowth;
-            }
-            if (__any_sync(0xFFFFFFFFu, grew)) {
-                float by[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const bool move = top[x] > m[x] + kGrowth;
-                    by[x] = move ? ex2(m[x] - top[x]) : 1.0f;
-                    if (move) m[x] = top[x];
-                    l[x] = mul2(l[x], pack(by[x], by[x]));
-                }
-                if (j > 0) {
-                    // O as the previous tile left it
-                    ok = wait_bounded(&o_done[b ^ 1], ((j - 1) >> 1) & 1, ctl);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll 1
-                        for (int part = 0; part < D / 64; ++part) {
-                            uint32_t o[32];
-                            const uint32_t at = quad + (static_cast<uint32_t>(16 * h) << 16) + S::kOCol + 64 * part;
-                            tmem_load_frag8(at, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                asm volatile("" : "+r"(o[k]));
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * by[2 * h + ((k >> 1) & 1)]);
-                            }
-                            tmem_store_frag8(at, o);
-                        }
-                    }
-                    tmem_wait_st();
-                }
-            }
+            // 16 rows at a time, in one pass against the reference as it
+            // stands; only where a row's maximum has outgrown it (the first
+            // tiles) the reference moves and the pass is made again.
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                const uint32_t half = quad + (static_cast<uint32_t>(16 * h) << 16);
+                const int x0 = 2 * h;
                 uint32_t w[32];
+                f32x2 part[2];
+                float top[2];
+#pragma unroll 1
+                for (int again = 0; again < 2; ++again) {
+                    const float base0 = m[x0] == -INFINITY ? 0.0f : -m[x0];
+                    const float base1 = m[x0 + 1] == -INFINITY ? 0.0f : -m[x0 + 1];
+                    const f32x2 base[2] = {pack(base0, base0), pack(base1, base1)};
+                    const f32x2 q2[2] = {pack(qs[x0], qs[x0]), pack(qs[x0 + 1], qs[x0 + 1])};
+                    part[0] = part[1] = 0ull;
+                    top[0] = top[1] = -INFINITY;
+                    uint32_t s[2][16];
+                    tmem_load_frag4(half + 128 * b, s[0]);
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    const f32x2 rs = *reinterpret_cast<const f32x2*>(f + 256 + 8 * n);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t(&v)[16] = s[k & 1];
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[e]));
+                        if (k < 3) tmem_load_frag4(half + 128 * b + 32 * (k + 1), s[(k + 1) & 1]);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const int col = 32 * k + 8 * n;
+                            const f32x2 sk = *reinterpret_cast<const f32x2*>(f + col);
+                            const f32x2 lg = *reinterpret_cast<const f32x2*>(f + 128 + col);
+                            const f32x2 rs = *reinterpret_cast<const f32x2*>(f + 256 + col);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const f32x2 sc = pack(__uint_as_float(v[4 * n + 2 * i]),
+                                                      __uint_as_float(v[4 * n + 2 * i + 1]));
+                                const float2 y = unpack(fma2(mul2(sc, sk), q2[i], add2(lg, base[i])));
+                                top[i] = fmaxf(top[i], fmaxf(y.x, y.y));
+                                const float e0 = ex2(y.x), e1 = ex2(y.y);
+                                part[i] = fma2(pack(e0, e1), rs, part[i]);
+                                w[8 * k + 2 * n + i] = f32x2_to_f16x2(e0, e1);
+                            }
+                        }
+                    }
+                    bool grew = false;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int x = 2 * h + i;
-                        const float base = m[x] == -INFINITY ? 0.0f : -m[x];
-                        const uint32_t* p = &s[h][4 * n + 2 * i];
-                        const float2 y = unpack(add2(pack(__uint_as_float(p[0]), __uint_as_float(p[1])),
-                                                     pack(base, base)));
-                        const float e0 = ex2(y.x), e1 = ex2(y.y);
-                        l[x] = fma2(pack(e0, e1), rs, l[x]);
-                        w[2 * n + i] = f32x2_to_f16x2(e0, e1);
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+                        // relative to the reference, or to 0 while there is none
+                        grew |= m[x0 + i] == -INFINITY ? top[i] > -INFINITY : top[i] > kGrowth;
+                    }
+                    if (!__any_sync(0xFFFFFFFFu, grew) || again == 1) break;
+                    float by[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float& ref = m[x0 + i];
+                        const bool none = ref == -INFINITY;
+                        const bool move = none ? top[i] > -INFINITY : top[i] > kGrowth;
+                        by[i] = !move ? 1.0f : none ? 0.0f : ex2(-top[i]);
+                        if (move) ref = none ? top[i] : ref + top[i];
+                        l[x0 + i] = mul2(l[x0 + i], pack(by[i], by[i]));
+                    }
+                    // O as the stream's previous tile left it; a wait that
+                    // runs out ends the loop below
+                    if (j >= 2 && __all_sync(0xFFFFFFFFu, wait_soon(&o_done[b], ((j - 2) >> 1) & 1, ctl))) {
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int p = 0; p < D / 32; ++p) {
+                            uint32_t o[16];
+                            tmem_load_frag4(half + o_col + 32 * p, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                asm volatile("" : "+r"(o[k]));
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * by[(k >> 1) & 1]);
+                            }
+                            tmem_store_frag4(half + o_col + 32 * p, o);
+                        }
                     }
                 }
-                tmem_store_pairs16(quad + (static_cast<uint32_t>(16 * h) << 16) + 128 * b, w);
+                l[x0] = add2(l[x0], part[0]);
+                l[x0 + 1] = add2(l[x0 + 1], part[1]);
+                tmem_store_pairs16(half + 128 * b, w);
             }
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive(&w_full[b]);
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(&o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, ctl));
-        if (ok) {
-            tc_fence_after_sync();
+        // ---- both streams' results, joined by the first group
+        if (ok && tiles > b) {
+            const int last = tiles - 1 - ((tiles - 1 - b) & 1);
+            ok = wait_soon(&o_done[b], (last >> 1) & 1, ctl);
+        }
+        // Every MMA is done: the operands' memory is free.
+        ok = named_bar_and(3, 256, ok);
+        tc_fence_after_sync();
+        float* other = reinterpret_cast<float*>(smem + S::kKAt);   // the second stream's states
+        float sums[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float2 part = unpack(l[x]);
+            sums[x] = part.x + part.y;
+            sums[x] += __shfl_xor_sync(0xFFFFFFFFu, sums[x], 1);
+            sums[x] += __shfl_xor_sync(0xFFFFFFFFu, sums[x], 2);
+        }
+        const bool second = tiles > 1;   // the second stream has a tile
+        if (ok && b == 1 && second) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float* row[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    row[i] = other + (32 * quarter + 16 * h + 8 * i + g) * S::kState;
+                    if (c == 0) *reinterpret_cast<float2*>(row[i]) = make_float2(m[2 * h + i], sums[2 * h + i]);
+                }
 #pragma unroll 1
+                for (int part = 0; part < D / 32; ++part) {
+                    uint32_t o[16];
+                    tmem_load_frag4(quad + (static_cast<uint32_t>(16 * h) << 16) + o_col + 32 * part, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(o[k]));
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint2*>(row[i] + 4 + 32 * part + 8 * n + 2 * c) =
+                                make_uint2(o[4 * n + 2 * i], o[4 * n + 2 * i + 1]);
+                }
+            }
+        }
+        ok = named_bar_and(3, 256, ok);
+        if (ok && b == 0) {
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float* dst[2];
+                const float* row[2];
+                float w0[2], w1[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int x = 2 * h + i;
-                    const float2 part = unpack(l[x]);
-                    float sum = part.x + part.y;
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                    const int in_tile = 32 * warp + 16 * h + 8 * i + g, r = rt * kTileRows + in_tile;
+                    const int in_tile = 32 * quarter + 16 * h + 8 * i + g, r = rt * kTileRows + in_tile;
+                    row[i] = other + in_tile * S::kState;
+                    const float2 ml = second ? *reinterpret_cast<const float2*>(row[i]) : make_float2(-INFINITY, 0.0f);
+                    const float top = fmaxf(m[x], ml.x), base = top == -INFINITY ? 0.0f : top;
+                    w0[i] = ex2(m[x] - base);
+                    w1[i] = ex2(ml.x - base);
                     dst[i] = nullptr;
                     if (r >= a.rows) continue;
                     if (a.splits > 1) {
                         dst[i] = a.slots + (static_cast<int64_t>(blockIdx.x) * kTileRows + in_tile) * S::kState;
                     } else {
                         const int token = r / a.group;
-                        const int64_t row = static_cast<int64_t>(token) * a.q_heads + head * a.group + r - token * a.group;
-                        dst[i] = a.states + row * S::kState;
+                        const int64_t at = static_cast<int64_t>(token) * a.q_heads + head * a.group + r - token * a.group;
+                        dst[i] = a.states + at * S::kState;
                     }
-                    if (c == 0) *reinterpret_cast<float2*>(dst[i]) = make_float2(m[x], sum);
+                    if (c == 0)
+                        *reinterpret_cast<float2*>(dst[i]) =
+                            make_float2(top, w0[i] * sums[x] + (second ? w1[i] * ml.y : 0.0f));
                 }
+                __syncwarp();   // the rows past the end skipped ahead
 #pragma unroll 1
-                for (int part = 0; part < D / 64; ++part) {
-                    uint32_t o[32];
-                    tmem_load_frag8(quad + (static_cast<uint32_t>(16 * h) << 16) + S::kOCol + 64 * part, o);
+                for (int part = 0; part < D / 32; ++part) {
+                    uint32_t o[16];
+                    tmem_load_frag4(quad + (static_cast<uint32_t>(16 * h) << 16) + o_col + 32 * part, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(o[k]));
+                    for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(o[k]));
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
+                    for (int n = 0; n < 4; ++n)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (dst[i] != nullptr)
-                                *reinterpret_cast<float2*>(dst[i] + 4 + 64 * part + 8 * n + 2 * c) =
-                                    make_float2(__uint_as_float(o[4 * n + 2 * i]),
-                                                __uint_as_float(o[4 * n + 2 * i + 1]));
+                        for (int i = 0; i < 2; ++i) {
+                            if (dst[i] == nullptr) continue;
+                            const int d = 4 + 32 * part + 8 * n + 2 * c;
+                            float2 y = make_float2(__uint_as_float(o[4 * n + 2 * i]) * w0[i],
+                                                   __uint_as_float(o[4 * n + 2 * i + 1]) * w0[i]);
+                            if (second) {
+                                const float2 z = *reinterpret_cast<const float2*>(row[i] + d);
+                                y.x = fmaf(w1[i], z.x, y.x);
+                                y.y = fmaf(w1[i], z.y, y.y);
+                            }
+                            *reinterpret_cast<float2*>(dst[i] + d) = y;
+                        }
+                    __syncwarp();
                 }
             }
         }
-    } else if (warp < 8) {
-        // -------------------------------------------------- codes to operands
-        const int i = static_cast<int>(threadIdx.x) - 128;
-        constexpr int kPerRow = D / 16, kPasses = kPerRow;   // 128 / kPerRow tokens a pass
-        const int chunk = i % kPerRow, token_in = i / kPerRow;
-        constexpr int kStep = 128 / kPerRow;
-        const int in_page = (1 << a.page_shift) - 1;
-        // cache row of token i of tile j (-1: none), from its page
-        auto find_row = [&](int j) -> int64_t {
-            const int t = (tile0 + j) * kTileTokens + i;
-            if (j >= tiles || t >= a.len) return -1;
-            const int p = a.page_list[t >> a.page_shift];
-            if (p < 0 || p >= a.pages) {
-                atomicOr(a.status, kStatusBadArgument);
-                return -1;
-            }
-            return ((static_cast<int64_t>(p) * a.kv_heads + head) << a.page_shift) + (t & in_page);
-        };
-        auto load = [&](const uint8_t* codes, const int64_t* rows, uint4 (&x)[kPasses]) {
-#pragma unroll
-            for (int s = 0; s < kPasses; ++s) {
-                const int64_t r = rows[token_in + s * kStep];
-                x[s] = make_uint4(0, 0, 0, 0);
-                if (r >= 0) x[s] = __ldg(reinterpret_cast<const uint4*>(codes + r * D + chunk * 16));
-            }
-        };
-        auto load_scales = [&](int64_t r, float* sk, float* sv) {
-            *sk = 0.0f;
-            *sv = -1.0f;   // no token
-            if (r >= 0) {
-                *sk = __ldg(a.k_scale + r);
-                *sv = __ldg(a.v_scale + r);
-            }
-        };
-        uint4 kc[kPasses], vc[kPasses];
-        float sk, sv;
-        int64_t mine = find_row(0);
-        cache_rows[i] = mine;
-        load_scales(mine, &sk, &sv);
-        int64_t next = find_row(1);
-        cache_rows[128 + i] = next;
-        named_bar_sync(2, 128);
-        load(a.k, cache_rows, kc);
-        load(a.v, cache_rows, vc);
-        named_bar_sync(2, 128);   // before rows are replaced
-        bool ok = true;
-        for (int j = 0; j < tiles && ok; ++j) {
-            const int b = j & 1;
-            const int64_t after = find_row(j + 2);   // its page is on its way meanwhile
-            // scores and factors of tile j - 2 are read
-            if (j >= 2) ok = __all_sync(0xFFFFFFFFu, wait_bounded(&w_full[b], ((j - 2) >> 1) & 1, ctl));
-            const int64_t* rows_next = cache_rows + (b ^ 1) * 128;
-            if (ok) {
-                uint8_t* keys = smem + S::kKAt + b * S::kOperandBytes;
-#pragma unroll
-                for (int s = 0; s < kPasses; ++s) store_chunk16<D>(keys, token_in + s * kStep, chunk, kc[s]);
-                float* f = factors + b * 3 * 128;
-                const bool none = sv == -1.0f;
-                const float safe = sv < 0x1p-100f ? 0x1p-100f : sv;
-                f[i] = sk;
-                f[128 + i] = none ? -INFINITY : __log2f(safe);
-                f[256 + i] = none ? 0.0f : rcp(safe);
-                fence_proxy_async_smem();
-                mbar_arrive(&k_full[b]);
-                if (j + 1 < tiles) {
-                    load(a.k, rows_next, kc);
-                    load_scales(next, &sk, &sv);
-                }
-                // the values of tile j - 2 are read
-                if (j >= 2) ok = __all_sync(0xFFFFFFFFu, wait_bounded(&o_done[b], ((j - 2) >> 1) & 1, ctl));
-            }
-            if (ok) {
-                uint8_t* values = smem + S::kVAt + b * S::kOperandBytes;
-#pragma unroll
-                for (int s = 0; s < kPasses; ++s) store_chunk16<D>(values, token_in + s * kStep, chunk, vc[s]);
-                fence_proxy_async_smem();
-                mbar_arrive(&v_full[b]);
-                if (j + 1 < tiles) load(a.v, rows_next, vc);
-            }
-            // rows of tile j (whose loads were issued an iteration ago) make
-            // room for those of tile j + 2; after a wait that ran out the
-            // four warps leave together
-            next = after;
-            cache_rows[b * 128 + i] = after;
-            ok = named_bar_and(2, 128, ok);
-        }
+    } else if (warp < 16) {
+        // ---------------------------- codes to operands: keys, then values' warps
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp < 12)
+            convert_role<D, false>(a, smem, bars, ctl, tile0, tiles, head);
+        else
+            convert_role<D, true>(a, smem, bars, ctl, tile0, tiles, head);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        if (warp == 8 && lane == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 16 && lane == 0) {
             // -------------------------------------------------- MMA issue
             constexpr uint32_t kScoreDesc = idesc_f32acc(kTileRows, kTileTokens, 0, 0);
             constexpr uint32_t kValueDesc = idesc_f32acc(kTileRows, D, 0, 0) | (1u << 16);
+            // Descriptors are formed once: a step along k is an addition to
+            // the start address (in 16-byte units).  Formed at each MMA they
+            // kept this thread, and with it the tensor cores, at 90 cycles
+            // an MMA.
+            const uint64_t q_desc = sdesc_k_major_sw128(smem_addr(sq));
+            const uint64_t k_desc = sdesc_k_major_sw128(smem_addr(smem + S::kKAt));
+            const uint64_t v_desc = sdesc_mn_major_sw128(smem_addr(smem + S::kVAt), S::kColumnBytes);
+            constexpr uint64_t kStage = S::kOperandBytes >> 4, kColumn = S::kColumnBytes >> 4;
             auto scores = [&](int j) {
-                const uint32_t k0 = smem_addr(smem + S::kKAt + (j & 1) * S::kOperandBytes), q0 = smem_addr(sq);
+                const uint64_t kd = k_desc + (j & 1) * kStage;
+                const uint32_t d = tmem + 128 * (j & 1);
 #pragma unroll
                 for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        mma_f16(tmem + 128 * (j & 1), sdesc_k_major_sw128(q0 + h * S::kColumnBytes + 32 * x),
-                                sdesc_k_major_sw128(k0 + h * S::kColumnBytes + 32 * x), kScoreDesc,
-                                h > 0 || x > 0);
+                        mma_f16(d, q_desc + h * kColumn + 2 * x, kd + h * kColumn + 2 * x, kScoreDesc, h > 0 || x > 0);
                 mma_commit(&s_full[j & 1]);
             };
-            bool ok = wait_bounded(q_full, 0, ctl) && wait_bounded(&k_full[0], 0, ctl);
+            bool ok = wait_soon(q_full, 0, ctl) && wait_soon(&k_full[0], 0, ctl);
             bool issued = false;
             if (ok) {
                 tc_fence_after_sync();
@@ -572,20 +626,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                 const int b = j & 1;
                 if (j + 1 < tiles) {
                     // the buffer of tile j + 1's scores holds the weights of tile j - 1
-                    ok = wait_bounded(&k_full[b ^ 1], ((j + 1) >> 1) & 1, ctl) &&
-                         (j == 0 || wait_bounded(&o_done[b ^ 1], ((j - 1) >> 1) & 1, ctl));
+                    ok = wait_soon(&k_full[b ^ 1], ((j + 1) >> 1) & 1, ctl) &&
+                         (j == 0 || wait_soon(&o_done[b ^ 1], ((j - 1) >> 1) & 1, ctl));
                     if (!ok) break;
                     tc_fence_after_sync();
                     scores(j + 1);
                 }
-                ok = wait_bounded(&v_full[b], (j >> 1) & 1, ctl) && wait_bounded(&w_full[b], (j >> 1) & 1, ctl);
+                ok = wait_soon(&v_full[b], (j >> 1) & 1, ctl) && wait_soon(&w_full[b], (j >> 1) & 1, ctl);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t v0 = smem_addr(smem + S::kVAt + b * S::kOperandBytes);
+                const uint64_t vd = v_desc + b * kStage;
 #pragma unroll
                 for (int x = 0; x < kTileTokens / 16; ++x)
-                    mma_f16_ts(tmem + S::kOCol, tmem + 128 * b + 8 * x,
-                               sdesc_mn_major_sw128(v0 + x * 2048, S::kColumnBytes), kValueDesc, j > 0 || x > 0);
+                    mma_f16_ts(tmem + S::kOCol + D * b, tmem + 128 * b + 8 * x, vd + x * (2048 >> 4), kValueDesc,
+                               j > 1 || x > 0);
                 mma_commit(&o_done[b]);
             }
             if (issued) {
@@ -598,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     tc_fence_before_sync();
     cta_sync_diverged();
     tc_fence_after_sync();
-    if (warp == 8) {
+    if (warp == 16) {
         __syncwarp();
         tmem_dealloc<512>(tmem);
     }
