@@ -94,6 +94,8 @@ class _KvCache(ctypes.Structure):
 def lib():
     """The loaded libdg (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -168,8 +170,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream (which
+# takes longer than a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -328,17 +338,18 @@ _HALF_TYPES = {torch.bfloat16: DG_BF16, torch.float16: DG_FP16}
 
 def _heads(t, what, like=None):
     """[tokens, heads, head_dim] (any token and head stride) as a dg_heads."""
+    stride = t.stride()
+    if len(stride) != 3 or t.dtype not in _HALF_TYPES or (stride[2] != 1 and t.shape[2] > 1):
+        raise ValueError(f"{what} must be BF16 or FP16 [tokens, heads, head_dim] with contiguous heads")
     if not t.is_cuda:
         raise ValueError("tensor must be in CUDA device memory")
-    if t.dim() != 3 or t.dtype not in _HALF_TYPES or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{what} must be BF16 or FP16 [tokens, heads, head_dim] with contiguous heads")
     if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
         raise ValueError(f"{what} must have the shape and type of its counterpart")
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    return _Heads(t.data_ptr(), stride[0], stride[1])
 
 
 def _int32(t, n, what):
-    if t.dtype != torch.int32 or t.numel() != n:
+    if t.dtype is not torch.int32 or t.numel() != n:
         raise ValueError(f"{what} must be int32 with {n} elements")
     return _ptr(t)
 
@@ -386,25 +397,27 @@ def dg_rope_table(table, base=10000.0, scaling=DG_ROPE_UNSCALED, factor=1.0,
 def dg_rope(x, out, positions, rotary, inverse=False, stream=None) -> None:
     """out = x with each head's first rotary_dim elements turned (inverse: back)."""
     hx, ho = _heads(x, "x"), _heads(out, "out", x)
-    _check(lib().dg_rope(hx, ho, x.shape[0], x.shape[1], x.shape[2],
-                         _int32(positions, x.shape[0], "positions"), rotary.c, int(bool(inverse)),
-                         _HALF_TYPES[x.dtype], _stream(stream)), "dg_rope")
+    tokens, heads, dim = x.shape
+    _check(lib().dg_rope(hx, ho, tokens, heads, dim, _int32(positions, tokens, "positions"), rotary.c,
+                         1 if inverse else 0, _HALF_TYPES[x.dtype], _stream(stream)), "dg_rope")
 
 
 def dg_kv_append(k, v, slots, cache, positions=None, rotary=None, q=None, q_out=None,
                  stream=None) -> None:
     """Turn (with rotary) and quantise k, v [tokens, kv_heads, head_dim] into the
     cache's slots; q is turned into q_out in the same launch."""
-    n = k.shape[0]
     hk, hv = _heads(k, "k"), _heads(v, "v", k)
-    if k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+    n, heads, dim = k.shape
+    if heads != cache.kv_heads or dim != cache.head_dim:
         raise ValueError("k and v must have the cache's heads and head_dim")
     hq = ho = None
+    q_heads = 0
     if q is not None:
         hq, ho = _heads(q, "q"), _heads(q_out, "q_out", q)
-        if q.shape[0] != n or q.shape[2] != k.shape[2] or q.dtype != k.dtype:
+        q_tokens, q_heads, q_dim = q.shape
+        if q_tokens != n or q_dim != dim or q.dtype != k.dtype:
             raise ValueError("q must have the tokens, head_dim and type of k")
-    _check(lib().dg_kv_append(hq, ho, 0 if q is None else q.shape[1], hk, hv, n,
+    _check(lib().dg_kv_append(hq, ho, q_heads, hk, hv, n,
                               None if positions is None else _int32(positions, n, "positions"),
                               None if rotary is None else rotary.c, _int32(slots, n, "slots"),
                               cache.c, _HALF_TYPES[k.dtype], _stream(stream)), "dg_kv_append")
@@ -415,11 +428,12 @@ def dg_kv_read(cache, slots, k=None, v=None, stream=None) -> None:
     some = k if k is not None else v
     if some is None:
         return
-    if some.shape[1] != cache.kv_heads or some.shape[2] != cache.head_dim:
-        raise ValueError("k and v must have the cache's heads and head_dim")
     hk = None if k is None else _heads(k, "k")
     hv = None if v is None else _heads(v, "v", k)
-    _check(lib().dg_kv_read(cache.c, _int32(slots, some.shape[0], "slots"), some.shape[0], hk, hv,
+    n, heads, dim = some.shape
+    if heads != cache.kv_heads or dim != cache.head_dim:
+        raise ValueError("k and v must have the cache's heads and head_dim")
+    _check(lib().dg_kv_read(cache.c, _int32(slots, n, "slots"), n, hk, hv,
                             _HALF_TYPES[some.dtype], _stream(stream)), "dg_kv_read")
 
 
@@ -439,8 +453,9 @@ def dg_attn_decode(q, out, cache, page_table, kv_lens, scratch, scale=None, lse=
     hq, ho = _heads(q, "q"), _heads(out, "out", q)
     tokens, heads, dim = q.shape
     batch, max_pages = page_table.shape
-    if dim != cache.head_dim or page_table.dtype != torch.int32 or not page_table.is_cuda or \
-            (max_pages > 1 and page_table.stride(1) != 1):
+    pitch, step = page_table.stride()
+    if dim != cache.head_dim or page_table.dtype is not torch.int32 or not page_table.is_cuda or \
+            (max_pages > 1 and step != 1):
         raise ValueError("q must have the cache's head_dim, page_table must be int32 with contiguous rows")
     if tokens % batch if batch else tokens:
         raise ValueError("q must have the same number of tokens for each request")
@@ -450,10 +465,10 @@ def dg_attn_decode(q, out, cache, page_table, kv_lens, scratch, scale=None, lse=
         raise ValueError("prefix_pages must name every page of the prefix")
     _check(lib().dg_attn_decode(
         hq, ho, _ptr(lse), batch, tokens // batch if batch else 1, heads, cache.c, page_table.data_ptr(),
-        max(page_table.stride(0), max_pages), max_pages, _int32(kv_lens, batch, "kv_lens"),
+        max(pitch, max_pages), max_pages, _int32(kv_lens, batch, "kv_lens"),
         _int32(prefix_pages, prefix_pages.numel(), "prefix_pages") if prefix_len else None,
         prefix_len, dim ** -0.5 if scale is None else scale, _HALF_TYPES[q.dtype], _ptr(scratch),
-        scratch.numel() * scratch.element_size(), _stream(stream)), "dg_attn_decode")
+        scratch.nbytes, _stream(stream)), "dg_attn_decode")
 
 
 def dg_gemm_plan(M, N, K, in_dtype=DG_E4M3, out_dtype=DG_BF16, sm_count=0) -> dict:

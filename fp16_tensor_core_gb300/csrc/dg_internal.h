@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
+#include <unordered_map>
 #include <cuda_runtime.h>
 
 #include "dg.h"
@@ -94,6 +96,27 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Raises a kernel's dynamic shared memory limit to `bytes`, once per kernel
+// and device (the call costs about as much as half a launch).
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kern)(KArgs...), int bytes) {
+    struct Done {
+        std::mutex mu;
+        std::unordered_map<const void*, uint64_t> devices;   // one bit per device
+    };
+    static Done done;   // one per signature; keyed by kernel
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const void* key = reinterpret_cast<const void*>(kern);
+    std::lock_guard<std::mutex> lk(done.mu);
+    uint64_t& bits = done.devices[key];
+    if (bits >> dev & 1u) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) bits |= uint64_t{1} << dev;
+    return e;
 }
 
 // Runtime knobs (host globals, read at launch time).

@@ -25,11 +25,13 @@
 // ragged lengths balance and one long cache spreads over all SMs.  A warp
 // writes the units that lie inside its run; the pieces of a unit that
 // crosses warps are joined in shared memory, and those of a unit that
-// crosses blocks through scratch by a second, small kernel.  Every join goes
-// in token order: results do not depend on timing.
+// crosses blocks through scratch by the block that finishes last.  Every join
+// goes in token order: results do not depend on timing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 
 #include "attn_common.cuh"
 #include "dg_internal.h"
@@ -68,7 +70,8 @@ struct AttnArgs {
     bool causal;
     float scale_log2;          // softmax scale * log2(e)
     float* slots;              // two states of kRows rows per block
-    int4* crossings;           // per block: the unit that goes on past it
+    unsigned long long* arrivals;   // per block: of the unit that goes on past it
+    unsigned long long epoch;  // this launch's number (48 bits)
     const float* prefix;       // states of the prefix, per (token, head), or null
     float* states;             // where this call leaves states instead of outputs, or null
     uint32_t* status;
@@ -102,8 +105,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 template <int D, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;             // query rows per unit
-    static constexpr int kWarps = D == 256 ? 4 : D == 128 && NT == 2 ? 8 : 16;
-    static constexpr int kStages = D == 64 || kWarps <= 8 ? 2 : 1;
+    static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kPerSm = D == 128 && NT == 2 ? 1 : 2;   // resident blocks (registers)
+    static constexpr int kStages = D == 64 || kPerSm == 1 ? 2 : 1;
     static constexpr int kParts = D == 256 ? 2 : 1;
     static constexpr int kSpan = D / kParts;         // 64 or 128
     static constexpr int kDims = kSpan / 4;          // 16 or 32
@@ -142,7 +146,7 @@ __device__ __forceinline__ uint32_t chunk_at(int t, int chunk) {
 constexpr int kUnitCost = 1;
 struct Cursor {
     int b;       // request
-    int unit;    // key head * row_tiles + row tile
+    int h, rt;   // unit: key head, row tile
     int tile;
     int ntile;   // tiles of the request's units
     int len;     // its tokens
@@ -263,31 +267,73 @@ __device__ __forceinline__ void scan_tiles(const AttnArgs& a, uint32_t* cum, int
     __syncthreads();
 }
 
+__device__ __forceinline__ unsigned long long cas_acq_rel(unsigned long long* p, unsigned long long expect,
+                                                          unsigned long long put) {
+    unsigned long long was;
+    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                 : "=l"(was) : "l"(p), "l"(expect), "l"(put) : "memory");
+    return was;
+}
+
+// Counts one of `expected` (at least two) arrivals at *word and tells whether
+// it was the last; what the caller's block wrote before is visible to the
+// last one.  The word needs no initialisation: a count belongs to the launch
+// whose number stands above it, anything else counts as none.  The last
+// arrival leaves 0, so a launch that is replayed from a graph starts anew.
+// At most four atomics: 0 or another's remains are replaced by the first
+// arrival, all others add.
+__device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long epoch, int expected) {
+    unsigned long long seen = 0;   // what an earlier launch left
+    while (true) {
+        const unsigned long long was = cas_acq_rel(word, seen, epoch << 16 | 1);
+        if (was == seen) return false;
+        if (was >> 16 == epoch) break;
+        seen = was;
+    }
+    unsigned long long before;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(before) : "l"(word) : "memory");
+    const bool last = static_cast<int>(before & 0xFFFF) + 1 == expected;
+    if (last) *const_cast<volatile unsigned long long*>(word) = 0;
+    return last;
+}
+
+// a / b for non-negative a, in 32 bits where they suffice (as they do but for
+// the largest calls): a 64-bit division is a hundred instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // Room a warp takes: an equal share of all, at least one tile beside a
 // unit's cost.
 __device__ __forceinline__ int64_t room_per_warp(int64_t total, int64_t warps) {
-    return max(static_cast<int64_t>(kUnitCost + 1), (total + warps - 1) / warps);
+    return max(static_cast<int64_t>(kUnitCost + 1), quotient(total + warps - 1, warps));
 }
 
-// The request whose tiles hold flat position f (which is below the total).
-__device__ __forceinline__ int find_request(const uint32_t* cum, int batch, int64_t units, int64_t f) {
-    int lo = 0, hi = batch;   // cum[lo] * units <= f < cum[hi] * units
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<int64_t>(cum[mid]) * units <= f) lo = mid;
-        else hi = mid;
+// The request whose room holds position f (which is below the total), by a
+// whole warp: 32 places a step.
+__device__ __forceinline__ int find_request(const uint32_t* cum, int batch, int64_t units, int64_t f, int lane) {
+    int lo = 0, n = batch;   // it is one of lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const bool starts_before = lane * step < n && static_cast<int64_t>(cum[lo + lane * step]) * units <= f;
+        const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, starts_before));   // lane 0's always does
+        lo += k * step;
+        n = min(step, n - k * step);
     }
     return lo;
 }
 
 template <int D, int NT, bool kFp16>
-__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1)
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kPerSm)
 attn_split_kernel(const AttnArgs a) {
     using S = Shape<D, NT>;
     constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kStages = S::kStages, kRows = S::kRows;
+    constexpr int kParts = D > 128 ? 2 : 1;   // float4s of a row a lane
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t warp_sum[kWarps];
     __shared__ int piece_b[2 * kWarps], piece_unit[2 * kWarps];   // request (-1: no piece), unit
+    __shared__ bool joins[2];
     uint32_t* cum = reinterpret_cast<uint32_t*>(smem + S::kSmem);
     int* lens = reinterpret_cast<int*>(cum + a.batch + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,38 +370,42 @@ attn_split_kernel(const AttnArgs a) {
 
     if (f0 < f1) {
         // ---- the run's tiles: from the one at f0 up to the one at f1
-        auto at_room = [&](int64_t f) {
-            Cursor u;
-            u.b = find_request(cum, a.batch, units, f);
-            const int room = static_cast<int>(cum[u.b + 1] - cum[u.b]);
-            u.ntile = room - kUnitCost;
-            const int64_t in = f - static_cast<int64_t>(cum[u.b]) * units;
-            u.unit = in < 0x7FFFFFFF ? static_cast<int>(in) / room : static_cast<int>(in / room);
-            u.tile = max(0, static_cast<int>(in - static_cast<int64_t>(u.unit) * room) - kUnitCost);
-            u.len = lens[u.b];
-            return u;
-        };
-        const Cursor end = f1 < total ? at_room(f1) : Cursor{a.batch, 0, 0, 0, 0, 0};
         // Sets u.stop; whether u (at its unit's first tile of the run) is in the run.
         auto settle = [&](Cursor& u) {
-            u.stop = u.b == end.b && u.unit == end.unit ? end.tile : u.ntile;
-            return u.b < a.batch && u.tile < u.stop;
+            const int64_t tiles_at = static_cast<int64_t>(cum[u.b]) * units +
+                                     static_cast<int64_t>(u.h * a.row_tiles + u.rt) * (u.ntile + kUnitCost) + kUnitCost;
+            u.stop = static_cast<int>(min(max(f1 - tiles_at, static_cast<int64_t>(0)), static_cast<int64_t>(u.ntile)));
+            return u.tile < u.stop;
         };
         // The next tile; whether it is in the run.
         auto advance = [&](Cursor& u) {
             if (++u.tile < u.stop) return true;
             if (u.stop < u.ntile) return false;
             u.tile = 0;
-            if (++u.unit == units) {
-                u.unit = 0;
-                do ++u.b; while (u.b < a.batch && cum[u.b + 1] == cum[u.b]);
-                if (u.b == a.batch) return false;
-                u.ntile = static_cast<int>(cum[u.b + 1] - cum[u.b]) - kUnitCost;
-                u.len = lens[u.b];
+            if (++u.rt == a.row_tiles) {
+                u.rt = 0;
+                if (++u.h == a.kv_heads) {
+                    u.h = 0;
+                    do ++u.b; while (u.b < a.batch && cum[u.b + 1] == cum[u.b]);
+                    if (u.b == a.batch) return false;
+                    u.ntile = static_cast<int>(cum[u.b + 1] - cum[u.b]) - kUnitCost;
+                    u.len = lens[u.b];
+                }
             }
             return settle(u);
         };
-        Cursor at = at_room(f0);
+        Cursor at;
+        {
+            at.b = find_request(cum, a.batch, units, f0, lane);
+            const int room = static_cast<int>(cum[at.b + 1] - cum[at.b]);
+            at.ntile = room - kUnitCost;
+            at.len = lens[at.b];
+            const int64_t in_b = f0 - static_cast<int64_t>(cum[at.b]) * units;
+            const int unit = static_cast<int>(quotient(in_b, room));
+            at.tile = max(0, static_cast<int>(in_b - static_cast<int64_t>(unit) * room) - kUnitCost);
+            at.h = a.row_tiles == 1 ? unit : unit / a.row_tiles;
+            at.rt = unit - at.h * a.row_tiles;
+        }
         bool running = settle(at);
         Cursor in = at;
 
@@ -370,8 +420,7 @@ attn_split_kernel(const AttnArgs a) {
             if (t >= in.len) return;
             const int p = a.page_table[in.b * a.table_stride + (t >> a.page_shift)];
             if (p >= 0 && p < a.pages) {
-                const int h = in.unit / a.row_tiles;
-                token_row = ((static_cast<int64_t>(p) * a.kv_heads + h) << a.page_shift) + (t & in_page);
+                token_row = ((static_cast<int64_t>(p) * a.kv_heads + in.h) << a.page_shift) + (t & in_page);
             } else {
                 atomicOr(a.status, kStatusBadArgument);
             }
@@ -406,20 +455,6 @@ attn_split_kernel(const AttnArgs a) {
             load_codes(a.v, ring + (kStages + stage) * S::kTileBytes);
         };
 
-        bool more = running;   // `in` is a tile of this run
-        if (more) find_row();
-#pragma unroll 1
-        for (int s = 0; s < kStages; ++s) {
-            if (more) load_keys(s);
-            cp_commit();
-            if (more) {
-                load_values(s);
-                more = advance(in);
-                if (more) find_row();
-            }
-            cp_commit();
-        }
-
         // This unit's queries as the first product's B operand (row 8 n + g
         // of the unit), and per row 8 n + 2c + i of this lane's scores:
         uint32_t qb[NT][D / 16][2];
@@ -427,72 +462,99 @@ attn_split_kernel(const AttnArgs a) {
         int seen[NT][2];          // tokens the row sees
         float m[NT][2], l[NT][2]; // running maximum; this lane's part of l
         float acc[D / 16][NT][4]; // [.][n][i]: dim pair's first, [.][n][2 + i]: second
-        int seen_min = 0, stage = 0, first_tile = 0, h = 0, r0 = 0;
-        bool fresh = true;
+        int seen_min = 0, stage = 0, first_tile = 0;
+        // The queries of unit `at`: rows 8 n + g.
+        auto load_queries = [&](uint4 (&w)[NT][D / 32]) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int r = at.rt * kRows + 8 * n + g;
+                int64_t token = 0;
+                int head = 0;
+                if (r < a.rows) row_place(a, at.b, at.h, r, &token, &head);
+                const uint16_t* src = a.q + token * a.q_ts + head * a.q_hs + c * S::kDims;
+#pragma unroll
+                for (int p = 0; p < S::kParts; ++p)
+#pragma unroll
+                    for (int i = 0; i < S::kDims / 8; ++i)
+                        w[n][p * (S::kDims / 8) + i] =
+                            r < a.rows ? *reinterpret_cast<const uint4*>(src + p * S::kSpan + 8 * i)
+                                       : make_uint4(0, 0, 0, 0);
+            }
+        };
+        // Makes `at` the current unit, with those queries.
+        auto take_up = [&](uint4 (&w)[NT][D / 32]) {
+            first_tile = at.tile;
+            seen_min = at.len;
+            const int r0 = at.rt * kRows;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float mul = 1.0f, factor = a.scale_log2;
+                if constexpr (!kFp16) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) top = max(top, top_abs_bf16(w[n][k]));
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    const PowerOfTwo p = power_below(top);
+                    mul = p.inverse;
+                    factor *= p.value;
+                }
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint4 v = kFp16 ? w[n][k] : bf16_to_half8(w[n][k], mul);
+                    // dims 8k + 2i, +1 of the lane's run: MMA step 2k + i/2
+                    qb[n][2 * k][0] = v.x;
+                    qb[n][2 * k][1] = v.y;
+                    qb[n][2 * k + 1][0] = v.z;
+                    qb[n][2 * k + 1][1] = v.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = r0 + 8 * n + 2 * c + i;
+                    qscale[n][i] = __shfl_sync(0xFFFFFFFFu, factor, 4 * (2 * c + i));
+                    seen[n][i] = rr >= a.rows || !a.causal ? at.len
+                                                           : max(0, at.len - a.q_len + 1 + rr / a.group);
+                    seen_min = min(seen_min, seen[n][i]);
+                    m[n][i] = -INFINITY;
+                    l[n][i] = 0.0f;
+                }
+            }
+            seen_min = __reduce_min_sync(0xFFFFFFFFu, seen_min);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][n][i] = 0.0f;
+        };
+
+        // ---- the first unit's queries travel with the first tiles
+        bool more = running;   // `in` is a tile of this run
+        {
+            uint4 w[NT][D / 32];
+            if (more) find_row();
+            if (running) load_queries(w);
+#pragma unroll 1
+            for (int s = 0; s < kStages; ++s) {
+                if (more) load_keys(s);
+                cp_commit();
+                if (more) {
+                    load_values(s);
+                    more = advance(in);
+                    if (more) find_row();
+                }
+                cp_commit();
+            }
+            if (running) take_up(w);
+        }
+        bool fresh = false;
 
         while (running) {
             if (fresh) {
-                // ---- a new unit: its queries
+                uint4 w[NT][D / 32];
+                load_queries(w);
+                take_up(w);
                 fresh = false;
-                h = at.unit / a.row_tiles;
-                r0 = (at.unit - h * a.row_tiles) * kRows;
-                first_tile = at.tile;
-                seen_min = at.len;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int r = r0 + 8 * n + g;
-                    const bool valid = r < a.rows;
-                    int64_t token = 0;
-                    int head = 0;
-                    if (valid) row_place(a, at.b, h, r, &token, &head);
-                    const uint16_t* src = a.q + token * a.q_ts + head * a.q_hs;
-                    uint4 w[D / 32];
-#pragma unroll
-                    for (int p = 0; p < S::kParts; ++p)
-#pragma unroll
-                        for (int i = 0; i < S::kDims / 8; ++i)
-                            w[p * (S::kDims / 8) + i] =
-                                valid ? *reinterpret_cast<const uint4*>(src + p * S::kSpan + c * S::kDims + 8 * i)
-                                      : make_uint4(0, 0, 0, 0);
-                    float mul = 1.0f, factor = a.scale_log2;
-                    if constexpr (!kFp16) {
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) top = max(top, top_abs_bf16(w[k]));
-                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                        const PowerOfTwo p = power_below(top);
-                        mul = p.inverse;
-                        factor *= p.value;
-                    }
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        if constexpr (!kFp16) w[k] = bf16_to_half8(w[k], mul);
-                        // dims 8k + 2i, +1 of the lane's run: MMA step 2k + i/2
-                        qb[n][2 * k][0] = w[k].x;
-                        qb[n][2 * k][1] = w[k].y;
-                        qb[n][2 * k + 1][0] = w[k].z;
-                        qb[n][2 * k + 1][1] = w[k].w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int rr = r0 + 8 * n + 2 * c + i;
-                        qscale[n][i] = __shfl_sync(0xFFFFFFFFu, factor, 4 * (2 * c + i));
-                        seen[n][i] = rr >= a.rows || !a.causal
-                                         ? at.len
-                                         : max(0, at.len - a.q_len + 1 + rr / a.group);
-                        seen_min = min(seen_min, seen[n][i]);
-                        m[n][i] = -INFINITY;
-                        l[n][i] = 0.0f;
-                    }
-                }
-                seen_min = __reduce_min_sync(0xFFFFFFFFu, seen_min);
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[j][n][i] = 0.0f;
             }
 
             // ---- scores: s[t][n][..] of tokens 4g + 2t (first two) and 4g + 2t + 1
@@ -664,10 +726,11 @@ attn_split_kernel(const AttnArgs a) {
 
             // ---- the unit's (or the run's) end
             const bool unit_end = at.tile + 1 == at.ntile;
-            const int was_b = at.b, was_unit = at.unit;
+            const Cursor was = at;
             running = advance(at);
             if (unit_end || !running) {
                 fresh = true;
+                const int r0 = was.rt * kRows;
                 const bool whole = unit_end && first_tile == 0;
                 // first piece of the run when its unit began before it, else the last one
                 const bool is_head = !whole && first_tile != 0;
@@ -677,8 +740,8 @@ attn_split_kernel(const AttnArgs a) {
                     __syncwarp();
                 }
                 if (!whole && lane == 0) {
-                    piece_b[2 * warp + (is_head ? 0 : 1)] = was_b;
-                    piece_unit[2 * warp + (is_head ? 0 : 1)] = was_unit;
+                    piece_b[2 * warp + (is_head ? 0 : 1)] = was.b;
+                    piece_unit[2 * warp + (is_head ? 0 : 1)] = was.h * a.row_tiles + was.rt;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -693,7 +756,7 @@ attn_split_kernel(const AttnArgs a) {
                         if (whole) {
                             int64_t token;
                             int head;
-                            row_place(a, was_b, h, r0 + rr, &token, &head);
+                            row_place(a, was.b, was.h, r0 + rr, &token, &head);
                             e = row_end<D>(a, token, head, m[n][i], l[n][i], g == 0);
                         } else {
                             e.state = stash + rr * S::kState;
@@ -717,11 +780,15 @@ attn_split_kernel(const AttnArgs a) {
     }
     __syncthreads();
 
-    // ---- join the pieces of each unit, in warp (token) order.  Lane p of
-    // every warp looks at piece p; a unit's pieces are neighbours among those
-    // that exist, and its rows are dealt out over the warps.
+    // ---- joins.  First the pieces of each unit in this block, in warp
+    // (token) order: lane p of every warp looks at piece p; a unit's pieces
+    // are neighbours among those that exist, and its rows are dealt out over
+    // the warps.  Then, by the last block to arrive at it, the states of a
+    // unit that crosses blocks, in block (token) order: lane p looks at the
+    // p-th of them.  Both go through the same few instructions: code that a
+    // block runs only once costs it more in fetches than in execution (the
+    // same joins unrolled on their own: 4 to 14 us a call).
     static_assert(2 * kWarps <= 32, "a lane per piece");
-    bool crossed = false;
     const int my_b = lane < 2 * kWarps ? piece_b[lane] : -1;
     const int my_unit = my_b >= 0 ? piece_unit[lane] : 0;
     const uint32_t exist = __ballot_sync(0xFFFFFFFFu, my_b >= 0);
@@ -729,134 +796,173 @@ attn_split_kernel(const AttnArgs a) {
     const int prev = below != 0 ? 31 - __clz(below) : lane;
     const int prev_b = __shfl_sync(0xFFFFFFFFu, my_b, prev), prev_unit = __shfl_sync(0xFFFFFFFFu, my_unit, prev);
     uint32_t starts = __ballot_sync(0xFFFFFFFFu, my_b >= 0 && (below == 0 || prev_b != my_b || prev_unit != my_unit));
-    const uint8_t* my_piece = (lane & 1) ? smem + (lane >> 1) * S::kRingBytes
-                                         : smem + kWarps * S::kRingBytes + (lane >> 1) * S::kStashBytes;
-    int turn = 0;   // (unit, row) pairs so far
-    while (starts != 0) {
-        const int first = __ffs(starts) - 1;
-        starts &= starts - 1;
-        const uint32_t upto = starts != 0 ? (starts & -starts) - 1u : 0xFFFFFFFFu;
-        const uint32_t chain = exist & upto & ~((1u << first) - 1u);
-        const int b = __shfl_sync(0xFFFFFFFFu, my_b, first), unit = __shfl_sync(0xFFFFFFFFu, my_unit, first);
-        const int64_t room = cum[b + 1] - cum[b];
-        const int64_t u0 = static_cast<int64_t>(cum[b]) * units + unit * room, u1 = u0 + room;
+    const float* my_piece = reinterpret_cast<const float*>(
+        (lane & 1) ? smem + (lane >> 1) * S::kRingBytes
+                   : smem + kWarps * S::kRingBytes + (lane >> 1) * S::kStashBytes);
+    // What lane p knows of the unit whose pieces begin with piece p.
+    const bool is_start = (starts >> lane & 1u) != 0;
+    int my_h = 0, my_r0 = 0, my_rows = 0, my_to = 2, my_first = 0, my_n = 0;
+    if (is_start) {
+        my_h = a.row_tiles == 1 ? my_unit : my_unit / a.row_tiles;
+        my_r0 = (my_unit - my_h * a.row_tiles) * kRows;
+        my_rows = min(kRows, a.rows - my_r0);
+        const int64_t room = cum[my_b + 1] - cum[my_b], per_block = kWarps * run;
+        const int64_t u0 = static_cast<int64_t>(cum[my_b]) * units + my_unit * room, u1 = u0 + room;
         const bool begins = block0 <= u0 + kUnitCost, ends = u1 <= block1;
-        float* slot = a.slots + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * (kRows * S::kState);
-        const int h = unit / a.row_tiles, r0 = (unit - h * a.row_tiles) * kRows;
-        const int rows = min(kRows, a.rows - r0);
-        const bool mine_too = (chain >> lane & 1u) != 0;
-        for (int r = ((warp - turn) % kWarps + kWarps) % kWarps; r < rows; r += kWarps) {
-            const float2 ml = mine_too ? reinterpret_cast<const float2*>(my_piece)[r * (S::kState / 2)]
-                                       : make_float2(-INFINITY, 0.0f);
-            float m = ml.x;
+        if (!(begins && ends)) {
+            // slot 1 when it goes on in a later block, 0 when it began in an earlier one
+            my_to = begins ? 1 : 0;
+            my_first = begins ? static_cast<int>(blockIdx.x) : static_cast<int>(quotient(u0 + kUnitCost, per_block));
+            my_n = (ends ? static_cast<int>(blockIdx.x) : static_cast<int>(quotient(u1 - 1, per_block))) - my_first + 1;
+        }
+    }
+    uint32_t crossing = __ballot_sync(0xFFFFFFFFu, is_start && my_to != 2);   // at most two
+    bool again = false;   // the second phase
+    int turn = 0;         // (unit, row) pairs so far
+    while (true) {
+        if (starts == 0) {
+            if (again || crossing == 0) break;
+            __syncthreads();
+            if (warp == 0 && is_start && my_to != 2)
+                joins[my_to] = arrive_last(a.arrivals + my_first, a.epoch, my_n);
+            __syncthreads();
+            again = true;
+            starts = __ballot_sync(0xFFFFFFFFu, is_start && my_to != 2 && joins[my_to & 1]);
+            if (starts == 0) break;
+        }
+        const int p = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const int b = __shfl_sync(0xFFFFFFFFu, my_b, p), h = __shfl_sync(0xFFFFFFFFu, my_h, p);
+        const int r0 = __shfl_sync(0xFFFFFFFFu, my_r0, p), rows = __shfl_sync(0xFFFFFFFFu, my_rows, p);
+        const int to = again ? 2 : __shfl_sync(0xFFFFFFFFu, my_to, p);
+        const int first = __shfl_sync(0xFFFFFFFFu, my_first, p);
+        const int n = again ? __shfl_sync(0xFFFFFFFFu, my_n, p) : 32;
+        const float* from;   // this lane's piece of row 0, or null
+        if (again) {
+            // slot 1 of the first block, then slot 0 of each later one
+            from = a.slots + (2 * static_cast<int64_t>(first + lane) + (lane == 0 ? 1 : 0)) * (kRows * S::kState);
+        } else {
+            const uint32_t upto = starts != 0 ? (starts & -starts) - 1u : 0xFFFFFFFFu;
+            from = (exist & upto & ~((1u << p) - 1u)) >> lane & 1u ? my_piece : nullptr;
+        }
+#pragma unroll 1
+        for (int r = (warp - turn) & (kWarps - 1); r < rows; r += kWarps) {
+            float m = -INFINITY, l = 0.0f;
+            float4 x[kParts];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const float w = mine_too ? ex2(ml.x - (m == -INFINITY ? 0.0f : m)) : 0.0f;
-            float l = mine_too ? w * ml.y : 0.0f;
+            for (int k = 0; k < kParts; ++k) x[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int c0 = 0; c0 < n; c0 += 32) {   // 32 pieces at a time
+                const float* mine = from;
+                if (again)
+                    mine = c0 + lane < n ? from + (c0 == 0 ? 0 : (2 * c0 - (lane == 0 ? 1 : 0)) * (kRows * S::kState)) : nullptr;
+                const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine != nullptr);
+                if (mine != nullptr) mine += r * S::kState;
+                const float2 ml = mine != nullptr ? *reinterpret_cast<const float2*>(mine) : make_float2(-INFINITY, 0.0f);
+                float top = ml.x;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                top = fmaxf(top, m);
+                const float base = top == -INFINITY ? 0.0f : top;
+                const float w = mine != nullptr ? ex2(ml.x - base) : 0.0f;
+                float sum = mine != nullptr ? w * ml.y : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                const float before = ex2(m - base);
+                l = fmaf(l, before, sum);
+                m = top;
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) x[k] = scaled(x[k], before);
+                // four pieces' loads in flight; a gap (weight 0) reads the first piece
+                const int lo = __ffs(valid) - 1, hi = 31 - __clz(valid);
+                const unsigned long long at = reinterpret_cast<unsigned long long>(mine);
+                const unsigned long long some = __shfl_sync(0xFFFFFFFFu, at, lo);
+#pragma unroll 1
+                for (int q0 = lo; q0 <= hi; q0 += 4) {
+                    float wq[4];
+                    float4 y[4][kParts];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const unsigned long long there = __shfl_sync(0xFFFFFFFFu, at, (q0 + q) & 31);
+                        wq[q] = __shfl_sync(0xFFFFFFFFu, w, (q0 + q) & 31);
+                        if (q0 + q > hi) wq[q] = 0.0f;
+                        const float* row = reinterpret_cast<const float*>(there != 0 && q0 + q <= hi ? there : some);
+                        if (D >= 128 || 4 * lane < D) {
+#pragma unroll
+                            for (int k = 0; k < kParts; ++k)
+                                y[q][k] = *reinterpret_cast<const float4*>(row + 4 + 4 * lane + 128 * k);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int k = 0; k < kParts; ++k) x[k] = plus_scaled(x[k], wq[q], y[q][k]);
+                }
+            }
             RowEnd e;
-            if (begins && ends) {
+            if (to == 2) {
                 int64_t token;
                 int head;
                 row_place(a, b, h, r0 + r, &token, &head);
                 e = row_end<D>(a, token, head, m, l, lane == 0);
             } else {
-                e.state = slot + r * S::kState;
+                e.state = a.slots + ((2 * static_cast<int64_t>(blockIdx.x) + to) * kRows + r) * S::kState;
                 if (lane == 0) *reinterpret_cast<float2*>(e.state) = make_float2(m, l);
             }
+            if (D >= 128 || 4 * lane < D) {
 #pragma unroll
-            for (int d0 = 0; d0 < D; d0 += 128) {
-                const int d = d0 + 4 * lane;
-                float4 x = make_float4(0, 0, 0, 0);
-                for (uint32_t left = chain; left != 0; left &= left - 1) {
-                    const int p = __ffs(left) - 1;
-                    const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
-                    const uint8_t* base = (p & 1) ? smem + (p >> 1) * S::kRingBytes
-                                                  : smem + kWarps * S::kRingBytes + (p >> 1) * S::kStashBytes;
-                    if (D >= 128 || d < D) {
-                        const float4 y = reinterpret_cast<const float4*>(base)[(r * S::kState + 4 + d) / 4];
-                        x = plus_scaled(x, wp, y);
-                    }
-                }
-                if (D >= 128 || d < D) emit4<D, kFp16>(e, d, x);
+                for (int k = 0; k < kParts; ++k) emit4<D, kFp16>(e, 4 * lane + 128 * k, x[k]);
             }
         }
         turn += rows;
-        // what the joining kernel needs to know of this block's end
-        if (begins && !ends && threadIdx.x == 0) {
-            const int last = static_cast<int>((u1 - 1) / (kWarps * run));
-            a.crossings[blockIdx.x] = make_int4(b, unit, last, 0);
-            crossed = true;
-        }
     }
-    if (threadIdx.x == 0 && !crossed) a.crossings[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
-// Joins the units that cross blocks: block x of the grid takes the unit that
-// begins in block x of the split kernel and goes on past it, warp y one of
-// its rows.
-template <int D, int NT, bool kFp16>
-__global__ void __launch_bounds__(128)
-attn_join_kernel(const AttnArgs a) {
-    constexpr int kState = Shape<D, NT>::kState, kRows = Shape<D, NT>::kRows;
-    pdl_wait();
-    const int4 crossing = a.crossings[blockIdx.x];
-    if (crossing.x < 0) return;
-    const int b = crossing.x, unit = crossing.y, first = blockIdx.x, last = crossing.z;
-    const int h = unit / a.row_tiles, r0 = (unit - h * a.row_tiles) * kRows;
-    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r0 + r >= a.rows) return;
-    int64_t token;
-    int head;
-    row_place(a, b, h, r0 + r, &token, &head);
-    // slot 1 of the first block, then slot 0 of each later one
-    constexpr int64_t kBlock = 2 * kRows * kState;
-    const float* tail = a.slots + first * kBlock + (kRows + r) * kState;
-    constexpr int kParts = D > 128 ? 2 : 1;
-    float4 x[kParts], y[kParts];
-    float m, l;
-    join_states<D>(tail + (kBlock - kRows * kState), kBlock, last - first, lane, &m, &l, y);
-    // the first piece, joined last: a sum of two
-    const float2 ml = *reinterpret_cast<const float2*>(tail);
-    const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
-    const float w0 = ex2(ml.x - base), w1 = ex2(m - base);
-    const bool live = 4 * lane < D;
-    const RowEnd e = row_end<D>(a, token, head, top, w0 * ml.y + w1 * l, lane == 0);
-    if (live) {
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-            x[k] = *reinterpret_cast<const float4*>(tail + 4 + 4 * lane + 128 * k);
-            emit4<D, kFp16>(e, 4 * lane + 128 * k, plus_scaled(scaled(x[k], w0), w1, y[k]));
-        }
+// Blocks of a launch: the two that an SM holds.  (A block spends about 15 us
+// on its start, its joins and its end, so more and smaller runs, handed to
+// the SMs that are done first, cost more than the evenness gains: 3 x 120001
+// tokens 97, 113 and 138 us with 2, 4 and 6 blocks per SM.)
+int attn_blocks(int sm_count) {
+    return 2 * sm_count;
+}
+
+// The arrival words' room in floats (keeping 16-byte alignment).
+int64_t arrival_floats(int sm_count) { return (static_cast<int64_t>(attn_blocks(sm_count)) * 2 + 3) / 4 * 4; }
+
+// Launch numbers: 48 bits from a starting point that another process' use of
+// the same memory is unlikely to have had.
+unsigned long long next_epoch() {
+    static std::atomic<unsigned long long> last{static_cast<unsigned long long>(
+        std::chrono::system_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull >> 16};
+    while (true) {
+        const unsigned long long e = last.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
+        if (e != 0) return e;
     }
 }
 
 template <int D, int NT, bool kFp16>
-cudaError_t run_split_nt(AttnArgs a, int blocks, cudaStream_t s) {
+cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     using S = Shape<D, NT>;
+    const int blocks = attn_blocks(sm_count);
     a.row_tiles = (a.rows + S::kRows - 1) / S::kRows;
     const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
     const size_t smem = S::kSmem + cum;
-    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, NT, kFp16>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
+    const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16>,
+                                     S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
     if (e != cudaSuccess) return e;
-    e = launch_kernel(attn_split_kernel<D, NT, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(blocks, (std::min(S::kRows, a.rows) + 3) / 4);
-    return launch_kernel(attn_join_kernel<D, NT, kFp16>, grid, dim3(128), 0, s, a);
+    a.epoch = next_epoch();
+    return launch_kernel(attn_split_kernel<D, NT, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
 }
 
 // 8-row units while a key head's rows fit one (a 16-row one would idle half
 // of its MMAs and registers), else 16-row ones; 256-wide heads leave no
 // registers for a second row tile.
 template <int D, bool kFp16>
-cudaError_t run_split(const AttnArgs& a, int blocks, cudaStream_t s) {
+cudaError_t run_split(const AttnArgs& a, int sm_count, cudaStream_t s) {
     if constexpr (D < 256) {
-        if (a.rows > 8) return run_split_nt<D, 2, kFp16>(a, blocks, s);
+        if (a.rows > 8) return run_split_nt<D, 2, kFp16>(a, sm_count, s);
     }
-    return run_split_nt<D, 1, kFp16>(a, blocks, s);
+    return run_split_nt<D, 1, kFp16>(a, sm_count, s);
 }
 
 template <int D, bool kFp16>
@@ -879,8 +985,8 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.q_heads = L.q_heads;
     a.group = L.q_heads / a.kv_heads;
     a.scale_log2 = static_cast<float>(L.scale * 1.4426950408889634074);
-    a.crossings = static_cast<int4*>(L.scratch);
-    a.slots = reinterpret_cast<float*>(a.crossings + L.sm_count);
+    a.arrivals = static_cast<unsigned long long*>(L.scratch);
+    a.slots = static_cast<float*>(L.scratch) + arrival_floats(L.sm_count);
     a.status = L.status;
     float* states = a.slots + attn_slot_floats(L.sm_count, D);
     const int64_t prefix_rows = static_cast<int64_t>(L.batch) * L.q_len * a.group;
@@ -916,7 +1022,7 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
 }  // namespace
 
 int64_t attn_slot_floats(int sm_count, int head_dim) {
-    return static_cast<int64_t>(2) * sm_count * kMaxUnitRows * (head_dim + 4);
+    return static_cast<int64_t>(2) * attn_blocks(sm_count) * kMaxUnitRows * (head_dim + 4);
 }
 
 int64_t attn_state_floats(int batch, int q_len, int q_heads, int head_dim) {
@@ -929,7 +1035,7 @@ bool attn_prefix_on_tensor_cores(int64_t rows, int head_dim) { return head_dim <
 
 int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
                            int sm_count) {
-    int64_t n = attn_slot_floats(sm_count, head_dim) + static_cast<int64_t>(sm_count) * 4;
+    int64_t n = arrival_floats(sm_count) + attn_slot_floats(sm_count, head_dim);
     if (prefix_len > 0)
         n += attn_state_floats(batch, q_len, q_heads, head_dim) + attn_prefix_slot_floats(sm_count, head_dim);
     return n * static_cast<int64_t>(sizeof(float));

@@ -682,8 +682,7 @@ __global__ void __launch_bounds__(128) attn_prefix_join_kernel(const PrefixArgs 
 
 template <int D, bool kFp16>
 cudaError_t run_prefix(const PrefixArgs& a, cudaStream_t s) {
-    const cudaError_t set = cudaFuncSetAttribute(
-        attn_prefix_kernel<D, kFp16>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixShape<D>::kSmem);
+    const cudaError_t set = allow_smem(attn_prefix_kernel<D, kFp16>, PrefixShape<D>::kSmem);
     if (set != cudaSuccess) return set;
     const unsigned blocks = static_cast<unsigned>(a.kv_heads) * a.splits * a.row_tiles;
     const cudaError_t e = launch_kernel(attn_prefix_kernel<D, kFp16>, dim3(blocks), dim3(kThreads),
