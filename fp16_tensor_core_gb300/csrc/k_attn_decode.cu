@@ -25,13 +25,11 @@
 // ragged lengths balance and one long cache spreads over all SMs.  A warp
 // writes the units that lie inside its run; the pieces of a unit that
 // crosses warps are joined in shared memory, and those of a unit that
-// crosses blocks through scratch by the block that finishes last.  Every join
-// goes in token order: results do not depend on timing.
+// crosses blocks through scratch by a second, small kernel.  Every join goes
+// in token order: results do not depend on timing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
-#include <chrono>
 
 #include "attn_common.cuh"
 #include "dg_internal.h"
@@ -70,8 +68,7 @@ struct AttnArgs {
     bool causal;
     float scale_log2;          // softmax scale * log2(e)
     float* slots;              // two states of kRows rows per block
-    unsigned long long* arrivals;   // per block: of the unit that goes on past it
-    unsigned long long epoch;  // this launch's number (48 bits)
+    int4* crossings;           // per block: the unit that goes on past it
     const float* prefix;       // states of the prefix, per (token, head), or null
     float* states;             // where this call leaves states instead of outputs, or null
     uint32_t* status;
@@ -107,7 +104,7 @@ struct Shape {
     static constexpr int kRows = 8 * NT;             // query rows per unit
     static constexpr int kWarps = D == 256 ? 4 : 8;
     static constexpr int kPerSm = D == 128 && NT == 2 ? 1 : 2;   // resident blocks (registers)
-    static constexpr int kStages = D == 64 || kPerSm == 1 ? 2 : 1;
+    static constexpr int kStages = D == 64 || (D == 128 && NT == 2) ? 2 : 1;
     static constexpr int kParts = D == 256 ? 2 : 1;
     static constexpr int kSpan = D / kParts;         // 64 or 128
     static constexpr int kDims = kSpan / 4;          // 16 or 32
@@ -267,36 +264,6 @@ __device__ __forceinline__ void scan_tiles(const AttnArgs& a, uint32_t* cum, int
     __syncthreads();
 }
 
-__device__ __forceinline__ unsigned long long cas_acq_rel(unsigned long long* p, unsigned long long expect,
-                                                          unsigned long long put) {
-    unsigned long long was;
-    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
-                 : "=l"(was) : "l"(p), "l"(expect), "l"(put) : "memory");
-    return was;
-}
-
-// Counts one of `expected` (at least two) arrivals at *word and tells whether
-// it was the last; what the caller's block wrote before is visible to the
-// last one.  The word needs no initialisation: a count belongs to the launch
-// whose number stands above it, anything else counts as none.  The last
-// arrival leaves 0, so a launch that is replayed from a graph starts anew.
-// At most four atomics: 0 or another's remains are replaced by the first
-// arrival, all others add.
-__device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long epoch, int expected) {
-    unsigned long long seen = 0;   // what an earlier launch left
-    while (true) {
-        const unsigned long long was = cas_acq_rel(word, seen, epoch << 16 | 1);
-        if (was == seen) return false;
-        if (was >> 16 == epoch) break;
-        seen = was;
-    }
-    unsigned long long before;
-    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(before) : "l"(word) : "memory");
-    const bool last = static_cast<int>(before & 0xFFFF) + 1 == expected;
-    if (last) *const_cast<volatile unsigned long long*>(word) = 0;
-    return last;
-}
-
 // a / b for non-negative a, in 32 bits where they suffice (as they do but for
 // the largest calls): a 64-bit division is a hundred instructions.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -333,7 +300,6 @@ attn_split_kernel(const AttnArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t warp_sum[kWarps];
     __shared__ int piece_b[2 * kWarps], piece_unit[2 * kWarps];   // request (-1: no piece), unit
-    __shared__ bool joins[2];
     uint32_t* cum = reinterpret_cast<uint32_t*>(smem + S::kSmem);
     int* lens = reinterpret_cast<int*>(cum + a.batch + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -780,14 +746,9 @@ attn_split_kernel(const AttnArgs a) {
     }
     __syncthreads();
 
-    // ---- joins.  First the pieces of each unit in this block, in warp
-    // (token) order: lane p of every warp looks at piece p; a unit's pieces
-    // are neighbours among those that exist, and its rows are dealt out over
-    // the warps.  Then, by the last block to arrive at it, the states of a
-    // unit that crosses blocks, in block (token) order: lane p looks at the
-    // p-th of them.  Both go through the same few instructions: code that a
-    // block runs only once costs it more in fetches than in execution (the
-    // same joins unrolled on their own: 4 to 14 us a call).
+    // ---- join the pieces of each unit, in warp (token) order.  Lane p of
+    // every warp looks at piece p; a unit's pieces are neighbours among those
+    // that exist, and its rows are dealt out over the warps.
     static_assert(2 * kWarps <= 32, "a lane per piece");
     const int my_b = lane < 2 * kWarps ? piece_b[lane] : -1;
     const int my_unit = my_b >= 0 ? piece_unit[lane] : 0;
@@ -801,7 +762,7 @@ attn_split_kernel(const AttnArgs a) {
                    : smem + kWarps * S::kRingBytes + (lane >> 1) * S::kStashBytes);
     // What lane p knows of the unit whose pieces begin with piece p.
     const bool is_start = (starts >> lane & 1u) != 0;
-    int my_h = 0, my_r0 = 0, my_rows = 0, my_to = 2, my_first = 0, my_n = 0;
+    int my_h = 0, my_r0 = 0, my_rows = 0, my_to = 2, my_n = 0;   // my_n: blocks from this one on
     if (is_start) {
         my_h = a.row_tiles == 1 ? my_unit : my_unit / a.row_tiles;
         my_r0 = (my_unit - my_h * a.row_tiles) * kRows;
@@ -812,91 +773,49 @@ attn_split_kernel(const AttnArgs a) {
         if (!(begins && ends)) {
             // slot 1 when it goes on in a later block, 0 when it began in an earlier one
             my_to = begins ? 1 : 0;
-            my_first = begins ? static_cast<int>(blockIdx.x) : static_cast<int>(quotient(u0 + kUnitCost, per_block));
-            my_n = (ends ? static_cast<int>(blockIdx.x) : static_cast<int>(quotient(u1 - 1, per_block))) - my_first + 1;
+            if (begins) my_n = static_cast<int>(quotient(u1 - 1, per_block)) - static_cast<int>(blockIdx.x) + 1;
         }
     }
-    uint32_t crossing = __ballot_sync(0xFFFFFFFFu, is_start && my_to != 2);   // at most two
-    bool again = false;   // the second phase
-    int turn = 0;         // (unit, row) pairs so far
-    while (true) {
-        if (starts == 0) {
-            if (again || crossing == 0) break;
-            __syncthreads();
-            if (warp == 0 && is_start && my_to != 2)
-                joins[my_to] = arrive_last(a.arrivals + my_first, a.epoch, my_n);
-            __syncthreads();
-            again = true;
-            starts = __ballot_sync(0xFFFFFFFFu, is_start && my_to != 2 && joins[my_to & 1]);
-            if (starts == 0) break;
-        }
+    if (warp == 0) {
+        // what the joining kernel needs to know of this block's end
+        const bool goes_on = is_start && my_to == 1;
+        if (goes_on) a.crossings[blockIdx.x] = make_int4(my_b, my_unit, my_n, 0);
+        if (!__any_sync(0xFFFFFFFFu, goes_on) && lane == 0) a.crossings[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    int turn = 0;   // (unit, row) pairs so far
+    while (starts != 0) {
         const int p = __ffs(starts) - 1;
         starts &= starts - 1;
+        const uint32_t upto = starts != 0 ? (starts & -starts) - 1u : 0xFFFFFFFFu;
+        const uint32_t chain = exist & upto & ~((1u << p) - 1u);
         const int b = __shfl_sync(0xFFFFFFFFu, my_b, p), h = __shfl_sync(0xFFFFFFFFu, my_h, p);
         const int r0 = __shfl_sync(0xFFFFFFFFu, my_r0, p), rows = __shfl_sync(0xFFFFFFFFu, my_rows, p);
-        const int to = again ? 2 : __shfl_sync(0xFFFFFFFFu, my_to, p);
-        const int first = __shfl_sync(0xFFFFFFFFu, my_first, p);
-        const int n = again ? __shfl_sync(0xFFFFFFFFu, my_n, p) : 32;
-        const float* from;   // this lane's piece of row 0, or null
-        if (again) {
-            // slot 1 of the first block, then slot 0 of each later one
-            from = a.slots + (2 * static_cast<int64_t>(first + lane) + (lane == 0 ? 1 : 0)) * (kRows * S::kState);
-        } else {
-            const uint32_t upto = starts != 0 ? (starts & -starts) - 1u : 0xFFFFFFFFu;
-            from = (exist & upto & ~((1u << p) - 1u)) >> lane & 1u ? my_piece : nullptr;
-        }
+        const int to = __shfl_sync(0xFFFFFFFFu, my_to, p);
+        const bool mine_too = (chain >> lane & 1u) != 0;
 #pragma unroll 1
         for (int r = (warp - turn) & (kWarps - 1); r < rows; r += kWarps) {
-            float m = -INFINITY, l = 0.0f;
+            const float2 ml = mine_too ? reinterpret_cast<const float2*>(my_piece)[r * (S::kState / 2)]
+                                       : make_float2(-INFINITY, 0.0f);
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float w = mine_too ? ex2(ml.x - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+            float l = mine_too ? w * ml.y : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
             float4 x[kParts];
 #pragma unroll
             for (int k = 0; k < kParts; ++k) x[k] = make_float4(0, 0, 0, 0);
 #pragma unroll 1
-            for (int c0 = 0; c0 < n; c0 += 32) {   // 32 pieces at a time
-                const float* mine = from;
-                if (again)
-                    mine = c0 + lane < n ? from + (c0 == 0 ? 0 : (2 * c0 - (lane == 0 ? 1 : 0)) * (kRows * S::kState)) : nullptr;
-                const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine != nullptr);
-                if (mine != nullptr) mine += r * S::kState;
-                const float2 ml = mine != nullptr ? *reinterpret_cast<const float2*>(mine) : make_float2(-INFINITY, 0.0f);
-                float top = ml.x;
+            for (uint32_t left = chain; left != 0; left &= left - 1) {
+                const int q = __ffs(left) - 1;
+                const float wq = __shfl_sync(0xFFFFFFFFu, w, q);
+                const uint8_t* base = (q & 1) ? smem + (q >> 1) * S::kRingBytes
+                                              : smem + kWarps * S::kRingBytes + (q >> 1) * S::kStashBytes;
+                if (D >= 128 || 4 * lane < D) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                top = fmaxf(top, m);
-                const float base = top == -INFINITY ? 0.0f : top;
-                const float w = mine != nullptr ? ex2(ml.x - base) : 0.0f;
-                float sum = mine != nullptr ? w * ml.y : 0.0f;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                const float before = ex2(m - base);
-                l = fmaf(l, before, sum);
-                m = top;
-#pragma unroll
-                for (int k = 0; k < kParts; ++k) x[k] = scaled(x[k], before);
-                // four pieces' loads in flight; a gap (weight 0) reads the first piece
-                const int lo = __ffs(valid) - 1, hi = 31 - __clz(valid);
-                const unsigned long long at = reinterpret_cast<unsigned long long>(mine);
-                const unsigned long long some = __shfl_sync(0xFFFFFFFFu, at, lo);
-#pragma unroll 1
-                for (int q0 = lo; q0 <= hi; q0 += 4) {
-                    float wq[4];
-                    float4 y[4][kParts];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const unsigned long long there = __shfl_sync(0xFFFFFFFFu, at, (q0 + q) & 31);
-                        wq[q] = __shfl_sync(0xFFFFFFFFu, w, (q0 + q) & 31);
-                        if (q0 + q > hi) wq[q] = 0.0f;
-                        const float* row = reinterpret_cast<const float*>(there != 0 && q0 + q <= hi ? there : some);
-                        if (D >= 128 || 4 * lane < D) {
-#pragma unroll
-                            for (int k = 0; k < kParts; ++k)
-                                y[q][k] = *reinterpret_cast<const float4*>(row + 4 + 4 * lane + 128 * k);
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int k = 0; k < kParts; ++k) x[k] = plus_scaled(x[k], wq[q], y[q][k]);
+                    for (int k = 0; k < kParts; ++k)
+                        x[k] = plus_scaled(x[k], wq, reinterpret_cast<const float4*>(base)[(r * S::kState + 4) / 4 + lane + 32 * k]);
                 }
             }
             RowEnd e;
@@ -918,40 +837,66 @@ attn_split_kernel(const AttnArgs a) {
     }
 }
 
-// Blocks of a launch: the two that an SM holds.  (A block spends about 15 us
-// on its start, its joins and its end, so more and smaller runs, handed to
-// the SMs that are done first, cost more than the evenness gains: 3 x 120001
-// tokens 97, 113 and 138 us with 2, 4 and 6 blocks per SM.)
-int attn_blocks(int sm_count) {
-    return 2 * sm_count;
-}
-
-// The arrival words' room in floats (keeping 16-byte alignment).
-int64_t arrival_floats(int sm_count) { return (static_cast<int64_t>(attn_blocks(sm_count)) * 2 + 3) / 4 * 4; }
-
-// Launch numbers: 48 bits from a starting point that another process' use of
-// the same memory is unlikely to have had.
-unsigned long long next_epoch() {
-    static std::atomic<unsigned long long> last{static_cast<unsigned long long>(
-        std::chrono::system_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull >> 16};
-    while (true) {
-        const unsigned long long e = last.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
-        if (e != 0) return e;
+// Joins the units that cross blocks: block x of the grid takes the unit that
+// begins in block x of the split kernel and goes on past it, warp y one of
+// its rows.
+template <int D, int NT, bool kFp16>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
+    constexpr int kState = Shape<D, NT>::kState, kRows = Shape<D, NT>::kRows, kParts = D > 128 ? 2 : 1;
+    pdl_wait();
+    const int4 unit = a.crossings[blockIdx.x];   // request, number, blocks
+    if (unit.x < 0) return;
+    const int h = unit.y / a.row_tiles, r0 = (unit.y - h * a.row_tiles) * kRows;
+    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r0 + r >= a.rows) return;
+    int64_t token;
+    int head;
+    row_place(a, unit.x, h, r0 + r, &token, &head);
+    // slot 1 of the first block, then slot 0 of each later one
+    constexpr int64_t kBlock = 2 * kRows * kState;
+    const float* first = a.slots + blockIdx.x * kBlock + (kRows + r) * kState;
+    float4 x[kParts], y[kParts];
+    float m, l;
+    const bool live = 4 * lane < D;
+    const float2 ml = *reinterpret_cast<const float2*>(first);
+    if (live) {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) x[k] = *reinterpret_cast<const float4*>(first + 4 + 4 * lane + 128 * k);
+    }
+    join_states<D>(first + (kBlock - kRows * kState), kBlock, unit.z - 1, lane, &m, &l, y);
+    const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.0f : top;
+    const float w0 = ex2(ml.x - base), w1 = ex2(m - base);
+    const RowEnd e = row_end<D>(a, token, head, top, w0 * ml.y + w1 * l, lane == 0);
+    if (live) {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+            emit4<D, kFp16>(e, 4 * lane + 128 * k, plus_scaled(scaled(x[k], w0), w1, y[k]));
     }
 }
+
+// Most blocks of a launch: the two that an SM holds.  (A block spends 10 us
+// on its start, its joins and its end, so more and smaller runs, handed to
+// the SMs that are done first, cost more than their evenness gains: 3 x
+// 120001 tokens 85 us with 2 blocks per SM, 97 with 3, 88 with 4.)
+int attn_blocks(int sm_count) { return 2 * sm_count; }
+
+// The crossings' room in floats.
+int64_t crossing_floats(int sm_count) { return static_cast<int64_t>(attn_blocks(sm_count)) * 4; }
 
 template <int D, int NT, bool kFp16>
 cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     using S = Shape<D, NT>;
-    const int blocks = attn_blocks(sm_count);
+    const int blocks = S::kPerSm * sm_count;
     a.row_tiles = (a.rows + S::kRows - 1) / S::kRows;
     const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
     const size_t smem = S::kSmem + cum;
     const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16>,
                                      S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
     if (e != cudaSuccess) return e;
-    a.epoch = next_epoch();
-    return launch_kernel(attn_split_kernel<D, NT, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
+    const cudaError_t k = launch_kernel(attn_split_kernel<D, NT, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
+    if (k != cudaSuccess) return k;
+    return launch_kernel(attn_join_kernel<D, NT, kFp16>, dim3(blocks, (std::min(S::kRows, a.rows) + 3) / 4),
+                         dim3(128), 0, s, a);
 }
 
 // 8-row units while a key head's rows fit one (a 16-row one would idle half
@@ -985,8 +930,8 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.q_heads = L.q_heads;
     a.group = L.q_heads / a.kv_heads;
     a.scale_log2 = static_cast<float>(L.scale * 1.4426950408889634074);
-    a.arrivals = static_cast<unsigned long long*>(L.scratch);
-    a.slots = static_cast<float*>(L.scratch) + arrival_floats(L.sm_count);
+    a.crossings = static_cast<int4*>(L.scratch);
+    a.slots = static_cast<float*>(L.scratch) + crossing_floats(L.sm_count);
     a.status = L.status;
     float* states = a.slots + attn_slot_floats(L.sm_count, D);
     const int64_t prefix_rows = static_cast<int64_t>(L.batch) * L.q_len * a.group;
@@ -1035,7 +980,7 @@ bool attn_prefix_on_tensor_cores(int64_t rows, int head_dim) { return head_dim <
 
 int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
                            int sm_count) {
-    int64_t n = arrival_floats(sm_count) + attn_slot_floats(sm_count, head_dim);
+    int64_t n = crossing_floats(sm_count) + attn_slot_floats(sm_count, head_dim);
     if (prefix_len > 0)
         n += attn_state_floats(batch, q_len, q_heads, head_dim) + attn_prefix_slot_floats(sm_count, head_dim);
     return n * static_cast<int64_t>(sizeof(float));
