@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "attn_common.cuh"
 #include "dg_internal.h"
@@ -291,7 +292,9 @@ __device__ __forceinline__ int find_request(const uint32_t* cum, int batch, int6
     return lo;
 }
 
-template <int D, int NT, bool kFp16>
+// kWhole: every block takes one whole unit instead (its warps equal runs of
+// the unit's tiles): nothing to search for, no unit that crosses blocks.
+template <int D, int NT, bool kFp16, bool kWhole>
 __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kPerSm)
 attn_split_kernel(const AttnArgs a) {
     using S = Shape<D, NT>;
@@ -305,24 +308,51 @@ attn_split_kernel(const AttnArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     pdl_wait();
-    scan_tiles<kThreads>(a, cum, lens, warp_sum);
     pdl_launch_dependents();
-
     const int units = a.kv_heads * a.row_tiles;
-    const int64_t total = static_cast<int64_t>(cum[a.batch]) * units;
-    const int64_t run = room_per_warp(total, static_cast<int64_t>(gridDim.x) * kWarps);
-    const int64_t block0 = min(total, static_cast<int64_t>(blockIdx.x) * kWarps * run);
-    const int64_t block1 = min(total, block0 + kWarps * run);
-    const int64_t f0 = min(total, block0 + warp * run), f1 = min(total, f0 + run);
+    Cursor unit;                // kWhole: this block's
+    int64_t run, block0, block1, f0, f1;   // room, or the unit's tiles
+    if constexpr (kWhole) {
+        unit.b = static_cast<int>(blockIdx.x) / units;
+        const int u = static_cast<int>(blockIdx.x) - unit.b * units;
+        unit.h = a.row_tiles == 1 ? u : u / a.row_tiles;
+        unit.rt = u - unit.h * a.row_tiles;
+        unit.len = request_len(a, unit.b);
+        unit.ntile = (unit.len + kTile - 1) / kTile;
+        if (unit.ntile == 0) {
+            const int r0 = unit.rt * kRows;
+            for (int i = threadIdx.x; i < min(kRows, a.rows - r0) * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), d = 4 * (i % (D / 4));
+                int64_t token;
+                int head;
+                row_place(a, unit.b, unit.h, r0 + r, &token, &head);
+                emit4<D, kFp16>(row_end<D>(a, token, head, -INFINITY, 0.0f, d == 0), d, make_float4(0, 0, 0, 0));
+            }
+            return;
+        }
+        run = (unit.ntile + kWarps - 1) / kWarps;
+        block0 = 0;
+        block1 = unit.ntile;
+        f0 = min(block1, warp * run);
+        f1 = min(block1, f0 + run);
+    } else {
+        scan_tiles<kThreads>(a, cum, lens, warp_sum);
+        const int64_t total = static_cast<int64_t>(cum[a.batch]) * units;
+        run = room_per_warp(total, static_cast<int64_t>(gridDim.x) * kWarps);
+        block0 = min(total, static_cast<int64_t>(blockIdx.x) * kWarps * run);
+        block1 = min(total, block0 + kWarps * run);
+        f0 = min(total, block0 + warp * run);
+        f1 = min(total, f0 + run);
 
-    // Requests without a token of their own: nothing below reaches them.
-    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-        if (cum[b + 1] != cum[b]) continue;
-        for (int i = threadIdx.x; i < a.q_len * a.q_heads * (D / 4); i += kThreads) {
-            const int row = i / (D / 4), d = 4 * (i % (D / 4));
-            const RowEnd e = row_end<D>(a, static_cast<int64_t>(b) * a.q_len + row / a.q_heads,
-                                        row % a.q_heads, -INFINITY, 0.0f, d == 0);
-            emit4<D, kFp16>(e, d, make_float4(0, 0, 0, 0));
+        // Requests without a token of their own: nothing below reaches them.
+        for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+            if (cum[b + 1] != cum[b]) continue;
+            for (int i = threadIdx.x; i < a.q_len * a.q_heads * (D / 4); i += kThreads) {
+                const int row = i / (D / 4), d = 4 * (i % (D / 4));
+                const RowEnd e = row_end<D>(a, static_cast<int64_t>(b) * a.q_len + row / a.q_heads,
+                                            row % a.q_heads, -INFINITY, 0.0f, d == 0);
+                emit4<D, kFp16>(e, d, make_float4(0, 0, 0, 0));
+            }
         }
     }
 
@@ -338,6 +368,10 @@ attn_split_kernel(const AttnArgs a) {
         // ---- the run's tiles: from the one at f0 up to the one at f1
         // Sets u.stop; whether u (at its unit's first tile of the run) is in the run.
         auto settle = [&](Cursor& u) {
+            if constexpr (kWhole) {
+                u.stop = static_cast<int>(f1);
+                return u.tile < u.stop;
+            }
             const int64_t tiles_at = static_cast<int64_t>(cum[u.b]) * units +
                                      static_cast<int64_t>(u.h * a.row_tiles + u.rt) * (u.ntile + kUnitCost) + kUnitCost;
             u.stop = static_cast<int>(min(max(f1 - tiles_at, static_cast<int64_t>(0)), static_cast<int64_t>(u.ntile)));
@@ -346,7 +380,7 @@ attn_split_kernel(const AttnArgs a) {
         // The next tile; whether it is in the run.
         auto advance = [&](Cursor& u) {
             if (++u.tile < u.stop) return true;
-            if (u.stop < u.ntile) return false;
+            if (kWhole || u.stop < u.ntile) return false;
             u.tile = 0;
             if (++u.rt == a.row_tiles) {
                 u.rt = 0;
@@ -361,7 +395,10 @@ attn_split_kernel(const AttnArgs a) {
             return settle(u);
         };
         Cursor at;
-        {
+        if constexpr (kWhole) {
+            at = unit;
+            at.tile = static_cast<int>(f0);
+        } else {
             at.b = find_request(cum, a.batch, units, f0, lane);
             const int room = static_cast<int>(cum[at.b + 1] - cum[at.b]);
             at.ntile = room - kUnitCost;
@@ -767,16 +804,18 @@ attn_split_kernel(const AttnArgs a) {
         my_h = a.row_tiles == 1 ? my_unit : my_unit / a.row_tiles;
         my_r0 = (my_unit - my_h * a.row_tiles) * kRows;
         my_rows = min(kRows, a.rows - my_r0);
-        const int64_t room = cum[my_b + 1] - cum[my_b], per_block = kWarps * run;
-        const int64_t u0 = static_cast<int64_t>(cum[my_b]) * units + my_unit * room, u1 = u0 + room;
-        const bool begins = block0 <= u0 + kUnitCost, ends = u1 <= block1;
-        if (!(begins && ends)) {
-            // slot 1 when it goes on in a later block, 0 when it began in an earlier one
-            my_to = begins ? 1 : 0;
-            if (begins) my_n = static_cast<int>(quotient(u1 - 1, per_block)) - static_cast<int>(blockIdx.x) + 1;
+        if constexpr (!kWhole) {
+            const int64_t room = cum[my_b + 1] - cum[my_b], per_block = kWarps * run;
+            const int64_t u0 = static_cast<int64_t>(cum[my_b]) * units + my_unit * room, u1 = u0 + room;
+            const bool begins = block0 <= u0 + kUnitCost, ends = u1 <= block1;
+            if (!(begins && ends)) {
+                // slot 1 when it goes on in a later block, 0 when it began in an earlier one
+                my_to = begins ? 1 : 0;
+                if (begins) my_n = static_cast<int>(quotient(u1 - 1, per_block)) - static_cast<int>(blockIdx.x) + 1;
+            }
         }
     }
-    if (warp == 0) {
+    if (!kWhole && warp == 0) {
         // what the joining kernel needs to know of this block's end
         const bool goes_on = is_start && my_to == 1;
         if (goes_on) a.crossings[blockIdx.x] = make_int4(my_b, my_unit, my_n, 0);
@@ -886,14 +925,27 @@ int64_t crossing_floats(int sm_count) { return static_cast<int64_t>(attn_blocks(
 template <int D, int NT, bool kFp16>
 cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     using S = Shape<D, NT>;
-    const int blocks = S::kPerSm * sm_count;
     a.row_tiles = (a.rows + S::kRows - 1) / S::kRows;
+    const dim3 threads(S::kWarps * 32);
+    // Whole units while a unit is at most four tiles a warp, by the page
+    // table's width (the lengths are not known here).  Measured with 32/8
+    // heads of 128, us, whole units against equal runs: 1 x 300 tokens 6.5 /
+    // 10.5, 8 x 1000 10.2 / 12.0, 64 x 400 15.8 / 16.9, 64 x 1000 23.4 /
+    // 22.8, 8 x 2000 16.1 / 12.7; one launch less besides.
+    const int64_t units = static_cast<int64_t>(a.batch) * a.kv_heads * a.row_tiles;
+    if (a.max_len <= 4 * S::kWarps * kTile && units <= INT_MAX) {
+        const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16, true>, S::kSmem);
+        if (e != cudaSuccess) return e;
+        return launch_kernel(attn_split_kernel<D, NT, kFp16, true>, dim3(static_cast<unsigned>(units)), threads,
+                             S::kSmem, s, a);
+    }
+    const int blocks = S::kPerSm * sm_count;
     const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
-    const size_t smem = S::kSmem + cum;
-    const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16>,
+    const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16, false>,
                                      S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
     if (e != cudaSuccess) return e;
-    const cudaError_t k = launch_kernel(attn_split_kernel<D, NT, kFp16>, dim3(blocks), dim3(S::kWarps * 32), smem, s, a);
+    const cudaError_t k = launch_kernel(attn_split_kernel<D, NT, kFp16, false>, dim3(blocks), threads,
+                                        S::kSmem + cum, s, a);
     if (k != cudaSuccess) return k;
     return launch_kernel(attn_join_kernel<D, NT, kFp16>, dim3(blocks, (std::min(S::kRows, a.rows) + 3) / 4),
                          dim3(128), 0, s, a);

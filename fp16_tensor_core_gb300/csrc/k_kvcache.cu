@@ -102,8 +102,10 @@ struct RopeArgs {
     int heads;
     int rot8;              // rotated dims / 8
     int items;             // work items per head
-    int head_steps;        // heads are taken in this many interleaved sets (one per thread)
-    int threads_per_token; // items * head_steps
+    int head_steps;        // heads are taken in this many interleaved sets
+    int sets;              // sets a block holds: all of them, or what fits it
+    int head_blocks;       // blocks that share out a token's sets
+    int threads_per_token; // items * sets
     int tokens_per_block;
     const int32_t* positions;   // null: nothing is rotated
     const float4* table;   // rows of rotary_dim floats: (cos, sin) per pair
@@ -119,12 +121,13 @@ struct RopeArgs {
 // its cosines and sines stay in registers across the heads, and both halves
 // of a pair are in its hands, so each element is read and written once.
 template <bool kFp16, bool kHalf, int kHeads>
-__device__ __forceinline__ void rope_block(const RopeArgs& a, int64_t block) {
+__device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, int head_block) {
     const int local = static_cast<int>(threadIdx.x) / a.threads_per_token;
     const int rest = static_cast<int>(threadIdx.x) - local * a.threads_per_token;
-    const int item = rest % a.items, h0 = rest / a.items;
-    const int64_t t = block * a.tokens_per_block + local;
-    if (local >= a.tokens_per_block || t >= a.tokens) return;
+    const int set = rest / a.items;
+    const int item = rest - set * a.items, h0 = head_block * a.sets + set;
+    const int64_t t = static_cast<int64_t>(token_block) * a.tokens_per_block + local;
+    if (local >= a.tokens_per_block || t >= a.tokens || h0 >= a.head_steps) return;
     const int64_t pos = a.positions != nullptr ? a.positions[t] : 0;
     const int slot = a.slots != nullptr ? a.slots[t] : -1;
     const int pair_items = kHalf ? a.rot8 / 2 : a.rot8;
@@ -196,7 +199,7 @@ template <bool kFp16, bool kHalf, int kHeads>
 __global__ void __launch_bounds__(256)
 rope_kernel(const RopeArgs a) {
     pdl_wait();
-    rope_block<kFp16, kHalf, kHeads>(a, blockIdx.x);
+    rope_block<kFp16, kHalf, kHeads>(a, blockIdx.x, blockIdx.y);
 }
 
 // ------------------------------------------------------------ cache writes
@@ -233,6 +236,15 @@ __device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+// Out of line: taken once in hundreds of rows.
+__device__ __noinline__ uint2 divide8(float x0, float x1, float x2, float x3, float x4, float x5,
+                                      float x6, float x7, float scale) {
+    const float q[8] = {__fdiv_rn(x0, scale), __fdiv_rn(x1, scale), __fdiv_rn(x2, scale),
+                        __fdiv_rn(x3, scale), __fdiv_rn(x4, scale), __fdiv_rn(x5, scale),
+                        __fdiv_rn(x6, scale), __fdiv_rn(x7, scale)};
+    return codes8(q);
+}
+
 // E4M3(fl32(x / scale)) of 8 elements, scale finite and at least 2^-60, |x|
 // at most about 448 scale.  An IEEE division per element would cost more
 // than the memory time of the whole row, so the quotient is enclosed: with
@@ -254,9 +266,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
     for (int i = 0; i < 8; ++i) q[i] = x[i] * above;
     const uint2 hi = codes8(q);
     if (lo.x == hi.x && lo.y == hi.y) return lo;
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], scale);
-    return codes8(q);
+    return divide8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale);
 }
 
 // A group of kLanes lanes owns one row (a key or value head) and walks over
@@ -365,8 +375,11 @@ kv_append_kernel(const AppendArgs a, const RopeArgs q, int kv_blocks, int kv_eve
     const int round = static_cast<int>(blockIdx.x) / kv_every;
     if (round < kv_blocks && static_cast<int>(blockIdx.x) - round * kv_every == kv_every - 1)
         append_block<kFp16, kHalf, kLanes, kTokens>(a, round);
-    else
-        rope_block<kFp16, kHalf, kTokens>(q, static_cast<int>(blockIdx.x) - min(round, kv_blocks));
+    else {
+        const int b = static_cast<int>(blockIdx.x) - min(round, kv_blocks);
+        const int token_block = q.head_blocks == 1 ? b : b / q.head_blocks;
+        rope_block<kFp16, kHalf, kTokens>(q, token_block, b - token_block * q.head_blocks);
+    }
 }
 
 // ------------------------------------------------------------- cache reads
@@ -519,14 +532,15 @@ RopeArgs rope_args(const dg_heads& x, const dg_heads& out, int64_t tokens, int h
     return a;
 }
 
-// Splits a rotation over blocks with `per_thread` heads a thread; false if a
-// token does not fit one block.  Returns the number of blocks.
+// Splits a rotation over blocks with `per_thread` heads a thread; returns
+// their number.
 int64_t rope_split(RopeArgs* a, int per_thread) {
     a->head_steps = (a->heads + per_thread - 1) / per_thread;
-    a->threads_per_token = a->items * a->head_steps;
-    if (a->threads_per_token > 256) return 0;
+    a->sets = std::min(a->head_steps, 256 / a->items);
+    a->head_blocks = (a->head_steps + a->sets - 1) / a->sets;
+    a->threads_per_token = a->items * a->sets;
     a->tokens_per_block = 256 / a->threads_per_token;
-    return (a->tokens + a->tokens_per_block - 1) / a->tokens_per_block;
+    return (a->tokens + a->tokens_per_block - 1) / a->tokens_per_block * a->head_blocks;
 }
 
 }  // namespace
@@ -534,28 +548,17 @@ int64_t rope_split(RopeArgs* a, int per_thread) {
 cudaError_t launch_rope(const dg_heads& x, const dg_heads& out, int64_t tokens, int heads,
                         int head_dim, const int32_t* positions, const dg_rotary& rot, bool inverse,
                         bool fp16, int sm_count, uint32_t* status, cudaStream_t s) {
-    const RopeArgs a = rope_args(x, out, tokens, heads, head_dim, positions, &rot, inverse, status);
+    RopeArgs a = rope_args(x, out, tokens, heads, head_dim, positions, &rot, inverse, status);
     const bool half = rot.layout == DG_ROPE_HALF;
     // Four heads a thread once that still leaves every SM two blocks.
     const int per_thread = tokens * heads * a.items < static_cast<int64_t>(4) * 2 * sm_count * 256 ? 1 : 4;
-    // A token has to fit one block: more heads a token than that are taken by further launches.
-    const int most = 256 / a.items * per_thread;
-    for (int h = 0; h < heads; h += most) {
-        RopeArgs b = a;
-        b.x += h * a.x_hs;
-        b.out += h * a.o_hs;
-        b.heads = std::min(most, heads - h);
-        const dim3 grid(static_cast<unsigned>(rope_split(&b, per_thread)));
-        cudaError_t e;
-        if (fp16)
-            e = half ? rope_dispatch<true, true>(b, per_thread, grid, s)
-                     : rope_dispatch<true, false>(b, per_thread, grid, s);
-        else
-            e = half ? rope_dispatch<false, true>(b, per_thread, grid, s)
-                     : rope_dispatch<false, false>(b, per_thread, grid, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const int64_t blocks = rope_split(&a, per_thread) / a.head_blocks;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.head_blocks));
+    if (fp16)
+        return half ? rope_dispatch<true, true>(a, per_thread, grid, s)
+                    : rope_dispatch<true, false>(a, per_thread, grid, s);
+    return half ? rope_dispatch<false, true>(a, per_thread, grid, s)
+                : rope_dispatch<false, false>(a, per_thread, grid, s);
 }
 
 cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_heads,
@@ -600,27 +603,6 @@ cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_hea
         qa.slots = slots;
         qa.nslots = cache.pages * cache.page_size;
         q_blocks = rope_split(&qa, few ? 1 : 4);
-        if (q_blocks == 0) {
-            // More heads than one block takes: a launch of their own.
-            const int most = 256 / qa.items * (few ? 1 : 4);
-            for (int h = most; h < q_heads; h += most) {
-                RopeArgs b = qa;
-                b.x += h * qa.x_hs;
-                b.out += h * qa.o_hs;
-                b.heads = std::min(most, q_heads - h);
-                const dim3 grid(static_cast<unsigned>(rope_split(&b, few ? 1 : 4)));
-                cudaError_t e;
-                if (fp16)
-                    e = half ? rope_dispatch<true, true>(b, few ? 1 : 4, grid, s)
-                             : rope_dispatch<true, false>(b, few ? 1 : 4, grid, s);
-                else
-                    e = half ? rope_dispatch<false, true>(b, few ? 1 : 4, grid, s)
-                             : rope_dispatch<false, false>(b, few ? 1 : 4, grid, s);
-                if (e != cudaSuccess) return e;
-            }
-            qa.heads = most;
-            q_blocks = rope_split(&qa, few ? 1 : 4);
-        }
     }
     if (q_blocks + kv_blocks > INT_MAX) return cudaErrorInvalidValue;
     if (fp16) {
