@@ -10,8 +10,8 @@
 // A CTA holds one 128-row tile of one key head and walks over its share of
 // the prefix.  Roles: four warps each take the codes of the keys and of the
 // values from the cache and write them as FP16 (exact) into swizzled shared
-// memory, in two stages; one thread issues the MMAs; two groups of four warps turn scores into
-// weights.  Tiles of even and odd number are two streams with a group, a
+// memory, in two stages; one thread issues the MMAs; two groups of four warps
+// turn scores into weights.  Tiles of even and odd number are two streams with a group, a
 // stage, S and O of their own (a tile's weights take the place of its
 // scores), joined at the end: while one stream's weights are formed the
 // tensor cores work for the other.  One stream alone left them idle: its
@@ -165,8 +165,8 @@ struct PrefixShape {
     static_assert(kOCol + 2 * D <= 512, "tensor memory");
     static constexpr int kKAt = kOperandBytes;
     static constexpr int kVAt = kKAt + 2 * kOperandBytes;
-    static constexpr int kFactorsAt = kVAt + 2 * kOperandBytes;  // [2][3][128] per-token factors
-    static constexpr int kRowsAt = kFactorsAt + 2 * 3 * 128 * 4; // [2][2][128] cache rows
+    static constexpr int kFactorsAt = kVAt + 2 * kOperandBytes;  // [4][3][128] per-token factors
+    static constexpr int kRowsAt = kFactorsAt + 4 * 3 * 128 * 4; // [2][2][128] cache rows
     static constexpr int kQScaleAt = kRowsAt + 2 * 2 * 128 * 8;
     static constexpr int kBarsAt = kQScaleAt + 128 * 4;
     static constexpr int kSmem = kBarsAt + 256 + 1024;           // and alignment
@@ -179,7 +179,10 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
     using S = PrefixShape<D>;
     constexpr uint32_t kBarrier = kValues ? 4 : 2;
     uint64_t* full = kValues ? bars + 3 : bars + 1;
-    uint64_t* free = kValues ? bars + 9 : bars + 7;   // values: O done; keys: scores and factors read
+    // A stage is free when the product that reads it is done.  The factors
+    // are read later, but are four deep: the scores of tile j come after the
+    // weights of tile j - 2.
+    uint64_t* free = kValues ? bars + 9 : bars + 5;
     float* factors = reinterpret_cast<float*>(smem + S::kFactorsAt);
     int64_t* cache_rows = reinterpret_cast<int64_t*>(smem + S::kRowsAt) + (kValues ? 2 * 128 : 0);
     uint8_t* operand = smem + (kValues ? S::kVAt : S::kKAt);
@@ -192,6 +195,9 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
     const uint32_t dst0 = smem_addr(operand) + token0 * 128 + ((2 * (i & 3)) ^ swz) * 16;
     const uint32_t dst1 = smem_addr(operand) + token0 * 128 + ((2 * (i & 3) + 1) ^ swz) * 16;
     const int in_page = (1 << a.page_shift) - 1;
+    // Order of the factors: a softmax thread's columns 2c and 2c + 1 of two
+    // groups of 8 lie side by side, one load of 16 bytes.
+    const int factor_at = (i & ~15) + ((i >> 1) & 3) * 4 + ((i >> 3) & 1) * 2 + (i & 1);
     const uint8_t* codes = (kValues ? a.v : a.k) + (i & 3) * 16;
     // Page of token i of tile j (kNoToken past the end); its cache row is
     // formed later, so that nothing waits for the load.
@@ -259,14 +265,15 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
                 st_shared_v4(dst1 + at, h[4], h[5], h[6], h[7]);
             }
             if constexpr (!kValues) {
-                float* f = factors + b * 3 * 128;
+                float* f = factors + (j & 3) * 3 * 128 + factor_at;
                 const float safe = sv < 0x1p-100f ? 0x1p-100f : sv;
-                f[i] = sk;
-                f[128 + i] = sv == -1.0f ? -INFINITY : __log2f(safe);
-                f[256 + i] = sv == -1.0f ? 0.0f : rcp(safe);
+                f[0] = sk;
+                f[128] = sv == -1.0f ? -INFINITY : __log2f(safe);
+                f[256] = sv == -1.0f ? 0.0f : rcp(safe);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&full[b]);
+            __syncwarp();
+            if ((i & 31) == 0) mbar_arrive(&full[b]);
             if (j + 1 < tiles) {
                 fetch(j + 1);
                 load_scales(row1, &sk, &sv);
@@ -292,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     float* qscale = reinterpret_cast<float*>(smem + S::kQScaleAt);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBarsAt);
     uint64_t* q_full = bars;          // 128 arrivals
-    uint64_t* k_full = bars + 1;      // [2], 128
-    uint64_t* v_full = bars + 3;      // [2], 128
+    uint64_t* k_full = bars + 1;      // [2], a warp
+    uint64_t* v_full = bars + 3;      // [2], a warp
     uint64_t* s_full = bars + 5;      // [2], commit
-    uint64_t* w_full = bars + 7;      // [2], 128: weights in place, scores and factors read
+    uint64_t* w_full = bars + 7;      // [2], a warp: weights in place
     uint64_t* o_done = bars + 9;      // [2], commit
     uint64_t* drain = bars + 11;      // commit
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
@@ -305,10 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     if (threadIdx.x == 0) {
         mbar_init(q_full, 128);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&k_full[b], 128);
-            mbar_init(&v_full[b], 128);
+            mbar_init(&k_full[b], 4);
+            mbar_init(&v_full[b], 4);
             mbar_init(&s_full[b], 1);
-            mbar_init(&w_full[b], 128);
+            mbar_init(&w_full[b], 4);
             mbar_init(&o_done[b], 1);
         }
         mbar_init(drain, 1);
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             ok = *ctl.abort_flag == 0 && wait_soon(&k_full[b], parity, ctl) && wait_soon(&s_full[b], parity, ctl);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after_sync();
-            const float* f = factors + b * 3 * 128 + 2 * c;
+            const float* f = factors + (j & 3) * 3 * 128 + 4 * c;
             // 16 rows at a time, in one pass against the reference as it
             // stands; only where a row's maximum has outgrown it (the first
             // tiles) the reference moves and the pass is made again.
@@ -414,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                     part[0] = part[1] = 0ull;
                     top[0] = top[1] = -INFINITY;
                     uint32_t s[2][16];
+                    ulonglong2 sk2, lg2, rs2;   // factors of two groups of 8 columns
                     tmem_load_frag4(half + 128 * b, s[0]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -424,10 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                         if (k < 3) tmem_load_frag4(half + 128 * b + 32 * (k + 1), s[(k + 1) & 1]);
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            const int col = 32 * k + 8 * n;
-                            const f32x2 sk = *reinterpret_cast<const f32x2*>(f + col);
-                            const f32x2 lg = *reinterpret_cast<const f32x2*>(f + 128 + col);
-                            const f32x2 rs = *reinterpret_cast<const f32x2*>(f + 256 + col);
+                            if ((n & 1) == 0) {
+                                const int at = 32 * k + 8 * n;
+                                sk2 = *reinterpret_cast<const ulonglong2*>(f + at);
+                                lg2 = *reinterpret_cast<const ulonglong2*>(f + 128 + at);
+                                rs2 = *reinterpret_cast<const ulonglong2*>(f + 256 + at);
+                            }
+                            const f32x2 sk = n & 1 ? sk2.y : sk2.x, lg = n & 1 ? lg2.y : lg2.x,
+                                        rs = n & 1 ? rs2.y : rs2.x;
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const f32x2 sc = pack(__uint_as_float(v[4 * n + 2 * i]),
@@ -483,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             }
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&w_full[b]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_full[b]);
         }
         // ---- both streams' results, joined by the first group
         if (ok && tiles > b) {
@@ -615,23 +628,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                         mma_f16(d, q_desc + h * kColumn + 2 * x, kd + h * kColumn + 2 * x, kScoreDesc, h > 0 || x > 0);
                 mma_commit(&s_full[j & 1]);
             };
-            bool ok = wait_soon(q_full, 0, ctl) && wait_soon(&k_full[0], 0, ctl);
+            bool ok = wait_soon(q_full, 0, ctl);
             bool issued = false;
-            if (ok) {
+            for (int j = 0; j < 2 && j < tiles && ok; ++j) {
+                ok = wait_soon(&k_full[j], 0, ctl);
+                if (!ok) break;
                 tc_fence_after_sync();
                 issued = true;
-                scores(0);
+                scores(j);
             }
             for (int j = 0; j < tiles && ok; ++j) {
                 const int b = j & 1;
-                if (j + 1 < tiles) {
-                    // the buffer of tile j + 1's scores holds the weights of tile j - 1
-                    ok = wait_soon(&k_full[b ^ 1], ((j + 1) >> 1) & 1, ctl) &&
-                         (j == 0 || wait_soon(&o_done[b ^ 1], ((j - 1) >> 1) & 1, ctl));
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    scores(j + 1);
-                }
                 ok = wait_soon(&v_full[b], (j >> 1) & 1, ctl) && wait_soon(&w_full[b], (j >> 1) & 1, ctl);
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -641,6 +648,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                     mma_f16_ts(tmem + S::kOCol + D * b, tmem + 128 * b + 8 * x, vd + x * (2048 >> 4), kValueDesc,
                                j > 1 || x > 0);
                 mma_commit(&o_done[b]);
+                if (j + 2 < tiles) {
+                    // they take the place of the weights just read
+                    ok = wait_soon(&k_full[b], ((j + 2) >> 1) & 1, ctl) && wait_soon(&o_done[b], (j >> 1) & 1, ctl);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    scores(j + 2);
+                }
             }
             if (issued) {
                 // Tensor memory is freed below: wait for every MMA issued.
