@@ -239,7 +239,12 @@ struct AttnLaunch {
     uint32_t* status;
 };
 cudaError_t launch_attn_decode(const AttnLaunch& L, cudaStream_t s);
-// The prefix's states on tcgen05, into `states`; `slots` holds the shares'.
+// The prefix on tcgen05, in attn_prefix_splits() shares of its tokens: the
+// rows' states (m, l, 2 unused, D sums) per token and query head to `states`
+// when there is one share, else per key head, share, row tile of
+// kPrefixTileRows and row to `slots`.
+constexpr int kPrefixTileRows = 128;
+int attn_prefix_splits(int rows, int kv_heads, int64_t prefix_len, int sm_count);
 cudaError_t launch_attn_prefix(const AttnLaunch& L, float* slots, float* states, cudaStream_t s);
 bool attn_prefix_on_tensor_cores(int64_t rows, int head_dim);
 int64_t attn_prefix_slot_floats(int sm_count, int head_dim);

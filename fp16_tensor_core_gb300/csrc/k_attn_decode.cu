@@ -913,6 +913,35 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
     }
 }
 
+// The end of a call whose prefix was cut into shares on the tensor cores: a
+// row's shares, in token order, and the state of its own tokens (a.prefix;
+// addition is the same either way).  One warp a row.
+struct PrefixShares {
+    const float* slots;   // per share, row tile and row
+    int splits, row_tiles, tile_rows, rows;
+};
+template <int D, bool kFp16>
+__global__ void __launch_bounds__(128) attn_prefix_join_kernel(const AttnArgs a, const PrefixShares p) {
+    constexpr int kState = D + 4;
+    static_assert(D <= 128, "a lane holds 4 dims");
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int r = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5), h = blockIdx.y;
+    if (r >= p.rows) return;
+    const int rt = r / p.tile_rows;
+    const int64_t stride = static_cast<int64_t>(p.row_tiles) * p.tile_rows * kState;   // from share to share
+    const float* first = p.slots + ((static_cast<int64_t>(h) * p.splits * p.row_tiles + rt) * p.tile_rows +
+                                    (r - rt * p.tile_rows)) * kState;
+    float m, l;
+    float4 x;
+    join_states<D>(first, stride, p.splits, lane, &m, &l, &x);
+    int64_t token;
+    int head;
+    row_place(a, 0, h, r, &token, &head);
+    const RowEnd e = row_end<D>(a, token, head, m, l, lane == 0);
+    if (4 * lane < D) emit4<D, kFp16>(e, 4 * lane, x);
+}
+
 // Most blocks of a launch: the two that an SM holds.  (A block spends 10 us
 // on its start, its joins and its end, so more and smaller runs, handed to
 // the SMs that are done first, cost more than their evenness gains: 3 x
@@ -987,9 +1016,16 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.status = L.status;
     float* states = a.slots + attn_slot_floats(L.sm_count, D);
     const int64_t prefix_rows = static_cast<int64_t>(L.batch) * L.q_len * a.group;
-    if (L.prefix_len > 0 && attn_prefix_on_tensor_cores(prefix_rows, D)) {
-        float* prefix_slots = states + attn_state_floats(L.batch, L.q_len, L.q_heads, D);
-        const cudaError_t e = launch_attn_prefix(L, prefix_slots, states, s);
+    const bool on_tensor_cores = L.prefix_len > 0 && attn_prefix_on_tensor_cores(prefix_rows, D);
+    const int splits =
+        on_tensor_cores ? attn_prefix_splits(static_cast<int>(prefix_rows), a.kv_heads, L.prefix_len, L.sm_count) : 1;
+    // In shares, the prefix comes after the own tokens: its CTAs start while
+    // the last of those run, and the join of the shares is the call's end.
+    const bool prefix_last = splits > 1;
+    if (prefix_last) {
+        a.states = states;
+    } else if (on_tensor_cores) {
+        const cudaError_t e = launch_attn_prefix(L, nullptr, states, s);
         if (e != cudaSuccess) return e;
         a.prefix = states;
     } else if (L.prefix_len > 0) {
@@ -1013,7 +1049,20 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.q_len = L.q_len;
     a.rows = L.q_len * a.group;
     a.causal = true;
-    return run_split<D, kFp16>(a, L.sm_count, s);
+    const cudaError_t own = run_split<D, kFp16>(a, L.sm_count, s);
+    if (own != cudaSuccess || !prefix_last) return own;
+    if constexpr (D <= 128) {
+        float* shares = states + attn_state_floats(L.batch, L.q_len, L.q_heads, D);
+        const cudaError_t e = launch_attn_prefix(L, shares, nullptr, s);
+        if (e != cudaSuccess) return e;
+        a.prefix = states;
+        a.states = nullptr;
+        const int rows = static_cast<int>(prefix_rows);
+        const PrefixShares p{shares, splits, (rows + kPrefixTileRows - 1) / kPrefixTileRows, kPrefixTileRows, rows};
+        return launch_kernel(attn_prefix_join_kernel<D, kFp16>, dim3((rows + 3) / 4, a.kv_heads), dim3(128), 0, s,
+                             a, p);
+    }
+    return cudaSuccess;
 }
 
 }  // namespace

@@ -38,7 +38,7 @@ namespace dg {
 namespace {
 
 constexpr int kTileTokens = 128;
-constexpr int kTileRows = 128;
+constexpr int kTileRows = kPrefixTileRows;
 constexpr int kThreads = 640;   // warpgroups: softmax of even and of odd tiles, keys, values, MMA
 constexpr float kGrowth = 8.0f; // log2 of how far weights may pass 1
 
@@ -339,7 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     const int all_tiles = (a.len + kTileTokens - 1) / kTileTokens;
     const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / a.splits);
     const int tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / a.splits) - tile0;
-    pdl_wait();
+    // With several shares the own tokens' kernels ran before: they waited for
+    // all that this one reads, which may begin while they end.
+    if (a.splits == 1) pdl_wait();
 
     // Registers: 96 a thread at launch; the softmax warps take what the
     // others leave (144 + 144 + 72 + 72 + 40 <= 5 * 96).
@@ -503,7 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             const int last = tiles - 1 - ((tiles - 1 - b) & 1);
             ok = wait_soon(&o_done[b], (last >> 1) & 1, ctl);
         }
-        // Every MMA is done: the operands' memory is free.
+        // Every MMA is done: the operands' memory is free.  (And the kernel
+        // before this one: whoever waits for this one waits for both.)
+        pdl_wait();
         ok = named_bar_and(3, 256, ok);
         tc_fence_after_sync();
         float* other = reinterpret_cast<float*>(smem + S::kKAt);   // the second stream's states
@@ -672,37 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     }
 }
 
-// The states of a row's shares of the prefix, joined in token order: one warp
-// a row.
-template <int D>
-__global__ void __launch_bounds__(128) attn_prefix_join_kernel(const PrefixArgs a) {
-    constexpr int kState = D + 4;
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int r = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5), head = blockIdx.y;
-    if (r >= a.rows) return;
-    const int rt = r / kTileRows;
-    const int64_t stride = static_cast<int64_t>(a.row_tiles) * kTileRows * kState;   // from split to split
-    const float* first = a.slots + ((static_cast<int64_t>(head) * a.splits * a.row_tiles + rt) * kTileRows +
-                                    (r - rt * kTileRows)) * kState;
-    float m = -INFINITY, l = 0.0f;
-    float4 x = make_float4(0, 0, 0, 0);
-    join_states<D>(first, stride, a.splits, lane, &m, &l, &x);
-    const int token = r / a.group;
-    float* dst = a.states + (static_cast<int64_t>(token) * a.q_heads + head * a.group + r - token * a.group) * kState;
-    if (lane == 0) *reinterpret_cast<float2*>(dst) = make_float2(m, l);
-    if (4 * lane < D) *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = x;
-}
-
 template <int D, bool kFp16>
 cudaError_t run_prefix(const PrefixArgs& a, cudaStream_t s) {
     const cudaError_t set = allow_smem(attn_prefix_kernel<D, kFp16>, PrefixShape<D>::kSmem);
     if (set != cudaSuccess) return set;
     const unsigned blocks = static_cast<unsigned>(a.kv_heads) * a.splits * a.row_tiles;
-    const cudaError_t e = launch_kernel(attn_prefix_kernel<D, kFp16>, dim3(blocks), dim3(kThreads),
-                                        PrefixShape<D>::kSmem, s, a);
-    if (e != cudaSuccess || a.splits == 1) return e;
-    return launch_kernel(attn_prefix_join_kernel<D>, dim3((a.rows + 3) / 4, a.kv_heads), dim3(128), 0, s, a);
+    return launch_kernel(attn_prefix_kernel<D, kFp16>, dim3(blocks), dim3(kThreads), PrefixShape<D>::kSmem, s, a);
 }
 
 }  // namespace
