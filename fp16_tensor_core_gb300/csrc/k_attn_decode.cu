@@ -67,6 +67,7 @@ struct AttnArgs {
     int row_tiles;
     int q_heads;
     bool causal;
+    bool behind;               // started behind the kernel that leaves a.prefix, which ends later
     float scale_log2;          // softmax scale * log2(e)
     float* slots;              // two states of kRows rows per block
     int4* crossings;           // per block: the unit that goes on past it
@@ -307,7 +308,8 @@ attn_split_kernel(const AttnArgs a) {
     int* lens = reinterpret_cast<int*>(cum + a.batch + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    pdl_wait();
+    // A prefix's kernel reads nothing of the one before it but a.prefix.
+    if (!a.behind) pdl_wait();
     pdl_launch_dependents();
     const int units = a.kv_heads * a.row_tiles;
     Cursor unit;                // kWhole: this block's
@@ -735,6 +737,7 @@ attn_split_kernel(const AttnArgs a) {
                 fresh = true;
                 const int r0 = was.rt * kRows;
                 const bool whole = unit_end && first_tile == 0;
+                if (whole && a.behind) pdl_wait();
                 // first piece of the run when its unit began before it, else the last one
                 const bool is_head = !whole && first_tile != 0;
                 float* stash = is_head ? head_stash : tail_stash;
@@ -782,6 +785,7 @@ attn_split_kernel(const AttnArgs a) {
         cp_wait<0>();
     }
     __syncthreads();
+    if (a.behind) pdl_wait();
 
     // ---- join the pieces of each unit, in warp (token) order.  Lane p of
     // every warp looks at piece p; a unit's pieces are neighbours among those
@@ -1015,54 +1019,52 @@ cudaError_t run_attn(const AttnLaunch& L, cudaStream_t s) {
     a.slots = static_cast<float*>(L.scratch) + crossing_floats(L.sm_count);
     a.status = L.status;
     float* states = a.slots + attn_slot_floats(L.sm_count, D);
-    const int64_t prefix_rows = static_cast<int64_t>(L.batch) * L.q_len * a.group;
-    const bool on_tensor_cores = L.prefix_len > 0 && attn_prefix_on_tensor_cores(prefix_rows, D);
-    const int splits =
-        on_tensor_cores ? attn_prefix_splits(static_cast<int>(prefix_rows), a.kv_heads, L.prefix_len, L.sm_count) : 1;
-    // In shares, the prefix comes after the own tokens: its CTAs start while
-    // the last of those run, and the join of the shares is the call's end.
-    const bool prefix_last = splits > 1;
-    if (prefix_last) {
-        a.states = states;
-    } else if (on_tensor_cores) {
+    AttnArgs own = a;
+    own.page_table = L.page_table;
+    own.table_stride = L.table_stride;
+    own.max_len = static_cast<int>(L.max_len);
+    own.kv_lens = L.kv_lens;
+    own.batch = L.batch;
+    own.q_len = L.q_len;
+    own.rows = L.q_len * a.group;
+    own.causal = true;
+    if (L.prefix_len == 0) return run_split<D, kFp16>(own, L.sm_count, s);
+
+    // The rows' states over one part of their tokens go to scratch, the other
+    // part's kernel joins them with its own (addition is the same either
+    // way).  The own tokens come first where the prefix's kernel can start
+    // while their last blocks run: its first reads need nothing of theirs.
+    const int rows = L.batch * L.q_len * a.group;
+    const bool on_tensor_cores = attn_prefix_on_tensor_cores(rows, D);
+    const int splits = on_tensor_cores ? attn_prefix_splits(rows, a.kv_heads, L.prefix_len, L.sm_count) : 0;
+    if (splits == 1) {
         const cudaError_t e = launch_attn_prefix(L, nullptr, states, s);
         if (e != cudaSuccess) return e;
-        a.prefix = states;
-    } else if (L.prefix_len > 0) {
-        // The prefix as one request that every query row of the batch asks.
-        AttnArgs p = a;
-        p.page_table = L.prefix_pages;
-        p.max_len = static_cast<int>(L.prefix_len);
-        p.batch = 1;
-        p.q_len = L.batch * L.q_len;
-        p.rows = p.q_len * p.group;
-        p.states = states;
-        const cudaError_t e = run_split<D, kFp16>(p, L.sm_count, s);
-        if (e != cudaSuccess) return e;
-        a.prefix = states;
+        own.prefix = states;
+        return run_split<D, kFp16>(own, L.sm_count, s);
     }
-    a.page_table = L.page_table;
-    a.table_stride = L.table_stride;
-    a.max_len = static_cast<int>(L.max_len);
-    a.kv_lens = L.kv_lens;
-    a.batch = L.batch;
-    a.q_len = L.q_len;
-    a.rows = L.q_len * a.group;
-    a.causal = true;
-    const cudaError_t own = run_split<D, kFp16>(a, L.sm_count, s);
-    if (own != cudaSuccess || !prefix_last) return own;
+    own.states = states;
+    const cudaError_t e = run_split<D, kFp16>(own, L.sm_count, s);
+    if (e != cudaSuccess) return e;
+    a.prefix = states;
     if constexpr (D <= 128) {
-        float* shares = states + attn_state_floats(L.batch, L.q_len, L.q_heads, D);
-        const cudaError_t e = launch_attn_prefix(L, shares, nullptr, s);
-        if (e != cudaSuccess) return e;
-        a.prefix = states;
-        a.states = nullptr;
-        const int rows = static_cast<int>(prefix_rows);
-        const PrefixShares p{shares, splits, (rows + kPrefixTileRows - 1) / kPrefixTileRows, kPrefixTileRows, rows};
-        return launch_kernel(attn_prefix_join_kernel<D, kFp16>, dim3((rows + 3) / 4, a.kv_heads), dim3(128), 0, s,
-                             a, p);
+        if (on_tensor_cores) {
+            float* shares = states + attn_state_floats(L.batch, L.q_len, L.q_heads, D);
+            const cudaError_t k = launch_attn_prefix(L, shares, nullptr, s);
+            if (k != cudaSuccess) return k;
+            const PrefixShares p{shares, splits, (rows + kPrefixTileRows - 1) / kPrefixTileRows, kPrefixTileRows, rows};
+            return launch_kernel(attn_prefix_join_kernel<D, kFp16>, dim3((rows + 3) / 4, a.kv_heads), dim3(128), 0, s,
+                                 a, p);
+        }
     }
-    return cudaSuccess;
+    // The prefix as one request that every query row of the batch asks.
+    a.page_table = L.prefix_pages;
+    a.max_len = static_cast<int>(L.prefix_len);
+    a.batch = 1;
+    a.q_len = L.batch * L.q_len;
+    a.rows = rows;
+    a.behind = true;
+    return run_split<D, kFp16>(a, L.sm_count, s);
 }
 
 }  // namespace
