@@ -467,9 +467,10 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  *   page_table  int32, device: row b, at b * table_stride, names the pages of
  *               request b's tokens in order; max_pages entries a row.
  *   kv_lens     int32[batch], device, 0 .. max_pages * page_size each.  A
- *               length outside that counts as 0, a page outside the cache as
- *               a page of zeros (no access leaves the cache), and
- *               dg_sync_status reports DG_ERR_INVALID_VALUE.
+ *               length outside that counts as 0; queries that see a token
+ *               on a page outside the cache get unspecified results (no
+ *               access leaves the cache).  dg_sync_status reports
+ *               DG_ERR_INVALID_VALUE for both.
  *   prefix_pages  int32[ceil(prefix_len / page_size)], device; NULL with
  *               prefix_len 0.
  *   scale       finite, typically 1 / sqrt(head_dim).
