@@ -78,24 +78,41 @@ const Knobs& knobs();
 // Whether launches use programmatic dependent launch (knobs().pdl).
 inline bool pdl_enabled() { return knobs().pdl; }
 
-// Launches `kern` on `s`, with programmatic stream serialization when
-// pdl_enabled(): the kernel may be scheduled while the preceding kernel in
-// the stream drains, and waits (pdl_wait) before touching global memory.
+// Launches `kern` on `s` in clusters of `ranks` blocks, with programmatic
+// stream serialization when pdl_enabled(): the kernel may be scheduled while
+// the preceding kernel in the stream drains, and waits (pdl_wait) before
+// touching global memory.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t s, Args&&... args) {
+cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, int ranks, size_t smem,
+                            cudaStream_t s, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (pdl_enabled()) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (ranks > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    cfg.numAttrs = n;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The same without clusters.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t s, Args&&... args) {
+    return launch_clusters(kern, grid, block, 1, smem, s, static_cast<Args&&>(args)...);
 }
 
 // Raises a kernel's dynamic shared memory limit to `bytes`, once per kernel

@@ -65,6 +65,7 @@ struct AttnArgs {
     int group;                 // query heads per key head
     int rows;                  // q_len * group
     int row_tiles;
+    int ranks_log2;            // of the blocks (a cluster) that share a unit, where units are taken whole
     int q_heads;
     bool causal;
     bool behind;               // started behind the kernel that leaves a.prefix, which ends later
@@ -75,6 +76,21 @@ struct AttnArgs {
     float* states;             // where this call leaves states instead of outputs, or null
     uint32_t* status;
 };
+
+constexpr int kMaxRanks = 8;   // blocks of a cluster
+
+// Reads of another block's shared memory (addresses of map_to_rank).
+__device__ __forceinline__ float2 load_peer2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
@@ -293,8 +309,9 @@ __device__ __forceinline__ int find_request(const uint32_t* cum, int batch, int6
     return lo;
 }
 
-// kWhole: every block takes one whole unit instead (its warps equal runs of
-// the unit's tiles): nothing to search for, no unit that crosses blocks.
+// kWhole: every block, or cluster of blocks, takes one whole unit
+// instead (its warps equal runs of the unit's tiles): nothing to search for,
+// and the blocks' pieces meet in shared memory, without another launch.
 template <int D, int NT, bool kFp16, bool kWhole>
 __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kPerSm)
 attn_split_kernel(const AttnArgs a) {
@@ -314,13 +331,20 @@ attn_split_kernel(const AttnArgs a) {
     const int units = a.kv_heads * a.row_tiles;
     Cursor unit;                // kWhole: this block's
     int64_t run, block0, block1, f0, f1;   // room, or the unit's tiles
+    int rank = 0;               // kWhole: this block's in its cluster
     if constexpr (kWhole) {
-        unit.b = static_cast<int>(blockIdx.x) / units;
-        const int u = static_cast<int>(blockIdx.x) - unit.b * units;
+        int u = static_cast<int>(blockIdx.x);
+        rank = u & ((1 << a.ranks_log2) - 1);
+        u >>= a.ranks_log2;
+        unit.b = u / units;
+        u -= unit.b * units;
         unit.h = a.row_tiles == 1 ? u : u / a.row_tiles;
         unit.rt = u - unit.h * a.row_tiles;
         unit.len = request_len(a, unit.b);
         unit.ntile = (unit.len + kTile - 1) / kTile;
+        // One tile has one warp's row ends, none at all is written here: by
+        // the first block alone.
+        if (unit.ntile <= 1 && rank > 0) return;
         if (unit.ntile == 0) {
             const int r0 = unit.rt * kRows;
             for (int i = threadIdx.x; i < min(kRows, a.rows - r0) * (D / 4); i += kThreads) {
@@ -332,10 +356,10 @@ attn_split_kernel(const AttnArgs a) {
             }
             return;
         }
-        run = (unit.ntile + kWarps - 1) / kWarps;
-        block0 = 0;
-        block1 = unit.ntile;
-        f0 = min(block1, warp * run);
+        run = ((unit.ntile + kWarps - 1) / kWarps + (1 << a.ranks_log2) - 1) >> a.ranks_log2;
+        block0 = min(static_cast<int64_t>(unit.ntile), rank * kWarps * run);
+        block1 = min(static_cast<int64_t>(unit.ntile), block0 + kWarps * run);
+        f0 = min(block1, block0 + warp * run);
         f1 = min(block1, f0 + run);
     } else {
         scan_tiles<kThreads>(a, cum, lens, warp_sum);
@@ -862,7 +886,10 @@ attn_split_kernel(const AttnArgs a) {
                 }
             }
             RowEnd e;
-            if (to == 2) {
+            if (kWhole && a.ranks_log2 > 0) {   // over the row of the first piece: its readers are these lanes
+                e.state = reinterpret_cast<float*>(smem + (p == 1 ? 0 : kWarps * S::kRingBytes)) + r * S::kState;
+                if (lane == 0) *reinterpret_cast<float2*>(e.state) = make_float2(m, l);
+            } else if (to == 2) {
                 int64_t token;
                 int head;
                 row_place(a, b, h, r0 + r, &token, &head);
@@ -877,6 +904,58 @@ attn_split_kernel(const AttnArgs a) {
             }
         }
         turn += rows;
+    }
+    if constexpr (kWhole) {
+        if (a.ranks_log2 == 0 || unit.ntile <= 1) return;
+        // ---- join the blocks' states in token order.  A block's first piece
+        // is its first warp's: the tail of the unit's first run (over the
+        // ring) in the first block, a head in the others.
+        cluster_sync_all_diverged();
+        const int blocks = static_cast<int>((unit.ntile + kWarps * run - 1) / (kWarps * run));   // with tiles
+        const int r0 = unit.rt * kRows, rows = min(kRows, a.rows - r0);
+#pragma unroll 1
+        for (int r = rank * kWarps + warp; r < rows; r += kWarps << a.ranks_log2) {
+            auto state_of = [&](int q) {
+                return map_to_rank(smem + (q == 0 ? 0 : kWarps * S::kRingBytes) + r * S::kState * 4, q);
+            };
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (lane < blocks) ml = load_peer2(state_of(lane));
+            float m = ml.x;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            m = __shfl_sync(0xFFFFFFFFu, m, 0);
+            const float w = ex2(ml.x - (m == -INFINITY ? 0.0f : m));
+            float l = w * ml.y;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            l = __shfl_sync(0xFFFFFFFFu, l, 0);
+            float4 x[kParts], y[kMaxRanks][kParts];
+#pragma unroll
+            for (int q = 0; q < kMaxRanks; ++q)
+                if (q < blocks && (D >= 128 || 4 * lane < D)) {
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) y[q][k] = load_peer4(state_of(q) + 16 + 16 * (lane + 32 * k));
+                }
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) x[k] = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < kMaxRanks; ++q) {
+                const float wq = __shfl_sync(0xFFFFFFFFu, w, q);
+                if (q < blocks && (D >= 128 || 4 * lane < D)) {
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) x[k] = plus_scaled(x[k], wq, y[q][k]);
+                }
+            }
+            int64_t token;
+            int head;
+            row_place(a, unit.b, unit.h, r0 + r, &token, &head);
+            const RowEnd e = row_end<D>(a, token, head, m, l, lane == 0);
+            if (D >= 128 || 4 * lane < D) {
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) emit4<D, kFp16>(e, 4 * lane + 128 * k, x[k]);
+            }
+        }
+        cluster_sync_all_diverged();   // until nobody reads this block's states
     }
 }
 
@@ -961,18 +1040,27 @@ cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     a.row_tiles = (a.rows + S::kRows - 1) / S::kRows;
     const dim3 threads(S::kWarps * 32);
     // Whole units while a unit is at most four tiles a warp, by the page
-    // table's width (the lengths are not known here).  Measured with 32/8
-    // heads of 128, us, whole units against equal runs: 1 x 300 tokens 6.5 /
-    // 10.5, 8 x 1000 10.2 / 12.0, 64 x 400 15.8 / 16.9, 64 x 1000 23.4 /
-    // 22.8, 8 x 2000 16.1 / 12.7; one launch less besides.
+    // table's width (the lengths are not known here), over clusters of as many
+    // blocks as fit the GPU at once, until most warps have a single tile.
+    // Measured with 32/8 heads of 128, us, whole units (blocks a cluster)
+    // against equal runs: 1 x 300 tokens 6.5 (1) / 10.6, 1 x 1000 7.2 (4) /
+    // 10.5, 1 x 8000 12.2 (8) / 14.5, 8 x 2000 11.3 (4) / 13.0, 16 x 2000
+    // 15.2 (2) / 16.2, 64 x 1000 23.8 (1) / 23.1, 64 x 2000 (8 tiles a warp)
+    // 36.2 (1) / 33.6.  Clusters past one wave lose: 64 x 400 16.4 (1), 29.6
+    // (2), 51.5 (4).
+    const int blocks = S::kPerSm * sm_count;
     const int64_t units = static_cast<int64_t>(a.batch) * a.kv_heads * a.row_tiles;
-    if (a.max_len <= 4 * S::kWarps * kTile && units <= INT_MAX) {
+    const int64_t tiles = (static_cast<int64_t>(a.max_len) + kTile - 1) / kTile;
+    int ranks = 1;
+    for (a.ranks_log2 = 0; ranks < kMaxRanks && 2 * tiles > 3 * ranks * S::kWarps && units * ranks * 2 <= blocks;
+         ++a.ranks_log2)
+        ranks *= 2;
+    if (tiles <= 4 * ranks * S::kWarps && units <= INT_MAX) {
         const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16, true>, S::kSmem);
         if (e != cudaSuccess) return e;
-        return launch_kernel(attn_split_kernel<D, NT, kFp16, true>, dim3(static_cast<unsigned>(units)), threads,
-                             S::kSmem, s, a);
+        return launch_clusters(attn_split_kernel<D, NT, kFp16, true>, dim3(static_cast<unsigned>(units * ranks)),
+                               threads, ranks, S::kSmem, s, a);
     }
-    const int blocks = S::kPerSm * sm_count;
     const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
     const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16, false>,
                                      S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));

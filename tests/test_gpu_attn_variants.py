@@ -159,3 +159,59 @@ def test_uneven_scores_in_a_prefix_of_many_rows(dim):
     v = torch.randn(1500, 1, dim, device="cuda")
     dg.dg_kv_append(k.half(), v.half(), torch.from_numpy(c.prefix_slots.astype(np.int32)).cuda(), c.cache)
     c.check(*c.run(), requests=[0, 17, 39])
+
+
+@pytest.mark.parametrize("dtype", [dg.DG_BF16, dg.DG_FP16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q_heads,kv_heads", [(1, 1), (6, 6), (8, 2), (20, 1), (32, 8)])
+def test_tables_for_equal_runs(q_heads, kv_heads, dim, dtype):
+    """Tables too wide for a cluster per request."""
+    c = wide(LENS, tokens=9000, q_heads=q_heads, kv_heads=kv_heads, dim=dim, dtype=dtype)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 40])
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(4, 4, 64), (8, 2, 128), (14, 2, 128), (6, 2, 256)])
+def test_equal_runs_of_uneven_requests(q_len, q_heads, kv_heads, dim):
+    c = wide([0, 1, 3, 2300, 33, 0, 64, 700], tokens=9000, q_len=q_len, q_heads=q_heads, kv_heads=kv_heads, dim=dim)
+    c.check(*c.run(), requests=[0, 1, 2, 4, 5, 6] if q_len == 40 else None)
+
+
+@pytest.mark.parametrize("batch", [1, 2, 5, 10, 20, 39, 77])
+@pytest.mark.parametrize("dim,q_heads", [(64, 4), (64, 60), (128, 8), (128, 40), (256, 4)])
+def test_clusters_of_every_size(batch, dim, q_heads):
+    """From a cluster of eight blocks per (request, key head) to one block;
+    requests shorter than the cluster's first block among them."""
+    lens = [(1500, 0, 1, 32, 33, 64, 65, 256, 257, 900)[i % 10] for i in range(batch)]
+    c = wide(lens, tokens=1600, q_heads=q_heads, kv_heads=4, dim=dim)
+    c.check(*c.run(), requests=sorted({0, batch // 2, batch - 1} | set(range(min(batch, 9)))))
+
+
+@pytest.mark.parametrize("tokens", [1600, 9000])
+def test_graph_of_back_to_back_calls(tokens):
+    """Calls that follow one another in a graph, each reading the last one's output."""
+    c = wide([1500, 40, 0, 700], tokens=tokens, q_heads=8, kv_heads=2, dim=128)
+    outs = [torch.zeros_like(c.q) for _ in range(4)]
+
+    def chain():
+        q = c.q
+        for o in outs:
+            c.run(q=q, out=o)
+            q = o
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain()
+    s.synchronize()
+    want = [o.clone() for o in outs]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        chain()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
