@@ -9,6 +9,7 @@ if ``_build/libdg.so`` has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -50,6 +51,7 @@ EXPORTED_SYMBOLS = (
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libdg.so")
+_NATIVE_PATH = os.path.join(_HERE, "_build", "dg_python.so")
 _lib = None
 _lock = threading.Lock()
 
@@ -333,25 +335,29 @@ def dg_convert_f16_amax_pair(a, b, out_a, out_b, factor, amax_a, amax_b, stream=
                                           _stream(stream)), "dg_convert_f16_amax_pair")
 
 
-_HALF_TYPES = {torch.bfloat16: DG_BF16, torch.float16: DG_FP16}
+# The serving calls' arguments are read natively: see csrc/dg_python.c.
+_native = None
 
 
-def _heads(t, what, like=None):
-    """[tokens, heads, head_dim] (any token and head stride) as a dg_heads."""
-    stride = t.stride()
-    if len(stride) != 3 or t.dtype not in _HALF_TYPES or (stride[2] != 1 and t.shape[2] > 1):
-        raise ValueError(f"{what} must be BF16 or FP16 [tokens, heads, head_dim] with contiguous heads")
-    if not t.is_cuda:
-        raise ValueError("tensor must be in CUDA device memory")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{what} must have the shape and type of its counterpart")
-    return _Heads(t.data_ptr(), stride[0], stride[1])
-
-
-def _int32(t, n, what):
-    if t.dtype is not torch.int32 or t.numel() != n:
-        raise ValueError(f"{what} must be int32 with {n} elements")
-    return _ptr(t)
+def _load_native():
+    global _native
+    L = lib()
+    with _lock:
+        if _native is None:
+            spec = importlib.util.spec_from_file_location("dg_python", _NATIVE_PATH)
+            if spec is None or not os.path.exists(_NATIVE_PATH):
+                raise RuntimeError(f"{_NATIVE_PATH} not found; build it with the library")
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            if _raw_stream is not None and _current_device is not None:
+                stream, device = _raw_stream, _current_device
+            else:
+                stream, device = lambda _: torch.cuda.current_stream().cuda_stream, int
+            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                          for f in (L.dg_rope, L.dg_kv_append, L.dg_kv_read, L.dg_attn_decode)),
+                        torch.bfloat16, torch.float16, torch.int32, torch.float32, stream, device, _check)
+            _native = module
+    return _native
 
 
 class DgRotary:
@@ -363,6 +369,7 @@ class DgRotary:
             raise ValueError("table must be FP32 [positions, rotary_dim / 2, 2]")
         self.table = table
         self.c = _Rotary(_ptr(table), table.shape[0], 2 * table.shape[1], int(layout))
+        self.address = ctypes.addressof(self.c)
 
 
 class DgKvCache:
@@ -380,6 +387,7 @@ class DgKvCache:
         pages, self.kv_heads, page_size, self.head_dim = k.shape
         self.c = _KvCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, self.kv_heads,
                           page_size, self.head_dim)
+        self.address = ctypes.addressof(self.c)
 
 
 def dg_rope_table(table, base=10000.0, scaling=DG_ROPE_UNSCALED, factor=1.0,
@@ -396,45 +404,20 @@ def dg_rope_table(table, base=10000.0, scaling=DG_ROPE_UNSCALED, factor=1.0,
 
 def dg_rope(x, out, positions, rotary, inverse=False, stream=None) -> None:
     """out = x with each head's first rotary_dim elements turned (inverse: back)."""
-    hx, ho = _heads(x, "x"), _heads(out, "out", x)
-    tokens, heads, dim = x.shape
-    _check(lib().dg_rope(hx, ho, tokens, heads, dim, _int32(positions, tokens, "positions"), rotary.c,
-                         1 if inverse else 0, _HALF_TYPES[x.dtype], _stream(stream)), "dg_rope")
+    (_native or _load_native()).rope(x, out, positions, rotary, inverse, stream)
 
 
 def dg_kv_append(k, v, slots, cache, positions=None, rotary=None, q=None, q_out=None,
                  stream=None) -> None:
     """Turn (with rotary) and quantise k, v [tokens, kv_heads, head_dim] into the
     cache's slots; q is turned into q_out in the same launch."""
-    hk, hv = _heads(k, "k"), _heads(v, "v", k)
-    n, heads, dim = k.shape
-    if heads != cache.kv_heads or dim != cache.head_dim:
-        raise ValueError("k and v must have the cache's heads and head_dim")
-    hq = ho = None
-    q_heads = 0
-    if q is not None:
-        hq, ho = _heads(q, "q"), _heads(q_out, "q_out", q)
-        q_tokens, q_heads, q_dim = q.shape
-        if q_tokens != n or q_dim != dim or q.dtype != k.dtype:
-            raise ValueError("q must have the tokens, head_dim and type of k")
-    _check(lib().dg_kv_append(hq, ho, q_heads, hk, hv, n,
-                              None if positions is None else _int32(positions, n, "positions"),
-                              None if rotary is None else rotary.c, _int32(slots, n, "slots"),
-                              cache.c, _HALF_TYPES[k.dtype], _stream(stream)), "dg_kv_append")
+    (_native or _load_native()).kv_append(k, v, slots, cache, positions, rotary, q, q_out, stream)
 
 
 def dg_kv_read(cache, slots, k=None, v=None, stream=None) -> None:
     """k[t], v[t] = the cached key and value of slots[t] (code times scale)."""
-    some = k if k is not None else v
-    if some is None:
-        return
-    hk = None if k is None else _heads(k, "k")
-    hv = None if v is None else _heads(v, "v", k)
-    n, heads, dim = some.shape
-    if heads != cache.kv_heads or dim != cache.head_dim:
-        raise ValueError("k and v must have the cache's heads and head_dim")
-    _check(lib().dg_kv_read(cache.c, _int32(slots, n, "slots"), n, hk, hv,
-                            _HALF_TYPES[some.dtype], _stream(stream)), "dg_kv_read")
+    if k is not None or v is not None:
+        (_native or _load_native()).kv_read(cache, slots, k, v, stream)
 
 
 def dg_attn_decode_scratch(batch, q_len, q_heads, cache, prefix_len=0, sm_count=0) -> int:
@@ -450,25 +433,8 @@ def dg_attn_decode(q, out, cache, page_table, kv_lens, scratch, scale=None, lse=
     """Attention of q [batch * q_len, q_heads, head_dim] over the cache: own
     tokens by page_table [batch, max_pages] and kv_lens [batch], after a prefix
     that the whole batch shares (prefix_pages, prefix_len)."""
-    hq, ho = _heads(q, "q"), _heads(out, "out", q)
-    tokens, heads, dim = q.shape
-    batch, max_pages = page_table.shape
-    pitch, step = page_table.stride()
-    if dim != cache.head_dim or page_table.dtype is not torch.int32 or not page_table.is_cuda or \
-            (max_pages > 1 and step != 1):
-        raise ValueError("q must have the cache's head_dim, page_table must be int32 with contiguous rows")
-    if tokens % batch if batch else tokens:
-        raise ValueError("q must have the same number of tokens for each request")
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != tokens * heads):
-        raise ValueError("lse must be FP32 with one element per token and head")
-    if prefix_len and prefix_pages.numel() < -(-prefix_len // cache.c.page_size):
-        raise ValueError("prefix_pages must name every page of the prefix")
-    _check(lib().dg_attn_decode(
-        hq, ho, _ptr(lse), batch, tokens // batch if batch else 1, heads, cache.c, page_table.data_ptr(),
-        max(pitch, max_pages), max_pages, _int32(kv_lens, batch, "kv_lens"),
-        _int32(prefix_pages, prefix_pages.numel(), "prefix_pages") if prefix_len else None,
-        prefix_len, dim ** -0.5 if scale is None else scale, _HALF_TYPES[q.dtype], _ptr(scratch),
-        scratch.nbytes, _stream(stream)), "dg_attn_decode")
+    (_native or _load_native()).attn_decode(q, out, cache, page_table, kv_lens, scratch, scale, lse,
+                                            prefix_pages, prefix_len, stream)
 
 
 def dg_gemm_plan(M, N, K, in_dtype=DG_E4M3, out_dtype=DG_BF16, sm_count=0) -> dict:

@@ -10,6 +10,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdg.so")
+NATIVE = os.path.join(OUT_DIR, "dg_python.so")   # argument marshalling for Python
 
 SOURCES = ["dg_api.cu", "k_scale.cu", "k_gemv.cu", "k_gemv_mma.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu",
            "k_gemm_skinny.cu", "dg_static.cu", "k_kvcache.cu", "k_attn_decode.cu",
@@ -64,9 +66,25 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _build_native(force: bool) -> None:
+    src = os.path.join(CSRC, "dg_python.c")
+    deps = (src, os.path.join(INCLUDE, "dg.h"), __file__)
+    if not force and os.path.exists(NATIVE) and all(
+            os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps):
+        return
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], src,
+           "-o", tmp, "-lm"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for dg_python.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile the CUDA sources and link libdg.so; return the library path."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    _build_native(force)
     if force:
         for s in SOURCES:
             o = os.path.join(OUT_DIR, os.path.splitext(s)[0] + ".o")

@@ -1,0 +1,71 @@
+"""What the Python serving calls refuse before anything reaches the library.
+CPU only: the tensors' shapes and types are looked at first, then that they
+are on a device."""
+import pytest
+import torch
+
+import fp16_tensor_core_gb300 as dg
+from fp16_tensor_core_gb300 import build as dg_build
+
+BF, I32 = torch.bfloat16, torch.int32
+
+
+class Handle:
+    """A cache or rotary handle as the calls see it, over host memory."""
+
+    def __init__(self, c):
+        import ctypes
+        self.c, self.address = c, ctypes.addressof(c)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    dg_build.build()
+
+
+def heads(tokens=3, n=4, dim=64, dtype=BF):
+    return torch.zeros(tokens, n, dim, dtype=dtype)
+
+
+CACHE = Handle(dg._KvCache(0, 0, 0, 0, 10, 2, 16, 64))
+ROTARY = Handle(dg._Rotary(0, 100, 64, 0))
+SHAPE = r"x must be BF16 or FP16 \[tokens, heads, head_dim\] with contiguous heads"
+
+
+@pytest.mark.parametrize("x,match", [
+    (heads(dtype=torch.float32), SHAPE), (torch.zeros(3, 64, dtype=BF), SHAPE),
+    (torch.zeros(2, 3, 4, 64, dtype=BF), SHAPE), (heads(dim=128)[..., ::2], SHAPE),
+    (heads(), "CUDA device memory"), (heads(dtype=torch.float16), "CUDA device memory"),
+])
+def test_heads(x, match):
+    with pytest.raises(ValueError, match=match):
+        dg.dg_rope(x, x, torch.zeros(3, dtype=I32), ROTARY)
+
+
+def test_what_is_no_tensor():
+    with pytest.raises(AttributeError):
+        dg.dg_rope(None, None, None, ROTARY)
+    with pytest.raises(AttributeError):
+        dg.dg_kv_read(CACHE, torch.zeros(3, dtype=I32), k=[1.0])
+    with pytest.raises(AttributeError):
+        dg.dg_kv_append("k", "v", "slots", CACHE)
+    with pytest.raises((AttributeError, ValueError)):
+        dg.dg_attn_decode(1, 2, 3, 4, 5, 6)
+
+
+def test_calls_with_host_tensors():
+    k, slots = heads(n=2), torch.zeros(3, dtype=I32)
+    for call in (lambda: dg.dg_kv_append(k, k, slots, CACHE), lambda: dg.dg_kv_read(CACHE, slots, v=k),
+                 lambda: dg.dg_attn_decode(k, k, CACHE, slots[:, None], slots, slots)):
+        with pytest.raises(ValueError, match="CUDA device memory"):
+            call()
+    assert dg.dg_kv_read(CACHE, slots) is None
+
+
+def test_the_native_functions_count_their_arguments():
+    native = dg._load_native()
+    for f in (native.rope, native.kv_append, native.kv_read, native.attn_decode, native.bind):
+        with pytest.raises(TypeError, match="arguments wanted"):
+            f()
+        with pytest.raises(TypeError, match="arguments wanted"):
+            f(*range(20))
