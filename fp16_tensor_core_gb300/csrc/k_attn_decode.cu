@@ -442,15 +442,20 @@ attn_split_kernel(const AttnArgs a) {
         const int in_page = (1 << a.page_shift) - 1;
         constexpr int kPerRow = D / 16, kPerStep = 32 / kPerRow;   // 16-byte copies of a row; rows a step
         const int chunk = lane % kPerRow, row_in = lane / kPerRow;
+        // The page is asked for when the tile's turn comes up and first looked
+        // at when its keys are loaded, a product later.
+        int page = -1;
         int64_t token_row = -1;   // its row in the cache, or -1
+        auto find_page = [&]() {
+            const int t = in.tile * kTile + lane;
+            page = t < in.len ? a.page_table[in.b * a.table_stride + (t >> a.page_shift)] : -1;
+        };
         auto find_row = [&]() {
             const int t = in.tile * kTile + lane;
             token_row = -1;
-            if (t >= in.len) return;
-            const int p = a.page_table[in.b * a.table_stride + (t >> a.page_shift)];
-            if (p >= 0 && p < a.pages) {
-                token_row = ((static_cast<int64_t>(p) * a.kv_heads + in.h) << a.page_shift) + (t & in_page);
-            } else {
+            if (page >= 0 && page < a.pages) {
+                token_row = ((static_cast<int64_t>(page) * a.kv_heads + in.h) << a.page_shift) + (t & in_page);
+            } else if (t < in.len) {
                 atomicOr(a.status, kStatusBadArgument);
             }
         };
@@ -474,6 +479,7 @@ attn_split_kernel(const AttnArgs a) {
             }
         };
         auto load_keys = [&](int stage) {   // and both scales
+            find_row();
             load_codes(a.k, ring + stage * S::kTileBytes);
             const uint32_t sc = ring + S::kScaleAt + stage * (2 * kTile * 4) + lane * 4;
             const int64_t r = max(token_row, static_cast<int64_t>(0));
@@ -561,7 +567,7 @@ attn_split_kernel(const AttnArgs a) {
         bool more = running;   // `in` is a tile of this run
         {
             uint4 w[NT][D / 32];
-            if (more) find_row();
+            if (more) find_page();
             if (running) load_queries(w);
 #pragma unroll 1
             for (int s = 0; s < kStages; ++s) {
@@ -570,7 +576,7 @@ attn_split_kernel(const AttnArgs a) {
                 if (more) {
                     load_values(s);
                     more = advance(in);
-                    if (more) find_row();
+                    if (more) find_page();
                 }
                 cp_commit();
             }
@@ -748,7 +754,7 @@ attn_split_kernel(const AttnArgs a) {
             if (more) {
                 load_values(stage);
                 more = advance(in);
-                if (more) find_row();
+                if (more) find_page();
             }
             cp_commit();
             stage = stage + 1 == kStages ? 0 : stage + 1;
