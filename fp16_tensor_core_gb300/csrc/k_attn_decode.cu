@@ -117,11 +117,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // lane % 4 == c holds dims c * kDims .. of each kSpan-wide part of the head
 // in the first product, one with lane / 4 == g dims g * kSpan / 8 .. in the
 // second.
-template <int D, int NT>
+template <int D, int NT, int W = D == 256 ? 4 : 8>
 struct Shape {
     static constexpr int kRows = 8 * NT;             // query rows per unit
-    static constexpr int kWarps = D == 256 ? 4 : 8;
-    static constexpr int kPerSm = D == 128 && NT == 2 ? 1 : 2;   // resident blocks (registers)
+    static constexpr int kWarps = W;                 // of a block
+    static constexpr int kPerSm = (D == 128 && NT == 2 ? 8 : D == 256 ? 8 : 16) / W;   // resident blocks (registers)
     static constexpr int kStages = D == 64 || (D == 128 && NT == 2) ? 2 : 1;
     static constexpr int kParts = D == 256 ? 2 : 1;
     static constexpr int kSpan = D / kParts;         // 64 or 128
@@ -312,10 +312,10 @@ __device__ __forceinline__ int find_request(const uint32_t* cum, int batch, int6
 // kWhole: every block, or cluster of blocks, takes one whole unit
 // instead (its warps equal runs of the unit's tiles): nothing to search for,
 // and the blocks' pieces meet in shared memory, without another launch.
-template <int D, int NT, bool kFp16, bool kWhole>
-__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kPerSm)
+template <int D, int NT, int W, bool kFp16, bool kWhole>
+__global__ void __launch_bounds__(W * 32, Shape<D, NT, W>::kPerSm)
 attn_split_kernel(const AttnArgs a) {
-    using S = Shape<D, NT>;
+    using S = Shape<D, NT, W>;
     constexpr int kWarps = S::kWarps, kThreads = kWarps * 32, kStages = S::kStages, kRows = S::kRows;
     constexpr int kParts = D > 128 ? 2 : 1;   // float4s of a row a lane
     extern __shared__ __align__(16) uint8_t smem[];
@@ -1040,6 +1040,16 @@ int attn_blocks(int sm_count) { return 2 * sm_count; }
 // The crossings' room in floats.
 int64_t crossing_floats(int sm_count) { return static_cast<int64_t>(attn_blocks(sm_count)) * 4; }
 
+// Whole units, one per cluster of 1 << a.ranks_log2 blocks of W warps.
+template <int D, int NT, int W, bool kFp16>
+cudaError_t run_whole(const AttnArgs& a, int64_t units, cudaStream_t s) {
+    const auto kernel = attn_split_kernel<D, NT, W, kFp16, true>;
+    const cudaError_t e = allow_smem(kernel, Shape<D, NT, W>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kernel, dim3(static_cast<unsigned>(units << a.ranks_log2)), dim3(W * 32), 1 << a.ranks_log2,
+                           Shape<D, NT, W>::kSmem, s, a);
+}
+
 template <int D, int NT, bool kFp16>
 cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     using S = Shape<D, NT>;
@@ -1049,10 +1059,10 @@ cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     // table's width (the lengths are not known here), over clusters of as many
     // blocks as fit the GPU at once, until most warps have a single tile.
     // Measured with 32/8 heads of 128, us, whole units (blocks a cluster)
-    // against equal runs: 1 x 300 tokens 6.5 (1) / 10.6, 1 x 1000 7.2 (4) /
-    // 10.5, 1 x 8000 12.2 (8) / 14.5, 8 x 2000 11.3 (4) / 13.0, 16 x 2000
-    // 15.2 (2) / 16.2, 64 x 1000 23.8 (1) / 23.1, 64 x 2000 (8 tiles a warp)
-    // 36.2 (1) / 33.6.  Clusters past one wave lose: 64 x 400 16.4 (1), 29.6
+    // against equal runs: 1 x 300 tokens 6.7 (1) / 10.6, 1 x 1000 7.0 (4) /
+    // 10.5, 1 x 8000 12.0 (8) / 14.5, 8 x 2000 11.3 (4) / 13.0, 16 x 2000
+    // 15.2 (2) / 16.2, 64 x 1000 21.8 (1) / 23.1, 64 x 2000 (8 tiles a warp)
+    // 36.2 (1) / 33.6.  Clusters past one wave lose: 64 x 400 16.5 (1), 29.6
     // (2), 51.5 (4).
     const int blocks = S::kPerSm * sm_count;
     const int64_t units = static_cast<int64_t>(a.batch) * a.kv_heads * a.row_tiles;
@@ -1062,16 +1072,19 @@ cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
          ++a.ranks_log2)
         ranks *= 2;
     if (tiles <= 4 * ranks * S::kWarps && units <= INT_MAX) {
-        const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16, true>, S::kSmem);
-        if (e != cudaSuccess) return e;
-        return launch_clusters(attn_split_kernel<D, NT, kFp16, true>, dim3(static_cast<unsigned>(units * ranks)),
-                               threads, ranks, S::kSmem, s, a);
+        // More units than blocks at once: half as many warps a block, twice as
+        // many blocks, whose starts and joins overlap (64 x 400 tokens 13.0
+        // against 16.5 us, 64 x 1000 21.8 / 23.8; but 8 x 1000 9.2 / 8.7).
+        if constexpr (S::kWarps == 8) {
+            if (units > blocks) return run_whole<D, NT, 4, kFp16>(a, units, s);
+        }
+        return run_whole<D, NT, S::kWarps, kFp16>(a, units, s);
     }
     const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
-    const cudaError_t e = allow_smem(attn_split_kernel<D, NT, kFp16, false>,
+    const cudaError_t e = allow_smem(attn_split_kernel<D, NT, S::kWarps, kFp16, false>,
                                      S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
     if (e != cudaSuccess) return e;
-    const cudaError_t k = launch_kernel(attn_split_kernel<D, NT, kFp16, false>, dim3(blocks), threads,
+    const cudaError_t k = launch_kernel(attn_split_kernel<D, NT, S::kWarps, kFp16, false>, dim3(blocks), threads,
                                         S::kSmem + cum, s, a);
     if (k != cudaSuccess) return k;
     return launch_kernel(attn_join_kernel<D, NT, kFp16>, dim3(blocks, (std::min(S::kRows, a.rows) + 3) / 4),
