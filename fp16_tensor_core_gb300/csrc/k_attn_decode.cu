@@ -1054,7 +1054,6 @@ template <int D, int NT, bool kFp16>
 cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
     using S = Shape<D, NT>;
     a.row_tiles = (a.rows + S::kRows - 1) / S::kRows;
-    const dim3 threads(S::kWarps * 32);
     // Whole units while a unit is at most four tiles a warp, by the page
     // table's width (the lengths are not known here), over clusters of as many
     // blocks as fit the GPU at once, until most warps have a single tile.
@@ -1080,14 +1079,19 @@ cudaError_t run_split_nt(AttnArgs a, int sm_count, cudaStream_t s) {
         }
         return run_whole<D, NT, S::kWarps, kFp16>(a, units, s);
     }
+    // Equal runs: 16 warps an SM, in two blocks, but 16-row units of 64-wide
+    // heads in one (24 x 5 x 2500 tokens of 16/4 heads 22.7 / 23.8 us, 2 x 8 x
+    // 30000 25.8 / 28.4; 8-row units 13.9 / 12.8 for 24 x 2500).
+    using F = Shape<D, NT, D == 64 && NT == 2 ? 16 : S::kWarps>;
+    const int run_blocks = F::kPerSm * sm_count;
     const size_t cum = sizeof(uint32_t) * (2 * a.batch + 1);
-    const cudaError_t e = allow_smem(attn_split_kernel<D, NT, S::kWarps, kFp16, false>,
-                                     S::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
+    const auto kernel = attn_split_kernel<D, NT, F::kWarps, kFp16, false>;
+    const cudaError_t e =
+        allow_smem(kernel, F::kSmem + static_cast<int>(sizeof(uint32_t)) * (2 * kAttnMaxBatch + 1));
     if (e != cudaSuccess) return e;
-    const cudaError_t k = launch_kernel(attn_split_kernel<D, NT, S::kWarps, kFp16, false>, dim3(blocks), threads,
-                                        S::kSmem + cum, s, a);
+    const cudaError_t k = launch_kernel(kernel, dim3(run_blocks), dim3(F::kWarps * 32), F::kSmem + cum, s, a);
     if (k != cudaSuccess) return k;
-    return launch_kernel(attn_join_kernel<D, NT, kFp16>, dim3(blocks, (std::min(S::kRows, a.rows) + 3) / 4),
+    return launch_kernel(attn_join_kernel<D, NT, kFp16>, dim3(run_blocks, (std::min(S::kRows, a.rows) + 3) / 4),
                          dim3(128), 0, s, a);
 }
 
