@@ -119,7 +119,9 @@ struct RopeArgs {
 // A thread owns one item (8 rotated pairs of the half layout, 4 of the
 // interleaved one, or 8 dims that are copied) of one token for kHeads heads:
 // its cosines and sines stay in registers across the heads, and both halves
-// of a pair are in its hands, so each element is read and written once.
+// of a pair are in its hands, so each element is read and written once:
+// 16385 tokens x 32 heads of 128, half of each turned, 43.8 us (6.2 TB/s, 0.92
+// of a copy).
 template <bool kFp16, bool kHalf, int kHeads>
 __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, int head_block) {
     const int local = static_cast<int>(threadIdx.x) / a.threads_per_token;
@@ -229,6 +231,13 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     return d;
 }
 
+// (a, b) * m, both products in one instruction.
+__device__ __forceinline__ void mul2(float a, float b, float m, float* x, float* y) {
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\t"
+        "mul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(*x), "=f"(*y) : "f"(a), "f"(b), "f"(m));
+}
+
 __device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
     uint32_t c[4];
 #pragma unroll
@@ -260,19 +269,21 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
     const float below = r * (1.0f - 0x1p-21f), above = r * (1.0f + 0x1p-21f);
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = x[i] * below;
+    for (int i = 0; i < 8; i += 2) mul2(x[i], x[i + 1], below, &q[i], &q[i + 1]);
     const uint2 lo = codes8(q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = x[i] * above;
+    for (int i = 0; i < 8; i += 2) mul2(x[i], x[i + 1], above, &q[i], &q[i + 1]);
     const uint2 hi = codes8(q);
     if (lo.x == hi.x && lo.y == hi.y) return lo;
     return divide8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale);
 }
 
 // A group of kLanes lanes owns one row (a key or value head) and walks over
-// kTokens tokens, 8 dims a lane: row and dims are fixed, so a token costs
-// little more than its loads.  A rotated lane also reads the 8 dims that its
-// own are paired with (the other lane's line, from L1).
+// kTokens tokens, 16 dims a lane: row and dims are fixed, so a token costs
+// little more than its loads, and what a row costs whatever its width (its
+// place, maximum and scale) is spread over few lanes.  A rotated lane of the
+// half layout owns 8 dims and the 8 they are paired with, so that nothing is
+// read twice.
 template <bool kFp16, bool kHalf, int kLanes, int kTokens>
 __device__ __forceinline__ void append_block(const AppendArgs& a, int block) {
     constexpr int kGroups = 256 / kLanes;
@@ -283,32 +294,33 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int block) {
     const int r = row_block * kGroups + (a.tokens_at_once > 1 ? group % rows : group);
     const int local = a.tokens_at_once > 1 ? group / rows : 0;
     const int64_t t0 = static_cast<int64_t>(token_block) * (a.tokens_at_once * kTokens) + local;
-    const int d = 8 * l;
     const bool is_k = r < kv_heads;
-    const bool live = d < a.dim && r < rows && local < a.tokens_at_once;
-    const bool turn = live && is_k && d < a.rot;
-    const int half = a.rot / 2;
-    const bool upper = kHalf && d >= half;
+    const bool live = 16 * l < a.dim && r < rows && local < a.tokens_at_once;
+    const bool turn = live && is_k && 16 * l < a.rot;
+    const bool apart = kHalf && turn;
+    const int d = apart ? 8 * l : 16 * l;                    // this lane's first 8 dims
+    const int d2 = apart ? a.rot / 2 + 8 * l : 16 * l + 8;   // and its others
     const int h = is_k ? r : r - kv_heads;
-    const uint16_t* src = is_k ? a.k + h * a.k_hs + d : a.v + h * a.v_hs + d;
+    const uint16_t* src = is_k ? a.k + h * a.k_hs : a.v + h * a.v_hs;
     const int64_t ts = is_k ? a.k_ts : a.v_ts;
-    const int to_pair = !kHalf ? 0 : upper ? -half : half;
     const int64_t nslots = a.cache.pages << a.page_shift;
 
-    uint4 own[kTokens], pair[kTokens];
+    uint4 own[kTokens][2];
     int slot[kTokens];
     int64_t pos[kTokens];
 #pragma unroll
     for (int j = 0; j < kTokens; ++j) {
         const int64_t t = t0 + j * a.tokens_at_once;
-        own[j] = pair[j] = make_uint4(0, 0, 0, 0);
+        own[j][0] = own[j][1] = make_uint4(0, 0, 0, 0);
         slot[j] = -1;
         pos[j] = 0;
         if (t < a.tokens) {
             slot[j] = a.slots[t];
             if (a.rot > 0) pos[j] = a.positions[t];
-            if (live) own[j] = *reinterpret_cast<const uint4*>(src + t * ts);
-            if (kHalf && turn) pair[j] = *reinterpret_cast<const uint4*>(src + t * ts + to_pair);
+            if (live) {
+                own[j][0] = *reinterpret_cast<const uint4*>(src + t * ts + d);
+                own[j][1] = *reinterpret_cast<const uint4*>(src + t * ts + d2);
+            }
         }
     }
 #pragma unroll
@@ -316,39 +328,39 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int block) {
         const bool bad = slot[j] >= nslots || pos[j] < 0 || (a.rot > 0 && pos[j] >= a.table_positions);
         if (bad && threadIdx.x % kLanes == 0) atomicOr(a.status, kStatusBadArgument);
         if (bad) slot[j] = -1;
-        float x[8];
-        unpack8<kFp16>(own[j], x);
+        float x[2][8];
+        unpack8<kFp16>(own[j][0], x[0]);
+        unpack8<kFp16>(own[j][1], x[1]);
         if (turn && slot[j] >= 0) {
-            float y[8], p[8];
             const float* row = a.table + pos[j] * a.rot;
             if constexpr (kHalf) {
-                unpack8<kFp16>(pair[j], p);
-                const int i0 = upper ? d - half : d;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + 2 * i0 + 4 * i));
-                    y[2 * i] = x[2 * i] * f.x + p[2 * i] * (upper ? f.y : -f.y);
-                    y[2 * i + 1] = x[2 * i + 1] * f.z + p[2 * i + 1] * (upper ? f.w : -f.w);
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + 2 * (d + i)));
+                    const float p0 = x[0][i], q0 = x[1][i], p1 = x[0][i + 1], q1 = x[1][i + 1];
+                    x[0][i] = p0 * f.x - q0 * f.y;
+                    x[1][i] = q0 * f.x + p0 * f.y;
+                    x[0][i + 1] = p1 * f.z - q1 * f.w;
+                    x[1][i + 1] = q1 * f.z + p1 * f.w;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + d + 4 * i));
-                    y[4 * i] = x[4 * i] * f.x - x[4 * i + 1] * f.y;
-                    y[4 * i + 1] = x[4 * i + 1] * f.x + x[4 * i] * f.y;
-                    y[4 * i + 2] = x[4 * i + 2] * f.z - x[4 * i + 3] * f.w;
-                    y[4 * i + 3] = x[4 * i + 3] * f.z + x[4 * i + 2] * f.w;
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + d + i));
+                    float* y = &x[i >> 3][i & 7];
+                    const float y0 = y[0], y2 = y[2];
+                    y[0] = y0 * f.x - y[1] * f.y;
+                    y[1] = y[1] * f.x + y0 * f.y;
+                    y[2] = y2 * f.z - y[3] * f.w;
+                    y[3] = y[3] * f.z + y2 * f.w;
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = y[i];
         }
         // The rotated key goes to its scale and code in FP32, not through a
         // 16-bit rounding.
-        float top = max3_abs(x[0], x[1], x[2]);
-        top = max3_abs(top, x[3], x[4]);
-        top = max3_abs(top, x[5], x[6]);
-        top = max3_abs(top, x[7], x[7]);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) top = max3_abs(top, x[i >> 3][i & 7], x[i >> 3][(i & 7) + 1]);
 #pragma unroll
         for (int w = kLanes / 2; w > 0; w >>= 1) {
             const float other = __shfl_xor_sync(0xFFFFFFFFu, top, w);
@@ -359,26 +371,40 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int block) {
         const int64_t row = ((page * kv_heads + h) << a.page_shift) + (slot[j] & ((1 << a.page_shift) - 1));
         const bool finite = top <= 3.4028235e38f;   // false for NaN
         const float scale = finite ? fmaxf(__fdiv_rn(top, 448.0f), kKvMinScale) : __int_as_float(0x7FC00000);
-        const uint2 packed = finite ? quantise8(x, scale) : make_uint2(0, 0);
-        *reinterpret_cast<uint2*>((is_k ? a.cache.k : a.cache.v) + row * a.dim + d) = packed;
+        const uint2 lo = finite ? quantise8(x[0], scale) : make_uint2(0, 0);
+        const uint2 hi = finite ? quantise8(x[1], scale) : make_uint2(0, 0);
+        uint8_t* dst = (is_k ? a.cache.k : a.cache.v) + row * a.dim;
+        if (apart) {
+            *reinterpret_cast<uint2*>(dst + d) = lo;
+            *reinterpret_cast<uint2*>(dst + d2) = hi;
+        } else {
+            *reinterpret_cast<uint4*>(dst + d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
         if (l == 0) (is_k ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
     }
 }
 
+constexpr int kAppendTokens = 2;   // of a lane group, in large calls
+
 // Every kv_every-th block writes the cache (bound by its instructions), the
 // others turn the queries (bound by HBM): dealt out among one another they
-// share the SMs.
-template <bool kFp16, bool kHalf, int kLanes, int kTokens>
-__global__ void __launch_bounds__(256)
+// share the SMs.  16001 tokens of 32 + 8 + 8 heads of 128, half of each
+// turned, interleaved: 63 us, 5.8 TB/s, 0.86 of a copy; whole heads in the
+// half layout 65; 32 + 32 + 32 heads 148 (0.67: two thirds of it are cache
+// rows).  With 8 dims a lane and 4 tokens in flight 72, 80 and 220.  Blocks
+// per SM by the registers of the four query heads a thread holds: the half
+// layout spills at 5 (68) and 6 (79).
+template <bool kFp16, bool kHalf, int kLanes, bool kMany>
+__global__ void __launch_bounds__(256, kMany ? (kHalf ? 4 : 6) : 6)
 kv_append_kernel(const AppendArgs a, const RopeArgs q, int kv_blocks, int kv_every) {
     pdl_wait();
     const int round = static_cast<int>(blockIdx.x) / kv_every;
     if (round < kv_blocks && static_cast<int>(blockIdx.x) - round * kv_every == kv_every - 1)
-        append_block<kFp16, kHalf, kLanes, kTokens>(a, round);
+        append_block<kFp16, kHalf, kLanes, kMany ? kAppendTokens : 1>(a, round);
     else {
         const int b = static_cast<int>(blockIdx.x) - min(round, kv_blocks);
         const int token_block = q.head_blocks == 1 ? b : b / q.head_blocks;
-        rope_block<kFp16, kHalf, kTokens>(q, token_block, b - token_block * q.head_blocks);
+        rope_block<kFp16, kHalf, kMany ? 4 : 1>(q, token_block, b - token_block * q.head_blocks);
     }
 }
 
@@ -401,7 +427,9 @@ struct ReadArgs {
 
 // A thread owns 8 dims of one row (a warp's stores are whole lines) and walks
 // over the tokens, kTokens at a time, the next ones' slots already on their
-// way: code x scale in FP32, rounded once to the output type.
+// way: code x scale in FP32, rounded once to the output type.  40001 tokens x
+// 8 heads of 128, keys and values: 41.9 us (5.9 TB/s, 0.88 of a copy); two
+// waves of blocks with half the walk 42.9, one pass a block 52.
 template <bool kFp16, int kTokens>
 __global__ void __launch_bounds__(256)
 kv_read_kernel(const ReadArgs a) {
@@ -478,14 +506,14 @@ cudaError_t rope_dispatch(const RopeArgs& a, int heads_per_thread, dim3 grid, cu
                : launch_kernel(rope_kernel<kFp16, kHalf, 1>, grid, dim3(256), 0, s, a);
 }
 
-template <bool kFp16, bool kHalf, int kTokens>
+template <bool kFp16, bool kHalf, bool kMany>
 cudaError_t append_dispatch(const AppendArgs& a, const RopeArgs& q, int64_t q_blocks, int64_t kv_blocks,
                             cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks)), block(256);
     const int kv = static_cast<int>(kv_blocks), every = static_cast<int>((q_blocks + kv_blocks) / kv_blocks);
-    if (a.dim <= 64) return launch_kernel(kv_append_kernel<kFp16, kHalf, 8, kTokens>, grid, block, 0, s, a, q, kv, every);
-    if (a.dim <= 128) return launch_kernel(kv_append_kernel<kFp16, kHalf, 16, kTokens>, grid, block, 0, s, a, q, kv, every);
-    return launch_kernel(kv_append_kernel<kFp16, kHalf, 32, kTokens>, grid, block, 0, s, a, q, kv, every);
+    if (a.dim <= 64) return launch_kernel(kv_append_kernel<kFp16, kHalf, 4, kMany>, grid, block, 0, s, a, q, kv, every);
+    if (a.dim <= 128) return launch_kernel(kv_append_kernel<kFp16, kHalf, 8, kMany>, grid, block, 0, s, a, q, kv, every);
+    return launch_kernel(kv_append_kernel<kFp16, kHalf, 16, kMany>, grid, block, 0, s, a, q, kv, every);
 }
 
 int shift_of(int page_size) {
@@ -586,15 +614,15 @@ cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_hea
     a.page_shift = shift_of(cache.page_size);
     a.status = status;
     const bool half = rot == nullptr || rot->layout == DG_ROPE_HALF;
-    const int lanes = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32;
+    const int lanes = a.dim <= 64 ? 4 : a.dim <= 128 ? 8 : 16;
     const int groups = 256 / lanes, rows = 2 * cache.kv_heads;
     a.row_blocks = (rows + groups - 1) / groups;
     a.tokens_at_once = a.row_blocks == 1 ? groups / rows : 1;
-    // Four tokens a lane group (and four query heads a thread) once that
-    // still leaves every SM two blocks of cache rows.
+    // Two tokens a lane group (and four query heads a thread) once that still
+    // leaves every SM four blocks of cache rows.
     const int64_t passes = (tokens + a.tokens_at_once - 1) / a.tokens_at_once;
     const bool few = passes * a.row_blocks < static_cast<int64_t>(4) * 2 * sm_count;
-    const int per_block = a.tokens_at_once * (few ? 1 : 4);
+    const int per_block = a.tokens_at_once * (few ? 1 : kAppendTokens);
     const int64_t kv_blocks = (tokens + per_block - 1) / per_block * a.row_blocks;
     RopeArgs qa{};
     int64_t q_blocks = 0;
@@ -607,16 +635,16 @@ cudaError_t launch_kv_append(const dg_heads* q, const dg_heads* q_out, int q_hea
     if (q_blocks + kv_blocks > INT_MAX) return cudaErrorInvalidValue;
     if (fp16) {
         if (half)
-            return few ? append_dispatch<true, true, 1>(a, qa, q_blocks, kv_blocks, s)
-                       : append_dispatch<true, true, 4>(a, qa, q_blocks, kv_blocks, s);
-        return few ? append_dispatch<true, false, 1>(a, qa, q_blocks, kv_blocks, s)
-                   : append_dispatch<true, false, 4>(a, qa, q_blocks, kv_blocks, s);
+            return few ? append_dispatch<true, true, false>(a, qa, q_blocks, kv_blocks, s)
+                       : append_dispatch<true, true, true>(a, qa, q_blocks, kv_blocks, s);
+        return few ? append_dispatch<true, false, false>(a, qa, q_blocks, kv_blocks, s)
+                   : append_dispatch<true, false, true>(a, qa, q_blocks, kv_blocks, s);
     }
     if (half)
-        return few ? append_dispatch<false, true, 1>(a, qa, q_blocks, kv_blocks, s)
-                   : append_dispatch<false, true, 4>(a, qa, q_blocks, kv_blocks, s);
-    return few ? append_dispatch<false, false, 1>(a, qa, q_blocks, kv_blocks, s)
-               : append_dispatch<false, false, 4>(a, qa, q_blocks, kv_blocks, s);
+        return few ? append_dispatch<false, true, false>(a, qa, q_blocks, kv_blocks, s)
+                   : append_dispatch<false, true, true>(a, qa, q_blocks, kv_blocks, s);
+    return few ? append_dispatch<false, false, false>(a, qa, q_blocks, kv_blocks, s)
+               : append_dispatch<false, false, true>(a, qa, q_blocks, kv_blocks, s);
 }
 
 cudaError_t launch_kv_read(const dg_kv_cache& cache, const int32_t* slots, int64_t tokens,
