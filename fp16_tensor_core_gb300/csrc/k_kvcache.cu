@@ -116,8 +116,9 @@ struct RopeArgs {
     uint32_t* status;
 };
 
-// A thread owns one item (8 rotated pairs of the half layout, 4 of the
-// interleaved one, or 8 dims that are copied) of one token for kHeads heads:
+// A thread owns one item (of the half layout 8 rotated pairs or 16 dims that
+// are copied, of the interleaved one 4 pairs or 8 dims) of one token for kHeads
+// heads:
 // its cosines and sines stay in registers across the heads, and both halves
 // of a pair are in its hands, so each element is read and written once:
 // 16385 tokens x 32 heads of 128, half of each turned, 43.8 us (6.2 TB/s, 0.92
@@ -134,9 +135,9 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
     const int slot = a.slots != nullptr ? a.slots[t] : -1;
     const int pair_items = kHalf ? a.rot8 / 2 : a.rot8;
     const bool turn = item < pair_items;
-    // first (and for the half layout second) 8 dims of the item
-    const int d0 = kHalf && !turn ? 8 * (item - pair_items + a.rot8) : 8 * item;
-    const int d1 = kHalf && turn ? d0 + 4 * a.rot8 : d0;
+    // first and (half layout) second 8 dims of the item
+    const int d0 = !kHalf ? 8 * item : turn ? 8 * item : 8 * a.rot8 + 16 * (item - pair_items);
+    const int d1 = turn ? d0 + 4 * a.rot8 : d0 + 8;
     const uint16_t* x = a.x + t * a.x_ts;
     uint16_t* out = a.out + t * a.o_ts;
     uint4 v0[kHeads], v1[kHeads];
@@ -145,7 +146,7 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
         const int h = h0 + k * a.head_steps;
         if (h < a.heads) {
             v0[k] = ld_once(x + h * a.x_hs + d0);
-            if (kHalf && turn) v1[k] = ld_once(x + h * a.x_hs + d1);
+            if (kHalf) v1[k] = ld_once(x + h * a.x_hs + d1);
         }
     }
     if (a.positions != nullptr && (pos < 0 || pos >= a.table_positions)) {
@@ -182,7 +183,7 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
                     y1[i] = q[i] * c[i] + p[i] * s[i];
                 }
                 v0[k] = pack8<kFp16>(y0);
-                *reinterpret_cast<uint4*>(out + h * a.o_hs + d1) = pack8<kFp16>(y1);
+                v1[k] = pack8<kFp16>(y1);
             } else {
                 float y[8];
 #pragma unroll
@@ -194,6 +195,7 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
             }
         }
         *reinterpret_cast<uint4*>(out + h * a.o_hs + d0) = v0[k];
+        if (kHalf) *reinterpret_cast<uint4*>(out + h * a.o_hs + d1) = v1[k];
     }
 }
 
@@ -554,7 +556,7 @@ RopeArgs rope_args(const dg_heads& x, const dg_heads& out, int64_t tokens, int h
         a.table_positions = rot->positions;
     }
     const bool half = rot == nullptr || rot->layout == DG_ROPE_HALF;
-    a.items = half ? head_dim / 8 - a.rot8 / 2 : head_dim / 8;
+    a.items = head_dim / (half ? 16 : 8);
     a.sign = inverse ? -1.0f : 1.0f;
     a.status = status;
     return a;
