@@ -116,12 +116,11 @@ struct RopeArgs {
     uint32_t* status;
 };
 
-// A thread owns one item (of the half layout 8 rotated pairs or 16 dims that
-// are copied, of the interleaved one 4 pairs or 8 dims) of one token for kHeads
-// heads:
+// A thread owns one item (8 rotated pairs, or 16 dims that are copied) of one
+// token for kHeads heads:
 // its cosines and sines stay in registers across the heads, and both halves
 // of a pair are in its hands, so each element is read and written once:
-// 16385 tokens x 32 heads of 128, half of each turned, 43.8 us (6.2 TB/s, 0.92
+// 16385 tokens x 32 heads of 128, half of each turned, 42.5 us (6.4 TB/s, 0.95
 // of a copy).
 template <bool kFp16, bool kHalf, int kHeads>
 __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, int head_block) {
@@ -133,11 +132,10 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
     if (local >= a.tokens_per_block || t >= a.tokens || h0 >= a.head_steps) return;
     const int64_t pos = a.positions != nullptr ? a.positions[t] : 0;
     const int slot = a.slots != nullptr ? a.slots[t] : -1;
-    const int pair_items = kHalf ? a.rot8 / 2 : a.rot8;
-    const bool turn = item < pair_items;
-    // first and (half layout) second 8 dims of the item
-    const int d0 = !kHalf ? 8 * item : turn ? 8 * item : 8 * a.rot8 + 16 * (item - pair_items);
-    const int d1 = turn ? d0 + 4 * a.rot8 : d0 + 8;
+    const bool turn = item < a.rot8 / 2, apart = kHalf && turn;
+    // first and second 8 dims of the item
+    const int d0 = apart ? 8 * item : 16 * item;
+    const int d1 = apart ? d0 + 4 * a.rot8 : d0 + 8;
     const uint16_t* x = a.x + t * a.x_ts;
     uint16_t* out = a.out + t * a.o_ts;
     uint4 v0[kHeads], v1[kHeads];
@@ -146,7 +144,7 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
         const int h = h0 + k * a.head_steps;
         if (h < a.heads) {
             v0[k] = ld_once(x + h * a.x_hs + d0);
-            if (kHalf) v1[k] = ld_once(x + h * a.x_hs + d1);
+            v1[k] = ld_once(x + h * a.x_hs + d1);
         }
     }
     if (a.positions != nullptr && (pos < 0 || pos >= a.table_positions)) {
@@ -154,12 +152,11 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
         return;
     }
     if (a.slots != nullptr && slot >= a.nslots) return;   // the cache's blocks report it
-    constexpr int kPairs = kHalf ? 8 : 4;
-    float c[kPairs], s[kPairs];
+    float c[8], s[8];
     if (turn) {
-        const float4* row = a.table + (pos * (4 * a.rot8) + item * kPairs) / 2;
+        const float4* row = a.table + (pos * (4 * a.rot8) + item * 8) / 2;
 #pragma unroll
-        for (int i = 0; i < kPairs / 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float4 f = __ldg(row + i);
             c[2 * i] = f.x;
             s[2 * i] = a.sign * f.y;
@@ -172,30 +169,29 @@ __device__ __forceinline__ void rope_block(const RopeArgs& a, int token_block, i
         const int h = h0 + k * a.head_steps;
         if (h >= a.heads) continue;
         if (turn) {
-            float p[8];
+            float p[8], q[8], y0[8], y1[8];
             unpack8<kFp16>(v0[k], p);
+            unpack8<kFp16>(v1[k], q);
             if constexpr (kHalf) {
-                float q[8], y0[8], y1[8];
-                unpack8<kFp16>(v1[k], q);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     y0[i] = p[i] * c[i] - q[i] * s[i];
                     y1[i] = q[i] * c[i] + p[i] * s[i];
                 }
-                v0[k] = pack8<kFp16>(y0);
-                v1[k] = pack8<kFp16>(y1);
             } else {
-                float y[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    y[2 * i] = p[2 * i] * c[i] - p[2 * i + 1] * s[i];
-                    y[2 * i + 1] = p[2 * i + 1] * c[i] + p[2 * i] * s[i];
+                    y0[2 * i] = p[2 * i] * c[i] - p[2 * i + 1] * s[i];
+                    y0[2 * i + 1] = p[2 * i + 1] * c[i] + p[2 * i] * s[i];
+                    y1[2 * i] = q[2 * i] * c[4 + i] - q[2 * i + 1] * s[4 + i];
+                    y1[2 * i + 1] = q[2 * i + 1] * c[4 + i] + q[2 * i] * s[4 + i];
                 }
-                v0[k] = pack8<kFp16>(y);
             }
+            v0[k] = pack8<kFp16>(y0);
+            v1[k] = pack8<kFp16>(y1);
         }
         *reinterpret_cast<uint4*>(out + h * a.o_hs + d0) = v0[k];
-        if (kHalf) *reinterpret_cast<uint4*>(out + h * a.o_hs + d1) = v1[k];
+        *reinterpret_cast<uint4*>(out + h * a.o_hs + d1) = v1[k];
     }
 }
 
@@ -391,13 +387,13 @@ constexpr int kAppendTokens = 2;   // of a lane group, in large calls
 // Every kv_every-th block writes the cache (bound by its instructions), the
 // others turn the queries (bound by HBM): dealt out among one another they
 // share the SMs.  16001 tokens of 32 + 8 + 8 heads of 128, half of each
-// turned, interleaved: 63 us, 5.8 TB/s, 0.86 of a copy; whole heads in the
-// half layout 65; 32 + 32 + 32 heads 148 (0.67: two thirds of it are cache
-// rows).  With 8 dims a lane and 4 tokens in flight 72, 80 and 220.  Blocks
-// per SM by the registers of the four query heads a thread holds: the half
-// layout spills at 5 (68) and 6 (79).
+// turned, interleaved: 60.5 us, 6.0 TB/s, 0.89 of a copy; whole heads in the
+// half layout 61.7; 32 + 32 + 32 heads 145 (0.68: two thirds of it are cache
+// rows).  With 8 dims a lane and 4 tokens in flight 72, 80 and 220.  Four
+// blocks an SM, by the registers of the four query heads a thread holds; with
+// two heads and six blocks 65 us.
 template <bool kFp16, bool kHalf, int kLanes, bool kMany>
-__global__ void __launch_bounds__(256, kMany ? (kHalf ? 4 : 6) : 6)
+__global__ void __launch_bounds__(256, kMany ? 4 : 6)
 kv_append_kernel(const AppendArgs a, const RopeArgs q, int kv_blocks, int kv_every) {
     pdl_wait();
     const int round = static_cast<int>(blockIdx.x) / kv_every;
@@ -556,7 +552,7 @@ RopeArgs rope_args(const dg_heads& x, const dg_heads& out, int64_t tokens, int h
         a.table_positions = rot->positions;
     }
     const bool half = rot == nullptr || rot->layout == DG_ROPE_HALF;
-    a.items = head_dim / (half ? 16 : 8);
+    a.items = head_dim / 16;
     a.sign = inverse ? -1.0f : 1.0f;
     a.status = status;
     return a;
