@@ -369,7 +369,7 @@ class DgRotary:
             raise ValueError("table must be FP32 [positions, rotary_dim / 2, 2]")
         self.table = table
         self.c = _Rotary(_ptr(table), table.shape[0], 2 * table.shape[1], int(layout))
-        self.address = ctypes.addressof(self.c)
+        self.rotary_address = ctypes.addressof(self.c)
 
 
 class DgKvCache:
@@ -387,7 +387,7 @@ class DgKvCache:
         pages, self.kv_heads, page_size, self.head_dim = k.shape
         self.c = _KvCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, self.kv_heads,
                           page_size, self.head_dim)
-        self.address = ctypes.addressof(self.c)
+        self.cache_address = ctypes.addressof(self.c)
 
 
 def dg_rope_table(table, base=10000.0, scaling=DG_ROPE_UNSCALED, factor=1.0,

@@ -33,7 +33,7 @@ static PyObject *current_device;   /* () -> index */
 static PyObject *check;            /* (status, name): raises unless DG_OK */
 
 static PyObject *n_stride, *n_shape, *n_dtype, *n_is_cuda, *n_data_ptr, *n_numel, *n_is_contiguous, *n_nbytes,
-    *n_address, *n_cuda_stream;
+    *n_rotary, *n_cache, *n_cuda_stream;
 
 static int fail(const char* message) {
     PyErr_SetString(PyExc_ValueError, message);
@@ -137,7 +137,8 @@ static int get_array(PyObject* t, PyObject* type, const char* type_name, int64_t
 }
 
 /* The struct that a DgRotary or DgKvCache holds. */
-static int get_struct(PyObject* handle, void** out) { return as_address(PyObject_GetAttr(handle, n_address), out); }
+static int get_rotary(PyObject* handle, void** out) { return as_address(PyObject_GetAttr(handle, n_rotary), out); }
+static int get_cache(PyObject* handle, void** out) { return as_address(PyObject_GetAttr(handle, n_cache), out); }
 
 /* None: the current device's current stream; else a handle or a Stream. */
 static int get_stream(PyObject* s, dg_stream_t* out) {
@@ -176,7 +177,7 @@ static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
     if (want_args(n, 6) < 0 || get_heads(a[0], "x", NULL, &x) < 0 || get_heads(a[1], "out", &x, &out) < 0 ||
         get_array(a[2], type_int32, "int32", x.shape[0], "positions", &positions) < 0 ||
-        get_struct(a[3], &rotary) < 0)
+        get_rotary(a[3], &rotary) < 0)
         return NULL;
     const int inverse = PyObject_IsTrue(a[4]);
     if (inverse < 0 || get_stream(a[5], &stream) < 0) return NULL;
@@ -201,7 +202,7 @@ static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     dg_stream_t stream;
     (void)self;
     if (want_args(n, 9) < 0 || get_heads(a[0], "k", NULL, &k) < 0 || get_heads(a[1], "v", &k, &v) < 0 ||
-        get_struct(a[3], &cache) < 0 || cache_heads(&k, cache) < 0)
+        get_cache(a[3], &cache) < 0 || cache_heads(&k, cache) < 0)
         return NULL;
     const int queries = a[6] != Py_None;
     if (queries) {
@@ -212,7 +213,7 @@ static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) 
         }
     }
     if ((a[4] != Py_None && get_array(a[4], type_int32, "int32", k.shape[0], "positions", &positions) < 0) ||
-        (a[5] != Py_None && get_struct(a[5], &rotary) < 0) ||
+        (a[5] != Py_None && get_rotary(a[5], &rotary) < 0) ||
         get_array(a[2], type_int32, "int32", k.shape[0], "slots", &slots) < 0 || get_stream(a[8], &stream) < 0)
         return NULL;
     dg_status status;
@@ -233,7 +234,7 @@ static PyObject* py_kv_read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     const int keys = a[2] != Py_None, values = a[3] != Py_None;
     const heads_arg* some = keys ? &k : &v;
     if ((keys && get_heads(a[2], "k", NULL, &k) < 0) ||
-        ((values || !keys) && get_heads(a[3], "v", keys ? &k : NULL, &v) < 0) || get_struct(a[0], &cache) < 0 ||
+        ((values || !keys) && get_heads(a[3], "v", keys ? &k : NULL, &v) < 0) || get_cache(a[0], &cache) < 0 ||
         cache_heads(some, cache) < 0 ||
         get_array(a[1], type_int32, "int32", some->shape[0], "slots", &slots) < 0 || get_stream(a[4], &stream) < 0)
         return NULL;
@@ -253,7 +254,7 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
     dg_stream_t stream;
     (void)self;
     if (want_args(n, 11) < 0 || get_heads(a[0], "q", NULL, &q) < 0 || get_heads(a[1], "out", &q, &out) < 0 ||
-        get_struct(a[2], &handle) < 0 || numbers(PyObject_GetAttr(a[3], n_shape), 2, shape, "q", kTable) < 0 ||
+        get_cache(a[2], &handle) < 0 || numbers(PyObject_GetAttr(a[3], n_shape), 2, shape, "q", kTable) < 0 ||
         numbers(PyObject_CallMethodNoArgs(a[3], n_stride), 2, stride, "q", kTable) < 0)
         return NULL;
     const dg_kv_cache* cache = handle;
@@ -337,7 +338,7 @@ PyMODINIT_FUNC PyInit_dg_python(void) {
     } names[] = {
         {&n_stride, "stride"}, {&n_shape, "shape"}, {&n_dtype, "dtype"}, {&n_is_cuda, "is_cuda"},
         {&n_data_ptr, "data_ptr"}, {&n_numel, "numel"}, {&n_is_contiguous, "is_contiguous"}, {&n_nbytes, "nbytes"},
-        {&n_address, "address"}, {&n_cuda_stream, "cuda_stream"},
+        {&n_rotary, "rotary_address"}, {&n_cache, "cache_address"}, {&n_cuda_stream, "cuda_stream"},
     };
     for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
         if (*names[i].at == NULL && (*names[i].at = PyUnicode_InternFromString(names[i].name)) == NULL) return NULL;

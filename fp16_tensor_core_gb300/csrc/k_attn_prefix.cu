@@ -48,6 +48,10 @@ constexpr int kTileTokens = 128;
 constexpr int kTileRows = kPrefixTileRows;
 constexpr int kThreads = 640;   // warpgroups: softmax of even and of odd tiles, keys, values, MMA
 constexpr float kGrowth = 8.0f; // log2 of how far weights may pass 1
+// Registers a thread of the softmax, the conversion and the MMA warps.  Their
+// sum has to be there at the launch (an increase waits for what others give
+// back, and for ever for what nobody has): run_prefix() looks.
+constexpr int kSoftmaxRegs = 144, kConvertRegs = 72, kMmaRegs = 40;
 
 __device__ __forceinline__ void tmem_load_frag4(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -350,11 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     // all that this one reads, which may begin while they end.
     if (a.splits == 1) pdl_wait();
 
-    // Registers: 96 a thread at launch; the softmax warps take what the
-    // others leave (144 + 144 + 72 + 72 + 40 <= 5 * 96).
+    // The softmax warps take the registers that the others leave.
     if (warp < 8) {
         // -------------------------------------------------- queries, softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
         const int b = warp >> 2;   // stream
         const int g = lane >> 2, c = lane & 3;
         if (b == 0) {   // thread i takes row i of the tile, scaled by a power of two (BF16)
@@ -610,13 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
         }
     } else if (warp < 16) {
         // ---------------------------- codes to operands: keys, then values' warps
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvertRegs));
         if (warp < 12)
             convert_role<D, false>(a, smem, bars, ctl, tile0, tiles, head);
         else
             convert_role<D, true>(a, smem, bars, ctl, tile0, tiles, head);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMmaRegs));
         if (warp == 16 && lane == 0) {
             // -------------------------------------------------- MMA issue
             constexpr uint32_t kScoreDesc = idesc_f32acc(kTileRows, kTileTokens, 0, 0);
@@ -687,6 +690,15 @@ template <int D, bool kFp16>
 cudaError_t run_prefix(const PrefixArgs& a, cudaStream_t s) {
     const cudaError_t set = allow_smem(attn_prefix_kernel<D, kFp16>, PrefixShape<D>::kSmem);
     if (set != cudaSuccess) return set;
+    static const cudaError_t registers = [] {
+        cudaFuncAttributes f{};
+        const cudaError_t e = cudaFuncGetAttributes(&f, attn_prefix_kernel<D, kFp16>);
+        if (e != cudaSuccess) return e;
+        return kThreads / 128 * f.numRegs >= 2 * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs
+                   ? cudaSuccess
+                   : cudaErrorInvalidConfiguration;
+    }();
+    if (registers != cudaSuccess) return registers;
     const unsigned blocks = static_cast<unsigned>(a.kv_heads) * a.splits * a.row_tiles;
     return launch_kernel(attn_prefix_kernel<D, kFp16>, dim3(blocks), dim3(kThreads), PrefixShape<D>::kSmem, s, a);
 }

@@ -1,6 +1,8 @@
 """What the Python serving calls refuse before anything reaches the library.
 CPU only: the tensors' shapes and types are looked at first, then that they
 are on a device."""
+import ctypes
+
 import pytest
 import torch
 
@@ -13,9 +15,9 @@ BF, I32 = torch.bfloat16, torch.int32
 class Handle:
     """A cache or rotary handle as the calls see it, over host memory."""
 
-    def __init__(self, c):
-        import ctypes
-        self.c, self.address = c, ctypes.addressof(c)
+    def __init__(self, c, name):
+        self.c = c
+        setattr(self, name, ctypes.addressof(c))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -27,8 +29,8 @@ def heads(tokens=3, n=4, dim=64, dtype=BF):
     return torch.zeros(tokens, n, dim, dtype=dtype)
 
 
-CACHE = Handle(dg._KvCache(0, 0, 0, 0, 10, 2, 16, 64))
-ROTARY = Handle(dg._Rotary(0, 100, 64, 0))
+CACHE = Handle(dg._KvCache(0, 0, 0, 0, 10, 2, 16, 64), "cache_address")
+ROTARY = Handle(dg._Rotary(0, 100, 64, 0), "rotary_address")
 SHAPE = r"x must be BF16 or FP16 \[tokens, heads, head_dim\] with contiguous heads"
 
 
@@ -51,6 +53,24 @@ def test_what_is_no_tensor():
         dg.dg_kv_append("k", "v", "slots", CACHE)
     with pytest.raises((AttributeError, ValueError)):
         dg.dg_attn_decode(1, 2, 3, 4, 5, 6)
+
+
+def test_the_other_kind_of_handle():
+    """A rotary table is no cache: nothing is read from it as one."""
+    with pytest.raises(AttributeError, match="cache_address"):
+        dg.dg_kv_append(FakeHeads(), FakeHeads(), torch.zeros(3, dtype=I32), ROTARY)
+
+
+class FakeHeads:
+    """What the calls read of a device tensor of heads."""
+
+    dtype, shape, is_cuda = BF, (3, 2, 64), True
+
+    def stride(self):
+        return (128, 64, 1)
+
+    def data_ptr(self):
+        return 0x7F0000000000
 
 
 def test_calls_with_host_tensors():
