@@ -23,7 +23,7 @@ NATIVE = os.path.join(OUT_DIR, "dg_python.so")   # argument marshalling for Pyth
 SOURCES = ["dg_api.cu", "k_scale.cu", "k_gemv.cu", "k_gemv_mma.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu",
            "k_gemm_skinny.cu", "dg_static.cu", "k_kvcache.cu", "k_attn_decode.cu",
            "k_attn_prefix.cu"]
-HEADERS = ["dg_ptx.cuh", "dg_internal.h", "gemm_common.cuh", "attn_common.cuh"]
+HEADERS = ["dg_ptx.cuh", "dg_internal.h", "gemm_common.cuh", "attn_common.cuh", "prefix_barriers.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

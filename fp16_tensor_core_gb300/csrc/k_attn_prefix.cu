@@ -40,6 +40,7 @@
 #include "attn_common.cuh"
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
+#include "prefix_barriers.h"
 
 namespace dg {
 namespace {
@@ -116,6 +117,9 @@ __device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, const 
         if (mbar_try_wait(bar, parity)) return true;
     return wait_bounded(bar, parity, ctl);
 }
+__device__ __forceinline__ bool wait_soon(uint64_t* bars, prefix::Phase p, const WaitCtl& ctl) {
+    return wait_soon(bars + p.barrier, p.parity, ctl);
+}
 
 // Two FP32 lanes at once.
 using f32x2 = unsigned long long;
@@ -176,10 +180,11 @@ struct PrefixShape {
     static_assert(kOCol + 2 * D <= 512, "tensor memory");
     static constexpr int kKAt = kOperandBytes;
     static constexpr int kVAt = kKAt + 2 * kOperandBytes;
-    static constexpr int kFactorsAt = kVAt + 2 * kOperandBytes;  // [4][3][128] per-token factors
-    static constexpr int kRowsAt = kFactorsAt + 4 * 3 * 128 * 4; // [2][2][128] cache rows
+    static constexpr int kFactorsAt = kVAt + 2 * kOperandBytes;  // [slots][3][128] per-token factors
+    static constexpr int kRowsAt = kFactorsAt + prefix::kFactorSlots * 3 * 128 * 4;   // [2][2][128] cache rows
     static constexpr int kQScaleAt = kRowsAt + 2 * 2 * 128 * 8;
     static constexpr int kBarsAt = kQScaleAt + 128 * 4;
+    static_assert(prefix::kBarriers * 8 + 8 <= 256, "barriers, tensor memory's address, abort flag");
     static constexpr int kSmem = kBarsAt + 256 + 1024;           // and alignment
 };
 
@@ -189,11 +194,9 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
                                              const WaitCtl& ctl, int tile0, int tiles, int head) {
     using S = PrefixShape<D>;
     constexpr uint32_t kBarrier = kValues ? 4 : 2;
-    uint64_t* full = kValues ? bars + 3 : bars + 1;
     // A stage is free when the product that reads it is done.  The factors
     // are read later, but are four deep: the scores of tile j come after the
     // weights of tile j - 2.
-    uint64_t* free = kValues ? bars + 9 : bars + 5;
     float* factors = reinterpret_cast<float*>(smem + S::kFactorsAt);
     int64_t* cache_rows = reinterpret_cast<int64_t*>(smem + S::kRowsAt) + (kValues ? 2 * 128 : 0);
     uint8_t* operand = smem + (kValues ? S::kVAt : S::kKAt);
@@ -262,7 +265,8 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
     for (int j = 0; j < tiles && ok; ++j) {
         const int b = j & 1;
         const int page2 = find_page(j + 2);   // on its way meanwhile
-        if (j >= 2) ok = __all_sync(0xFFFFFFFFu, wait_soon(&free[b], ((j - 2) >> 1) & 1, ctl));
+        if (j >= 2)
+            ok = __all_sync(0xFFFFFFFFu, wait_soon(bars, kValues ? prefix::output(j - 2) : prefix::scores(j - 2), ctl));
         if (ok) {
 #pragma unroll
             for (int s = 0; s < kPasses; ++s) {
@@ -276,7 +280,7 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
                 st_shared_v4(dst1 + at, h[4], h[5], h[6], h[7]);
             }
             if constexpr (!kValues) {
-                float* f = factors + (j & 3) * 3 * 128 + factor_at;
+                float* f = factors + prefix::factor_slot(j) * 3 * 128 + factor_at;
                 const float safe = sv < 0x1p-100f ? 0x1p-100f : sv;
                 f[0] = sk;
                 f[128] = sv == -1.0f ? -INFINITY : __log2f(safe);
@@ -284,7 +288,10 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if ((i & 31) == 0) mbar_arrive(&full[b]);
+            if ((i & 31) == 0) {
+                mbar_arrive(bars + (kValues ? prefix::values(j) : prefix::keys(j)).barrier);
+                if (!kValues) mbar_arrive(bars + prefix::factors(j).barrier);
+            }
             if (j + 1 < tiles) {
                 fetch(j + 1);
                 load_scales(row1, &sk, &sv);
@@ -309,27 +316,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
     float* factors = reinterpret_cast<float*>(smem + S::kFactorsAt);
     float* qscale = reinterpret_cast<float*>(smem + S::kQScaleAt);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBarsAt);
-    uint64_t* q_full = bars;          // 128 arrivals
-    uint64_t* k_full = bars + 1;      // [2], a warp
-    uint64_t* v_full = bars + 3;      // [2], a warp
-    uint64_t* s_full = bars + 5;      // [2], commit
-    uint64_t* w_full = bars + 7;      // [2], a warp: weights in place
-    uint64_t* o_done = bars + 9;      // [2], commit
-    uint64_t* drain = bars + 11;      // commit
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + prefix::kBarriers);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 128);
+        // arrivals: a thread, four warps, or a commit of the MMA thread
+        mbar_init(bars + prefix::kQueries, 128);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&k_full[b], 4);
-            mbar_init(&v_full[b], 4);
-            mbar_init(&s_full[b], 1);
-            mbar_init(&w_full[b], 4);
-            mbar_init(&o_done[b], 1);
+            mbar_init(bars + prefix::kKeys + b, 4);
+            mbar_init(bars + prefix::kValues + b, 4);
+            mbar_init(bars + prefix::kScores + b, 1);
+            mbar_init(bars + prefix::kWeights + b, 4);
+            mbar_init(bars + prefix::kOutput + b, 1);
         }
-        mbar_init(drain, 1);
+        for (int f = 0; f < prefix::kFactorSlots; ++f) mbar_init(bars + prefix::kFactors + f, 4);
+        mbar_init(bars + prefix::kDrain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             }
             qscale[i] = factor;
             fence_proxy_async_smem();
-            mbar_arrive(q_full);
+            mbar_arrive(bars + prefix::kQueries);
         }
         named_bar_sync(1, 256);   // before the factors are read
         const int quarter = warp & 3;
@@ -408,12 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
         const uint32_t o_col = S::kOCol + D * b;
         bool ok = true;
         for (int j = b; j < tiles; j += 2) {
-            const uint32_t parity = (j >> 1) & 1;
-            // the keys' barrier also hands over the per-token factors
-            ok = *ctl.abort_flag == 0 && wait_soon(&k_full[b], parity, ctl) && wait_soon(&s_full[b], parity, ctl);
+            ok = *ctl.abort_flag == 0 && wait_soon(bars, prefix::factors(j), ctl) &&
+                 wait_soon(bars, prefix::scores(j), ctl);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after_sync();
-            const float* f = factors + (j & 3) * 3 * 128 + 4 * c;
+            const float* f = factors + prefix::factor_slot(j) * 3 * 128 + 4 * c;
             // 16 rows at a time, in one pass against the reference as it
             // stands; only where a row's maximum has outgrown it (the first
             // tiles) the reference moves and the pass is made again.
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                     }
                     // O as the stream's previous tile left it; a wait that
                     // runs out ends the loop below
-                    if (j >= 2 && __all_sync(0xFFFFFFFFu, wait_soon(&o_done[b], ((j - 2) >> 1) & 1, ctl))) {
+                    if (j >= 2 && __all_sync(0xFFFFFFFFu, wait_soon(bars, prefix::output(j - 2), ctl))) {
                         tc_fence_after_sync();
 #pragma unroll 1
                         for (int p = 0; p < D / 32; ++p) {
@@ -508,12 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&w_full[b]);
+            if (lane == 0) mbar_arrive(bars + prefix::weights(j).barrier);
         }
         // ---- both streams' results, joined by the first group
         if (ok && tiles > b) {
             const int last = tiles - 1 - ((tiles - 1 - b) & 1);
-            ok = wait_soon(&o_done[b], (last >> 1) & 1, ctl);
+            ok = wait_soon(bars, prefix::output(last), ctl);
         }
         // Every MMA is done: the operands' memory is free.  (And the kernel
         // before this one: whoever waits for this one waits for both.)
@@ -640,12 +641,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         mma_f16(d, q_desc + h * kColumn + 2 * x, kd + h * kColumn + 2 * x, kScoreDesc, h > 0 || x > 0);
-                mma_commit(&s_full[j & 1]);
+                mma_commit(bars + prefix::scores(j).barrier);
             };
-            bool ok = wait_soon(q_full, 0, ctl);
+            bool ok = wait_soon(bars + prefix::kQueries, 0, ctl);
             bool issued = false;
             for (int j = 0; j < 2 && j < tiles && ok; ++j) {
-                ok = wait_soon(&k_full[j], 0, ctl);
+                ok = wait_soon(bars, prefix::keys(j), ctl);
                 if (!ok) break;
                 tc_fence_after_sync();
                 issued = true;
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             }
             for (int j = 0; j < tiles && ok; ++j) {
                 const int b = j & 1;
-                ok = wait_soon(&v_full[b], (j >> 1) & 1, ctl) && wait_soon(&w_full[b], (j >> 1) & 1, ctl);
+                ok = wait_soon(bars, prefix::values(j), ctl) && wait_soon(bars, prefix::weights(j), ctl);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint64_t vd = v_desc + b * kStage;
@@ -661,10 +662,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                 for (int x = 0; x < kTileTokens / 16; ++x)
                     mma_f16_ts(tmem + S::kOCol + D * b, tmem + 128 * b + 8 * x, vd + x * (2048 >> 4), kValueDesc,
                                j > 1 || x > 0);
-                mma_commit(&o_done[b]);
+                mma_commit(bars + prefix::output(j).barrier);
                 if (j + 2 < tiles) {
                     // they take the place of the weights just read
-                    ok = wait_soon(&k_full[b], ((j + 2) >> 1) & 1, ctl) && wait_soon(&o_done[b], (j >> 1) & 1, ctl);
+                    ok = wait_soon(bars, prefix::keys(j + 2), ctl) && wait_soon(bars, prefix::output(j), ctl);
                     if (!ok) break;
                     tc_fence_after_sync();
                     scores(j + 2);
@@ -672,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
             }
             if (issued) {
                 // Tensor memory is freed below: wait for every MMA issued.
-                mma_commit(drain);
-                wait_bounded(drain, 0, ctl, false);
+                mma_commit(bars + prefix::kDrain);
+                wait_bounded(bars + prefix::kDrain, 0, ctl, false);
             }
         }
     }
