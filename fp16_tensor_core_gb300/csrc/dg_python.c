@@ -266,6 +266,10 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
         fail_about("q", kTable);
         return NULL;
     }
+    if (batch > 1 && stride[0] < pages) {   /* rows that share entries: an expanded table, overlapping windows */
+        fail("page_table must have a row of its own for each request");
+        return NULL;
+    }
     if (batch != 0 ? tokens % batch != 0 : tokens != 0) {
         fail("q must have the same number of tokens for each request");
         return NULL;
@@ -297,7 +301,7 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
     dg_status status;
     Py_BEGIN_ALLOW_THREADS
     status = lib_attn_decode(&q.c, &out.c, lse, to_int(batch), to_int(batch != 0 ? tokens / batch : 1),
-                             to_int(q.shape[1]), cache, table, stride[0] > pages ? stride[0] : pages, pages, lens,
+                             to_int(q.shape[1]), cache, table, batch > 1 ? stride[0] : pages, pages, lens,
                              prefix, prefix_len, scale, q.type, scratch, scratch_bytes, stream);
     Py_END_ALLOW_THREADS
     return done(status, "dg_attn_decode");

@@ -465,7 +465,8 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  *               exponentials, or NULL.
  *   batch       0 .. 2048; q_len >= 1; q_heads a multiple of kv_heads.
  *   page_table  int32, device: row b, at b * table_stride, names the pages of
- *               request b's tokens in order; max_pages entries a row.
+ *               request b's tokens in order; max_pages entries a row,
+ *               table_stride >= max_pages.
  *   kv_lens     int32[batch], device, 0 .. max_pages * page_size each.  A
  *               length outside that counts as 0; queries that see a token
  *               on a page outside the cache get unspecified results (no

@@ -1,0 +1,36 @@
+"""Arguments that the Python serving calls must refuse although each tensor by
+itself is well formed.  CPU only: refused before anything reaches the library."""
+import pytest
+
+import fp16_tensor_core_gb300 as dg
+from fp16_tensor_core_gb300 import build as dg_build
+from test_serving_binding import CACHE, I32, FakeHeads
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    dg_build.build()
+
+
+class FakeTable:
+    """What dg_attn_decode reads of a device page table."""
+
+    dtype, is_cuda = I32, True
+
+    def __init__(self, shape, stride):
+        self.shape, self._stride = shape, stride
+
+    def stride(self):
+        return self._stride
+
+    def data_ptr(self):
+        return 0x7F0000000000
+
+
+@pytest.mark.parametrize("stride", [(0, 1), (1, 1), (4, 1)])
+def test_page_table_rows_that_share_entries(stride):
+    """An expanded table, and overlapping windows: a row's pages are looked up
+    a row's width apart, past the end of what such a table holds."""
+    q = FakeHeads()
+    with pytest.raises(ValueError, match="page_table must have a row of its own"):
+        dg.dg_attn_decode(q, q, CACHE, FakeTable((3, 5), stride), None, None)
