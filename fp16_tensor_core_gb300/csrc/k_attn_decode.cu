@@ -380,13 +380,17 @@ attn_split_kernel(const AttnArgs a) {
         f1 = min(total, f0 + run);
 
         // Requests without a token of their own: nothing below reaches them.
+        // A warp a row (rows are counted in 32 bits, their elements are not).
         for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
             if (cum[b + 1] != cum[b]) continue;
-            for (int i = threadIdx.x; i < a.q_len * a.q_heads * (D / 4); i += kThreads) {
-                const int row = i / (D / 4), d = 4 * (i % (D / 4));
-                const RowEnd e = row_end<D>(a, static_cast<int64_t>(b) * a.q_len + row / a.q_heads,
-                                            row % a.q_heads, -INFINITY, 0.0f, d == 0);
-                emit4<D, kFp16>(e, d, make_float4(0, 0, 0, 0));
+            for (int row = warp; row < a.q_len * a.q_heads; row += kWarps) {
+                const int i = row / a.q_heads;
+                const RowEnd e = row_end<D>(a, static_cast<int64_t>(b) * a.q_len + i, row - i * a.q_heads, -INFINITY,
+                                            0.0f, lane == 0);
+                if (D >= 128 || 4 * lane < D) {
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) emit4<D, kFp16>(e, 4 * lane + 128 * k, make_float4(0, 0, 0, 0));
+                }
             }
         }
     }
