@@ -429,10 +429,10 @@ def dg_attn_decode_scratch(batch, q_len, q_heads, cache, prefix_len=0, sm_count=
 
 
 def dg_attn_decode(q, out, cache, page_table, kv_lens, scratch, scale=None, lse=None,
-                   prefix_pages=None, prefix_len=0, stream=None) -> None:
+                   prefix_pages=None, prefix_len=None, stream=None) -> None:
     """Attention of q [batch * q_len, q_heads, head_dim] over the cache: own
     tokens by page_table [batch, max_pages] and kv_lens [batch], after a prefix
-    that the whole batch shares (prefix_pages, prefix_len)."""
+    that the whole batch shares (prefix_pages and prefix_len, given together)."""
     (_native or _load_native()).attn_decode(q, out, cache, page_table, kv_lens, scratch, scale, lse,
                                             prefix_pages, prefix_len, stream)
 

@@ -250,10 +250,15 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
     static const char kTable[] = "must have the cache's head_dim, page_table must be int32 with contiguous rows";
     heads_arg q, out;
     void *handle, *table, *lens, *scratch, *lse = NULL, *prefix = NULL;
-    int64_t shape[2], stride[2], scratch_bytes, prefix_len;
+    int64_t shape[2], stride[2], scratch_bytes, prefix_len = 0;
     dg_stream_t stream;
     (void)self;
-    if (want_args(n, 11) < 0 || get_heads(a[0], "q", NULL, &q) < 0 || get_heads(a[1], "out", &q, &out) < 0 ||
+    if (want_args(n, 11) < 0 || (a[9] != Py_None && as_int64(Py_NewRef(a[9]), &prefix_len) < 0)) return NULL;
+    if (a[8] == Py_None ? prefix_len != 0 : a[9] == Py_None) {   /* a length of 0 is no prefix, pages or not */
+        fail("prefix_pages and prefix_len must be given together");
+        return NULL;
+    }
+    if (get_heads(a[0], "q", NULL, &q) < 0 || get_heads(a[1], "out", &q, &out) < 0 ||
         get_cache(a[2], &handle) < 0 || numbers(PyObject_GetAttr(a[3], n_shape), 2, shape, "q", kTable) < 0 ||
         numbers(PyObject_CallMethodNoArgs(a[3], n_stride), 2, stride, "q", kTable) < 0)
         return NULL;
@@ -286,7 +291,6 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
         if (scale == -1.0 && PyErr_Occurred()) return NULL;
     }
     if (a[7] != Py_None && get_array(a[7], type_float32, "FP32", tokens * q.shape[1], "lse", &lse) < 0) return NULL;
-    if (as_int64(Py_NewRef(a[9]), &prefix_len) < 0) return NULL;
     if (prefix_len != 0) {
         int64_t named;
         if (get_array(a[8], type_int32, "int32", -1, "prefix_pages", &prefix) < 0 ||

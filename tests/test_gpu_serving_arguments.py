@@ -37,3 +37,12 @@ def test_page_table_views():
         with pytest.raises(ValueError, match="page_table must have a row of its own"):
             c.run(page_table=table, out=out)
     assert torch.all(out == 3.0)
+
+
+def test_a_length_of_zero_is_no_prefix():
+    """A buffer of pages that is kept while nothing is shared."""
+    c = Case([100, 40], q_heads=4, kv_heads=2, dim=64)
+    want = c.run(prefix_pages=None, prefix_len=None)
+    for pages in (None, c.table[0], c.table[0, :0]):
+        got = c.run(prefix_pages=pages, prefix_len=0)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

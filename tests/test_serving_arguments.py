@@ -34,3 +34,10 @@ def test_page_table_rows_that_share_entries(stride):
     q = FakeHeads()
     with pytest.raises(ValueError, match="page_table must have a row of its own"):
         dg.dg_attn_decode(q, q, CACHE, FakeTable((3, 5), stride), None, None)
+
+
+def test_a_prefix_without_its_length_and_the_other_way_round():
+    q, table = FakeHeads(), FakeTable((3, 5), (5, 1))
+    for kw in (dict(prefix_pages=FakeTable((5,), (1,))), dict(prefix_len=20), dict(prefix_len=-1)):
+        with pytest.raises(ValueError, match="prefix_pages and prefix_len must be given together"):
+            dg.dg_attn_decode(q, q, CACHE, table, None, None, **kw)
