@@ -410,7 +410,7 @@ def dg_rope(x, out, positions, rotary, inverse=False, stream=None) -> None:
 def dg_kv_append(k, v, slots, cache, positions=None, rotary=None, q=None, q_out=None,
                  stream=None) -> None:
     """Turn (with rotary) and quantise k, v [tokens, kv_heads, head_dim] into the
-    cache's slots; q is turned into q_out in the same launch."""
+    cache's slots; q is turned into q_out (given together) in the same launch."""
     (_native or _load_native()).kv_append(k, v, slots, cache, positions, rotary, q, q_out, stream)
 
 

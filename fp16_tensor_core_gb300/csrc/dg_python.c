@@ -205,6 +205,10 @@ static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) 
         get_cache(a[3], &cache) < 0 || cache_heads(&k, cache) < 0)
         return NULL;
     const int queries = a[6] != Py_None;
+    if (queries != (a[7] != Py_None)) {
+        fail("q and q_out must be given together");
+        return NULL;
+    }
     if (queries) {
         if (get_heads(a[6], "q", NULL, &q) < 0 || get_heads(a[7], "q_out", &q, &q_out) < 0) return NULL;
         if (q.shape[0] != k.shape[0] || q.shape[2] != k.shape[2] || q.type != k.type) {

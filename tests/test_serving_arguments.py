@@ -41,3 +41,10 @@ def test_a_prefix_without_its_length_and_the_other_way_round():
     for kw in (dict(prefix_pages=FakeTable((5,), (1,))), dict(prefix_len=20), dict(prefix_len=-1)):
         with pytest.raises(ValueError, match="prefix_pages and prefix_len must be given together"):
             dg.dg_attn_decode(q, q, CACHE, table, None, None, **kw)
+
+
+def test_queries_without_their_output_and_the_other_way_round():
+    k = FakeHeads()
+    for kw in (dict(q=k), dict(q_out=k)):
+        with pytest.raises(ValueError, match="q and q_out must be given together"):
+            dg.dg_kv_append(k, k, None, CACHE, **kw)
