@@ -4,14 +4,18 @@
 // For one query row and the tokens t it sees, with codes kc, vc and scales
 // sk, sv of one cached row each (k_t = sk_t kc_t, v_t = sv_t vc_t):
 //   x_t = scale sk_t (q . kc_t)                the score
-//   w_t = exp(x_t + ln sv_t - m),  m = max_t (x_t + ln sv_t)
+//   w_t = exp(x_t + ln sv_t - m),  m = max_t (x_t + ln sv_t) - 15 ln 2
 //   acc = sum_t w_t vc_t,          l = sum_t w_t / sv_t
 //   o   = acc / l,                 lse = m + ln l
 // The value's scale sits inside the exponential, so a weight costs one
-// exponential, w is at most 1 (exactly 1 for the row's largest) and goes to
-// the second product as FP16 with 11 bits: a weight below 2^-14 of the
-// largest contribution keeps an absolute error of 2^-25 of it.  E4M3 codes
-// are exact in FP16; sums, maxima and the state are FP32.
+// exponential.  It goes to the second product as FP16, rounded to 11 bits
+// (more would take a second FP16 operand and twice the MMAs; against codes
+// of 4 bits they are not what limits an output); l takes it before that
+// rounding.  The reference m lies 2^15 below the row's largest contribution,
+// so that weights use FP16's whole range: one below 2^-29 of the largest
+// keeps an absolute error of 2^-40 of it, and a long tail behind a single
+// heavy token is not lost (with m at the largest, tokens below 2^-25 of it
+// were).  E4M3 codes are exact in FP16; sums, maxima and the state are FP32.
 //
 // A cached element is read once and takes 4 flop per row, so for the few
 // rows that share a key head the kernel is bound by HBM: it streams codes
@@ -51,6 +55,7 @@ namespace {
 constexpr int kTile = 32;        // tokens per warp step
 constexpr int kMaxUnitRows = 16; // query rows of a unit
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kHeadroom = 15.0f;   // log2 of the largest weight (FP16 ends at 2^16)
 
 struct AttnArgs {
     const uint16_t* q;
@@ -508,7 +513,7 @@ attn_split_kernel(const AttnArgs a) {
         uint32_t qb[NT][D / 16][2];
         float qscale[NT][2];      // factor from MMA sums to base-2 scores
         int seen[NT][2];          // tokens the row sees
-        float m[NT][2], l[NT][2]; // running maximum; this lane's part of l
+        float m[NT][2], l[NT][2]; // running reference; this lane's part of l
         float acc[D / 16][NT][4]; // [.][n][i]: dim pair's first, [.][n][2 + i]: second
         int seen_min = 0, stage = 0, first_tile = 0;
         // The queries of unit `at`: rows 8 n + g.
@@ -677,6 +682,8 @@ attn_split_kernel(const AttnArgs a) {
                     top[n][i] = fmaxf(top[n][i], __shfl_xor_sync(0xFFFFFFFFu, top[n][i], 4));
                     top[n][i] = fmaxf(top[n][i], __shfl_xor_sync(0xFFFFFFFFu, top[n][i], 8));
                     top[n][i] = fmaxf(top[n][i], __shfl_xor_sync(0xFFFFFFFFu, top[n][i], 16));
+                    // rounded up: no weight passes 2^kHeadroom
+                    top[n][i] = __fadd_ru(top[n][i], -kHeadroom);
                     grew |= top[n][i] > m[n][i];
                 }
             if (__any_sync(0xFFFFFFFFu, grew)) {

@@ -478,9 +478,11 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  *   scratch     device, 16-byte aligned, at least dg_attn_decode_scratch()
  *               bytes; need not be initialised, and holds nothing between
  *               calls.  Calls that may overlap in time need one each.
- * Weights enter the second product as FP16 relative to the row's largest
- * weight times value scale; everything else is FP32.  Results do not depend
- * on timing. */
+ * Weights enter the second product as FP16: 11 bits each, down to 2^-29 of
+ * the row's largest weight times value scale (2^-21 over a prefix of more
+ * than 32 rows per key head and a head_dim up to 128), below that an absolute
+ * 2^-40 (2^-32) of it; the sum that divides them is of the unrounded weights.
+ * Sums, maxima and exponentials are FP32.  Results do not depend on timing. */
 dg_status dg_attn_decode(const dg_heads* q, const dg_heads* out, float* lse, int batch, int q_len,
                          int q_heads, const dg_kv_cache* cache, const int32_t* page_table,
                          int64_t table_stride, int64_t max_pages, const int32_t* kv_lens,
