@@ -64,14 +64,17 @@ __device__ __forceinline__ uint32_t top_abs_bf16(uint4 w) {
 }
 
 // BF16 queries go to the MMA as FP16, which has more mantissa but less range:
-// a row is divided by the power of two at or below its largest magnitude
-// (given as BF16 bits), so that its largest value lies in [1, 2).
+// a row is divided by 2^-14 times the power of two at or below its largest
+// magnitude (given as BF16 bits), so that its largest value lies in [2^14,
+// 2^15) and FP16's whole range is below it: elements are exact down to 2^-32
+// of the largest, and zero only below 2^-40.  (Rows below 2^-112 are divided
+// by 2^-126: still exact.)
 struct PowerOfTwo {
     float value, inverse;
 };
-__device__ __forceinline__ PowerOfTwo power_below(uint32_t top_bf16) {
-    const int e = min(max(static_cast<int>(top_bf16 >> 7), 1), 253);   // biased exponent
-    return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
+__device__ __forceinline__ PowerOfTwo query_scale(uint32_t top_bf16) {
+    const int e = min(max(static_cast<int>(top_bf16 >> 7), 15), 254);   // biased exponent
+    return {__uint_as_float(static_cast<uint32_t>(e - 14) << 23), __uint_as_float(static_cast<uint32_t>(268 - e) << 23)};
 }
 __device__ __forceinline__ uint32_t bf16_to_half2(uint32_t v, float mul) {
     return f32x2_to_f16x2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);

@@ -548,7 +548,7 @@ attn_split_kernel(const AttnArgs a) {
                     for (int k = 0; k < D / 32; ++k) top = max(top, top_abs_bf16(w[n][k]));
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    const PowerOfTwo p = power_below(top);
+                    const PowerOfTwo p = query_scale(top);
                     mul = p.inverse;
                     factor *= p.value;
                 }
@@ -665,7 +665,8 @@ attn_split_kernel(const AttnArgs a) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float& y = s[q >> 1][n][2 * (q & 1) + i];
-                        y = fmaf(y * kk[q], qscale[n][i], lg[q]);
+                        // both factors first: the sum times a large one alone could pass FP32
+                        y = fmaf(y, kk[q] * qscale[n][i], lg[q]);
                     }
                     if (masked) {
 #pragma unroll

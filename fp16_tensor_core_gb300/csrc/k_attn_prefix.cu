@@ -191,8 +191,13 @@ struct PrefixShape {
     static constexpr int kSmem = kBarsAt + 256 + 1024;           // and alignment
 };
 
+// What BF16 queries are scaled up by (query_scale) leaves a score with the
+// key's scale, which is applied first, so that their product stays in FP32.
+template <bool kFp16>
+constexpr float kKeyFactor = kFp16 ? 1.0f : 0x1p-14f;
+
 // The keys' (or values') four warps: codes from the cache to swizzled FP16.
-template <int D, bool kValues>
+template <int D, bool kFp16, bool kValues>
 __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem, uint64_t* bars,
                                              const WaitCtl& ctl, int tile0, int tiles, int head) {
     using S = PrefixShape<D>;
@@ -285,7 +290,7 @@ __device__ __forceinline__ void convert_role(const PrefixArgs& a, uint8_t* smem,
             if constexpr (!kValues) {
                 float* f = factors + prefix::factor_slot(j) * 3 * 128 + factor_at;
                 const float safe = sv < 0x1p-100f ? 0x1p-100f : sv;
-                f[0] = sk;
+                f[0] = sk * kKeyFactor<kFp16>;
                 f[128] = sv == -1.0f ? -INFINITY : __log2f(safe);
                 f[256] = sv == -1.0f ? 0.0f : rcp(safe);
             }
@@ -384,9 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
                 uint32_t top = 0;
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) top = max(top, top_abs_bf16(w[k]));
-                const PowerOfTwo p = power_below(top);
+                const PowerOfTwo p = query_scale(top);
                 mul = p.inverse;
-                factor *= p.value;
+                factor *= p.value / kKeyFactor<kFp16>;
             }
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
@@ -619,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const PrefixAr
         // ---------------------------- codes to operands: keys, then values' warps
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvertRegs));
         if (warp < 12)
-            convert_role<D, false>(a, smem, bars, ctl, tile0, tiles, head);
+            convert_role<D, kFp16, false>(a, smem, bars, ctl, tile0, tiles, head);
         else
-            convert_role<D, true>(a, smem, bars, ctl, tile0, tiles, head);
+            convert_role<D, kFp16, true>(a, smem, bars, ctl, tile0, tiles, head);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kMmaRegs));
         if (warp == 16 && lane == 0) {

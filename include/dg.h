@@ -482,6 +482,8 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  * the row's largest weight times value scale (2^-21 over a prefix of more
  * than 32 rows per key head and a head_dim up to 128), below that an absolute
  * 2^-40 (2^-32) of it; the sum that divides them is of the unrounded weights.
+ * BF16 queries enter the first as FP16 scaled by a power of two: exact down to
+ * 2^-32 of the row's largest element, off by at most 2^-40 of it below.
  * Sums, maxima and exponentials are FP32.  Results do not depend on timing. */
 dg_status dg_attn_decode(const dg_heads* q, const dg_heads* out, float* lse, int batch, int q_len,
                          int q_heads, const dg_kv_cache* cache, const int32_t* page_table,
