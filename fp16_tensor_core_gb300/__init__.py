@@ -346,7 +346,8 @@ def _load_native():
         if _native is None:
             spec = importlib.util.spec_from_file_location("dg_python", _NATIVE_PATH)
             if spec is None or not os.path.exists(_NATIVE_PATH):
-                raise RuntimeError(f"{_NATIVE_PATH} not found; build it with the library")
+                raise RuntimeError(f"{_NATIVE_PATH} not found; build it with the library "
+                                   "(needs gcc and Python's headers)")
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             if _raw_stream is not None and _current_device is not None:

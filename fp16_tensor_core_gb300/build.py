@@ -2,7 +2,8 @@
 
 One translation unit per kernel family, compiled in parallel, then linked
 into ``fp16_tensor_core_gb300/_build/libdg.so`` against the shared CUDA
-runtime (the same one PyTorch loads).
+runtime (the same one PyTorch loads).  ``dg_python``, a small C module that
+reads the serving calls' arguments, is compiled with gcc and Python's headers.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -66,7 +68,22 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _native_missing() -> str:
+    """What the marshalling module needs and this machine lacks ("" if nothing)."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return f"Python.h (looked in {include})"
+    return "" if shutil.which("gcc") else "gcc"
+
+
 def _build_native(force: bool) -> None:
+    """dg_python, for the serving calls from Python.  libdg and everything
+    else need only nvcc: without a C compiler or Python's headers this is left
+    out with a warning, and the serving calls raise when they are made."""
+    missing = _native_missing()
+    if missing:
+        warnings.warn(f"{missing} not found: the serving calls cannot be made from Python")
+        return
     src = os.path.join(CSRC, "dg_python.c")
     deps = (src, os.path.join(INCLUDE, "dg.h"), __file__)
     if not force and os.path.exists(NATIVE) and all(
@@ -84,7 +101,6 @@ def _build_native(force: bool) -> None:
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile the CUDA sources and link libdg.so; return the library path."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    _build_native(force)
     if force:
         for s in SOURCES:
             o = os.path.join(OUT_DIR, os.path.splitext(s)[0] + ".o")
@@ -101,6 +117,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_native(force)
     return LIB
 
 
