@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sysconfig
 import threading
 
 import torch
@@ -51,7 +52,7 @@ EXPORTED_SYMBOLS = (
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libdg.so")
-_NATIVE_PATH = os.path.join(_HERE, "_build", "dg_python.so")
+_NATIVE_PATH = os.path.join(_HERE, "_build", "dg_python" + sysconfig.get_config_var("EXT_SUFFIX"))
 _lib = None
 _lock = threading.Lock()
 

@@ -20,7 +20,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdg.so")
-NATIVE = os.path.join(OUT_DIR, "dg_python.so")   # argument marshalling for Python
+# Argument marshalling for Python; the name carries the interpreter's ABI, so
+# that another interpreter builds and loads its own.
+NATIVE = os.path.join(OUT_DIR, "dg_python" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["dg_api.cu", "k_scale.cu", "k_gemv.cu", "k_gemv_mma.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu",
            "k_gemm_skinny.cu", "dg_static.cu", "k_kvcache.cu", "k_attn_decode.cu",

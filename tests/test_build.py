@@ -1,5 +1,6 @@
 """What the build needs of the machine: libdg only nvcc; the serving calls'
 marshalling module gcc and Python's headers.  CPU only."""
+import importlib.machinery
 import os
 
 import pytest
@@ -37,3 +38,10 @@ def test_errors_in_the_marshalling_module_are_errors(monkeypatch, tmp_path, else
     monkeypatch.setattr(dg_build, "CSRC", os.fspath(tmp_path))
     with pytest.raises(RuntimeError, match="gcc failed for dg_python.c"):
         dg_build._build_native(False)
+
+
+def test_another_interpreter_loads_its_own(elsewhere):
+    assert any(s != ".so" and elsewhere.endswith(s) for s in importlib.machinery.EXTENSION_SUFFIXES)
+    assert os.path.basename(dg._NATIVE_PATH) == os.path.basename(dg_build.NATIVE)
+    dg_build._build_native(False)
+    assert os.path.exists(elsewhere) and dg._load_native().__file__ == elsewhere
