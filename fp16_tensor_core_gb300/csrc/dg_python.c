@@ -110,8 +110,8 @@ static int get_heads(PyObject* t, const char* what, const heads_arg* like, heads
     void* data;
     if (on_device(t) < 0 || as_address(PyObject_CallMethodNoArgs(t, n_data_ptr), &data) < 0) return -1;
     h->c.data = data;
-    h->c.token_stride = stride[0];
-    h->c.head_stride = stride[1];
+    h->c.token_stride = h->shape[0] > 1 ? stride[0] : 0;   /* a single one's stride may be anything */
+    h->c.head_stride = h->shape[1] > 1 ? stride[1] : 0;
     return 0;
 }
 

@@ -46,3 +46,27 @@ def test_a_length_of_zero_is_no_prefix():
     for pages in (None, c.table[0], c.table[0, :0]):
         got = c.run(prefix_pages=pages, prefix_len=0)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_the_stride_of_a_single_token_or_head():
+    """A view of one row of a pitch that no second row could have."""
+    rows = torch.randn(5, 132, device="cuda").bfloat16()
+    one = rows[:, :128].view(5, 2, 64)[:1]
+    table = torch.empty(50, 32, 2, device="cuda")
+    dg.dg_rope_table(table)
+    rot, at = dg.DgRotary(table), torch.tensor([7], dtype=torch.int32, device="cuda")
+    want = torch.empty(1, 2, 64, dtype=one.dtype, device="cuda")
+    dg.dg_rope(one.contiguous(), want, at, rot)
+    before = rows.clone()
+    dg.dg_rope(one, one, at, rot)
+    assert torch.equal(one, want)
+    before[0, :128] = want.flatten()
+    assert torch.equal(rows, before)
+    x = torch.randn(5, 1, 64, device="cuda").half()
+    want, got = torch.empty_like(x), torch.zeros_like(x)
+    at = torch.arange(5, dtype=torch.int32, device="cuda")
+    dg.dg_rope(x, want, at, rot)
+    dg.dg_rope(x.as_strided((5, 1, 64), (64, 7, 1)), got.as_strided((5, 1, 64), (64, 3, 1)), at, rot)
+    assert torch.equal(got, want)
+    with pytest.raises(dg.DgError, match="MISALIGNED"):
+        dg.dg_rope(rows[:, :128].view(5, 2, 64), torch.empty(5, 2, 64, dtype=rows.dtype, device="cuda"), at, rot)
