@@ -217,9 +217,10 @@ cudaError_t launch_gemm_skinny(const TcLaunch& L, float* partials, uint32_t* cou
 void plan_skinny(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count, dg_plan* p);
 
 // Rotary positions and the E4M3 key/value cache (arguments already checked).
-// The smallest scale of a cached row: a row of zeros (or of values that no
-// 16-bit output could tell from zero) has a positive scale too, so that its
-// logarithm and reciprocal are finite.
+// The smallest scale of a cached row: a row of zeros has a positive scale too,
+// so that its logarithm and reciprocal are finite.  It costs BF16 rows their
+// smallest values: what lies below 2^-70 in a row of at most 448 * 2^-60 has
+// code 0.  (FP16 ends at 2^-24.)
 constexpr float kKvMinScale = 0x1p-60f;
 cudaError_t launch_rope_table(float* table, int64_t positions, int rotary_dim,
                               const dg_rope_scaling& sc, int sm_count, cudaStream_t s);

@@ -33,13 +33,20 @@
 // in token order: results do not depend on timing.
 //
 // Measured: 3 requests of up to 120001 tokens, 32/8 heads of 128: 85 us
-// (5.5 TB/s, 0.82 of a copy); 64 of up to 4099: 55 us (0.75).  The loop runs
+// (5.5 TB/s, 0.82 of a copy); 64 of up to 4099: 55 us (0.75).  Heads of 256:
+// 178 (0.77) and 111 (0.73).  The loop runs
 // at what HBM gives; the rest is the start (lengths, pages, first tiles: 5
 // us), the join (4), and SMs that end at different times: four groups of ten
 // SMs get an eighth less of the bandwidth than the others and end 8 us later,
 // always the same ones.  Runs handed out as warps become free would even that
 // out, but each piece more costs a state (as many bytes as a quarter of a
 // tile) to write and join, which takes the gain back.
+//
+// Units of 8 or 16 rows read and convert the cache once each, so many rows a
+// key head are this kernel's weak side: a prompt's own 2048 tokens as q_len
+// (32/8 heads of 128) 410 us, 0.04 of the tensor rate; 96 requests behind
+// 2000 and 12000 shared tokens with 256-wide heads, which the tcgen05 kernel
+// does not hold, 100 and 351 us (38 and 58 with heads of 128 there).
 #include <cuda_runtime.h>
 
 #include <algorithm>

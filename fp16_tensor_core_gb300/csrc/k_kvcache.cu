@@ -66,7 +66,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // table[p][i] = magnitude * (cos, sin)(p * f_i).  Everything up to the final
 // rounding is FP64: at p = 10^6 an FP32 angle would already be off by 0.06.
 // One block column per frequency, so that each thread forms its frequency
-// once and then walks over positions.
+// once and then walks over positions.  Bound by FP64 arithmetic, and in small
+// tables by the one pow of a thread: 8192 positions of 64 pairs 140 us (by
+// parts 163), 131072 of 64 601, 10^6 of 32 1900 (17 G entries/s; its bytes
+// would take 38).  A program makes its table once.
 __global__ void __launch_bounds__(256)
 rope_table_kernel(float2* __restrict__ table, int64_t positions, int half, dg_rope_scaling s) {
     pdl_wait();
@@ -384,12 +387,14 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int block) {
 
 constexpr int kAppendTokens = 2;   // of a lane group, in large calls
 
-// Every kv_every-th block writes the cache (bound by its instructions), the
+// Every kv_every-th block writes the cache (many instructions a load), the
 // others turn the queries (bound by HBM): dealt out among one another they
 // share the SMs.  16001 tokens of 32 + 8 + 8 heads of 128, half of each
 // turned, interleaved: 60.5 us, 6.0 TB/s, 0.89 of a copy; whole heads in the
-// half layout 61.7; 32 + 32 + 32 heads 145 (0.68: two thirds of it are cache
-// rows).  With 8 dims a lane and 4 tokens in flight 72, 80 and 220.  Four
+// half layout 61.9; 32 + 32 + 32 heads 146 in FP16 and 153 in BF16 (0.68 and
+// 0.64): two thirds of those are cache rows, whose warps wait for their loads
+// with 57% of the issue slots used and 28 warps an SM, so neither limit is
+// reached.  With 8 dims a lane and 4 tokens in flight 72, 80 and 220.  Four
 // blocks an SM, by the registers of the four query heads a thread holds; with
 // two heads and six blocks 65 us.
 template <bool kFp16, bool kHalf, int kLanes, bool kMany>

@@ -411,7 +411,8 @@ dg_status dg_rope(const dg_heads* x, const dg_heads* out, int64_t tokens, int he
  * code * scale, one scale per head of a token ([FP8-guide] §3.2's rule with
  * that as the tensor): scale = max(fl32(amax / 448), 2^-60), code =
  * E4M3(fl32(x / scale)) (§4.3).  The floor stands in for dg_amax's scale 1
- * of an all-zero tensor.  A row that holds a NaN or an infinity has scale
+ * of an all-zero tensor; with it, BF16 values below 2^-70 in a row no larger
+ * than 448 * 2^-60 have code 0.  A row that holds a NaN or an infinity has scale
  * NaN and codes 0, so codes are always finite.
  *   head_dim   a multiple of 16 up to 256 (dg_attn_decode: 64, 128 or 256)
  *   page_size  a power of two, 1 .. 65536
@@ -466,7 +467,14 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  *   batch       0 .. 2048; q_len >= 1; q_heads a multiple of kv_heads.
  *   page_table  int32, device: row b, at b * table_stride, names the pages of
  *               request b's tokens in order; max_pages entries a row,
- *               table_stride >= max_pages.
+ *               table_stride >= max_pages.  max_pages alone says, before the
+ *               lengths are read on the device, how long a request can be,
+ *               and so picks how the work is cut: a table far wider than its
+ *               longest request costs time (one of 300 tokens, 32 heads of
+ *               128: 6.8 us with max_pages for 320 or 1024 tokens, 7.9 for
+ *               4096, 10.9 for 16384 or 65536; 16 of 300, 32/8 heads: 7.2,
+ *               and 12.3 from 4096 on).  A caller that knows a bound passes
+ *               the columns it needs, with the wide table's table_stride.
  *   kv_lens     int32[batch], device, 0 .. max_pages * page_size each.  A
  *               length outside that counts as 0; queries that see a token
  *               on a page outside the cache get unspecified results (no
@@ -481,7 +489,8 @@ dg_status dg_kv_read(const dg_kv_cache* cache, const int32_t* slots, int64_t tok
  * Weights enter the second product as FP16: 11 bits each, down to 2^-29 of
  * the row's largest weight times value scale (2^-21 over a prefix of more
  * than 32 rows per key head and a head_dim up to 128), below that an absolute
- * 2^-40 (2^-32) of it; the sum that divides them is of the unrounded weights.
+ * 2^-40 (2^-32) of it; the sum that divides them is of the unrounded weights
+ * (where weight times value scale is below 2^-133 of the largest, of none).
  * BF16 queries enter the first as FP16 scaled by a power of two: exact down to
  * 2^-32 of the row's largest element, off by at most 2^-40 of it below.
  * Sums, maxima and exponentials are FP32.  Results do not depend on timing. */
