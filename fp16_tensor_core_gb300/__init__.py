@@ -29,6 +29,9 @@ __all__ = [
     "DG_ROPE_HALF", "DG_ROPE_INTERLEAVED", "DG_ROPE_UNSCALED", "DG_ROPE_LINEAR", "DG_ROPE_NTK",
     "DG_ROPE_BY_PARTS", "DgRotary", "DgKvCache", "dg_rope_table", "dg_rope", "dg_kv_append",
     "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch",
+    "DG_ACT_NONE", "DG_ACT_RELU", "DG_ACT_GELU", "DG_ACT_GELU_TANH", "DG_ACT_SILU", "dg_rmsnorm",
+    "dg_rmsnorm_e4m3", "dg_rmsnorm_e4m3_amax", "dg_rmsnorm_grad", "dg_rmsnorm_grad_scratch",
+    "dg_activate", "dg_activate_grad", "dg_activate_grad_scratch",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -36,6 +39,7 @@ DG_OK, DG_ERR_INVALID_VALUE, DG_ERR_MISALIGNED, DG_ERR_UNSUPPORTED, DG_ERR_CUDA,
 DG_BF16, DG_E4M3, DG_FP16 = 0, 1, 2
 DG_ROPE_HALF, DG_ROPE_INTERLEAVED = 0, 1
 DG_ROPE_UNSCALED, DG_ROPE_LINEAR, DG_ROPE_NTK, DG_ROPE_BY_PARTS = range(4)
+DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_GELU_TANH, DG_ACT_SILU = range(5)
 
 #: Every function include/dg.h declares.
 EXPORTED_SYMBOLS = (
@@ -47,7 +51,9 @@ EXPORTED_SYMBOLS = (
     "dg_status_string", "dg_version", "dg_release_stream", "dg_reload_env", "dg_convert_f16_amax",
     "dg_convert_f16_amax_pair", "dg_quantize_e4m3_pair",
     "dg_rope_table", "dg_rope", "dg_kv_append", "dg_kv_read", "dg_attn_decode",
-    "dg_attn_decode_scratch",
+    "dg_attn_decode_scratch", "dg_rmsnorm", "dg_rmsnorm_e4m3", "dg_rmsnorm_e4m3_amax",
+    "dg_rmsnorm_grad", "dg_rmsnorm_grad_scratch", "dg_activate", "dg_activate_grad",
+    "dg_activate_grad_scratch",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -86,6 +92,10 @@ class _RopeScaling(ctypes.Structure):
 class _Rotary(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int64),
                 ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
 class _KvCache(ctypes.Structure):
@@ -137,6 +147,16 @@ def lib():
             L.dg_attn_decode.argtypes = [heads, heads, vp, i32, i32, i32, cache, vp, i64, i64, vp, vp,
                                          i64, ctypes.c_double, i32, vp, i64, vp]
             L.dg_attn_decode_scratch.argtypes = [i32, i32, i32, i32, i64, i32, ctypes.POINTER(i64)]
+            rows, f64 = ctypes.POINTER(_Rows), ctypes.c_double
+            norm = [rows, rows, rows, vp, i64, i64, f64, i32]
+            L.dg_rmsnorm.argtypes = [*norm, rows, vp]
+            L.dg_rmsnorm_e4m3.argtypes = [*norm, vp, vp, vp]
+            L.dg_rmsnorm_e4m3_amax.argtypes = [*norm, vp, vp, vp, vp, vp]
+            L.dg_rmsnorm_grad.argtypes = [rows, vp, rows, rows, i64, i64, f64, i32, rows, vp, vp, i64, vp]
+            L.dg_rmsnorm_grad_scratch.argtypes = [i64, i64, i32, ctypes.POINTER(i64)]
+            L.dg_activate.argtypes = [rows, i32, i32, i64, i64, i32, rows, vp, vp, vp, vp, vp]
+            L.dg_activate_grad.argtypes = [rows, rows, vp, vp, i32, i32, i64, i64, i32, rows, vp, vp, i64, vp]
+            L.dg_activate_grad_scratch.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64)]
             L.dg_init.argtypes = []
             L.dg_sync_status.argtypes = [vp]
             L.dg_set_wait_timeout_us.argtypes = [ctypes.c_uint64]
@@ -155,7 +175,10 @@ def lib():
                          "dg_convert_f16", "dg_quantize_e4m3_amax", "dg_release_stream",
                          "dg_convert_f16_amax", "dg_convert_f16_amax_pair",
                          "dg_quantize_e4m3_pair", "dg_rope_table", "dg_rope", "dg_kv_append",
-                         "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch"):
+                         "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch", "dg_rmsnorm",
+                         "dg_rmsnorm_e4m3", "dg_rmsnorm_e4m3_amax", "dg_rmsnorm_grad",
+                         "dg_rmsnorm_grad_scratch", "dg_activate", "dg_activate_grad",
+                         "dg_activate_grad_scratch"):
                 getattr(L, name).restype = st
             _lib = L
     return _lib
@@ -336,7 +359,8 @@ def dg_convert_f16_amax_pair(a, b, out_a, out_b, factor, amax_a, amax_b, stream=
                                           _stream(stream)), "dg_convert_f16_amax_pair")
 
 
-# The serving calls' arguments are read natively: see csrc/dg_python.c.
+# The arguments of the serving calls and of those around a layer's products
+# are read natively: see csrc/dg_python.c.
 _native = None
 
 
@@ -358,6 +382,10 @@ def _load_native():
             module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (L.dg_rope, L.dg_kv_append, L.dg_kv_read, L.dg_attn_decode)),
                         torch.bfloat16, torch.float16, torch.int32, torch.float32, stream, device, _check)
+            module.bind_layer(*(ctypes.cast(f, ctypes.c_void_p).value
+                                for f in (L.dg_rmsnorm, L.dg_rmsnorm_e4m3, L.dg_rmsnorm_e4m3_amax,
+                                          L.dg_rmsnorm_grad, L.dg_activate, L.dg_activate_grad)),
+                              torch.uint8)
             _native = module
     return _native
 
@@ -437,6 +465,56 @@ def dg_attn_decode(q, out, cache, page_table, kv_lens, scratch, scale=None, lse=
     that the whole batch shares (prefix_pages and prefix_len, given together)."""
     (_native or _load_native()).attn_decode(q, out, cache, page_table, kv_lens, scratch, scale, lse,
                                             prefix_pages, prefix_len, stream)
+
+
+def dg_rmsnorm(x, y, weight=None, residual=None, sum=None, eps=1e-6, stream=None) -> None:
+    """y = norm(x + residual) * weight on rows [rows, cols]; sum receives x + residual."""
+    (_native or _load_native()).rmsnorm(x, y, weight, residual, sum, eps, stream)
+
+
+def dg_rmsnorm_e4m3(x, q, row_scale, weight=None, residual=None, sum=None, eps=1e-6, stream=None) -> None:
+    """dg_rmsnorm with E4M3 codes (uint8) and an FP32 scale per row in place of y."""
+    (_native or _load_native()).rmsnorm_e4m3(x, q, row_scale, weight, residual, sum, eps, stream)
+
+
+def dg_rmsnorm_e4m3_amax(x, scale, q, amax_out, next_scale_out=None, weight=None, residual=None, sum=None,
+                         eps=1e-6, stream=None) -> None:
+    """dg_rmsnorm with codes E4M3(y / scale[0]); amax_out[0] = max |y| and
+    optionally next_scale_out[0] = amax / 448 for the next call (delayed scaling)."""
+    (_native or _load_native()).rmsnorm_e4m3_amax(x, scale, q, amax_out, next_scale_out, weight, residual, sum,
+                                                  eps, stream)
+
+
+def dg_rmsnorm_grad_scratch(rows, cols, sm_count=0) -> int:
+    """Bytes of scratch dg_rmsnorm_grad needs for dweight."""
+    n = ctypes.c_int64()
+    _check(lib().dg_rmsnorm_grad_scratch(rows, cols, sm_count, ctypes.byref(n)), "dg_rmsnorm_grad_scratch")
+    return n.value
+
+
+def dg_rmsnorm_grad(s, dy, dx, weight=None, dsum=None, dweight=None, scratch=None, eps=1e-6, stream=None) -> None:
+    """dx (of x and residual alike, plus dsum) and FP32 dweight of dg_rmsnorm, from s = x + residual."""
+    (_native or _load_native()).rmsnorm_grad(s, dy, dx, weight, dsum, dweight, scratch, eps, stream)
+
+
+def dg_activate(x, act, y=None, q=None, q_scale=None, x_q=None, x_scale=None, gated=False, stream=None) -> None:
+    """act(x), or act(gate) * up of x = [gate, up], as y and/or as E4M3 codes q with a
+    scale per row; x_q and x_scale [rows, 1 or 2] receive an 8-bit checkpoint of x."""
+    (_native or _load_native()).activate(x, act, y, q, q_scale, x_q, x_scale, gated, stream)
+
+
+def dg_activate_grad_scratch(rows, cols, gated=False, sm_count=0) -> int:
+    """Bytes of scratch dg_activate_grad needs for dbias (cols: of dy)."""
+    n = ctypes.c_int64()
+    _check(lib().dg_activate_grad_scratch(rows, cols, 1 if gated else 0, sm_count, ctypes.byref(n)),
+           "dg_activate_grad_scratch")
+    return n.value
+
+
+def dg_activate_grad(dy, act, dx, x=None, x_q=None, x_scale=None, gated=False, dbias=None, scratch=None,
+                     stream=None) -> None:
+    """dx of dg_activate from its input x or the checkpoint x_q, x_scale; dbias (FP32) = column sums of dx."""
+    (_native or _load_native()).activate_grad(dy, act, dx, x, x_q, x_scale, gated, dbias, scratch, stream)
 
 
 def dg_gemm_plan(M, N, K, in_dtype=DG_E4M3, out_dtype=DG_BF16, sm_count=0) -> dict:

@@ -26,8 +26,9 @@ NATIVE = os.path.join(OUT_DIR, "dg_python" + sysconfig.get_config_var("EXT_SUFFI
 
 SOURCES = ["dg_api.cu", "k_scale.cu", "k_gemv.cu", "k_gemv_mma.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu",
            "k_gemm_skinny.cu", "dg_static.cu", "k_kvcache.cu", "k_attn_decode.cu",
-           "k_attn_prefix.cu"]
-HEADERS = ["dg_ptx.cuh", "dg_internal.h", "gemm_common.cuh", "attn_common.cuh", "prefix_barriers.h"]
+           "k_attn_prefix.cu", "k_norm.cu", "k_activate.cu"]
+HEADERS = ["dg_ptx.cuh", "dg_internal.h", "gemm_common.cuh", "attn_common.cuh", "prefix_barriers.h",
+           "activation.cuh", "row_common.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

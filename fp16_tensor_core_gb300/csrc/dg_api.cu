@@ -1008,6 +1008,272 @@ dg_status dg_attn_decode(const dg_heads* q, const dg_heads* out, float* lse, int
     return from_cuda(launch_attn_decode(L, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+dg_status check_rows(const dg_rows* r) {
+    if (r == nullptr || r->data == nullptr || r->stride < 0) return DG_ERR_INVALID_VALUE;
+    return aligned16(r->data) && r->stride % 8 == 0 ? DG_OK : DG_ERR_MISALIGNED;
+}
+
+// An optional view.
+dg_status check_rows_or_null(const dg_rows* r) { return r == nullptr ? DG_OK : check_rows(r); }
+
+dg_status check_row_sizes(int64_t rows, int64_t cols) {
+    if (rows < 0 || rows > INT_MAX || cols < 1 || cols > kMaxRowElements) return DG_ERR_INVALID_VALUE;
+    return cols % 8 == 0 ? DG_OK : DG_ERR_MISALIGNED;
+}
+
+// Rows that are written lie apart.
+bool own_rows(const dg_rows* r, int64_t rows, int64_t cols) { return rows <= 1 || r->stride >= cols; }
+
+// The smallest eps that FP32 holds as a normal number: zero rows stay finite.
+bool good_eps(double eps) { return eps >= 0x1p-126 && eps <= 3.0e38; }
+
+dg_status check_activation(dg_activation a) {
+    return a == DG_ACT_NONE || a == DG_ACT_RELU || a == DG_ACT_GELU || a == DG_ACT_GELU_TANH || a == DG_ACT_SILU
+               ? DG_OK
+               : DG_ERR_INVALID_VALUE;
+}
+
+uint16_t* elements(const dg_rows* r) { return r == nullptr ? nullptr : static_cast<uint16_t*>(r->data); }
+int64_t stride_of(const dg_rows* r) { return r == nullptr ? 0 : r->stride; }
+
+// Arguments that every form of the norm has; the sizes first, so that an
+// empty call needs no pointers.
+dg_status check_norm(const dg_rows* x, const dg_rows* residual, const dg_rows* sum, const void* weight,
+                     int64_t rows, int64_t cols, double eps, dg_dtype dtype) {
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_row_sizes(rows, cols);
+    if (rc != DG_OK) return rc;
+    if (!good_eps(eps)) return DG_ERR_INVALID_VALUE;
+    if (rows == 0) return DG_OK;
+    rc = check_rows(x);
+    if (rc == DG_OK) rc = check_rows_or_null(residual);
+    if (rc == DG_OK) rc = check_rows_or_null(sum);
+    if (rc != DG_OK) return rc;
+    if (sum != nullptr && !own_rows(sum, rows, cols)) return DG_ERR_INVALID_VALUE;
+    return aligned16(weight) ? DG_OK : DG_ERR_MISALIGNED;
+}
+
+NormArgs norm_args(const dg_rows* x, const dg_rows* residual, const dg_rows* sum, const void* weight,
+                   int64_t rows, int64_t cols, double eps) {
+    NormArgs a{};
+    a.x = elements(x);
+    a.x_stride = stride_of(x);
+    a.residual = elements(residual);
+    a.residual_stride = stride_of(residual);
+    a.sum = elements(sum);
+    a.sum_stride = stride_of(sum);
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.rows = rows;
+    a.cols = static_cast<int>(cols);
+    a.eps = static_cast<float>(eps);
+    return a;
+}
+
+// SMs to size a scratch for: given, or the current device's.
+dg_status sms_or_current(int* sm_count) {
+    if (*sm_count > 0) return DG_OK;
+    DeviceState* st = nullptr;
+    const dg_status rc = current_device_state(&st);
+    if (rc == DG_OK) *sm_count = st->sm_count;
+    return rc;
+}
+
+}  // namespace
+
+dg_status dg_rmsnorm(const dg_rows* x, const dg_rows* residual, const dg_rows* sum, const void* weight,
+                     int64_t rows, int64_t cols, double eps, dg_dtype dtype, const dg_rows* y,
+                     dg_stream_t stream) {
+    dg_status rc = check_norm(x, residual, sum, weight, rows, cols, eps, dtype);
+    if (rc != DG_OK || rows == 0) return rc;
+    rc = check_rows(y);
+    if (rc != DG_OK) return rc;
+    if (!own_rows(y, rows, cols) || (sum != nullptr && sum->data == y->data)) return DG_ERR_INVALID_VALUE;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    NormArgs a = norm_args(x, residual, sum, weight, rows, cols, eps);
+    a.y = elements(y);
+    a.y_stride = y->stride;
+    return from_cuda(launch_rmsnorm(a, kNormHalf, dtype == DG_FP16, nullptr, st->sm_count,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_rmsnorm_e4m3(const dg_rows* x, const dg_rows* residual, const dg_rows* sum, const void* weight,
+                          int64_t rows, int64_t cols, double eps, dg_dtype dtype, uint8_t* q,
+                          float* row_scale, dg_stream_t stream) {
+    dg_status rc = check_norm(x, residual, sum, weight, rows, cols, eps, dtype);
+    if (rc != DG_OK || rows == 0) return rc;
+    if (q == nullptr || row_scale == nullptr) return DG_ERR_INVALID_VALUE;
+    if (!aligned16(q) || !aligned4(row_scale)) return DG_ERR_MISALIGNED;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    NormArgs a = norm_args(x, residual, sum, weight, rows, cols, eps);
+    a.q = q;
+    a.row_scale = row_scale;
+    return from_cuda(launch_rmsnorm(a, kNormRows, dtype == DG_FP16, nullptr, st->sm_count,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_rmsnorm_e4m3_amax(const dg_rows* x, const dg_rows* residual, const dg_rows* sum,
+                               const void* weight, int64_t rows, int64_t cols, double eps, dg_dtype dtype,
+                               const float* scale, uint8_t* q, float* amax_out, float* next_scale_out,
+                               dg_stream_t stream) {
+    dg_status rc = check_norm(x, residual, sum, weight, rows, cols, eps, dtype);
+    if (rc != DG_OK) return rc;
+    if (scale == nullptr || amax_out == nullptr || (rows > 0 && q == nullptr)) return DG_ERR_INVALID_VALUE;
+    if (!aligned16(q) || !aligned4(scale) || !aligned4(amax_out) || !aligned4(next_scale_out))
+        return DG_ERR_MISALIGNED;
+    if (amax_out == scale || amax_out == next_scale_out) return DG_ERR_INVALID_VALUE;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    NormArgs a = norm_args(x, residual, sum, weight, rows, cols, eps);
+    a.q = q;
+    a.scale = scale;
+    a.amax_bits = reinterpret_cast<uint32_t*>(amax_out);
+    return from_cuda(launch_rmsnorm(a, kNormTensor, dtype == DG_FP16, next_scale_out, st->sm_count,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_rmsnorm_grad_scratch(int64_t rows, int64_t cols, int sm_count, int64_t* bytes) {
+    if (bytes == nullptr) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_row_sizes(rows, cols);
+    if (rc == DG_OK) rc = sms_or_current(&sm_count);
+    if (rc == DG_OK) *bytes = rmsnorm_grad_scratch_bytes(rows, static_cast<int>(cols), sm_count);
+    return rc;
+}
+
+dg_status dg_rmsnorm_grad(const dg_rows* s, const void* weight, const dg_rows* dy, const dg_rows* dsum,
+                          int64_t rows, int64_t cols, double eps, dg_dtype dtype, const dg_rows* dx,
+                          float* dweight, void* scratch, int64_t scratch_bytes, dg_stream_t stream) {
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_row_sizes(rows, cols);
+    if (rc != DG_OK) return rc;
+    if (!good_eps(eps)) return DG_ERR_INVALID_VALUE;
+    if (rows > 0) {
+        rc = check_rows(s);
+        if (rc == DG_OK) rc = check_rows(dy);
+        if (rc == DG_OK) rc = check_rows_or_null(dsum);
+        if (rc == DG_OK) rc = check_rows(dx);
+        if (rc != DG_OK) return rc;
+        if (!own_rows(dx, rows, cols) || (dweight != nullptr && scratch == nullptr)) return DG_ERR_INVALID_VALUE;
+    }
+    if (!aligned16(weight) || !aligned16(dweight) || !aligned16(scratch)) return DG_ERR_MISALIGNED;
+    if (rows == 0 && dweight == nullptr) return DG_OK;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    if (dweight != nullptr &&
+        scratch_bytes < rmsnorm_grad_scratch_bytes(rows, static_cast<int>(cols), st->sm_count))
+        return DG_ERR_INVALID_VALUE;
+    NormGradArgs a{};
+    a.x = elements(s);
+    a.x_stride = stride_of(s);
+    a.dy = elements(dy);
+    a.dy_stride = stride_of(dy);
+    a.dsum = elements(dsum);
+    a.dsum_stride = stride_of(dsum);
+    a.dx = elements(dx);
+    a.dx_stride = stride_of(dx);
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.rows = rows;
+    a.cols = static_cast<int>(cols);
+    a.eps = static_cast<float>(eps);
+    a.partials = dweight != nullptr ? static_cast<float*>(scratch) : nullptr;
+    return from_cuda(launch_rmsnorm_grad(a, dtype == DG_FP16, dweight, st->sm_count,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_activate(const dg_rows* x, int gated, dg_activation act, int64_t rows, int64_t cols,
+                      dg_dtype dtype, const dg_rows* y, uint8_t* q, float* q_scale, uint8_t* x_q,
+                      float* x_scale, dg_stream_t stream) {
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_row_sizes(rows, cols);
+    if (rc == DG_OK) rc = check_activation(act);
+    if (rc != DG_OK) return rc;
+    if ((q == nullptr) != (q_scale == nullptr) || (x_q == nullptr) != (x_scale == nullptr))
+        return DG_ERR_INVALID_VALUE;
+    if (rows == 0 || (y == nullptr && q == nullptr && x_q == nullptr)) return DG_OK;
+    rc = check_rows(x);
+    if (rc == DG_OK) rc = check_rows_or_null(y);
+    if (rc != DG_OK) return rc;
+    if (y != nullptr && (!own_rows(y, rows, cols) || (gated != 0 && y->data == x->data)))
+        return DG_ERR_INVALID_VALUE;
+    if (!aligned16(q) || !aligned16(x_q) || !aligned4(q_scale) || !aligned4(x_scale)) return DG_ERR_MISALIGNED;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    ActArgs a{};
+    a.x = elements(x);
+    a.x_stride = x->stride;
+    a.y = elements(y);
+    a.y_stride = stride_of(y);
+    a.rows = rows;
+    a.cols = static_cast<int>(cols);
+    a.gated = gated != 0;
+    a.act = act;
+    a.q = q;
+    a.q_scale = q_scale;
+    a.x_q = x_q;
+    a.x_scale = x_scale;
+    return from_cuda(launch_activate(a, dtype == DG_FP16, st->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_activate_grad_scratch(int64_t rows, int64_t cols, int gated, int sm_count, int64_t* bytes) {
+    if (bytes == nullptr) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_row_sizes(rows, cols);
+    if (rc == DG_OK) rc = sms_or_current(&sm_count);
+    if (rc == DG_OK) *bytes = activate_grad_scratch_bytes(rows, static_cast<int>(cols), gated != 0, sm_count);
+    return rc;
+}
+
+dg_status dg_activate_grad(const dg_rows* dy, const dg_rows* x, const uint8_t* x_q, const float* x_scale,
+                           int gated, dg_activation act, int64_t rows, int64_t cols, dg_dtype dtype,
+                           const dg_rows* dx, float* dbias, void* scratch, int64_t scratch_bytes,
+                           dg_stream_t stream) {
+    dg_status rc = check_16bit(dtype);
+    if (rc == DG_OK) rc = check_row_sizes(rows, cols);
+    if (rc == DG_OK) rc = check_activation(act);
+    if (rc != DG_OK) return rc;
+    if ((x_q == nullptr) != (x_scale == nullptr) || (x != nullptr && x_q != nullptr)) return DG_ERR_INVALID_VALUE;
+    if (rows > 0) {
+        rc = check_rows(dy);
+        if (rc == DG_OK) rc = check_rows_or_null(x);
+        if (rc == DG_OK) rc = check_rows(dx);
+        if (rc != DG_OK) return rc;
+        if ((x == nullptr && x_q == nullptr) || !own_rows(dx, rows, gated != 0 ? 2 * cols : cols) ||
+            (gated != 0 && dx->data == dy->data) || (dbias != nullptr && scratch == nullptr))
+            return DG_ERR_INVALID_VALUE;
+    }
+    if (!aligned16(x_q) || !aligned4(x_scale) || !aligned16(dbias) || !aligned16(scratch)) return DG_ERR_MISALIGNED;
+    if (rows == 0 && dbias == nullptr) return DG_OK;
+    DeviceState* st = nullptr;
+    rc = current_device_state(&st);
+    if (rc != DG_OK) return rc;
+    if (dbias != nullptr &&
+        scratch_bytes < activate_grad_scratch_bytes(rows, static_cast<int>(cols), gated != 0, st->sm_count))
+        return DG_ERR_INVALID_VALUE;
+    ActGradArgs a{};
+    a.dy = elements(dy);
+    a.dy_stride = stride_of(dy);
+    a.x = elements(x);
+    a.x_stride = stride_of(x);
+    a.x_q = x_q;
+    a.x_scale = x_scale;
+    a.dx = elements(dx);
+    a.dx_stride = stride_of(dx);
+    a.rows = rows;
+    a.cols = static_cast<int>(cols);
+    a.gated = gated != 0;
+    a.act = act;
+    a.partials = dbias != nullptr ? static_cast<float*>(scratch) : nullptr;
+    return from_cuda(launch_activate_grad(a, dtype == DG_FP16, dbias, st->sm_count,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
 dg_status dg_gemm_plan(int64_t M, int64_t N, int64_t K, dg_dtype in, dg_dtype out,
                        int sm_count, dg_plan* plan) {
     if (plan == nullptr) return DG_ERR_INVALID_VALUE;

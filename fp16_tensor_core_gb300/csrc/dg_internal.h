@@ -271,6 +271,71 @@ int64_t attn_slot_floats(int sm_count, int head_dim);
 int64_t attn_scratch_bytes(int batch, int q_len, int q_heads, int head_dim, int64_t prefix_len,
                            int sm_count);
 
+// Norm and activation of rows (arguments already checked).
+// A row's scale is at least this: its reciprocal is finite.
+constexpr float kRowMinScale = 0x1p-120f;
+constexpr int kMaxRowElements = 32768;   // a block holds a row in registers
+enum NormOut : int { kNormHalf = 0, kNormRows = 1, kNormTensor = 2 };
+struct NormArgs {
+    const uint16_t* x;
+    const uint16_t* residual;   // or null
+    uint16_t* sum;              // or null
+    const uint16_t* weight;     // or null: ones
+    int64_t x_stride, residual_stride, sum_stride, y_stride;
+    int64_t rows;
+    int cols;
+    float eps;
+    uint16_t* y;           // kNormHalf
+    uint8_t* q;            // kNormRows, kNormTensor
+    float* row_scale;      // kNormRows
+    const float* scale;    // kNormTensor
+    uint32_t* amax_bits;   // kNormTensor
+};
+cudaError_t launch_rmsnorm(const NormArgs& a, int out, bool fp16, float* next_scale, int sm_count, cudaStream_t s);
+struct NormGradArgs {
+    const uint16_t* x;
+    const uint16_t* dy;
+    const uint16_t* dsum;     // or null
+    const uint16_t* weight;   // or null: ones
+    uint16_t* dx;
+    int64_t x_stride, dy_stride, dsum_stride, dx_stride;
+    int64_t rows;
+    int cols;
+    float eps;
+    float* partials;          // [blocks][cols], or null
+};
+int64_t rmsnorm_grad_scratch_bytes(int64_t rows, int cols, int sm_count);
+cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool fp16, float* dweight, int sm_count, cudaStream_t s);
+struct ActArgs {
+    const uint16_t* x;
+    int64_t x_stride, y_stride;
+    int64_t rows;
+    int cols;              // of the output
+    bool gated;
+    int act;
+    uint16_t* y;           // or null
+    uint8_t* q;            // with q_scale, or null
+    float* q_scale;
+    uint8_t* x_q;          // with x_scale, or null
+    float* x_scale;
+};
+cudaError_t launch_activate(const ActArgs& a, bool fp16, int sm_count, cudaStream_t s);
+struct ActGradArgs {
+    const uint16_t* dy;
+    const uint16_t* x;     // or null: x_q and x_scale
+    const uint8_t* x_q;
+    const float* x_scale;
+    uint16_t* dx;
+    int64_t dy_stride, x_stride, dx_stride;
+    int64_t rows;
+    int cols;
+    bool gated;
+    int act;
+    float* partials;       // [runs][columns of dx], or null
+};
+int64_t activate_grad_scratch_bytes(int64_t rows, int cols, bool gated, int sm_count);
+cudaError_t launch_activate_grad(const ActGradArgs& a, bool fp16, float* dbias, int sm_count, cudaStream_t s);
+
 // Tile table for the tensor-core path (fills block_n, stages, smem, grid).
 void plan_tc(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count,
              dg_plan* p);

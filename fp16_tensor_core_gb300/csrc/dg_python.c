@@ -1,5 +1,6 @@
 /* dg_python.c -- argument marshalling of the serving entry points (rotary
- * positions, cache writes and reads, attention) for Python.
+ * positions, cache writes and reads, attention) and of those around a layer's
+ * products (norm, activation) for Python.
  *
  * A decode step makes these calls for every layer and token, with kernels of
  * 2 to 10 us: read attribute by attribute in Python and handed over through
@@ -27,7 +28,21 @@ static dg_status (*lib_kv_read)(const dg_kv_cache*, const int32_t*, int64_t, con
 static dg_status (*lib_attn_decode)(const dg_heads*, const dg_heads*, float*, int, int, int, const dg_kv_cache*,
                                     const int32_t*, int64_t, int64_t, const int32_t*, const int32_t*, int64_t,
                                     double, dg_dtype, void*, int64_t, dg_stream_t);
-static PyObject *type_bf16, *type_fp16, *type_int32, *type_float32;   /* torch.dtype objects */
+static dg_status (*lib_rmsnorm)(const dg_rows*, const dg_rows*, const dg_rows*, const void*, int64_t, int64_t,
+                                double, dg_dtype, const dg_rows*, dg_stream_t);
+static dg_status (*lib_rmsnorm_e4m3)(const dg_rows*, const dg_rows*, const dg_rows*, const void*, int64_t, int64_t,
+                                     double, dg_dtype, uint8_t*, float*, dg_stream_t);
+static dg_status (*lib_rmsnorm_e4m3_amax)(const dg_rows*, const dg_rows*, const dg_rows*, const void*, int64_t,
+                                          int64_t, double, dg_dtype, const float*, uint8_t*, float*, float*,
+                                          dg_stream_t);
+static dg_status (*lib_rmsnorm_grad)(const dg_rows*, const void*, const dg_rows*, const dg_rows*, int64_t, int64_t,
+                                     double, dg_dtype, const dg_rows*, float*, void*, int64_t, dg_stream_t);
+static dg_status (*lib_activate)(const dg_rows*, int, dg_activation, int64_t, int64_t, dg_dtype, const dg_rows*,
+                                 uint8_t*, float*, uint8_t*, float*, dg_stream_t);
+static dg_status (*lib_activate_grad)(const dg_rows*, const dg_rows*, const uint8_t*, const float*, int,
+                                      dg_activation, int64_t, int64_t, dg_dtype, const dg_rows*, float*, void*,
+                                      int64_t, dg_stream_t);
+static PyObject *type_bf16, *type_fp16, *type_int32, *type_float32, *type_uint8;   /* torch.dtype objects */
 static PyObject *current_stream;   /* (device) -> handle of its current stream */
 static PyObject *current_device;   /* () -> index */
 static PyObject *check;            /* (status, name): raises unless DG_OK */
@@ -134,6 +149,57 @@ static int get_array(PyObject* t, PyObject* type, const char* type_name, int64_t
         return -1;
     }
     return get_data(t, out);
+}
+
+/* The same, or NULL for None. */
+static int get_optional(PyObject* t, PyObject* type, const char* type_name, int64_t n, const char* what, void** out) {
+    *out = NULL;
+    return t == Py_None ? 0 : get_array(t, type, type_name, n, what, out);
+}
+
+typedef struct {
+    dg_rows c;
+    int64_t shape[2];
+    dg_dtype type;
+} rows_arg;
+
+/* [rows, columns] BF16 or FP16, any row stride; with `like`, of its type and
+ * rows and (cols >= 0) this many columns. */
+static int get_rows(PyObject* t, const char* what, const rows_arg* like, int64_t cols, rows_arg* r) {
+    static const char kWanted[] = "must be BF16 or FP16 [rows, columns] with contiguous rows";
+    int64_t stride[2];
+    if (numbers(PyObject_CallMethodNoArgs(t, n_stride), 2, stride, what, kWanted) < 0 ||
+        numbers(PyObject_GetAttr(t, n_shape), 2, r->shape, what, kWanted) < 0)
+        return -1;
+    PyObject* type = PyObject_GetAttr(t, n_dtype);
+    if (type == NULL) return -1;
+    const int bf16 = type == type_bf16, fp16 = type == type_fp16;
+    Py_DECREF(type);
+    if (!(bf16 || fp16) || (stride[1] != 1 && r->shape[1] > 1)) return fail_about(what, kWanted);
+    r->type = bf16 ? DG_BF16 : DG_FP16;
+    if (like != NULL && (r->type != like->type || r->shape[0] != like->shape[0] || (cols >= 0 && r->shape[1] != cols)))
+        return fail_about(what, "must have the shape and type of its counterpart");
+    void* data;
+    if (on_device(t) < 0 || as_address(PyObject_CallMethodNoArgs(t, n_data_ptr), &data) < 0) return -1;
+    r->c.data = data;
+    r->c.stride = r->shape[0] > 1 ? stride[0] : r->shape[1];   /* a single one's stride may be anything */
+    return 0;
+}
+/* The same, or no view (*c NULL) for None. */
+static int get_rows_or_none(PyObject* t, const char* what, const rows_arg* like, int64_t cols, rows_arg* r,
+                            const dg_rows** c) {
+    *c = NULL;
+    if (t == Py_None) return 0;
+    *c = &r->c;
+    return get_rows(t, what, like, cols, r);
+}
+
+/* A contiguous tensor's address and bytes, or NULL and 0 for None. */
+static int get_scratch(PyObject* t, void** data, int64_t* bytes) {
+    *data = NULL;
+    *bytes = 0;
+    if (t == Py_None) return 0;
+    return get_data(t, data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), bytes) < 0 ? -1 : 0;
 }
 
 /* The struct that a DgRotary or DgKvCache holds. */
@@ -315,6 +381,196 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
     return done(status, "dg_attn_decode");
 }
 
+/* What every norm takes: x, weight, residual, sum, eps. */
+typedef struct {
+    rows_arg x, residual, sum;
+    const dg_rows *r, *s;
+    void* weight;
+    double eps;
+} norm_arg;
+
+static int get_norm(PyObject* x, PyObject* weight, PyObject* residual, PyObject* sum, PyObject* eps, norm_arg* n) {
+    if (get_rows(x, "x", NULL, -1, &n->x) < 0 ||
+        get_rows_or_none(residual, "residual", &n->x, n->x.shape[1], &n->residual, &n->r) < 0 ||
+        get_rows_or_none(sum, "sum", &n->x, n->x.shape[1], &n->sum, &n->s) < 0 ||
+        get_optional(weight, n->x.type == DG_BF16 ? type_bf16 : type_fp16, "of x's type", n->x.shape[1], "weight",
+                     &n->weight) < 0)
+        return -1;
+    n->eps = PyFloat_AsDouble(eps);
+    return n->eps == -1.0 && PyErr_Occurred() ? -1 : 0;
+}
+
+/* (x, y, weight, residual, sum, eps, stream) */
+static PyObject* py_rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    norm_arg m;
+    rows_arg y;
+    dg_stream_t stream;
+    (void)self;
+    if (want_args(n, 7) < 0 || get_norm(a[0], a[2], a[3], a[4], a[5], &m) < 0 ||
+        get_rows(a[1], "y", &m.x, m.x.shape[1], &y) < 0 || get_stream(a[6], &stream) < 0)
+        return NULL;
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lib_rmsnorm(&m.x.c, m.r, m.s, m.weight, m.x.shape[0], m.x.shape[1], m.eps, m.x.type, &y.c, stream);
+    Py_END_ALLOW_THREADS
+    return done(status, "dg_rmsnorm");
+}
+
+/* (x, q, row_scale, weight, residual, sum, eps, stream) */
+static PyObject* py_rmsnorm_e4m3(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    norm_arg m;
+    void *q, *scale;
+    dg_stream_t stream;
+    (void)self;
+    if (want_args(n, 8) < 0 || get_norm(a[0], a[3], a[4], a[5], a[6], &m) < 0 ||
+        get_array(a[1], type_uint8, "uint8", m.x.shape[0] * m.x.shape[1], "q", &q) < 0 ||
+        get_array(a[2], type_float32, "FP32", m.x.shape[0], "row_scale", &scale) < 0 || get_stream(a[7], &stream) < 0)
+        return NULL;
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lib_rmsnorm_e4m3(&m.x.c, m.r, m.s, m.weight, m.x.shape[0], m.x.shape[1], m.eps, m.x.type, q, scale,
+                              stream);
+    Py_END_ALLOW_THREADS
+    return done(status, "dg_rmsnorm_e4m3");
+}
+
+/* (x, scale, q, amax_out, next_scale_out, weight, residual, sum, eps, stream) */
+static PyObject* py_rmsnorm_e4m3_amax(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    norm_arg m;
+    void *scale, *q, *amax, *next;
+    dg_stream_t stream;
+    (void)self;
+    if (want_args(n, 10) < 0 || get_norm(a[0], a[5], a[6], a[7], a[8], &m) < 0 ||
+        get_array(a[1], type_float32, "FP32", 1, "scale", &scale) < 0 ||
+        get_array(a[2], type_uint8, "uint8", m.x.shape[0] * m.x.shape[1], "q", &q) < 0 ||
+        get_array(a[3], type_float32, "FP32", 1, "amax_out", &amax) < 0 ||
+        get_optional(a[4], type_float32, "FP32", 1, "next_scale_out", &next) < 0 || get_stream(a[9], &stream) < 0)
+        return NULL;
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lib_rmsnorm_e4m3_amax(&m.x.c, m.r, m.s, m.weight, m.x.shape[0], m.x.shape[1], m.eps, m.x.type, scale, q,
+                                   amax, next, stream);
+    Py_END_ALLOW_THREADS
+    return done(status, "dg_rmsnorm_e4m3_amax");
+}
+
+/* (s, dy, dx, weight, dsum, dweight, scratch, eps, stream) */
+static PyObject* py_rmsnorm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    norm_arg m;
+    rows_arg dy, dx, dsum;
+    const dg_rows* extra;
+    void *dweight, *scratch;
+    int64_t bytes;
+    dg_stream_t stream;
+    (void)self;
+    if (want_args(n, 9) < 0 || get_norm(a[0], a[3], Py_None, Py_None, a[7], &m) < 0) return NULL;
+    const int64_t cols = m.x.shape[1];
+    if (get_rows(a[1], "dy", &m.x, cols, &dy) < 0 || get_rows(a[2], "dx", &m.x, cols, &dx) < 0 ||
+        get_rows_or_none(a[4], "dsum", &m.x, cols, &dsum, &extra) < 0 ||
+        get_optional(a[5], type_float32, "FP32", cols, "dweight", &dweight) < 0 ||
+        get_scratch(a[6], &scratch, &bytes) < 0 || get_stream(a[8], &stream) < 0)
+        return NULL;
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lib_rmsnorm_grad(&m.x.c, m.weight, &dy.c, extra, m.x.shape[0], cols, m.eps, m.x.type, &dx.c, dweight,
+                              scratch, bytes, stream);
+    Py_END_ALLOW_THREADS
+    return done(status, "dg_rmsnorm_grad");
+}
+
+/* gated as 0 or 1, and the activation. */
+static int get_activation(PyObject* gated_arg, PyObject* act_arg, int* gated, dg_activation* act) {
+    int64_t kind;
+    *gated = PyObject_IsTrue(gated_arg);
+    if (*gated < 0 || as_int64(PyNumber_Index(act_arg), &kind) < 0) return -1;
+    *act = (dg_activation)to_int(kind);
+    return 0;
+}
+
+/* (x, act, y, q, q_scale, x_q, x_scale, gated, stream) */
+static PyObject* py_activate(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    rows_arg x, y;
+    const dg_rows* out;
+    void *q, *q_scale, *x_q, *x_scale;
+    int gated;
+    dg_activation act;
+    dg_stream_t stream;
+    (void)self;
+    if (want_args(n, 9) < 0 || get_activation(a[7], a[1], &gated, &act) < 0 || get_rows(a[0], "x", NULL, -1, &x) < 0)
+        return NULL;
+    if (gated && x.shape[1] % 2 != 0) {
+        fail("x must have two halves when gated");
+        return NULL;
+    }
+    const int64_t rows = x.shape[0], width = x.shape[1], cols = gated ? width / 2 : width;
+    if (get_rows_or_none(a[2], "y", &x, cols, &y, &out) < 0 ||
+        get_optional(a[3], type_uint8, "uint8", rows * cols, "q", &q) < 0 ||
+        get_optional(a[4], type_float32, "FP32", rows, "q_scale", &q_scale) < 0 ||
+        get_optional(a[5], type_uint8, "uint8", rows * width, "x_q", &x_q) < 0 ||
+        get_optional(a[6], type_float32, "FP32", gated ? 2 * rows : rows, "x_scale", &x_scale) < 0 ||
+        get_stream(a[8], &stream) < 0)
+        return NULL;
+    if ((a[3] == Py_None) != (a[4] == Py_None) || (a[5] == Py_None) != (a[6] == Py_None)) {
+        fail("codes and their scales must be given together");
+        return NULL;
+    }
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lib_activate(&x.c, gated, act, rows, cols, x.type, out, q, q_scale, x_q, x_scale, stream);
+    Py_END_ALLOW_THREADS
+    return done(status, "dg_activate");
+}
+
+/* (dy, act, dx, x, x_q, x_scale, gated, dbias, scratch, stream) */
+static PyObject* py_activate_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    rows_arg dy, dx, x;
+    const dg_rows* in;
+    void *x_q, *x_scale, *dbias, *scratch;
+    int64_t bytes;
+    int gated;
+    dg_activation act;
+    dg_stream_t stream;
+    (void)self;
+    if (want_args(n, 10) < 0 || get_activation(a[6], a[1], &gated, &act) < 0 ||
+        get_rows(a[0], "dy", NULL, -1, &dy) < 0)
+        return NULL;
+    const int64_t rows = dy.shape[0], cols = dy.shape[1], width = gated ? 2 * cols : cols;
+    if ((a[3] == Py_None) == (a[4] == Py_None) || (a[4] == Py_None) != (a[5] == Py_None)) {
+        fail("x, or x_q and x_scale, must be given");
+        return NULL;
+    }
+    if (get_rows(a[2], "dx", &dy, width, &dx) < 0 || get_rows_or_none(a[3], "x", &dy, width, &x, &in) < 0 ||
+        get_optional(a[4], type_uint8, "uint8", rows * width, "x_q", &x_q) < 0 ||
+        get_optional(a[5], type_float32, "FP32", gated ? 2 * rows : rows, "x_scale", &x_scale) < 0 ||
+        get_optional(a[7], type_float32, "FP32", width, "dbias", &dbias) < 0 ||
+        get_scratch(a[8], &scratch, &bytes) < 0 || get_stream(a[9], &stream) < 0)
+        return NULL;
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lib_activate_grad(&dy.c, in, x_q, x_scale, gated, act, rows, cols, dy.type, &dx.c, dbias, scratch, bytes,
+                               stream);
+    Py_END_ALLOW_THREADS
+    return done(status, "dg_activate_grad");
+}
+
+/* (addresses of the library's functions around a layer's products, in the
+ * order of the pointers above; torch's uint8) */
+static PyObject* py_bind_layer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void* f[6];
+    (void)self;
+    if (want_args(n, 7) < 0) return NULL;
+    for (int i = 0; i < 6; ++i)
+        if (as_address(Py_NewRef(a[i]), &f[i]) < 0) return NULL;
+    *(void**)&lib_rmsnorm = f[0];
+    *(void**)&lib_rmsnorm_e4m3 = f[1];
+    *(void**)&lib_rmsnorm_e4m3_amax = f[2];
+    *(void**)&lib_rmsnorm_grad = f[3];
+    *(void**)&lib_activate = f[4];
+    *(void**)&lib_activate_grad = f[5];
+    Py_XSETREF(type_uint8, Py_NewRef(a[6]));
+    Py_RETURN_NONE;
+}
+
 /* (addresses of dg_rope, dg_kv_append, dg_kv_read, dg_attn_decode; torch's
  * bfloat16, float16, int32, float32; current_stream; current_device; check) */
 static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -334,6 +590,13 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL, NULL},
+    {"bind_layer", (PyCFunction)(void (*)(void))py_bind_layer, METH_FASTCALL, NULL},
+    {"rmsnorm", (PyCFunction)(void (*)(void))py_rmsnorm, METH_FASTCALL, NULL},
+    {"rmsnorm_e4m3", (PyCFunction)(void (*)(void))py_rmsnorm_e4m3, METH_FASTCALL, NULL},
+    {"rmsnorm_e4m3_amax", (PyCFunction)(void (*)(void))py_rmsnorm_e4m3_amax, METH_FASTCALL, NULL},
+    {"rmsnorm_grad", (PyCFunction)(void (*)(void))py_rmsnorm_grad, METH_FASTCALL, NULL},
+    {"activate", (PyCFunction)(void (*)(void))py_activate, METH_FASTCALL, NULL},
+    {"activate_grad", (PyCFunction)(void (*)(void))py_activate_grad, METH_FASTCALL, NULL},
     {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
     {"kv_append", (PyCFunction)(void (*)(void))py_kv_append, METH_FASTCALL, NULL},
     {"kv_read", (PyCFunction)(void (*)(void))py_kv_read, METH_FASTCALL, NULL},

@@ -505,6 +505,129 @@ dg_status dg_attn_decode(const dg_heads* q, const dg_heads* out, float* lse, int
 dg_status dg_attn_decode_scratch(int batch, int q_len, int q_heads, int head_dim,
                                  int64_t prefix_len, int sm_count, int64_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * Around a layer's products: norm, activation and their gradients on BF16 or
+ * FP16 rows, with E4M3 codes and a scale per row as output ([FP8-guide]
+ * §3.2's rule with the row as the tensor), and products that take such
+ * scales.  The pages stop at per-tensor scales; these have no counterpart
+ * there.
+ *
+ * Row scales.  scale = max(fl32(amax / 448), 2^-120) of the row's FP32
+ * values, code = E4M3 of the value times the scale's FP32 reciprocal (within
+ * FP32's rounding of the quotient of §4.3).  A row that holds a NaN or an
+ * infinity has scale NaN or infinity; code times scale is NaN there.
+ * ------------------------------------------------------------------------ */
+
+/* rows x columns BF16 or FP16 elements: element (r, c) at
+ * data[r * stride + c].  data 16-byte aligned, stride a multiple of 8
+ * elements (DG_ERR_MISALIGNED), not negative; as an output, rows must not
+ * overlap one another. */
+typedef struct {
+    void* data;
+    int64_t stride;
+} dg_rows;
+
+/* Root-mean-square norm of rows, the residual added first:
+ *   s = x + residual,   y = s / sqrt(mean(s^2) + eps) * weight
+ * in FP32, each output rounded once (s is not rounded before its norm).
+ *   x         rows x cols of dtype (BF16 or FP16).
+ *   residual  the same, or NULL: s = x.
+ *   sum       receives s rounded to dtype (the new residual stream); may be
+ *             NULL, and may be x or residual itself (same pointer and
+ *             stride).
+ *   weight    dtype[cols], or NULL for ones.
+ *   cols      a multiple of 8 (DG_ERR_MISALIGNED), 8 .. 32768.
+ *   eps       at least 2^-126, finite.
+ *   y         receives y rounded to dtype; may be x or residual itself,
+ *             unless sum is. */
+dg_status dg_rmsnorm(const dg_rows* x, const dg_rows* residual, const dg_rows* sum,
+                     const void* weight, int64_t rows, int64_t cols, double eps, dg_dtype dtype,
+                     const dg_rows* y, dg_stream_t stream);
+
+/* The same with E4M3 output, y not rounded in between.
+ *   q          uint8[rows][cols] codes, 16-byte aligned.
+ *   row_scale  FP32[rows], 4-byte aligned. */
+dg_status dg_rmsnorm_e4m3(const dg_rows* x, const dg_rows* residual, const dg_rows* sum,
+                          const void* weight, int64_t rows, int64_t cols, double eps,
+                          dg_dtype dtype, uint8_t* q, float* row_scale, dg_stream_t stream);
+
+/* The same with one scale for all rows, recorded earlier (as
+ * dg_quantize_e4m3_amax): q = E4M3(y / scale[0]), saturating, and
+ * amax_out[0] = max |y| (NaN propagates; 0 for no rows); then, if
+ * next_scale_out is not NULL, next_scale_out[0] = amax / 448 (1 when amax is
+ * 0).  next_scale_out may be scale itself; amax_out must be neither. */
+dg_status dg_rmsnorm_e4m3_amax(const dg_rows* x, const dg_rows* residual, const dg_rows* sum,
+                               const void* weight, int64_t rows, int64_t cols, double eps,
+                               dg_dtype dtype, const float* scale, uint8_t* q, float* amax_out,
+                               float* next_scale_out, dg_stream_t stream);
+
+/* Gradient of the norm.  With u = s / sqrt(mean(s^2) + eps), g = dy * weight:
+ *   dx      = (g - u mean(g u)) / sqrt(mean(s^2) + eps) + dsum
+ *   dweight = sum over rows of dy * u
+ * dx is the gradient of x and of residual alike; dsum is what flows back
+ * into s by other ways.
+ *   s        what sum received (or x, without a residual); dy, dsum, dx as s.
+ *            dsum may be NULL; dx may be any of the others itself.
+ *   dweight  FP32[cols], 16-byte aligned, or NULL.  Summed in FP32 in a fixed
+ *            order; overwritten.
+ *   scratch  device, 16-byte aligned, at least dg_rmsnorm_grad_scratch()
+ *            bytes; unused (may be NULL) without dweight.  Holds nothing
+ *            between calls; calls that may overlap in time need one each. */
+dg_status dg_rmsnorm_grad(const dg_rows* s, const void* weight, const dg_rows* dy,
+                          const dg_rows* dsum, int64_t rows, int64_t cols, double eps,
+                          dg_dtype dtype, const dg_rows* dx, float* dweight, void* scratch,
+                          int64_t scratch_bytes, dg_stream_t stream);
+
+/* Bytes of scratch dg_rmsnorm_grad needs, in *bytes.  sm_count <= 0 queries
+ * the current device. */
+dg_status dg_rmsnorm_grad_scratch(int64_t rows, int64_t cols, int sm_count, int64_t* bytes);
+
+typedef enum {
+    DG_ACT_NONE = 0,
+    DG_ACT_RELU = 1,
+    DG_ACT_GELU = 2,      /* x (1 + erf(x / sqrt 2)) / 2                                */
+    DG_ACT_GELU_TANH = 3, /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2          */
+    DG_ACT_SILU = 4       /* x / (1 + exp(-x))                                          */
+} dg_activation;
+
+/* The activation between two products:
+ *   y = act(x)   or, gated,   y = act(x[:, :cols]) * x[:, cols:]
+ * in FP32 (DG_ACT_RELU keeps NaN; the smooth ones give NaN at -infinity, and
+ * 0 for results below 2^-126 |x|).  Any of the three outputs may be left out
+ * (NULL):
+ *   x        rows x cols of dtype, or rows x 2 cols when gated.
+ *   y        rows x cols of dtype; may be x itself when not gated.
+ *   q, q_scale  y as codes uint8[rows][cols] and FP32[rows].
+ *   x_q, x_scale  an 8-bit checkpoint of x for dg_activate_grad: codes dense
+ *            like x, FP32[rows], or FP32[rows][2] when gated (a scale for each
+ *            half).
+ *   cols     a multiple of 8 (DG_ERR_MISALIGNED), 8 .. 32768.
+ * Codes 16-byte, scales 4-byte aligned; each pair is given together. */
+dg_status dg_activate(const dg_rows* x, int gated, dg_activation act, int64_t rows, int64_t cols,
+                      dg_dtype dtype, const dg_rows* y, uint8_t* q, float* q_scale, uint8_t* x_q,
+                      float* x_scale, dg_stream_t stream);
+
+/* Gradient of the activation, from its input or that input's checkpoint:
+ *   dx = dy * act'(x)
+ *   or, gated,   dx = (dy * up * act'(gate), dy * act(gate))
+ *   dbias = sum over rows of dx, before its rounding
+ *   dy       rows x cols of dtype.
+ *   x        as dg_activate, or NULL: x_q and x_scale (codes times scale).
+ *   dx       like x; may be x itself, or dy when not gated.
+ *   dbias    FP32 of dx's columns, 16-byte aligned, or NULL.  Summed in FP32 in
+ *            a fixed order; overwritten.
+ *   scratch  as dg_rmsnorm_grad, for dbias.
+ * The derivative of DG_ACT_RELU at 0 is 0; those of the smooth activations
+ * are NaN at the infinities. */
+dg_status dg_activate_grad(const dg_rows* dy, const dg_rows* x, const uint8_t* x_q,
+                           const float* x_scale, int gated, dg_activation act, int64_t rows,
+                           int64_t cols, dg_dtype dtype, const dg_rows* dx, float* dbias,
+                           void* scratch, int64_t scratch_bytes, dg_stream_t stream);
+
+/* Bytes of scratch dg_activate_grad needs, in *bytes. */
+dg_status dg_activate_grad_scratch(int64_t rows, int64_t cols, int gated, int sm_count,
+                                   int64_t* bytes);
+
 /* Tile / path selection for a GEMM shape, host only (launches nothing).
  * [FP8-guide] §2.2, §3.1, §3.3 (per-shape tile choice, smaller tiles where
  * edge waste is high) and [HGEMM-L2] §3.1-§3.3 (tile and stage count chosen
