@@ -31,7 +31,7 @@ __all__ = [
     "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch",
     "DG_ACT_NONE", "DG_ACT_RELU", "DG_ACT_GELU", "DG_ACT_GELU_TANH", "DG_ACT_SILU", "dg_rmsnorm",
     "dg_rmsnorm_e4m3", "dg_rmsnorm_e4m3_amax", "dg_rmsnorm_grad", "dg_rmsnorm_grad_scratch",
-    "dg_activate", "dg_activate_grad", "dg_activate_grad_scratch",
+    "dg_activate", "dg_activate_grad", "dg_activate_grad_scratch", "dg_fp8_gemm_fused", "dg_hgemm_fused",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -53,7 +53,7 @@ EXPORTED_SYMBOLS = (
     "dg_rope_table", "dg_rope", "dg_kv_append", "dg_kv_read", "dg_attn_decode",
     "dg_attn_decode_scratch", "dg_rmsnorm", "dg_rmsnorm_e4m3", "dg_rmsnorm_e4m3_amax",
     "dg_rmsnorm_grad", "dg_rmsnorm_grad_scratch", "dg_activate", "dg_activate_grad",
-    "dg_activate_grad_scratch",
+    "dg_activate_grad_scratch", "dg_fp8_gemm_fused", "dg_hgemm_fused",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -96,6 +96,13 @@ class _Rotary(ctypes.Structure):
 
 class _Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p), ("scale_a_rows", ctypes.c_int),
+                ("scale_b_rows", ctypes.c_int), ("bias", ctypes.c_void_p), ("act", ctypes.c_int),
+                ("residual", ctypes.c_void_p), ("residual_type", ctypes.c_int),
+                ("scale_d", ctypes.c_void_p), ("amax_d", ctypes.c_void_p)]
 
 
 class _KvCache(ctypes.Structure):
@@ -154,6 +161,9 @@ def lib():
             L.dg_rmsnorm_e4m3_amax.argtypes = [*norm, vp, vp, vp, vp, vp]
             L.dg_rmsnorm_grad.argtypes = [rows, vp, rows, rows, i64, i64, f64, i32, rows, vp, vp, i64, vp]
             L.dg_rmsnorm_grad_scratch.argtypes = [i64, i64, i32, ctypes.POINTER(i64)]
+            fused = [vp, vp, vp, i64, i64, i64, ctypes.POINTER(_Epilogue), i32, vp]
+            L.dg_fp8_gemm_fused.argtypes = fused
+            L.dg_hgemm_fused.argtypes = fused
             L.dg_activate.argtypes = [rows, i32, i32, i64, i64, i32, rows, vp, vp, vp, vp, vp]
             L.dg_activate_grad.argtypes = [rows, rows, vp, vp, i32, i32, i64, i64, i32, rows, vp, vp, i64, vp]
             L.dg_activate_grad_scratch.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64)]
@@ -178,7 +188,7 @@ def lib():
                          "dg_kv_read", "dg_attn_decode", "dg_attn_decode_scratch", "dg_rmsnorm",
                          "dg_rmsnorm_e4m3", "dg_rmsnorm_e4m3_amax", "dg_rmsnorm_grad",
                          "dg_rmsnorm_grad_scratch", "dg_activate", "dg_activate_grad",
-                         "dg_activate_grad_scratch"):
+                         "dg_activate_grad_scratch", "dg_fp8_gemm_fused", "dg_hgemm_fused"):
                 getattr(L, name).restype = st
             _lib = L
     return _lib
@@ -384,7 +394,8 @@ def _load_native():
                         torch.bfloat16, torch.float16, torch.int32, torch.float32, stream, device, _check)
             module.bind_layer(*(ctypes.cast(f, ctypes.c_void_p).value
                                 for f in (L.dg_rmsnorm, L.dg_rmsnorm_e4m3, L.dg_rmsnorm_e4m3_amax,
-                                          L.dg_rmsnorm_grad, L.dg_activate, L.dg_activate_grad)),
+                                          L.dg_rmsnorm_grad, L.dg_activate, L.dg_activate_grad,
+                                          L.dg_fp8_gemm_fused, L.dg_hgemm_fused)),
                               torch.uint8)
             _native = module
     return _native
@@ -515,6 +526,22 @@ def dg_activate_grad(dy, act, dx, x=None, x_q=None, x_scale=None, gated=False, d
                      stream=None) -> None:
     """dx of dg_activate from its input x or the checkpoint x_q, x_scale; dbias (FP32) = column sums of dx."""
     (_native or _load_native()).activate_grad(dy, act, dx, x, x_q, x_scale, gated, dbias, scratch, stream)
+
+
+def dg_fp8_gemm_fused(A, B, D, scale_a, scale_b, bias=None, act=DG_ACT_NONE, residual=None, scale_d=None,
+                      amax_d=None, out=DG_BF16, stream=None) -> None:
+    """D = out(act(scale_a * scale_b * A @ B^T + bias) + residual) on E4M3 operands
+    A [M, K], B [N, K]: scales of one element or of one a row, bias FP32 [N],
+    residual BF16 or FP16 [M, N] (may be D)."""
+    (_native or _load_native()).fp8_gemm_fused(A, B, D, scale_a, scale_b, bias, act, residual, scale_d, amax_d,
+                                               out, stream)
+
+
+def dg_hgemm_fused(A, B, D, bias=None, act=DG_ACT_NONE, residual=None, scale_a=None, scale_b=None, amax_d=None,
+                   out=DG_FP16, stream=None) -> None:
+    """dg_fp8_gemm_fused on FP16 operands; scales are optional (both or neither)."""
+    (_native or _load_native()).hgemm_fused(A, B, D, scale_a, scale_b, bias, act, residual, None, amax_d, out,
+                                            stream)
 
 
 def dg_gemm_plan(M, N, K, in_dtype=DG_E4M3, out_dtype=DG_BF16, sm_count=0) -> dict:

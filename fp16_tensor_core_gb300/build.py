@@ -26,9 +26,11 @@ NATIVE = os.path.join(OUT_DIR, "dg_python" + sysconfig.get_config_var("EXT_SUFFI
 
 SOURCES = ["dg_api.cu", "k_scale.cu", "k_gemv.cu", "k_gemv_mma.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu",
            "k_gemm_skinny.cu", "dg_static.cu", "k_kvcache.cu", "k_attn_decode.cu",
-           "k_attn_prefix.cu", "k_norm.cu", "k_activate.cu"]
+           "k_attn_prefix.cu", "k_norm.cu", "k_activate.cu",
+           "k_gemm_tc_fused.cu", "k_gemm_tc2_fused.cu", "k_gemm_skinny_fused.cu", "k_epilogue.cu"]
 HEADERS = ["dg_ptx.cuh", "dg_internal.h", "gemm_common.cuh", "attn_common.cuh", "prefix_barriers.h",
-           "activation.cuh", "row_common.cuh"]
+           "activation.cuh", "row_common.cuh", "gemm_tc_kernel.cuh", "gemm_pair_kernel.cuh",
+           "gemm_skinny_kernel.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

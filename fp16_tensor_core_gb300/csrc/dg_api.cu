@@ -214,7 +214,11 @@ double splitk_estimate_us(int64_t M, int64_t N, int64_t K, bool fp16_in, const d
 }
 
 // Shared path selection for dg_gemm_plan and the GEMM entry points.
-dg_status make_plan(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count, dg_plan* p) {
+// fused: the product has more in its epilogue than one scale, which the
+// CUDA-core GEMV does not: its shapes (M = 1 on more CTAs than one wave) take
+// the warp-MMA one.
+dg_status make_plan(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count, dg_plan* p,
+                    bool fused = false) {
     *p = dg_plan{};
     if (M == 0 || N == 0) {
         p->path = 0;
@@ -252,7 +256,7 @@ dg_status make_plan(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count,
     if (use_mma && kn.mma_gemv != 1) {
         use_mma = kn.mma_gemv != 0 &&
                   (fp16_in || M <= 8 || N * K <= (int64_t{1} << 22)) &&
-                  !(M == 1 && !fp16_in && mma_ctas > 6 * sms);
+                  (fused || !(M == 1 && !fp16_in && mma_ctas > 6 * sms));
     }
     if (use_mma) {
         p->path = 5;
@@ -265,7 +269,7 @@ dg_status make_plan(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count,
         p->tiles = static_cast<int>(mma_ctas);
         return DG_OK;
     }
-    if (M <= kn.gemv_max_m) {
+    if (M <= kn.gemv_max_m && !fused) {
         p->path = 2;
         int rows = M <= 4 ? 8 : 4;   // 4 warps x (2 or 1) rows of B
         int chunks = 4;              // 16-byte chunks per lane per row in flight
@@ -455,12 +459,12 @@ dg_status splitk_workspace(const DeviceState* st, cudaStream_t s, SplitkWs* out,
 
 dg_status run_gemm(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
                    bool fp16_in, const float* sa, const float* sb, const float* sd,
-                   dg_dtype out, cudaStream_t s, float* amax_d = nullptr) {
+                   dg_dtype out, cudaStream_t s, float* amax_d = nullptr, const Epilogue* epi = nullptr) {
     DeviceState* st = nullptr;
     dg_status rc = current_device_state(&st);
     if (rc != DG_OK) return rc;
     dg_plan plan;
-    rc = make_plan(M, N, K, fp16_in, st->sm_count, &plan);
+    rc = make_plan(M, N, K, fp16_in, st->sm_count, &plan, epi != nullptr);
     if (rc != DG_OK) return rc;
     log_plan(fp16_in ? "hgemm" : "fp8_gemm", M, N, K, plan);
     const int ok = out_kind_of(out);
@@ -474,6 +478,17 @@ dg_status run_gemm(const void* A, const void* B, void* D, int64_t M, int64_t N, 
         case 0:
             return DG_OK;
         case 1:
+            if (epi != nullptr) {
+                TcLaunch L{};
+                L.D = D;
+                L.M = static_cast<int>(M);
+                L.N = static_cast<int>(N);
+                L.sd = sd;
+                L.out_kind = ok;
+                L.amax_out = amax_bits;
+                L.epi = epi;
+                return from_cuda(launch_epilogue_only(L, s));
+            }
             return from_cuda(cudaMemsetAsync(D, 0, static_cast<size_t>(M * N * elem_bytes(out)), s));
         case 2:
             return from_cuda(launch_gemv(A, B, D, static_cast<int>(M), static_cast<int>(N),
@@ -500,6 +515,7 @@ dg_status run_gemm(const void* A, const void* B, void* D, int64_t M, int64_t N, 
             L.amax_out = amax_bits;
             L.group_off = nullptr;
             L.groups = 0;
+            L.epi = epi;
             if (plan.path == 5) return from_cuda(launch_gemv_mma(L, s));
             if (plan.path == 3 && plan.block_m == 256 &&
                 (knobs().split_tail || knobs().stream_k)) {
@@ -1272,6 +1288,60 @@ dg_status dg_activate_grad(const dg_rows* dy, const dg_rows* x, const uint8_t* x
     a.partials = dbias != nullptr ? static_cast<float*>(scratch) : nullptr;
     return from_cuda(launch_activate_grad(a, dtype == DG_FP16, dbias, st->sm_count,
                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// What the fused products take besides their operands (checked in the same
+// order as the plain ones': sizes and types, pointers, alignment).
+dg_status check_epilogue(const dg_epilogue* e, const void* D, int64_t M, int64_t N, bool scaled, dg_dtype out) {
+    if (e == nullptr) return DG_ERR_INVALID_VALUE;
+    const dg_status rc = check_activation(e->act);
+    if (rc != DG_OK) return rc;
+    if (e->residual != nullptr && check_16bit(e->residual_type) != DG_OK) return DG_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) return aligned4(e->amax_d) ? DG_OK : DG_ERR_MISALIGNED;
+    if ((e->scale_a == nullptr) != (e->scale_b == nullptr) || (scaled && e->scale_a == nullptr))
+        return DG_ERR_INVALID_VALUE;
+    if (e->scale_a == nullptr && (e->scale_a_rows != 0 || e->scale_b_rows != 0)) return DG_ERR_INVALID_VALUE;
+    if (out == DG_E4M3 && e->scale_d == nullptr) return DG_ERR_INVALID_VALUE;
+    // in place only element by element
+    if (e->residual == D && (out == DG_E4M3 || e->residual_type != out)) return DG_ERR_INVALID_VALUE;
+    if (e->amax_d != nullptr && e->amax_d == e->scale_d) return DG_ERR_INVALID_VALUE;   // zeroed before it is read
+    auto vector = [](const float* p, int rows) { return rows != 0 ? aligned16(p) : aligned4(p); };
+    if (!vector(e->scale_a, e->scale_a_rows) || !vector(e->scale_b, e->scale_b_rows) || !aligned16(e->bias) ||
+        !aligned16(e->residual) || !aligned4(e->scale_d) || !aligned4(e->amax_d))
+        return DG_ERR_MISALIGNED;
+    return DG_OK;
+}
+
+dg_status run_fused(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K, bool fp16_in,
+                    const dg_epilogue* e, dg_dtype out, dg_stream_t stream) {
+    Epilogue epi;
+    epi.sa_step = e->scale_a_rows != 0 ? 1 : 0;
+    epi.sb_step = e->scale_b_rows != 0 ? 1 : 0;
+    epi.bias = e->bias;
+    epi.residual = static_cast<const uint16_t*>(e->residual);
+    epi.residual_fp16 = e->residual_type == DG_FP16 ? 1 : 0;
+    epi.act = e->act;
+    return run_gemm(A, B, D, M, N, K, fp16_in, e->scale_a, e->scale_b, e->scale_d, out,
+                    reinterpret_cast<cudaStream_t>(stream), e->amax_d, &epi);
+}
+
+}  // namespace
+
+dg_status dg_fp8_gemm_fused(const uint8_t* A, const uint8_t* B, void* D, int64_t M, int64_t N, int64_t K,
+                            const dg_epilogue* epilogue, dg_dtype out, dg_stream_t stream) {
+    if (epilogue == nullptr) return DG_ERR_INVALID_VALUE;
+    dg_status rc = check_fp8_gemm_args(A, B, D, M, N, K, epilogue->scale_a, epilogue->scale_b, epilogue->scale_d, out);
+    if (rc == DG_OK) rc = check_epilogue(epilogue, D, M, N, K > 0, out);
+    return rc != DG_OK ? rc : run_fused(A, B, D, M, N, K, false, epilogue, out, stream);
+}
+
+dg_status dg_hgemm_fused(const uint16_t* A, const uint16_t* B, void* D, int64_t M, int64_t N, int64_t K,
+                         const dg_epilogue* epilogue, dg_dtype out, dg_stream_t stream) {
+    dg_status rc = check_hgemm_args(A, B, D, M, N, K, out);
+    if (rc == DG_OK) rc = check_epilogue(epilogue, D, M, N, false, out);
+    return rc != DG_OK ? rc : run_fused(A, B, D, M, N, K, true, epilogue, out, stream);
 }
 
 dg_status dg_gemm_plan(int64_t M, int64_t N, int64_t K, dg_dtype in, dg_dtype out,

@@ -178,6 +178,15 @@ cudaError_t launch_quantize_e4m3_pair(const float* a, int64_t na, const float* b
 // Sets *bits = 0 on stream s (one-thread kernel).
 cudaError_t launch_zero_word(uint32_t* bits, cudaStream_t s);
 
+// What a fused product does with its accumulators besides the scales.
+struct Epilogue {
+    int sa_step = 0, sb_step = 0;         // 1: a scale per row of A, of B
+    const float* bias = nullptr;          // [N]
+    const uint16_t* residual = nullptr;   // M x N
+    int residual_fp16 = 0;
+    int act = 0;
+};
+
 struct TcLaunch {
     const void* A;
     const void* B;
@@ -199,6 +208,7 @@ struct TcLaunch {
     float* tail_ws = nullptr;
     size_t tail_ws_bytes = 0;
     uint32_t* tail_counts = nullptr;
+    const Epilogue* epi = nullptr;   // fused kernels, else the plain ones
 };
 cudaError_t launch_gemm_tc(const TcLaunch& L, cudaStream_t s);
 // Grouped variant (single-CTA tiles; L.plan->block_n is 128 or 256).
@@ -214,6 +224,9 @@ cudaError_t launch_gemv_mma(const TcLaunch& L, cudaStream_t s);
 // nc_for(M) <= max_cols.
 cudaError_t launch_gemm_skinny(const TcLaunch& L, float* partials, uint32_t* counts, int max_cols,
                                cudaStream_t s);
+cudaError_t launch_gemm_skinny_fused(const TcLaunch& L, float* partials, uint32_t* counts, cudaStream_t s);
+// K = 0: the epilogue of an empty sum.
+cudaError_t launch_epilogue_only(const TcLaunch& L, cudaStream_t s);
 void plan_skinny(int64_t M, int64_t N, int64_t K, bool fp16_in, int sm_count, dg_plan* p);
 
 // Rotary positions and the E4M3 key/value cache (arguments already checked).

@@ -1,6 +1,6 @@
 /* dg_python.c -- argument marshalling of the serving entry points (rotary
  * positions, cache writes and reads, attention) and of those around a layer's
- * products (norm, activation) for Python.
+ * products (norm, activation, fused products) for Python.
  *
  * A decode step makes these calls for every layer and token, with kernels of
  * 2 to 10 us: read attribute by attribute in Python and handed over through
@@ -42,6 +42,10 @@ static dg_status (*lib_activate)(const dg_rows*, int, dg_activation, int64_t, in
 static dg_status (*lib_activate_grad)(const dg_rows*, const dg_rows*, const uint8_t*, const float*, int,
                                       dg_activation, int64_t, int64_t, dg_dtype, const dg_rows*, float*, void*,
                                       int64_t, dg_stream_t);
+static dg_status (*lib_fp8_gemm_fused)(const uint8_t*, const uint8_t*, void*, int64_t, int64_t, int64_t,
+                                       const dg_epilogue*, dg_dtype, dg_stream_t);
+static dg_status (*lib_hgemm_fused)(const uint16_t*, const uint16_t*, void*, int64_t, int64_t, int64_t,
+                                    const dg_epilogue*, dg_dtype, dg_stream_t);
 static PyObject *type_bf16, *type_fp16, *type_int32, *type_float32, *type_uint8;   /* torch.dtype objects */
 static PyObject *current_stream;   /* (device) -> handle of its current stream */
 static PyObject *current_device;   /* () -> index */
@@ -553,13 +557,105 @@ static PyObject* py_activate_grad(PyObject* self, PyObject* const* a, Py_ssize_t
     return done(status, "dg_activate_grad");
 }
 
+/* A contiguous matrix: address, rows, columns and bytes an element. */
+typedef struct {
+    void* data;
+    int64_t rows, cols, bytes;
+} matrix_arg;
+
+static int get_matrix(PyObject* t, const char* what, matrix_arg* m) {
+    int64_t shape[2], bytes;
+    if (numbers(PyObject_GetAttr(t, n_shape), 2, shape, what, "must have two dimensions") < 0 ||
+        get_data(t, &m->data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), &bytes) < 0)
+        return -1;
+    m->rows = shape[0];
+    m->cols = shape[1];
+    m->bytes = shape[0] > 0 && shape[1] > 0 ? bytes / (shape[0] * shape[1]) : 0;
+    return 0;
+}
+
+/* A scale for the whole operand, or one a row. */
+static int get_scales(PyObject* t, const char* what, int64_t rows, void** out, int* per_row) {
+    int64_t n;
+    *out = NULL;
+    *per_row = 0;
+    if (t == Py_None) return 0;
+    if (as_int64(PyObject_CallMethodNoArgs(t, n_numel), &n) < 0) return -1;
+    *per_row = n != 1;
+    return get_array(t, type_float32, "FP32", n == 1 ? 1 : rows, what, out);
+}
+
+/* (A, B, D, scale_a, scale_b, bias, act, residual, scale_d, amax_d, out, stream) */
+static PyObject* fused(PyObject* const* a, Py_ssize_t n, int fp16) {
+    const char* name = fp16 ? "dg_hgemm_fused" : "dg_fp8_gemm_fused";
+    const int64_t in_bytes = fp16 ? 2 : 1;
+    matrix_arg A, B, D, R;
+    dg_epilogue e;
+    void *sa, *sb, *bias, *sd, *amax;
+    int64_t act, out;
+    dg_stream_t stream;
+    if (want_args(n, 12) < 0 || get_matrix(a[0], "A", &A) < 0 || get_matrix(a[1], "B", &B) < 0 ||
+        get_matrix(a[2], "D", &D) < 0 || as_int64(PyNumber_Index(a[6]), &act) < 0 ||
+        as_int64(PyNumber_Index(a[10]), &out) < 0)
+        return NULL;
+    const int64_t out_bytes = out == DG_E4M3 ? 1 : 2;
+    if (A.cols != B.cols || D.rows != A.rows || D.cols != B.rows || (A.bytes != 0 && A.bytes != in_bytes) ||
+        (B.bytes != 0 && B.bytes != in_bytes) || (D.bytes != 0 && D.bytes != out_bytes)) {
+        fail("A [M, K], B [N, K] and D [M, N] must agree, with elements of the operands' and the output's type");
+        return NULL;
+    }
+    e.residual = NULL;
+    e.residual_type = DG_BF16;
+    if (a[7] != Py_None) {
+        if (get_matrix(a[7], "residual", &R) < 0) return NULL;
+        PyObject* type = PyObject_GetAttr(a[7], n_dtype);
+        if (type == NULL) return NULL;
+        const int bf16 = type == type_bf16, half = type == type_fp16;
+        Py_DECREF(type);
+        if (!(bf16 || half) || R.rows != D.rows || R.cols != D.cols) {
+            fail_about("residual", "must be BF16 or FP16 with the shape of D");
+            return NULL;
+        }
+        e.residual = R.data;
+        e.residual_type = bf16 ? DG_BF16 : DG_FP16;
+    }
+    if (get_scales(a[3], "scale_a", A.rows, &sa, &e.scale_a_rows) < 0 ||
+        get_scales(a[4], "scale_b", B.rows, &sb, &e.scale_b_rows) < 0 ||
+        get_optional(a[5], type_float32, "FP32", B.rows, "bias", &bias) < 0 ||
+        get_optional(a[8], type_float32, "FP32", 1, "scale_d", &sd) < 0 ||
+        get_optional(a[9], type_float32, "FP32", 1, "amax_d", &amax) < 0 || get_stream(a[11], &stream) < 0)
+        return NULL;
+    e.scale_a = sa;
+    e.scale_b = sb;
+    e.bias = bias;
+    e.act = (dg_activation)to_int(act);
+    e.scale_d = sd;
+    e.amax_d = amax;
+    dg_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = fp16 ? lib_hgemm_fused(A.data, B.data, D.data, A.rows, B.rows, A.cols, &e, (dg_dtype)to_int(out), stream)
+                  : lib_fp8_gemm_fused(A.data, B.data, D.data, A.rows, B.rows, A.cols, &e, (dg_dtype)to_int(out),
+                                       stream);
+    Py_END_ALLOW_THREADS
+    return done(status, name);
+}
+
+static PyObject* py_fp8_gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    return fused(a, n, 0);
+}
+static PyObject* py_hgemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    return fused(a, n, 1);
+}
+
 /* (addresses of the library's functions around a layer's products, in the
  * order of the pointers above; torch's uint8) */
 static PyObject* py_bind_layer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    void* f[6];
+    void* f[8];
     (void)self;
-    if (want_args(n, 7) < 0) return NULL;
-    for (int i = 0; i < 6; ++i)
+    if (want_args(n, 9) < 0) return NULL;
+    for (int i = 0; i < 8; ++i)
         if (as_address(Py_NewRef(a[i]), &f[i]) < 0) return NULL;
     *(void**)&lib_rmsnorm = f[0];
     *(void**)&lib_rmsnorm_e4m3 = f[1];
@@ -567,7 +663,9 @@ static PyObject* py_bind_layer(PyObject* self, PyObject* const* a, Py_ssize_t n)
     *(void**)&lib_rmsnorm_grad = f[3];
     *(void**)&lib_activate = f[4];
     *(void**)&lib_activate_grad = f[5];
-    Py_XSETREF(type_uint8, Py_NewRef(a[6]));
+    *(void**)&lib_fp8_gemm_fused = f[6];
+    *(void**)&lib_hgemm_fused = f[7];
+    Py_XSETREF(type_uint8, Py_NewRef(a[8]));
     Py_RETURN_NONE;
 }
 
@@ -595,6 +693,8 @@ static PyMethodDef methods[] = {
     {"rmsnorm_e4m3", (PyCFunction)(void (*)(void))py_rmsnorm_e4m3, METH_FASTCALL, NULL},
     {"rmsnorm_e4m3_amax", (PyCFunction)(void (*)(void))py_rmsnorm_e4m3_amax, METH_FASTCALL, NULL},
     {"rmsnorm_grad", (PyCFunction)(void (*)(void))py_rmsnorm_grad, METH_FASTCALL, NULL},
+    {"fp8_gemm_fused", (PyCFunction)(void (*)(void))py_fp8_gemm_fused, METH_FASTCALL, NULL},
+    {"hgemm_fused", (PyCFunction)(void (*)(void))py_hgemm_fused, METH_FASTCALL, NULL},
     {"activate", (PyCFunction)(void (*)(void))py_activate, METH_FASTCALL, NULL},
     {"activate_grad", (PyCFunction)(void (*)(void))py_activate_grad, METH_FASTCALL, NULL},
     {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},

@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "activation.cuh"
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
 
@@ -53,6 +54,7 @@ struct Params {
     int b_edge_bytes;
     int a_edge_row;
     int b_edge_row;
+    Epilogue epi;   // of the fused kernels only
 };
 
 constexpr int kMaxGroups = 1024;
@@ -62,6 +64,9 @@ constexpr int kMaxGroups = 1024;
 int pair_smem_for(int bn, int kps);   // kps: K blocks per stage (1 or 2)
 int pair_stages(int bn, int kps);
 cudaError_t launch_gemm_tc_pair(const TcLaunch& L, const Params& prm, cudaStream_t s);
+// The same kernels with a fused epilogue (L.epi).
+cudaError_t launch_gemm_tc_pair_fused(const TcLaunch& L, const Params& prm, cudaStream_t s);
+cudaError_t launch_gemm_tc_fused(const TcLaunch& L, const Params& prm, cudaStream_t s);
 
 namespace {
 
@@ -94,23 +99,10 @@ __device__ __forceinline__ void st_global_v4(void* p, uint32_t a, uint32_t b, ui
                  :: "l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Scale, convert and store 32 consecutive accumulator columns of one row.
-// Returns max |acc| over the stored elements as ordered bits (the bit
-// pattern of a non-negative float; NaN above every number), 0 if none.
-__device__ __forceinline__ uint32_t store_chunk(const Params& p, int row, int row_end, int col0,
-                                                const uint32_t (&r)[32], float alpha) {
-    if (row >= row_end) return 0u;
-    const int ncols = min(32, p.N - col0);
-    if (ncols <= 0) return 0u;
-    uint32_t amax_bits = 0u;
-    if (p.amax_out != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < ncols) amax_bits = max(amax_bits, r[i] & 0x7FFFFFFFu);
-    }
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+// Convert and store 32 consecutive output columns of one row, `ncols` (at
+// most 32) of them inside D.
+__device__ __forceinline__ void store_values(const Params& p, int row, int ncols, int col0,
+                                             const float (&v)[32]) {
     const int64_t off = static_cast<int64_t>(row) * p.N + col0;
     if (p.out_kind == kOutE4M3) {
         uint8_t* dst = static_cast<uint8_t*>(p.D) + off;
@@ -144,6 +136,26 @@ __device__ __forceinline__ uint32_t store_chunk(const Params& p, int row, int ro
                 if (i < ncols) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
         }
     }
+}
+
+// Scale, convert and store 32 consecutive accumulator columns of one row.
+// Returns max |acc| over the stored elements as ordered bits (the bit
+// pattern of a non-negative float; NaN above every number), 0 if none.
+__device__ __forceinline__ uint32_t store_chunk(const Params& p, int row, int row_end, int col0,
+                                                const uint32_t (&r)[32], float alpha) {
+    if (row >= row_end) return 0u;
+    const int ncols = min(32, p.N - col0);
+    if (ncols <= 0) return 0u;
+    uint32_t amax_bits = 0u;
+    if (p.amax_out != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < ncols) amax_bits = max(amax_bits, r[i] & 0x7FFFFFFFu);
+    }
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+    store_values(p, row, ncols, col0, v);
     return amax_bits;
 }
 
@@ -154,22 +166,9 @@ __device__ __forceinline__ uint32_t store_chunk(const Params& p, int row, int ro
 // and columns >= N.
 constexpr int kBoxBytes = 2048;   // 32 x 32 two-byte elements (E4M3 uses half)
 
-// Thread `lane` converts accumulator row `row`, columns col0 .. col0 + 31,
-// into its line of `box`.  Returns max |acc| over the columns < N of a row
-// < row_end (ordered bits) when p.amax_out is set, else 0.
-__device__ __forceinline__ uint32_t stage_box(const Params& p, uint8_t* box, int row, int row_end,
-                                              int col0, const uint32_t (&r)[32], float alpha,
-                                              int lane) {
-    uint32_t amax_bits = 0u;
-    if (p.amax_out != nullptr && row < row_end) {
-        const int ncols = min(32, p.N - col0);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < ncols) amax_bits = max(amax_bits, r[i] & 0x7FFFFFFFu);
-    }
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+// Thread `lane` converts one row's 32 values into its line of `box`.
+__device__ __forceinline__ void stage_values(const Params& p, uint8_t* box, const float (&v)[32],
+                                             int lane) {
     if (p.out_kind == kOutE4M3) {
         uint32_t w[8];
 #pragma unroll
@@ -195,7 +194,135 @@ __device__ __forceinline__ uint32_t stage_box(const Params& p, uint8_t* box, int
                          w[4 * k + 3]);
         }
     }
+}
+
+// Thread `lane` converts accumulator row `row`, columns col0 .. col0 + 31,
+// into its line of `box`.  Returns max |acc| over the columns < N of a row
+// < row_end (ordered bits) when p.amax_out is set, else 0.
+__device__ __forceinline__ uint32_t stage_box(const Params& p, uint8_t* box, int row, int row_end,
+                                              int col0, const uint32_t (&r)[32], float alpha,
+                                              int lane) {
+    uint32_t amax_bits = 0u;
+    if (p.amax_out != nullptr && row < row_end) {
+        const int ncols = min(32, p.N - col0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < ncols) amax_bits = max(amax_bits, r[i] & 0x7FFFFFFFu);
+    }
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+    stage_values(p, box, v, lane);
     return amax_bits;
+}
+
+// ---- the fused epilogue: act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n]
+
+// 32 elements of one row of the residual, 16 bits each (zeros past column N
+// and without a residual).  Not the read-only path: D may be the residual,
+// each element read by the thread that later writes it.
+__device__ __forceinline__ void load_residual(const Params& p, int row, bool row_ok, int col0,
+                                              uint32_t (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = 0u;
+    if (p.epi.residual == nullptr || !row_ok || col0 >= p.N) return;
+    const uint16_t* src = p.epi.residual + static_cast<int64_t>(row) * p.N + col0;
+    if (col0 + 32 <= p.N && (p.N & 7) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                         : "l"(src + 8 * i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            uint16_t e = 0;
+            if (col0 + i < p.N) asm volatile("ld.global.u16 %0, [%1];" : "=h"(e) : "l"(src + i));
+            w[i >> 1] |= static_cast<uint32_t>(e) << (16 * (i & 1));
+        }
+    }
+}
+
+// Elements at .. at + 3 of a vector of n floats (16-byte aligned), which all
+// threads of a warp read together.
+__device__ __forceinline__ float4 load_columns(const float* x, int at, int n) {
+    if (at + 4 <= n) return __ldg(reinterpret_cast<const float4*>(x + at));
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (at < n) v.x = __ldg(x + at);
+    if (at + 1 < n) v.y = __ldg(x + at + 1);
+    if (at + 2 < n) v.z = __ldg(x + at + 2);
+    return v;
+}
+
+template <int kAct>
+__device__ __forceinline__ void activate32(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activation(kAct, v[i]);
+}
+
+// The values of 32 accumulator columns of one row; sa: the row's scale.
+// Returns their largest magnitude inside D (ordered bits) when it is wanted,
+// before the division by the output's scale.
+__device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col0, const uint32_t (&r)[32],
+                                           const uint32_t (&res)[16], float sa, ByScale out,
+                                           float (&v)[32]) {
+    const float sb = p.sb == nullptr || p.epi.sb_step != 0 ? 1.0f : __ldg(p.sb);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float4 s = make_float4(sb, sb, sb, sb), b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p.epi.sb_step != 0) s = load_columns(p.sb, col0 + 4 * j, p.N);
+        if (p.epi.bias != nullptr) b = load_columns(p.epi.bias, col0 + 4 * j, p.N);
+        v[4 * j] = fmaf(__uint_as_float(r[4 * j]), sa * s.x, b.x);
+        v[4 * j + 1] = fmaf(__uint_as_float(r[4 * j + 1]), sa * s.y, b.y);
+        v[4 * j + 2] = fmaf(__uint_as_float(r[4 * j + 2]), sa * s.z, b.z);
+        v[4 * j + 3] = fmaf(__uint_as_float(r[4 * j + 3]), sa * s.w, b.w);
+    }
+    switch (p.epi.act) {
+        case DG_ACT_RELU: activate32<DG_ACT_RELU>(v); break;
+        case DG_ACT_GELU: activate32<DG_ACT_GELU>(v); break;
+        case DG_ACT_GELU_TANH: activate32<DG_ACT_GELU_TANH>(v); break;
+        case DG_ACT_SILU: activate32<DG_ACT_SILU>(v); break;
+        default: break;
+    }
+    if (p.epi.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float2 x;
+            if (p.epi.residual_fp16 != 0)
+                x = f16x2_to_f32x2(res[i]);
+            else
+                x = make_float2(__uint_as_float(res[i] << 16), __uint_as_float(res[i] & 0xFFFF0000u));
+            v[2 * i] += x.x;
+            v[2 * i + 1] += x.y;
+        }
+    }
+    uint32_t top = 0u;
+    if (p.amax_out != nullptr && row_ok) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (col0 + i < p.N) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    if (p.out_kind == kOutE4M3) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = v[i] * out.pre * out.inv;
+    }
+    return top;
+}
+
+// A row's scale of A (1 without scales, and for rows outside).
+__device__ __forceinline__ float scale_of_row(const Params& p, int row, bool row_ok) {
+    return p.sa == nullptr || !row_ok ? 1.0f : __ldg(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
+}
+
+__device__ __forceinline__ ByScale output_scale(int out_kind, const float* sd) {
+    return out_kind == kOutE4M3 ? by_scale(__ldg(sd)) : ByScale{1.0f, 1.0f};
+}
+
+// The fused kernels' maximum, one warp's: already of the values themselves.
+__device__ __forceinline__ void publish_top(uint32_t* amax_out, uint32_t top) {
+    if (amax_out == nullptr) return;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((threadIdx.x & 31) == 0 && top != 0u) atomicMax(amax_out, top);
 }
 
 // Waits until every bulk store this thread committed has finished reading

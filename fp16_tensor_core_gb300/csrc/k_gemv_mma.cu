@@ -30,6 +30,7 @@
 // zeros by predicated loads; stores are predicated on m < M, n < N.
 #include <cuda_runtime.h>
 
+#include "activation.cuh"
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
 
@@ -89,12 +90,12 @@ constexpr int min_ctas_per_sm() { return W >= 8 ? 3 : 6; }
 template <int W>
 constexpr int batch_for() { return W == 2 ? 8 : W == 3 ? 6 : 4; }
 
-template <int MT, bool kFp16, int W, int U>
+template <int MT, bool kFp16, int W, int U, bool kFused>
 __global__ void __launch_bounds__(W * 32, min_ctas_per_sm<W>())
 gemv_mma_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
-                void* __restrict__ D, int M, int N, int K, const float* __restrict__ sa,
+                void* D, int M, int N, int K, const float* __restrict__ sa,
                 const float* __restrict__ sb, const float* __restrict__ sd, int out_kind,
-                uint32_t* __restrict__ amax_out) {
+                uint32_t* __restrict__ amax_out, const Epilogue epi) {
     __shared__ float4 red[W][MT][32];   // per-warp partial accumulators
     __shared__ float scales[3];          // sa, sb, sd: loaded first, used last
     pdl_wait();
@@ -105,7 +106,7 @@ gemv_mma_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
     const uint64_t policy = evict_first_policy();
     if (threadIdx.x == 0) {
         scales[0] = sa != nullptr ? ld_scalar(sa) : 1.0f;
-        scales[1] = sa != nullptr ? ld_scalar(sb) : 1.0f;
+        scales[1] = sa != nullptr ? ld_scalar(sb) : 1.0f;   // (of row 0, when there is one a row)
         scales[2] = out_kind == kOutE4M3 ? ld_scalar(sd) : 1.0f;
     }
 
@@ -190,6 +191,49 @@ gemv_mma_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
         v[j][2] = t.z;
         v[j][3] = t.w;
     }
+    if constexpr (kFused) {
+        // Lane (g, q): D^T rows n = r0 + g and r0 + g + 8, columns m = 8 j + 2 q
+        // and 8 j + 2 q + 1, as below.
+        const ByScale by = by_scale(scales[2]);
+        float sbn[2], bias[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = min(r0 + g + 8 * h, N - 1);
+            sbn[h] = epi.sb_step != 0 ? ld_scalar(sb + n) : scales[1];
+            bias[h] = epi.bias != nullptr ? ld_scalar(epi.bias + n) : 0.0f;
+        }
+        uint32_t top = 0u;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int h = i >> 1, n = r0 + g + 8 * h, m = 8 * j + 2 * q + (i & 1);
+                if (n >= N || m >= M) continue;
+                const int64_t off = static_cast<int64_t>(m) * N + n;
+                const float sam = epi.sa_step != 0 ? ld_scalar(sa + m) : scales[0];
+                float y = activation(epi.act, fmaf(v[j][i], sam * sbn[h], bias[h]));
+                if (epi.residual != nullptr) {
+                    uint16_t e;   // not the read-only path: D may be the residual
+                    asm volatile("ld.global.u16 %0, [%1];" : "=h"(e) : "l"(epi.residual + off));
+                    y += epi.residual_fp16 != 0 ? f16x2_to_f32x2(e).x
+                                                : __uint_as_float(static_cast<uint32_t>(e) << 16);
+                }
+                top = max(top, __float_as_uint(y) & 0x7FFFFFFFu);
+                if (out_kind == kOutE4M3)
+                    static_cast<uint8_t*>(D)[off] =
+                        static_cast<uint8_t>(f32x2_to_e4m3x2(y * by.pre * by.inv, 0.0f) & 0xFFu);
+                else if (out_kind == kOutFP16)
+                    static_cast<uint16_t*>(D)[off] = static_cast<uint16_t>(f32x2_to_f16x2(y, 0.0f) & 0xFFFFu);
+                else
+                    static_cast<uint16_t*>(D)[off] = static_cast<uint16_t>(f32x2_to_bf16x2(y, 0.0f) & 0xFFFFu);
+            }
+        }
+        if (amax_out != nullptr) {
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            if (lane == 0 && top != 0u) atomicMax(amax_out, top);
+        }
+        return;
+    }
     // Lane (g, q) holds D^T rows n = r0 + g (v[.][0..1]) and r0 + g + 8
     // (v[.][2..3]) at columns m = 8 j + 2 q and 8 j + 2 q + 1.
     const float ab = scales[0] * scales[1];
@@ -225,9 +269,13 @@ gemv_mma_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
 template <int MT, bool kFp16, int W, int U>
 cudaError_t launch_one(const TcLaunch& L, cudaStream_t s) {
     const dim3 grid((L.N + kRowsPerCta - 1) / kRowsPerCta), block(W * 32);
-    return launch_kernel(gemv_mma_kernel<MT, kFp16, W, U>, grid, block, 0, s,
-                         static_cast<const uint8_t*>(L.A), static_cast<const uint8_t*>(L.B), L.D,
-                         L.M, L.N, L.K, L.sa, L.sb, L.sd, L.out_kind, L.amax_out);
+    const uint8_t* A = static_cast<const uint8_t*>(L.A);
+    const uint8_t* B = static_cast<const uint8_t*>(L.B);
+    if (L.epi != nullptr)
+        return launch_kernel(gemv_mma_kernel<MT, kFp16, W, U, true>, grid, block, 0, s, A, B, L.D, L.M, L.N,
+                             L.K, L.sa, L.sb, L.sd, L.out_kind, L.amax_out, *L.epi);
+    return launch_kernel(gemv_mma_kernel<MT, kFp16, W, U, false>, grid, block, 0, s, A, B, L.D, L.M, L.N, L.K,
+                         L.sa, L.sb, L.sd, L.out_kind, L.amax_out, Epilogue{});
 }
 
 template <int MT, bool kFp16>

@@ -628,6 +628,41 @@ dg_status dg_activate_grad(const dg_rows* dy, const dg_rows* x, const uint8_t* x
 dg_status dg_activate_grad_scratch(int64_t rows, int64_t cols, int gated, int sm_count,
                                    int64_t* bytes);
 
+/* What a product may have in its epilogue. */
+typedef struct {
+    const float* scale_a;   /* FP32[1], or with scale_a_rows != 0 FP32[M]: one a row of A       */
+    const float* scale_b;   /* FP32[1], or with scale_b_rows != 0 FP32[N]: one a row of B       */
+    int scale_a_rows;
+    int scale_b_rows;
+    const float* bias;      /* FP32[N], or NULL                                                 */
+    dg_activation act;
+    const void* residual;   /* M x N dense of residual_type, or NULL                            */
+    dg_dtype residual_type; /* DG_BF16 or DG_FP16                                               */
+    const float* scale_d;   /* FP32[1]; required iff out is DG_E4M3                             */
+    float* amax_d;          /* FP32[1], or NULL                                                 */
+} dg_epilogue;
+
+/* dg_fp8_gemm with more in its epilogue, on the accumulators in FP32:
+ *   v      = act(scale_a[m] * scale_b[n] * sum_k A[m,k] * B[n,k] + bias[n]) + residual[m,n]
+ *   D[m,n] = out(v), or E4M3(v / *scale_d)
+ *   amax_d = max |v| over D (as dg_fp8_gemm_amax; zeroed by the call)
+ * rounded once.  Row scales of A are what dg_rmsnorm_e4m3 and dg_activate
+ * write; a weight quantised by rows has its own (one scale serves either side
+ * as before).  With K == 0 the sum is empty.  D may be the residual itself
+ * when both have the same 16-bit type.  Smooth activations as dg_activate.
+ * Vectors, bias and residual 16-byte aligned, scalars 4-byte.  Operands, sizes
+ * and other errors as dg_fp8_gemm; paths as there, but that one row of A never
+ * takes the CUDA-core GEMV. */
+dg_status dg_fp8_gemm_fused(const uint8_t* A, const uint8_t* B, void* D, int64_t M, int64_t N,
+                            int64_t K, const dg_epilogue* epilogue, dg_dtype out,
+                            dg_stream_t stream);
+
+/* The same on FP16 operands (as dg_hgemm; out is DG_FP16 or DG_BF16).  The
+ * scales are optional: both or neither. */
+dg_status dg_hgemm_fused(const uint16_t* A, const uint16_t* B, void* D, int64_t M, int64_t N,
+                         int64_t K, const dg_epilogue* epilogue, dg_dtype out,
+                         dg_stream_t stream);
+
 /* Tile / path selection for a GEMM shape, host only (launches nothing).
  * [FP8-guide] §2.2, §3.1, §3.3 (per-shape tile choice, smaller tiles where
  * edge waste is high) and [HGEMM-L2] §3.1-§3.3 (tile and stage count chosen
