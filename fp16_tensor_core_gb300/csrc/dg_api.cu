@@ -1112,7 +1112,7 @@ dg_status dg_rmsnorm(const dg_rows* x, const dg_rows* residual, const dg_rows* s
     NormArgs a = norm_args(x, residual, sum, weight, rows, cols, eps);
     a.y = elements(y);
     a.y_stride = y->stride;
-    return from_cuda(launch_rmsnorm(a, kNormHalf, dtype == DG_FP16, nullptr, st->sm_count,
+    return from_cuda(launch_rmsnorm(a, kNormHalf, dtype == DG_FP16, st->sm_count,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1129,7 +1129,7 @@ dg_status dg_rmsnorm_e4m3(const dg_rows* x, const dg_rows* residual, const dg_ro
     NormArgs a = norm_args(x, residual, sum, weight, rows, cols, eps);
     a.q = q;
     a.row_scale = row_scale;
-    return from_cuda(launch_rmsnorm(a, kNormRows, dtype == DG_FP16, nullptr, st->sm_count,
+    return from_cuda(launch_rmsnorm(a, kNormRows, dtype == DG_FP16, st->sm_count,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1150,7 +1150,8 @@ dg_status dg_rmsnorm_e4m3_amax(const dg_rows* x, const dg_rows* residual, const 
     a.q = q;
     a.scale = scale;
     a.amax_bits = reinterpret_cast<uint32_t*>(amax_out);
-    return from_cuda(launch_rmsnorm(a, kNormTensor, dtype == DG_FP16, next_scale_out, st->sm_count,
+    a.next_scale = next_scale_out;
+    return from_cuda(launch_rmsnorm(a, kNormTensor, dtype == DG_FP16, st->sm_count,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 

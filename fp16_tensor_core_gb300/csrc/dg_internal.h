@@ -303,8 +303,9 @@ struct NormArgs {
     float* row_scale;      // kNormRows
     const float* scale;    // kNormTensor
     uint32_t* amax_bits;   // kNormTensor
+    float* next_scale;     // kNormTensor, or null
 };
-cudaError_t launch_rmsnorm(const NormArgs& a, int out, bool fp16, float* next_scale, int sm_count, cudaStream_t s);
+cudaError_t launch_rmsnorm(const NormArgs& a, int out, bool fp16, int sm_count, cudaStream_t s);
 struct NormGradArgs {
     const uint16_t* x;
     const uint16_t* dy;

@@ -243,39 +243,61 @@ __device__ __forceinline__ void load_residual(const Params& p, int row, bool row
     }
 }
 
-// Elements at .. at + 3 of a vector of n floats (16-byte aligned), which all
-// threads of a warp read together.
-__device__ __forceinline__ float4 load_columns(const float* x, int at, int n) {
-    if (at + 4 <= n) return __ldg(reinterpret_cast<const float4*>(x + at));
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (at < n) v.x = __ldg(x + at);
-    if (at + 1 < n) v.y = __ldg(x + at + 1);
-    if (at + 2 < n) v.z = __ldg(x + at + 2);
-    return v;
+// What an epilogue warp holds of its tile's columns in shared memory: each
+// column's scale of B and bias, as pairs of columns {scale, scale, bias, bias}
+// so that one 16-byte read serves two columns.  Loaded while the main loop
+// runs; a tile's columns past N get zeros.
+constexpr int columns_bytes(int bn) { return 4 * bn * 8; }   // of the four warps
+
+template <int BN>
+__device__ __forceinline__ void stage_columns(const Params& p, float* columns, int col0, int lane) {
+    float s[BN / 32], b[BN / 32];
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i) {
+        const int n = col0 + 32 * i + lane;
+        s[i] = p.sb == nullptr ? 1.0f : 0.0f;
+        b[i] = 0.0f;
+        if (n < p.N && p.sb != nullptr) s[i] = __ldg(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
+        if (n < p.N && p.epi.bias != nullptr) b[i] = __ldg(p.epi.bias + n);
+    }
+    __syncwarp();   // every lane has read the last tile's
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i) {
+        const int at = 2 * (32 * i + (lane & ~1)) + (lane & 1);
+        columns[at] = s[i];
+        columns[at + 2] = b[i];
+    }
+    __syncwarp();
+}
+
+// Moves the rest of a tile row's residual into L2, 128 bytes a time.
+template <int BN>
+__device__ __forceinline__ void prefetch_residual(const Params& p, int row, bool row_ok, int col0) {
+    if (p.epi.residual == nullptr || !row_ok) return;
+    const uint16_t* src = p.epi.residual + static_cast<int64_t>(row) * p.N + col0;
+#pragma unroll
+    for (int i = 32; i < BN; i += 64)
+        if (col0 + i < p.N) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + i));
 }
 
 template <int kAct>
-__device__ __forceinline__ void activate32(float (&v)[32]) {
+__device__ __forceinline__ void activate32(pair (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activation(kAct, v[i]);
+    for (int i = 0; i < 16; ++i) v[i] = activation(kAct, v[i]);
 }
 
-// The values of 32 accumulator columns of one row; sa: the row's scale.
-// Returns their largest magnitude inside D (ordered bits) when it is wanted,
-// before the division by the output's scale.
+// The values of 32 accumulator columns of one row; sa: the row's scale,
+// columns: theirs (stage_columns).  Returns their largest magnitude inside D
+// (ordered bits) when it is wanted, before the division by the output's scale.
 __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col0, const uint32_t (&r)[32],
-                                           const uint32_t (&res)[16], float sa, ByScale out,
-                                           float (&v)[32]) {
-    const float sb = p.sb == nullptr || p.epi.sb_step != 0 ? 1.0f : __ldg(p.sb);
+                                           const uint32_t (&res)[16], float sa, const float* columns, ByScale out,
+                                           float (&f)[32]) {
+    pair v[16];
+    const pair row_scale = pair_of(sa);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float4 s = make_float4(sb, sb, sb, sb), b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (p.epi.sb_step != 0) s = load_columns(p.sb, col0 + 4 * j, p.N);
-        if (p.epi.bias != nullptr) b = load_columns(p.epi.bias, col0 + 4 * j, p.N);
-        v[4 * j] = fmaf(__uint_as_float(r[4 * j]), sa * s.x, b.x);
-        v[4 * j + 1] = fmaf(__uint_as_float(r[4 * j + 1]), sa * s.y, b.y);
-        v[4 * j + 2] = fmaf(__uint_as_float(r[4 * j + 2]), sa * s.z, b.z);
-        v[4 * j + 3] = fmaf(__uint_as_float(r[4 * j + 3]), sa * s.w, b.w);
+    for (int i = 0; i < 16; ++i) {
+        const ulonglong2 c = reinterpret_cast<const ulonglong2*>(columns)[i];
+        v[i] = pair_fma(pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), pair_mul(row_scale, c.x), c.y);
     }
     switch (p.epi.act) {
         case DG_ACT_RELU: activate32<DG_ACT_RELU>(v); break;
@@ -292,21 +314,31 @@ __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col
                 x = f16x2_to_f32x2(res[i]);
             else
                 x = make_float2(__uint_as_float(res[i] << 16), __uint_as_float(res[i] & 0xFFFF0000u));
-            v[2 * i] += x.x;
-            v[2 * i + 1] += x.y;
+            v[i] = pair_add(v[i], pair_of(x.x, x.y));
         }
     }
-    uint32_t top = 0u;
+    float top = 0.0f;
     if (p.amax_out != nullptr && row_ok) {
+        if (col0 + 32 <= p.N) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (col0 + i < p.N) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    }
-    if (p.out_kind == kOutE4M3) {
+            for (int i = 0; i < 16; ++i) top = pair_top(v[i], top);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = v[i] * out.pre * out.inv;
+            for (int i = 0; i < 16; ++i) {
+                const float2 x = floats_of(v[i]);
+                if (col0 + 2 * i < p.N) top = pair_top(pair_of(x.x), top);
+                if (col0 + 2 * i + 1 < p.N) top = pair_top(pair_of(x.y), top);
+            }
+        }
     }
-    return top;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (p.out_kind == kOutE4M3) v[i] = pair_mul(pair_mul(v[i], pair_of(out.pre)), pair_of(out.inv));
+        const float2 x = floats_of(v[i]);
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+    }
+    return __float_as_uint(top);
 }
 
 // A row's scale of A (1 without scales, and for rows outside).

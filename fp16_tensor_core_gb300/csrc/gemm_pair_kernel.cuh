@@ -22,16 +22,17 @@ constexpr int kHalfBM = 128;   // rows of it per CTA
 constexpr int kStagingBytes = 4 * kBoxBytes;
 
 // Stage count: what fits in 227 KB beside the barrier block (1 KB, keeping
-// the staging boxes 1024-byte aligned) and the staging boxes, at most 8
+// the staging boxes 1024-byte aligned), the staging boxes and a fused
+// epilogue's columns, at most 8
 // (4 with two K blocks per stage).
-constexpr int pair_stages_for(int bn, int kps = 1) {
-    const int st = (kSmemLimit - 1024 - 1024 - kStagingBytes) /
+constexpr int pair_stages_for(int bn, int kps = 1, bool fused = false) {
+    const int st = (kSmemLimit - 1024 - 1024 - kStagingBytes - (fused ? columns_bytes(bn) : 0)) /
                    (kps * (kHalfBM * kBKBytes + (bn / 2) * kBKBytes));
     return st > 8 / kps ? 8 / kps : st;
 }
 
 // KPS: K blocks per pipeline stage (1 or 2, adjacent blocks loaded together).
-template <int BN, int STAGES, bool kFp16In, int KPS = 1>
+template <int BN, int STAGES, bool kFp16In, int KPS = 1, bool kFused = false>
 struct PairCfg {
     static constexpr int kBK = kFp16In ? 64 : 128;         // K elements per K block
     static constexpr int kABox = kHalfBM * kBKBytes;       // this CTA's 128 rows of A
@@ -42,7 +43,8 @@ struct PairCfg {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * BN);
     static constexpr int kStagingOff = STAGES * kStageBytes + 1024;   // after the barriers
-    static constexpr int kSmemBytes = 1024 + kStagingOff + kStagingBytes;
+    static constexpr int kColumnsOff = kStagingOff + kStagingBytes;   // fused: its columns' scales, bias
+    static constexpr int kSmemBytes = 1024 + kColumnsOff + (kFused ? columns_bytes(BN) : 0);
     static constexpr uint32_t kIdesc = idesc_f32acc(kPairBM, BN, 0, 0);
     static_assert(BN % 32 == 0 && BN >= 128 && BN <= 256, "BN");
     static_assert(kBBytes % 1024 == 0, "1024-byte aligned B stages (128-byte swizzle atoms)");
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_d, const Params p) {
-    using C = PairCfg<BN, STAGES, kFp16In, KPS>;
+    using C = PairCfg<BN, STAGES, kFp16In, KPS, kFused>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -324,6 +326,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         float alpha = 1.0f;
         if (!kFused && p.sa != nullptr) alpha = (*p.sa) * (*p.sb);
         if (!kFused && p.out_kind == kOutE4M3) alpha = __fdiv_rn(alpha, *p.sd);
+        float* columns = reinterpret_cast<float*>(smem + C::kColumnsOff) + q * 2 * BN;
         const ByScale out_scale = kFused ? output_scale(p.out_kind, p.sd) : ByScale{1.0f, 1.0f};
         const uint32_t leader_acc_empty = map_to_rank(acc_empty, 0);
         uint32_t amax_bits = 0u;
@@ -359,7 +362,11 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             uint32_t res[16];
             if constexpr (kFused) {
                 sa = scale_of_row(p, row, row_ok);
-                if (it.part <= 0) load_residual(p, row, row_ok, nt * BN, res);
+                if (it.part <= 0) {
+                    load_residual(p, row, row_ok, nt * BN, res);
+                    prefetch_residual<BN>(p, row, row_ok, nt * BN);
+                    stage_columns<BN>(p, columns, nt * BN, lane);
+                }
             }
             // The four warps continue or leave together (the split tail
             // below synchronises them on a named barrier).
@@ -482,7 +489,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = nt * BN + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, out_scale, v));
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
                         if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
                         stage_values(p, box, v, lane);
                     } else {
@@ -519,7 +526,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = nt * BN + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, out_scale, v));
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
                         if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
                         if (row_ok && col0 < p.N) store_values(p, row, min(32, p.N - col0), col0, v);
                     } else {
@@ -587,7 +594,7 @@ cudaError_t launch_pair(Kern kern, dim3 grid, size_t smem, cudaStream_t s,
 
 template <int BN, int STAGES, bool kFp16In, int KPS = 1, bool kFused = false>
 cudaError_t launch_pair_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s) {
-    using C = PairCfg<BN, STAGES, kFp16In, KPS>;
+    using C = PairCfg<BN, STAGES, kFp16In, KPS, kFused>;
     auto kern = gemm_tc_pair_kernel<BN, STAGES, kFp16In, KPS, kFused>;
     static std::mutex mu;
     static int max_clusters[64] = {};
@@ -673,8 +680,8 @@ cudaError_t launch_pair_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s
 template <int BN, bool kFp16In, bool kFused>
 cudaError_t launch_pair_bn(const TcLaunch& L, const Params& prm, cudaStream_t s) {
     if (L.plan->block_k == 2 * PairCfg<BN, 1, kFp16In>::kBK)
-        return launch_pair_cfg<BN, pair_stages_for(BN, 2), kFp16In, 2, kFused>(L, prm, s);
-    return launch_pair_cfg<BN, pair_stages_for(BN), kFp16In, 1, kFused>(L, prm, s);
+        return launch_pair_cfg<BN, pair_stages_for(BN, 2, kFused), kFp16In, 2, kFused>(L, prm, s);
+    return launch_pair_cfg<BN, pair_stages_for(BN, 1, kFused), kFp16In, 1, kFused>(L, prm, s);
 }
 
 template <bool kFp16In, bool kFused>

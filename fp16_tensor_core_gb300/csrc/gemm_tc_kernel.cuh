@@ -24,10 +24,11 @@ constexpr int kGroupSmem = 4 * (kMaxGroups + 1) + 12;
 constexpr int kStagingBytes = 4 * kBoxBytes;
 
 // Stage count = what fits in 227 KB beside the barrier block (1 KB, keeping
-// the staging boxes 1024-byte aligned), the staging boxes and the grouped
-// variant's tile prefix, at most 8 (4 with two K blocks per stage).
-constexpr int stages_for(int bn, bool grouped = false, int kps = 1) {
-    const int st = (kSmemLimit - 1024 - 1024 - kStagingBytes - (grouped ? kGroupSmem : 0)) /
+// the staging boxes 1024-byte aligned), the staging boxes, the grouped
+// variant's tile prefix and the fused one's columns, at most 8 (4 with two K blocks per stage).
+constexpr int stages_for(int bn, bool grouped = false, int kps = 1, bool fused = false) {
+    const int st = (kSmemLimit - 1024 - 1024 - kStagingBytes - (grouped ? kGroupSmem : 0) -
+                    (fused ? columns_bytes(bn) : 0)) /
                    (kps * (kBM * kBKBytes + bn * kBKBytes));
     return st > 8 / kps ? 8 / kps : st;
 }
@@ -35,7 +36,7 @@ constexpr int stages_for(int bn, bool grouped = false, int kps = 1) {
 // KPS: K blocks per pipeline stage (1, or 2: each stage holds two adjacent
 // 128-byte K blocks of every row, so a row's 256 bytes are requested
 // together).
-template <int BN, int STAGES, bool kFp16In, bool kGrouped = false, int KPS = 1>
+template <int BN, int STAGES, bool kFp16In, bool kGrouped = false, int KPS = 1, bool kFused = false>
 struct Cfg {
     static constexpr int kBK = kFp16In ? 64 : 128;        // K elements per K block
     static constexpr int kABox = kBM * kBKBytes;          // 16 KB
@@ -47,7 +48,8 @@ struct Cfg {
     static constexpr int kBarBytes = 256;
     static constexpr int kStagingOff = STAGES * kStageBytes + 1024;   // after the barriers
     static constexpr int kGroupOff = kStagingOff + kStagingBytes;     // grouped: tile prefix
-    static constexpr int kSmemBytes = 1024 + kGroupOff + (kGrouped ? kGroupSmem : 0);
+    static constexpr int kColumnsOff = kGroupOff + (kGrouped ? kGroupSmem : 0);   // fused: its columns' scales, bias
+    static constexpr int kSmemBytes = 1024 + kColumnsOff + (kFused ? columns_bytes(BN) : 0);
     static constexpr uint32_t kIdesc = idesc_f32acc(kBM, BN, 0, 0);
     static_assert(BN % 32 == 0 && BN >= 64 && BN <= 256,
                   "BN: MMA N (multiple of 16, <= 256) and 32-column epilogue chunks");
@@ -71,7 +73,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                const __grid_constant__ CUtensorMap tmap_d,
                const __grid_constant__ CUtensorMap tmap_a_edge,
                const __grid_constant__ CUtensorMap tmap_b_edge, const Params p) {
-    using C = Cfg<BN, STAGES, kFp16In, kGrouped, KPS>;
+    using C = Cfg<BN, STAGES, kFp16In, kGrouped, KPS, kFused>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -297,6 +299,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
         };
         float alpha = alpha_of(0);
         int alpha_g = 0;
+        float* columns = reinterpret_cast<float*>(smem + C::kColumnsOff) + q * 2 * BN;
         const ByScale out_scale = kFused ? output_scale(p.out_kind, p.sd) : ByScale{1.0f, 1.0f};
         uint32_t amax_bits = 0u;
         int acc = 0;
@@ -322,6 +325,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if constexpr (kFused) {
                 sa = scale_of_row(p, row, row_ok);
                 load_residual(p, row, row_ok, T.col0, res);
+                prefetch_residual<BN>(p, row, row_ok, T.col0);
+                stage_columns<BN>(p, columns, T.col0, lane);
             }
             // Every lane waits; the vote reconverges the warp (tcgen05.ld is
             // .sync.aligned) and makes the whole warp leave together.
@@ -351,7 +356,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = T.col0 + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, out_scale, v));
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
                         if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
                         stage_values(p, box, v, lane);
                     } else {
@@ -369,7 +374,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = T.col0 + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, out_scale, v));
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
                         if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
                         if (row_ok && col0 < p.N) store_values(p, row, min(32, p.N - col0), col0, v);
                     } else {
@@ -415,7 +420,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
 template <int BN, int STAGES, bool kFp16In, bool kGrouped = false, int KPS = 1, bool kFused = false>
 cudaError_t launch_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s) {
-    using C = Cfg<BN, STAGES, kFp16In, kGrouped, KPS>;
+    using C = Cfg<BN, STAGES, kFp16In, kGrouped, KPS, kFused>;
     static std::mutex mu;
     static bool attr_done[64] = {};
     int dev = 0;
@@ -487,20 +492,20 @@ cudaError_t launch_in(const TcLaunch& L, const Params& prm, cudaStream_t s) {
         // two K blocks per stage: block_k is twice the K block
         case 64:
             if (L.plan->block_k == 2 * (kFp16In ? 64 : 128))
-                return launch_cfg<64, stages_for(64, false, 2), kFp16In, false, 2, kFused>(L, prm, s);
-            return launch_cfg<64, stages_for(64), kFp16In, false, 1, kFused>(L, prm, s);
+                return launch_cfg<64, stages_for(64, false, 2, kFused), kFp16In, false, 2, kFused>(L, prm, s);
+            return launch_cfg<64, stages_for(64, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
         case 96:
             if (L.plan->block_k == 2 * (kFp16In ? 64 : 128))
-                return launch_cfg<96, stages_for(96, false, 2), kFp16In, false, 2, kFused>(L, prm, s);
-            return launch_cfg<96, stages_for(96), kFp16In, false, 1, kFused>(L, prm, s);
+                return launch_cfg<96, stages_for(96, false, 2, kFused), kFp16In, false, 2, kFused>(L, prm, s);
+            return launch_cfg<96, stages_for(96, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
         case 128:
             if (L.plan->block_k == 2 * (kFp16In ? 64 : 128))
-                return launch_cfg<128, stages_for(128, false, 2), kFp16In, false, 2, kFused>(L, prm, s);
-            return launch_cfg<128, stages_for(128), kFp16In, false, 1, kFused>(L, prm, s);
-        case 160: return launch_cfg<160, stages_for(160), kFp16In, false, 1, kFused>(L, prm, s);
-        case 192: return launch_cfg<192, stages_for(192), kFp16In, false, 1, kFused>(L, prm, s);
-        case 224: return launch_cfg<224, stages_for(224), kFp16In, false, 1, kFused>(L, prm, s);
-        default: return launch_cfg<256, stages_for(256), kFp16In, false, 1, kFused>(L, prm, s);
+                return launch_cfg<128, stages_for(128, false, 2, kFused), kFp16In, false, 2, kFused>(L, prm, s);
+            return launch_cfg<128, stages_for(128, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
+        case 160: return launch_cfg<160, stages_for(160, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
+        case 192: return launch_cfg<192, stages_for(192, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
+        case 224: return launch_cfg<224, stages_for(224, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
+        default: return launch_cfg<256, stages_for(256, false, 1, kFused), kFp16In, false, 1, kFused>(L, prm, s);
     }
 }
 

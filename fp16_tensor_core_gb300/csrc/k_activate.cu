@@ -29,208 +29,248 @@
 namespace dg {
 namespace {
 
+// Threads of a block, and blocks an SM at least, by vectors (of each half) a
+// thread: the registers (64, 80, 128) hold a row's input and output.
+template <int NV>
+constexpr int block_limit() { return NV == 4 ? 384 : 512; }
+template <int NV>
+constexpr int block_min() { return NV == 8 ? 1 : 2; }
+constexpr int kLimits[3] = {512, 384, 512};
+constexpr int kPerSm[3] = {1024, 768, 512};
+
 template <int NV, bool kFp16, bool kGated>
-__global__ void __launch_bounds__(kRowThreads) activate_kernel(const ActArgs a) {
+__global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_kernel(const ActArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
     pdl_wait();
-    RowReduce reduce{buffer};
     constexpr int kHalves = kGated ? 2 : 1;
-    const int vectors = a.cols >> 3, t = threadIdx.x, step = blockDim.x;
+    const RowTeam team = row_team(team_size);
+    RowReduce reduce{buffer, team.size};
+    const int vectors = a.cols >> 3;
     uint4 x[kHalves][NV];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[h][i] = make_uint4(0, 0, 0, 0);
     auto fetch = [&](int64_t row) {
+        if (row >= a.rows) return;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (t + i * step < vectors)
-                    x[h][i] = load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + 8 * (t + i * step));
+            for (int i = 0; i < NV; ++i) {
+                const int at = team.at + i * team.size;
+                if (at < vectors) x[h][i] = load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + 8 * at);
+            }
     };
-    int64_t row = blockIdx.x;
-    if (row < a.rows) fetch(row);
-    for (; row < a.rows; row += gridDim.x) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
+    int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;   // the block's rows, together
+    fetch(first + team.row);
+    for (; first < a.rows; first += step) {
+        const int64_t row = first + team.row;
+        const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
         if (a.x_q != nullptr) {
-            uint32_t top[2] = {0, 0};
+            float top[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    float f[8];
+                    pair f[4];
                     unpack8<kFp16>(x[h][i], f);
-                    top[h] = max(top[h], top8(f));
+                    top[h] = top8(f, top[h]);
                 }
-            const uint2 both = reduce.max2(top[0], top[1]);
+            const float2 both = reduce.max2(top[0], top[1]);
             const float scale[2] = {row_scale(both.x), row_scale(both.y)};
-            if (t < kHalves) a.x_scale[row * kHalves + t] = scale[t];
+            if (team.at == 0 && end != 0) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) a.x_scale[row * kHalves + h] = scale[h];
+            }
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 const float by = __frcp_rn(scale[h]);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    if (t + i * step >= vectors) continue;
-                    float f[8];
+                    const int at = team.at + i * team.size;
+                    if (at >= end) continue;
+                    pair f[4];
                     unpack8<kFp16>(x[h][i], f);
-                    *reinterpret_cast<uint2*>(a.x_q + (row * kHalves + h) * a.cols + 8 * (t + i * step)) =
-                        codes8(f, by);
+                    *reinterpret_cast<uint2*>(a.x_q + (row * kHalves + h) * a.cols + 8 * at) = codes8(f, by);
                 }
             }
         }
         if (a.y == nullptr && a.q == nullptr) {
-            if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+            fetch(row + step);
             continue;
         }
-        float y[NV][8];
-        uint32_t top = 0;
+        pair y[NV][4];
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             unpack8<kFp16>(x[0][i], y[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = activation(a.act, y[i][e]);
+            for (int e = 0; e < 4; ++e) y[i][e] = activation(a.act, y[i][e]);
             if constexpr (kGated) {
-                float up[8];
+                pair up[4];
                 unpack8<kFp16>(x[kHalves - 1][i], up);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[i][e] *= up[e];
+                for (int e = 0; e < 4; ++e) y[i][e] = pair_mul(y[i][e], up[e]);
             }
-            top = max(top, top8(y[i]));
+            if (team.at + i * team.size < end) top = top8(y[i], top);
         }
-        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        fetch(row + step);
         if (a.y != nullptr) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (t + i * step < vectors)
-                    *reinterpret_cast<uint4*>(a.y + row * a.y_stride + 8 * (t + i * step)) = pack8<kFp16>(y[i]);
+            for (int i = 0; i < NV; ++i) {
+                const int at = team.at + i * team.size;
+                if (at < end) *reinterpret_cast<uint4*>(a.y + row * a.y_stride + 8 * at) = pack8<kFp16>(y[i]);
+            }
         }
         if (a.q != nullptr) {
             const float scale = row_scale(reduce.max1(top));
             const float by = __frcp_rn(scale);
-            if (t == 0) a.q_scale[row] = scale;
+            if (team.at == 0 && end != 0) a.q_scale[row] = scale;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (t + i * step < vectors)
-                    *reinterpret_cast<uint2*>(a.q + row * a.cols + 8 * (t + i * step)) = codes8(y[i], by);
+            for (int i = 0; i < NV; ++i) {
+                const int at = team.at + i * team.size;
+                if (at < end) *reinterpret_cast<uint2*>(a.q + row * a.cols + 8 * at) = codes8(y[i], by);
+            }
         }
     }
 }
 
-constexpr int kGradThreads = 128;   // 1024 columns a block
+constexpr int kGradThreads = 128;   // 1024 columns a block, or fewer and several rows at once
 
 template <bool kFp16, bool kGated, bool kCodes>
-__global__ void __launch_bounds__(kGradThreads) activate_grad_kernel(const ActGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads) activate_grad_kernel(const ActGradArgs a, int across) {
+    __shared__ float4 columns[kGradThreads][4];   // narrow rows: the threads' sums
     pdl_wait();
     constexpr int kHalves = kGated ? 2 : 1;
-    const int c = 8 * static_cast<int>(blockIdx.x * kGradThreads + threadIdx.x);
-    if (c >= a.cols) return;
-    const int64_t first = a.rows * blockIdx.y / gridDim.y, end = a.rows * (blockIdx.y + 1) / gridDim.y;
+    // `across` threads (a power of two) side by side, the others on other rows
+    const int t = threadIdx.x, down = kGradThreads / across;
+    const int c = 8 * static_cast<int>(blockIdx.x * across + (t & (across - 1)));
     const int64_t width = static_cast<int64_t>(kHalves) * a.cols;
-    float sums[kHalves][8];
+    const int64_t first = a.rows * blockIdx.y / gridDim.y, end = a.rows * (blockIdx.y + 1) / gridDim.y;
+    pair sums[kHalves][4];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[h][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) sums[h][e] = 0;
+    if (c < a.cols) {
 #pragma unroll 2
-    for (int64_t row = first; row < end; ++row) {
-        float dy[8], x[kHalves][8];
-        unpack8<kFp16>(load_once(a.dy + row * a.dy_stride + c), dy);
+        for (int64_t row = first + t / across; row < end; row += down) {
+            pair dy[4], x[kHalves][4];
+            unpack8<kFp16>(load_once(a.dy + row * a.dy_stride + c), dy);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-            if constexpr (kCodes)
-                decode8(load_once8(a.x_q + row * width + static_cast<int64_t>(h) * a.cols + c),
-                        __ldg(a.x_scale + row * kHalves + h), x[h]);
-            else
-                unpack8<kFp16>(load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + c), x[h]);
-        }
-        float dx[kHalves][8];
+            for (int h = 0; h < kHalves; ++h) {
+                if constexpr (kCodes)
+                    decode8(load_once8(a.x_q + row * width + static_cast<int64_t>(h) * a.cols + c),
+                            __ldg(a.x_scale + row * kHalves + h), x[h]);
+                else
+                    unpack8<kFp16>(load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + c), x[h]);
+            }
+            pair dx[kHalves][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const ValueSlope f = activation_slope(a.act, x[0][e]);
-            if constexpr (kGated) {
-                dx[0][e] = dy[e] * x[kHalves - 1][e] * f.slope;
-                dx[kHalves - 1][e] = dy[e] * f.value;
-            } else {
-                dx[0][e] = dy[e] * f.slope;
+            for (int e = 0; e < 4; ++e) {
+                const ValueSlope f = activation_slope(a.act, x[0][e]);
+                if constexpr (kGated) {
+                    dx[0][e] = pair_mul(pair_mul(dy[e], x[kHalves - 1][e]), f.slope);
+                    dx[kHalves - 1][e] = pair_mul(dy[e], f.value);
+                } else {
+                    dx[0][e] = pair_mul(dy[e], f.slope);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[h][e] = pair_add(sums[h][e], dx[h][e]);
+                *reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + static_cast<int64_t>(h) * a.cols + c) =
+                    pack8<kFp16>(dx[h]);
             }
         }
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sums[h][e] += dx[h][e];
-            *reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + static_cast<int64_t>(h) * a.cols + c) =
-                pack8<kFp16>(dx[h]);
-        }
     }
-    if (a.partials != nullptr) {
+    if (a.partials == nullptr) return;
+    float* part = a.partials + blockIdx.y * width;
+    if (down == 1) {
+        if (c >= a.cols) return;
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-            float4* dst = reinterpret_cast<float4*>(a.partials + blockIdx.y * width + static_cast<int64_t>(h) * a.cols + c);
-            dst[0] = make_float4(sums[h][0], sums[h][1], sums[h][2], sums[h][3]);
-            dst[1] = make_float4(sums[h][4], sums[h][5], sums[h][6], sums[h][7]);
-        }
+        for (int h = 0; h < kHalves; ++h) store_sums(part + static_cast<int64_t>(h) * a.cols + c, sums[h]);
+        return;
     }
-}
-
-// Vectors a thread: up to 2 of each half, more for wide rows.
-int act_vectors_each(int vectors) {
-    for (int each = 2; each < kRowVectors; each *= 2)
-        if (row_threads(vectors, each) <= kRowThreads) return each;
-    return kRowVectors;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) store_sums(reinterpret_cast<float*>(&columns[t][2 * h]), sums[h]);
+    __syncthreads();
+    // thread t of the first row adds up what lies below it, in order
+    if (t >= across || c >= a.cols) return;
+#pragma unroll
+    for (int i = 0; i < 2 * kHalves; ++i) {
+        float4 s = columns[t][i];
+        for (int r = 1; r < down; ++r) {
+            const float4 v = columns[t + r * across][i];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        *reinterpret_cast<float4*>(part + static_cast<int64_t>(i >> 1) * a.cols + c + 4 * (i & 1)) = s;
+    }
 }
 
 template <int NV, bool kFp16>
-cudaError_t run_act(const ActArgs& a, int sm_count, cudaStream_t s) {
-    const int threads = row_threads(a.cols >> 3, NV);
-    const int64_t blocks = std::min<int64_t>(a.rows, static_cast<int64_t>(sm_count) * std::max(1, 1024 / threads));
-    const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
-    return a.gated ? launch_kernel(activate_kernel<NV, kFp16, true>, grid, block, 0, s, a)
-                   : launch_kernel(activate_kernel<NV, kFp16, false>, grid, block, 0, s, a);
+cudaError_t run_act(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
+    const dim3 grid(p.blocks), block(p.threads);
+    return a.gated ? launch_kernel(activate_kernel<NV, kFp16, true>, grid, block, 0, s, a, p.team)
+                   : launch_kernel(activate_kernel<NV, kFp16, false>, grid, block, 0, s, a, p.team);
 }
 
 template <int NV>
-cudaError_t run_act_type(const ActArgs& a, bool fp16, int sm_count, cudaStream_t s) {
-    return fp16 ? run_act<NV, true>(a, sm_count, s) : run_act<NV, false>(a, sm_count, s);
+cudaError_t run_act_type(const ActArgs& a, bool fp16, const RowPlan& p, cudaStream_t s) {
+    return fp16 ? run_act<NV, true>(a, p, s) : run_act<NV, false>(a, p, s);
 }
 
-// Runs of rows: enough blocks for 16 an SM over all column blocks, but no
-// run without a row.
-int act_grad_runs(int64_t rows, int cols, int sm_count) {
-    const int64_t column_blocks = (cols / 8 + kGradThreads - 1) / kGradThreads;
-    const int64_t runs = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * 16 / column_blocks);
-    return static_cast<int>(std::min(rows, runs));
+// The gradient's blocks: `across` threads side by side, `columns` blocks of
+// them, `runs` runs of rows: ten blocks an SM over all column blocks, but no
+// run of fewer rows than a block takes at once.
+struct ActGradPlan {
+    int across, columns, runs;
+};
+ActGradPlan act_grad_plan(int64_t rows, int cols, int sm_count) {
+    ActGradPlan p{1, 1, 1};
+    const int vectors = cols / 8;
+    while (p.across < kGradThreads && p.across < vectors) p.across *= 2;
+    p.columns = (vectors + p.across - 1) / p.across;
+    const int down = kGradThreads / p.across;
+    const int64_t runs = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * 10 / p.columns);
+    p.runs = static_cast<int>(std::min((rows + down - 1) / down, runs));
+    return p;
 }
 
 template <bool kFp16, bool kGated>
-cudaError_t run_act_grad(const ActGradArgs& a, int runs, cudaStream_t s) {
-    const dim3 grid((a.cols / 8 + kGradThreads - 1) / kGradThreads, runs), block(kGradThreads);
-    return a.x_q != nullptr ? launch_kernel(activate_grad_kernel<kFp16, kGated, true>, grid, block, 0, s, a)
-                            : launch_kernel(activate_grad_kernel<kFp16, kGated, false>, grid, block, 0, s, a);
+cudaError_t run_act_grad(const ActGradArgs& a, const ActGradPlan& p, cudaStream_t s) {
+    const dim3 grid(p.columns, p.runs), block(kGradThreads);
+    return a.x_q != nullptr ? launch_kernel(activate_grad_kernel<kFp16, kGated, true>, grid, block, 0, s, a, p.across)
+                            : launch_kernel(activate_grad_kernel<kFp16, kGated, false>, grid, block, 0, s, a, p.across);
 }
 
 }  // namespace
 
 cudaError_t launch_activate(const ActArgs& a, bool fp16, int sm_count, cudaStream_t s) {
-    switch (act_vectors_each(a.cols >> 3)) {
-        case 2: return run_act_type<2>(a, fp16, sm_count, s);
-        case 4: return run_act_type<4>(a, fp16, sm_count, s);
-        default: return run_act_type<8>(a, fp16, sm_count, s);
-    }
+    const RowPlan p = row_plan(a.rows, a.cols, sm_count, kLimits, kPerSm);
+    if (p.each == 2) return run_act_type<2>(a, fp16, p, s);
+    if (p.each == 4) return run_act_type<4>(a, fp16, p, s);
+    return run_act_type<8>(a, fp16, p, s);
 }
 
 int64_t activate_grad_scratch_bytes(int64_t rows, int cols, bool gated, int sm_count) {
-    return static_cast<int64_t>(act_grad_runs(rows, cols, sm_count)) * cols * (gated ? 8 : 4);
+    return static_cast<int64_t>(act_grad_plan(rows, cols, sm_count).runs) * cols * (gated ? 8 : 4);
 }
 
 cudaError_t launch_activate_grad(const ActGradArgs& a, bool fp16, float* dbias, int sm_count, cudaStream_t s) {
-    const int runs = act_grad_runs(a.rows, a.cols, sm_count);
-    if (runs > 0) {
-        const cudaError_t e = fp16 ? (a.gated ? run_act_grad<true, true>(a, runs, s) : run_act_grad<true, false>(a, runs, s))
-                                   : (a.gated ? run_act_grad<false, true>(a, runs, s) : run_act_grad<false, false>(a, runs, s));
+    const ActGradPlan p = act_grad_plan(a.rows, a.cols, sm_count);
+    if (a.rows > 0) {
+        const cudaError_t e = fp16 ? (a.gated ? run_act_grad<true, true>(a, p, s) : run_act_grad<true, false>(a, p, s))
+                                   : (a.gated ? run_act_grad<false, true>(a, p, s) : run_act_grad<false, false>(a, p, s));
         if (e != cudaSuccess) return e;
     }
     return dbias == nullptr ? cudaSuccess
-                            : launch_join_columns(a.partials, runs, a.gated ? 2 * a.cols : a.cols, dbias, s);
+                            : launch_join_columns(a.partials, p.runs, a.gated ? 2 * a.cols : a.cols, dbias, s);
 }
 
 }  // namespace dg

@@ -34,26 +34,39 @@ namespace {
 // A sum of squares past FP32's range is taken again of elements times this.
 constexpr float kDown = 0x1p-64f;
 
+// Threads of a block, and blocks an SM at least, by vectors a thread: the
+// registers (64, 80, 128) hold a row and the next row's loads.
+template <int NV>
+constexpr int block_limit() { return NV == 4 ? 384 : 512; }
+template <int NV>
+constexpr int block_min() { return NV == 8 ? 1 : 2; }
+constexpr int kLimits[3] = {512, 384, 512};
+constexpr int kPerSm[3] = {1024, 768, 512};
+
+// A vector of the weight: every block reads it for every row, from L1.
+__device__ __forceinline__ uint4 weight_at(const uint16_t* weight, int at) {
+    return __ldg(reinterpret_cast<const uint4*>(weight) + at);
+}
+
 template <int NV, bool kFp16, int kOut>
-__global__ void __launch_bounds__(kRowThreads) rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_kernel(const NormArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
     pdl_wait();
-    RowReduce reduce{buffer};
-    const int vectors = a.cols >> 3, t = threadIdx.x, step = blockDim.x;
+    const RowTeam team = row_team(team_size);
+    RowReduce reduce{buffer, team.size};
+    const int vectors = a.cols >> 3;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    uint4 w[NV], x[NV], r[NV];
+    uint4 x[NV], r[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        w[i] = x[i] = r[i] = make_uint4(0, 0, 0, 0);
-        if (a.weight != nullptr && t + i * step < vectors)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(a.weight) + t + i * step);
-    }
+    for (int i = 0; i < NV; ++i) x[i] = r[i] = make_uint4(0, 0, 0, 0);
     auto fetch = [&](int64_t row) {
+        if (row >= a.rows) return;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (t + i * step >= vectors) continue;
-            x[i] = load_once(a.x + row * a.x_stride + 8 * (t + i * step));
-            if (a.residual != nullptr) r[i] = load_once(a.residual + row * a.residual_stride + 8 * (t + i * step));
+            const int at = team.at + i * team.size;
+            if (at >= vectors) continue;
+            x[i] = load_once(a.x + row * a.x_stride + 8 * at);
+            if (a.residual != nullptr) r[i] = load_once(a.residual + row * a.residual_stride + 8 * at);
         }
     };
     float pre = 1.0f, by = 0.0f;
@@ -62,206 +75,262 @@ __global__ void __launch_bounds__(kRowThreads) rmsnorm_kernel(const NormArgs a) 
         pre = given.pre;
         by = given.inv;
     }
-    uint32_t tensor_top = 0;
-    int64_t row = blockIdx.x;
-    if (row < a.rows) fetch(row);
-    for (; row < a.rows; row += gridDim.x) {
-        float v[NV][8];
-        float squares = 0.0f;
+    float tensor_top = 0.0f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
+    int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;   // the block's rows, together
+    fetch(first + team.row);
+    for (; first < a.rows; first += step) {
+        const int64_t row = first + team.row;
+        const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
+        pair v[NV][4], squares = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
             unpack8<kFp16>(x[i], v[i]);
             if (a.residual != nullptr) {
-                float add[8];
+                pair add[4];
                 unpack8<kFp16>(r[i], add);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] += add[e];
+                for (int e = 0; e < 4; ++e) v[i][e] = pair_add(v[i][e], add[e]);
             }
-            if (a.sum != nullptr && t + i * step < vectors)
-                *reinterpret_cast<uint4*>(a.sum + row * a.sum_stride + 8 * (t + i * step)) = pack8<kFp16>(v[i]);
+            if (a.sum != nullptr && at < end)
+                *reinterpret_cast<uint4*>(a.sum + row * a.sum_stride + 8 * at) = pack8<kFp16>(v[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) squares = fmaf(v[i][e], v[i][e], squares);
+            for (int e = 0; e < 4; ++e) squares = pair_fma(v[i][e], v[i][e], squares);
         }
-        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
-        squares = reduce.sum(squares);
-        float eps = a.eps;
-        if (!(squares <= 3.0e38f)) {   // the whole block
-            squares = 0.0f;
+        fetch(row + step);
+        float total = reduce.sum(pair_sum(squares)), eps = a.eps;
+        // (a vote: rows of a warp differ, and the reduction takes all of it)
+        const bool again = !(total <= 3.0e38f);
+        if (team.size < 32 ? __any_sync(0xFFFFFFFFu, again) : again) {
+            const float down = again ? kDown : 1.0f;
+            squares = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[i][e] *= kDown;
-                    squares = fmaf(v[i][e], v[i][e], squares);
+                for (int e = 0; e < 4; ++e) {
+                    v[i][e] = pair_mul(v[i][e], pair_of(down));
+                    squares = pair_fma(v[i][e], v[i][e], squares);
                 }
-            squares = reduce.sum(squares);
-            eps = eps * kDown * kDown;
+            total = reduce.sum(pair_sum(squares));
+            eps = eps * down * down;
         }
-        const float inv = rsqrtf(fmaf(squares, inv_cols, eps));
-        uint32_t top = 0;
+        const float inv = rsqrtf(fmaf(total, inv_cols, eps));
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[8];
-            unpack8<kFp16>(w[i], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * inv * (a.weight != nullptr ? f[e] : 1.0f);
-            if (kOut != kNormHalf && t + i * step < vectors) top = max(top, top8(v[i]));
+            for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(inv));
+            if (a.weight != nullptr && team.at + i * team.size < vectors) {
+                pair f[4];
+                unpack8<kFp16>(weight_at(a.weight, team.at + i * team.size), f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], f[e]);
+            }
+            if (kOut != kNormHalf && team.at + i * team.size < end) top = top8(v[i], top);
         }
         if constexpr (kOut == kNormRows) {
             const float scale = row_scale(reduce.max1(top));
             by = __frcp_rn(scale);
-            if (t == 0) a.row_scale[row] = scale;
+            if (team.at == 0 && end != 0) a.row_scale[row] = scale;
         }
-        if constexpr (kOut == kNormTensor) tensor_top = max(tensor_top, top);
+        if constexpr (kOut == kNormTensor)   // (fmaxf would drop a NaN)
+            tensor_top = __uint_as_float(max(__float_as_uint(tensor_top), __float_as_uint(top)));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int at = t + i * step;
-            if (at >= vectors) continue;
+            const int at = team.at + i * team.size;
+            if (at >= end) continue;
             if constexpr (kOut == kNormHalf) {
                 *reinterpret_cast<uint4*>(a.y + row * a.y_stride + 8 * at) = pack8<kFp16>(v[i]);
             } else {
                 if constexpr (kOut == kNormTensor) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] *= pre;
+                    for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(pre));
                 }
                 *reinterpret_cast<uint2*>(a.q + row * a.cols + 8 * at) = codes8(v[i], by);
             }
         }
     }
     if constexpr (kOut == kNormTensor) {
-        tensor_top = reduce.max1(tensor_top);
-        if (t == 0 && tensor_top != 0) atomicMax(a.amax_bits, tensor_top);
-    }
-}
-
-// amax / 448 (1 for an all-zero tensor), when the blocks' maxima are in.
-__global__ void next_scale_kernel(const float* amax, float* scale) {
-    pdl_wait();
-    const float a = *amax;
-    *scale = a == 0.0f ? 1.0f : __fdiv_rn(a, 448.0f);
-}
-
-template <int NV, bool kFp16>
-__global__ void __launch_bounds__(kRowThreads) rmsnorm_grad_kernel(const NormGradArgs a) {
-    __shared__ float2 buffer[2][kRowThreads / 32];
-    pdl_wait();
-    RowReduce reduce{buffer};
-    const int vectors = a.cols >> 3, t = threadIdx.x, step = blockDim.x;
-    const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    uint4 w[NV];
-    float dw[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (a.weight != nullptr && t + i * step < vectors)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(a.weight) + t + i * step);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
-    }
-    uint4 x[NV], d[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = d[i] = make_uint4(0, 0, 0, 0);
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (t + i * step >= vectors) continue;
-            x[i] = load_once(a.x + row * a.x_stride + 8 * (t + i * step));
-            d[i] = load_once(a.dy + row * a.dy_stride + 8 * (t + i * step));
-        }
-    };
-    int64_t row = blockIdx.x;
-    if (row < a.rows) fetch(row);
-    for (; row < a.rows; row += gridDim.x) {
-        float v[NV][8], dy[NV][8];
-        float squares = 0.0f, dot = 0.0f;
-        // g = dy w, formed where it is needed: registers
-        auto g_of = [&](int i, float (&g)[8]) {
-            if (a.weight != nullptr) unpack8<kFp16>(w[i], g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = a.weight != nullptr ? g[e] * dy[i][e] : dy[i][e];
-        };
-        auto sums = [&]() {
-            squares = dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float g[8];
-                g_of(i, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    squares = fmaf(v[i][e], v[i][e], squares);
-                    dot = fmaf(g[e], v[i][e], dot);
+        const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tensor_top));
+        if ((threadIdx.x & 31) == 0 && bits != 0) atomicMax(a.amax_bits, bits);
+        if (a.next_scale != nullptr) {
+            // The last block to arrive forms the next call's scale; the word
+            // counts the arrivals until then (it is zeroed with the maximum).
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                __threadfence();
+                if (atomicAdd(reinterpret_cast<uint32_t*>(a.next_scale), 1u) == gridDim.x - 1) {
+                    __threadfence();
+                    *a.next_scale = scale_of_amax(__uint_as_float(atomicOr(a.amax_bits, 0u)));
                 }
             }
-            const float2 both = reduce.sum2(squares, dot);
-            squares = both.x;
-            dot = both.y;
-        };
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack8<kFp16>(x[i], v[i]);
-            unpack8<kFp16>(d[i], dy[i]);
-        }
-        uint4 add[NV];
-        if (a.dsum != nullptr) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (t + i * step < vectors) add[i] = load_once(a.dsum + row * a.dsum_stride + 8 * (t + i * step));
-        }
-        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
-        sums();
-        float eps = a.eps, down = 1.0f;
-        if (!(squares <= 3.0e38f)) {   // the whole block
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] *= kDown;
-            sums();
-            eps = eps * kDown * kDown;
-            down = kDown;
-        }
-        const float inv = rsqrtf(fmaf(squares, inv_cols, eps));
-        const float share = dot * inv * inv_cols;   // mean(g u)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (t + i * step >= vectors) continue;
-            float g[8], out[8];
-            g_of(i, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float u = v[i][e] * inv;
-                dw[i][e] = fmaf(dy[i][e], u, dw[i][e]);
-                out[e] = fmaf(-u, share, g[e]) * inv * down;
-            }
-            if (a.dsum != nullptr) {
-                float extra[8];
-                unpack8<kFp16>(add[i], extra);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) out[e] += extra[e];
-            }
-            *reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + 8 * (t + i * step)) = pack8<kFp16>(out);
-        }
-    }
-    if (a.partials != nullptr) {
-        float* part = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (t + i * step >= vectors) continue;
-            float4* dst = reinterpret_cast<float4*>(part + 8 * (t + i * step));
-            dst[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-            dst[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
         }
     }
 }
 
-// Eight warps take an eighth of the parts each, 32 columns a block.
-__global__ void __launch_bounds__(256) join_columns_kernel(const float* __restrict__ partials, int parts, int cols,
-                                                           float* __restrict__ out) {
-    __shared__ float run[8][32];
+__global__ void zero_words_kernel(uint32_t* a, uint32_t* b) {
+    pdl_wait();
+    *a = 0u;
+    if (b != nullptr) *b = 0u;
+}
+
+// The next scale where no last block can write it: no rows, or the word is
+// the scale that the rows read.
+__global__ void next_scale_kernel(const float* amax, float* scale) {
+    pdl_wait();
+    *scale = scale_of_amax(*amax);
+}
+
+// Columns' sums of a block: the teams of a warp and then the warps are added in
+// order; one partial a block.
+template <int NV>
+constexpr int grad_limit() { return NV == 2 ? 384 : 512; }
+template <int NV>
+constexpr int grad_min() { return NV == 2 ? 2 : 1; }
+constexpr int kGradLimits[3] = {384, 512, 512};
+constexpr int kGradPerSm[3] = {768, 512, 512};
+
+template <int NV, bool kFp16>
+__global__ void __launch_bounds__(grad_limit<NV>(), grad_min<NV>()) rmsnorm_grad_kernel(const NormGradArgs a,
+                                                                                         int team_size) {
+    __shared__ float2 buffer[2][kRowThreads / 32];
+    __shared__ float columns[4][256];   // narrow rows: four warps' sums
+    pdl_wait();
+    const RowTeam team = row_team(team_size);
+    RowReduce reduce{buffer, team.size};
+    const int vectors = a.cols >> 3;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    constexpr bool kAhead = NV == 2;   // the next row's loads in flight: registers
+    pair dw[NV][4];
+    uint4 x[NV], d[NV], next_d[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        x[i] = next_d[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dw[i][e] = 0;
+    }
+    auto fetch = [&](int64_t row) {
+        if (row >= a.rows) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
+            if (at >= vectors) continue;
+            x[i] = load_once(a.x + row * a.x_stride + 8 * at);
+            next_d[i] = load_once(a.dy + row * a.dy_stride + 8 * at);
+        }
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
+    int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;
+    if (kAhead) fetch(first + team.row);
+    for (; first < a.rows; first += step) {
+        const int64_t row = first + team.row;
+        const int end = row < a.rows ? vectors : 0;
+        if (!kAhead) fetch(row);
+        pair v[NV][4];
+        uint4 add[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
+            add[i] = make_uint4(0, 0, 0, 0);
+            if (a.dsum != nullptr && at < end) add[i] = load_once(a.dsum + row * a.dsum_stride + 8 * at);
+            unpack8<kFp16>(x[i], v[i]);
+            d[i] = next_d[i];
+        }
+        if (kAhead) fetch(row + step);
+        // dy, and g = dy w, formed where they are needed: registers
+        auto g_of = [&](int i, pair (&dy)[4], pair (&g)[4]) {
+            unpack8<kFp16>(d[i], dy);
+            const int at = team.at + i * team.size;
+            if (a.weight != nullptr && at < vectors) {
+                unpack8<kFp16>(weight_at(a.weight, at), g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[e] = pair_mul(g[e], dy[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[e] = dy[e];
+            }
+        };
+        float2 both;   // sums of s^2 and of g s
+        auto sums = [&]() {
+            pair squares = 0, dot = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                pair dy[4], g[4];
+                g_of(i, dy, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    squares = pair_fma(v[i][e], v[i][e], squares);
+                    dot = pair_fma(g[e], v[i][e], dot);
+                }
+            }
+            both = reduce.sum2(pair_sum(squares), pair_sum(dot));
+        };
+        sums();
+        float eps = a.eps, down = 1.0f;
+        const bool again = !(both.x <= 3.0e38f);
+        if (team.size < 32 ? __any_sync(0xFFFFFFFFu, again) : again) {
+            down = again ? kDown : 1.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(down));
+            sums();
+            eps = eps * down * down;
+        }
+        const float inv = rsqrtf(fmaf(both.x, inv_cols, eps));
+        const float share = both.y * inv * inv_cols;   // mean(g u)
+        const float out_by = inv * down;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
+            if (at >= end) continue;
+            pair dy[4], g[4], more[4];
+            g_of(i, dy, g);
+            unpack8<kFp16>(add[i], more);   // zeros without dsum
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const pair u = pair_mul(v[i][e], pair_of(inv));
+                dw[i][e] = pair_fma(dy[e], u, dw[i][e]);
+                g[e] = pair_fma(pair_fma(u, pair_of(-share), g[e]), pair_of(out_by), more[e]);
+            }
+            *reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + 8 * at) = pack8<kFp16>(g);
+        }
+    }
+    if (a.partials == nullptr) return;
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
+    if (team.size >= 32) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
+            if (at < vectors) store_sums(part + 8 * at, dw[i]);
+        }
+        return;
+    }
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // narrow rows have two vectors a thread, 256 columns
+        for (int o = team.size; o < 32; o *= 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dw[i][e] = pair_add(dw[i][e], __shfl_xor_sync(0xFFFFFFFFu, dw[i][e], o));
+        const int at = team.at + i * team.size;
+        if ((threadIdx.x & 31) < team.size && at < vectors) store_sums(columns[warp] + 8 * at, dw[i]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x)
+        part[c] = columns[0][c] + columns[1][c] + columns[2][c] + columns[3][c];
+}
+
+// 32 warps take a run of parts each, 32 columns a block.
+__global__ void __launch_bounds__(1024) join_columns_kernel(const float* __restrict__ partials, int parts, int cols,
+                                                            float* __restrict__ out) {
+    __shared__ float run[32][33];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    const int p0 = static_cast<int>(static_cast<int64_t>(parts) * warp / 8);
-    const int p1 = static_cast<int>(static_cast<int64_t>(parts) * (warp + 1) / 8);
+    const int p0 = static_cast<int>(static_cast<int64_t>(parts) * warp / 32);
+    const int p1 = static_cast<int>(static_cast<int64_t>(parts) * (warp + 1) / 32);
     float sum = 0.0f;
     if (c < cols) {
 #pragma unroll 8
@@ -269,87 +338,79 @@ __global__ void __launch_bounds__(256) join_columns_kernel(const float* __restri
     }
     run[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        for (int i = 1; i < 8; ++i) sum += run[i][lane];
-        out[c] = sum;
-    }
-}
-
-// Vectors a thread: 2, fewer for narrow rows, more for wide ones.
-int vectors_each(int vectors) {
-    for (int each = 2; each < kRowVectors; each *= 2)
-        if (row_threads(vectors, each) <= kRowThreads) return each;
-    return kRowVectors;
+    // warp i adds column i's runs, as a tree in their order
+    sum = run[lane][warp];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) sum += __shfl_down_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0 && static_cast<int>(blockIdx.x) * 32 + warp < cols) out[blockIdx.x * 32 + warp] = sum;
 }
 
 template <int NV, bool kFp16>
-cudaError_t run_norm(const NormArgs& a, int out, int sm_count, cudaStream_t s) {
-    const int threads = row_threads(a.cols >> 3, NV);
-    const int64_t blocks = std::min<int64_t>(a.rows, static_cast<int64_t>(sm_count) * std::max(1, 1024 / threads));
-    const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
-    if (out == kNormRows) return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormRows>, grid, block, 0, s, a);
-    if (out == kNormTensor) return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormTensor>, grid, block, 0, s, a);
-    return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormHalf>, grid, block, 0, s, a);
+cudaError_t run_norm(const NormArgs& a, int out, const RowPlan& p, cudaStream_t s) {
+    const dim3 grid(p.blocks), block(p.threads);
+    if (out == kNormRows) return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormRows>, grid, block, 0, s, a, p.team);
+    if (out == kNormTensor) return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormTensor>, grid, block, 0, s, a, p.team);
+    return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormHalf>, grid, block, 0, s, a, p.team);
 }
 
 template <int NV>
-cudaError_t run_norm_type(const NormArgs& a, int out, bool fp16, int sm_count, cudaStream_t s) {
-    return fp16 ? run_norm<NV, true>(a, out, sm_count, s) : run_norm<NV, false>(a, out, sm_count, s);
+cudaError_t run_norm_type(const NormArgs& a, int out, bool fp16, const RowPlan& p, cudaStream_t s) {
+    return fp16 ? run_norm<NV, true>(a, out, p, s) : run_norm<NV, false>(a, out, p, s);
 }
 
-int grad_blocks(int64_t rows, int cols, int sm_count) {
-    const int threads = row_threads(cols >> 3, vectors_each(cols >> 3));
-    return static_cast<int>(std::min<int64_t>(rows, static_cast<int64_t>(sm_count) * std::max(1, 1024 / threads)));
+RowPlan grad_plan(int64_t rows, int cols, int sm_count) {
+    return row_plan(rows, cols, sm_count, kGradLimits, kGradPerSm);
 }
 
 template <int NV>
-cudaError_t run_grad(const NormGradArgs& a, bool fp16, int blocks, cudaStream_t s) {
-    const dim3 grid(blocks), block(row_threads(a.cols >> 3, NV));
-    return fp16 ? launch_kernel(rmsnorm_grad_kernel<NV, true>, grid, block, 0, s, a)
-                : launch_kernel(rmsnorm_grad_kernel<NV, false>, grid, block, 0, s, a);
+cudaError_t run_grad(const NormGradArgs& a, bool fp16, const RowPlan& p, cudaStream_t s) {
+    const dim3 grid(p.blocks), block(p.threads);
+    return fp16 ? launch_kernel(rmsnorm_grad_kernel<NV, true>, grid, block, 0, s, a, p.team)
+                : launch_kernel(rmsnorm_grad_kernel<NV, false>, grid, block, 0, s, a, p.team);
 }
 
 }  // namespace
 
 cudaError_t launch_join_columns(const float* partials, int parts, int cols, float* out, cudaStream_t s) {
-    return launch_kernel(join_columns_kernel, dim3((cols + 31) / 32), dim3(256), 0, s, partials, parts, cols, out);
+    return launch_kernel(join_columns_kernel, dim3((cols + 31) / 32), dim3(1024), 0, s, partials, parts, cols, out);
 }
 
-cudaError_t launch_rmsnorm(const NormArgs& a, int out, bool fp16, float* next_scale, int sm_count, cudaStream_t s) {
+cudaError_t launch_rmsnorm(const NormArgs& args, int out, bool fp16, int sm_count, cudaStream_t s) {
+    NormArgs a = args;
+    float* after = nullptr;   // a next scale that only a further kernel can write
     if (out == kNormTensor) {
-        const cudaError_t e = launch_zero_word(a.amax_bits, s);
+        if (a.rows == 0 || a.next_scale == a.scale) {
+            after = a.next_scale;
+            a.next_scale = nullptr;
+        }
+        const cudaError_t e = launch_kernel(zero_words_kernel, dim3(1), dim3(1), 0, s, a.amax_bits,
+                                            reinterpret_cast<uint32_t*>(a.next_scale));
         if (e != cudaSuccess) return e;
     }
     if (a.rows > 0) {
-        cudaError_t e;
-        switch (vectors_each(a.cols >> 3)) {
-            case 2: e = run_norm_type<2>(a, out, fp16, sm_count, s); break;
-            case 4: e = run_norm_type<4>(a, out, fp16, sm_count, s); break;
-            default: e = run_norm_type<8>(a, out, fp16, sm_count, s); break;
-        }
+        const RowPlan p = row_plan(a.rows, a.cols, sm_count, kLimits, kPerSm);
+        const cudaError_t e = p.each == 2   ? run_norm_type<2>(a, out, fp16, p, s)
+                              : p.each == 4 ? run_norm_type<4>(a, out, fp16, p, s)
+                                            : run_norm_type<8>(a, out, fp16, p, s);
         if (e != cudaSuccess) return e;
     }
-    if (next_scale == nullptr) return cudaSuccess;
-    return launch_kernel(next_scale_kernel, dim3(1), dim3(1), 0, s, reinterpret_cast<const float*>(a.amax_bits),
-                         next_scale);
+    if (after == nullptr) return cudaSuccess;
+    return launch_kernel(next_scale_kernel, dim3(1), dim3(1), 0, s, reinterpret_cast<const float*>(a.amax_bits), after);
 }
 
 int64_t rmsnorm_grad_scratch_bytes(int64_t rows, int cols, int sm_count) {
-    return static_cast<int64_t>(grad_blocks(rows, cols, sm_count)) * cols * 4;
+    return static_cast<int64_t>(grad_plan(rows, cols, sm_count).blocks) * cols * 4;
 }
 
 cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool fp16, float* dweight, int sm_count, cudaStream_t s) {
-    const int blocks = grad_blocks(a.rows, a.cols, sm_count);
-    if (blocks > 0) {
-        cudaError_t e;
-        switch (vectors_each(a.cols >> 3)) {
-            case 2: e = run_grad<2>(a, fp16, blocks, s); break;
-            case 4: e = run_grad<4>(a, fp16, blocks, s); break;
-            default: e = run_grad<8>(a, fp16, blocks, s); break;
-        }
+    const RowPlan p = grad_plan(a.rows, a.cols, sm_count);
+    if (a.rows > 0) {
+        const cudaError_t e = p.each == 2   ? run_grad<2>(a, fp16, p, s)
+                              : p.each == 4 ? run_grad<4>(a, fp16, p, s)
+                                            : run_grad<8>(a, fp16, p, s);
         if (e != cudaSuccess) return e;
     }
-    return dweight == nullptr ? cudaSuccess : launch_join_columns(a.partials, blocks, a.cols, dweight, s);
+    return dweight == nullptr ? cudaSuccess : launch_join_columns(a.partials, p.blocks, a.cols, dweight, s);
 }
 
 }  // namespace dg

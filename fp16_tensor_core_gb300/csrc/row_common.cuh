@@ -1,9 +1,10 @@
 // row_common.cuh -- pieces of the kernels that work on rows of BF16 or FP16
 // elements (norm, activation and their gradients).
 //
-// A thread holds vectors of 8 elements (16 bytes): vector i of a thread is
-// vector threadIdx.x + i * blockDim.x of the row, so that a warp's loads are
-// whole lines.  Arithmetic is FP32; each output is rounded once.
+// A thread holds vectors of 8 elements (16 bytes): vector i of thread t of a
+// row's n is vector t + i n of the row, so that a warp's loads are whole
+// lines.  Arithmetic is FP32, two elements an instruction; each output is
+// rounded once.
 #pragma once
 
 #include <cstdint>
@@ -20,51 +21,50 @@ constexpr int kRowThreads = 512;   // at most, a row
 constexpr int kRowVectors = 8;     // at most, a thread
 static_assert(kRowThreads * kRowVectors * 8 == kMaxRowElements, "widest row");
 
+// Eight elements as four pairs.
 template <bool kFp16>
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(uint4 v, pair (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (kFp16) {
             const float2 t = f16x2_to_f32x2(w[i]);
-            f[2 * i] = t.x;
-            f[2 * i + 1] = t.y;
+            f[i] = pair_of(t.x, t.y);
         } else {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            f[i] = pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
         }
     }
 }
 
 template <bool kFp16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return kFp16 ? f32x2_to_f16x2(lo, hi) : f32x2_to_bf16x2(lo, hi);
+__device__ __forceinline__ uint32_t pack2(pair v) {
+    const float2 f = floats_of(v);
+    return kFp16 ? f32x2_to_f16x2(f.x, f.y) : f32x2_to_bf16x2(f.x, f.y);
 }
 
 template <bool kFp16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack2<kFp16>(f[0], f[1]), pack2<kFp16>(f[2], f[3]), pack2<kFp16>(f[4], f[5]),
-                      pack2<kFp16>(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const pair (&f)[4]) {
+    return make_uint4(pack2<kFp16>(f[0]), pack2<kFp16>(f[1]), pack2<kFp16>(f[2]), pack2<kFp16>(f[3]));
 }
 
 // Eight values times `by` as E4M3 codes, saturating, NaN as 0x7F.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float by) {
+__device__ __forceinline__ uint2 codes8(const pair (&f)[4], float by) {
     uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i] * by, f[4 * i + 1] * by)) |
-               static_cast<uint32_t>(f32x2_to_e4m3x2(f[4 * i + 2] * by, f[4 * i + 3] * by)) << 16;
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = floats_of(pair_mul(f[2 * i], pair_of(by))), b = floats_of(pair_mul(f[2 * i + 1], pair_of(by)));
+        w[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(a.x, a.y)) | static_cast<uint32_t>(f32x2_to_e4m3x2(b.x, b.y)) << 16;
+    }
     return make_uint2(w[0], w[1]);
 }
 
 // Eight E4M3 codes times `by`.
-__device__ __forceinline__ void decode8(uint2 q, float by, float (&f)[8]) {
+__device__ __forceinline__ void decode8(uint2 q, float by, pair (&f)[4]) {
     const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 t = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)))));
-        f[2 * i] = t.x * by;
-        f[2 * i + 1] = t.y * by;
+        f[i] = pair_mul(pair_of(t.x, t.y), pair_of(by));
     }
 }
 
@@ -82,35 +82,43 @@ __device__ __forceinline__ uint2 load_once8(const void* p) {
     return v;
 }
 
-// The largest magnitude of eight values, as ordered bits (NaN above all).
-__device__ __forceinline__ uint32_t top8(const float (&f)[8]) {
-    uint32_t top = 0;
+// The largest magnitude of eight values and of one that there is.
+__device__ __forceinline__ float top8(const pair (&f)[4], float top) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 4; ++i) top = pair_top(f[i], top);
     return top;
 }
 
-// Reductions over a block that give every thread the result.  Two buffers,
-// taken in turn: between two uses of one lies the barrier of the other, so
-// that one barrier a reduction is enough.
+// The threads of a row: a block, or for narrow rows a power of two of lanes,
+// several rows to a warp.
+struct RowTeam {
+    int size;     // threads a row
+    int at;       // this thread's place in its row
+    int row;      // the row's place among those of the block
+    int rows;     // rows of a block
+};
+__device__ __forceinline__ RowTeam row_team(int size) {
+    const int t = static_cast<int>(threadIdx.x);
+    if (size >= 32) return {size, t, 0, 1};
+    return {size, t & (size - 1), t / size, static_cast<int>(blockDim.x) / size};
+}
+
+// Reductions over a row's threads that give every one the result; all threads
+// of the block take part.  Two buffers, taken in turn: between two uses of
+// one lies the barrier of the other, so that one barrier a reduction is
+// enough.
 struct RowReduce {
     float2 (*buffer)[kRowThreads / 32];   // [2], shared memory
+    int size;                             // threads a row
     int turn = 0;
 
     __device__ __forceinline__ float2 sum2(float a, float b) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+        for (int o = min(size, 32) >> 1; o > 0; o >>= 1) {
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
             b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
         }
-        const int warps = static_cast<int>(blockDim.x) >> 5;
-        if (warps == 1) return make_float2(a, b);
-        float2* buf = buffer[turn];
-        turn ^= 1;
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        const float2 t = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+        if (size <= 32) return make_float2(a, b);
+        const float2 t = exchange(make_float2(a, b));
         a = t.x;
         b = t.y;
 #pragma unroll
@@ -122,35 +130,92 @@ struct RowReduce {
     }
     __device__ __forceinline__ float sum(float a) { return sum2(a, 0.0f).x; }
 
-    // Two maxima of ordered bits.
-    __device__ __forceinline__ uint2 max2(uint32_t a, uint32_t b) {
-        a = __reduce_max_sync(0xFFFFFFFFu, a);
-        b = __reduce_max_sync(0xFFFFFFFFu, b);
-        const int warps = static_cast<int>(blockDim.x) >> 5;
-        if (warps == 1) return make_uint2(a, b);
-        uint2* buf = reinterpret_cast<uint2*>(buffer[turn]);
+    // Two maxima of magnitudes (as ordered bits: NaN above all).
+    __device__ __forceinline__ float2 max2(float top_a, float top_b) {
+        uint32_t a = __float_as_uint(top_a), b = __float_as_uint(top_b);
+        if (size < 32) {
+            for (int o = size >> 1; o > 0; o >>= 1) {
+                a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+                b = max(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
+            }
+        } else {
+            a = __reduce_max_sync(0xFFFFFFFFu, a);
+            b = __reduce_max_sync(0xFFFFFFFFu, b);
+        }
+        if (size <= 32) return make_float2(__uint_as_float(a), __uint_as_float(b));
+        const float2 t = exchange(make_float2(__uint_as_float(a), __uint_as_float(b)));
+        a = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(t.x));
+        b = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(t.y));
+        return make_float2(__uint_as_float(a), __uint_as_float(b));
+    }
+    __device__ __forceinline__ float max1(float a) { return max2(a, 0.0f).x; }
+
+private:
+    // Every warp's value to every warp: lane i gets warp i's (or zeros).
+    __device__ __forceinline__ float2 exchange(float2 v) {
+        float2* buf = buffer[turn];
         turn ^= 1;
         const int lane = threadIdx.x & 31;
-        if (lane == 0) buf[threadIdx.x >> 5] = make_uint2(a, b);
+        if (lane == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
-        const uint2 t = lane < warps ? buf[lane] : make_uint2(0u, 0u);
-        return make_uint2(__reduce_max_sync(0xFFFFFFFFu, t.x), __reduce_max_sync(0xFFFFFFFFu, t.y));
+        return lane < static_cast<int>(blockDim.x) >> 5 ? buf[lane] : make_float2(0.0f, 0.0f);
     }
-    __device__ __forceinline__ uint32_t max1(uint32_t a) { return max2(a, 0u).x; }
 };
+
+__device__ __forceinline__ float pair_sum(pair v) {
+    const float2 f = floats_of(v);
+    return f.x + f.y;
+}
+
+// Eight columns' sums, 16-byte aligned.
+__device__ __forceinline__ void store_sums(float* dst, const pair (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = floats_of(f[2 * i]), b = floats_of(f[2 * i + 1]);
+        reinterpret_cast<float4*>(dst)[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+
+// A tensor's scale: amax / 448, 1 for an all-zero one.
+__device__ __forceinline__ float scale_of_amax(float a) { return a == 0.0f ? 1.0f : __fdiv_rn(a, 448.0f); }
 
 // A row's scale: fl32(amax / 448), at least 2^-120 so that its reciprocal is
 // finite (a row of zeros has a scale too); NaN and infinity stay.
-__device__ __forceinline__ float row_scale(uint32_t top_bits) {
-    const float s = __fdiv_rn(__uint_as_float(top_bits), 448.0f);
+__device__ __forceinline__ float row_scale(float top) {
+    const float s = __fdiv_rn(top, 448.0f);
     return s < kRowMinScale ? kRowMinScale : s;
 }
 
-// Threads a row of `vectors` vectors gets when each thread holds `each`.
-inline int row_threads(int vectors, int each) { return ((vectors + each - 1) / each + 31) / 32 * 32; }
+// How rows are dealt out: `each` vectors a thread, `team` threads a row,
+// blocks of `threads`, and as many of them as are resident at once.
+struct RowPlan {
+    int each, team, threads, blocks;
+};
+// per_sm: threads an SM holds at the kernel's registers, by vectors a thread
+// (2, 4, 8).
+inline RowPlan row_plan(int64_t rows, int cols, int sm_count, const int (&limits)[3], const int (&per_sm)[3]) {
+    const int vectors = cols >> 3;
+    int k = 0;
+    while (k < 2 && (vectors + (2 << k) - 1) / (2 << k) > limits[k]) ++k;
+    RowPlan p{};
+    p.each = 2 << k;
+    const int need = (vectors + p.each - 1) / p.each;
+    int64_t teams = rows;   // blocks that every row would fill
+    if (need <= 16) {
+        p.team = 1;
+        while (p.team < need) p.team *= 2;
+        p.threads = 128;
+        teams = (rows + 128 / p.team - 1) / (128 / p.team);
+    } else {
+        p.team = p.threads = (need + 31) / 32 * 32;
+    }
+    const int64_t resident = static_cast<int64_t>(sm_count) * (per_sm[k] / p.threads > 0 ? per_sm[k] / p.threads : 1);
+    p.blocks = static_cast<int>(teams < resident ? teams : resident);
+    return p;
+}
 
 // Sums of columns: out[c] = the sum over parts p of partials[p][c], in the
-// order of p within eight runs, joined in order.  partials: [parts][cols].
+// order of p within 32 runs, joined in order.  partials: [parts][cols].
 cudaError_t launch_join_columns(const float* partials, int parts, int cols, float* out, cudaStream_t s);
 
 }  // namespace dg
