@@ -71,6 +71,12 @@ cudaError_t launch_gemm_tc_fused(const TcLaunch& L, const Params& prm, cudaStrea
 namespace {
 
 constexpr int kThreads = 256;   // warps: 0 TMA, 1 MMA, 2 TMEM owner, 3 idle, 4-7 epilogue
+// The fused tiled kernels have eight epilogue warps (4-11): two take the 32
+// columns of a chunk in turn, so that one's arithmetic runs while the other
+// waits for its loads and stores.  With four the epilogue was longer than the
+// main loop at K = 4096 (4096 x 11008 x 4096 E4M3, SiLU and bias: 139 us).
+constexpr int epilogue_warps(bool fused) { return fused ? 8 : 4; }
+constexpr int gemm_threads(bool fused) { return 128 + 32 * epilogue_warps(fused); }
 constexpr int kBKBytes = 128;   // one 128-byte swizzle row of K per stage
 
 constexpr uint32_t pow2_at_least(uint32_t v) {
@@ -236,25 +242,29 @@ __device__ __forceinline__ void load_residual(const Params& p, int row, bool row
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            uint16_t e = 0;
-            if (col0 + i < p.N) asm volatile("ld.global.u16 %0, [%1];" : "=h"(e) : "l"(src + i));
-            w[i >> 1] |= static_cast<uint32_t>(e) << (16 * (i & 1));
+            uint32_t e = 0;
+            if (col0 + i < p.N) asm volatile("ld.global.u16 %0, [%1];" : "=r"(e) : "l"(src + i));
+            w[i >> 1] |= e << (16 * (i & 1));
         }
     }
 }
 
-// What an epilogue warp holds of its tile's columns in shared memory: each
-// column's scale of B and bias, as pairs of columns {scale, scale, bias, bias}
-// so that one 16-byte read serves two columns.  Loaded while the main loop
-// runs; a tile's columns past N get zeros.
-constexpr int columns_bytes(int bn) { return 4 * bn * 8; }   // of the four warps
+// What a fused epilogue warp holds of its chunks of a tile in shared memory:
+// each column's scale of B and bias, as pairs of columns {scale, scale, bias,
+// bias} so that one 16-byte read serves two columns.  Loaded while the main
+// loop runs; columns past N get zeros.
+constexpr int kColumnFloats = 64;   // of a chunk
+constexpr int fused_chunks(int bn) { return (bn / 32 + 1) / 2; }   // a warp's, at most
+constexpr int columns_bytes(int bn) { return epilogue_warps(true) * fused_chunks(bn) * kColumnFloats * 4; }
 
+// Chunks first, first + 2, ... of the tile whose columns start at col0.
 template <int BN>
-__device__ __forceinline__ void stage_columns(const Params& p, float* columns, int col0, int lane) {
-    float s[BN / 32], b[BN / 32];
+__device__ __forceinline__ void stage_columns(const Params& p, float* columns, int col0, int first, int lane) {
+    constexpr int kChunks = fused_chunks(BN);
+    float s[kChunks], b[kChunks];
 #pragma unroll
-    for (int i = 0; i < BN / 32; ++i) {
-        const int n = col0 + 32 * i + lane;
+    for (int i = 0; i < kChunks; ++i) {
+        const int n = col0 + 32 * (first + 2 * i) + lane;
         s[i] = p.sb == nullptr ? 1.0f : 0.0f;
         b[i] = 0.0f;
         if (n < p.N && p.sb != nullptr) s[i] = __ldg(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
@@ -262,22 +272,24 @@ __device__ __forceinline__ void stage_columns(const Params& p, float* columns, i
     }
     __syncwarp();   // every lane has read the last tile's
 #pragma unroll
-    for (int i = 0; i < BN / 32; ++i) {
-        const int at = 2 * (32 * i + (lane & ~1)) + (lane & 1);
+    for (int i = 0; i < kChunks; ++i) {
+        const int at = kColumnFloats * i + 2 * (lane & ~1) + (lane & 1);
         columns[at] = s[i];
         columns[at + 2] = b[i];
     }
     __syncwarp();
 }
 
-// Moves the rest of a tile row's residual into L2, 128 bytes a time.
+// Moves a tile row's residual (this warp's lines of 64 columns: the first half
+// or the second) into L2.
 template <int BN>
-__device__ __forceinline__ void prefetch_residual(const Params& p, int row, bool row_ok, int col0) {
+__device__ __forceinline__ void prefetch_residual(const Params& p, int row, bool row_ok, int col0, int half) {
     if (p.epi.residual == nullptr || !row_ok) return;
     const uint16_t* src = p.epi.residual + static_cast<int64_t>(row) * p.N + col0;
 #pragma unroll
-    for (int i = 32; i < BN; i += 64)
-        if (col0 + i < p.N) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + i));
+    for (int i = 0; i < BN; i += 128)
+        if (i + 64 * half < BN && col0 + i + 64 * half < p.N)
+            asm volatile("prefetch.global.L2 [%0];" :: "l"(src + i + 64 * half));
 }
 
 template <int kAct>

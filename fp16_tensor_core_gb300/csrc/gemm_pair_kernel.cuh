@@ -19,14 +19,14 @@ constexpr uint32_t kEpiBarrier = 1;   // named barrier of the four epilogue warp
 constexpr int kHalfBM = 128;   // rows of it per CTA
 
 // Staging boxes of the epilogue: one 32 x 32 box per epilogue warp.
-constexpr int kStagingBytes = 4 * kBoxBytes;
+constexpr int pair_staging_bytes(bool fused) { return epilogue_warps(fused) * kBoxBytes; }
 
 // Stage count: what fits in 227 KB beside the barrier block (1 KB, keeping
 // the staging boxes 1024-byte aligned), the staging boxes and a fused
 // epilogue's columns, at most 8
 // (4 with two K blocks per stage).
 constexpr int pair_stages_for(int bn, int kps = 1, bool fused = false) {
-    const int st = (kSmemLimit - 1024 - 1024 - kStagingBytes - (fused ? columns_bytes(bn) : 0)) /
+    const int st = (kSmemLimit - 1024 - 1024 - pair_staging_bytes(fused) - (fused ? columns_bytes(bn) : 0)) /
                    (kps * (kHalfBM * kBKBytes + (bn / 2) * kBKBytes));
     return st > 8 / kps ? 8 / kps : st;
 }
@@ -43,7 +43,7 @@ struct PairCfg {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * BN);
     static constexpr int kStagingOff = STAGES * kStageBytes + 1024;   // after the barriers
-    static constexpr int kColumnsOff = kStagingOff + kStagingBytes;   // fused: its columns' scales, bias
+    static constexpr int kColumnsOff = kStagingOff + pair_staging_bytes(kFused);   // fused: its columns' scales, bias
     static constexpr int kSmemBytes = 1024 + kColumnsOff + (kFused ? columns_bytes(BN) : 0);
     static constexpr uint32_t kIdesc = idesc_f32acc(kPairBM, BN, 0, 0);
     static_assert(BN % 32 == 0 && BN >= 128 && BN <= 256, "BN");
@@ -146,7 +146,7 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {
 }
 
 template <int BN, int STAGES, bool kFp16In, int KPS = 1, bool kFused = false>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(kFused), 1)
 gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_d, const Params p) {
@@ -176,7 +176,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], 2 * epilogue_warps(kFused));
         }
         mbar_init(drain, 1);
         mbar_init(fix_bar, 1);
@@ -323,10 +323,15 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else if (warp >= 4) {
         // ------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;
+        // its chunks of 32 columns: every one, or every second from `half` on
+        constexpr int kChunkStep = epilogue_warps(kFused) / 4;
+        constexpr uint32_t kEpiThreads = 32 * epilogue_warps(kFused);
+        const int half = kFused ? (warp - 4) >> 2 : 0;
         float alpha = 1.0f;
         if (!kFused && p.sa != nullptr) alpha = (*p.sa) * (*p.sb);
         if (!kFused && p.out_kind == kOutE4M3) alpha = __fdiv_rn(alpha, *p.sd);
-        float* columns = reinterpret_cast<float*>(smem + C::kColumnsOff) + q * 2 * BN;
+        float* columns = reinterpret_cast<float*>(smem + C::kColumnsOff) +
+                         (warp - 4) * fused_chunks(BN) * kColumnFloats;
         const ByScale out_scale = kFused ? output_scale(p.out_kind, p.sd) : ByScale{1.0f, 1.0f};
         const uint32_t leader_acc_empty = map_to_rank(acc_empty, 0);
         uint32_t amax_bits = 0u;
@@ -363,15 +368,15 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if constexpr (kFused) {
                 sa = scale_of_row(p, row, row_ok);
                 if (it.part <= 0) {
-                    load_residual(p, row, row_ok, nt * BN, res);
-                    prefetch_residual<BN>(p, row, row_ok, nt * BN);
-                    stage_columns<BN>(p, columns, nt * BN, lane);
+                    load_residual(p, row, row_ok, nt * BN + 32 * half, res);
+                    prefetch_residual<BN>(p, row, row_ok, nt * BN, half);
+                    stage_columns<BN>(p, columns, nt * BN, half, lane);
                 }
             }
             // The four warps continue or leave together (the split tail
             // below synchronises them on a named barrier).
             const bool got = wait_bounded_cluster(&acc_full[acc], acc_phase, ctl);
-            if (!named_bar_and(kEpiBarrier, 128, got)) break;
+            if (!named_bar_and(kEpiBarrier, kEpiThreads, got)) break;
             tc_fence_after_sync();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * BN);
@@ -392,7 +397,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 // 512-byte run), then count the arrival.
                 float4* mine = slot_of(it.part);
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
+                for (int c = half; c < BN / 32; c += kChunkStep) {
                     uint32_t r[32];
                     __syncwarp();
                     tmem_load_32cols(tbase + c * 32, r);
@@ -403,7 +408,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
                                            __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3])));
                 }
-                named_bar_sync(kEpiBarrier, 128);   // every row of the CTA's half is out
+                named_bar_sync(kEpiBarrier, kEpiThreads);   // every row of the CTA's half is out
                 if (threadIdx.x == 128) {
                     __threadfence();
                     atomicAdd(counter, 1u);
@@ -424,7 +429,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         }
                     }
                 }
-                ready = named_bar_and(kEpiBarrier, 128, arrived);
+                ready = named_bar_and(kEpiBarrier, kEpiThreads, arrived);
                 if (ready && staged_parts) {
                     // the other parts' partial tiles into the idle ring, in
                     // part order, on one barrier (used once per CTA)
@@ -439,7 +444,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                               kCopyPiece, fix_bar);
                     }
                     const bool landed = wait_bounded(fix_bar, 0, ctl);
-                    ready = named_bar_and(kEpiBarrier, 128, landed);
+                    ready = named_bar_and(kEpiBarrier, kEpiThreads, landed);
                     if (!ready && threadIdx.x == 128) wait_bounded(fix_bar, 0, ctl, false);
                 }
             }
@@ -475,13 +480,13 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 const int ring_base = (it.part == 0 && staged_parts)
                                           ? (nparts - 1) * kSlotBytes : 0;
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
+                for (int c = half; c < BN / 32; c += kChunkStep) {
                     uint32_t r[32];
                     __syncwarp();
                     tmem_load_32cols(tbase + c * 32, r);
                     uint8_t* box = last_item
                         ? smem + ring_base + (q * (BN / 32) + c) * kBoxBytes
-                        : smem + C::kStagingOff + q * kBoxBytes;
+                        : smem + C::kStagingOff + (warp - 4) * kBoxBytes;
                     if (!last_item && lane == 0) bulk_wait_read_all();
                     __syncwarp();
                     tmem_load_wait(r);
@@ -489,8 +494,8 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = nt * BN + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
-                        if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
+                        if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         stage_values(p, box, v, lane);
                     } else {
                         amax_bits = max(amax_bits, stage_box(p, box, row, p.M, col0, r, alpha, lane));
@@ -509,7 +514,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M) {
-                        for (int c = 0; c < BN / 32 && nt * BN + c * 32 < p.N; ++c)
+                        for (int c = half; c < BN / 32 && nt * BN + c * 32 < p.N; c += kChunkStep)
                             tma_store_2d(&tmap_d, smem + ring_base + (q * (BN / 32) + c) * kBoxBytes,
                                          nt * BN + c * 32, row0);
                         bulk_commit();
@@ -517,7 +522,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 }
             } else {
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
+                for (int c = half; c < BN / 32; c += kChunkStep) {
                     uint32_t r[32];
                     __syncwarp();
                     tmem_load_32cols(tbase + c * 32, r);
@@ -526,8 +531,8 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = nt * BN + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
-                        if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
+                        if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         if (row_ok && col0 < p.N) store_values(p, row, min(32, p.N - col0), col0, v);
                     } else {
                         amax_bits = max(amax_bits, store_chunk(p, row, p.M, col0, r, alpha));
@@ -537,7 +542,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if (it.part == 0 && ready) {
                 // every partial has been read: the counter is zero again for
                 // the next launch
-                named_bar_sync(kEpiBarrier, 128);
+                named_bar_sync(kEpiBarrier, kEpiThreads);
                 if (threadIdx.x == 128) atomicExch(counter, 0u);
             }
             tc_fence_before_sync();
@@ -571,12 +576,12 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 }
 
 template <typename Kern>
-cudaError_t launch_pair(Kern kern, dim3 grid, size_t smem, cudaStream_t s,
+cudaError_t launch_pair(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s,
                         const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
                         const Params& prm) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -610,7 +615,7 @@ cudaError_t launch_pair_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s
             if (e != cudaSuccess) return e;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(2);
-            cfg.blockDim = dim3(kThreads);
+            cfg.blockDim = dim3(gemm_threads(kFused));
             cfg.dynamicSmemBytes = C::kSmemBytes;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -672,7 +677,7 @@ cudaError_t launch_pair_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s
         prm2.staged = 0;
         td = ta;
     }
-    return launch_pair(kern, dim3(2 * pairs), C::kSmemBytes, s, ta, tb, td, prm2);
+    return launch_pair(kern, dim3(2 * pairs), gemm_threads(kFused), C::kSmemBytes, s, ta, tb, td, prm2);
 }
 
 // One or two K blocks per stage, as the plan says (block_k = K elements per

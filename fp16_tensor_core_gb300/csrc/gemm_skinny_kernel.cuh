@@ -42,11 +42,13 @@ struct SkCfg {
     static constexpr int kStageW = KPS * kWBytes;
     static constexpr int kStageX = KPS * kXBytes;
     static constexpr int kSmemBytes = 1024 + kRing * kKBBytes + kBarBytes;
+    static constexpr int kScalesOff = kRing * kKBBytes + kBarBytes;   // fused: the rows' scales of A
+    static constexpr int kFusedSmemBytes = kSmemBytes + NC * 4;
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * NC);   // two accumulators
     static constexpr uint32_t kIdesc = idesc_f32acc(kRows, NC, 0, 0);
     static_assert(NC % 16 == 0 && NC >= 16 && NC <= kSplitkMaxCols, "MMA N");
     static_assert(kRing % KPS == 0 && kStages <= 12, "ring");
-    static_assert(kSmemBytes <= kSmemLimit, "shared memory");
+    static_assert(kFusedSmemBytes <= kSmemLimit, "shared memory");
     static_assert(kXBytes % 1024 == 0, "1024-byte aligned A blocks (128-byte swizzle atoms)");
     // barriers: full/empty per stage, 2 + 2 accumulator, drain, fix-up,
     // helpers; then the TMEM address, the abort flag, the last-arrival flag
@@ -114,51 +116,87 @@ __device__ __forceinline__ void store_chunk16(const SkParams& p, int c0, int n, 
     }
 }
 
-// The fused epilogue of column n of D (a row of B): its scale of B, bias and
-// the output's scale.
+// The fused epilogue of column n of D (a row of B): its scale of B and bias,
+// loaded while the tile's main loop runs.
 struct FusedColumn {
-    float sb, bias;
-    ByScale out;
+    float sb = 1.0f, bias = 0.0f;
 };
 __device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live, int n) {
-    FusedColumn c{1.0f, 0.0f, {1.0f, 1.0f}};
-    if (!live) return c;
-    if (p.sb != nullptr) c.sb = __ldg(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
-    if (p.epi.bias != nullptr) c.bias = __ldg(p.epi.bias + n);
-    c.out = output_scale(p.out_kind, p.sd);
+    FusedColumn c;
+    if (live && p.sb != nullptr) c.sb = __ldg(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
+    if (live && p.epi.bias != nullptr) c.bias = __ldg(p.epi.bias + n);
     return c;
+}
+
+// The residual of tile t moves into L2: thread r of 128 takes lines r, r + 128
+// of the M rows' two.
+__device__ __forceinline__ void prefetch_residual_tile(const SkParams& p, int t, int r) {
+    if (p.epi.residual == nullptr) return;
+    for (int i = r; i < 2 * p.M; i += 128) {
+        const int n = t * p.tile_rows + 64 * (i & 1);
+        if (64 * (i & 1) < p.tile_rows && n < p.N)
+            asm volatile("prefetch.global.L2 [%0];" :: "l"(p.epi.residual + static_cast<int64_t>(i >> 1) * p.N + n));
+    }
 }
 
 // Rows c0 .. c0 + 15 of the residual's column n (not the read-only path: D
 // may be the residual).
 __device__ __forceinline__ void load_residual16(const SkParams& p, bool live, int c0, int n,
-                                                uint16_t (&res)[16]) {
+                                                uint32_t (&res)[16]) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         res[j] = 0;
         if (p.epi.residual != nullptr && live && c0 + j < p.M)
-            asm volatile("ld.global.u16 %0, [%1];"
-                         : "=h"(res[j]) : "l"(p.epi.residual + static_cast<int64_t>(c0 + j) * p.N + n));
+            asm volatile("ld.global.u16 %0, [%1];"   // (into 32 bits: nothing waits for it here)
+                         : "=r"(res[j]) : "l"(p.epi.residual + static_cast<int64_t>(c0 + j) * p.N + n));
     }
 }
 
-// act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n] for rows c0 ..
-// c0 + jn - 1; returns the largest magnitude (ordered bits).
-__device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, const FusedColumn& col,
-                                           const uint16_t (&res)[16], float (&v)[16]) {
-    uint32_t top = 0u;
+template <int kAct>
+__device__ __forceinline__ void activate16(pair (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        if (j >= jn) continue;
-        const float sa = p.sa == nullptr ? 1.0f : __ldg(p.sa + (c0 + j) * p.epi.sa_step);
-        float y = activation(p.epi.act, fmaf(v[j], sa * col.sb, col.bias));
-        if (p.epi.residual != nullptr)
-            y += p.epi.residual_fp16 != 0 ? f16x2_to_f32x2(res[j]).x
-                                          : __uint_as_float(static_cast<uint32_t>(res[j]) << 16);
-        top = max(top, __float_as_uint(y) & 0x7FFFFFFFu);
-        v[j] = y * col.out.pre * col.out.inv;
+    for (int i = 0; i < 8; ++i) v[i] = activation(kAct, v[i]);
+}
+
+// act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n] for rows c0 ..
+// c0 + jn - 1 (sa: the rows' scales, in shared memory); returns the largest
+// magnitude (ordered bits).
+__device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, const FusedColumn& col,
+                                           ByScale out, const float* sa, const uint32_t (&res)[16],
+                                           float (&f)[16]) {
+    pair v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const ulonglong2 s = reinterpret_cast<const ulonglong2*>(sa + c0)[i];
+        v[2 * i] = pair_fma(pair_of(f[4 * i], f[4 * i + 1]), pair_mul(s.x, pair_of(col.sb)), pair_of(col.bias));
+        v[2 * i + 1] = pair_fma(pair_of(f[4 * i + 2], f[4 * i + 3]), pair_mul(s.y, pair_of(col.sb)), pair_of(col.bias));
     }
-    return top;
+    switch (p.epi.act) {
+        case DG_ACT_RELU: activate16<DG_ACT_RELU>(v); break;
+        case DG_ACT_GELU: activate16<DG_ACT_GELU>(v); break;
+        case DG_ACT_GELU_TANH: activate16<DG_ACT_GELU_TANH>(v); break;
+        case DG_ACT_SILU: activate16<DG_ACT_SILU>(v); break;
+        default: break;
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (p.epi.residual != nullptr) {
+            const uint32_t w = res[2 * i] | res[2 * i + 1] << 16;
+            const float2 x = p.epi.residual_fp16 != 0
+                                 ? f16x2_to_f32x2(w)
+                                 : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+            v[i] = pair_add(v[i], pair_of(x.x, x.y));
+        }
+        const float2 y = floats_of(v[i]);
+        if (2 * i + 1 < jn)
+            top = pair_top(v[i], top);
+        else if (2 * i < jn)
+            top = pair_top(pair_of(y.x), top);
+        f[2 * i] = y.x * out.pre * out.inv;
+        f[2 * i + 1] = y.y * out.pre * out.inv;
+    }
+    return __float_as_uint(top);
 }
 
 // Adds up, scales and stores the 16-column chunks c0 = c0_begin,
@@ -172,15 +210,14 @@ __device__ __forceinline__ void finish_chunks(const SkParams& p, uint8_t* smem, 
                                               int r, int n, int c0_begin, int c0_step, int me,
                                               int c_first, int c_last, int first_slot,
                                               bool staged, int quads, const float (&first)[16],
-                                              float alpha, uint32_t& amax_bits) {
+                                              float alpha, uint32_t& amax_bits,
+                                              const FusedColumn& column, ByScale out, const float* sa) {
     const int others = c_last - c_first;
     const bool live = r < p.tile_rows && n < p.N;
-    FusedColumn column;
-    if constexpr (kFused) column = fused_column(p, live, n);
 #pragma unroll 1
     for (int c0 = c0_begin; c0 < NC && c0 < p.M; c0 += c0_step) {
         float v[16];
-        uint16_t res[16];   // on its way while the partial tiles are added up
+        uint32_t res[16];   // on its way while the partial tiles are added up
         if constexpr (kFused) load_residual16(p, live, c0, n, res);
         if (c_last > c_first && c0 == 0) {
 #pragma unroll
@@ -276,7 +313,7 @@ __device__ __forceinline__ void finish_chunks(const SkParams& p, uint8_t* smem, 
         if (live) {
             const int jn = min(16, p.M - c0);   // rows of A in this chunk
             if constexpr (kFused) {
-                amax_bits = max(amax_bits, fuse16(p, c0, jn, column, res, v));
+                amax_bits = max(amax_bits, fuse16(p, c0, jn, column, out, sa, res, v));
                 store_chunk16(p, c0, n, jn, v, 1.0f);
                 continue;
             }
@@ -314,6 +351,8 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
     volatile int* last_flag = abort_flag + 1;
     volatile int* help = last_flag + 1;     // [kHelpInts]
+
+    float* row_scales = reinterpret_cast<float*>(smem + C::kScalesOff);   // [NC], fused
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -469,6 +508,13 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
         float ab = 1.0f;   // (a fused epilogue has scales of its own)
         if (!kFused && p.sa != nullptr) ab = p.sa[0] * p.sb[0];
         const float alpha = !kFused && p.out_kind == kOutE4M3 ? __fdiv_rn(ab, p.sd[0]) : ab;
+        ByScale out{1.0f, 1.0f};
+        FusedColumn column;
+        if constexpr (kFused) {
+            out = output_scale(p.out_kind, p.sd);
+            if (r < NC) row_scales[r] = p.sa != nullptr && r < p.M ? __ldg(p.sa + r * p.epi.sa_step) : 1.0f;
+            named_bar_sync(kEpiBar, kEpiThreads);   // (the helpers' reads come after a hand-off)
+        }
         uint32_t amax_bits = 0u;
         bool released = false;   // the last tile handed to warps 0-3 (thread 128)
         int acc = 0;
@@ -483,6 +529,11 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             const int c_last = cta_of_unit(tile_u0 + KB - 1, G, units);
             const int first_slot =
                 range_start(c_first, G, units) == tile_u0 ? 2 * c_first : 2 * c_first + 1;
+            if constexpr (kFused) {
+                const int n0 = t * p.tile_rows + r;
+                column = fused_column(p, r < p.tile_rows && n0 < p.N, n0);
+                prefetch_residual_tile(p, t, r);
+            }
             // The four warps continue or leave together (named barriers below).
             const bool got = wait_bounded(&acc_full[acc], acc_phase, ctl);
             if (!named_bar_and(kEpiBar, kEpiThreads, got)) break;
@@ -583,7 +634,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             }
             if (finish)
                 finish_chunks<NC, kFused>(p, smem, tacc, r, n, 0, helped ? 32 : 16, me, c_first, c_last,
-                                  first_slot, staged, quads, first, alpha, amax_bits);
+                                  first_slot, staged, quads, first, alpha, amax_bits, column, out, row_scales);
             // The accumulator is free once every chunk has been read.
             tc_fence_before_sync();
             __syncwarp();
@@ -611,6 +662,13 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             // Warps 0-3, once their own roles are done, take the odd
             // 16-column chunks of the CTA's last tile when it finishes one.
             __syncwarp();
+            ByScale out{1.0f, 1.0f};
+            FusedColumn column;
+            if constexpr (kFused) {   // of the CTA's last tile
+                const int t_last = static_cast<int>((u_begin + n_units - 1) / KB), n = t_last * p.tile_rows + warp * 32 + lane;
+                out = output_scale(p.out_kind, p.sd);
+                column = fused_column(p, warp * 32 + lane < p.tile_rows && n < p.N, n);
+            }
             const bool go = wait_bounded(help_bar, 0, ctl) && help[0] != 0;
             if (__all_sync(0xFFFFFFFFu, go)) {
                 const int t = help[1], acc = help[2], c_first = help[3], c_last = help[4];
@@ -631,7 +689,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     uint32_t amax_bits = 0u;
                     finish_chunks<NC, kFused>(p, smem, tacc, r, t * p.tile_rows + r, 16, 32,
                                       static_cast<int>(blockIdx.x), c_first, c_last, first_slot,
-                                      staged, quads, none, alpha, amax_bits);
+                                      staged, quads, none, alpha, amax_bits, column, out, row_scales);
                     if (p.amax_out != nullptr) {
                         __syncwarp();
                         const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, amax_bits);
@@ -674,7 +732,8 @@ cudaError_t launch_sk(const TcLaunch& L, float* partials, uint32_t* counts, cuda
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (!attr_done[dev]) {
             e = cudaFuncSetAttribute(gemm_skinny_kernel<kFp16In, KPS, NC, kFused>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kFused ? C::kFusedSmemBytes : C::kSmemBytes);
             if (e != cudaSuccess) return e;
             attr_done[dev] = true;
         }
@@ -706,7 +765,7 @@ cudaError_t launch_sk(const TcLaunch& L, float* partials, uint32_t* counts, cuda
     prm.prefetch_kblocks = splitk_prefetch_kblocks(C::kRing);
     if (L.epi != nullptr) prm.epi = *L.epi;
     return launch_kernel(gemm_skinny_kernel<kFp16In, KPS, NC, kFused>, dim3(L.plan->grid), dim3(kThreads),
-                         C::kSmemBytes, s, tw, tx, prm);
+                         kFused ? C::kFusedSmemBytes : C::kSmemBytes, s, tw, tx, prm);
 }
 
 // K blocks per stage: DG_SPLITK_KPS=1|2 (sweeps), default 2.

@@ -21,13 +21,13 @@ constexpr int kBM = 128;
 constexpr int kGroupSmem = 4 * (kMaxGroups + 1) + 12;
 
 // Staging boxes of the epilogue: one 32 x 32 box per epilogue warp.
-constexpr int kStagingBytes = 4 * kBoxBytes;
+constexpr int staging_bytes(bool fused) { return epilogue_warps(fused) * kBoxBytes; }
 
 // Stage count = what fits in 227 KB beside the barrier block (1 KB, keeping
 // the staging boxes 1024-byte aligned), the staging boxes, the grouped
 // variant's tile prefix and the fused one's columns, at most 8 (4 with two K blocks per stage).
 constexpr int stages_for(int bn, bool grouped = false, int kps = 1, bool fused = false) {
-    const int st = (kSmemLimit - 1024 - 1024 - kStagingBytes - (grouped ? kGroupSmem : 0) -
+    const int st = (kSmemLimit - 1024 - 1024 - staging_bytes(fused) - (grouped ? kGroupSmem : 0) -
                     (fused ? columns_bytes(bn) : 0)) /
                    (kps * (kBM * kBKBytes + bn * kBKBytes));
     return st > 8 / kps ? 8 / kps : st;
@@ -47,7 +47,7 @@ struct Cfg {
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * BN);  // two accumulators
     static constexpr int kBarBytes = 256;
     static constexpr int kStagingOff = STAGES * kStageBytes + 1024;   // after the barriers
-    static constexpr int kGroupOff = kStagingOff + kStagingBytes;     // grouped: tile prefix
+    static constexpr int kGroupOff = kStagingOff + staging_bytes(kFused);     // grouped: tile prefix
     static constexpr int kColumnsOff = kGroupOff + (kGrouped ? kGroupSmem : 0);   // fused: its columns' scales, bias
     static constexpr int kSmemBytes = 1024 + kColumnsOff + (kFused ? columns_bytes(BN) : 0);
     static constexpr uint32_t kIdesc = idesc_f32acc(kBM, BN, 0, 0);
@@ -67,7 +67,7 @@ struct Tile {
 };
 
 template <int BN, int STAGES, bool kFp16In, bool kGrouped = false, int KPS = 1, bool kFused = false>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(kFused), 1)
 gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                const __grid_constant__ CUtensorMap tmap_b,
                const __grid_constant__ CUtensorMap tmap_d,
@@ -98,7 +98,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], epilogue_warps(kFused));
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -290,6 +290,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else if (warp >= 4) {
         // ------------------------------------------------ epilogue
         const int q = warp & 3;              // TMEM lane quarter of this warp
+        // its chunks of 32 columns: every one, or every second from `half` on
+        constexpr int kChunkStep = epilogue_warps(kFused) / 4;
+        const int half = kFused ? (warp - 4) >> 2 : 0;
         auto alpha_of = [&](int g) {
             float a = 1.0f;
             if (kFused) return a;
@@ -299,7 +302,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
         };
         float alpha = alpha_of(0);
         int alpha_g = 0;
-        float* columns = reinterpret_cast<float*>(smem + C::kColumnsOff) + q * 2 * BN;
+        float* columns = reinterpret_cast<float*>(smem + C::kColumnsOff) +
+                         (warp - 4) * fused_chunks(BN) * kColumnFloats;
         const ByScale out_scale = kFused ? output_scale(p.out_kind, p.sd) : ByScale{1.0f, 1.0f};
         uint32_t amax_bits = 0u;
         int acc = 0;
@@ -324,9 +328,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             uint32_t res[16];
             if constexpr (kFused) {
                 sa = scale_of_row(p, row, row_ok);
-                load_residual(p, row, row_ok, T.col0, res);
-                prefetch_residual<BN>(p, row, row_ok, T.col0);
-                stage_columns<BN>(p, columns, T.col0, lane);
+                load_residual(p, row, row_ok, T.col0 + 32 * half, res);
+                prefetch_residual<BN>(p, row, row_ok, T.col0, half);
+                stage_columns<BN>(p, columns, T.col0, half, lane);
             }
             // Every lane waits; the vote reconverges the warp (tcgen05.ld is
             // .sync.aligned) and makes the whole warp leave together.
@@ -343,21 +347,21 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             // a place of its own in it, so the stores go out back to back.
             const bool staged = p.staged && (!kGrouped || row0 + 32 <= T.row_end);
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = half; c < BN / 32; c += kChunkStep) {
                 uint32_t r[32];
                 __syncwarp();
                 tmem_load_32cols(tbase + c * 32, r);
                 if (staged) {
                     uint8_t* box = last_tile ? smem + (q * (BN / 32) + c) * kBoxBytes
-                                             : smem + C::kStagingOff + q * kBoxBytes;
+                                             : smem + C::kStagingOff + (warp - 4) * kBoxBytes;
                     if (!last_tile && lane == 0) bulk_wait_read_all();   // the box is free again
                     __syncwarp();
                     tmem_load_wait(r);
                     const int col0 = T.col0 + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
-                        if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
+                        if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         stage_values(p, box, v, lane);
                     } else {
                         amax_bits = max(amax_bits, stage_box(p, box, row, T.row_end, col0, r, alpha, lane));
@@ -374,8 +378,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = T.col0 + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + 64 * c, out_scale, v));
-                        if (c + 1 < BN / 32) load_residual(p, row, row_ok, col0 + 32, res);
+                        amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
+                        if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         if (row_ok && col0 < p.N) store_values(p, row, min(32, p.N - col0), col0, v);
                     } else {
                         amax_bits = max(amax_bits, store_chunk(p, row, T.row_end, col0, r, alpha));
@@ -388,7 +392,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && row0 < T.row_end) {
-                    for (int c = 0; c < BN / 32 && T.col0 + c * 32 < p.N; ++c)
+                    for (int c = half; c < BN / 32 && T.col0 + c * 32 < p.N; c += kChunkStep)
                         tma_store_2d(&tmap_d, smem + (q * (BN / 32) + c) * kBoxBytes, T.col0 + c * 32,
                                      row0);
                     bulk_commit();
@@ -483,7 +487,7 @@ cudaError_t launch_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s) {
         td = ta;
     }
     return launch_kernel(gemm_tc_kernel<BN, STAGES, kFp16In, kGrouped, KPS, kFused>, dim3(L.plan->grid),
-                         dim3(kThreads), C::kSmemBytes, s, ta, tb, td, tae, tbe, prm2);
+                         dim3(gemm_threads(kFused)), C::kSmemBytes, s, ta, tb, td, tae, tbe, prm2);
 }
 
 template <bool kFp16In, bool kFused>

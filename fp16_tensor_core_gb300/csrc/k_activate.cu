@@ -12,8 +12,7 @@
 //
 // Memory bounds both: 2 bytes an input element and 1 to 3 of output; the
 // checkpoint halves what the backward pass reads of the input.  Forward, a
-// block keeps a row in registers until the maxima of the row are known and
-// has the next row's loads in flight.  Backward needs nothing of a row but
+// block keeps a row in registers until the maxima of the row are known.  Backward needs nothing of a row but
 // its scales: a thread owns eight columns over a run of rows, so that dbias
 // is summed in registers; the runs' sums are joined in order by a second
 // kernel.
@@ -38,35 +37,33 @@ constexpr int block_min() { return NV == 8 ? 1 : 2; }
 constexpr int kLimits[3] = {512, 384, 512};
 constexpr int kPerSm[3] = {1024, 768, 512};
 
-template <int NV, bool kFp16, bool kGated>
+template <int NV, bool kFp16, bool kGated, bool kNarrow>
 __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_kernel(const ActArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
     pdl_wait();
     constexpr int kHalves = kGated ? 2 : 1;
-    const RowTeam team = row_team(team_size);
-    RowReduce reduce{buffer, team.size};
+    const RowTeam<kNarrow> team(team_size);
+    RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
     uint4 x[kHalves][NV];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[h][i] = make_uint4(0, 0, 0, 0);
-    auto fetch = [&](int64_t row) {
-        if (row >= a.rows) return;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows; first < a.rows; first += step) {
+        const int64_t row = first + team.row;
+        const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
+        const uint16_t* x_row = a.x + row * a.x_stride;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = team.at + i * team.size;
-                if (at < vectors) x[h][i] = load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + 8 * at);
+                if (at < end) x[h][i] = load_once(x_row + h * a.cols + 8 * at);
             }
-    };
-    const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
-    int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;   // the block's rows, together
-    fetch(first + team.row);
-    for (; first < a.rows; first += step) {
-        const int64_t row = first + team.row;
-        const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
+        if (!kNarrow && threadIdx.x == 0 && row + step < a.rows)
+            prefetch_row(a.x + (row + step) * a.x_stride, 2 * kHalves * a.cols);
         if (a.x_q != nullptr) {
             float top[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -78,6 +75,10 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
                     top[h] = top8(f, top[h]);
                 }
             const float2 both = reduce.max2(top[0], top[1]);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) forget(x[h][i]);
             const float scale[2] = {row_scale(both.x), row_scale(both.y)};
             if (team.at == 0 && end != 0) {
 #pragma unroll
@@ -86,20 +87,22 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 const float by = __frcp_rn(scale[h]);
+                uint8_t* q_row = a.x_q + (row * kHalves + h) * a.cols;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int at = team.at + i * team.size;
                     if (at >= end) continue;
                     pair f[4];
                     unpack8<kFp16>(x[h][i], f);
-                    *reinterpret_cast<uint2*>(a.x_q + (row * kHalves + h) * a.cols + 8 * at) = codes8(f, by);
+                    *reinterpret_cast<uint2*>(q_row + 8 * at) = codes8(f, by);
                 }
             }
         }
-        if (a.y == nullptr && a.q == nullptr) {
-            fetch(row + step);
-            continue;
-        }
+        if (a.y == nullptr && a.q == nullptr) continue;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) forget(x[h][i]);
         pair y[NV][4];
         float top = 0.0f;
 #pragma unroll
@@ -115,31 +118,33 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
             }
             if (team.at + i * team.size < end) top = top8(y[i], top);
         }
-        fetch(row + step);
         if (a.y != nullptr) {
+            uint16_t* y_row = a.y + row * a.y_stride;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = team.at + i * team.size;
-                if (at < end) *reinterpret_cast<uint4*>(a.y + row * a.y_stride + 8 * at) = pack8<kFp16>(y[i]);
+                if (at < end) *reinterpret_cast<uint4*>(y_row + 8 * at) = pack8<kFp16>(y[i]);
             }
         }
         if (a.q != nullptr) {
             const float scale = row_scale(reduce.max1(top));
             const float by = __frcp_rn(scale);
             if (team.at == 0 && end != 0) a.q_scale[row] = scale;
+            uint8_t* q_row = a.q + row * a.cols;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = team.at + i * team.size;
-                if (at < end) *reinterpret_cast<uint2*>(a.q + row * a.cols + 8 * at) = codes8(y[i], by);
+                if (at < end) *reinterpret_cast<uint2*>(q_row + 8 * at) = codes8(y[i], by);
             }
         }
     }
 }
 
+constexpr int kGradResident = 9;    // blocks an SM
 constexpr int kGradThreads = 128;   // 1024 columns a block, or fewer and several rows at once
 
 template <bool kFp16, bool kGated, bool kCodes>
-__global__ void __launch_bounds__(kGradThreads) activate_grad_kernel(const ActGradArgs a, int across) {
+__global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_kernel(const ActGradArgs a, int across) {
     __shared__ float4 columns[kGradThreads][4];   // narrow rows: the threads' sums
     pdl_wait();
     constexpr int kHalves = kGated ? 2 : 1;
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kGradThreads) activate_grad_kernel(const ActGr
 #pragma unroll
         for (int e = 0; e < 4; ++e) sums[h][e] = 0;
     if (c < a.cols) {
-#pragma unroll 2
+#pragma unroll 1
         for (int64_t row = first + t / across; row < end; row += down) {
             pair dy[4], x[kHalves][4];
             unpack8<kFp16>(load_once(a.dy + row * a.dy_stride + c), dy);
@@ -213,21 +218,24 @@ __global__ void __launch_bounds__(kGradThreads) activate_grad_kernel(const ActGr
     }
 }
 
-template <int NV, bool kFp16>
-cudaError_t run_act(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
+template <int NV, bool kFp16, bool kNarrow>
+cudaError_t run_act_rows(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
     const dim3 grid(p.blocks), block(p.threads);
-    return a.gated ? launch_kernel(activate_kernel<NV, kFp16, true>, grid, block, 0, s, a, p.team)
-                   : launch_kernel(activate_kernel<NV, kFp16, false>, grid, block, 0, s, a, p.team);
+    return a.gated ? launch_kernel(activate_kernel<NV, kFp16, true, kNarrow>, grid, block, 0, s, a, p.team)
+                   : launch_kernel(activate_kernel<NV, kFp16, false, kNarrow>, grid, block, 0, s, a, p.team);
 }
 
-template <int NV>
-cudaError_t run_act_type(const ActArgs& a, bool fp16, const RowPlan& p, cudaStream_t s) {
-    return fp16 ? run_act<NV, true>(a, p, s) : run_act<NV, false>(a, p, s);
+template <bool kFp16>
+cudaError_t run_act(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
+    if (p.narrow) return run_act_rows<2, kFp16, true>(a, p, s);
+    if (p.each == 2) return run_act_rows<2, kFp16, false>(a, p, s);
+    if (p.each == 4) return run_act_rows<4, kFp16, false>(a, p, s);
+    return run_act_rows<8, kFp16, false>(a, p, s);
 }
 
 // The gradient's blocks: `across` threads side by side, `columns` blocks of
-// them, `runs` runs of rows: ten blocks an SM over all column blocks, but no
-// run of fewer rows than a block takes at once.
+// them, `runs` runs of rows: as many blocks as are resident at once (nine an
+// SM at its registers), but no run of fewer rows than a block takes at once.
 struct ActGradPlan {
     int across, columns, runs;
 };
@@ -237,7 +245,7 @@ ActGradPlan act_grad_plan(int64_t rows, int cols, int sm_count) {
     while (p.across < kGradThreads && p.across < vectors) p.across *= 2;
     p.columns = (vectors + p.across - 1) / p.across;
     const int down = kGradThreads / p.across;
-    const int64_t runs = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * 10 / p.columns);
+    const int64_t runs = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * kGradResident / p.columns);
     p.runs = static_cast<int>(std::min((rows + down - 1) / down, runs));
     return p;
 }
@@ -253,9 +261,7 @@ cudaError_t run_act_grad(const ActGradArgs& a, const ActGradPlan& p, cudaStream_
 
 cudaError_t launch_activate(const ActArgs& a, bool fp16, int sm_count, cudaStream_t s) {
     const RowPlan p = row_plan(a.rows, a.cols, sm_count, kLimits, kPerSm);
-    if (p.each == 2) return run_act_type<2>(a, fp16, p, s);
-    if (p.each == 4) return run_act_type<4>(a, fp16, p, s);
-    return run_act_type<8>(a, fp16, p, s);
+    return fp16 ? run_act<true>(a, p, s) : run_act<false>(a, p, s);
 }
 
 int64_t activate_grad_scratch_bytes(int64_t rows, int cols, bool gated, int sm_count) {

@@ -48,26 +48,28 @@ __device__ __forceinline__ uint4 weight_at(const uint16_t* weight, int at) {
     return __ldg(reinterpret_cast<const uint4*>(weight) + at);
 }
 
-template <int NV, bool kFp16, int kOut>
+template <int NV, bool kFp16, int kOut, bool kNarrow, bool kResidual>
 __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_kernel(const NormArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
     pdl_wait();
-    const RowTeam team = row_team(team_size);
-    RowReduce reduce{buffer, team.size};
+    const RowTeam<kNarrow> team(team_size);
+    RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     uint4 x[NV], r[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) x[i] = r[i] = make_uint4(0, 0, 0, 0);
+    // The next row's loads are in flight while a row is worked on: x and r; or,
+    // without a residual, those of the next two rows (x, then r).
+    auto load_row = [&](const uint16_t* row, uint4 (&to)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (team.at + i * team.size < vectors) to[i] = load_once(row + 8 * (team.at + i * team.size));
+    };
     auto fetch = [&](int64_t row) {
         if (row >= a.rows) return;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int at = team.at + i * team.size;
-            if (at >= vectors) continue;
-            x[i] = load_once(a.x + row * a.x_stride + 8 * at);
-            if (a.residual != nullptr) r[i] = load_once(a.residual + row * a.residual_stride + 8 * at);
-        }
+        load_row(a.x + row * a.x_stride, x);
+        if constexpr (kResidual) load_row(a.residual + row * a.residual_stride, r);
     };
     float pre = 1.0f, by = 0.0f;
     if constexpr (kOut == kNormTensor) {
@@ -79,6 +81,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
     const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
     int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;   // the block's rows, together
     fetch(first + team.row);
+    if (!kResidual && first + team.row + step < a.rows) load_row(a.x + (first + team.row + step) * a.x_stride, r);
     for (; first < a.rows; first += step) {
         const int64_t row = first + team.row;
         const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
             unpack8<kFp16>(x[i], v[i]);
-            if (a.residual != nullptr) {
+            if constexpr (kResidual) {
                 pair add[4];
                 unpack8<kFp16>(r[i], add);
 #pragma unroll
@@ -98,11 +101,17 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
 #pragma unroll
             for (int e = 0; e < 4; ++e) squares = pair_fma(v[i][e], v[i][e], squares);
         }
-        fetch(row + step);
+        if constexpr (kResidual) {
+            fetch(row + step);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) x[i] = r[i];
+            if (row + 2 * step < a.rows) load_row(a.x + (row + 2 * step) * a.x_stride, r);
+        }
         float total = reduce.sum(pair_sum(squares)), eps = a.eps;
         // (a vote: rows of a warp differ, and the reduction takes all of it)
         const bool again = !(total <= 3.0e38f);
-        if (team.size < 32 ? __any_sync(0xFFFFFFFFu, again) : again) {
+        if (kNarrow ? __any_sync(0xFFFFFFFFu, again) : again) {
             const float down = again ? kDown : 1.0f;
             squares = 0;
 #pragma unroll
@@ -152,13 +161,19 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
         }
     }
     if constexpr (kOut == kNormTensor) {
+        // One atomic a block: a warp's each, on one address, took 5 us.
+        uint32_t* tops = reinterpret_cast<uint32_t*>(buffer);
         const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tensor_top));
-        if ((threadIdx.x & 31) == 0 && bits != 0) atomicMax(a.amax_bits, bits);
-        if (a.next_scale != nullptr) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = bits;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint32_t top = 0;
+            for (unsigned i = 0; i < blockDim.x >> 5; ++i) top = max(top, tops[i]);
+            if (top != 0) atomicMax(a.amax_bits, top);
             // The last block to arrive forms the next call's scale; the word
             // counts the arrivals until then (it is zeroed with the maximum).
-            __syncthreads();
-            if (threadIdx.x == 0) {
+            if (a.next_scale != nullptr) {
                 __threadfence();
                 if (atomicAdd(reinterpret_cast<uint32_t*>(a.next_scale), 1u) == gridDim.x - 1) {
                     __threadfence();
@@ -170,6 +185,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
 }
 
 __global__ void zero_words_kernel(uint32_t* a, uint32_t* b) {
+    pdl_launch_dependents();   // the norm's launch overlaps this one's; it waits for its end
     pdl_wait();
     *a = 0u;
     if (b != nullptr) *b = 0u;
@@ -182,42 +198,45 @@ __global__ void next_scale_kernel(const float* amax, float* scale) {
     *scale = scale_of_amax(*amax);
 }
 
+// The gradient's blocks: at most 128 registers a thread for the elements as
+// they came, the columns' sums in FP32 and (two vectors a thread) the next
+// row's loads.
+constexpr int kGradLimits[3] = {512, 512, 512};
+constexpr int kGradPerSm[3] = {512, 512, 512};
+
 // Columns' sums of a block: the teams of a warp and then the warps are added in
 // order; one partial a block.
-template <int NV>
-constexpr int grad_limit() { return NV == 2 ? 384 : 512; }
-template <int NV>
-constexpr int grad_min() { return NV == 2 ? 2 : 1; }
-constexpr int kGradLimits[3] = {384, 512, 512};
-constexpr int kGradPerSm[3] = {768, 512, 512};
-
-template <int NV, bool kFp16>
-__global__ void __launch_bounds__(grad_limit<NV>(), grad_min<NV>()) rmsnorm_grad_kernel(const NormGradArgs a,
+template <int NV, bool kFp16, bool kNarrow>
+__global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const NormGradArgs a,
                                                                                          int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
-    __shared__ float columns[4][256];   // narrow rows: four warps' sums
+    __shared__ float columns[kNarrow ? 4 : 1][256];   // four warps' sums
     pdl_wait();
-    const RowTeam team = row_team(team_size);
-    RowReduce reduce{buffer, team.size};
+    const RowTeam<kNarrow> team(team_size);
+    RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    constexpr bool kAhead = NV == 2;   // the next row's loads in flight: registers
+    constexpr bool kAhead = NV == 2;
     pair dw[NV][4];
-    uint4 x[NV], d[NV], next_d[NV];
+    uint4 next_x[NV], next_d[NV], next_add[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        x[i] = next_d[i] = make_uint4(0, 0, 0, 0);
+        next_x[i] = next_d[i] = next_add[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw[i][e] = 0;
     }
     auto fetch = [&](int64_t row) {
         if (row >= a.rows) return;
+        const uint16_t* x_row = a.x + row * a.x_stride;
+        const uint16_t* d_row = a.dy + row * a.dy_stride;
+        const uint16_t* add_row = a.dsum + row * a.dsum_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
             if (at >= vectors) continue;
-            x[i] = load_once(a.x + row * a.x_stride + 8 * at);
-            next_d[i] = load_once(a.dy + row * a.dy_stride + 8 * at);
+            next_x[i] = load_once(x_row + 8 * at);
+            next_d[i] = load_once(d_row + 8 * at);
+            if (a.dsum != nullptr) next_add[i] = load_once(add_row + 8 * at);
         }
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
@@ -227,18 +246,21 @@ __global__ void __launch_bounds__(grad_limit<NV>(), grad_min<NV>()) rmsnorm_grad
         const int64_t row = first + team.row;
         const int end = row < a.rows ? vectors : 0;
         if (!kAhead) fetch(row);
-        pair v[NV][4];
-        uint4 add[NV];
+        uint4 x[NV], d[NV], add[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int at = team.at + i * team.size;
-            add[i] = make_uint4(0, 0, 0, 0);
-            if (a.dsum != nullptr && at < end) add[i] = load_once(a.dsum + row * a.dsum_stride + 8 * at);
-            unpack8<kFp16>(x[i], v[i]);
+            x[i] = next_x[i];
             d[i] = next_d[i];
+            add[i] = next_add[i];
         }
         if (kAhead) fetch(row + step);
-        // dy, and g = dy w, formed where they are needed: registers
+        const int64_t later = row + (kAhead ? 2 : 1) * step;
+        if (!kNarrow && threadIdx.x == 0 && later < a.rows) {
+            prefetch_row(a.x + later * a.x_stride, 2 * a.cols);
+            prefetch_row(a.dy + later * a.dy_stride, 2 * a.cols);
+            if (a.dsum != nullptr) prefetch_row(a.dsum + later * a.dsum_stride, 2 * a.cols);
+        }
+        // dy, and g = dy w
         auto g_of = [&](int i, pair (&dy)[4], pair (&g)[4]) {
             unpack8<kFp16>(d[i], dy);
             const int at = team.at + i * team.size;
@@ -251,55 +273,60 @@ __global__ void __launch_bounds__(grad_limit<NV>(), grad_min<NV>()) rmsnorm_grad
                 for (int e = 0; e < 4; ++e) g[e] = dy[e];
             }
         };
-        float2 both;   // sums of s^2 and of g s
-        auto sums = [&]() {
+        float down = 1.0f, eps = a.eps;
+        float2 both;   // sums of (s down)^2 and of g s down
+        bool again = false;   // out of FP32's range: once more, scaled down
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            down = again ? kDown : 1.0f;
             pair squares = 0, dot = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                pair dy[4], g[4];
+                pair v[4], dy[4], g[4];
+                unpack8<kFp16>(x[i], v);
                 g_of(i, dy, g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    squares = pair_fma(v[i][e], v[i][e], squares);
-                    dot = pair_fma(g[e], v[i][e], dot);
+                    v[e] = pair_mul(v[e], pair_of(down));
+                    squares = pair_fma(v[e], v[e], squares);
+                    dot = pair_fma(g[e], v[e], dot);
                 }
             }
             both = reduce.sum2(pair_sum(squares), pair_sum(dot));
-        };
-        sums();
-        float eps = a.eps, down = 1.0f;
-        const bool again = !(both.x <= 3.0e38f);
-        if (team.size < 32 ? __any_sync(0xFFFFFFFFu, again) : again) {
-            down = again ? kDown : 1.0f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(down));
-            sums();
-            eps = eps * down * down;
+            for (int i = 0; i < NV; ++i) {
+                forget(x[i]);
+                forget(d[i]);
+            }
+            again = pass == 0 && !(both.x <= 3.0e38f);
+            // (a vote: rows of a warp differ, and the reduction takes all of it)
+            if (kNarrow ? !__any_sync(0xFFFFFFFFu, again) : !again) break;
         }
+        eps = eps * down * down;
         const float inv = rsqrtf(fmaf(both.x, inv_cols, eps));
         const float share = both.y * inv * inv_cols;   // mean(g u)
-        const float out_by = inv * down;
+        const float unit = inv * down;                 // u = s unit
+        uint16_t* dx_row = a.dx + row * a.dx_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
             if (at >= end) continue;
-            pair dy[4], g[4], more[4];
+            pair v[4], dy[4], g[4], more[4];
+            unpack8<kFp16>(x[i], v);
             g_of(i, dy, g);
             unpack8<kFp16>(add[i], more);   // zeros without dsum
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const pair u = pair_mul(v[i][e], pair_of(inv));
+                const pair u = pair_mul(v[e], pair_of(unit));
                 dw[i][e] = pair_fma(dy[e], u, dw[i][e]);
-                g[e] = pair_fma(pair_fma(u, pair_of(-share), g[e]), pair_of(out_by), more[e]);
+                g[e] = pair_fma(pair_fma(u, pair_of(-share), g[e]), pair_of(unit), more[e]);
             }
-            *reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + 8 * at) = pack8<kFp16>(g);
+            *reinterpret_cast<uint4*>(dx_row + 8 * at) = pack8<kFp16>(g);
         }
     }
     if (a.partials == nullptr) return;
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
-    if (team.size >= 32) {
+    if constexpr (!kNarrow) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(grad_limit<NV>(), grad_min<NV>()) rmsnorm_grad
         }
         return;
     }
-    const int warp = threadIdx.x >> 5;
+    const int warp = kNarrow ? threadIdx.x >> 5 : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {   // narrow rows have two vectors a thread, 256 columns
         for (int o = team.size; o < 32; o *= 2)
@@ -345,28 +372,40 @@ __global__ void __launch_bounds__(1024) join_columns_kernel(const float* __restr
     if (lane == 0 && static_cast<int>(blockIdx.x) * 32 + warp < cols) out[blockIdx.x * 32 + warp] = sum;
 }
 
-template <int NV, bool kFp16>
-cudaError_t run_norm(const NormArgs& a, int out, const RowPlan& p, cudaStream_t s) {
+template <int NV, bool kFp16, bool kNarrow, bool kResidual>
+cudaError_t run_norm_out(const NormArgs& a, int out, const RowPlan& p, cudaStream_t s) {
     const dim3 grid(p.blocks), block(p.threads);
-    if (out == kNormRows) return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormRows>, grid, block, 0, s, a, p.team);
-    if (out == kNormTensor) return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormTensor>, grid, block, 0, s, a, p.team);
-    return launch_kernel(rmsnorm_kernel<NV, kFp16, kNormHalf>, grid, block, 0, s, a, p.team);
+    auto launch = [&](void (*kernel)(const NormArgs, int)) { return launch_kernel(kernel, grid, block, 0, s, a, p.team); };
+    if (out == kNormRows) return launch(rmsnorm_kernel<NV, kFp16, kNormRows, kNarrow, kResidual>);
+    if (out == kNormTensor) return launch(rmsnorm_kernel<NV, kFp16, kNormTensor, kNarrow, kResidual>);
+    return launch(rmsnorm_kernel<NV, kFp16, kNormHalf, kNarrow, kResidual>);
 }
 
-template <int NV>
-cudaError_t run_norm_type(const NormArgs& a, int out, bool fp16, const RowPlan& p, cudaStream_t s) {
-    return fp16 ? run_norm<NV, true>(a, out, p, s) : run_norm<NV, false>(a, out, p, s);
+template <int NV, bool kFp16, bool kNarrow>
+cudaError_t run_norm_rows(const NormArgs& a, int out, const RowPlan& p, cudaStream_t s) {
+    return a.residual != nullptr ? run_norm_out<NV, kFp16, kNarrow, true>(a, out, p, s)
+                                 : run_norm_out<NV, kFp16, kNarrow, false>(a, out, p, s);
+}
+
+template <bool kFp16>
+cudaError_t run_norm(const NormArgs& a, int out, const RowPlan& p, cudaStream_t s) {
+    if (p.narrow) return run_norm_rows<2, kFp16, true>(a, out, p, s);
+    if (p.each == 2) return run_norm_rows<2, kFp16, false>(a, out, p, s);
+    if (p.each == 4) return run_norm_rows<4, kFp16, false>(a, out, p, s);
+    return run_norm_rows<8, kFp16, false>(a, out, p, s);
 }
 
 RowPlan grad_plan(int64_t rows, int cols, int sm_count) {
     return row_plan(rows, cols, sm_count, kGradLimits, kGradPerSm);
 }
 
-template <int NV>
-cudaError_t run_grad(const NormGradArgs& a, bool fp16, const RowPlan& p, cudaStream_t s) {
+template <bool kFp16>
+cudaError_t run_grad(const NormGradArgs& a, const RowPlan& p, cudaStream_t s) {
     const dim3 grid(p.blocks), block(p.threads);
-    return fp16 ? launch_kernel(rmsnorm_grad_kernel<NV, true>, grid, block, 0, s, a, p.team)
-                : launch_kernel(rmsnorm_grad_kernel<NV, false>, grid, block, 0, s, a, p.team);
+    if (p.narrow) return launch_kernel(rmsnorm_grad_kernel<2, kFp16, true>, grid, block, 0, s, a, p.team);
+    if (p.each == 2) return launch_kernel(rmsnorm_grad_kernel<2, kFp16, false>, grid, block, 0, s, a, p.team);
+    if (p.each == 4) return launch_kernel(rmsnorm_grad_kernel<4, kFp16, false>, grid, block, 0, s, a, p.team);
+    return launch_kernel(rmsnorm_grad_kernel<8, kFp16, false>, grid, block, 0, s, a, p.team);
 }
 
 }  // namespace
@@ -389,9 +428,7 @@ cudaError_t launch_rmsnorm(const NormArgs& args, int out, bool fp16, int sm_coun
     }
     if (a.rows > 0) {
         const RowPlan p = row_plan(a.rows, a.cols, sm_count, kLimits, kPerSm);
-        const cudaError_t e = p.each == 2   ? run_norm_type<2>(a, out, fp16, p, s)
-                              : p.each == 4 ? run_norm_type<4>(a, out, fp16, p, s)
-                                            : run_norm_type<8>(a, out, fp16, p, s);
+        const cudaError_t e = fp16 ? run_norm<true>(a, out, p, s) : run_norm<false>(a, out, p, s);
         if (e != cudaSuccess) return e;
     }
     if (after == nullptr) return cudaSuccess;
@@ -405,9 +442,7 @@ int64_t rmsnorm_grad_scratch_bytes(int64_t rows, int cols, int sm_count) {
 cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool fp16, float* dweight, int sm_count, cudaStream_t s) {
     const RowPlan p = grad_plan(a.rows, a.cols, sm_count);
     if (a.rows > 0) {
-        const cudaError_t e = p.each == 2   ? run_grad<2>(a, fp16, p, s)
-                              : p.each == 4 ? run_grad<4>(a, fp16, p, s)
-                                            : run_grad<8>(a, fp16, p, s);
+        const cudaError_t e = fp16 ? run_grad<true>(a, p, s) : run_grad<false>(a, p, s);
         if (e != cudaSuccess) return e;
     }
     return dweight == nullptr ? cudaSuccess : launch_join_columns(a.partials, p.blocks, a.cols, dweight, s);

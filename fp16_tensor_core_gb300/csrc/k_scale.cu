@@ -132,6 +132,7 @@ __global__ void scale_pow2_kernel(const float* __restrict__ amax, float* __restr
 // the scale word when the reduction's last CTA writes the scale).
 __global__ void amax_init_kernel(uint32_t* __restrict__ out_bits, uint32_t* __restrict__ count,
                                  uint32_t* __restrict__ other) {
+    pdl_launch_dependents();   // the reduction's launch overlaps this one's; it waits for its end
     pdl_wait();
     *out_bits = 0u;
     if (count != nullptr) *count = 0u;

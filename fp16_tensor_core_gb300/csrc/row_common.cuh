@@ -82,6 +82,16 @@ __device__ __forceinline__ uint2 load_once8(const void* p) {
     return v;
 }
 
+// A row to come moves into L2 (one thread; 16-byte aligned, a multiple of 16
+// bytes): no registers, and the loads that follow wait a third as long.
+__device__ __forceinline__ void prefetch_row(const void* p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p), "r"(bytes) : "memory");
+}
+
+// Forgets what has been formed from packed elements: they are unpacked again,
+// where the compiler would keep (and spill) twice their registers.
+__device__ __forceinline__ void forget(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+
 // The largest magnitude of eight values and of one that there is.
 __device__ __forceinline__ float top8(const pair (&f)[4], float top) {
 #pragma unroll
@@ -89,35 +99,60 @@ __device__ __forceinline__ float top8(const pair (&f)[4], float top) {
     return top;
 }
 
-// The threads of a row: a block, or for narrow rows a power of two of lanes,
-// several rows to a warp.
+// The threads of a row: a block, or for narrow rows (kNarrow) a power of two
+// of lanes, several rows to a warp.  Two kernels for the two: where a row is
+// a block's, its addresses are uniform and its reductions have no loops.
+template <bool kNarrow>
 struct RowTeam {
     int size;     // threads a row
     int at;       // this thread's place in its row
     int row;      // the row's place among those of the block
     int rows;     // rows of a block
+    __device__ __forceinline__ explicit RowTeam(int team_size) {
+        if constexpr (kNarrow) {
+            size = team_size;
+            at = static_cast<int>(threadIdx.x) & (size - 1);
+            row = static_cast<int>(threadIdx.x) / size;
+            rows = static_cast<int>(blockDim.x) / size;
+        } else {
+            size = static_cast<int>(blockDim.x);
+            at = static_cast<int>(threadIdx.x);
+            row = 0;
+            rows = 1;
+        }
+    }
 };
-__device__ __forceinline__ RowTeam row_team(int size) {
-    const int t = static_cast<int>(threadIdx.x);
-    if (size >= 32) return {size, t, 0, 1};
-    return {size, t & (size - 1), t / size, static_cast<int>(blockDim.x) / size};
-}
 
 // Reductions over a row's threads that give every one the result; all threads
 // of the block take part.  Two buffers, taken in turn: between two uses of
 // one lies the barrier of the other, so that one barrier a reduction is
 // enough.
+template <bool kNarrow>
 struct RowReduce {
     float2 (*buffer)[kRowThreads / 32];   // [2], shared memory
     int size;                             // threads a row
     int turn = 0;
 
+    __device__ __forceinline__ float sum(float a) {
+        if constexpr (kNarrow) {
+            for (int o = size >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            return a;
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            a = exchange(make_float2(a, 0.0f)).x;
+#pragma unroll
+            for (int o = kRowThreads / 64; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            return a;
+        }
+    }
     __device__ __forceinline__ float2 sum2(float a, float b) {
-        for (int o = min(size, 32) >> 1; o > 0; o >>= 1) {
+        if constexpr (kNarrow) return make_float2(sum(a), sum(b));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
             b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
         }
-        if (size <= 32) return make_float2(a, b);
         const float2 t = exchange(make_float2(a, b));
         a = t.x;
         b = t.y;
@@ -126,41 +161,41 @@ struct RowReduce {
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
             b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
         }
-        return make_float2(__shfl_sync(0xFFFFFFFFu, a, 0), __shfl_sync(0xFFFFFFFFu, b, 0));
+        return make_float2(a, b);
     }
-    __device__ __forceinline__ float sum(float a) { return sum2(a, 0.0f).x; }
 
-    // Two maxima of magnitudes (as ordered bits: NaN above all).
-    __device__ __forceinline__ float2 max2(float top_a, float top_b) {
-        uint32_t a = __float_as_uint(top_a), b = __float_as_uint(top_b);
-        if (size < 32) {
-            for (int o = size >> 1; o > 0; o >>= 1) {
-                a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-                b = max(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
-            }
-        } else {
-            a = __reduce_max_sync(0xFFFFFFFFu, a);
-            b = __reduce_max_sync(0xFFFFFFFFu, b);
-        }
-        if (size <= 32) return make_float2(__uint_as_float(a), __uint_as_float(b));
-        const float2 t = exchange(make_float2(__uint_as_float(a), __uint_as_float(b)));
-        a = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(t.x));
-        b = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(t.y));
-        return make_float2(__uint_as_float(a), __uint_as_float(b));
+    // Maxima of magnitudes (as ordered bits: NaN above all).
+    __device__ __forceinline__ float max1(float a) {
+        if constexpr (kNarrow) return narrow_max(a);
+        const float2 t = exchange(make_float2(warp_max(a), 0.0f));
+        return warp_max(t.x);
     }
-    __device__ __forceinline__ float max1(float a) { return max2(a, 0.0f).x; }
+    __device__ __forceinline__ float2 max2(float a, float b) {
+        if constexpr (kNarrow) return make_float2(narrow_max(a), narrow_max(b));
+        const float2 t = exchange(make_float2(warp_max(a), warp_max(b)));
+        return make_float2(warp_max(t.x), warp_max(t.y));
+    }
 
 private:
-    // Every warp's value to every warp: lane i gets warp i's (or zeros).
+    static __device__ __forceinline__ float warp_max(float a) {
+        return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));
+    }
+    __device__ __forceinline__ float narrow_max(float a) {
+        uint32_t v = __float_as_uint(a);
+        for (int o = size >> 1; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        return __uint_as_float(v);
+    }
+    // Every warp's value to every warp: lanes i and i + 16 get warp i's (or zeros).
     __device__ __forceinline__ float2 exchange(float2 v) {
         float2* buf = buffer[turn];
         turn ^= 1;
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) buf[threadIdx.x >> 5] = v;
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
-        return lane < static_cast<int>(blockDim.x) >> 5 ? buf[lane] : make_float2(0.0f, 0.0f);
+        const unsigned from = threadIdx.x & 15;
+        return from < blockDim.x >> 5 ? buf[from] : make_float2(0.0f, 0.0f);
     }
 };
+static_assert(kRowThreads / 32 == 16, "exchange");
 
 __device__ __forceinline__ float pair_sum(pair v) {
     const float2 f = floats_of(v);
@@ -190,6 +225,7 @@ __device__ __forceinline__ float row_scale(float top) {
 // blocks of `threads`, and as many of them as are resident at once.
 struct RowPlan {
     int each, team, threads, blocks;
+    bool narrow;
 };
 // per_sm: threads an SM holds at the kernel's registers, by vectors a thread
 // (2, 4, 8).
@@ -202,6 +238,7 @@ inline RowPlan row_plan(int64_t rows, int cols, int sm_count, const int (&limits
     const int need = (vectors + p.each - 1) / p.each;
     int64_t teams = rows;   // blocks that every row would fill
     if (need <= 16) {
+        p.narrow = true;
         p.team = 1;
         while (p.team < need) p.team *= 2;
         p.threads = 128;
