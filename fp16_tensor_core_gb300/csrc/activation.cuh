@@ -172,6 +172,23 @@ __device__ __forceinline__ ValueSlope activation_slope(int act, pair x) {
     }
 }
 
+// Calls f with the activation as a compile-time constant: one branch for all
+// that f does.
+template <int kAct>
+struct ActConstant {
+    static constexpr int value = kAct;
+};
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+    switch (act) {
+        case DG_ACT_RELU: f(ActConstant<DG_ACT_RELU>{}); break;
+        case DG_ACT_GELU: f(ActConstant<DG_ACT_GELU>{}); break;
+        case DG_ACT_GELU_TANH: f(ActConstant<DG_ACT_GELU_TANH>{}); break;
+        case DG_ACT_SILU: f(ActConstant<DG_ACT_SILU>{}); break;
+        default: f(ActConstant<DG_ACT_NONE>{}); break;
+    }
+}
+
 // Division by a given scale as two multiplications: x / s = (x pre) inv.  pre
 // is 1 but for scales whose reciprocal FP32 does not hold; with it the
 // product overflows or vanishes only where the code saturates or is 0 anyway.

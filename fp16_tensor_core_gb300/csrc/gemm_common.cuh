@@ -292,12 +292,6 @@ __device__ __forceinline__ void prefetch_residual(const Params& p, int row, bool
             asm volatile("prefetch.global.L2 [%0];" :: "l"(src + i + 64 * half));
 }
 
-template <int kAct>
-__device__ __forceinline__ void activate32(pair (&v)[16]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = activation(kAct, v[i]);
-}
-
 // The values of 32 accumulator columns of one row; sa: the row's scale,
 // columns: theirs (stage_columns).  Returns their largest magnitude inside D
 // (ordered bits) when it is wanted, before the division by the output's scale.
@@ -311,13 +305,10 @@ __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col
         const ulonglong2 c = reinterpret_cast<const ulonglong2*>(columns)[i];
         v[i] = pair_fma(pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), pair_mul(row_scale, c.x), c.y);
     }
-    switch (p.epi.act) {
-        case DG_ACT_RELU: activate32<DG_ACT_RELU>(v); break;
-        case DG_ACT_GELU: activate32<DG_ACT_GELU>(v); break;
-        case DG_ACT_GELU_TANH: activate32<DG_ACT_GELU_TANH>(v); break;
-        case DG_ACT_SILU: activate32<DG_ACT_SILU>(v); break;
-        default: break;
-    }
+    with_activation(p.epi.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = activation(act.value, v[i]);
+    });
     if (p.epi.residual != nullptr) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

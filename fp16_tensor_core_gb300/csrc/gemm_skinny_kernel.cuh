@@ -152,12 +152,6 @@ __device__ __forceinline__ void load_residual16(const SkParams& p, bool live, in
     }
 }
 
-template <int kAct>
-__device__ __forceinline__ void activate16(pair (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activation(kAct, v[i]);
-}
-
 // act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n] for rows c0 ..
 // c0 + jn - 1 (sa: the rows' scales, in shared memory); returns the largest
 // magnitude (ordered bits).
@@ -171,13 +165,10 @@ __device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, co
         v[2 * i] = pair_fma(pair_of(f[4 * i], f[4 * i + 1]), pair_mul(s.x, pair_of(col.sb)), pair_of(col.bias));
         v[2 * i + 1] = pair_fma(pair_of(f[4 * i + 2], f[4 * i + 3]), pair_mul(s.y, pair_of(col.sb)), pair_of(col.bias));
     }
-    switch (p.epi.act) {
-        case DG_ACT_RELU: activate16<DG_ACT_RELU>(v); break;
-        case DG_ACT_GELU: activate16<DG_ACT_GELU>(v); break;
-        case DG_ACT_GELU_TANH: activate16<DG_ACT_GELU_TANH>(v); break;
-        case DG_ACT_SILU: activate16<DG_ACT_SILU>(v); break;
-        default: break;
-    }
+    with_activation(p.epi.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activation(act.value, v[i]);
+    });
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

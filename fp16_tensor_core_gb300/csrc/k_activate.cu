@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = team.at + i * team.size;
-                if (at < end) x[h][i] = load_once(x_row + h * a.cols + 8 * at);
+                load_if(at < end, x_row + h * a.cols + 8 * at, x[h][i]);
             }
         if (!kNarrow && threadIdx.x == 0 && row + step < a.rows)
             prefetch_row(a.x + (row + step) * a.x_stride, 2 * kHalves * a.cols);
@@ -79,22 +79,21 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) forget(x[h][i]);
-            const float scale[2] = {row_scale(both.x), row_scale(both.y)};
+            const float halves[2] = {both.x, both.y};
             if (team.at == 0 && end != 0) {
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) a.x_scale[row * kHalves + h] = scale[h];
+                for (int h = 0; h < kHalves; ++h) a.x_scale[row * kHalves + h] = row_scale(halves[h]);
             }
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-                const float by = __frcp_rn(scale[h]);
+                const float by = row_factor(halves[h]);
                 uint8_t* q_row = a.x_q + (row * kHalves + h) * a.cols;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int at = team.at + i * team.size;
-                    if (at >= end) continue;
                     pair f[4];
                     unpack8<kFp16>(x[h][i], f);
-                    *reinterpret_cast<uint2*>(q_row + 8 * at) = codes8(f, by);
+                    store_if(at < end, q_row + 8 * at, codes8(f, by));
                 }
             }
         }
@@ -104,43 +103,48 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
 #pragma unroll
             for (int i = 0; i < NV; ++i) forget(x[h][i]);
         pair y[NV][4];
+        with_activation(a.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                unpack8<kFp16>(x[0][i], y[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[i][e] = activation(act.value, y[i][e]);
+            }
+        });
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            unpack8<kFp16>(x[0][i], y[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[i][e] = activation(a.act, y[i][e]);
             if constexpr (kGated) {
                 pair up[4];
                 unpack8<kFp16>(x[kHalves - 1][i], up);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[i][e] = pair_mul(y[i][e], up[e]);
             }
-            if (team.at + i * team.size < end) top = top8(y[i], top);
+            top = top8(y[i], top);   // (zeros past the row; a team without one has its own maximum)
         }
         if (a.y != nullptr) {
             uint16_t* y_row = a.y + row * a.y_stride;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = team.at + i * team.size;
-                if (at < end) *reinterpret_cast<uint4*>(y_row + 8 * at) = pack8<kFp16>(y[i]);
+                store_if(at < end, y_row + 8 * at, pack8<kFp16>(y[i]));
             }
         }
         if (a.q != nullptr) {
-            const float scale = row_scale(reduce.max1(top));
-            const float by = __frcp_rn(scale);
-            if (team.at == 0 && end != 0) a.q_scale[row] = scale;
+            top = reduce.max1(top);
+            const float by = row_factor(top);
+            if (team.at == 0 && end != 0) a.q_scale[row] = row_scale(top);
             uint8_t* q_row = a.q + row * a.cols;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = team.at + i * team.size;
-                if (at < end) *reinterpret_cast<uint2*>(q_row + 8 * at) = codes8(y[i], by);
+                store_if(at < end, q_row + 8 * at, codes8(y[i], by));
             }
         }
     }
 }
 
-constexpr int kGradResident = 9;    // blocks an SM
+constexpr int kGradResident = 8;    // blocks an SM
 constexpr int kGradThreads = 128;   // 1024 columns a block, or fewer and several rows at once
 
 template <bool kFp16, bool kGated, bool kCodes>
@@ -159,29 +163,49 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
 #pragma unroll
         for (int e = 0; e < 4; ++e) sums[h][e] = 0;
     if (c < a.cols) {
+        // The next row's loads are in flight while a row is worked on.
+        uint4 next_dy = make_uint4(0, 0, 0, 0), next_x[kHalves];
+        uint2 next_q[kHalves];
+        float next_scale[kHalves];
+        auto fetch = [&](int64_t row) {
+            next_dy = load_once(a.dy + row * a.dy_stride + c);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                if constexpr (kCodes) {
+                    next_q[h] = load_once8(a.x_q + row * width + static_cast<int64_t>(h) * a.cols + c);
+                    next_scale[h] = __ldg(a.x_scale + row * kHalves + h);
+                } else {
+                    next_x[h] = load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + c);
+                }
+            }
+        };
+        int64_t row = first + t / across;
+        if (row < end) fetch(row);
 #pragma unroll 1
-        for (int64_t row = first + t / across; row < end; row += down) {
+        for (; row < end; row += down) {
             pair dy[4], x[kHalves][4];
-            unpack8<kFp16>(load_once(a.dy + row * a.dy_stride + c), dy);
+            unpack8<kFp16>(next_dy, dy);
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 if constexpr (kCodes)
-                    decode8(load_once8(a.x_q + row * width + static_cast<int64_t>(h) * a.cols + c),
-                            __ldg(a.x_scale + row * kHalves + h), x[h]);
+                    decode8(next_q[h], next_scale[h], x[h]);
                 else
-                    unpack8<kFp16>(load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + c), x[h]);
+                    unpack8<kFp16>(next_x[h], x[h]);
             }
+            if (row + down < end) fetch(row + down);
             pair dx[kHalves][4];
+            with_activation(a.act, [&](auto act) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const ValueSlope f = activation_slope(a.act, x[0][e]);
-                if constexpr (kGated) {
-                    dx[0][e] = pair_mul(pair_mul(dy[e], x[kHalves - 1][e]), f.slope);
-                    dx[kHalves - 1][e] = pair_mul(dy[e], f.value);
-                } else {
-                    dx[0][e] = pair_mul(dy[e], f.slope);
+                for (int e = 0; e < 4; ++e) {
+                    const ValueSlope f = activation_slope(act.value, x[0][e]);
+                    if constexpr (kGated) {
+                        dx[0][e] = pair_mul(pair_mul(dy[e], x[kHalves - 1][e]), f.slope);
+                        dx[kHalves - 1][e] = pair_mul(dy[e], f.value);
+                    } else {
+                        dx[0][e] = pair_mul(dy[e], f.slope);
+                    }
                 }
-            }
+            });
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
 #pragma unroll
@@ -192,6 +216,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
         }
     }
     if (a.partials == nullptr) return;
+    pdl_launch_dependents();   // the join's launch
     float* part = a.partials + blockIdx.y * width;
     if (down == 1) {
         if (c >= a.cols) return;
@@ -234,7 +259,7 @@ cudaError_t run_act(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
 }
 
 // The gradient's blocks: `across` threads side by side, `columns` blocks of
-// them, `runs` runs of rows: as many blocks as are resident at once (nine an
+// them, `runs` runs of rows: as many blocks as are resident at once (eight an
 // SM at its registers), but no run of fewer rows than a block takes at once.
 struct ActGradPlan {
     int across, columns, runs;

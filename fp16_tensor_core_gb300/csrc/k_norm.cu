@@ -43,11 +43,6 @@ constexpr int block_min() { return NV == 8 ? 1 : 2; }
 constexpr int kLimits[3] = {512, 384, 512};
 constexpr int kPerSm[3] = {1024, 768, 512};
 
-// A vector of the weight: every block reads it for every row, from L1.
-__device__ __forceinline__ uint4 weight_at(const uint16_t* weight, int at) {
-    return __ldg(reinterpret_cast<const uint4*>(weight) + at);
-}
-
 template <int NV, bool kFp16, int kOut, bool kNarrow, bool kResidual>
 __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_kernel(const NormArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
@@ -56,20 +51,22 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
     RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    uint4 x[NV], r[NV];
+    // The weight, packed, in registers where they reach; else it is read again
+    // for every row.
+    constexpr bool kKeepWeight = NV == 2 && (kOut == kNormRows || (kOut == kNormTensor && !kResidual));
+    uint4 x[NV], r[NV], w[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = r[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < NV; ++i) {
+        x[i] = r[i] = make_uint4(0, 0, 0, 0);
+        const int at = team.at + i * team.size;
+        if (kKeepWeight) w[i] = weight_if(a.weight != nullptr && at < vectors, a.weight, at);
+    }
     // The next row's loads are in flight while a row is worked on: x and r; or,
     // without a residual, those of the next two rows (x, then r).
     auto load_row = [&](const uint16_t* row, uint4 (&to)[NV]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (team.at + i * team.size < vectors) to[i] = load_once(row + 8 * (team.at + i * team.size));
-    };
-    auto fetch = [&](int64_t row) {
-        if (row >= a.rows) return;
-        load_row(a.x + row * a.x_stride, x);
-        if constexpr (kResidual) load_row(a.residual + row * a.residual_stride, r);
+            load_if(team.at + i * team.size < vectors, row + 8 * (team.at + i * team.size), to[i]);
     };
     float pre = 1.0f, by = 0.0f;
     if constexpr (kOut == kNormTensor) {
@@ -80,8 +77,16 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
     float tensor_top = 0.0f;
     const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
     int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;   // the block's rows, together
-    fetch(first + team.row);
-    if (!kResidual && first + team.row + step < a.rows) load_row(a.x + (first + team.row + step) * a.x_stride, r);
+    // The addresses of x, residual and codes are stepped, not multiplied out
+    // again (all of them stepped took more registers than there are).
+    const uint16_t* x_next = a.x + (first + team.row) * a.x_stride;
+    const uint16_t* r_next = kResidual ? a.residual + (first + team.row) * a.residual_stride : nullptr;
+    uint8_t* q_row = kOut != kNormHalf ? a.q + (first + team.row) * a.cols : nullptr;
+    if (first + team.row < a.rows) {
+        load_row(x_next, x);
+        if constexpr (kResidual) load_row(r_next, r);
+    }
+    if (!kResidual && first + team.row + step < a.rows) load_row(x_next += step * a.x_stride, r);
     for (; first < a.rows; first += step) {
         const int64_t row = first + team.row;
         const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
@@ -96,17 +101,19 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i][e] = pair_add(v[i][e], add[e]);
             }
-            if (a.sum != nullptr && at < end)
-                *reinterpret_cast<uint4*>(a.sum + row * a.sum_stride + 8 * at) = pack8<kFp16>(v[i]);
+            if (a.sum != nullptr) store_if(at < end, a.sum + row * a.sum_stride + 8 * at, pack8<kFp16>(v[i]));
 #pragma unroll
             for (int e = 0; e < 4; ++e) squares = pair_fma(v[i][e], v[i][e], squares);
         }
         if constexpr (kResidual) {
-            fetch(row + step);
+            if (row + step < a.rows) {
+                load_row(x_next += step * a.x_stride, x);
+                load_row(r_next += step * a.residual_stride, r);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) x[i] = r[i];
-            if (row + 2 * step < a.rows) load_row(a.x + (row + 2 * step) * a.x_stride, r);
+            if (row + 2 * step < a.rows) load_row(x_next += step * a.x_stride, r);
         }
         float total = reduce.sum(pair_sum(squares)), eps = a.eps;
         // (a vote: rows of a warp differ, and the reduction takes all of it)
@@ -130,35 +137,36 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(inv));
-            if (a.weight != nullptr && team.at + i * team.size < vectors) {
+            const int at = team.at + i * team.size;
+            if (a.weight != nullptr) {
                 pair f[4];
-                unpack8<kFp16>(weight_at(a.weight, team.at + i * team.size), f);
+                unpack8<kFp16>(kKeepWeight ? w[i] : weight_if(at < vectors, a.weight, at), f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], f[e]);
             }
-            if (kOut != kNormHalf && team.at + i * team.size < end) top = top8(v[i], top);
+            if (kOut != kNormHalf) top = top8(v[i], top);   // (zeros past the row)
         }
         if constexpr (kOut == kNormRows) {
-            const float scale = row_scale(reduce.max1(top));
-            by = __frcp_rn(scale);
-            if (team.at == 0 && end != 0) a.row_scale[row] = scale;
+            top = reduce.max1(top);
+            by = row_factor(top);
+            if (team.at == 0 && end != 0) a.row_scale[row] = row_scale(top);
         }
-        if constexpr (kOut == kNormTensor)   // (fmaxf would drop a NaN)
+        if (kOut == kNormTensor && end != 0)   // (fmaxf would drop a NaN)
             tensor_top = __uint_as_float(max(__float_as_uint(tensor_top), __float_as_uint(top)));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
-            if (at >= end) continue;
             if constexpr (kOut == kNormHalf) {
-                *reinterpret_cast<uint4*>(a.y + row * a.y_stride + 8 * at) = pack8<kFp16>(v[i]);
+                store_if(at < end, a.y + row * a.y_stride + 8 * at, pack8<kFp16>(v[i]));
             } else {
                 if constexpr (kOut == kNormTensor) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(pre));
                 }
-                *reinterpret_cast<uint2*>(a.q + row * a.cols + 8 * at) = codes8(v[i], by);
+                store_if(at < end, q_row + 8 * at, codes8(v[i], by));
             }
         }
+        if (kOut != kNormHalf) q_row += step * a.cols;
     }
     if constexpr (kOut == kNormTensor) {
         // One atomic a block: a warp's each, on one address, took 5 us.
@@ -216,56 +224,60 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
     RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    // Two vectors a thread: the next row's x and dy are loaded ahead, and the
+    // packed weight stays in registers.
     constexpr bool kAhead = NV == 2;
     pair dw[NV][4];
-    uint4 next_x[NV], next_d[NV], next_add[NV];
+    uint4 next_x[NV], next_d[NV], add[NV], w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        next_x[i] = next_d[i] = next_add[i] = make_uint4(0, 0, 0, 0);
+        const int at = team.at + i * team.size;
+        next_x[i] = next_d[i] = add[i] = make_uint4(0, 0, 0, 0);
+        if (kAhead) w[i] = weight_if(a.weight != nullptr && at < vectors, a.weight, at);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw[i][e] = 0;
     }
-    auto fetch = [&](int64_t row) {
-        if (row >= a.rows) return;
-        const uint16_t* x_row = a.x + row * a.x_stride;
-        const uint16_t* d_row = a.dy + row * a.dy_stride;
-        const uint16_t* add_row = a.dsum + row * a.dsum_stride;
+    auto fetch = [&](const uint16_t* x_row, const uint16_t* d_row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
-            if (at >= vectors) continue;
-            next_x[i] = load_once(x_row + 8 * at);
-            next_d[i] = load_once(d_row + 8 * at);
-            if (a.dsum != nullptr) next_add[i] = load_once(add_row + 8 * at);
+            load_if(at < vectors, x_row + 8 * at, next_x[i]);
+            load_if(at < vectors, d_row + 8 * at, next_d[i]);
         }
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
     int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;
-    if (kAhead) fetch(first + team.row);
+    const uint16_t* x_next = a.x + (first + team.row) * a.x_stride;
+    const uint16_t* d_next = a.dy + (first + team.row) * a.dy_stride;
+    if (first + team.row < a.rows) fetch(x_next, d_next);
     for (; first < a.rows; first += step) {
         const int64_t row = first + team.row;
         const int end = row < a.rows ? vectors : 0;
-        if (!kAhead) fetch(row);
-        uint4 x[NV], d[NV], add[NV];
+        uint4 x[NV], d[NV];
+        const uint16_t* add_row = a.dsum + row * a.dsum_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
             x[i] = next_x[i];
             d[i] = next_d[i];
-            add[i] = next_add[i];
+            if (a.dsum != nullptr) load_if(at < end, add_row + 8 * at, add[i]);
         }
-        if (kAhead) fetch(row + step);
+        x_next += step * a.x_stride;
+        d_next += step * a.dy_stride;
+        if (kAhead && row + step < a.rows) fetch(x_next, d_next);
         const int64_t later = row + (kAhead ? 2 : 1) * step;
-        if (!kNarrow && threadIdx.x == 0 && later < a.rows) {
-            prefetch_row(a.x + later * a.x_stride, 2 * a.cols);
-            prefetch_row(a.dy + later * a.dy_stride, 2 * a.cols);
-            if (a.dsum != nullptr) prefetch_row(a.dsum + later * a.dsum_stride, 2 * a.cols);
+        if (!kNarrow && threadIdx.x == 0) {
+            if (later < a.rows) {
+                prefetch_row(a.x + later * a.x_stride, 2 * a.cols);
+                prefetch_row(a.dy + later * a.dy_stride, 2 * a.cols);
+            }
+            if (a.dsum != nullptr && row + step < a.rows) prefetch_row(a.dsum + (row + step) * a.dsum_stride, 2 * a.cols);
         }
-        // dy, and g = dy w
-        auto g_of = [&](int i, pair (&dy)[4], pair (&g)[4]) {
-            unpack8<kFp16>(d[i], dy);
+        // g = dy w
+        auto g_of = [&](int i, const pair (&dy)[4], pair (&g)[4]) {
             const int at = team.at + i * team.size;
-            if (a.weight != nullptr && at < vectors) {
-                unpack8<kFp16>(weight_at(a.weight, at), g);
+            if (a.weight != nullptr) {
+                unpack8<kFp16>(kAhead ? w[i] : weight_if(at < vectors, a.weight, at), g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) g[e] = pair_mul(g[e], dy[e]);
             } else {
@@ -273,46 +285,50 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
                 for (int e = 0; e < 4; ++e) g[e] = dy[e];
             }
         };
-        float down = 1.0f, eps = a.eps;
-        float2 both;   // sums of (s down)^2 and of g s down
-        bool again = false;   // out of FP32's range: once more, scaled down
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-            down = again ? kDown : 1.0f;
+        // sums of (s by)^2 and of g s by
+        auto sums = [&](float by) {
             pair squares = 0, dot = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 pair v[4], dy[4], g[4];
                 unpack8<kFp16>(x[i], v);
+                unpack8<kFp16>(d[i], dy);
                 g_of(i, dy, g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    v[e] = pair_mul(v[e], pair_of(down));
+                    if (by != 1.0f) v[e] = pair_mul(v[e], pair_of(by));
                     squares = pair_fma(v[e], v[e], squares);
                     dot = pair_fma(g[e], v[e], dot);
                 }
             }
-            both = reduce.sum2(pair_sum(squares), pair_sum(dot));
+            const float2 both = reduce.sum2(pair_sum(squares), pair_sum(dot));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 forget(x[i]);
                 forget(d[i]);
             }
-            again = pass == 0 && !(both.x <= 3.0e38f);
-            // (a vote: rows of a warp differ, and the reduction takes all of it)
-            if (kNarrow ? !__any_sync(0xFFFFFFFFu, again) : !again) break;
+            return both;
+        };
+        float down = 1.0f;
+        float2 both = sums(1.0f);
+        // Out of FP32's range: once more, scaled down.  (A vote: rows of a warp
+        // differ, and the reduction takes all of it.)
+        const bool again = !(both.x <= 3.0e38f);
+        if (kNarrow ? __any_sync(0xFFFFFFFFu, again) : again) {
+            down = again ? kDown : 1.0f;
+            both = sums(down);
         }
-        eps = eps * down * down;
-        const float inv = rsqrtf(fmaf(both.x, inv_cols, eps));
+        const float inv = rsqrtf(fmaf(both.x, inv_cols, a.eps * down * down));
         const float share = both.y * inv * inv_cols;   // mean(g u)
         const float unit = inv * down;                 // u = s unit
         uint16_t* dx_row = a.dx + row * a.dx_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = team.at + i * team.size;
-            if (at >= end) continue;
+            if (kNarrow && end == 0) continue;   // dw: no row of this team's (zeros past a row)
             pair v[4], dy[4], g[4], more[4];
             unpack8<kFp16>(x[i], v);
+            unpack8<kFp16>(d[i], dy);
             g_of(i, dy, g);
             unpack8<kFp16>(add[i], more);   // zeros without dsum
 #pragma unroll
@@ -321,10 +337,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
                 dw[i][e] = pair_fma(dy[e], u, dw[i][e]);
                 g[e] = pair_fma(pair_fma(u, pair_of(-share), g[e]), pair_of(unit), more[e]);
             }
-            *reinterpret_cast<uint4*>(dx_row + 8 * at) = pack8<kFp16>(g);
+            store_if(at < end, dx_row + 8 * at, pack8<kFp16>(g));
         }
+        if (!kAhead && row + step < a.rows) fetch(x_next, d_next);
     }
     if (a.partials == nullptr) return;
+    pdl_launch_dependents();   // the join's launch
     float* part = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
     if constexpr (!kNarrow) {
 #pragma unroll
@@ -349,27 +367,38 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
         part[c] = columns[0][c] + columns[1][c] + columns[2][c] + columns[3][c];
 }
 
-// 32 warps take a run of parts each, 32 columns a block.
+// 32 warps take a run of parts each, 128 columns a block (a multiple of 8 of
+// them in all): 2.2 times as fast as 32 columns a block for 110 parts of
+// 22016 columns.
 __global__ void __launch_bounds__(1024) join_columns_kernel(const float* __restrict__ partials, int parts, int cols,
                                                             float* __restrict__ out) {
-    __shared__ float run[32][33];
+    __shared__ float4 run[32][32];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    const int c = blockIdx.x * 128 + 4 * lane;
     const int p0 = static_cast<int>(static_cast<int64_t>(parts) * warp / 32);
     const int p1 = static_cast<int>(static_cast<int64_t>(parts) * (warp + 1) / 32);
-    float sum = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < cols) {
-#pragma unroll 8
-        for (int p = p0; p < p1; ++p) sum += partials[static_cast<int64_t>(p) * cols + c];
+#pragma unroll 4
+        for (int p = p0; p < p1; ++p) {
+            const float4 v = *reinterpret_cast<const float4*>(partials + static_cast<int64_t>(p) * cols + c);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
     }
     run[warp][lane] = sum;
     __syncthreads();
-    // warp i adds column i's runs, as a tree in their order
-    sum = run[lane][warp];
+    // thread t adds column t's runs, in their order
+    const int t = threadIdx.x;
+    if (t >= 128 || static_cast<int>(blockIdx.x) * 128 + t >= cols) return;
+    const float* column = reinterpret_cast<const float*>(run) + t;
+    float total = 0.0f;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) sum += __shfl_down_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0 && static_cast<int>(blockIdx.x) * 32 + warp < cols) out[blockIdx.x * 32 + warp] = sum;
+    for (int i = 0; i < 32; ++i) total += column[128 * i];
+    out[blockIdx.x * 128 + t] = total;
 }
 
 template <int NV, bool kFp16, bool kNarrow, bool kResidual>
@@ -411,7 +440,7 @@ cudaError_t run_grad(const NormGradArgs& a, const RowPlan& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_join_columns(const float* partials, int parts, int cols, float* out, cudaStream_t s) {
-    return launch_kernel(join_columns_kernel, dim3((cols + 31) / 32), dim3(1024), 0, s, partials, parts, cols, out);
+    return launch_kernel(join_columns_kernel, dim3((cols + 127) / 128), dim3(1024), 0, s, partials, parts, cols, out);
 }
 
 cudaError_t launch_rmsnorm(const NormArgs& args, int out, bool fp16, int sm_count, cudaStream_t s) {

@@ -68,17 +68,46 @@ __device__ __forceinline__ void decode8(uint2 q, float by, pair (&f)[4]) {
     }
 }
 
-// 16 bytes that no other block reads.  Not the read-only path: an output may
-// be the input itself.
+// 16 (8) bytes that no other block reads, where `take`; else what was there.
+// Predicated: as branches, these took a third of a narrow row's instructions.
+// Not the read-only path: an output may be the input itself.
+__device__ __forceinline__ void load_if(bool take, const void* p, uint4& v) {
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.u32 q, %5, 0;\n\t"
+                 "@q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(static_cast<uint32_t>(take)));
+}
+__device__ __forceinline__ void store_if(bool take, void* p, uint4 v) {
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.u32 q, %5, 0;\n\t"
+                 "@q st.global.v4.u32 [%0], {%1, %2, %3, %4};\n\t}"
+                 :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(static_cast<uint32_t>(take)));
+}
+__device__ __forceinline__ void store_if(bool take, void* p, uint2 v) {
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.u32 q, %3, 0;\n\t"
+                 "@q st.global.v2.u32 [%0], {%1, %2};\n\t}"
+                 :: "l"(p), "r"(v.x), "r"(v.y), "r"(static_cast<uint32_t>(take)));
+}
 __device__ __forceinline__ uint4 load_once(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    uint4 v = make_uint4(0, 0, 0, 0);
+    load_if(true, p, v);
     return v;
 }
 __device__ __forceinline__ uint2 load_once8(const void* p) {
     uint2 v;
     asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+// A vector of the norm's weight (every block reads it for every row, from
+// L1), or zeros.
+__device__ __forceinline__ uint4 weight_if(bool take, const uint16_t* weight, int at) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    asm("{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(weight + 8 * at), "r"(static_cast<uint32_t>(take)));
     return v;
 }
 
@@ -219,6 +248,14 @@ __device__ __forceinline__ float scale_of_amax(float a) { return a == 0.0f ? 1.0
 __device__ __forceinline__ float row_scale(float top) {
     const float s = __fdiv_rn(top, 448.0f);
     return s < kRowMinScale ? kRowMinScale : s;
+}
+
+// What multiplies a row's values to give codes: the reciprocal of row_scale,
+// without its division (off by FP32's rounding): 448 / amax, 2^120 at most.
+__device__ __forceinline__ float row_factor(float top) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top));
+    return top < 448.0f * kRowMinScale ? 1.0f / kRowMinScale : 448.0f * r;
 }
 
 // How rows are dealt out: `each` vectors a thread, `team` threads a row,
