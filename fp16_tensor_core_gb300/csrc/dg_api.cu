@@ -1307,7 +1307,9 @@ dg_status check_epilogue(const dg_epilogue* e, const void* D, int64_t M, int64_t
     if (out == DG_E4M3 && e->scale_d == nullptr) return DG_ERR_INVALID_VALUE;
     // in place only element by element
     if (e->residual == D && (out == DG_E4M3 || e->residual_type != out)) return DG_ERR_INVALID_VALUE;
-    if (e->amax_d != nullptr && e->amax_d == e->scale_d) return DG_ERR_INVALID_VALUE;   // zeroed before it is read
+    // zeroed before anything is read
+    if (e->amax_d != nullptr && (e->amax_d == e->scale_a || e->amax_d == e->scale_b || e->amax_d == e->scale_d))
+        return DG_ERR_INVALID_VALUE;
     auto vector = [](const float* p, int rows) { return rows != 0 ? aligned16(p) : aligned4(p); };
     if (!vector(e->scale_a, e->scale_a_rows) || !vector(e->scale_b, e->scale_b_rows) || !aligned16(e->bias) ||
         !aligned16(e->residual) || !aligned4(e->scale_d) || !aligned4(e->amax_d))

@@ -52,7 +52,7 @@ static PyObject *current_device;   /* () -> index */
 static PyObject *check;            /* (status, name): raises unless DG_OK */
 
 static PyObject *n_stride, *n_shape, *n_dtype, *n_is_cuda, *n_data_ptr, *n_numel, *n_is_contiguous, *n_nbytes,
-    *n_rotary, *n_cache, *n_cuda_stream;
+    *n_rotary, *n_cache, *n_cuda_stream, *n_get_device;
 
 static int fail(const char* message) {
     PyErr_SetString(PyExc_ValueError, message);
@@ -89,6 +89,18 @@ static int is_object(PyObject* v, PyObject* want) {   /* takes the reference */
 static int on_device(PyObject* t) {
     const int yes = is_object(PyObject_GetAttr(t, n_is_cuda), Py_True);
     return yes == 0 ? fail("tensor must be in CUDA device memory") : yes < 0 ? -1 : 0;
+}
+
+/* Whether a tensor is on the current device, where the library launches: for
+ * the calls around a layer's products (one attribute serves as well as
+ * is_cuda).  *current is the device's index once it has been asked for, -1
+ * before. */
+static int on_current_device(PyObject* t, int64_t* current) {
+    int64_t device;
+    if (as_int64(PyObject_CallMethodNoArgs(t, n_get_device), &device) < 0) return -1;
+    if (device < 0) return fail("tensor must be in CUDA device memory");
+    if (*current < 0 && as_int64(PyObject_CallNoArgs(current_device), current) < 0) return -1;
+    return device == *current ? 0 : fail("tensor must be on the current device");
 }
 
 /* A tuple's first n numbers (exactly n entries wanted). */
@@ -155,10 +167,32 @@ static int get_array(PyObject* t, PyObject* type, const char* type_name, int64_t
     return get_data(t, out);
 }
 
+/* Address of a contiguous tensor on the current device. */
+static int get_data_here(PyObject* t, int64_t* device, void** out) {
+    if (on_current_device(t, device) < 0) return -1;
+    const int yes = is_object(PyObject_CallMethodNoArgs(t, n_is_contiguous), Py_True);
+    if (yes <= 0) return yes < 0 ? -1 : fail("tensor must be contiguous");
+    return as_address(PyObject_CallMethodNoArgs(t, n_data_ptr), out);
+}
+
+/* Of n elements of a type. */
+static int get_array_here(PyObject* t, PyObject* type, const char* type_name, int64_t n, const char* what,
+                          int64_t* device, void** out) {
+    int64_t have = 0;
+    const int yes = is_object(PyObject_GetAttr(t, n_dtype), type);
+    if (yes < 0 || as_int64(PyObject_CallMethodNoArgs(t, n_numel), &have) < 0) return -1;
+    if (!yes || have != n) {
+        PyErr_Format(PyExc_ValueError, "%s must be %s with %lld elements", what, type_name, (long long)n);
+        return -1;
+    }
+    return get_data_here(t, device, out);
+}
+
 /* The same, or NULL for None. */
-static int get_optional(PyObject* t, PyObject* type, const char* type_name, int64_t n, const char* what, void** out) {
+static int get_optional(PyObject* t, PyObject* type, const char* type_name, int64_t n, const char* what,
+                        int64_t* device, void** out) {
     *out = NULL;
-    return t == Py_None ? 0 : get_array(t, type, type_name, n, what, out);
+    return t == Py_None ? 0 : get_array_here(t, type, type_name, n, what, device, out);
 }
 
 typedef struct {
@@ -169,7 +203,7 @@ typedef struct {
 
 /* [rows, columns] BF16 or FP16, any row stride; with `like`, of its type and
  * rows and (cols >= 0) this many columns. */
-static int get_rows(PyObject* t, const char* what, const rows_arg* like, int64_t cols, rows_arg* r) {
+static int get_rows(PyObject* t, const char* what, const rows_arg* like, int64_t cols, int64_t* device, rows_arg* r) {
     static const char kWanted[] = "must be BF16 or FP16 [rows, columns] with contiguous rows";
     int64_t stride[2];
     if (numbers(PyObject_CallMethodNoArgs(t, n_stride), 2, stride, what, kWanted) < 0 ||
@@ -184,26 +218,26 @@ static int get_rows(PyObject* t, const char* what, const rows_arg* like, int64_t
     if (like != NULL && (r->type != like->type || r->shape[0] != like->shape[0] || (cols >= 0 && r->shape[1] != cols)))
         return fail_about(what, "must have the shape and type of its counterpart");
     void* data;
-    if (on_device(t) < 0 || as_address(PyObject_CallMethodNoArgs(t, n_data_ptr), &data) < 0) return -1;
+    if (on_current_device(t, device) < 0 || as_address(PyObject_CallMethodNoArgs(t, n_data_ptr), &data) < 0) return -1;
     r->c.data = data;
     r->c.stride = r->shape[0] > 1 ? stride[0] : r->shape[1];   /* a single one's stride may be anything */
     return 0;
 }
 /* The same, or no view (*c NULL) for None. */
-static int get_rows_or_none(PyObject* t, const char* what, const rows_arg* like, int64_t cols, rows_arg* r,
-                            const dg_rows** c) {
+static int get_rows_or_none(PyObject* t, const char* what, const rows_arg* like, int64_t cols, int64_t* device,
+                            rows_arg* r, const dg_rows** c) {
     *c = NULL;
     if (t == Py_None) return 0;
     *c = &r->c;
-    return get_rows(t, what, like, cols, r);
+    return get_rows(t, what, like, cols, device, r);
 }
 
 /* A contiguous tensor's address and bytes, or NULL and 0 for None. */
-static int get_scratch(PyObject* t, void** data, int64_t* bytes) {
+static int get_scratch(PyObject* t, int64_t* device, void** data, int64_t* bytes) {
     *data = NULL;
     *bytes = 0;
     if (t == Py_None) return 0;
-    return get_data(t, data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), bytes) < 0 ? -1 : 0;
+    return get_data_here(t, device, data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), bytes) < 0 ? -1 : 0;
 }
 
 /* The struct that a DgRotary or DgKvCache holds. */
@@ -391,14 +425,16 @@ typedef struct {
     const dg_rows *r, *s;
     void* weight;
     double eps;
+    int64_t device;
 } norm_arg;
 
 static int get_norm(PyObject* x, PyObject* weight, PyObject* residual, PyObject* sum, PyObject* eps, norm_arg* n) {
-    if (get_rows(x, "x", NULL, -1, &n->x) < 0 ||
-        get_rows_or_none(residual, "residual", &n->x, n->x.shape[1], &n->residual, &n->r) < 0 ||
-        get_rows_or_none(sum, "sum", &n->x, n->x.shape[1], &n->sum, &n->s) < 0 ||
+    n->device = -1;
+    if (get_rows(x, "x", NULL, -1, &n->device, &n->x) < 0 ||
+        get_rows_or_none(residual, "residual", &n->x, n->x.shape[1], &n->device, &n->residual, &n->r) < 0 ||
+        get_rows_or_none(sum, "sum", &n->x, n->x.shape[1], &n->device, &n->sum, &n->s) < 0 ||
         get_optional(weight, n->x.type == DG_BF16 ? type_bf16 : type_fp16, "of x's type", n->x.shape[1], "weight",
-                     &n->weight) < 0)
+                     &n->device, &n->weight) < 0)
         return -1;
     n->eps = PyFloat_AsDouble(eps);
     return n->eps == -1.0 && PyErr_Occurred() ? -1 : 0;
@@ -411,7 +447,7 @@ static PyObject* py_rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     dg_stream_t stream;
     (void)self;
     if (want_args(n, 7) < 0 || get_norm(a[0], a[2], a[3], a[4], a[5], &m) < 0 ||
-        get_rows(a[1], "y", &m.x, m.x.shape[1], &y) < 0 || get_stream(a[6], &stream) < 0)
+        get_rows(a[1], "y", &m.x, m.x.shape[1], &m.device, &y) < 0 || get_stream(a[6], &stream) < 0)
         return NULL;
     dg_status status;
     Py_BEGIN_ALLOW_THREADS
@@ -427,8 +463,8 @@ static PyObject* py_rmsnorm_e4m3(PyObject* self, PyObject* const* a, Py_ssize_t 
     dg_stream_t stream;
     (void)self;
     if (want_args(n, 8) < 0 || get_norm(a[0], a[3], a[4], a[5], a[6], &m) < 0 ||
-        get_array(a[1], type_uint8, "uint8", m.x.shape[0] * m.x.shape[1], "q", &q) < 0 ||
-        get_array(a[2], type_float32, "FP32", m.x.shape[0], "row_scale", &scale) < 0 || get_stream(a[7], &stream) < 0)
+        get_array_here(a[1], type_uint8, "uint8", m.x.shape[0] * m.x.shape[1], "q", &m.device, &q) < 0 ||
+        get_array_here(a[2], type_float32, "FP32", m.x.shape[0], "row_scale", &m.device, &scale) < 0 || get_stream(a[7], &stream) < 0)
         return NULL;
     dg_status status;
     Py_BEGIN_ALLOW_THREADS
@@ -445,10 +481,10 @@ static PyObject* py_rmsnorm_e4m3_amax(PyObject* self, PyObject* const* a, Py_ssi
     dg_stream_t stream;
     (void)self;
     if (want_args(n, 10) < 0 || get_norm(a[0], a[5], a[6], a[7], a[8], &m) < 0 ||
-        get_array(a[1], type_float32, "FP32", 1, "scale", &scale) < 0 ||
-        get_array(a[2], type_uint8, "uint8", m.x.shape[0] * m.x.shape[1], "q", &q) < 0 ||
-        get_array(a[3], type_float32, "FP32", 1, "amax_out", &amax) < 0 ||
-        get_optional(a[4], type_float32, "FP32", 1, "next_scale_out", &next) < 0 || get_stream(a[9], &stream) < 0)
+        get_array_here(a[1], type_float32, "FP32", 1, "scale", &m.device, &scale) < 0 ||
+        get_array_here(a[2], type_uint8, "uint8", m.x.shape[0] * m.x.shape[1], "q", &m.device, &q) < 0 ||
+        get_array_here(a[3], type_float32, "FP32", 1, "amax_out", &m.device, &amax) < 0 ||
+        get_optional(a[4], type_float32, "FP32", 1, "next_scale_out", &m.device, &next) < 0 || get_stream(a[9], &stream) < 0)
         return NULL;
     dg_status status;
     Py_BEGIN_ALLOW_THREADS
@@ -469,10 +505,10 @@ static PyObject* py_rmsnorm_grad(PyObject* self, PyObject* const* a, Py_ssize_t 
     (void)self;
     if (want_args(n, 9) < 0 || get_norm(a[0], a[3], Py_None, Py_None, a[7], &m) < 0) return NULL;
     const int64_t cols = m.x.shape[1];
-    if (get_rows(a[1], "dy", &m.x, cols, &dy) < 0 || get_rows(a[2], "dx", &m.x, cols, &dx) < 0 ||
-        get_rows_or_none(a[4], "dsum", &m.x, cols, &dsum, &extra) < 0 ||
-        get_optional(a[5], type_float32, "FP32", cols, "dweight", &dweight) < 0 ||
-        get_scratch(a[6], &scratch, &bytes) < 0 || get_stream(a[8], &stream) < 0)
+    if (get_rows(a[1], "dy", &m.x, cols, &m.device, &dy) < 0 || get_rows(a[2], "dx", &m.x, cols, &m.device, &dx) < 0 ||
+        get_rows_or_none(a[4], "dsum", &m.x, cols, &m.device, &dsum, &extra) < 0 ||
+        get_optional(a[5], type_float32, "FP32", cols, "dweight", &m.device, &dweight) < 0 ||
+        get_scratch(a[6], &m.device, &scratch, &bytes) < 0 || get_stream(a[8], &stream) < 0)
         return NULL;
     dg_status status;
     Py_BEGIN_ALLOW_THREADS
@@ -497,21 +533,22 @@ static PyObject* py_activate(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     const dg_rows* out;
     void *q, *q_scale, *x_q, *x_scale;
     int gated;
+    int64_t device = -1;
     dg_activation act;
     dg_stream_t stream;
     (void)self;
-    if (want_args(n, 9) < 0 || get_activation(a[7], a[1], &gated, &act) < 0 || get_rows(a[0], "x", NULL, -1, &x) < 0)
+    if (want_args(n, 9) < 0 || get_activation(a[7], a[1], &gated, &act) < 0 || get_rows(a[0], "x", NULL, -1, &device, &x) < 0)
         return NULL;
     if (gated && x.shape[1] % 2 != 0) {
         fail("x must have two halves when gated");
         return NULL;
     }
     const int64_t rows = x.shape[0], width = x.shape[1], cols = gated ? width / 2 : width;
-    if (get_rows_or_none(a[2], "y", &x, cols, &y, &out) < 0 ||
-        get_optional(a[3], type_uint8, "uint8", rows * cols, "q", &q) < 0 ||
-        get_optional(a[4], type_float32, "FP32", rows, "q_scale", &q_scale) < 0 ||
-        get_optional(a[5], type_uint8, "uint8", rows * width, "x_q", &x_q) < 0 ||
-        get_optional(a[6], type_float32, "FP32", gated ? 2 * rows : rows, "x_scale", &x_scale) < 0 ||
+    if (get_rows_or_none(a[2], "y", &x, cols, &device, &y, &out) < 0 ||
+        get_optional(a[3], type_uint8, "uint8", rows * cols, "q", &device, &q) < 0 ||
+        get_optional(a[4], type_float32, "FP32", rows, "q_scale", &device, &q_scale) < 0 ||
+        get_optional(a[5], type_uint8, "uint8", rows * width, "x_q", &device, &x_q) < 0 ||
+        get_optional(a[6], type_float32, "FP32", gated ? 2 * rows : rows, "x_scale", &device, &x_scale) < 0 ||
         get_stream(a[8], &stream) < 0)
         return NULL;
     if ((a[3] == Py_None) != (a[4] == Py_None) || (a[5] == Py_None) != (a[6] == Py_None)) {
@@ -532,22 +569,23 @@ static PyObject* py_activate_grad(PyObject* self, PyObject* const* a, Py_ssize_t
     void *x_q, *x_scale, *dbias, *scratch;
     int64_t bytes;
     int gated;
+    int64_t device = -1;
     dg_activation act;
     dg_stream_t stream;
     (void)self;
     if (want_args(n, 10) < 0 || get_activation(a[6], a[1], &gated, &act) < 0 ||
-        get_rows(a[0], "dy", NULL, -1, &dy) < 0)
+        get_rows(a[0], "dy", NULL, -1, &device, &dy) < 0)
         return NULL;
     const int64_t rows = dy.shape[0], cols = dy.shape[1], width = gated ? 2 * cols : cols;
     if ((a[3] == Py_None) == (a[4] == Py_None) || (a[4] == Py_None) != (a[5] == Py_None)) {
         fail("x, or x_q and x_scale, must be given");
         return NULL;
     }
-    if (get_rows(a[2], "dx", &dy, width, &dx) < 0 || get_rows_or_none(a[3], "x", &dy, width, &x, &in) < 0 ||
-        get_optional(a[4], type_uint8, "uint8", rows * width, "x_q", &x_q) < 0 ||
-        get_optional(a[5], type_float32, "FP32", gated ? 2 * rows : rows, "x_scale", &x_scale) < 0 ||
-        get_optional(a[7], type_float32, "FP32", width, "dbias", &dbias) < 0 ||
-        get_scratch(a[8], &scratch, &bytes) < 0 || get_stream(a[9], &stream) < 0)
+    if (get_rows(a[2], "dx", &dy, width, &device, &dx) < 0 || get_rows_or_none(a[3], "x", &dy, width, &device, &x, &in) < 0 ||
+        get_optional(a[4], type_uint8, "uint8", rows * width, "x_q", &device, &x_q) < 0 ||
+        get_optional(a[5], type_float32, "FP32", gated ? 2 * rows : rows, "x_scale", &device, &x_scale) < 0 ||
+        get_optional(a[7], type_float32, "FP32", width, "dbias", &device, &dbias) < 0 ||
+        get_scratch(a[8], &device, &scratch, &bytes) < 0 || get_stream(a[9], &stream) < 0)
         return NULL;
     dg_status status;
     Py_BEGIN_ALLOW_THREADS
@@ -563,10 +601,10 @@ typedef struct {
     int64_t rows, cols, bytes;
 } matrix_arg;
 
-static int get_matrix(PyObject* t, const char* what, matrix_arg* m) {
+static int get_matrix(PyObject* t, const char* what, int64_t* device, matrix_arg* m) {
     int64_t shape[2], bytes;
     if (numbers(PyObject_GetAttr(t, n_shape), 2, shape, what, "must have two dimensions") < 0 ||
-        get_data(t, &m->data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), &bytes) < 0)
+        get_data_here(t, device, &m->data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), &bytes) < 0)
         return -1;
     m->rows = shape[0];
     m->cols = shape[1];
@@ -575,14 +613,14 @@ static int get_matrix(PyObject* t, const char* what, matrix_arg* m) {
 }
 
 /* A scale for the whole operand, or one a row. */
-static int get_scales(PyObject* t, const char* what, int64_t rows, void** out, int* per_row) {
+static int get_scales(PyObject* t, const char* what, int64_t rows, int64_t* device, void** out, int* per_row) {
     int64_t n;
     *out = NULL;
     *per_row = 0;
     if (t == Py_None) return 0;
     if (as_int64(PyObject_CallMethodNoArgs(t, n_numel), &n) < 0) return -1;
     *per_row = n != 1;
-    return get_array(t, type_float32, "FP32", n == 1 ? 1 : rows, what, out);
+    return get_array_here(t, type_float32, "FP32", n == 1 ? 1 : rows, what, device, out);
 }
 
 /* (A, B, D, scale_a, scale_b, bias, act, residual, scale_d, amax_d, out, stream) */
@@ -592,10 +630,10 @@ static PyObject* fused(PyObject* const* a, Py_ssize_t n, int fp16) {
     matrix_arg A, B, D, R;
     dg_epilogue e;
     void *sa, *sb, *bias, *sd, *amax;
-    int64_t act, out;
+    int64_t act, out, device = -1;
     dg_stream_t stream;
-    if (want_args(n, 12) < 0 || get_matrix(a[0], "A", &A) < 0 || get_matrix(a[1], "B", &B) < 0 ||
-        get_matrix(a[2], "D", &D) < 0 || as_int64(PyNumber_Index(a[6]), &act) < 0 ||
+    if (want_args(n, 12) < 0 || get_matrix(a[0], "A", &device, &A) < 0 || get_matrix(a[1], "B", &device, &B) < 0 ||
+        get_matrix(a[2], "D", &device, &D) < 0 || as_int64(PyNumber_Index(a[6]), &act) < 0 ||
         as_int64(PyNumber_Index(a[10]), &out) < 0)
         return NULL;
     const int64_t out_bytes = out == DG_E4M3 ? 1 : 2;
@@ -607,7 +645,7 @@ static PyObject* fused(PyObject* const* a, Py_ssize_t n, int fp16) {
     e.residual = NULL;
     e.residual_type = DG_BF16;
     if (a[7] != Py_None) {
-        if (get_matrix(a[7], "residual", &R) < 0) return NULL;
+        if (get_matrix(a[7], "residual", &device, &R) < 0) return NULL;
         PyObject* type = PyObject_GetAttr(a[7], n_dtype);
         if (type == NULL) return NULL;
         const int bf16 = type == type_bf16, half = type == type_fp16;
@@ -619,11 +657,11 @@ static PyObject* fused(PyObject* const* a, Py_ssize_t n, int fp16) {
         e.residual = R.data;
         e.residual_type = bf16 ? DG_BF16 : DG_FP16;
     }
-    if (get_scales(a[3], "scale_a", A.rows, &sa, &e.scale_a_rows) < 0 ||
-        get_scales(a[4], "scale_b", B.rows, &sb, &e.scale_b_rows) < 0 ||
-        get_optional(a[5], type_float32, "FP32", B.rows, "bias", &bias) < 0 ||
-        get_optional(a[8], type_float32, "FP32", 1, "scale_d", &sd) < 0 ||
-        get_optional(a[9], type_float32, "FP32", 1, "amax_d", &amax) < 0 || get_stream(a[11], &stream) < 0)
+    if (get_scales(a[3], "scale_a", A.rows, &device, &sa, &e.scale_a_rows) < 0 ||
+        get_scales(a[4], "scale_b", B.rows, &device, &sb, &e.scale_b_rows) < 0 ||
+        get_optional(a[5], type_float32, "FP32", B.rows, "bias", &device, &bias) < 0 ||
+        get_optional(a[8], type_float32, "FP32", 1, "scale_d", &device, &sd) < 0 ||
+        get_optional(a[9], type_float32, "FP32", 1, "amax_d", &device, &amax) < 0 || get_stream(a[11], &stream) < 0)
         return NULL;
     e.scale_a = sa;
     e.scale_b = sb;
@@ -714,6 +752,7 @@ PyMODINIT_FUNC PyInit_dg_python(void) {
         {&n_stride, "stride"}, {&n_shape, "shape"}, {&n_dtype, "dtype"}, {&n_is_cuda, "is_cuda"},
         {&n_data_ptr, "data_ptr"}, {&n_numel, "numel"}, {&n_is_contiguous, "is_contiguous"}, {&n_nbytes, "nbytes"},
         {&n_rotary, "rotary_address"}, {&n_cache, "cache_address"}, {&n_cuda_stream, "cuda_stream"},
+        {&n_get_device, "get_device"},
     };
     for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
         if (*names[i].at == NULL && (*names[i].at = PyUnicode_InternFromString(names[i].name)) == NULL) return NULL;

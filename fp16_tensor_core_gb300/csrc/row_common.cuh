@@ -251,11 +251,13 @@ __device__ __forceinline__ float row_scale(float top) {
 }
 
 // What multiplies a row's values to give codes: the reciprocal of row_scale,
-// without its division (off by FP32's rounding): 448 / amax, 2^120 at most.
+// without its division (off by FP32's rounding), 2^120 at most.  (amax / 448
+// first: the reciprocal of an amax near FP32's largest would be 0.)
 __device__ __forceinline__ float row_factor(float top) {
+    const float s = top * (1.0f / 448.0f);
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top));
-    return top < 448.0f * kRowMinScale ? 1.0f / kRowMinScale : 448.0f * r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s < kRowMinScale ? 1.0f / kRowMinScale : r;
 }
 
 // How rows are dealt out: `each` vectors a thread, `team` threads a row,

@@ -639,7 +639,7 @@ typedef struct {
     const void* residual;   /* M x N dense of residual_type, or NULL                            */
     dg_dtype residual_type; /* DG_BF16 or DG_FP16                                               */
     const float* scale_d;   /* FP32[1]; required iff out is DG_E4M3                             */
-    float* amax_d;          /* FP32[1], or NULL                                                 */
+    float* amax_d;          /* FP32[1], none of the scales, or NULL                             */
 } dg_epilogue;
 
 /* dg_fp8_gemm with more in its epilogue, on the accumulators in FP32:

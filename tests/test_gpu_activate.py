@@ -140,6 +140,11 @@ def test_extremes(act, dtype):
     for codes, scale in ((q, qs[:, None]), (xq, xs)):
         value = codes.view(F8).double() * scale.double()
         assert value[1].isnan().all() and value[2].isnan().any()
+    # rows whose scale's reciprocal is near FP32's ends
+    check_codes(xq[:1], xs[:1, 0], x[:1].double(), 2.0 ** -22)
+    small = x[:1, :2].repeat(1, 4) + 2.0 ** (-130 if dtype == BF else -24) * torch.arange(8, device="cuda").to(dtype)
+    dg.dg_activate(small, act, x_q=xq[:1], x_scale=xs[:1])
+    check_codes(xq[:1], xs[:1, 0], small.double(), 2.0 ** -22)
     dx = torch.zeros_like(x)
     dg.dg_activate_grad(torch.ones_like(x), act, dx, x=x)
     slope = act64(x[0].double(), act)[1]

@@ -115,8 +115,9 @@ def test_scratch_sizes(L):
     assert L.dg_rmsnorm_grad_scratch(-1, 64, 152, ctypes.byref(n)) == BAD
     assert L.dg_activate_grad_scratch(4, 60, 0, 152, ctypes.byref(n)) == OFF
     assert L.dg_rmsnorm_grad_scratch(0, 64, 152, ctypes.byref(n)) == dg.DG_OK and n.value == 0
-    assert L.dg_rmsnorm_grad_scratch(3, 64, 152, ctypes.byref(n)) == dg.DG_OK and n.value == 3 * 64 * 4
-    assert L.dg_activate_grad_scratch(3, 64, 1, 152, ctypes.byref(n)) == dg.DG_OK and n.value == 3 * 128 * 4
+    # a partial sum of the columns a block, and no block without a row
+    assert L.dg_rmsnorm_grad_scratch(3, 64, 152, ctypes.byref(n)) == dg.DG_OK and 64 * 4 <= n.value <= 3 * 64 * 4
+    assert L.dg_activate_grad_scratch(3, 64, 1, 152, ctypes.byref(n)) == dg.DG_OK and 128 * 4 <= n.value <= 3 * 128 * 4
     # no more than the SMs need, however many rows
     assert L.dg_rmsnorm_grad_scratch(1 << 30, 4096, 152, ctypes.byref(n)) == dg.DG_OK and n.value < 1 << 25
 
@@ -134,6 +135,7 @@ EPILOGUE = [
     (dict(e=epilogue(scale_b=FAKE + 8, scale_b_rows=1)), OFF), (dict(e=epilogue(bias=FAKE + 4)), OFF),
     (dict(e=epilogue(residual=FAKE + 8)), OFF), (dict(e=epilogue(residual=FAKE + 64, residual_type=1)), BAD),
     (dict(e=epilogue(residual=FAKE, residual_type=dg.DG_FP16)), BAD), (dict(e=epilogue(amax_d=FAKE + 1)), OFF),
+    (dict(e=epilogue(amax_d=FAKE)), BAD),
     (dict(M=-1), BAD), (dict(N=1 << 31), BAD), (dict(A=None), BAD), (dict(D=None), BAD), (dict(A=FAKE + 8), OFF),
     (dict(K=36), OFF), (dict(out=7), BAD),
 ]
