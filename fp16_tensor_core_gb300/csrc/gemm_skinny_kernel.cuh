@@ -43,7 +43,8 @@ struct SkCfg {
     static constexpr int kStageX = KPS * kXBytes;
     static constexpr int kSmemBytes = 1024 + kRing * kKBBytes + kBarBytes;
     static constexpr int kScalesOff = kRing * kKBBytes + kBarBytes;   // fused: the rows' scales of A
-    static constexpr int kFusedSmemBytes = kSmemBytes + NC * 4;
+    static constexpr int kResidualOff = kScalesOff + NC * 4;          // and the tile's residual [NC][128]
+    static constexpr int kFusedSmemBytes = kSmemBytes + NC * 4 + NC * kRows * 2;
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * NC);   // two accumulators
     static constexpr uint32_t kIdesc = idesc_f32acc(kRows, NC, 0, 0);
     static_assert(NC % 16 == 0 && NC >= 16 && NC <= kSplitkMaxCols, "MMA N");
@@ -128,25 +129,36 @@ __device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live
     return c;
 }
 
-// The residual of tile t moves into L2: thread r of 128 takes lines r, r + 128
-// of the M rows' two.
-__device__ __forceinline__ void prefetch_residual_tile(const SkParams& p, int t, int r) {
-    if (p.epi.residual == nullptr) return;
-    for (int i = r; i < 2 * p.M; i += 128) {
-        const int n = t * p.tile_rows + 64 * (i & 1);
-        if (64 * (i & 1) < p.tile_rows && n < p.N)
-            asm volatile("prefetch.global.L2 [%0];" :: "l"(p.epi.residual + static_cast<int64_t>(i >> 1) * p.N + n));
+// The residual of tile t into shared memory, by asynchronous copies of 16
+// bytes of a row while the tile's main loop runs (rows of D that are not
+// multiples of 16 bytes: read at the end).  Read at the end, 16 rows at a
+// time, behind the weight stream of the next launch, it took 6 us of a 64 x
+// 4096 x 11008 product's 21.
+__device__ __forceinline__ bool residual_is_staged(const SkParams& p) {
+    return p.epi.residual != nullptr && (p.N & 7) == 0 && (p.tile_rows & 7) == 0;
+}
+__device__ __forceinline__ void stage_residual(const SkParams& p, uint16_t* tile, int t, int r) {
+    for (int i = r; i < p.M * (kRows / 8); i += 128) {
+        const int m = i >> 4, at = 8 * (i & 15), n = t * p.tile_rows + at;
+        if (at < p.tile_rows && n < p.N)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         :: "r"(smem_addr(tile + m * kRows + at)), "l"(p.epi.residual + static_cast<int64_t>(m) * p.N + n)
+                         : "memory");
     }
 }
 
-// Rows c0 .. c0 + 15 of the residual's column n (not the read-only path: D
-// may be the residual).
-__device__ __forceinline__ void load_residual16(const SkParams& p, bool live, int c0, int n,
-                                                uint32_t (&res)[16]) {
+// Rows c0 .. c0 + 15 of the residual's column n, the tile's column r (not the
+// read-only path: D may be the residual).
+__device__ __forceinline__ void load_residual16(const SkParams& p, bool live, int c0, int n, int r,
+                                                const uint16_t* tile, uint32_t (&res)[16]) {
+    const bool staged = residual_is_staged(p);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         res[j] = 0;
-        if (p.epi.residual != nullptr && live && c0 + j < p.M)
+        if (p.epi.residual == nullptr || !live || c0 + j >= p.M) continue;
+        if (staged)
+            res[j] = tile[(c0 + j) * kRows + r];
+        else
             asm volatile("ld.global.u16 %0, [%1];"   // (into 32 bits: nothing waits for it here)
                          : "=r"(res[j]) : "l"(p.epi.residual + static_cast<int64_t>(c0 + j) * p.N + n));
     }
@@ -202,14 +214,15 @@ __device__ __forceinline__ void finish_chunks(const SkParams& p, uint8_t* smem, 
                                               int c_first, int c_last, int first_slot,
                                               bool staged, int quads, const float (&first)[16],
                                               float alpha, uint32_t& amax_bits,
-                                              const FusedColumn& column, ByScale out, const float* sa) {
+                                              const FusedColumn& column, ByScale out, const float* sa,
+                                              const uint16_t* residual_tile) {
     const int others = c_last - c_first;
     const bool live = r < p.tile_rows && n < p.N;
 #pragma unroll 1
     for (int c0 = c0_begin; c0 < NC && c0 < p.M; c0 += c0_step) {
         float v[16];
         uint32_t res[16];   // on its way while the partial tiles are added up
-        if constexpr (kFused) load_residual16(p, live, c0, n, res);
+        if constexpr (kFused) load_residual16(p, live, c0, n, r, residual_tile, res);
         if (c_last > c_first && c0 == 0) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = first[j];
@@ -344,6 +357,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
     volatile int* help = last_flag + 1;     // [kHelpInts]
 
     float* row_scales = reinterpret_cast<float*>(smem + C::kScalesOff);   // [NC], fused
+    uint16_t* residual_tile = reinterpret_cast<uint16_t*>(smem + C::kResidualOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -523,10 +537,14 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             if constexpr (kFused) {
                 const int n0 = t * p.tile_rows + r;
                 column = fused_column(p, r < p.tile_rows && n0 < p.N, n0);
-                prefetch_residual_tile(p, t, r);
+                if (residual_is_staged(p)) {
+                    if (t != t_begin) named_bar_sync(kEpiBar, kEpiThreads);   // the last tile's has been read
+                    stage_residual(p, residual_tile, t, r);
+                }
             }
             // The four warps continue or leave together (named barriers below).
             const bool got = wait_bounded(&acc_full[acc], acc_phase, ctl);
+            if constexpr (kFused) asm volatile("cp.async.wait_all;" ::: "memory");
             if (!named_bar_and(kEpiBar, kEpiThreads, got)) break;
             tc_fence_after_sync();
             // Columns [c0, c0 + 16) of this row's accumulator, 16 at a time;
@@ -625,7 +643,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             }
             if (finish)
                 finish_chunks<NC, kFused>(p, smem, tacc, r, n, 0, helped ? 32 : 16, me, c_first, c_last,
-                                  first_slot, staged, quads, first, alpha, amax_bits, column, out, row_scales);
+                                  first_slot, staged, quads, first, alpha, amax_bits, column, out, row_scales, residual_tile);
             // The accumulator is free once every chunk has been read.
             tc_fence_before_sync();
             __syncwarp();
@@ -680,7 +698,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     uint32_t amax_bits = 0u;
                     finish_chunks<NC, kFused>(p, smem, tacc, r, t * p.tile_rows + r, 16, 32,
                                       static_cast<int>(blockIdx.x), c_first, c_last, first_slot,
-                                      staged, quads, none, alpha, amax_bits, column, out, row_scales);
+                                      staged, quads, none, alpha, amax_bits, column, out, row_scales, residual_tile);
                     if (p.amax_out != nullptr) {
                         __syncwarp();
                         const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, amax_bits);
