@@ -368,7 +368,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if constexpr (kFused) {
                 sa = scale_of_row(p, row, row_ok);
                 if (it.part <= 0) {
-                    load_residual(p, row, row_ok, nt * BN + 32 * half, res);
+                    if ((p.N & 7) == 0) load_residual(p, row, row_ok, nt * BN + 32 * half, res);
                     prefetch_residual<BN>(p, row, row_ok, nt * BN, half);
                     stage_columns<BN>(p, columns, nt * BN, half, lane);
                 }
@@ -530,10 +530,13 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     add_parts(c, r);
                     const int col0 = nt * BN + c * 32;
                     if constexpr (kFused) {
+                        uint8_t* box = smem + C::kStagingOff + (warp - 4) * kBoxBytes;
+                        if ((p.N & 7) != 0) load_residual_odd(p, box, row0, p.M, col0, lane, res);
                         float v[32];
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
-                        if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
-                        if (row_ok && col0 < p.N) store_values(p, row, min(32, p.N - col0), col0, v);
+                        if ((p.N & 7) == 0 && c + kChunkStep < BN / 32)
+                            load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
+                        store_box_odd(p, box, row0, p.M, col0, v, lane);
                     } else {
                         amax_bits = max(amax_bits, store_chunk(p, row, p.M, col0, r, alpha));
                     }

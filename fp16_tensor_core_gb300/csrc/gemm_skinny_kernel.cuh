@@ -129,46 +129,56 @@ __device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live
     return c;
 }
 
-// The residual of tile t into shared memory, by asynchronous copies of 16
-// bytes of a row while the tile's main loop runs (rows of D that are not
-// multiples of 16 bytes: read at the end).  Read at the end, 16 rows at a
-// time, behind the weight stream of the next launch, it took 6 us of a 64 x
-// 4096 x 11008 product's 21.
-__device__ __forceinline__ bool residual_is_staged(const SkParams& p) {
-    return p.epi.residual != nullptr && (p.N & 7) == 0 && (p.tile_rows & 7) == 0;
-}
+// The residual of tile t into shared memory while the tile's main loop runs:
+// asynchronous copies of 16 bytes of a row, of 4 where N is only even, or
+// elements one by one.  (Never the read-only path: D
+// may be the residual.)  Read at the end instead, 16 rows at a time, behind
+// the weight stream of the next launch, it took 6 us of a 64 x 4096 x 11008
+// product's 21.
 __device__ __forceinline__ void stage_residual(const SkParams& p, uint16_t* tile, int t, int r) {
-    for (int i = r; i < p.M * (kRows / 8); i += 128) {
-        const int m = i >> 4, at = 8 * (i & 15), n = t * p.tile_rows + at;
-        if (at < p.tile_rows && n < p.N)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                         :: "r"(smem_addr(tile + m * kRows + at)), "l"(p.epi.residual + static_cast<int64_t>(m) * p.N + n)
-                         : "memory");
+    if ((p.N & 7) == 0 && (p.tile_rows & 7) == 0) {
+        for (int i = r; i < p.M * (kRows / 8); i += 128) {
+            const int m = i >> 4, at = 8 * (i & 15), n = t * p.tile_rows + at;
+            if (at < p.tile_rows && n < p.N)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             :: "r"(smem_addr(tile + m * kRows + at)),
+                                "l"(p.epi.residual + static_cast<int64_t>(m) * p.N + n)
+                             : "memory");
+        }
+        return;
     }
-}
-
-// Rows c0 .. c0 + 15 of the residual's column n, the tile's column r (not the
-// read-only path: D may be the residual).
-__device__ __forceinline__ void load_residual16(const SkParams& p, bool live, int c0, int n, int r,
-                                                const uint16_t* tile, uint32_t (&res)[16]) {
-    const bool staged = residual_is_staged(p);
+    if ((p.N & 1) == 0 && (p.tile_rows & 1) == 0) {
+        for (int i = r; i < p.M * (kRows / 2); i += 128) {
+            const int m = i >> 6, at = 2 * (i & 63), n = t * p.tile_rows + at;
+            if (at < p.tile_rows && n < p.N)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                             :: "r"(smem_addr(tile + m * kRows + at)),
+                                "l"(p.epi.residual + static_cast<int64_t>(m) * p.N + n)
+                             : "memory");
+        }
+        return;
+    }
+    const int n = t * p.tile_rows + r;
+    if (r >= p.tile_rows || n >= p.N) return;
+#pragma unroll 1
+    for (int m0 = 0; m0 < p.M; m0 += 16) {
+        uint32_t e[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        res[j] = 0;
-        if (p.epi.residual == nullptr || !live || c0 + j >= p.M) continue;
-        if (staged)
-            res[j] = tile[(c0 + j) * kRows + r];
-        else
-            asm volatile("ld.global.u16 %0, [%1];"   // (into 32 bits: nothing waits for it here)
-                         : "=r"(res[j]) : "l"(p.epi.residual + static_cast<int64_t>(c0 + j) * p.N + n));
+        for (int i = 0; i < 16; ++i)
+            if (m0 + i < p.M)
+                asm volatile("ld.global.u16 %0, [%1];"
+                             : "=r"(e[i]) : "l"(p.epi.residual + static_cast<int64_t>(m0 + i) * p.N + n));
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (m0 + i < p.M) tile[(m0 + i) * kRows + r] = static_cast<uint16_t>(e[i]);
     }
 }
 
 // act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n] for rows c0 ..
-// c0 + jn - 1 (sa: the rows' scales, in shared memory); returns the largest
-// magnitude (ordered bits).
+// c0 + jn - 1 (sa: the rows' scales, residual: row c0 of this thread's column,
+// both in shared memory); returns the largest magnitude (ordered bits).
 __device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, const FusedColumn& col,
-                                           ByScale out, const float* sa, const uint32_t (&res)[16],
+                                           ByScale out, const float* sa, const uint16_t* residual,
                                            float (&f)[16]) {
     pair v[8];
 #pragma unroll
@@ -185,7 +195,7 @@ __device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, co
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (p.epi.residual != nullptr) {
-            const uint32_t w = res[2 * i] | res[2 * i + 1] << 16;
+            const uint32_t w = residual[2 * i * kRows] | static_cast<uint32_t>(residual[(2 * i + 1) * kRows]) << 16;
             const float2 x = p.epi.residual_fp16 != 0
                                  ? f16x2_to_f32x2(w)
                                  : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -221,8 +231,6 @@ __device__ __forceinline__ void finish_chunks(const SkParams& p, uint8_t* smem, 
 #pragma unroll 1
     for (int c0 = c0_begin; c0 < NC && c0 < p.M; c0 += c0_step) {
         float v[16];
-        uint32_t res[16];   // on its way while the partial tiles are added up
-        if constexpr (kFused) load_residual16(p, live, c0, n, r, residual_tile, res);
         if (c_last > c_first && c0 == 0) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = first[j];
@@ -317,7 +325,7 @@ __device__ __forceinline__ void finish_chunks(const SkParams& p, uint8_t* smem, 
         if (live) {
             const int jn = min(16, p.M - c0);   // rows of A in this chunk
             if constexpr (kFused) {
-                amax_bits = max(amax_bits, fuse16(p, c0, jn, column, out, sa, res, v));
+                amax_bits = max(amax_bits, fuse16(p, c0, jn, column, out, sa, residual_tile + c0 * kRows + r, v));
                 store_chunk16(p, c0, n, jn, v, 1.0f);
                 continue;
             }
@@ -537,7 +545,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             if constexpr (kFused) {
                 const int n0 = t * p.tile_rows + r;
                 column = fused_column(p, r < p.tile_rows && n0 < p.N, n0);
-                if (residual_is_staged(p)) {
+                if (p.epi.residual != nullptr) {
                     if (t != t_begin) named_bar_sync(kEpiBar, kEpiThreads);   // the last tile's has been read
                     stage_residual(p, residual_tile, t, r);
                 }

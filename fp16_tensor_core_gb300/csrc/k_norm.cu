@@ -367,19 +367,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
         part[c] = columns[0][c] + columns[1][c] + columns[2][c] + columns[3][c];
 }
 
-// 32 warps take a run of parts each, 128 columns a block (a multiple of 8 of
-// them in all): 2.2 times as fast as 32 columns a block for 110 parts of
-// 22016 columns.
-__global__ void __launch_bounds__(1024) join_columns_kernel(const float* __restrict__ partials, int parts, int cols,
+// Columns' sums over parts: kLanes threads side by side take four columns each,
+// the block's kThreads / kLanes runs of parts one under another.
+template <int kLanes, int kThreads>
+__global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* __restrict__ partials, int parts, int cols,
                                                             float* __restrict__ out) {
-    __shared__ float4 run[32][32];
+    constexpr int kRuns = kThreads / kLanes, kColumns = 4 * kLanes;
+    static_assert(kRuns % 8 == 0 && 8 * kColumns <= kThreads, "eight threads a column at the end");
+    __shared__ float4 sums[kThreads];
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 128 + 4 * lane;
-    const int p0 = static_cast<int>(static_cast<int64_t>(parts) * warp / 32);
-    const int p1 = static_cast<int>(static_cast<int64_t>(parts) * (warp + 1) / 32);
+    const int lane = threadIdx.x % kLanes, run = threadIdx.x / kLanes;
+    const int c = blockIdx.x * kColumns + 4 * lane;
+    const int p0 = static_cast<int>(static_cast<int64_t>(parts) * run / kRuns);
+    const int p1 = static_cast<int>(static_cast<int64_t>(parts) * (run + 1) / kRuns);
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < cols) {
+    if (c < cols) {   // (a multiple of 8 columns in all)
 #pragma unroll 4
         for (int p = p0; p < p1; ++p) {
             const float4 v = *reinterpret_cast<const float4*>(partials + static_cast<int64_t>(p) * cols + c);
@@ -389,16 +391,20 @@ __global__ void __launch_bounds__(1024) join_columns_kernel(const float* __restr
             sum.w += v.w;
         }
     }
-    run[warp][lane] = sum;
+    sums[threadIdx.x] = sum;
     __syncthreads();
-    // thread t adds column t's runs, in their order
-    const int t = threadIdx.x;
-    if (t >= 128 || static_cast<int>(blockIdx.x) * 128 + t >= cols) return;
-    const float* column = reinterpret_cast<const float*>(run) + t;
+    // eight threads a column add an eighth of its runs each, in their order,
+    // and are added in theirs
+    const int t = threadIdx.x >> 3, part = threadIdx.x & 7;
+    if (t >= kColumns) return;   // whole warps
+    const float* column = reinterpret_cast<const float*>(sums) + t + kColumns * (part * (kRuns / 8));
     float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) total += column[128 * i];
-    out[blockIdx.x * 128 + t] = total;
+    for (int i = 0; i < kRuns / 8; ++i) total += column[kColumns * i];
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) total += __shfl_down_sync(0xFFFFFFFFu, total, o, 8);
+    const int at = static_cast<int>(blockIdx.x) * kColumns + t;
+    if (part == 0 && at < cols) out[at] = total;
 }
 
 template <int NV, bool kFp16, bool kNarrow, bool kResidual>
@@ -440,7 +446,17 @@ cudaError_t run_grad(const NormGradArgs& a, const RowPlan& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_join_columns(const float* partials, int parts, int cols, float* out, cudaStream_t s) {
-    return launch_kernel(join_columns_kernel, dim3((cols + 127) / 128), dim3(1024), 0, s, partials, parts, cols, out);
+    // 128 columns a block for wide sums (110 parts of 22016: 2.2 times as fast
+    // as 32); 32 for those that would leave SMs idle, with fewer threads where
+    // there is little to add (63 parts of 2000: 0.8 us).
+    if (cols >= 8192)
+        return launch_kernel(join_columns_kernel<32, 1024>, dim3((cols + 127) / 128), dim3(1024), 0, s, partials, parts,
+                             cols, out);
+    if (parts > 256)
+        return launch_kernel(join_columns_kernel<8, 1024>, dim3((cols + 31) / 32), dim3(1024), 0, s, partials, parts,
+                             cols, out);
+    return launch_kernel(join_columns_kernel<8, 256>, dim3((cols + 31) / 32), dim3(256), 0, s, partials, parts, cols,
+                         out);
 }
 
 cudaError_t launch_rmsnorm(const NormArgs& args, int out, bool fp16, int sm_count, cudaStream_t s) {

@@ -290,8 +290,8 @@ inline RowPlan row_plan(int64_t rows, int cols, int sm_count, const int (&limits
     return p;
 }
 
-// Sums of columns: out[c] = the sum over parts p of partials[p][c], in the
-// order of p within 32 runs, joined in order.  partials: [parts][cols].
+// Sums of columns: out[c] = the sum over parts p of partials[p][c], in an order
+// that only their number and the columns' decides.  partials: [parts][cols].
 cudaError_t launch_join_columns(const float* partials, int parts, int cols, float* out, cudaStream_t s);
 
 }  // namespace dg
