@@ -13,9 +13,9 @@
 // exponential's argument (2^-23 of its size).
 //
 // Pairs because FP32 additions, products and fused products of two elements
-// are one instruction here: GELU takes 10 issue slots an element this way;
-// through the library's erfc, a branch each, it took the 4096 x 11008 x 4096
-// E4M3 product from 105 to 363 us.
+// are one instruction here: GELU takes 11 issue slots an element this way.
+// Through the library's erfc, with branches, the 4096 x 11008 x 4096 E4M3
+// product with GELU took 363 us instead of 127.
 #pragma once
 
 #include <cstdint>

@@ -595,10 +595,12 @@ static PyObject* py_activate_grad(PyObject* self, PyObject* const* a, Py_ssize_t
     return done(status, "dg_activate_grad");
 }
 
-/* A contiguous matrix: address, rows, columns and bytes an element. */
+/* A contiguous matrix: address, rows, columns, bytes an element, and whether
+ * its type is one of the two. */
 typedef struct {
     void* data;
     int64_t rows, cols, bytes;
+    int bf16, fp16;
 } matrix_arg;
 
 static int get_matrix(PyObject* t, const char* what, int64_t* device, matrix_arg* m) {
@@ -606,6 +608,11 @@ static int get_matrix(PyObject* t, const char* what, int64_t* device, matrix_arg
     if (numbers(PyObject_GetAttr(t, n_shape), 2, shape, what, "must have two dimensions") < 0 ||
         get_data_here(t, device, &m->data) < 0 || as_int64(PyObject_GetAttr(t, n_nbytes), &bytes) < 0)
         return -1;
+    PyObject* type = PyObject_GetAttr(t, n_dtype);
+    if (type == NULL) return -1;
+    m->bf16 = type == type_bf16;
+    m->fp16 = type == type_fp16;
+    Py_DECREF(type);
     m->rows = shape[0];
     m->cols = shape[1];
     m->bytes = shape[0] > 0 && shape[1] > 0 ? bytes / (shape[0] * shape[1]) : 0;
@@ -638,7 +645,8 @@ static PyObject* fused(PyObject* const* a, Py_ssize_t n, int fp16) {
         return NULL;
     const int64_t out_bytes = out == DG_E4M3 ? 1 : 2;
     if (A.cols != B.cols || D.rows != A.rows || D.cols != B.rows || (A.bytes != 0 && A.bytes != in_bytes) ||
-        (B.bytes != 0 && B.bytes != in_bytes) || (D.bytes != 0 && D.bytes != out_bytes)) {
+        (B.bytes != 0 && B.bytes != in_bytes) || (D.bytes != 0 && D.bytes != out_bytes) || A.bf16 || B.bf16 ||
+        (D.bf16 && out != DG_BF16) || (D.fp16 && out != DG_FP16)) {
         fail("A [M, K], B [N, K] and D [M, N] must agree, with elements of the operands' and the output's type");
         return NULL;
     }
@@ -646,16 +654,12 @@ static PyObject* fused(PyObject* const* a, Py_ssize_t n, int fp16) {
     e.residual_type = DG_BF16;
     if (a[7] != Py_None) {
         if (get_matrix(a[7], "residual", &device, &R) < 0) return NULL;
-        PyObject* type = PyObject_GetAttr(a[7], n_dtype);
-        if (type == NULL) return NULL;
-        const int bf16 = type == type_bf16, half = type == type_fp16;
-        Py_DECREF(type);
-        if (!(bf16 || half) || R.rows != D.rows || R.cols != D.cols) {
+        if (!(R.bf16 || R.fp16) || R.rows != D.rows || R.cols != D.cols) {
             fail_about("residual", "must be BF16 or FP16 with the shape of D");
             return NULL;
         }
         e.residual = R.data;
-        e.residual_type = bf16 ? DG_BF16 : DG_FP16;
+        e.residual_type = R.bf16 ? DG_BF16 : DG_FP16;
     }
     if (get_scales(a[3], "scale_a", A.rows, &device, &sa, &e.scale_a_rows) < 0 ||
         get_scales(a[4], "scale_b", B.rows, &device, &sb, &e.scale_b_rows) < 0 ||

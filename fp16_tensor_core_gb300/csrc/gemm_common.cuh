@@ -225,8 +225,8 @@ __device__ __forceinline__ uint32_t stage_box(const Params& p, uint8_t* box, int
 // ---- the fused epilogue: act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n]
 
 // 32 elements of one row of the residual, 16 bits each (zeros past column N
-// and without a residual); N a multiple of 8.  Not the read-only path: D may be the residual,
-// each element read by the thread that later writes it.
+// and without a residual); N a multiple of 8.  Not the read-only path: D may
+// be the residual, each element read by the warp that later writes it.
 __device__ __forceinline__ void load_residual(const Params& p, int row, bool row_ok, int col0,
                                               uint32_t (&w)[16]) {
 #pragma unroll

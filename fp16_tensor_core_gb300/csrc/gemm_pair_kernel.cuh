@@ -15,7 +15,7 @@ namespace dg {
 namespace {
 
 constexpr int kPairBM = 256;   // output rows of a pair tile
-constexpr uint32_t kEpiBarrier = 1;   // named barrier of the four epilogue warps
+constexpr uint32_t kEpiBarrier = 1;   // named barrier of the epilogue warps
 constexpr int kHalfBM = 128;   // rows of it per CTA
 
 // Staging boxes of the epilogue: one 32 x 32 box per epilogue warp.
@@ -373,7 +373,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     stage_columns<BN>(p, columns, nt * BN, half, lane);
                 }
             }
-            // The four warps continue or leave together (the split tail
+            // The warps continue or leave together (the split tail
             // below synchronises them on a named barrier).
             const bool got = wait_bounded_cluster(&acc_full[acc], acc_phase, ctl);
             if (!named_bar_and(kEpiBarrier, kEpiThreads, got)) break;

@@ -26,7 +26,7 @@
 //    CTAs with one multicast commit to `empty`; at the end of a tile it
 //    commits to `acc_full` in both CTAs;
 //  * both CTAs' epilogue warps release an accumulator buffer by arriving on
-//    the even CTA's `acc_empty` (count 8: four warps per CTA);
+//    the even CTA's `acc_empty` (count 8: four warps per CTA; 16 when fused);
 //  * a final multicast commit to `drain` tells both CTAs that no pair MMA
 //    still reads their shared memory or writes their tensor memory; only
 //    then is tensor memory freed (collectively) and the CTAs exit;

@@ -200,6 +200,8 @@ def test_refusals():
             (lambda: dg.dg_fp8_gemm_fused(A, B, codes, sa, sb), "must agree"),
             (lambda: dg.dg_fp8_gemm_fused(A.half(), B.half(), D, sa, sb), "must agree"),
             (lambda: dg.dg_hgemm_fused(A, B, D), "must agree"),
+            (lambda: dg.dg_hgemm_fused(A.to(BF), B.to(BF), D, out=dg.DG_BF16), "must agree"),
+            (lambda: dg.dg_fp8_gemm_fused(A, B, D, sa, sb, out=dg.DG_FP16), "must agree"),
             (lambda: dg.dg_fp8_gemm_fused(A, B, D, sa[:3], sb), "scale_a must be FP32 with 4"),
             (lambda: dg.dg_fp8_gemm_fused(A, B, D, sa, sb[:5]), "scale_b must be FP32 with 32"),
             (lambda: dg.dg_fp8_gemm_fused(A, B, D, sa, sb, bias=sb.half()), "bias must be FP32"),
