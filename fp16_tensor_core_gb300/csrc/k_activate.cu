@@ -12,10 +12,15 @@
 //
 // Memory bounds both: 2 bytes an input element and 1 to 3 of output; the
 // checkpoint halves what the backward pass reads of the input.  Forward, a
-// block keeps a row in registers until the maxima of the row are known.  Backward needs nothing of a row but
-// its scales: a thread owns eight columns over a run of rows, so that dbias
-// is summed in registers; the runs' sums are joined in order by a second
-// kernel.
+// block keeps a row in registers until the maxima of the row are known.
+// Backward needs nothing of a row but its scales: a thread owns eight columns
+// of every so-many-th row, so that dbias is summed in registers; the blocks'
+// sums are joined in order by a second kernel.  The blocks of a column take
+// the rows in turn, so that the grid moves through memory as one band (each
+// on a run of rows of its own: 5 % more time).
+// Gated, 8192 x 11008 BF16: codes and checkpoint 101.8 us, 0.91 of the rate of
+// a copy; gradient from the checkpoint 119.4 us, 0.89 (122.5 with dbias), from
+// the input 134.0 us, 0.99 (141.7).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -144,26 +149,29 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
     }
 }
 
-constexpr int kGradResident = 8;    // blocks an SM
-constexpr int kGradThreads = 128;   // 1024 columns a block, or fewer and several rows at once
+constexpr int kGradResident = 7;    // blocks an SM (with 8, 64 registers: 1 to 4 % more time; with 6: 4 to 5 %)
+constexpr int kGradThreads = 128;
+constexpr int kGradAcross = 32;     // threads side by side at most: a warp's 512 bytes of a row
 
 template <bool kFp16, bool kGated, bool kCodes>
 __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_kernel(const ActGradArgs a, int across) {
-    __shared__ float4 columns[kGradThreads][4];   // narrow rows: the threads' sums
+    __shared__ float4 columns[kGradThreads][4];   // the threads' sums
     pdl_wait();
     constexpr int kHalves = kGated ? 2 : 1;
     // `across` threads (a power of two) side by side, the others on other rows
     const int t = threadIdx.x, down = kGradThreads / across;
     const int c = 8 * static_cast<int>(blockIdx.x * across + (t & (across - 1)));
     const int64_t width = static_cast<int64_t>(kHalves) * a.cols;
-    const int64_t first = a.rows * blockIdx.y / gridDim.y, end = a.rows * (blockIdx.y + 1) / gridDim.y;
+    const int64_t step = static_cast<int64_t>(gridDim.y) * down;
     pair sums[kHalves][4];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sums[h][e] = 0;
     if (c < a.cols) {
-        // The next row's loads are in flight while a row is worked on.
+        // The next row's loads are in flight while a row is worked on.  Codes
+        // leave too few bytes in flight: the row after it is on its way to L2
+        // (126.0 -> 120.8 us; reading the input itself, 143 -> 160).
         uint4 next_dy = make_uint4(0, 0, 0, 0), next_x[kHalves];
         uint2 next_q[kHalves];
         float next_scale[kHalves];
@@ -179,10 +187,10 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
                 }
             }
         };
-        int64_t row = first + t / across;
-        if (row < end) fetch(row);
+        int64_t row = static_cast<int64_t>(blockIdx.y) * down + t / across;
+        if (row < a.rows) fetch(row);
 #pragma unroll 1
-        for (; row < end; row += down) {
+        for (; row < a.rows; row += step) {
             pair dy[4], x[kHalves][4];
             unpack8<kFp16>(next_dy, dy);
 #pragma unroll
@@ -192,7 +200,16 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
                 else
                     unpack8<kFp16>(next_x[h], x[h]);
             }
-            if (row + down < end) fetch(row + down);
+            if (row + step < a.rows) fetch(row + step);
+            if constexpr (kCodes) {
+                const int64_t later = row + 2 * step;
+                if (later < a.rows) {
+                    prefetch_line(a.dy + later * a.dy_stride + c);
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        prefetch_line(a.x_q + later * width + static_cast<int64_t>(h) * a.cols + c);
+                }
+            }
             pair dx[kHalves][4];
             with_activation(a.act, [&](auto act) {
 #pragma unroll
@@ -210,20 +227,14 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
             for (int h = 0; h < kHalves; ++h) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sums[h][e] = pair_add(sums[h][e], dx[h][e]);
-                *reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + static_cast<int64_t>(h) * a.cols + c) =
-                    pack8<kFp16>(dx[h]);
+                __stcs(reinterpret_cast<uint4*>(a.dx + row * a.dx_stride + static_cast<int64_t>(h) * a.cols + c),
+                       pack8<kFp16>(dx[h]));
             }
         }
     }
     if (a.partials == nullptr) return;
     pdl_launch_dependents();   // the join's launch
     float* part = a.partials + blockIdx.y * width;
-    if (down == 1) {
-        if (c >= a.cols) return;
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) store_sums(part + static_cast<int64_t>(h) * a.cols + c, sums[h]);
-        return;
-    }
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) store_sums(reinterpret_cast<float*>(&columns[t][2 * h]), sums[h]);
     __syncthreads();
@@ -258,18 +269,19 @@ cudaError_t run_act(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
     return run_act_rows<8, kFp16, false>(a, p, s);
 }
 
-// The gradient's blocks: `across` threads side by side, `columns` blocks of
-// them, `runs` runs of rows: as many blocks as are resident at once (eight an
-// SM at its registers), but no run of fewer rows than a block takes at once,
-// and past 256 runs, which the join has to add up, none of fewer than eight
-// (22397 x 64: 1216 runs 9.9 us, 256 runs 6.4).
+// The gradient's blocks: `across` threads side by side and the others below
+// them, `columns` blocks of that width, `runs` of them on the rows in turn: as
+// many blocks as are resident at once, but no more than have rows, and past
+// 256 runs, which the join has to add up, none of fewer than eight rows a
+// thread (100000 x 8, gated with dbias: 9.6 us, 11.2 without this; 4096 x 256:
+// 6.9, 7.6; 22397 x 64: 8.6, 8.1).
 struct ActGradPlan {
     int across, columns, runs;
 };
 ActGradPlan act_grad_plan(int64_t rows, int cols, int sm_count) {
     ActGradPlan p{1, 1, 1};
     const int vectors = cols / 8;
-    while (p.across < kGradThreads && p.across < vectors) p.across *= 2;
+    while (p.across < kGradAcross && p.across < vectors) p.across *= 2;
     p.columns = (vectors + p.across - 1) / p.across;
     const int down = kGradThreads / p.across;
     const int64_t runs = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * kGradResident / p.columns);

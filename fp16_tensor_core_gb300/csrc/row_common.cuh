@@ -117,6 +117,9 @@ __device__ __forceinline__ void prefetch_row(const void* p, int bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p), "r"(bytes) : "memory");
 }
 
+// The line at p is brought into L2 (any alignment; p inside the tensor).
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+
 // Forgets what has been formed from packed elements: they are unpacked again,
 // where the compiler would keep (and spill) twice their registers.
 __device__ __forceinline__ void forget(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }

@@ -100,7 +100,7 @@ def test_gradient(rows, cols, act, dtype, gated, checkpoint):
     # of itself, and act' changes by at most |x| |act''| <= 2 times that)
     close(dx, want, rounded(want, dtype) + terms * ACT + dy.double().abs().repeat(1, width // cols) * 2.0 ** -20, "dx")
     assert rest.isnan().all()
-    # at most 1300 rows in 1300 runs: 163 in a row, then 8
+    # at most 1300 terms a column, fewer than 200 additions in a row: 2^-24 200 < 2^-16
     close(dbias, want.sum(0), (terms * (ACT + 2.0 ** -16)).sum(0) + dy.double().abs().sum(0).repeat(width // cols) *
           2.0 ** -20, "dbias")
     again = torch.zeros_like(x)
