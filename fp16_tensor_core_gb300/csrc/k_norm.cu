@@ -31,8 +31,9 @@
 namespace dg {
 namespace {
 
-// A sum of squares past FP32's range is taken again of elements times this.
-constexpr float kDown = 0x1p-64f;
+// A sum of squares past FP32's range is taken again of elements times this:
+// 32768 squares of 2^128 2^-80 hold, and one element at least was above 2^56.
+constexpr float kDown = 0x1p-80f;
 
 // Threads of a block, and blocks an SM at least, by vectors a thread: the
 // registers (64, 80, 128) hold a row and the next row's loads.
@@ -115,23 +116,22 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
             for (int i = 0; i < NV; ++i) x[i] = r[i];
             if (row + 2 * step < a.rows) load_row(x_next += step * a.x_stride, r);
         }
-        float total = reduce.sum(pair_sum(squares)), eps = a.eps;
+        float total = reduce.sum(pair_sum(squares)), down = 1.0f;
         // (a vote: rows of a warp differ, and the reduction takes all of it)
         const bool again = !(total <= 3.0e38f);
         if (kNarrow ? __any_sync(0xFFFFFFFFu, again) : again) {
-            const float down = again ? kDown : 1.0f;
+            down = again ? kDown : 1.0f;
             squares = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    v[i][e] = pair_mul(v[i][e], pair_of(down));
-                    squares = pair_fma(v[i][e], v[i][e], squares);
+                    const pair t = pair_mul(v[i][e], pair_of(down));
+                    squares = pair_fma(t, t, squares);
                 }
             total = reduce.sum(pair_sum(squares));
-            eps = eps * down * down;
         }
-        const float inv = rsqrtf(fmaf(total, inv_cols, eps));
+        const float inv = rsqrtf(fmaf(total, inv_cols, a.eps * down * down)) * down;
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {

@@ -140,6 +140,36 @@ def test_special_rows(dtype):
     assert dx[1].isnan().all()
 
 
+@pytest.mark.parametrize("cols", [8, 256, 4096, 16384])
+def test_rows_at_the_top_of_the_range(cols):
+    """Elements up to BF16's largest, whose squares' sum leaves FP32 by far,
+    beside elements down to 2^-60."""
+    x = randn(21, 5, cols).clamp(-3, 3).mul(2.0 ** 126).to(BF)      # below 1.5 2^127
+    x[1] = torch.finfo(BF).max
+    x[2] = -torch.finfo(BF).max
+    x[2, 1::2] = 2.0 ** -60
+    x[3, 1:] = 2.0 ** 58
+    w = randn(22, cols).to(BF)
+    want = norm64(x.double(), w.double(), EPS)
+    y = torch.zeros_like(x)
+    dg.dg_rmsnorm(x, y, weight=w, eps=EPS)
+    # a reciprocal of 2^-128 keeps 21 bits: 2^-22, within `rounded`'s ROW
+    close(y, want, rounded(want, BF) + 2.0 ** -126, "y")
+    q, scale = torch.zeros(5, cols, dtype=torch.uint8, device="cuda"), torch.zeros(5, device="cuda")
+    dg.dg_rmsnorm_e4m3(x, q, scale, weight=w, eps=EPS)
+    check_codes(q, scale, want)
+    dy = randn(23, 5, cols).to(BF)
+    dx, dw = torch.zeros_like(x), torch.zeros(cols, device="cuda")
+    scratch = torch.empty(dg.dg_rmsnorm_grad_scratch(5, cols), dtype=torch.uint8, device="cuda")
+    dg.dg_rmsnorm_grad(x, dy, dx, weight=w, dweight=dw, scratch=scratch, eps=EPS)
+    size = torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + EPS)
+    u, g = x.double() / size, dy.double() * w.double()
+    grad = (g - u * (g * u).mean(-1, keepdim=True)) / size
+    terms = (g.abs() + u.abs() * (g * u).abs().mean(-1, keepdim=True)) / size
+    close(dx, grad, rounded(grad, BF) + terms * 4 * ROW, "dx")
+    close(dw, (dy.double() * u).sum(0), (dy.double() * u).abs().sum(0) * (2 * ROW + 2.0 ** -16), "dweight")
+
+
 @pytest.mark.parametrize("scale", [1e-40, 2.0 ** -130, 2.0 ** -100, 2.0 ** 125, 0.0, math.inf, math.nan])
 def test_recorded_scales_of_every_size(scale):
     x, _, w = inputs(3, 256, HALF, seed=6)
