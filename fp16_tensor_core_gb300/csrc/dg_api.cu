@@ -1042,6 +1042,12 @@ dg_status check_row_sizes(int64_t rows, int64_t cols) {
 // Rows that are written lie apart.
 bool own_rows(const dg_rows* r, int64_t rows, int64_t cols) { return rows <= 1 || r->stride >= cols; }
 
+// An output at an input's address is that input, row for row (else a row would
+// be written before another thread has read it).
+bool apart_or_same(const dg_rows* out, const dg_rows* in, int64_t rows) {
+    return out == nullptr || in == nullptr || out->data != in->data || out->stride == in->stride || rows <= 1;
+}
+
 // The smallest eps that FP32 holds as a normal number: zero rows stay finite.
 bool good_eps(double eps) { return eps >= 0x1p-126 && eps <= 3.0e38; }
 
@@ -1068,6 +1074,7 @@ dg_status check_norm(const dg_rows* x, const dg_rows* residual, const dg_rows* s
     if (rc == DG_OK) rc = check_rows_or_null(sum);
     if (rc != DG_OK) return rc;
     if (sum != nullptr && !own_rows(sum, rows, cols)) return DG_ERR_INVALID_VALUE;
+    if (!apart_or_same(sum, x, rows) || !apart_or_same(sum, residual, rows)) return DG_ERR_INVALID_VALUE;
     return aligned16(weight) ? DG_OK : DG_ERR_MISALIGNED;
 }
 
@@ -1105,7 +1112,9 @@ dg_status dg_rmsnorm(const dg_rows* x, const dg_rows* residual, const dg_rows* s
     if (rc != DG_OK || rows == 0) return rc;
     rc = check_rows(y);
     if (rc != DG_OK) return rc;
-    if (!own_rows(y, rows, cols) || (sum != nullptr && sum->data == y->data)) return DG_ERR_INVALID_VALUE;
+    if (!own_rows(y, rows, cols) || (sum != nullptr && sum->data == y->data) || !apart_or_same(y, x, rows) ||
+        !apart_or_same(y, residual, rows))
+        return DG_ERR_INVALID_VALUE;
     DeviceState* st = nullptr;
     rc = current_device_state(&st);
     if (rc != DG_OK) return rc;
@@ -1176,7 +1185,9 @@ dg_status dg_rmsnorm_grad(const dg_rows* s, const void* weight, const dg_rows* d
         if (rc == DG_OK) rc = check_rows_or_null(dsum);
         if (rc == DG_OK) rc = check_rows(dx);
         if (rc != DG_OK) return rc;
-        if (!own_rows(dx, rows, cols) || (dweight != nullptr && scratch == nullptr)) return DG_ERR_INVALID_VALUE;
+        if (!own_rows(dx, rows, cols) || (dweight != nullptr && scratch == nullptr) || !apart_or_same(dx, s, rows) ||
+            !apart_or_same(dx, dy, rows) || !apart_or_same(dx, dsum, rows))
+            return DG_ERR_INVALID_VALUE;
     }
     if (!aligned16(weight) || !aligned16(dweight) || !aligned16(scratch)) return DG_ERR_MISALIGNED;
     if (rows == 0 && dweight == nullptr) return DG_OK;
@@ -1217,7 +1228,7 @@ dg_status dg_activate(const dg_rows* x, int gated, dg_activation act, int64_t ro
     rc = check_rows(x);
     if (rc == DG_OK) rc = check_rows_or_null(y);
     if (rc != DG_OK) return rc;
-    if (y != nullptr && (!own_rows(y, rows, cols) || (gated != 0 && y->data == x->data)))
+    if (y != nullptr && (!own_rows(y, rows, cols) || (gated != 0 && y->data == x->data) || !apart_or_same(y, x, rows)))
         return DG_ERR_INVALID_VALUE;
     if (!aligned16(q) || !aligned16(x_q) || !aligned4(q_scale) || !aligned4(x_scale)) return DG_ERR_MISALIGNED;
     DeviceState* st = nullptr;
@@ -1262,7 +1273,8 @@ dg_status dg_activate_grad(const dg_rows* dy, const dg_rows* x, const uint8_t* x
         if (rc == DG_OK) rc = check_rows(dx);
         if (rc != DG_OK) return rc;
         if ((x == nullptr && x_q == nullptr) || !own_rows(dx, rows, gated != 0 ? 2 * cols : cols) ||
-            (gated != 0 && dx->data == dy->data) || (dbias != nullptr && scratch == nullptr))
+            (gated != 0 && dx->data == dy->data) || (dbias != nullptr && scratch == nullptr) ||
+            !apart_or_same(dx, dy, rows) || !apart_or_same(dx, x, rows))
             return DG_ERR_INVALID_VALUE;
     }
     if (!aligned16(x_q) || !aligned4(x_scale) || !aligned16(dbias) || !aligned16(scratch)) return DG_ERR_MISALIGNED;
@@ -1307,13 +1319,16 @@ dg_status check_epilogue(const dg_epilogue* e, const void* D, int64_t M, int64_t
     if (out == DG_E4M3 && e->scale_d == nullptr) return DG_ERR_INVALID_VALUE;
     // in place only element by element
     if (e->residual == D && (out == DG_E4M3 || e->residual_type != out)) return DG_ERR_INVALID_VALUE;
-    // zeroed before anything is read
-    if (e->amax_d != nullptr && (e->amax_d == e->scale_a || e->amax_d == e->scale_b || e->amax_d == e->scale_d))
-        return DG_ERR_INVALID_VALUE;
     auto vector = [](const float* p, int rows) { return rows != 0 ? aligned16(p) : aligned4(p); };
     if (!vector(e->scale_a, e->scale_a_rows) || !vector(e->scale_b, e->scale_b_rows) || !aligned16(e->bias) ||
         !aligned16(e->residual) || !aligned4(e->scale_d) || !aligned4(e->amax_d))
         return DG_ERR_MISALIGNED;
+    // zeroed before anything is read
+    auto among = [e](const float* p, int64_t n) { return p != nullptr && e->amax_d >= p && e->amax_d < p + n; };
+    if (e->amax_d != nullptr && (among(e->scale_a, e->scale_a_rows != 0 ? M : 1) ||
+                                 among(e->scale_b, e->scale_b_rows != 0 ? N : 1) || among(e->bias, N) ||
+                                 among(e->scale_d, 1)))
+        return DG_ERR_INVALID_VALUE;
     return DG_OK;
 }
 

@@ -521,7 +521,8 @@ dg_status dg_attn_decode_scratch(int batch, int q_len, int q_heads, int head_dim
 /* rows x columns BF16 or FP16 elements: element (r, c) at
  * data[r * stride + c].  data 16-byte aligned, stride a multiple of 8
  * elements (DG_ERR_MISALIGNED), not negative; as an output, rows must not
- * overlap one another. */
+ * overlap one another.  Where an output may be an input itself, that is with
+ * its address and its stride; otherwise outputs overlap nothing else. */
 typedef struct {
     void* data;
     int64_t stride;
@@ -570,6 +571,8 @@ dg_status dg_rmsnorm_e4m3_amax(const dg_rows* x, const dg_rows* residual, const 
  *            dsum may be NULL; dx may be any of the others itself.
  *   dweight  FP32[cols], 16-byte aligned, or NULL.  Summed in FP32 in a fixed
  *            order; overwritten.
+ * FP32 holds dx only where it holds g and the sum of g s (over 2^80 where
+ * that of s^2 is beyond its range).
  *   scratch  device, 16-byte aligned, at least dg_rmsnorm_grad_scratch()
  *            bytes; unused (may be NULL) without dweight.  Holds nothing
  *            between calls; calls that may overlap in time need one each. */
@@ -639,14 +642,14 @@ typedef struct {
     const void* residual;   /* M x N dense of residual_type, or NULL                            */
     dg_dtype residual_type; /* DG_BF16 or DG_FP16                                               */
     const float* scale_d;   /* FP32[1]; required iff out is DG_E4M3                             */
-    float* amax_d;          /* FP32[1], none of the scales, or NULL                             */
+    float* amax_d;          /* FP32[1], none of the scales or the bias, or NULL                 */
 } dg_epilogue;
 
 /* dg_fp8_gemm with more in its epilogue, on the accumulators in FP32:
  *   v      = act(scale_a[m] * scale_b[n] * sum_k A[m,k] * B[n,k] + bias[n]) + residual[m,n]
  *   D[m,n] = out(v), or E4M3(v / *scale_d)
  *   amax_d = max |v| over D (as dg_fp8_gemm_amax; zeroed by the call)
- * rounded once.  Row scales of A are what dg_rmsnorm_e4m3 and dg_activate
+ * rounded once (the two scales are multiplied first).  Row scales of A are what dg_rmsnorm_e4m3 and dg_activate
  * write; a weight quantised by rows has its own (one scale serves either side
  * as before).  With K == 0 the sum is empty.  D may be the residual itself
  * when both have the same 16-bit type.  Smooth activations as dg_activate.

@@ -34,7 +34,8 @@ NORM = COMMON + [
     (dict(x=rows(stride=-64)), BAD), (dict(residual=rows(FAKE + 2)), OFF), (dict(residual=rows(None)), BAD),
     (dict(sum=rows(FAKE, 4)), OFF), (dict(sum=rows(FAKE, 56)), BAD), (dict(weight=FAKE + 8), OFF),
     (dict(eps=0.0), BAD), (dict(eps=-1.0), BAD), (dict(eps=math.nan), BAD), (dict(eps=math.inf), BAD),
-    (dict(eps=2.0 ** -127), BAD),
+    (dict(eps=2.0 ** -127), BAD), (dict(sum=rows(FAKE, 128)), BAD),
+    (dict(residual=rows(FAKE + 4096, 0), sum=rows(FAKE + 4096, 64)), BAD),
 ]
 
 
@@ -46,7 +47,8 @@ def norm_args(kw):
 
 @pytest.mark.parametrize("kw,expect", NORM + [
     (dict(y=None), BAD), (dict(y=rows(FAKE + 4)), OFF), (dict(y=rows(stride=32)), BAD),
-    (dict(sum=rows(FAKE), y=rows(FAKE)), BAD),
+    (dict(sum=rows(FAKE), y=rows(FAKE)), BAD), (dict(y=rows(FAKE, 72)), BAD),
+    (dict(residual=rows(FAKE + 64, 0), y=rows(FAKE + 64)), BAD),
 ])
 def test_rmsnorm(L, kw, expect):
     assert L.dg_rmsnorm(*norm_args(kw), kw.get("y", rows(FAKE + 4096)), None) == expect
@@ -72,6 +74,7 @@ def test_rmsnorm_e4m3_amax(L, kw, expect):
 @pytest.mark.parametrize("kw,expect", COMMON + [
     (dict(x=None), BAD), (dict(x=rows(FAKE + 8)), OFF), (dict(dy=None), BAD), (dict(dy=rows(stride=12)), OFF),
     (dict(dsum=rows(FAKE + 2)), OFF), (dict(dx=None), BAD), (dict(dx=rows(stride=0)), BAD), (dict(eps=0.0), BAD),
+    (dict(dy=rows(FAKE, 0)), BAD), (dict(x=rows(FAKE, 72)), BAD), (dict(dsum=rows(FAKE, 72)), BAD),
     (dict(weight=FAKE + 8), OFF), (dict(dweight=FAKE, scratch=None), BAD), (dict(dweight=FAKE + 4), OFF),
     (dict(dweight=FAKE, scratch=FAKE + 4), OFF),
 ])
@@ -86,7 +89,7 @@ def test_rmsnorm_grad(L, kw, expect):
     (dict(act=-1), BAD), (dict(act=5), BAD), (dict(x=None), BAD), (dict(x=rows(stride=4)), OFF),
     (dict(y=rows(FAKE + 8)), OFF), (dict(y=rows(stride=40)), BAD), (dict(q=FAKE), BAD), (dict(q_scale=FAKE), BAD),
     (dict(x_q=FAKE), BAD), (dict(q=FAKE + 8, q_scale=FAKE), OFF), (dict(x_q=FAKE, x_scale=FAKE + 2), OFF),
-    (dict(gated=1, x=rows(FAKE, 128), y=rows(FAKE, 128)), BAD),
+    (dict(gated=1, x=rows(FAKE, 128), y=rows(FAKE, 128)), BAD), (dict(x=rows(FAKE, 0), y=rows(FAKE)), BAD),
 ])
 def test_activate(L, kw, expect):
     a = dict(x=rows(), gated=0, act=dg.DG_ACT_SILU, rows=4, cols=64, dtype=dg.DG_BF16, y=rows(FAKE + 4096), q=None,
@@ -99,7 +102,8 @@ def test_activate(L, kw, expect):
     (dict(act=7), BAD), (dict(dy=None), BAD), (dict(x=None), BAD), (dict(x=None, x_q=FAKE), BAD),
     (dict(x_q=FAKE, x_scale=FAKE), BAD), (dict(x=None, x_q=FAKE + 4, x_scale=FAKE), OFF), (dict(dx=None), BAD),
     (dict(dx=rows(stride=40)), BAD), (dict(gated=1), BAD), (dict(dbias=FAKE, scratch=None), BAD),
-    (dict(gated=1, x=rows(FAKE, 128), dx=rows(FAKE, 128)), BAD),
+    (dict(gated=1, x=rows(FAKE, 128), dx=rows(FAKE, 128)), BAD), (dict(dy=rows(FAKE, 0)), BAD),
+    (dict(x=rows(FAKE, 72)), BAD), (dict(gated=1, dy=rows(FAKE + 64), x=rows(FAKE, 0), dx=rows(FAKE, 128)), BAD),
     (dict(dbias=FAKE + 4), OFF), (dict(scratch=FAKE + 8), OFF),
 ])
 def test_activate_grad(L, kw, expect):
@@ -135,7 +139,8 @@ EPILOGUE = [
     (dict(e=epilogue(scale_b=FAKE + 8, scale_b_rows=1)), OFF), (dict(e=epilogue(bias=FAKE + 4)), OFF),
     (dict(e=epilogue(residual=FAKE + 8)), OFF), (dict(e=epilogue(residual=FAKE + 64, residual_type=1)), BAD),
     (dict(e=epilogue(residual=FAKE, residual_type=dg.DG_FP16)), BAD), (dict(e=epilogue(amax_d=FAKE + 1)), OFF),
-    (dict(e=epilogue(amax_d=FAKE)), BAD),
+    (dict(e=epilogue(amax_d=FAKE)), BAD), (dict(e=epilogue(scale_b_rows=1, amax_d=FAKE + 4 * 31)), BAD),
+    (dict(e=epilogue(scale_a_rows=1, amax_d=FAKE + 12)), BAD), (dict(e=epilogue(bias=FAKE + 256, amax_d=FAKE + 260)), BAD),
     (dict(M=-1), BAD), (dict(N=1 << 31), BAD), (dict(A=None), BAD), (dict(D=None), BAD), (dict(A=FAKE + 8), OFF),
     (dict(K=36), OFF), (dict(out=7), BAD),
 ]
