@@ -30,6 +30,14 @@ __device__ __forceinline__ void pdl_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A read of what an earlier kernel wrote, in its place behind pdl_wait (a
+// read-only load that is not volatile may be moved before it).
+__device__ __forceinline__ float ld_float(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // Lets the next kernel in the stream (launched with programmatic stream
 // serialization) be scheduled before this grid ends; it still waits in
 // pdl_wait for this grid to complete before it reads or writes memory.

@@ -334,8 +334,8 @@ __device__ __forceinline__ void stage_columns(const Params& p, float* columns, i
         const int n = col0 + 32 * (first + 2 * i) + lane;
         s[i] = p.sb == nullptr ? 1.0f : 0.0f;
         b[i] = 0.0f;
-        if (n < p.N && p.sb != nullptr) s[i] = __ldg(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
-        if (n < p.N && p.epi.bias != nullptr) b[i] = __ldg(p.epi.bias + n);
+        if (n < p.N && p.sb != nullptr) s[i] = ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
+        if (n < p.N && p.epi.bias != nullptr) b[i] = ld_float(p.epi.bias + n);
     }
     __syncwarp();   // every lane has read the last tile's
 #pragma unroll
@@ -413,11 +413,11 @@ __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col
 
 // A row's scale of A (1 without scales, and for rows outside).
 __device__ __forceinline__ float scale_of_row(const Params& p, int row, bool row_ok) {
-    return p.sa == nullptr || !row_ok ? 1.0f : __ldg(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
+    return p.sa == nullptr || !row_ok ? 1.0f : ld_float(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
 }
 
 __device__ __forceinline__ ByScale output_scale(int out_kind, const float* sd) {
-    return out_kind == kOutE4M3 ? by_scale(__ldg(sd)) : ByScale{1.0f, 1.0f};
+    return out_kind == kOutE4M3 ? by_scale(ld_float(sd)) : ByScale{1.0f, 1.0f};
 }
 
 // The fused kernels' maximum, one warp's: already of the values themselves.

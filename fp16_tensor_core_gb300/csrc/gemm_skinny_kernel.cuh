@@ -124,8 +124,8 @@ struct FusedColumn {
 };
 __device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live, int n) {
     FusedColumn c;
-    if (live && p.sb != nullptr) c.sb = __ldg(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
-    if (live && p.epi.bias != nullptr) c.bias = __ldg(p.epi.bias + n);
+    if (live && p.sb != nullptr) c.sb = ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
+    if (live && p.epi.bias != nullptr) c.bias = ld_float(p.epi.bias + n);
     return c;
 }
 
@@ -525,7 +525,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
         FusedColumn column;
         if constexpr (kFused) {
             out = output_scale(p.out_kind, p.sd);
-            if (r < NC) row_scales[r] = p.sa != nullptr && r < p.M ? __ldg(p.sa + r * p.epi.sa_step) : 1.0f;
+            if (r < NC) row_scales[r] = p.sa != nullptr && r < p.M ? ld_float(p.sa + r * p.epi.sa_step) : 1.0f;
             named_bar_sync(kEpiBar, kEpiThreads);   // (the helpers' reads come after a hand-off)
         }
         uint32_t amax_bits = 0u;

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
             for (int h = 0; h < kHalves; ++h) {
                 if constexpr (kCodes) {
                     next_q[h] = load_once8(a.x_q + row * width + static_cast<int64_t>(h) * a.cols + c);
-                    next_scale[h] = __ldg(a.x_scale + row * kHalves + h);
+                    next_scale[h] = ld_float(a.x_scale + row * kHalves + h);
                 } else {
                     next_x[h] = load_once(a.x + row * a.x_stride + static_cast<int64_t>(h) * a.cols + c);
                 }

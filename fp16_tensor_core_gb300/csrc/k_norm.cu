@@ -48,6 +48,7 @@ template <int NV, bool kFp16, int kOut, bool kNarrow, bool kResidual>
 __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_kernel(const NormArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
     pdl_wait();
+    const uint16_t* const weight = behind_wait(a.weight);
     const RowTeam<kNarrow> team(team_size);
     RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
     for (int i = 0; i < NV; ++i) {
         x[i] = r[i] = make_uint4(0, 0, 0, 0);
         const int at = team.at + i * team.size;
-        if (kKeepWeight) w[i] = weight_if(a.weight != nullptr && at < vectors, a.weight, at);
+        if (kKeepWeight) w[i] = weight_if(a.weight != nullptr && at < vectors, weight, at);
     }
     // The next row's loads are in flight while a row is worked on: x and r; or,
     // without a residual, those of the next two rows (x, then r).
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
             const int at = team.at + i * team.size;
             if (a.weight != nullptr) {
                 pair f[4];
-                unpack8<kFp16>(kKeepWeight ? w[i] : weight_if(at < vectors, a.weight, at), f);
+                unpack8<kFp16>(kKeepWeight ? w[i] : weight_if(at < vectors, weight, at), f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], f[e]);
             }
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
     __shared__ float2 buffer[2][kRowThreads / 32];
     __shared__ float columns[kNarrow ? 4 : 1][256];   // four warps' sums
     pdl_wait();
+    const uint16_t* const weight = behind_wait(a.weight);
     const RowTeam<kNarrow> team(team_size);
     RowReduce<kNarrow> reduce{buffer, team.size};
     const int vectors = a.cols >> 3;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
     for (int i = 0; i < NV; ++i) {
         const int at = team.at + i * team.size;
         next_x[i] = next_d[i] = add[i] = make_uint4(0, 0, 0, 0);
-        if (kAhead) w[i] = weight_if(a.weight != nullptr && at < vectors, a.weight, at);
+        if (kAhead) w[i] = weight_if(a.weight != nullptr && at < vectors, weight, at);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw[i][e] = 0;
     }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
         auto g_of = [&](int i, const pair (&dy)[4], pair (&g)[4]) {
             const int at = team.at + i * team.size;
             if (a.weight != nullptr) {
-                unpack8<kFp16>(kAhead ? w[i] : weight_if(at < vectors, a.weight, at), g);
+                unpack8<kFp16>(kAhead ? w[i] : weight_if(at < vectors, weight, at), g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) g[e] = pair_mul(g[e], dy[e]);
             } else {
@@ -368,10 +370,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
 }
 
 // Columns' sums over parts: kLanes threads side by side take four columns each,
-// the block's kThreads / kLanes runs of parts one under another.
+// the block's kThreads / kLanes runs of parts one under another.  (Pointers
+// that may alias: the loads stay behind pdl_wait.)
 template <int kLanes, int kThreads>
-__global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* __restrict__ partials, int parts, int cols,
-                                                            float* __restrict__ out) {
+__global__ void __launch_bounds__(kThreads) join_columns_kernel(const float* partials, int parts, int cols,
+                                                            float* out) {
     constexpr int kRuns = kThreads / kLanes, kColumns = 4 * kLanes;
     static_assert(kRuns % 8 == 0 && 8 * kColumns <= kThreads, "eight threads a column at the end");
     __shared__ float4 sums[kThreads];

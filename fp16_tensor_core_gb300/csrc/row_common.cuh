@@ -99,8 +99,14 @@ __device__ __forceinline__ uint2 load_once8(const void* p) {
     asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
+// A pointer as it is known after pdl_wait: reads through it cannot come first.
+__device__ __forceinline__ const uint16_t* behind_wait(const uint16_t* p) {
+    asm volatile("" : "+l"(p) :: "memory");
+    return p;
+}
 // A vector of the norm's weight (every block reads it for every row, from
-// L1), or zeros.
+// L1), or zeros.  The compiler may move it: past pdl_wait's call, `weight` is
+// taken from behind_wait.
 __device__ __forceinline__ uint4 weight_if(bool take, const uint16_t* weight, int at) {
     uint4 v = make_uint4(0, 0, 0, 0);
     asm("{\n\t.reg .pred q;\n\t"
@@ -179,21 +185,24 @@ struct RowReduce {
         }
     }
     __device__ __forceinline__ float2 sum2(float a, float b) {
-        if constexpr (kNarrow) return make_float2(sum(a), sum(b));
+        if constexpr (kNarrow) {
+            return make_float2(sum(a), sum(b));
+        } else {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-        }
-        const float2 t = exchange(make_float2(a, b));
-        a = t.x;
-        b = t.y;
+            for (int o = 16; o > 0; o >>= 1) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            const float2 t = exchange(make_float2(a, b));
+            a = t.x;
+            b = t.y;
 #pragma unroll
-        for (int o = kRowThreads / 64; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            for (int o = kRowThreads / 64; o > 0; o >>= 1) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            return make_float2(a, b);
         }
-        return make_float2(a, b);
     }
 
     // Maxima of magnitudes (as ordered bits: NaN above all).

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fp16_tensor_core_gb300 as dg
-from _layers import ACT, ACT_TINY, F8, HALF, ROW, act64, check_codes, close, norm64, rounded
+from _layers import ACT, ACT_TINY, BF, F8, HALF, ROW, act64, check_codes, close, norm64, rounded
 
 pytestmark = pytest.mark.gpu
 SILU = dg.DG_ACT_SILU
@@ -87,3 +87,60 @@ def test_decode_step_captured(example):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, block(x, delta))
+
+
+def test_operands_written_just_before():
+    """Weights, bias and scales that the kernel before still writes when the
+    launches overlap it: read as they are then, not as they were."""
+    M, N, K = 200, 1040, 1024
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def randn(*shape):
+        return torch.randn(*shape, device="cuda", generator=g)
+
+    x, r = randn(M, K).to(BF), randn(M, K).to(BF)
+    codes = randn(N, K).to(torch.float8_e4m3fn).view(torch.uint8)
+    new = [randn(K).to(BF), randn(N), 0.1 + randn(N).abs(), torch.full((1,), 0.02, device="cuda")]
+    zeros = [torch.zeros_like(t) for t in new]
+    weight, bias, scale_b, scale = at = [t.clone() for t in zeros]
+    q, row_scale = torch.zeros(M, K, dtype=torch.uint8, device="cuda"), torch.zeros(M, device="cuda")
+    amax, D = torch.zeros(1, device="cuda"), [torch.zeros(m, N, dtype=BF, device="cuda") for m in (4, 60, M)]
+    q_x, scale_x = torch.zeros(M, N, dtype=torch.uint8, device="cuda"), torch.zeros(M, device="cuda")
+    y, dx = torch.zeros_like(x), torch.zeros_like(D[2])
+    dy, dw = randn(M, N).to(BF), torch.zeros(K, device="cuda")
+    scratch = torch.empty(dg.dg_rmsnorm_grad_scratch(M, K), dtype=torch.uint8, device="cuda")
+    outputs = [q, row_scale, amax, *D, y, dx, dw]
+
+    def one(i):
+        if i == 0:
+            dg.dg_rmsnorm_e4m3_amax(x, scale, q, amax, weight=weight, residual=r)
+        elif i == 1:
+            dg.dg_rmsnorm(x, y, weight=weight)
+        elif i == 2:
+            dg.dg_rmsnorm_grad(x, r, y, weight=weight, dweight=dw, scratch=scratch)
+        elif i < 6:
+            d = D[i - 3]
+            dg.dg_fp8_gemm_fused(codes[:len(d)], codes, d, scale_b[:len(d)], scale_b, bias=bias, amax_d=amax)
+        else:
+            dg.dg_activate(D[2], dg.DG_ACT_SILU, x_q=q_x, x_scale=scale_x)
+            dg.dg_activate_grad(dy, dg.DG_ACT_SILU, dx, x_q=q_x, x_scale=scale_x)
+
+    def run(i, late):
+        for a, b in zip(at, zeros if late else new):
+            a.copy_(b)
+        for t in outputs if i < 6 else [dx, q_x, scale_x]:
+            t.zero_()
+        torch.cuda.synchronize()
+        if late:
+            torch.cuda._sleep(100000)
+            for a, b in zip(at, new):
+                a.copy_(b)
+        one(i)
+        torch.cuda.synchronize()
+        return [t.clone() for t in outputs]
+
+    for i in range(7):
+        want = run(i, False)
+        for _ in range(3):
+            for a, b in zip(run(i, True), want):
+                assert torch.equal(a, b), i
