@@ -236,3 +236,25 @@ def test_graph():
         calls()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(replayed, out))
+
+
+def test_offsets_past_32_bits():
+    """Rows behind element 2^32 of a gated input, their codes behind 2^31, as the
+    same rows alone."""
+    rows, cols = 70000, 32768
+    x = torch.zeros(rows, 2 * cols, dtype=BF, device="cuda")
+    few, dy = randn(41, 2, 2 * cols).to(BF), randn(42, 2, cols).to(BF)
+    x[-2:] = few
+    q, scale = torch.empty(rows, cols, dtype=torch.uint8, device="cuda"), torch.empty(rows, device="cuda")
+    x_q, x_scale = torch.empty(rows, 2 * cols, dtype=torch.uint8, device="cuda"), torch.empty(rows, 2, device="cuda")
+    dg.dg_activate(x, dg.DG_ACT_SILU, q=q, q_scale=scale, x_q=x_q, x_scale=x_scale, gated=True)
+    alone = [torch.empty_like(t[:2]) for t in (q, scale, x_q, x_scale)]
+    dg.dg_activate(few, dg.DG_ACT_SILU, q=alone[0], q_scale=alone[1], x_q=alone[2], x_scale=alone[3], gated=True)
+    for got, want in zip((q, scale, x_q, x_scale), alone):
+        assert torch.equal(got[-2:], want)
+    up = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    up[-2:] = dy
+    dg.dg_activate_grad(up, dg.DG_ACT_SILU, x, x_q=x_q, x_scale=x_scale, gated=True)
+    want = torch.empty_like(few)
+    dg.dg_activate_grad(dy, dg.DG_ACT_SILU, want, x_q=alone[2], x_scale=alone[3], gated=True)
+    assert torch.equal(x[-2:], want) and (x[0] == 0).all()

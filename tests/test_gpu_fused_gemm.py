@@ -252,3 +252,18 @@ def test_graph_and_streams():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(replayed, (D, codes, amax)))
         dg.dg_release_stream(side)
+
+
+@pytest.mark.parametrize("N", [33024, 33001])
+def test_offsets_past_32_bits(N):
+    """The last rows of an output of more than 2^31 elements, onto a residual."""
+    M, K = 66000, 64
+    A, B, sa, sb = operands(M, N, K, False, True, 6)
+    D, bias, few = torch.empty(M, N, dtype=BF, device="cuda"), randn(1, N), slice(M - 40, M)
+    D[few] = randn(2, 40, N).to(BF)
+    alone = D[few].clone()
+    dg.dg_fp8_gemm_fused(A, B, D, sa, sb, bias=bias, act=dg.DG_ACT_SILU, residual=D)
+    want = (wide(A[few]) @ wide(B).T) * sa[few].double()[:, None] * sb.double() + bias.double()
+    size = (wide(A[few]).abs() @ wide(B).T.abs()) * sa[few].double()[:, None] * sb.double() + bias.double().abs()
+    want = act64(want, dg.DG_ACT_SILU)[0] + alone.double()
+    close(D[few], want, 1.2 * size * 2.0 ** -18 + want.abs() * (STEP[BF] + 2.0 ** -22) + size * ACT + ACT_TINY, "D")

@@ -283,3 +283,26 @@ def test_streams_and_graphs():
     calls(stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(replayed, (q, s, dx, dw)))
+
+
+def test_offsets_past_32_bits():
+    """Rows behind element 2^32 (as views of a wide buffer, with dense E4M3
+    codes behind 2^31) as the same rows alone."""
+    rows, cols, stride = 70000, 32768, 65536
+    assert rows * cols > 2 ** 31 and rows * stride > 2 ** 32
+    wide = torch.empty(rows, stride, dtype=BF, device="cuda")
+    x, y = wide[:, :cols], wide[:, cols:]
+    few, w = randn(31, 2, cols).to(BF), randn(32, cols).to(BF)
+    x[:2], x[-2:] = few, few
+    dg.dg_rmsnorm(x, y, weight=w)
+    alone = torch.zeros_like(few)
+    dg.dg_rmsnorm(few, alone, weight=w)
+    assert torch.equal(y[:2], alone) and torch.equal(y[-2:], alone)
+    q, scale = torch.empty(rows, cols, dtype=torch.uint8, device="cuda"), torch.empty(rows, device="cuda")
+    dg.dg_rmsnorm_e4m3(x, q, scale, weight=w)
+    assert torch.equal(q[:2], q[-2:]) and torch.equal(scale[:2], scale[-2:])
+    check_codes(q[-2:], scale[-2:], norm64(few.double(), w.double(), 1e-6))
+    y[-2:] = few
+    dg.dg_rmsnorm_grad(x, y, y, weight=w)
+    dg.dg_rmsnorm_grad(few, few, alone, weight=w)
+    assert torch.equal(y[-2:], alone)
