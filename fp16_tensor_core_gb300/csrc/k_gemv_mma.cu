@@ -82,7 +82,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 
 // What the fused epilogue of a CTA's 16 columns of D reads, on its way through
 // asynchronous copies while B streams (read at the end instead, one load
-// after another, 4 x 4096 x 4096 took 0.7 us more).
+// after another, 4 x 4096 x 4096 took 6.65 us instead of 6.15).
 struct FusedOperands {
     float sa[16], sb[kRowsPerCta], bias[kRowsPerCta];
     uint32_t residual[16][kRowsPerCta / 2];   // two columns a word (N even)

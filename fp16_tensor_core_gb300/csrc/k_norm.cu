@@ -12,17 +12,23 @@
 // written, against some ten FP32 operations.  A block keeps a whole row in
 // registers between its two reductions (sum of squares, maximum), so each
 // element crosses memory once; blocks are persistent and have the next row's
-// loads in flight while a row is reduced and written.
+// loads in flight while a row is reduced and written.  BF16 with a residual to
+// codes, 16001 x 4096: 71.4 us, 0.95 of the rate of a copy; FP16 to codes of
+// one scale, 6001 x 8192: 32.5 us, 0.67 (2 bytes read and 1 written an element
+// leave the instructions as the bound: 65 % of the issue slots).
 //
 // Gradient, with u = s rsqrt(mean(s^2) + eps) and g = dy w:
 //   dx = rsqrt(..) (g - u mean(g u)) + dsum,   dw = sum over rows of dy u
 // dx belongs to x and to the residual alike.  A thread owns the same columns
 // of every row of its block, so dw is summed in registers and leaves the
 // block once; the blocks' sums are joined in order by a second kernel, so
-// that results do not depend on timing.
+// that results do not depend on timing.  BF16 with dsum and dw, 16384 x 4096:
+// 83.0 us, 0.95.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
@@ -35,17 +41,17 @@ namespace {
 // 32768 squares of 2^128 2^-80 hold, and one element at least was above 2^56.
 constexpr float kDown = 0x1p-80f;
 
-// Threads of a block, and blocks an SM at least, by vectors a thread: the
-// registers (64, 80, 128) hold a row and the next row's loads.
-template <int NV>
-constexpr int block_limit() { return NV == 4 ? 384 : 512; }
-template <int NV>
-constexpr int block_min() { return NV == 8 ? 1 : 2; }
-constexpr int kLimits[3] = {512, 384, 512};
-constexpr int kPerSm[3] = {1024, 768, 512};
+// A block's 1024 threads, or two blocks of 512 and more of fewer, at 64
+// registers: a row in FP32 and the next row's loads at two vectors a thread
+// (3000 x 16384 BF16 with residual, codes: 55.5 us, 0.91 of the rate of a
+// copy; four vectors of 512 threads at 128 registers 90.7); at four, past
+// 16384 columns, the row stays packed and is unpacked again for each pass, the
+// next one on its way to L2 (1500 x 24576: 55.8 us, 0.68; held in FP32 70.6).
+constexpr int kLimits[3] = {1024, 1024, 0};
+constexpr int kPerSm[3] = {1024, 1024, 0};
 
 template <int NV, bool kFp16, int kOut, bool kNarrow, bool kResidual>
-__global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_kernel(const NormArgs a, int team_size) {
+__global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_kernel(const NormArgs a, int team_size) {
     __shared__ float2 buffer[2][kRowThreads / 32];
     pdl_wait();
     const uint16_t* const weight = behind_wait(a.weight);
@@ -55,6 +61,7 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     // The weight, packed, in registers where they reach; else it is read again
     // for every row.
+    constexpr bool kKeep = NV == 2;
     constexpr bool kKeepWeight = NV == 2 && (kOut == kNormRows || (kOut == kNormTensor && !kResidual));
     uint4 x[NV], r[NV], w[NV];
 #pragma unroll
@@ -88,26 +95,43 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
         load_row(x_next, x);
         if constexpr (kResidual) load_row(r_next, r);
     }
-    if (!kResidual && first + team.row + step < a.rows) load_row(x_next += step * a.x_stride, r);
+    if (kKeep && !kResidual && first + team.row + step < a.rows) load_row(x_next += step * a.x_stride, r);
+    auto forget_all = [&] {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            forget(x[i]);
+            if constexpr (kResidual) forget(r[i]);
+        }
+    };
     for (; first < a.rows; first += step) {
         const int64_t row = first + team.row;
         const int end = row < a.rows ? vectors : 0;   // this thread's vectors lie below
-        pair v[NV][4], squares = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int at = team.at + i * team.size;
-            unpack8<kFp16>(x[i], v[i]);
+        if (!kKeep && threadIdx.x == 0 && row + step < a.rows) {
+            prefetch_row(x_next + step * a.x_stride, 2 * a.cols);
+            if constexpr (kResidual) prefetch_row(r_next + step * a.residual_stride, 2 * a.cols);
+        }
+        auto value = [&](int i, pair (&to)[4]) {   // s
+            unpack8<kFp16>(x[i], to);
             if constexpr (kResidual) {
                 pair add[4];
                 unpack8<kFp16>(r[i], add);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = pair_add(v[i][e], add[e]);
+                for (int e = 0; e < 4; ++e) to[e] = pair_add(to[e], add[e]);
             }
-            if (a.sum != nullptr) store_if(at < end, a.sum + row * a.sum_stride + 8 * at, pack8<kFp16>(v[i]));
+        };
+        pair v[kKeep ? NV : 1][4], squares = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) squares = pair_fma(v[i][e], v[i][e], squares);
+        for (int i = 0; i < NV; ++i) {
+            const int at = team.at + i * team.size;
+            pair (&t)[4] = v[kKeep ? i : 0];
+            value(i, t);
+            if (a.sum != nullptr) store_if(at < end, a.sum + row * a.sum_stride + 8 * at, pack8<kFp16>(t));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) squares = pair_fma(t[e], t[e], squares);
         }
-        if constexpr (kResidual) {
+        if constexpr (!kKeep) {
+            forget_all();
+        } else if constexpr (kResidual) {
             if (row + step < a.rows) {
                 load_row(x_next += step * a.x_stride, x);
                 load_row(r_next += step * a.residual_stride, r);
@@ -124,53 +148,77 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) rmsnorm_ke
             down = again ? kDown : 1.0f;
             squares = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                if constexpr (!kKeep) value(i, v[0]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const pair t = pair_mul(v[i][e], pair_of(down));
+                    const pair t = pair_mul(v[kKeep ? i : 0][e], pair_of(down));
                     squares = pair_fma(t, t, squares);
                 }
+            }
             total = reduce.sum(pair_sum(squares));
+            if constexpr (!kKeep) forget_all();
         }
         const float inv = rsqrtf(fmaf(total, inv_cols, a.eps * down * down)) * down;
+        auto normed = [&](int i, pair (&t)[4]) {   // y in place of s
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = pair_mul(t[e], pair_of(inv));
+            if (a.weight != nullptr) {
+                const int at = team.at + i * team.size;
+                pair f[4];
+                unpack8<kFp16>(kKeepWeight ? w[i] : weight_if(at < vectors, kKeep ? weight : behind_wait(weight), at), f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = pair_mul(t[e], f[e]);
+            }
+        };
+        auto emit = [&](int i, pair (&t)[4]) {
+            const int at = team.at + i * team.size;
+            if constexpr (kOut == kNormHalf) {
+                store_if(at < end, a.y + row * a.y_stride + 8 * at, pack8<kFp16>(t));
+            } else {
+                if constexpr (kOut == kNormTensor) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[e] = pair_mul(t[e], pair_of(pre));
+                }
+                store_if(at < end, q_row + 8 * at, codes8(t, by));
+            }
+        };
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(inv));
-            const int at = team.at + i * team.size;
-            if (a.weight != nullptr) {
-                pair f[4];
-                unpack8<kFp16>(kKeepWeight ? w[i] : weight_if(at < vectors, weight, at), f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], f[e]);
-            }
-            if (kOut != kNormHalf) top = top8(v[i], top);   // (zeros past the row)
+            pair (&t)[4] = v[kKeep ? i : 0];
+            if constexpr (!kKeep) value(i, t);
+            normed(i, t);
+            if (kOut != kNormHalf) top = top8(t, top);   // (zeros past the row)
+            if constexpr (!kKeep && kOut != kNormRows) emit(i, t);
         }
         if constexpr (kOut == kNormRows) {
             top = reduce.max1(top);
             by = row_factor(top);
             if (team.at == 0 && end != 0) a.row_scale[row] = row_scale(top);
+            if constexpr (!kKeep) forget_all();
         }
         if (kOut == kNormTensor && end != 0)   // (fmaxf would drop a NaN)
             tensor_top = __uint_as_float(max(__float_as_uint(tensor_top), __float_as_uint(top)));
+        if constexpr (kKeep || kOut == kNormRows) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int at = team.at + i * team.size;
-            if constexpr (kOut == kNormHalf) {
-                store_if(at < end, a.y + row * a.y_stride + 8 * at, pack8<kFp16>(v[i]));
-            } else {
-                if constexpr (kOut == kNormTensor) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[i][e] = pair_mul(v[i][e], pair_of(pre));
+            for (int i = 0; i < NV; ++i) {
+                pair (&t)[4] = v[kKeep ? i : 0];
+                if constexpr (!kKeep) {
+                    value(i, t);
+                    normed(i, t);
                 }
-                store_if(at < end, q_row + 8 * at, codes8(v[i], by));
+                emit(i, t);
             }
+        }
+        if (!kKeep && row + step < a.rows) {
+            load_row(x_next += step * a.x_stride, x);
+            if constexpr (kResidual) load_row(r_next += step * a.residual_stride, r);
         }
         if (kOut != kNormHalf) q_row += step * a.cols;
     }
     if constexpr (kOut == kNormTensor) {
-        // One atomic a block: a warp's each, on one address, took 5 us.
+        // One atomic a block.
         uint32_t* tops = reinterpret_cast<uint32_t*>(buffer);
         const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tensor_top));
         __syncthreads();
@@ -207,35 +255,97 @@ __global__ void next_scale_kernel(const float* amax, float* scale) {
     *scale = scale_of_amax(*amax);
 }
 
-// The gradient's blocks: at most 128 registers a thread for the elements as
-// they came, the columns' sums in FP32 and (two vectors a thread) the next
-// row's loads.
-constexpr int kGradLimits[3] = {512, 512, 512};
-constexpr int kGradPerSm[3] = {512, 512, 512};
+// The gradient's blocks: up to 512 threads at 128 registers (a row, the next
+// row's loads, the weight and the columns' sums).  Rows of more than 8192
+// columns are a cluster's of two or four blocks, each with its part of the
+// columns (BF16 with dw: 4000 x 11008 80.4 us, 3000 x 16384 77.8, 1500 x 24576
+// 71.0; four or eight vectors a thread of one block, with spills, 112.8, 104.8
+// and 181.1).
+constexpr int kGradThreads = 512, kGradPerSm = 512;
+constexpr int kGradColumns = 16 * kGradThreads;   // of a block
+constexpr int kGradRanks = kMaxRowElements / kGradColumns;   // at most, a cluster
+
+// Sums over a cluster's threads (each warp's value to every block, in one
+// buffer of two, taken in turn as RowReduce's).
+struct ClusterReduce {
+    float2 (*buffer)[kGradRanks * kGradThreads / 32];
+    int ranks, rank;
+    int turn = 0;
+
+    __device__ __forceinline__ float2 sum2(float a, float b) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        }
+        float2* buf = buffer[turn];
+        turn ^= 1;
+        if (lane < ranks)
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};"
+                         :: "r"(map_to_rank(buf + rank * warps + warp, static_cast<uint32_t>(lane))), "f"(a), "f"(b)
+                         : "memory");
+        cluster_sync_all_diverged();
+        const int n = ranks * warps;   // at most 64
+        const float2 zero = make_float2(0.0f, 0.0f);
+        const float2 u = lane < n ? buf[lane] : zero, v = lane + 32 < n ? buf[lane + 32] : zero;
+        a = u.x + v.x;
+        b = u.y + v.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        }
+        return make_float2(a, b);
+    }
+};
 
 // Columns' sums of a block: the teams of a warp and then the warps are added in
 // order; one partial a block.
-template <int NV, bool kFp16, bool kNarrow>
-__global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const NormGradArgs a,
-                                                                                         int team_size) {
-    __shared__ float2 buffer[2][kRowThreads / 32];
+enum GradRows : int { kWideRows, kNarrowRows, kClusterRows };
+template <bool kFp16, GradRows kRows>
+__global__ void __launch_bounds__(kGradThreads, kGradPerSm / kGradThreads) rmsnorm_grad_kernel(const NormGradArgs whole, int team_size) {
+    constexpr int NV = 2;
+    constexpr bool kNarrow = kRows == kNarrowRows, kCluster = kRows == kClusterRows;
+    using Reduce = std::conditional_t<kCluster, ClusterReduce, RowReduce<kNarrow>>;
+    __shared__ float2 buffer[2][kCluster ? kGradRanks * kGradThreads / 32 : kRowThreads / 32];
     __shared__ float columns[kNarrow ? 4 : 1][256];   // four warps' sums
+    // A cluster's block: the columns from `column` on.
+    NormGradArgs a = whole;
+    int vectors = a.cols >> 3, block = blockIdx.x, blocks = gridDim.x;
+    const RowTeam<kNarrow> team(team_size);
+    Reduce reduce{};
+    reduce.buffer = buffer;
+    if constexpr (kCluster) {
+        const int ranks = team_size, rank = static_cast<int>(cluster_ctarank()), each = (vectors + ranks - 1) / ranks;
+        const int column = 8 * each * rank;
+        a.x += column;
+        a.dy += column;
+        a.dx += column;
+        if (a.dsum != nullptr) a.dsum += column;
+        if (a.weight != nullptr) a.weight += column;
+        if (a.partials != nullptr) a.partials += column;
+        vectors = min(each, vectors - each * rank);
+        block /= ranks;
+        blocks /= ranks;
+        reduce.ranks = ranks;
+        reduce.rank = rank;
+        cluster_sync_all();   // every block has started: its shared memory may be written
+    } else {
+        reduce.size = team.size;
+    }
     pdl_wait();
     const uint16_t* const weight = behind_wait(a.weight);
-    const RowTeam<kNarrow> team(team_size);
-    RowReduce<kNarrow> reduce{buffer, team.size};
-    const int vectors = a.cols >> 3;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
-    // Two vectors a thread: the next row's x and dy are loaded ahead, and the
-    // packed weight stays in registers.
-    constexpr bool kAhead = NV == 2;
+    // The next row's x and dy are loaded ahead, and the packed weight stays in
+    // registers.
     pair dw[NV][4];
     uint4 next_x[NV], next_d[NV], add[NV], w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int at = team.at + i * team.size;
         next_x[i] = next_d[i] = add[i] = make_uint4(0, 0, 0, 0);
-        if (kAhead) w[i] = weight_if(a.weight != nullptr && at < vectors, weight, at);
+        w[i] = weight_if(a.weight != nullptr && at < vectors, weight, at);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw[i][e] = 0;
     }
@@ -247,8 +357,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
             load_if(at < vectors, d_row + 8 * at, next_d[i]);
         }
     };
-    const int64_t step = static_cast<int64_t>(gridDim.x) * team.rows;
-    int64_t first = static_cast<int64_t>(blockIdx.x) * team.rows;
+    const int64_t step = static_cast<int64_t>(blocks) * team.rows;
+    int64_t first = static_cast<int64_t>(block) * team.rows;
     const uint16_t* x_next = a.x + (first + team.row) * a.x_stride;
     const uint16_t* d_next = a.dy + (first + team.row) * a.dy_stride;
     if (first + team.row < a.rows) fetch(x_next, d_next);
@@ -266,20 +376,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
         }
         x_next += step * a.x_stride;
         d_next += step * a.dy_stride;
-        if (kAhead && row + step < a.rows) fetch(x_next, d_next);
-        const int64_t later = row + (kAhead ? 2 : 1) * step;
+        if (row + step < a.rows) fetch(x_next, d_next);
+        const int64_t later = row + 2 * step;
         if (!kNarrow && threadIdx.x == 0) {
             if (later < a.rows) {
-                prefetch_row(a.x + later * a.x_stride, 2 * a.cols);
-                prefetch_row(a.dy + later * a.dy_stride, 2 * a.cols);
+                prefetch_row(a.x + later * a.x_stride, 16 * vectors);
+                prefetch_row(a.dy + later * a.dy_stride, 16 * vectors);
             }
-            if (a.dsum != nullptr && row + step < a.rows) prefetch_row(a.dsum + (row + step) * a.dsum_stride, 2 * a.cols);
+            if (a.dsum != nullptr && row + step < a.rows) prefetch_row(a.dsum + (row + step) * a.dsum_stride, 16 * vectors);
         }
         // g = dy w
         auto g_of = [&](int i, const pair (&dy)[4], pair (&g)[4]) {
-            const int at = team.at + i * team.size;
             if (a.weight != nullptr) {
-                unpack8<kFp16>(kAhead ? w[i] : weight_if(at < vectors, weight, at), g);
+                unpack8<kFp16>(w[i], g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) g[e] = pair_mul(g[e], dy[e]);
             } else {
@@ -341,11 +450,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_grad_kernel(const Norm
             }
             store_if(at < end, dx_row + 8 * at, pack8<kFp16>(g));
         }
-        if (!kAhead && row + step < a.rows) fetch(x_next, d_next);
     }
     if (a.partials == nullptr) return;
     pdl_launch_dependents();   // the join's launch
-    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
+    float* part = a.partials + static_cast<int64_t>(block) * a.cols;
     if constexpr (!kNarrow) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -429,29 +537,75 @@ template <bool kFp16>
 cudaError_t run_norm(const NormArgs& a, int out, const RowPlan& p, cudaStream_t s) {
     if (p.narrow) return run_norm_rows<2, kFp16, true>(a, out, p, s);
     if (p.each == 2) return run_norm_rows<2, kFp16, false>(a, out, p, s);
-    if (p.each == 4) return run_norm_rows<4, kFp16, false>(a, out, p, s);
-    return run_norm_rows<8, kFp16, false>(a, out, p, s);
+    return run_norm_rows<4, kFp16, false>(a, out, p, s);
 }
 
-RowPlan grad_plan(int64_t rows, int cols, int sm_count) {
-    return row_plan(rows, cols, sm_count, kGradLimits, kGradPerSm);
+// p.blocks: of rows, or clusters of `ranks` blocks.
+struct GradPlan {
+    RowPlan p;
+    int ranks;
+};
+GradPlan grad_plan(int64_t rows, int cols, int sm_count) {
+    constexpr int kLimits2[3] = {kGradThreads, 0, 0}, kPerSm2[3] = {kGradPerSm, 0, 0};
+    if (cols <= kGradColumns) return {row_plan(rows, cols, sm_count, kLimits2, kPerSm2), 1};
+    int ranks = 2;
+    while (ranks * kGradColumns < cols) ranks *= 2;
+    const int each = (cols / 8 + ranks - 1) / ranks;   // vectors of a block
+    GradPlan g{{}, ranks};
+    g.p.each = 2;
+    g.p.team = g.p.threads = ((each + 1) / 2 + 31) / 32 * 32;
+    const int64_t resident = std::max(1, sm_count * (kGradPerSm / g.p.threads) / ranks);
+    g.p.blocks = static_cast<int>(std::min<int64_t>(rows, resident));
+    return g;
+}
+
+// No more clusters than are resident at once (a GPC's last SMs may be too few
+// for one; two clusters left over for a second round doubled the time).
+template <bool kFp16>
+cudaError_t fit_clusters(GradPlan* g) {
+    constexpr int kDevices = 64, kSizes = kGradThreads / 32 + 1;
+    static std::atomic<int> known[kDevices][kGradRanks + 1][kSizes];
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>* const cell = dev < kDevices ? &known[dev][g->ranks][g->p.threads / 32] : nullptr;
+    if (cell != nullptr) n = cell->load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(g->ranks);
+        cfg.blockDim = dim3(g->p.threads);
+        cudaLaunchAttribute ranks;
+        ranks.id = cudaLaunchAttributeClusterDimension;
+        ranks.val.clusterDim.x = static_cast<unsigned>(g->ranks);
+        ranks.val.clusterDim.y = ranks.val.clusterDim.z = 1;
+        cfg.attrs = &ranks;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, rmsnorm_grad_kernel<kFp16, kClusterRows>, &cfg);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
+        if (cell != nullptr) cell->store(n, std::memory_order_relaxed);
+    }
+    g->p.blocks = std::min(g->p.blocks, n);
+    return cudaSuccess;
 }
 
 template <bool kFp16>
-cudaError_t run_grad(const NormGradArgs& a, const RowPlan& p, cudaStream_t s) {
-    const dim3 grid(p.blocks), block(p.threads);
-    if (p.narrow) return launch_kernel(rmsnorm_grad_kernel<2, kFp16, true>, grid, block, 0, s, a, p.team);
-    if (p.each == 2) return launch_kernel(rmsnorm_grad_kernel<2, kFp16, false>, grid, block, 0, s, a, p.team);
-    if (p.each == 4) return launch_kernel(rmsnorm_grad_kernel<4, kFp16, false>, grid, block, 0, s, a, p.team);
-    return launch_kernel(rmsnorm_grad_kernel<8, kFp16, false>, grid, block, 0, s, a, p.team);
+cudaError_t run_grad(const NormGradArgs& a, const GradPlan& g, cudaStream_t s) {
+    const dim3 grid(g.p.blocks), block(g.p.threads);
+    if (g.ranks > 1)
+        return launch_clusters(rmsnorm_grad_kernel<kFp16, kClusterRows>, dim3(g.p.blocks * g.ranks), block, g.ranks, 0, s,
+                               a, g.ranks);
+    if (g.p.narrow) return launch_kernel(rmsnorm_grad_kernel<kFp16, kNarrowRows>, grid, block, 0, s, a, g.p.team);
+    return launch_kernel(rmsnorm_grad_kernel<kFp16, kWideRows>, grid, block, 0, s, a, g.p.team);
 }
 
 }  // namespace
 
 cudaError_t launch_join_columns(const float* partials, int parts, int cols, float* out, cudaStream_t s) {
-    // 128 columns a block for wide sums (110 parts of 22016: 2.2 times as fast
-    // as 32); 32 for those that would leave SMs idle, with fewer threads where
-    // there is little to add (63 parts of 2000: 0.8 us).
+    // 128 columns a block for wide sums (512 bytes of a part side by side); 32
+    // for those that would leave SMs idle, with fewer threads where there is
+    // little to add (the activation gradient of 63 x 2000 with dbias: 4.6 -> 3.7
+    // us).
     if (cols >= 8192)
         return launch_kernel(join_columns_kernel<32, 1024>, dim3((cols + 127) / 128), dim3(1024), 0, s, partials, parts,
                              cols, out);
@@ -484,16 +638,20 @@ cudaError_t launch_rmsnorm(const NormArgs& args, int out, bool fp16, int sm_coun
 }
 
 int64_t rmsnorm_grad_scratch_bytes(int64_t rows, int cols, int sm_count) {
-    return static_cast<int64_t>(grad_plan(rows, cols, sm_count).blocks) * cols * 4;
+    return static_cast<int64_t>(grad_plan(rows, cols, sm_count).p.blocks) * cols * 4;
 }
 
 cudaError_t launch_rmsnorm_grad(const NormGradArgs& a, bool fp16, float* dweight, int sm_count, cudaStream_t s) {
-    const RowPlan p = grad_plan(a.rows, a.cols, sm_count);
-    if (a.rows > 0) {
-        const cudaError_t e = fp16 ? run_grad<true>(a, p, s) : run_grad<false>(a, p, s);
+    GradPlan g = grad_plan(a.rows, a.cols, sm_count);
+    if (g.ranks > 1 && a.rows > 0) {
+        const cudaError_t e = fp16 ? fit_clusters<true>(&g) : fit_clusters<false>(&g);
         if (e != cudaSuccess) return e;
     }
-    return dweight == nullptr ? cudaSuccess : launch_join_columns(a.partials, p.blocks, a.cols, dweight, s);
+    if (a.rows > 0) {
+        const cudaError_t e = fp16 ? run_grad<true>(a, g, s) : run_grad<false>(a, g, s);
+        if (e != cudaSuccess) return e;
+    }
+    return dweight == nullptr ? cudaSuccess : launch_join_columns(a.partials, g.p.blocks, a.cols, dweight, s);
 }
 
 }  // namespace dg

@@ -15,10 +15,10 @@
 
 namespace dg {
 
-constexpr int kRowThreads = 512;   // at most, a row
+constexpr int kRowThreads = 1024;   // at most, a row
 
 // Rows too wide for the vectors of one block are refused.
-constexpr int kRowVectors = 8;     // at most, a thread
+constexpr int kRowVectors = 4;     // at most, a thread
 static_assert(kRowThreads * kRowVectors * 8 == kMaxRowElements, "widest row");
 
 // Eight elements as four pairs.
@@ -69,7 +69,7 @@ __device__ __forceinline__ void decode8(uint2 q, float by, pair (&f)[4]) {
 }
 
 // 16 (8) bytes that no other block reads, where `take`; else what was there.
-// Predicated: as branches, these took a third of a narrow row's instructions.
+// Predicated, without branches in a row's loop.
 // Not the read-only path: an output may be the input itself.
 __device__ __forceinline__ void load_if(bool take, const void* p, uint4& v) {
     asm volatile("{\n\t.reg .pred q;\n\t"
@@ -118,7 +118,7 @@ __device__ __forceinline__ uint4 weight_if(bool take, const uint16_t* weight, in
 }
 
 // A row to come moves into L2 (one thread; 16-byte aligned, a multiple of 16
-// bytes): no registers, and the loads that follow wait a third as long.
+// bytes): no registers are held meanwhile.
 __device__ __forceinline__ void prefetch_row(const void* p, int bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p), "r"(bytes) : "memory");
 }
@@ -178,10 +178,7 @@ struct RowReduce {
         } else {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            a = exchange(make_float2(a, 0.0f)).x;
-#pragma unroll
-            for (int o = kRowThreads / 64; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            return a;
+            return tree(exchange(make_float2(a, 0.0f)).x);
         }
     }
     __device__ __forceinline__ float2 sum2(float a, float b) {
@@ -194,14 +191,7 @@ struct RowReduce {
                 b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
             }
             const float2 t = exchange(make_float2(a, b));
-            a = t.x;
-            b = t.y;
-#pragma unroll
-            for (int o = kRowThreads / 64; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-            }
-            return make_float2(a, b);
+            return make_float2(tree(t.x), tree(t.y));
         }
     }
 
@@ -226,17 +216,23 @@ private:
         for (int o = size >> 1; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
         return __uint_as_float(v);
     }
-    // Every warp's value to every warp: lanes i and i + 16 get warp i's (or zeros).
+    // The sum of what exchange gave.
+    static __device__ __forceinline__ float tree(float a) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        return a;
+    }
+    // Every warp's value to every warp: lane i gets warp i's (or zero).
     __device__ __forceinline__ float2 exchange(float2 v) {
         float2* buf = buffer[turn];
         turn ^= 1;
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
-        const unsigned from = threadIdx.x & 15;
+        const unsigned from = threadIdx.x & 31;
         return from < blockDim.x >> 5 ? buf[from] : make_float2(0.0f, 0.0f);
     }
 };
-static_assert(kRowThreads / 32 == 16, "exchange");
+static_assert(kRowThreads / 32 == 32, "exchange");
 
 __device__ __forceinline__ float pair_sum(pair v) {
     const float2 f = floats_of(v);
