@@ -39,7 +39,10 @@ template <int NV>
 constexpr int block_limit() { return NV == 4 ? 384 : 512; }
 template <int NV>
 constexpr int block_min() { return NV == 8 ? 1 : 2; }
-constexpr int kLimits[3] = {512, 384, 512};
+// Codes wait for a row's maximum: smaller blocks, and more of them to an SM,
+// keep it busy meanwhile (4000 x 8192 BF16 ungated to codes 23.6 -> 20.8 us,
+// with checkpoint 30.7 -> 26.6; without codes 22.6 -> 23.0).
+constexpr int kLimits[3] = {512, 384, 512}, kCodeLimits[3] = {256, 384, 512};
 constexpr int kPerSm[3] = {1024, 768, 512};
 
 template <int NV, bool kFp16, bool kGated, bool kNarrow>
@@ -300,7 +303,8 @@ cudaError_t run_act_grad(const ActGradArgs& a, const ActGradPlan& p, cudaStream_
 }  // namespace
 
 cudaError_t launch_activate(const ActArgs& a, bool fp16, int sm_count, cudaStream_t s) {
-    const RowPlan p = row_plan(a.rows, a.cols, sm_count, kLimits, kPerSm);
+    const bool codes = a.q != nullptr || a.x_q != nullptr;
+    const RowPlan p = row_plan(a.rows, a.cols, sm_count, codes ? kCodeLimits : kLimits, kPerSm);
     return fp16 ? run_act<true>(a, p, s) : run_act<false>(a, p, s);
 }
 
