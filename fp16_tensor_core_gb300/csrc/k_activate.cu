@@ -156,16 +156,20 @@ constexpr int kGradResident = 7;    // blocks an SM (with 8, 64 registers: 1 to 
 constexpr int kGradThreads = 128;
 constexpr int kGradAcross = 32;     // threads side by side at most: a warp's 512 bytes of a row
 
-template <bool kFp16, bool kGated, bool kCodes>
-__global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_kernel(const ActGradArgs a, int across) {
+// kJoin: the runs are the blocks of a cluster, which add up the columns' sums
+// themselves (ranks of them; dbias in place of partials).
+template <bool kFp16, bool kGated, bool kCodes, bool kJoin>
+__global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_kernel(const ActGradArgs a, int across,
+                                                                                    int ranks) {
     __shared__ float4 columns[kGradThreads][4];   // the threads' sums
     pdl_wait();
     constexpr int kHalves = kGated ? 2 : 1;
     // `across` threads (a power of two) side by side, the others on other rows
     const int t = threadIdx.x, down = kGradThreads / across;
-    const int c = 8 * static_cast<int>(blockIdx.x * across + (t & (across - 1)));
+    const int run = kJoin ? static_cast<int>(cluster_ctarank()) : blockIdx.y, runs = kJoin ? ranks : gridDim.y;
+    const int c = 8 * static_cast<int>((kJoin ? blockIdx.x / ranks : blockIdx.x) * across + (t & (across - 1)));
     const int64_t width = static_cast<int64_t>(kHalves) * a.cols;
-    const int64_t step = static_cast<int64_t>(gridDim.y) * down;
+    const int64_t step = static_cast<int64_t>(runs) * down;
     pair sums[kHalves][4];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
                 }
             }
         };
-        int64_t row = static_cast<int64_t>(blockIdx.y) * down + t / across;
+        int64_t row = static_cast<int64_t>(run) * down + t / across;
         if (row < a.rows) fetch(row);
 #pragma unroll 1
         for (; row < a.rows; row += step) {
@@ -235,25 +239,48 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident) activate_grad_ker
             }
         }
     }
-    if (a.partials == nullptr) return;
-    pdl_launch_dependents();   // the join's launch
-    float* part = a.partials + blockIdx.y * width;
+    if (!kJoin && a.partials == nullptr) return;
+    if (!kJoin) pdl_launch_dependents();   // the join's launch
+    float* part = a.partials + (kJoin ? 0 : run * width);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) store_sums(reinterpret_cast<float*>(&columns[t][2 * h]), sums[h]);
     __syncthreads();
     // thread t of the first row adds up what lies below it, in order
-    if (t >= across || c >= a.cols) return;
+    const bool mine = t < across && c < a.cols;
+    auto add = [](float4& s, const float4& v) {
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    };
+    if (mine) {
 #pragma unroll
-    for (int i = 0; i < 2 * kHalves; ++i) {
-        float4 s = columns[t][i];
-        for (int r = 1; r < down; ++r) {
-            const float4 v = columns[t + r * across][i];
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+        for (int i = 0; i < 2 * kHalves; ++i) {
+            float4 s = columns[t][i];
+            for (int r = 1; r < down; ++r) add(s, columns[t + r * across][i]);
+            if (kJoin)
+                columns[t][i] = s;
+            else
+                *reinterpret_cast<float4*>(part + static_cast<int64_t>(i >> 1) * a.cols + c + 4 * (i & 1)) = s;
         }
-        *reinterpret_cast<float4*>(part + static_cast<int64_t>(i >> 1) * a.cols + c + 4 * (i & 1)) = s;
+    }
+    if constexpr (kJoin) {
+        cluster_sync_all_diverged();
+        if (run == 0 && mine) {
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                float4 s = columns[t][i];
+                for (int r = 1; r < runs; ++r) {
+                    float4 v;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                                 : "r"(map_to_rank(&columns[t][i], static_cast<uint32_t>(r))));
+                    add(s, v);
+                }
+                *reinterpret_cast<float4*>(part + static_cast<int64_t>(i >> 1) * a.cols + c + 4 * (i & 1)) = s;
+            }
+        }
+        cluster_sync_all_diverged();   // no block leaves while another reads its sums
     }
 }
 
@@ -279,25 +306,52 @@ cudaError_t run_act(const ActArgs& a, const RowPlan& p, cudaStream_t s) {
 // thread (100000 x 8, gated with dbias: 9.6 us, 11.2 without this; 4096 x 256:
 // 6.9, 7.6; 22397 x 64: 8.6, 8.1).
 struct ActGradPlan {
-    int across, columns, runs;
+    int across, columns, runs, down;
 };
 ActGradPlan act_grad_plan(int64_t rows, int cols, int sm_count) {
-    ActGradPlan p{1, 1, 1};
+    ActGradPlan p{1, 1, 1, 1};
     const int vectors = cols / 8;
     while (p.across < kGradAcross && p.across < vectors) p.across *= 2;
     p.columns = (vectors + p.across - 1) / p.across;
-    const int down = kGradThreads / p.across;
+    p.down = kGradThreads / p.across;
     const int64_t runs = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * kGradResident / p.columns);
-    const int64_t few = std::max<int64_t>(256, rows / (8 * down));
-    p.runs = static_cast<int>(std::min({(rows + down - 1) / down, runs, few}));
+    const int64_t few = std::max<int64_t>(256, rows / (8 * p.down));
+    p.runs = static_cast<int>(std::min({(rows + p.down - 1) / p.down, runs, few}));
     return p;
 }
 
+// dbias of few rows: as many runs as a cluster has blocks, and no second
+// kernel, while each thread has one row (11008 gated, 1 row: 4.6 -> 2.2 us, 16
+// rows 5.3 -> 4.8) or, where the blocks are no more than the SMs, two: that
+// takes 0.3 to 0.5 us more by itself (63 x 2000: 3.3 -> 3.6), but one launch
+// less, which is what calls that are not replayed from a graph wait for (6.9
+// -> 5.1 us a call).
+constexpr int kJoinRanks = 8;
+bool join_in_cluster(const ActGradPlan& p, int64_t rows, int sm_count) {
+    return rows <= (p.columns * kJoinRanks <= sm_count ? 2 : 1) * kJoinRanks * p.down;
+}
+
+template <bool kFp16, bool kGated, bool kCodes>
+cudaError_t run_act_grad_from(const ActGradArgs& a, float* dbias, const ActGradPlan& p, int sm_count, cudaStream_t s) {
+    const dim3 block(kGradThreads);
+    if (dbias != nullptr && join_in_cluster(p, a.rows, sm_count)) {
+        int ranks = 1;
+        while (ranks < kJoinRanks && ranks * p.down < a.rows) ranks *= 2;
+        ActGradArgs b = a;
+        b.partials = dbias;
+        return launch_clusters(activate_grad_kernel<kFp16, kGated, kCodes, true>, dim3(p.columns * ranks), block, ranks, 0,
+                               s, b, p.across, ranks);
+    }
+    const cudaError_t e = launch_kernel(activate_grad_kernel<kFp16, kGated, kCodes, false>, dim3(p.columns, p.runs), block,
+                                        0, s, a, p.across, 1);
+    if (e != cudaSuccess || dbias == nullptr) return e;
+    return launch_join_columns(a.partials, p.runs, kGated ? 2 * a.cols : a.cols, dbias, s);
+}
+
 template <bool kFp16, bool kGated>
-cudaError_t run_act_grad(const ActGradArgs& a, const ActGradPlan& p, cudaStream_t s) {
-    const dim3 grid(p.columns, p.runs), block(kGradThreads);
-    return a.x_q != nullptr ? launch_kernel(activate_grad_kernel<kFp16, kGated, true>, grid, block, 0, s, a, p.across)
-                            : launch_kernel(activate_grad_kernel<kFp16, kGated, false>, grid, block, 0, s, a, p.across);
+cudaError_t run_act_grad(const ActGradArgs& a, float* dbias, const ActGradPlan& p, int sm_count, cudaStream_t s) {
+    return a.x_q != nullptr ? run_act_grad_from<kFp16, kGated, true>(a, dbias, p, sm_count, s)
+                            : run_act_grad_from<kFp16, kGated, false>(a, dbias, p, sm_count, s);
 }
 
 }  // namespace
@@ -314,13 +368,10 @@ int64_t activate_grad_scratch_bytes(int64_t rows, int cols, bool gated, int sm_c
 
 cudaError_t launch_activate_grad(const ActGradArgs& a, bool fp16, float* dbias, int sm_count, cudaStream_t s) {
     const ActGradPlan p = act_grad_plan(a.rows, a.cols, sm_count);
-    if (a.rows > 0) {
-        const cudaError_t e = fp16 ? (a.gated ? run_act_grad<true, true>(a, p, s) : run_act_grad<true, false>(a, p, s))
-                                   : (a.gated ? run_act_grad<false, true>(a, p, s) : run_act_grad<false, false>(a, p, s));
-        if (e != cudaSuccess) return e;
-    }
-    return dbias == nullptr ? cudaSuccess
-                            : launch_join_columns(a.partials, p.runs, a.gated ? 2 * a.cols : a.cols, dbias, s);
+    if (a.rows == 0)
+        return dbias == nullptr ? cudaSuccess : launch_join_columns(nullptr, 0, a.gated ? 2 * a.cols : a.cols, dbias, s);
+    if (fp16) return a.gated ? run_act_grad<true, true>(a, dbias, p, sm_count, s) : run_act_grad<true, false>(a, dbias, p, sm_count, s);
+    return a.gated ? run_act_grad<false, true>(a, dbias, p, sm_count, s) : run_act_grad<false, false>(a, dbias, p, sm_count, s);
 }
 
 }  // namespace dg

@@ -596,8 +596,8 @@ typedef enum {
 /* The activation between two products:
  *   y = act(x)   or, gated,   y = act(x[:, :cols]) * x[:, cols:]
  * in FP32 (NaN stays NaN; DG_ACT_SILU and DG_ACT_GELU_TANH give NaN at
- * -infinity, and results below 2^-126 |x| may be 0).  Any of the three outputs may be left out
- * (NULL):
+ * -infinity, and values of act(x) below 2^-126 |x| may be 0).  Any of the
+ * three outputs may be left out (NULL):
  *   x        rows x cols of dtype, or rows x 2 cols when gated.
  *   y        rows x cols of dtype; may be x itself when not gated.
  *   q, q_scale  y as codes uint8[rows][cols] and FP32[rows].
