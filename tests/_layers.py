@@ -69,8 +69,9 @@ def act64(x, act):
 # The logistic forms: an exponential whose argument u is off by 2^-23 |u|, a
 # reciprocal and products; |u| stays below 32 in the tests (x below 12, where
 # the tanh form's u is larger but its value is x or 0 to FP32's last bits), so
-# 2^-23 32 + 2^-20 < 2^-17.  GELU: erfc at z = |x| / sqrt 2 <= 8.5 magnifies the
-# error of its argument by 2 z^2 < 2^7.2 : 2^-24 2^7.2 + 2^-21 < 2^-16.
+# 2^-23 32 + 2^-20 < 2^-17.  GELU: exp(-x^2 / 2)
+# with x^2 / 2 <= 72 of two roundings, 2^-23 72 < 2^-16.8, a polynomial of
+# relative error 5.2e-7 < 2^-20.8 and a few roundings more: below 2^-16.
 ACT = 2.0 ** -16
 # Reciprocals below 2^-126 are 0: values below that times |x| <= 12 are lost.
 ACT_TINY = 2.0 ** -122
