@@ -30,7 +30,7 @@ SOURCES = ["dg_api.cu", "k_scale.cu", "k_gemv.cu", "k_gemv_mma.cu", "k_gemm_tc.c
            "k_gemm_tc_fused.cu", "k_gemm_tc2_fused.cu", "k_gemm_skinny_fused.cu", "k_epilogue.cu"]
 HEADERS = ["dg_ptx.cuh", "dg_internal.h", "gemm_common.cuh", "attn_common.cuh", "prefix_barriers.h",
            "activation.cuh", "row_common.cuh", "gemm_tc_kernel.cuh", "gemm_pair_kernel.cuh",
-           "gemm_skinny_kernel.cuh"]
+           "gemm_skinny_kernel.cuh", "gemm_smem.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

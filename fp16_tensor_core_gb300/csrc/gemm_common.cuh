@@ -13,6 +13,7 @@
 #include "activation.cuh"
 #include "dg_internal.h"
 #include "dg_ptx.cuh"
+#include "gemm_smem.h"
 
 namespace dg {
 
@@ -71,24 +72,13 @@ cudaError_t launch_gemm_tc_fused(const TcLaunch& L, const Params& prm, cudaStrea
 namespace {
 
 constexpr int kThreads = 256;   // warps: 0 TMA, 1 MMA, 2 TMEM owner, 3 idle, 4-7 epilogue
-// The fused tiled kernels have eight epilogue warps (4-11): two take the 32
-// columns of a chunk in turn, so that one's arithmetic runs while the other
-// waits for its loads and stores.  With four the epilogue was longer than the
-// main loop at K = 4096 (4096 x 11008 x 4096 E4M3, SiLU and bias: 139 us,
-// with eight 128).
-constexpr int epilogue_warps(bool fused) { return fused ? 8 : 4; }
 constexpr int gemm_threads(bool fused) { return 128 + 32 * epilogue_warps(fused); }
-constexpr int kBKBytes = 128;   // one 128-byte swizzle row of K per stage
 
 constexpr uint32_t pow2_at_least(uint32_t v) {
     uint32_t p = 32;
     while (p < v) p <<= 1;
     return p;
 }
-
-// Shared memory per CTA available to a kernel (227 KB).
-constexpr int kSmemLimit = 232448;
-
 
 __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int group_m, int& mt,
                                             int& nt) {
@@ -171,7 +161,6 @@ __device__ __forceinline__ uint32_t store_chunk(const Params& p, int row, int ro
 // expects (64-byte swizzle for 2-byte outputs, 32-byte for E4M3) and writes
 // it with one bulk tensor store, which moves whole lines and clips rows >= M
 // and columns >= N.
-constexpr int kBoxBytes = 2048;   // 32 x 32 two-byte elements (E4M3 uses half)
 
 // Thread `lane` converts one row's 32 values into its line of `box`.
 __device__ __forceinline__ void stage_values(const Params& p, uint8_t* box, const float (&v)[32],
@@ -317,15 +306,9 @@ __device__ __forceinline__ void store_box_odd(const Params& p, uint8_t* box, int
     __syncwarp();   // before the box is written again
 }
 
-// What a fused epilogue warp holds of its chunks of a tile in shared memory:
-// each column's scale of B and bias, as pairs of columns {scale, scale, bias,
-// bias} so that one 16-byte read serves two columns.  Loaded while the main
-// loop runs; columns past N get zeros.
-constexpr int kColumnFloats = 64;   // of a chunk
-constexpr int fused_chunks(int bn) { return (bn / 32 + 1) / 2; }   // a warp's, at most
-constexpr int columns_bytes(int bn) { return epilogue_warps(true) * fused_chunks(bn) * kColumnFloats * 4; }
-
-// Chunks first, first + 2, ... of the tile whose columns start at col0.
+// The columns' scales of B and biases (laid out as kColumnFloats says) into
+// shared memory while the main loop runs, zeros past N: chunks first, first +
+// 2, ... of the tile whose columns start at col0.
 template <int BN>
 __device__ __forceinline__ void stage_columns(const Params& p, float* columns, int col0, int first, int lane) {
     constexpr int kChunks = fused_chunks(BN);

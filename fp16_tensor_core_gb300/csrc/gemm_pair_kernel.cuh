@@ -16,20 +16,7 @@ namespace {
 
 constexpr int kPairBM = 256;   // output rows of a pair tile
 constexpr uint32_t kEpiBarrier = 1;   // named barrier of the epilogue warps
-constexpr int kHalfBM = 128;   // rows of it per CTA
-
-// Staging boxes of the epilogue: one 32 x 32 box per epilogue warp.
-constexpr int pair_staging_bytes(bool fused) { return epilogue_warps(fused) * kBoxBytes; }
-
-// Stage count: what fits in 227 KB beside the barrier block (1 KB, keeping
-// the staging boxes 1024-byte aligned), the staging boxes and a fused
-// epilogue's columns, at most 8
-// (4 with two K blocks per stage).
-constexpr int pair_stages_for(int bn, int kps = 1, bool fused = false) {
-    const int st = (kSmemLimit - 1024 - 1024 - pair_staging_bytes(fused) - (fused ? columns_bytes(bn) : 0)) /
-                   (kps * (kHalfBM * kBKBytes + (bn / 2) * kBKBytes));
-    return st > 8 / kps ? 8 / kps : st;
-}
+constexpr int kHalfBM = kPairRows;   // rows of it per CTA
 
 // KPS: K blocks per pipeline stage (1 or 2, adjacent blocks loaded together).
 template <int BN, int STAGES, bool kFp16In, int KPS = 1, bool kFused = false>
@@ -41,6 +28,7 @@ struct PairCfg {
     static constexpr int kABytes = KPS * kABox;
     static constexpr int kBBytes = KPS * kBBox;
     static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kRingBytes = STAGES * kStageBytes;
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * BN);
     static constexpr int kStagingOff = STAGES * kStageBytes + 1024;   // after the barriers
     static constexpr int kColumnsOff = kStagingOff + pair_staging_bytes(kFused);   // fused: its columns' scales, bias
@@ -339,15 +327,16 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         uint32_t acc_phase = 0;
         const int r_local = q * 32 + lane;   // this thread's row of the CTA's 128
         constexpr int kSlotF4 = BN / 4 * kHalfBM;   // float4s of one partial tile
-        constexpr int kSlotBytes = kSlotF4 * 16;
+        constexpr int kSlotBytes = pair_partial_bytes(BN);
         constexpr int kCopyPiece = 16384;           // bulk copies of 16 KB
         static_assert(kSlotBytes % kCopyPiece == 0, "partial tile in whole pieces");
-        static_assert(STAGES * C::kStageBytes >= kSlotBytes + 4 * (BN / 32) * kBoxBytes,
+        static_assert(kSlotBytes == kSlotF4 * 16, "partial tile");
+        static_assert(pair_parts_in_ring(C::kRingBytes, BN, 2),
                       "a partial tile and every output box of a tile fit in the ring");
-        // every other part's partial tile fits in the idle ring: staged loads
+        // every other part's partial tile and the output boxes fit in the idle
+        // ring: staged loads
         const int nparts = parts_of(p.tail_split);   // K ranges of a split tile
-        const bool staged_parts =
-            static_cast<int64_t>(nparts - 1) * kSlotBytes <= STAGES * C::kStageBytes;
+        const bool staged_parts = pair_parts_in_ring(C::kRingBytes, BN, nparts);
         PairItem it;
         for (int i = 0; pair_item(i, pair, npairs, num_tiles, num_kb, p.tail_split, it); ++i) {
             int mt, nt;
@@ -477,8 +466,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 // the CTA's last item, whose ring of stages is idle, every
                 // box has a place of its own in the ring (after any staged
                 // partial tiles), so the stores go out back to back.
-                const int ring_base = (it.part == 0 && staged_parts)
-                                          ? (nparts - 1) * kSlotBytes : 0;
+                const int ring_base = it.part == 0 ? pair_boxes_at(C::kRingBytes, BN, nparts) : 0;
 #pragma unroll 1
                 for (int c = half; c < BN / 32; c += kChunkStep) {
                     uint32_t r[32];
@@ -665,7 +653,7 @@ cudaError_t launch_pair_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s
         const int rem = L.plan->tiles % pairs;
         const int num_kb = (L.K + C::kBK - 1) / C::kBK;
         int split = rem > 0 ? pairs / rem : 0;
-        if (split > 4) split = 4;
+        if (split > kPairMaxParts) split = kPairMaxParts;
         const size_t need = static_cast<size_t>(rem) * (split > 1 ? split - 1 : 0) * 2 * BN *
                             kHalfBM * sizeof(float);
         if (split >= 2 && num_kb >= split && need <= L.tail_ws_bytes &&
@@ -673,6 +661,9 @@ cudaError_t launch_pair_cfg(const TcLaunch& L, const Params& prm, cudaStream_t s
             prm2.tail_split = split;
             prm2.tail_ws = L.tail_ws;
             prm2.tail_counts = L.tail_counts;
+            if (knobs().log)
+                std::fprintf(stderr, "[dg] pair GEMM %dx%dx%d: %d tiles on %d pairs, the last %d in %d K ranges\n",
+                             L.M, L.N, L.K, L.plan->tiles, pairs, rem, split);
         }
     }
     // Output map of the staged epilogue (else the epilogue stores directly).
