@@ -87,14 +87,14 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) forget(x[h][i]);
-            const float halves[2] = {both.x, both.y};
+            const float scales[2] = {row_scale(both.x), row_scale(both.y)};
             if (team.at == 0 && end != 0) {
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) a.x_scale[row * kHalves + h] = row_scale(halves[h]);
+                for (int h = 0; h < kHalves; ++h) a.x_scale[row * kHalves + h] = scales[h];
             }
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-                const float by = row_factor(halves[h]);
+                const float by = row_factor(scales[h]);
                 uint8_t* q_row = a.x_q + (row * kHalves + h) * a.cols;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_k
         }
         if (a.q != nullptr) {
             top = reduce.max1(top);
-            const float by = row_factor(top);
-            if (team.at == 0 && end != 0) a.q_scale[row] = row_scale(top);
+            const float scale = row_scale(top), by = row_factor(scale);
+            if (team.at == 0 && end != 0) a.q_scale[row] = scale;
             uint8_t* q_row = a.q + row * a.cols;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {

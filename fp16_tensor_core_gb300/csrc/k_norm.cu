@@ -194,9 +194,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_kernel(const NormArgs 
         }
         if constexpr (kOut == kNormRows) {
             top = reduce.max1(top);
-            by = row_factor(top);
-            if (team.at == 0 && end != 0) a.row_scale[row] = row_scale(top);
-            if constexpr (!kKeep) forget_all();
+            const float scale = row_scale(top);
+            by = row_factor(scale);
+            if (team.at == 0 && end != 0) a.row_scale[row] = scale;
+            if constexpr (!kKeep) {
+                asm volatile("" : "+f"(by));   // (formed first: the pass behind it needs all registers)
+                forget_all();
+            }
         }
         if (kOut == kNormTensor && end != 0)   // (fmaxf would drop a NaN)
             tensor_top = __uint_as_float(max(__float_as_uint(tensor_top), __float_as_uint(top)));

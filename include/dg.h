@@ -513,9 +513,10 @@ dg_status dg_attn_decode_scratch(int batch, int q_len, int q_heads, int head_dim
  * there.
  *
  * Row scales.  scale = max(fl32(amax / 448), 2^-120) of the row's FP32
- * values, code = E4M3 of the value times the scale's FP32 reciprocal (within
- * FP32's rounding of the quotient of §4.3).  A row that holds a NaN or an
- * infinity has scale NaN or infinity; code times scale is NaN there.
+ * values, code = E4M3(fl32(value * fl32(1 / scale))): a rounding more than
+ * the quotient of §4.3, so that a value next to a tie of E4M3 may take the
+ * neighbouring code of it.  A row that holds a NaN or an infinity has scale
+ * NaN or infinity; code times scale is NaN there.
  * ------------------------------------------------------------------------ */
 
 /* rows x columns BF16 or FP16 elements: element (r, c) at
