@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kGradThreads, kGradPerSm / kGradThreads) rmsno
                 for (int e = 0; e < 4; ++e) g[e] = dy[e];
             }
         };
-        // sums of (s by)^2 and of g s by
-        auto sums = [&](float by) {
+        // sums of (s by)^2 and of (g g_by) (s by)
+        auto sums = [&](float by, float g_by) {
             pair squares = 0, dot = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradPerSm / kGradThreads) rmsno
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (by != 1.0f) v[e] = pair_mul(v[e], pair_of(by));
+                    if (g_by != 1.0f) g[e] = pair_mul(g[e], pair_of(g_by));
                     squares = pair_fma(v[e], v[e], squares);
                     dot = pair_fma(g[e], v[e], dot);
                 }
@@ -424,18 +425,21 @@ __global__ void __launch_bounds__(kGradThreads, kGradPerSm / kGradThreads) rmsno
             }
             return both;
         };
-        float down = 1.0f;
-        float2 both = sums(1.0f);
-        // Out of FP32's range: once more, scaled down.  (A vote: rows of a warp
-        // differ, and the reduction takes all of it.)
-        const bool again = !(both.x <= 3.0e38f);
-        if (kNarrow ? __any_sync(0xFFFFFFFFu, again) : again) {
-            down = again ? kDown : 1.0f;
-            both = sums(down);
+        float2 both = sums(1.0f, 1.0f);
+        float unit = rsqrtf(fmaf(both.x, inv_cols, a.eps));   // u = s unit
+        float share = both.y * unit * inv_cols;               // mean(g u)
+        // Out of FP32's range: once more, what left it scaled down.  |g| and |s|
+        // are below 2^128 each, or s 2^64 where its squares hold: 32768 products
+        // of the scaled ones do.  (A vote: rows of a warp differ, and the
+        // reduction takes all of it.)
+        const bool far_s = !(both.x <= 3.0e38f), far_g = !(fabsf(both.y) <= 3.0e38f);
+        if (kNarrow ? __any_sync(0xFFFFFFFFu, far_s || far_g) : far_s || far_g) {
+            const float down = far_s ? kDown : 1.0f, g_down = far_g ? kDown : 1.0f;
+            both = sums(down, g_down);
+            unit = rsqrtf(fmaf(both.x, inv_cols, a.eps * down * down));
+            share = both.y * unit * inv_cols * (far_g ? 1.0f / kDown : 1.0f);
+            unit *= down;
         }
-        const float inv = rsqrtf(fmaf(both.x, inv_cols, a.eps * down * down));
-        const float share = both.y * inv * inv_cols;   // mean(g u)
-        const float unit = inv * down;                 // u = s unit
         uint16_t* dx_row = a.dx + row * a.dx_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {

@@ -572,8 +572,8 @@ dg_status dg_rmsnorm_e4m3_amax(const dg_rows* x, const dg_rows* residual, const 
  *            dsum may be NULL; dx may be any of the others itself.
  *   dweight  FP32[cols], 16-byte aligned, or NULL.  Summed in FP32 in a fixed
  *            order; overwritten.
- * FP32 holds dx only where it holds g and the sum of g s (over 2^80 where
- * that of s^2 is beyond its range).
+ * FP32 holds dx where it holds g and u mean(g u); the sums of s^2 and of g u
+ * may be beyond its range.
  *   scratch  device, 16-byte aligned, at least dg_rmsnorm_grad_scratch()
  *            bytes; unused (may be NULL) without dweight.  Holds nothing
  *            between calls; calls that may overlap in time need one each. */
