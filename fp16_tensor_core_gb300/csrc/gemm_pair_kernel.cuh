@@ -466,7 +466,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 // the CTA's last item, whose ring of stages is idle, every
                 // box has a place of its own in the ring (after any staged
                 // partial tiles), so the stores go out back to back.
-                const int ring_base = it.part == 0 ? pair_boxes_at(C::kRingBytes, BN, nparts) : 0;
+                const int ring_base = (it.part == 0 && staged_parts) ? pair_boxes_at(BN, nparts) : 0;
 #pragma unroll 1
                 for (int c = half; c < BN / 32; c += kChunkStep) {
                     uint32_t r[32];

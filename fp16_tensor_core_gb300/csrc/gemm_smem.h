@@ -54,9 +54,7 @@ constexpr int pair_boxes_bytes(int bn) { return kPairRows / 32 * (bn / 32) * kBo
 constexpr bool pair_parts_in_ring(int ring_bytes, int bn, int parts) {
     return (parts - 1) * pair_partial_bytes(bn) + pair_boxes_bytes(bn) <= ring_bytes;
 }
-// Where the boxes of a tile in `parts` parts begin (whole tiles: one part).
-constexpr int pair_boxes_at(int ring_bytes, int bn, int parts) {
-    return parts > 1 && pair_parts_in_ring(ring_bytes, bn, parts) ? (parts - 1) * pair_partial_bytes(bn) : 0;
-}
+// Where the boxes begin behind the partial tiles of the other parts.
+constexpr int pair_boxes_at(int bn, int parts) { return (parts - 1) * pair_partial_bytes(bn); }
 
 }  // namespace dg

@@ -25,7 +25,7 @@ int stages(int bn, int kps, int fused) { return dg::pair_stages_for(bn, kps, fus
 int ring(int bn, int kps, int fused) { return dg::pair_ring_bytes(bn, kps, fused != 0); }
 int behind(int bn, int fused) { return dg::pair_staging_bytes(fused != 0) + (fused ? dg::columns_bytes(bn) : 0); }
 int in_ring(int ring, int bn, int parts) { return dg::pair_parts_in_ring(ring, bn, parts); }
-int boxes_at(int ring, int bn, int parts) { return dg::pair_boxes_at(ring, bn, parts); }
+int boxes_at(int bn, int parts) { return dg::pair_boxes_at(bn, parts); }
 }
 """)
     lib = where / "probe.so"
@@ -42,13 +42,12 @@ def test_what_a_tile_is_finished_with_fits(sizes, bn, kps, fused):
     # the alignment's slack, the ring, the barriers, staging boxes and columns
     assert 1024 + ring + 1024 + sizes.behind(bn, fused) <= sizes.limit()
     partial, boxes = 128 * bn * 4, 128 * bn * 2     # FP32 partial tile; 16-bit output, as 32 x 32 boxes
-    assert sizes.boxes_at(ring, bn, 1) == 0 and boxes <= ring
+    assert sizes.boxes_at(bn, 1) == 0 and boxes <= ring     # whole tiles, and partial tiles read from L2
     assert sizes.max_parts() == 4
     for parts in range(2, sizes.max_parts() + 1):
-        at = sizes.boxes_at(ring, bn, parts)
-        if sizes.in_ring(ring, bn, parts):
-            assert at >= (parts - 1) * partial, (parts, "boxes over partial tiles that are still read")
-        assert at % 1024 == 0 and at + boxes <= ring, (parts, at, boxes, ring)
+        at = sizes.boxes_at(bn, parts)
+        assert at % 1024 == 0 and at >= (parts - 1) * partial, (parts, "boxes over partial tiles that are still read")
+        assert not sizes.in_ring(ring, bn, parts) or at + boxes <= ring, (parts, at, boxes, ring)
     assert sizes.in_ring(ring, bn, 2)               # two parts always take the ring
 
 
