@@ -4,13 +4,16 @@
 //
 // SiLU and the tanh form of GELU are x times a logistic function:
 //   x / (1 + exp(-u)),  u = x  or  u = 2 sqrt(2 / pi) (x + 0.044715 x^3)
-// ((1 + tanh(u / 2)) / 2 = 1 / (1 + exp(-u))).  GELU is
+// ((1 + tanh(u / 2)) / 2 = 1 / (1 + exp(-u))).  That function is the reciprocal
+// of 2^-7 (1 + exp(-u)), times 2^-7: the reciprocal gives nothing below 2^-126,
+// the product is a subnormal number down to 2^-133 (u from -92), of 16 bits at
+// least, and x times it a normal one.  GELU is
 //   max(x, 0) - |x| h(|x|),  h(a) = erfc(a / sqrt 2) / 2 = exp(-a^2 / 2) P(1 / (1 + 0.35 a))
 // with P the polynomial of degree 7 that minimises the relative error over
 // 0 <= a <= 14 (a Lawson fit of exp(a^2 / 2) erfc(a / sqrt 2) / 2: 5.2e-7 with
 // FP32 coefficients and arithmetic).  In these forms nothing cancels for
 // negative x: results keep FP32's relative precision but for the
-// exponential's argument (2^-23 of its size).
+// exponential's argument (2^-23 of its size, or of 7).
 //
 // Pairs because FP32 additions, products and fused products of two elements
 // are one instruction here: GELU takes 11 issue slots an element this way.
@@ -88,9 +91,13 @@ constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
-// 1 / (1 + exp(-u)), given -u log2(e); 0 where the exponential overflows.
-__device__ __forceinline__ pair logistic(pair minus_u_log2e) {
-    return pair_rcp(pair_add(pair_ex2(minus_u_log2e), pair_of(1.0f)));
+// 1 / (1 + exp(-u)), given -u log2(e) - 7; 0 where the exponential overflows.
+constexpr float kLift = 7.0f;
+__device__ __forceinline__ pair logistic(pair t) {
+    return pair_mul(pair_rcp(pair_add(pair_ex2(t), pair_of(0x1p-7f))), pair_of(0x1p-7f));
+}
+__device__ __forceinline__ pair silu_logistic(pair x) {
+    return logistic(pair_fma(x, pair_of(-kLog2E), pair_of(-kLift)));
 }
 
 // x^2 as the tanh form uses it: past 1000 the function has long been x or 0,
@@ -101,7 +108,7 @@ __device__ __forceinline__ pair gelu_square(pair x) {
 }
 __device__ __forceinline__ pair gelu_logistic(pair x, pair square) {
     const pair t = pair_fma(pair_of(-kLog2E * kGeluSlope * kGeluCubic), square, pair_of(-kLog2E * kGeluSlope));
-    return logistic(pair_mul(x, t));
+    return logistic(pair_fma(x, t, pair_of(-kLift)));
 }
 
 // exp(-x^2 / 2), and h(|x|).
@@ -129,7 +136,7 @@ __device__ __forceinline__ pair activation(int act, pair x) {
             return pair_fma(pair_neg(a), gelu_tail(a, gelu_bell(x)), pair_relu(x));
         }
         case DG_ACT_GELU_TANH: return pair_mul(x, gelu_logistic(x, gelu_square(x)));
-        case DG_ACT_SILU: return pair_mul(x, logistic(pair_mul(x, pair_of(-kLog2E))));
+        case DG_ACT_SILU: return pair_mul(x, silu_logistic(x));
         default: return x;
     }
 }
@@ -164,7 +171,7 @@ __device__ __forceinline__ ValueSlope activation_slope(int act, pair x) {
             return {v, pair_fma(pair_mul(v, rest), du, g)};
         }
         case DG_ACT_SILU: {
-            const pair g = logistic(pair_mul(x, pair_of(-kLog2E))), v = pair_mul(x, g);
+            const pair g = silu_logistic(x), v = pair_mul(x, g);
             const pair rest = pair_fma(pair_neg(g), pair_of(1.0f), pair_of(1.0f));
             return {v, pair_fma(v, rest, g)};
         }

@@ -597,8 +597,8 @@ typedef enum {
 /* The activation between two products:
  *   y = act(x)   or, gated,   y = act(x[:, :cols]) * x[:, cols:]
  * in FP32 (NaN stays NaN; DG_ACT_SILU and DG_ACT_GELU_TANH give NaN at
- * -infinity, and values of act(x) below 2^-126 |x| may be 0).  Any of the
- * three outputs may be left out (NULL):
+ * -infinity; values of act(x) below FP32's normal numbers, 2^-126, may be 0).
+ * Any of the three outputs may be left out (NULL):
  *   x        rows x cols of dtype, or rows x 2 cols when gated.
  *   y        rows x cols of dtype; may be x itself when not gated.
  *   q, q_scale  y as codes uint8[rows][cols] and FP32[rows].
@@ -622,7 +622,7 @@ dg_status dg_activate(const dg_rows* x, int gated, dg_activation act, int64_t ro
  *            a fixed order; overwritten.
  *   scratch  as dg_rmsnorm_grad, for dbias.
  * The derivative of DG_ACT_RELU at 0 is 0; those of the smooth activations
- * are NaN at the infinities. */
+ * are NaN at the infinities; of DG_ACT_GELU's, what is below 2^-123 may be 0. */
 dg_status dg_activate_grad(const dg_rows* dy, const dg_rows* x, const uint8_t* x_q,
                            const float* x_scale, int gated, dg_activation act, int64_t rows,
                            int64_t cols, dg_dtype dtype, const dg_rows* dx, float* dbias,
