@@ -196,6 +196,38 @@ __device__ __forceinline__ void with_activation(int act, F&& f) {
     }
 }
 
+// acc scale_a scale_b, where the scales' product may be no normal number of
+// FP32 though the result is one: the larger scale first where their product
+// is small, the smaller one where it is large.
+__device__ __forceinline__ bool scale_in_range(float ab) {
+    return fabsf(ab) >= 0x1p-126f && fabsf(ab) <= 3.4e38f;
+}
+__device__ __forceinline__ float scaled(float acc, float a, float b) {
+    const float ab = a * b;
+    if (scale_in_range(ab)) return acc * ab;
+    const float small = fabsf(a) < fabsf(b) ? a : b, large = fabsf(a) < fabsf(b) ? b : a;
+    return fabsf(ab) < 1.0f ? acc * large * small : acc * small * large;
+}
+// acc scale_a scale_b + bias of two elements.
+__device__ __forceinline__ pair scale_and_bias(pair acc, pair a, float b, float bias) {
+    const pair ab = pair_mul(a, pair_of(b));
+    const float2 f = floats_of(ab);
+    if (scale_in_range(f.x) && scale_in_range(f.y)) return pair_fma(acc, ab, pair_of(bias));
+    const float2 x = floats_of(acc), s = floats_of(a);
+    return pair_of(scaled(x.x, s.x, b) + bias, scaled(x.y, s.y, b) + bias);
+}
+// The same for many products: a scale as whole x rest, whole 2^-62, 1 or 2^64.
+// The product of two rests is a normal number (of scales down to 2^-122), and
+// acc times both wholes overflows only where the result does.
+struct ScaleParts {
+    float whole, rest;
+};
+__device__ __forceinline__ bool scale_is_rest(float s) { return fabsf(s) >= 0x1p-62f && fabsf(s) < 0x1p64f; }
+__device__ __forceinline__ ScaleParts scale_parts(float s) {
+    if (scale_is_rest(s)) return {1.0f, s};
+    return fabsf(s) < 1.0f ? ScaleParts{0x1p-62f, s * 0x1p62f} : ScaleParts{0x1p64f, s * 0x1p-64f};
+}
+
 // Division by a given scale as two multiplications: x / s = (x pre) inv.  pre
 // is 1 but for scales whose reciprocal FP32 does not hold; with it the
 // product overflows or vanishes only where the code saturates or is 0 anyway.

@@ -308,9 +308,12 @@ __device__ __forceinline__ void store_box_odd(const Params& p, uint8_t* box, int
 
 // The columns' scales of B and biases (laid out as kColumnFloats says) into
 // shared memory while the main loop runs, zeros past N: chunks first, first +
-// 2, ... of the tile whose columns start at col0.
+// 2, ... of the tile whose columns start at col0.  What is kept of a scale is
+// its rest (scale_parts); returns whether any lane has one, or a row of scale
+// `sa`, that is more than its rest.
 template <int BN>
-__device__ __forceinline__ void stage_columns(const Params& p, float* columns, int col0, int first, int lane) {
+__device__ __forceinline__ bool stage_columns(const Params& p, float* columns, int col0, int first, int lane, float sa) {
+    bool parts = !scale_is_rest(sa);
     constexpr int kChunks = fused_chunks(BN);
     float s[kChunks], b[kChunks];
 #pragma unroll
@@ -318,7 +321,11 @@ __device__ __forceinline__ void stage_columns(const Params& p, float* columns, i
         const int n = col0 + 32 * (first + 2 * i) + lane;
         s[i] = p.sb == nullptr ? 1.0f : 0.0f;
         b[i] = 0.0f;
-        if (n < p.N && p.sb != nullptr) s[i] = ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
+        if (n < p.N && p.sb != nullptr) {
+            const float sb = ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
+            s[i] = scale_parts(sb).rest;
+            parts |= !scale_is_rest(sb);
+        }
         if (n < p.N && p.epi.bias != nullptr) b[i] = ld_float(p.epi.bias + n);
     }
     __syncwarp();   // every lane has read the last tile's
@@ -329,6 +336,21 @@ __device__ __forceinline__ void stage_columns(const Params& p, float* columns, i
         columns[at + 2] = b[i];
     }
     __syncwarp();
+    return __any_sync(0xFFFFFFFFu, parts);
+}
+
+// Multiplies 32 accumulator columns of one row by what stage_columns left out
+// of their scales and scale_of_row of the row's.
+__device__ __forceinline__ void apply_wholes(const Params& p, int row, bool row_ok, int col0, int lane,
+                                             uint32_t (&r)[32]) {
+    const int n = col0 + lane;
+    const float s = n < p.N && p.sb != nullptr ? ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step) : 1.0f;
+    const float column = scale_parts(s).whole;
+    const float a = p.sa == nullptr || !row_ok ? 1.0f : ld_float(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
+    const float whole = scale_parts(a).whole;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        r[i] = __float_as_uint(__uint_as_float(r[i]) * whole * __shfl_sync(0xFFFFFFFFu, column, i));
 }
 
 // Moves a tile row's residual (this warp's lines of 64 columns: the first half
@@ -395,7 +417,8 @@ __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col
     return __float_as_uint(top);
 }
 
-// A row's scale of A (1 without scales, and for rows outside).
+// A row's scale of A (1 without scales, and for rows outside); the epilogue
+// goes on with its rest (scale_parts).
 __device__ __forceinline__ float scale_of_row(const Params& p, int row, bool row_ok) {
     return p.sa == nullptr || !row_ok ? 1.0f : ld_float(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
 }

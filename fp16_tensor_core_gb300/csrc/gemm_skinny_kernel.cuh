@@ -184,8 +184,8 @@ __device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, co
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const ulonglong2 s = reinterpret_cast<const ulonglong2*>(sa + c0)[i];
-        v[2 * i] = pair_fma(pair_of(f[4 * i], f[4 * i + 1]), pair_mul(s.x, pair_of(col.sb)), pair_of(col.bias));
-        v[2 * i + 1] = pair_fma(pair_of(f[4 * i + 2], f[4 * i + 3]), pair_mul(s.y, pair_of(col.sb)), pair_of(col.bias));
+        v[2 * i] = scale_and_bias(pair_of(f[4 * i], f[4 * i + 1]), s.x, col.sb, col.bias);
+        v[2 * i + 1] = scale_and_bias(pair_of(f[4 * i + 2], f[4 * i + 3]), s.y, col.sb, col.bias);
     }
     with_activation(p.epi.act, [&](auto act) {
 #pragma unroll

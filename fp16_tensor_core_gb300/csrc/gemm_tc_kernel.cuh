@@ -325,12 +325,14 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             // loop runs; the residual one 32-column chunk ahead.
             const bool row_ok = row < T.row_end;
             float sa = 1.0f;
+            bool parts = false;
             uint32_t res[16];
             if constexpr (kFused) {
                 sa = scale_of_row(p, row, row_ok);
                 if ((p.N & 7) == 0) load_residual(p, row, row_ok, T.col0 + 32 * half, res);
                 prefetch_residual<BN>(p, row, row_ok, T.col0, half);
-                stage_columns<BN>(p, columns, T.col0, half, lane);
+                parts = stage_columns<BN>(p, columns, T.col0, half, lane, sa);
+                sa = scale_parts(sa).rest;
             }
             // Every lane waits; the vote reconverges the warp (tcgen05.ld is
             // .sync.aligned) and makes the whole warp leave together.
@@ -360,6 +362,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = T.col0 + c * 32;
                     if constexpr (kFused) {
                         float v[32];
+                        if (parts) apply_wholes(p, row, row_ok, col0, lane, r);
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
                         if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         stage_values(p, box, v, lane);
@@ -380,6 +383,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         uint8_t* box = smem + C::kStagingOff + (warp - 4) * kBoxBytes;
                         if ((p.N & 7) != 0) load_residual_odd(p, box, row0, T.row_end, col0, lane, res);
                         float v[32];
+                        if (parts) apply_wholes(p, row, row_ok, col0, lane, r);
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
                         if ((p.N & 7) == 0 && c + kChunkStep < BN / 32)
                             load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);

@@ -247,9 +247,8 @@ gemv_mma_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int at = g + 8 * h, n = r0 + at;
-                const pair s = pair_mul(sam, pair_of(fused.sb[at]));
                 const float2 y = floats_of(activation(
-                    epi.act, pair_fma(pair_of(v[j][2 * h], v[j][2 * h + 1]), s, pair_of(fused.bias[at]))));
+                    epi.act, scale_and_bias(pair_of(v[j][2 * h], v[j][2 * h + 1]), sam, fused.sb[at], fused.bias[at])));
                 float out[2] = {y.x, y.y};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {

@@ -650,9 +650,11 @@ typedef struct {
  *   v      = act(scale_a[m] * scale_b[n] * sum_k A[m,k] * B[n,k] + bias[n]) + residual[m,n]
  *   D[m,n] = out(v), or E4M3(v / *scale_d)
  *   amax_d = max |v| over D (as dg_fp8_gemm_amax; zeroed by the call)
- * rounded once (the two scales are multiplied first).  Row scales of A are what dg_rmsnorm_e4m3 and dg_activate
- * write; a weight quantised by rows has its own (one scale serves either side
- * as before).  With K == 0 the sum is empty.  D may be the residual itself
+ * rounded once (the two scales are multiplied first, where their product is a
+ * normal number of FP32; else one after the other, so that v holds where FP32
+ * does).  Row scales of A are what dg_rmsnorm_e4m3 and dg_activate write; a
+ * weight quantised by rows has its own (one scale serves either side as
+ * before).  With K == 0 the sum is empty.  D may be the residual itself
  * when both have the same 16-bit type.  Smooth activations as dg_activate.
  * Vectors, bias and residual 16-byte aligned, scalars 4-byte.  Operands, sizes
  * and other errors as dg_fp8_gemm; paths as there, but that one row of A never

@@ -87,3 +87,52 @@ def test_output_scales_of_values_as_small_or_large(M, scale):
     err = size * 2.0 ** -18 + 2.0 ** -149 * 9
     _, inside = check_saturating(codes, value, err, sd)
     assert inside > 0.9 * M * N
+
+
+# Powers of two of the rows' and the columns' scales, from a zero row's to the
+# largest that a row of BF16 values has; those of ordinary rows among them.
+ROW_POWERS = (0, -120, -70, 60, 119, -100, 63, -62, 64, -8)
+COLUMN_POWERS = (0, -12, -120, 119, 70, -62, 64, -63, -30, 5)
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("N", [264, 1001])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("fp16", [False, True])
+def test_products_of_scales_beyond_fp32(M, N, bias, fp16):
+    """Scales whose product leaves FP32, though the result does not; empty sums
+    are their bias whatever the scales."""
+    K = 256
+    A, B = (codes_of(i, n, K, size=0.5) for i, n in ((1, M), (2, N)))
+    if fp16:
+        A, B = wide(A).half(), wide(B).half()
+    A[0], A[M // 2] = 0, 0
+    power = [torch.tensor([p[i % len(p)] for i in range(n)], device="cuda", dtype=torch.float64)
+             for p, n in ((ROW_POWERS, M), (COLUMN_POWERS, N))]
+    sa, sb = ((2.0 ** p * (1 + torch.rand(len(p), device="cuda", dtype=torch.float64))).float() for p in power)
+    b = randn(5, N) if bias else None
+    D = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    if fp16:
+        dg.dg_hgemm_fused(A, B, D, bias=b, scale_a=sa, scale_b=sb, out=dg.DG_BF16)
+    else:
+        dg.dg_fp8_gemm_fused(A, B, D, sa, sb, bias=b)
+    acc, size = A.double() if fp16 else wide(A), B.double() if fp16 else wide(B)
+    acc, size = acc @ size.T, acc.abs() @ size.T.abs()
+    ab = sa.double()[:, None] * sb.double()
+    want = acc * ab + (b.double() if bias else 0)
+    got = D.double()
+    assert not got.isnan().any()
+    # accumulation, four roundings more, FP32's subnormal step, and BF16's rounding
+    err = size * ab * (2.0 ** -23 * (K / 16 + 24)) + 2.0 ** -149
+    bound = err + want.abs() * 2.0 ** -8 + 2.0 ** -134
+    top = torch.finfo(torch.bfloat16).max
+    beyond = want.abs() > top * (1 + 2.0 ** -9) + err
+    assert (got[beyond].isinf() & (got[beyond].sign() == want[beyond].sign())).all()
+    near = want.abs() <= top - err
+    assert ((got[near] - want[near]).abs() <= bound[near]).all()
+    # both kinds are there: a product of scales that FP32 does not hold, and a result that it does
+    if M > 10:
+        odd = (ab < 2.0 ** -126) | (ab > 2.0 ** 127)
+        assert (odd & near & (acc != 0)).sum() > 0.1 * M * N and beyond.any()
+    empty = (b.double() if bias else torch.zeros(N, dtype=torch.float64, device="cuda")).bfloat16().double()
+    assert torch.equal(got[0], empty) and torch.equal(got[M // 2], empty)
