@@ -10,10 +10,11 @@
 // least, and x times it a normal one.  GELU is
 //   max(x, 0) - |x| h(|x|),  h(a) = erfc(a / sqrt 2) / 2 = exp(-a^2 / 2) P(1 / (1 + 0.35 a))
 // with P the polynomial of degree 7 that minimises the relative error over
-// 0 <= a <= 14 (a Lawson fit of exp(a^2 / 2) erfc(a / sqrt 2) / 2: 5.2e-7 with
-// FP32 coefficients and arithmetic).  In these forms nothing cancels for
-// negative x: results keep FP32's relative precision but for the
-// exponential's argument (2^-23 of its size, or of 7).
+// 0 <= a <= 14 (a Lawson fit of exp(a^2 / 2) erfc(a / sqrt 2) / 2: below 2^-20
+// in FP32 arithmetic, 6.0e-7 of it with a rounded reciprocal and 8.8e-7 with
+// one off by 2^-23).  In these forms nothing cancels for negative x: the other
+// two keep FP32's relative precision, and all lose only by the exponential's
+// argument (2^-23 of its size, or of 7).
 //
 // Pairs because FP32 additions, products and fused products of two elements
 // are one instruction here: GELU takes 11 issue slots an element this way.
