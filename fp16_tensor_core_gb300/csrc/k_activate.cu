@@ -44,6 +44,11 @@ constexpr int block_min() { return NV == 8 ? 1 : 2; }
 // with checkpoint 30.7 -> 26.6; without codes 22.6 -> 23.0).
 constexpr int kLimits[3] = {512, 384, 512}, kCodeLimits[3] = {256, 384, 512};
 constexpr int kPerSm[3] = {1024, 768, 512};
+constexpr bool within_bounds(const int (&limits)[3]) {
+    return limits[0] <= block_limit<2>() && limits[1] <= block_limit<4>() && limits[2] <= block_limit<8>();
+}
+static_assert(hold_widest_row(kLimits) && within_bounds(kLimits), "launch bounds");
+static_assert(hold_widest_row(kCodeLimits) && within_bounds(kCodeLimits), "launch bounds");
 
 template <int NV, bool kFp16, bool kGated, bool kNarrow>
 __global__ void __launch_bounds__(block_limit<NV>(), block_min<NV>()) activate_kernel(const ActArgs a, int team_size) {

@@ -49,6 +49,7 @@ constexpr float kDown = 0x1p-80f;
 // next one on its way to L2 (1500 x 24576: 55.8 us, 0.68; held in FP32 70.6).
 constexpr int kLimits[3] = {1024, 1024, 0};
 constexpr int kPerSm[3] = {1024, 1024, 0};
+static_assert(hold_widest_row(kLimits) && kLimits[0] <= kRowThreads && kLimits[1] <= kRowThreads, "launch bounds");
 
 template <int NV, bool kFp16, int kOut, bool kNarrow, bool kResidual>
 __global__ void __launch_bounds__(kRowThreads, 1) rmsnorm_kernel(const NormArgs a, int team_size) {
@@ -268,6 +269,7 @@ __global__ void next_scale_kernel(const float* amax, float* scale) {
 constexpr int kGradThreads = 512, kGradPerSm = 512;
 constexpr int kGradColumns = 16 * kGradThreads;   // of a block
 constexpr int kGradRanks = kMaxRowElements / kGradColumns;   // at most, a cluster
+static_assert(kGradRanks * kGradColumns == kMaxRowElements, "widest row");
 
 // Sums over a cluster's threads (each warp's value to every block, in one
 // buffer of two, taken in turn as RowReduce's).

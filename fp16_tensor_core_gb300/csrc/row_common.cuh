@@ -17,10 +17,6 @@ namespace dg {
 
 constexpr int kRowThreads = 1024;   // at most, a row
 
-// Rows too wide for the vectors of one block are refused.
-constexpr int kRowVectors = 4;     // at most, a thread
-static_assert(kRowThreads * kRowVectors * 8 == kMaxRowElements, "widest row");
-
 // Eight elements as four pairs.
 template <bool kFp16>
 __device__ __forceinline__ void unpack8(uint4 v, pair (&f)[4]) {
@@ -274,8 +270,16 @@ struct RowPlan {
     int each, team, threads, blocks;
     bool narrow;
 };
-// per_sm: threads an SM holds at the kernel's registers, by vectors a thread
-// (2, 4, 8).
+// Whether the kernels behind `limits` hold every row of up to kMaxRowElements
+// (wider ones are refused before): row_plan takes the first that holds a row.
+constexpr bool hold_widest_row(const int (&limits)[3]) {
+    for (int k = 0; k < 3; ++k)
+        if (limits[k] % 32 == 0 && limits[k] * (2 << k) * 8 >= kMaxRowElements) return true;
+    return false;
+}
+// limits: a block's threads at most, per_sm: threads an SM holds at the
+// kernel's registers, both by vectors a thread (2, 4, 8); 0 where there is no
+// kernel of that many.
 inline RowPlan row_plan(int64_t rows, int cols, int sm_count, const int (&limits)[3], const int (&per_sm)[3]) {
     const int vectors = cols >> 3;
     int k = 0;
