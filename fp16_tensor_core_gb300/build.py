@@ -3,7 +3,8 @@
 One translation unit per kernel family, compiled in parallel, then linked
 into ``fp16_tensor_core_gb300/_build/libdg.so`` against the shared CUDA
 runtime (the same one PyTorch loads).  ``dg_python``, a small C module that
-reads the serving calls' arguments, is compiled with gcc and Python's headers.
+reads the arguments of the serving calls and of those around a layer's
+products, is compiled with gcc and Python's headers.
 """
 from __future__ import annotations
 
@@ -82,12 +83,17 @@ def _native_missing() -> str:
 
 
 def _build_native(force: bool) -> None:
-    """dg_python, for the serving calls from Python.  libdg and everything
-    else need only nvcc: without a C compiler or Python's headers this is left
-    out with a warning, and the serving calls raise when they are made."""
+    """dg_python, for the serving calls (rotary positions, cache, attention) and
+    those around a layer's products (norm, activation, fused products) from
+    Python.  libdg and everything else need only nvcc: without a C compiler or
+    Python's headers this is left out with a warning, and these calls raise
+    when they are made."""
     missing = _native_missing()
     if missing:
-        warnings.warn(f"{missing} not found: the serving calls cannot be made from Python")
+        warnings.warn(f"{missing} not found: the serving calls (dg_rope, dg_kv_append, dg_kv_read, dg_attn_decode) and "
+                      "those around a layer's products (dg_rmsnorm, dg_rmsnorm_e4m3, dg_rmsnorm_e4m3_amax, "
+                      "dg_rmsnorm_grad, dg_activate, dg_activate_grad, dg_fp8_gemm_fused, dg_hgemm_fused) cannot be "
+                      "made from Python")
         return
     src = os.path.join(CSRC, "dg_python.c")
     deps = (src, os.path.join(INCLUDE, "dg.h"), __file__)
