@@ -388,7 +388,7 @@ def _load_native():
             if _raw_stream is not None and _current_device is not None:
                 stream, device = _raw_stream, _current_device
             else:
-                stream, device = lambda _: torch.cuda.current_stream().cuda_stream, int
+                stream, device = lambda _: torch.cuda.current_stream().cuda_stream, torch.cuda.current_device
             module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                           for f in (L.dg_rope, L.dg_kv_append, L.dg_kv_read, L.dg_attn_decode)),
                         torch.bfloat16, torch.float16, torch.int32, torch.float32, stream, device, _check)
