@@ -121,11 +121,13 @@ __device__ __forceinline__ void store_chunk16(const SkParams& p, int c0, int n, 
 // loaded while the tile's main loop runs.
 struct FusedColumn {
     float sb = 1.0f, bias = 0.0f;
+    bool ordinary = true;   // its scale's product with each row's is a normal number
 };
-__device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live, int n) {
+__device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live, int n, bool ordinary_rows) {
     FusedColumn c;
     if (live && p.sb != nullptr) c.sb = ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
     if (live && p.epi.bias != nullptr) c.bias = ld_float(p.epi.bias + n);
+    c.ordinary = ordinary_rows && scale_is_rest(c.sb);
     return c;
 }
 
@@ -181,11 +183,18 @@ __device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, co
                                            ByScale out, const float* sa, const uint16_t* residual,
                                            float (&f)[16]) {
     pair v[8];
+    if (__builtin_expect(col.ordinary, 1)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const ulonglong2 s = reinterpret_cast<const ulonglong2*>(sa + c0)[i];
-        v[2 * i] = scale_and_bias(pair_of(f[4 * i], f[4 * i + 1]), s.x, col.sb, col.bias);
-        v[2 * i + 1] = scale_and_bias(pair_of(f[4 * i + 2], f[4 * i + 3]), s.y, col.sb, col.bias);
+        for (int i = 0; i < 4; ++i) {
+            const ulonglong2 s = reinterpret_cast<const ulonglong2*>(sa + c0)[i];
+            v[2 * i] = pair_fma(pair_of(f[4 * i], f[4 * i + 1]), pair_mul(s.x, pair_of(col.sb)), pair_of(col.bias));
+            v[2 * i + 1] = pair_fma(pair_of(f[4 * i + 2], f[4 * i + 3]), pair_mul(s.y, pair_of(col.sb)), pair_of(col.bias));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = pair_of(scaled(f[2 * i], sa[c0 + 2 * i], col.sb) + col.bias,
+                           scaled(f[2 * i + 1], sa[c0 + 2 * i + 1], col.sb) + col.bias);
     }
     with_activation(p.epi.act, [&](auto act) {
 #pragma unroll
@@ -523,10 +532,12 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
         const float alpha = !kFused && p.out_kind == kOutE4M3 ? __fdiv_rn(ab, p.sd[0]) : ab;
         ByScale out{1.0f, 1.0f};
         FusedColumn column;
+        bool ordinary_rows = true;
         if constexpr (kFused) {
             out = output_scale(p.out_kind, p.sd);
-            if (r < NC) row_scales[r] = p.sa != nullptr && r < p.M ? ld_float(p.sa + r * p.epi.sa_step) : 1.0f;
-            named_bar_sync(kEpiBar, kEpiThreads);   // (the helpers' reads come after a hand-off)
+            float s = 1.0f;
+            if (r < NC) row_scales[r] = s = p.sa != nullptr && r < p.M ? ld_float(p.sa + r * p.epi.sa_step) : 1.0f;
+            ordinary_rows = named_bar_and(kEpiBar, kEpiThreads, scale_is_rest(s));   // (the helpers' reads come after a hand-off)
         }
         uint32_t amax_bits = 0u;
         bool released = false;   // the last tile handed to warps 0-3 (thread 128)
@@ -544,7 +555,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
                 range_start(c_first, G, units) == tile_u0 ? 2 * c_first : 2 * c_first + 1;
             if constexpr (kFused) {
                 const int n0 = t * p.tile_rows + r;
-                column = fused_column(p, r < p.tile_rows && n0 < p.N, n0);
+                column = fused_column(p, r < p.tile_rows && n0 < p.N, n0, ordinary_rows);
                 if (p.epi.residual != nullptr) {
                     if (t != t_begin) named_bar_sync(kEpiBar, kEpiThreads);   // the last tile's has been read
                     stage_residual(p, residual_tile, t, r);
@@ -684,7 +695,10 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             if constexpr (kFused) {   // of the CTA's last tile
                 const int t_last = static_cast<int>((u_begin + n_units - 1) / KB), n = t_last * p.tile_rows + warp * 32 + lane;
                 out = output_scale(p.out_kind, p.sd);
-                column = fused_column(p, warp * 32 + lane < p.tile_rows && n < p.N, n);
+                bool rows = true;   // (read again: the hand-off comes later)
+                for (int m = lane; m < p.M && p.sa != nullptr; m += 32)
+                    rows &= scale_is_rest(ld_float(p.sa + m * p.epi.sa_step));
+                column = fused_column(p, warp * 32 + lane < p.tile_rows && n < p.N, n, __all_sync(0xFFFFFFFFu, rows));
             }
             const bool go = wait_bounded(help_bar, 0, ctl) && help[0] != 0;
             if (__all_sync(0xFFFFFFFFu, go)) {
