@@ -371,6 +371,9 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             tc_fence_after_sync();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * BN);
+            if constexpr (kFused) {   // (a split tile's parts are added first)
+                if (parts && it.part < 0) apply_wholes_to_tile<BN>(p, tbase, row, row_ok, nt * BN, half, lane);
+            }
             // Split tail tile: this CTA's partial tile of part s lives in slot
             // (r * (split - 1) + s - 1) * 2 + rank, as FP32 column quads
             // ([BN / 4][128] float4: a warp's 32 rows are one 512-byte run).
@@ -457,6 +460,9 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         r[4 * g + 3] = __float_as_uint(__uint_as_float(r[4 * g + 3]) + x.w);
                     }
                 }
+                if constexpr (kFused) {
+                    if (parts) apply_wholes(p, row, row_ok, nt * BN + c * 32, lane, r);
+                }
             };
             if (it.part > 0 || !ready) {
                 // nothing to store (a later part, or a wait that ran out)
@@ -484,7 +490,6 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = nt * BN + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        if (parts) apply_wholes(p, row, row_ok, col0, lane, r);
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
                         if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         stage_values(p, box, v, lane);
@@ -524,7 +529,6 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         uint8_t* box = smem + C::kStagingOff + (warp - 4) * kBoxBytes;
                         if ((p.N & 7) != 0) load_residual_odd(p, box, row0, p.M, col0, lane, res);
                         float v[32];
-                        if (parts) apply_wholes(p, row, row_ok, col0, lane, r);
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
                         if ((p.N & 7) == 0 && c + kChunkStep < BN / 32)
                             load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);

@@ -42,9 +42,9 @@ struct SkCfg {
     static constexpr int kStageW = KPS * kWBytes;
     static constexpr int kStageX = KPS * kXBytes;
     static constexpr int kSmemBytes = 1024 + kRing * kKBBytes + kBarBytes;
-    static constexpr int kScalesOff = kRing * kKBBytes + kBarBytes;   // fused: the rows' scales of A
-    static constexpr int kResidualOff = kScalesOff + NC * 4;          // and the tile's residual [NC][128]
-    static constexpr int kFusedSmemBytes = kSmemBytes + NC * 4 + NC * kRows * 2;
+    static constexpr int kScalesOff = kRing * kKBBytes + kBarBytes;   // fused: the rows' scales of A (rests [NC], wholes [NC])
+    static constexpr int kResidualOff = kScalesOff + NC * 8;          // and the tile's residual [NC][128]
+    static constexpr int kFusedSmemBytes = kSmemBytes + NC * 8 + NC * kRows * 2;
     static constexpr uint32_t kTmemCols = pow2_at_least(2 * NC);   // two accumulators
     static constexpr uint32_t kIdesc = idesc_f32acc(kRows, NC, 0, 0);
     static_assert(NC % 16 == 0 && NC >= 16 && NC <= kSplitkMaxCols, "MMA N");
@@ -121,13 +121,11 @@ __device__ __forceinline__ void store_chunk16(const SkParams& p, int c0, int n, 
 // loaded while the tile's main loop runs.
 struct FusedColumn {
     float sb = 1.0f, bias = 0.0f;
-    bool ordinary = true;   // its scale's product with each row's is a normal number
 };
-__device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live, int n, bool ordinary_rows) {
+__device__ __forceinline__ FusedColumn fused_column(const SkParams& p, bool live, int n) {
     FusedColumn c;
     if (live && p.sb != nullptr) c.sb = ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step);
     if (live && p.epi.bias != nullptr) c.bias = ld_float(p.epi.bias + n);
-    c.ordinary = ordinary_rows && scale_is_rest(c.sb);
     return c;
 }
 
@@ -177,24 +175,25 @@ __device__ __forceinline__ void stage_residual(const SkParams& p, uint16_t* tile
 }
 
 // act(scale_a[m] scale_b[n] acc + bias[n]) + residual[m, n] for rows c0 ..
-// c0 + jn - 1 (sa: the rows' scales, residual: row c0 of this thread's column,
-// both in shared memory); returns the largest magnitude (ordered bits).
+// c0 + jn - 1 (sa: the rows' scales, rests and then wholes, residual: row c0 of
+// this thread's column, both in shared memory); returns the largest magnitude
+// (ordered bits).  Two products more a pair for the wholes: a branch around
+// them took 0.3 to 0.7 us more of 64 x 4096 x 11008's 16.9.
+template <int NC>
 __device__ __forceinline__ uint32_t fuse16(const SkParams& p, int c0, int jn, const FusedColumn& col,
                                            ByScale out, const float* sa, const uint16_t* residual,
                                            float (&f)[16]) {
     pair v[8];
-    if (__builtin_expect(col.ordinary, 1)) {
+    const ScaleParts column = scale_parts(col.sb);
+    const float* wholes = sa + NC;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const ulonglong2 s = reinterpret_cast<const ulonglong2*>(sa + c0)[i];
-            v[2 * i] = pair_fma(pair_of(f[4 * i], f[4 * i + 1]), pair_mul(s.x, pair_of(col.sb)), pair_of(col.bias));
-            v[2 * i + 1] = pair_fma(pair_of(f[4 * i + 2], f[4 * i + 3]), pair_mul(s.y, pair_of(col.sb)), pair_of(col.bias));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = pair_of(scaled(f[2 * i], sa[c0 + 2 * i], col.sb) + col.bias,
-                           scaled(f[2 * i + 1], sa[c0 + 2 * i + 1], col.sb) + col.bias);
+    for (int i = 0; i < 4; ++i) {
+        const ulonglong2 s = reinterpret_cast<const ulonglong2*>(sa + c0)[i];
+        const ulonglong2 w = reinterpret_cast<const ulonglong2*>(wholes + c0)[i];
+        const pair x = pair_mul(pair_mul(pair_of(f[4 * i], f[4 * i + 1]), w.x), pair_of(column.whole));
+        const pair y = pair_mul(pair_mul(pair_of(f[4 * i + 2], f[4 * i + 3]), w.y), pair_of(column.whole));
+        v[2 * i] = pair_fma(x, pair_mul(s.x, pair_of(column.rest)), pair_of(col.bias));
+        v[2 * i + 1] = pair_fma(y, pair_mul(s.y, pair_of(column.rest)), pair_of(col.bias));
     }
     with_activation(p.epi.act, [&](auto act) {
 #pragma unroll
@@ -334,7 +333,7 @@ __device__ __forceinline__ void finish_chunks(const SkParams& p, uint8_t* smem, 
         if (live) {
             const int jn = min(16, p.M - c0);   // rows of A in this chunk
             if constexpr (kFused) {
-                amax_bits = max(amax_bits, fuse16(p, c0, jn, column, out, sa, residual_tile + c0 * kRows + r, v));
+                amax_bits = max(amax_bits, fuse16<NC>(p, c0, jn, column, out, sa, residual_tile + c0 * kRows + r, v));
                 store_chunk16(p, c0, n, jn, v, 1.0f);
                 continue;
             }
@@ -532,12 +531,14 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
         const float alpha = !kFused && p.out_kind == kOutE4M3 ? __fdiv_rn(ab, p.sd[0]) : ab;
         ByScale out{1.0f, 1.0f};
         FusedColumn column;
-        bool ordinary_rows = true;
         if constexpr (kFused) {
             out = output_scale(p.out_kind, p.sd);
-            float s = 1.0f;
-            if (r < NC) row_scales[r] = s = p.sa != nullptr && r < p.M ? ld_float(p.sa + r * p.epi.sa_step) : 1.0f;
-            ordinary_rows = named_bar_and(kEpiBar, kEpiThreads, scale_is_rest(s));   // (the helpers' reads come after a hand-off)
+            if (r < NC) {
+                const ScaleParts row = scale_parts(p.sa != nullptr && r < p.M ? ld_float(p.sa + r * p.epi.sa_step) : 1.0f);
+                row_scales[r] = row.rest;
+                row_scales[NC + r] = row.whole;
+            }
+            named_bar_sync(kEpiBar, kEpiThreads);   // (the helpers' reads come after a hand-off)
         }
         uint32_t amax_bits = 0u;
         bool released = false;   // the last tile handed to warps 0-3 (thread 128)
@@ -555,7 +556,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
                 range_start(c_first, G, units) == tile_u0 ? 2 * c_first : 2 * c_first + 1;
             if constexpr (kFused) {
                 const int n0 = t * p.tile_rows + r;
-                column = fused_column(p, r < p.tile_rows && n0 < p.N, n0, ordinary_rows);
+                column = fused_column(p, r < p.tile_rows && n0 < p.N, n0);
                 if (p.epi.residual != nullptr) {
                     if (t != t_begin) named_bar_sync(kEpiBar, kEpiThreads);   // the last tile's has been read
                     stage_residual(p, residual_tile, t, r);
@@ -695,10 +696,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w,
             if constexpr (kFused) {   // of the CTA's last tile
                 const int t_last = static_cast<int>((u_begin + n_units - 1) / KB), n = t_last * p.tile_rows + warp * 32 + lane;
                 out = output_scale(p.out_kind, p.sd);
-                bool rows = true;   // (read again: the hand-off comes later)
-                for (int m = lane; m < p.M && p.sa != nullptr; m += 32)
-                    rows &= scale_is_rest(ld_float(p.sa + m * p.epi.sa_step));
-                column = fused_column(p, warp * 32 + lane < p.tile_rows && n < p.N, n, __all_sync(0xFFFFFFFFu, rows));
+                column = fused_column(p, warp * 32 + lane < p.tile_rows && n < p.N, n);
             }
             const bool go = wait_bounded(help_bar, 0, ctl) && help[0] != 0;
             if (__all_sync(0xFFFFFFFFu, go)) {

@@ -341,6 +341,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             tc_fence_after_sync();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * BN);
+            if constexpr (kFused) {
+                if (parts) apply_wholes_to_tile<BN>(p, tbase, row, row_ok, T.col0, half, lane);
+            }
             // Staged bulk stores (whole lines, M / N edges clipped by the
             // tensor map) unless the warp's 32 rows cross a group's end,
             // which the tensor map cannot clip: those rows store directly.
@@ -362,7 +365,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const int col0 = T.col0 + c * 32;
                     if constexpr (kFused) {
                         float v[32];
-                        if (parts) apply_wholes(p, row, row_ok, col0, lane, r);
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
                         if (c + kChunkStep < BN / 32) load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);
                         stage_values(p, box, v, lane);
@@ -383,7 +385,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         uint8_t* box = smem + C::kStagingOff + (warp - 4) * kBoxBytes;
                         if ((p.N & 7) != 0) load_residual_odd(p, box, row0, T.row_end, col0, lane, res);
                         float v[32];
-                        if (parts) apply_wholes(p, row, row_ok, col0, lane, r);
                         amax_bits = max(amax_bits, fuse32(p, row_ok, col0, r, res, sa, columns + kColumnFloats * (c / kChunkStep), out_scale, v));
                         if ((p.N & 7) == 0 && c + kChunkStep < BN / 32)
                             load_residual(p, row, row_ok, col0 + 32 * kChunkStep, res);

@@ -103,3 +103,29 @@ def test_widths(ranges, bn, kps, fp16, capfd):
         want = act64(acc, dg.DG_ACT_RELU)[0] + residual.double()
         close(D, want, size * rel + want.abs() * (STEP[HALF] + 2.0 ** -23) + TINY[HALF], "fused")
         assert (whole[M * N:] == 77).all()
+
+
+@pytest.mark.parametrize("ranges", [2, 4])
+@pytest.mark.parametrize("bn", [128, 224])
+def test_scales_beyond_fp32_in_a_split_tile(ranges, bn, capfd):
+    """Scales that are applied in two steps, of a tile whose parts are added first."""
+    pairs = pairs_of(capfd)
+    left = pairs // ranges
+    N, K = bn * (pairs + left) - 8, 1040
+    A, B, sa, sb = operands(N, K, False, ranges)
+    sa[::3] *= 2.0 ** -100
+    sa[1::3] *= 2.0 ** 90
+    sb[::2] *= 2.0 ** -80
+    sb[1::4] *= 2.0 ** 30
+    D = torch.zeros(M, N, dtype=BF, device="cuda")
+    with knobs(DG_FORCE_BLOCK_N=str(bn)):
+        capfd.readouterr()
+        dg.dg_fp8_gemm_fused(A, B, D, sa, sb)
+        assert split_of(capfd) == (pairs, left, ranges)
+    ab = sa.double()[:, None] * sb.double()
+    want = (wide(A) @ wide(B).T) * ab
+    err = (wide(A).abs() @ wide(B).T.abs()) * ab * 2.0 ** -23 * (K / 16 + 24)
+    close(D, want, err + want.abs() * STEP[BF] + 2.0 ** -133, "D")
+    # rows and columns whose scale is more than its rest, under results that are normal numbers
+    for far in ((sa < 2.0 ** -62) | (sa >= 2.0 ** 64)).view(-1, 1), ((sb < 2.0 ** -62) | (sb >= 2.0 ** 64)).view(1, -1):
+        assert (far & (want.abs() > 2.0 ** -100)).any()
