@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import fp16_tensor_core_gb300 as dg
+from _knobs import knobs
 from _layers import F8, randn
 
 pytestmark = pytest.mark.gpu
@@ -136,3 +137,34 @@ def test_products_of_scales_beyond_fp32(M, N, bias, fp16):
         assert (odd & near & (acc != 0)).sum() > 0.1 * M * N and beyond.any()
     empty = (b.double() if bias else torch.zeros(N, dtype=torch.float64, device="cuda")).bfloat16().double()
     assert torch.equal(got[0], empty) and torch.equal(got[M // 2], empty)
+
+
+@pytest.mark.parametrize("env", [dict(DG_2CTA="0", DG_FORCE_BLOCK_N="96"), dict(DG_2CTA="0", DG_FORCE_BLOCK_N="256"),
+                                 dict(DG_2CTA="1", DG_FORCE_BLOCK_N="160"), dict(DG_2CTA="1", DG_FORCE_BLOCK_N="256"),
+                                 dict(DG_2CTA="1", DG_FORCE_BLOCK_N="224", DG_STREAM_K="1")])
+@pytest.mark.parametrize("short", [16, 3])
+def test_extreme_scales_of_some_tiles(env, short):
+    """Several tiles a CTA, of which some have extreme scales and others none;
+    bias, residual and ReLU behind them."""
+    M, K, bn = 500, 256, int(env["DG_FORCE_BLOCK_N"])
+    N = 100 * bn - short
+    A, B = (codes_of(i, n, K, size=0.5) for i, n in ((1, M), (2, N)))
+    sa, sb = 1 + randn(3, M).abs(), 1 + randn(4, N).abs()
+    sa[7], sa[300:310] = 2.0 ** -120, 2.0 ** 80
+    sb[5 * bn:6 * bn] *= 2.0 ** -90
+    sb[40 * bn + 3], sb[N - 1] = 2.0 ** 100, 2.0 ** -70
+    bias, residual = randn(5, N), randn(6, M, N).to(torch.bfloat16)
+    D = residual.clone()
+    with knobs(**env):
+        p = dg.dg_gemm_plan(M, N, K)
+        assert p["path"] == 3 and p["block_n"] == bn and p["tiles"] > p["grid"], p
+        dg.dg_fp8_gemm_fused(A, B, D, sa, sb, bias=bias, act=dg.DG_ACT_RELU, residual=D)
+    ab = sa.double()[:, None] * sb.double()
+    acc, size = (wide(A) @ wide(B).T) * ab, (wide(A).abs() @ wide(B).T.abs()) * ab
+    want = (acc + bias.double()).clamp_min(0) + residual.double()
+    err = (size + bias.double().abs()) * (2.0 ** -23 * (K / 16 + 24)) + want.abs() * 2.0 ** -23
+    top = torch.finfo(torch.bfloat16).max
+    near = want.abs() <= top - err
+    got = D.double()
+    assert not got.isnan().any() and near.float().mean() > 0.99
+    assert ((got[near] - want[near]).abs() <= (err + want.abs() * 2.0 ** -8 + 2.0 ** -134)[near]).all()
