@@ -18,9 +18,9 @@
 // sums are joined in order by a second kernel.  The blocks of a column take
 // the rows in turn, so that the grid moves through memory as one band (each
 // on a run of rows of its own: 5 % more time).
-// Gated, 8192 x 11008 BF16: codes and checkpoint 101.8 us, 0.91 of the rate of
+// Gated, 8192 x 11008 BF16: codes and checkpoint 103.2 us, 0.90 of the rate of
 // a copy; gradient from the checkpoint 119.4 us, 0.89 (122.5 with dbias), from
-// the input 134.0 us, 0.99 (141.7).
+// the input 134.0 us, 0.99 (142.2).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,7 +34,11 @@ namespace dg {
 namespace {
 
 // Threads of a block, and blocks an SM at least, by vectors (of each half) a
-// thread: the registers (64, 80, 128) hold a row's input and output.
+// thread: the registers (64, 80, 128) hold a row's packed input and FP32 output,
+// but for gated rows of more than 12288 columns: eight vectors of both halves
+// and their output are all of 128 registers, and 308 bytes a thread are spilled
+// (4096 x 14336 to codes 53.9 us, 0.80, with checkpoint 74.7, 0.81; 2048 x 28672
+// 57.5 and 84.8, 0.75 and 0.71).
 template <int NV>
 constexpr int block_limit() { return NV == 4 ? 384 : 512; }
 template <int NV>

@@ -13,7 +13,7 @@
 // registers between its two reductions (sum of squares, maximum), so each
 // element crosses memory once; blocks are persistent and have the next row's
 // loads in flight while a row is reduced and written.  BF16 with a residual to
-// codes, 16001 x 4096: 71.4 us, 0.95 of the rate of a copy; FP16 to codes of
+// codes, 16001 x 4096: 71.5 us, 0.95 of the rate of a copy; FP16 to codes of
 // one scale, 6001 x 8192: 32.5 us, 0.67 (2 bytes read and 1 written an element
 // leave the instructions as the bound: 65 % of the issue slots).
 //
@@ -23,7 +23,7 @@
 // of every row of its block, so dw is summed in registers and leaves the
 // block once; the blocks' sums are joined in order by a second kernel, so
 // that results do not depend on timing.  BF16 with dsum and dw, 16384 x 4096:
-// 83.0 us, 0.95.
+// 82.9 us, 0.95.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -46,7 +46,10 @@ constexpr float kDown = 0x1p-80f;
 // (3000 x 16384 BF16 with residual, codes: 55.5 us, 0.91 of the rate of a
 // copy; four vectors of 512 threads at 128 registers 90.7); at four, past
 // 16384 columns, the row stays packed and is unpacked again for each pass, the
-// next one on its way to L2 (1500 x 24576: 55.8 us, 0.68; held in FP32 70.6).
+// next one on its way to L2 (1500 x 24576: 56.6 us, 0.67; held in FP32 70.6).
+// Even so 64 registers are too few there: with a residual 84 bytes a thread are
+// spilled to codes, 308 to 16-bit output (62.4 us, 0.70) and 332 to one scale
+// (65.1, 0.58), without one 12, 144 and 120.
 constexpr int kLimits[3] = {1024, 1024, 0};
 constexpr int kPerSm[3] = {1024, 1024, 0};
 static_assert(hold_widest_row(kLimits) && kLimits[0] <= kRowThreads && kLimits[1] <= kRowThreads, "launch bounds");
@@ -263,8 +266,8 @@ __global__ void next_scale_kernel(const float* amax, float* scale) {
 // The gradient's blocks: up to 512 threads at 128 registers (a row, the next
 // row's loads, the weight and the columns' sums).  Rows of more than 8192
 // columns are a cluster's of two or four blocks, each with its part of the
-// columns (BF16 with dw: 4000 x 11008 80.4 us, 3000 x 16384 77.8, 1500 x 24576
-// 71.0; four or eight vectors a thread of one block, with spills, 112.8, 104.8
+// columns (BF16 with dw: 4000 x 11008 81.5 us, 3000 x 16384 77.8, 1500 x 24576
+// 71.4; four or eight vectors a thread of one block, with spills, 112.8, 104.8
 // and 181.1).
 constexpr int kGradThreads = 512, kGradPerSm = 512;
 constexpr int kGradColumns = 16 * kGradThreads;   // of a block
