@@ -309,11 +309,10 @@ __device__ __forceinline__ void store_box_odd(const Params& p, uint8_t* box, int
 // The columns' scales of B and biases (laid out as kColumnFloats says) into
 // shared memory while the main loop runs, zeros past N: chunks first, first +
 // 2, ... of the tile whose columns start at col0.  What is kept of a scale is
-// its rest (scale_parts); returns whether any lane has one, or a row of scale
-// `sa`, that is more than its rest.
+// its rest (scale_parts); returns whether any column's scale is more than that.
 template <int BN>
-__device__ __forceinline__ bool stage_columns(const Params& p, float* columns, int col0, int first, int lane, float sa) {
-    bool parts = !scale_is_rest(sa);
+__device__ __forceinline__ bool stage_columns(const Params& p, float* columns, int col0, int first, int lane) {
+    bool parts = false;
     constexpr int kChunks = fused_chunks(BN);
     float s[kChunks], b[kChunks];
 #pragma unroll
@@ -339,33 +338,29 @@ __device__ __forceinline__ bool stage_columns(const Params& p, float* columns, i
     return __any_sync(0xFFFFFFFFu, parts);
 }
 
-// Multiplies 32 accumulator columns of one row by what stage_columns left out
-// of their scales and scale_of_row of the row's.
-__device__ __forceinline__ void apply_wholes(const Params& p, int row, bool row_ok, int col0, int lane,
-                                             uint32_t (&r)[32]) {
+// Multiplies 32 accumulator columns by what stage_columns left out of their
+// scales.
+__device__ __forceinline__ void apply_wholes(const Params& p, int col0, int lane, uint32_t (&r)[32]) {
     const int n = col0 + lane;
     const float s = n < p.N && p.sb != nullptr ? ld_float(p.sb + static_cast<int64_t>(n) * p.epi.sb_step) : 1.0f;
     const float column = scale_parts(s).whole;
-    const float a = p.sa == nullptr || !row_ok ? 1.0f : ld_float(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
-    const float whole = scale_parts(a).whole;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        r[i] = __float_as_uint(__uint_as_float(r[i]) * whole * __shfl_sync(0xFFFFFFFFu, column, i));
+        r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xFFFFFFFFu, column, i));
 }
 
 // The same of a warp's chunks of a tile (first, first + 2, ...), in tensor
 // memory, before its epilogue: there a branch at every chunk took 1 us more
 // of 4096 x 4096 x 4096 E4M3's 49.
 template <int BN>
-__device__ __forceinline__ void apply_wholes_to_tile(const Params& p, uint32_t taddr, int row, bool row_ok, int col0,
-                                                     int first, int lane) {
+__device__ __forceinline__ void apply_wholes_to_tile(const Params& p, uint32_t taddr, int col0, int first, int lane) {
 #pragma unroll 1
     for (int c = first; c < BN / 32; c += 2) {
         uint32_t r[32];
         __syncwarp();
         tmem_load_32cols(taddr + c * 32, r);
         tmem_load_wait(r);
-        apply_wholes(p, row, row_ok, col0 + c * 32, lane, r);
+        apply_wholes(p, col0 + c * 32, lane, r);
         tmem_store_32cols(taddr + c * 32, r);
     }
     tmem_store_wait();
@@ -387,14 +382,15 @@ __device__ __forceinline__ void prefetch_residual(const Params& p, int row, bool
 // columns: theirs (stage_columns).  Returns their largest magnitude inside D
 // (ordered bits) when it is wanted, before the division by the output's scale.
 __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col0, const uint32_t (&r)[32],
-                                           const uint32_t (&res)[16], float sa, const float* columns, ByScale out,
+                                           const uint32_t (&res)[16], ScaleParts sa, const float* columns, ByScale out,
                                            float (&f)[32]) {
     pair v[16];
-    const pair row_scale = pair_of(sa);
+    const pair row_scale = pair_of(sa.rest), row_whole = pair_of(sa.whole);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const ulonglong2 c = reinterpret_cast<const ulonglong2*>(columns)[i];
-        v[i] = pair_fma(pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), pair_mul(row_scale, c.x), c.y);
+        const pair acc = pair_mul(pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), row_whole);
+        v[i] = pair_fma(acc, pair_mul(row_scale, c.x), c.y);
     }
     with_activation(p.epi.act, [&](auto act) {
 #pragma unroll

@@ -352,17 +352,16 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             // The fused epilogue's own operands, on their way while the main
             // loop runs; the residual one 32-column chunk ahead.
             const bool row_ok = row < p.M;
-            float sa = 1.0f;
+            ScaleParts sa{1.0f, 1.0f};
             bool parts = false;
             uint32_t res[16];
             if constexpr (kFused) {
-                sa = scale_of_row(p, row, row_ok);
+                sa = scale_parts(scale_of_row(p, row, row_ok));
                 if (it.part <= 0) {
                     if ((p.N & 7) == 0) load_residual(p, row, row_ok, nt * BN + 32 * half, res);
                     prefetch_residual<BN>(p, row, row_ok, nt * BN, half);
-                    parts = stage_columns<BN>(p, columns, nt * BN, half, lane, sa);
-                    sa = scale_parts(sa).rest;
-                }
+                    parts = stage_columns<BN>(p, columns, nt * BN, half, lane);
+                    }
             }
             // The warps continue or leave together (the split tail
             // below synchronises them on a named barrier).
@@ -372,7 +371,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * BN);
             if constexpr (kFused) {   // (a split tile's parts are added first)
-                if (parts && it.part < 0) apply_wholes_to_tile<BN>(p, tbase, row, row_ok, nt * BN, half, lane);
+                if (parts && it.part < 0) apply_wholes_to_tile<BN>(p, tbase, nt * BN, half, lane);
             }
             // Split tail tile: this CTA's partial tile of part s lives in slot
             // (r * (split - 1) + s - 1) * 2 + rank, as FP32 column quads
@@ -461,7 +460,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     }
                 }
                 if constexpr (kFused) {
-                    if (parts) apply_wholes(p, row, row_ok, nt * BN + c * 32, lane, r);
+                    if (parts) apply_wholes(p, nt * BN + c * 32, lane, r);
                 }
             };
             if (it.part > 0 || !ready) {

@@ -324,15 +324,14 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             // The fused epilogue's own operands, on their way while the main
             // loop runs; the residual one 32-column chunk ahead.
             const bool row_ok = row < T.row_end;
-            float sa = 1.0f;
+            ScaleParts sa{1.0f, 1.0f};
             bool parts = false;
             uint32_t res[16];
             if constexpr (kFused) {
-                sa = scale_of_row(p, row, row_ok);
+                sa = scale_parts(scale_of_row(p, row, row_ok));
                 if ((p.N & 7) == 0) load_residual(p, row, row_ok, T.col0 + 32 * half, res);
                 prefetch_residual<BN>(p, row, row_ok, T.col0, half);
-                parts = stage_columns<BN>(p, columns, T.col0, half, lane, sa);
-                sa = scale_parts(sa).rest;
+                parts = stage_columns<BN>(p, columns, T.col0, half, lane);
             }
             // Every lane waits; the vote reconverges the warp (tcgen05.ld is
             // .sync.aligned) and makes the whole warp leave together.
@@ -342,7 +341,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * BN);
             if constexpr (kFused) {
-                if (parts) apply_wholes_to_tile<BN>(p, tbase, row, row_ok, T.col0, half, lane);
+                if (parts) apply_wholes_to_tile<BN>(p, tbase, T.col0, half, lane);
             }
             // Staged bulk stores (whole lines, M / N edges clipped by the
             // tensor map) unless the warp's 32 rows cross a group's end,
