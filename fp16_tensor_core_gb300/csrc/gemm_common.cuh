@@ -378,8 +378,8 @@ __device__ __forceinline__ void prefetch_residual(const Params& p, int row, bool
             asm volatile("prefetch.global.L2 [%0];" :: "l"(src + i + 64 * half));
 }
 
-// The values of 32 accumulator columns of one row; sa: the row's scale,
-// columns: theirs (stage_columns).  Returns their largest magnitude inside D
+// The values of 32 accumulator columns of one row; sa: the row's scale in its
+// parts, columns: the rests of theirs (stage_columns).  Returns their largest magnitude inside D
 // (ordered bits) when it is wanted, before the division by the output's scale.
 __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col0, const uint32_t (&r)[32],
                                            const uint32_t (&res)[16], ScaleParts sa, const float* columns, ByScale out,
@@ -431,8 +431,7 @@ __device__ __forceinline__ uint32_t fuse32(const Params& p, bool row_ok, int col
     return __float_as_uint(top);
 }
 
-// A row's scale of A (1 without scales, and for rows outside); the epilogue
-// goes on with its rest (scale_parts).
+// A row's scale of A (1 without scales, and for rows outside).
 __device__ __forceinline__ float scale_of_row(const Params& p, int row, bool row_ok) {
     return p.sa == nullptr || !row_ok ? 1.0f : ld_float(p.sa + static_cast<int64_t>(row) * p.epi.sa_step);
 }

@@ -361,7 +361,7 @@ gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     if ((p.N & 7) == 0) load_residual(p, row, row_ok, nt * BN + 32 * half, res);
                     prefetch_residual<BN>(p, row, row_ok, nt * BN, half);
                     parts = stage_columns<BN>(p, columns, nt * BN, half, lane);
-                    }
+                }
             }
             // The warps continue or leave together (the split tail
             // below synchronises them on a named barrier).
